@@ -172,7 +172,7 @@ def _quantise(x):
     big = a.amax(-1, keepdim=True)
     first = torch.where(a == big, torch.arange(GROUP, device=x.device), GROUP).amin(-1, keepdim=True)
     m = g.gather(-1, first.clamp(max=GROUP - 1))
-    d = (m * -0.125).clamp(-65504.0, 65504.0).half().float()
+    d = (m * -0.125).bfloat16().float().clamp(-2720.0, 2720.0).half().float()
     d = torch.where(torch.isfinite(g).all(-1, keepdim=True), d, torch.full_like(d, float("nan")))
     r = torch.where(d != 0, g / d, torch.zeros_like(g))
     r = torch.nan_to_num(r.round(), nan=0.0).clamp(-8, 7)
@@ -541,7 +541,7 @@ def exact(case, seed):
                 at_lo = torch.where(has_lo, torch.arange(GROUP, device=DEV), GROUP).amin(-1, keepdim=True)
                 at_hi = torch.where(has_hi, torch.arange(GROUP, device=DEV), GROUP).amin(-1, keepdim=True)
                 m = torch.where(at_lo < at_hi, low, -low)
-                d = (m / -8.0).to(torch.float16).double()
+                d = (m / -8.0).to(torch.bfloat16).double().clamp(-2720.0, 2720.0).to(torch.float16).double()
                 t = torch.where(d == 0, torch.zeros_like(g), torch.round(g / d).clamp(-8, 7))
                 y[b, :, :c] = (t * d).flatten(-2)
             got.append(y)
