@@ -28,6 +28,8 @@ GDN_ERR_TIMEOUT = -6
 GDN_ERR_CAPACITY = -7
 GDN_ERR_STATE = -8
 GDN_ERR_SCHEDULE = -9
+GDN_ERR_CACHE = -10
+GDN_ERR_LOGITS = -11
 GDN_DTYPE_F32 = 0
 GDN_DTYPE_BF16 = 1
 GDN_COMMIT_COMPACT = 1
@@ -37,6 +39,7 @@ GDN_VERIFY_UT_SIMT = 4
 GDN_VERIFY_TC_PER_HEAD = 8
 GDN_VERIFY_CHAINS = 16
 GDN_MAX_NODES = 64
+GDN_KV4_PAGE = 64
 
 
 class GdnError(RuntimeError):
@@ -71,6 +74,16 @@ class gdn_banks(ctypes.Structure):
                 ("write_bank", c_i32), ("pend_bank", c_i32), ("verified_bank", c_i32)]
 
 
+class gdn_attn_dims(ctypes.Structure):
+    _fields_ = [("Hq", c_i32), ("Hkv", c_i32), ("D", c_i32), ("dtype", c_i32), ("scale", ctypes.c_float),
+                ("q_row", c_i32), ("kv_row", c_i32)]
+
+
+class gdn_kv4_cache(ctypes.Structure):
+    _fields_ = [("pool", c_p), ("page_table", c_p), ("seq_len", c_p), ("ticket", c_p), ("err", c_p),
+                ("B", c_i32), ("layers", c_i32), ("pages_max", c_i32), ("n_pages", ctypes.c_int64)]
+
+
 _lib = None
 
 
@@ -103,6 +116,22 @@ def lib():
         L.gdn_finish.argtypes = [P(gdn_dims), c_i32, c_i32, c_p, c_p, P(gdn_banks), c_p]
         L.gdn_check_error.argtypes = [P(gdn_banks), c_p]
         L.gdn_selftest_wait_timeout.argtypes = [P(gdn_banks), c_p]
+        L.gdn_kv4_pool_bytes.argtypes = [P(gdn_attn_dims), c_i32, ctypes.c_int64]
+        L.gdn_kv4_pool_bytes.restype = ctypes.c_size_t
+        L.gdn_kv4_append.argtypes = [P(gdn_attn_dims), c_i32, c_i32, c_p, c_p, c_p, c_p, P(gdn_kv4_cache), c_p]
+        L.gdn_kv4_read.argtypes = [P(gdn_attn_dims), c_i32, c_i32, c_p, c_i32, c_p, c_p, P(gdn_kv4_cache), c_p]
+        L.gdn_kv4_workspace_bytes.argtypes = [P(gdn_attn_dims), c_i32, c_i32, c_i32, c_i32]
+        L.gdn_kv4_workspace_bytes.restype = ctypes.c_size_t
+        L.gdn_kv4_attention.argtypes = [P(gdn_attn_dims), c_i32, P(gdn_batch_schedule), c_p, c_p, c_p, c_p,
+                                        P(gdn_kv4_cache), c_i32, c_p, ctypes.c_size_t, c_p]
+        L.gdn_accept_workspace_bytes.argtypes = [c_i32, c_i32, c_i32]
+        L.gdn_accept_workspace_bytes.restype = ctypes.c_size_t
+        L.gdn_tree_accept.argtypes = [P(gdn_batch_schedule), c_i32, c_i32, c_i32, c_p, c_p, c_p, c_i32, c_p, c_p, c_p,
+                                      c_p, c_p, c_p, c_p, c_p, ctypes.c_size_t, c_p]
+        L.gdn_check_error_words.argtypes = [c_p, c_p]
+        for name in ("gdn_kv4_append", "gdn_kv4_read", "gdn_kv4_attention", "gdn_tree_accept",
+                     "gdn_check_error_words"):
+            getattr(L, name).restype = c_i32
         for name in ("gdn_hld_schedule", "gdn_pack_schedules", "gdn_pack_schedules_per_node", "gdn_ddtree_build",
                      "gdn_ddtree_build_batch", "gdn_banks_init", "gdn_tree_verify",
                      "gdn_tree_verify_noalloc", "gdn_commit_fold", "gdn_finish", "gdn_check_error",
@@ -267,3 +296,47 @@ def gdn_check_error(banks: gdn_banks, stream=None):
 
 def gdn_selftest_wait_timeout(banks: gdn_banks, stream=None):
     _check(lib().gdn_selftest_wait_timeout(ctypes.byref(banks), _stream(stream)))
+
+
+def gdn_check_error_words(err, stream=None):
+    _check(lib().gdn_check_error_words(_ptr(err), _stream(stream)))
+
+
+def gdn_kv4_pool_bytes(dims: gdn_attn_dims, layers: int, n_pages: int) -> int:
+    return int(lib().gdn_kv4_pool_bytes(ctypes.byref(dims), layers, n_pages))
+
+
+def gdn_kv4_append(dims: gdn_attn_dims, layers: int, n_rows: int, k_new, v_new, path, count, cache: gdn_kv4_cache,
+                   stream=None):
+    _check(lib().gdn_kv4_append(ctypes.byref(dims), layers, n_rows, _ptr(k_new), _ptr(v_new), _ptr(path), _ptr(count),
+                                ctypes.byref(cache), _stream(stream)))
+
+
+def gdn_kv4_read(dims: gdn_attn_dims, layers: int, n_rows: int, start, out_dtype: int, k_out, v_out,
+                 cache: gdn_kv4_cache, stream=None):
+    _check(lib().gdn_kv4_read(ctypes.byref(dims), layers, n_rows, _ptr(start), out_dtype, _ptr(k_out), _ptr(v_out),
+                              ctypes.byref(cache), _stream(stream)))
+
+
+def gdn_kv4_workspace_bytes(dims: gdn_attn_dims, B: int, layers: int, n_max: int, max_len: int) -> int:
+    return int(lib().gdn_kv4_workspace_bytes(ctypes.byref(dims), B, layers, n_max, max_len))
+
+
+def gdn_kv4_attention(dims: gdn_attn_dims, layers: int, sched: Optional[gdn_batch_schedule], q, k_new, v_new, out,
+                      cache: gdn_kv4_cache, max_len: int, workspace, workspace_bytes: int, stream=None):
+    _check(lib().gdn_kv4_attention(ctypes.byref(dims), layers, None if sched is None else ctypes.byref(sched), _ptr(q),
+                                   _ptr(k_new), _ptr(v_new), _ptr(out), ctypes.byref(cache), max_len,
+                                   _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def gdn_accept_workspace_bytes(B: int, n_max: int, V: int) -> int:
+    return int(lib().gdn_accept_workspace_bytes(B, n_max, V))
+
+
+def gdn_tree_accept(sched: gdn_batch_schedule, V: int, v_stride: int, logits_dtype: int, logits, tokens, draft_probs,
+                    draft_dtype: int, uniform, gumbel, temperature, path, length, next_token, err, workspace,
+                    workspace_bytes: int, stream=None):
+    _check(lib().gdn_tree_accept(ctypes.byref(sched), V, v_stride, logits_dtype, _ptr(logits), _ptr(tokens),
+                                 _ptr(draft_probs), draft_dtype, _ptr(uniform), _ptr(gumbel), _ptr(temperature),
+                                 _ptr(path), _ptr(length), _ptr(next_token), _ptr(err), _ptr(workspace),
+                                 workspace_bytes, _stream(stream)))

@@ -1,12 +1,15 @@
 // extern "C" entry points: argument checks, the factor-bank lifecycle and the
 // kernel launches.  No entry point allocates memory or synchronises the host
 // except gdn_check_error.
+#include <algorithm>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
 
+#include "gdn_accept.cuh"
 #include "gdn_internal.h"
+#include "gdn_kv4.cuh"
 
 namespace gdn {
 namespace {
@@ -108,6 +111,84 @@ gdn_status cuda_fail(cudaError_t e, const char* what) {
 
 size_t ws_q_bytes(const gdn_dims* d, int B, int layers, int n_max) {
   return round_up(static_cast<size_t>(B) * layers * n_max * d->Hk * d->dk * sizeof(float), kAlign);
+}
+
+// Reads and clears device error words; the status of what they hold.
+gdn_status read_error_words(int32_t* err, cudaStream_t stream) {
+  cudaError_t e = cudaStreamSynchronize(stream);
+  if (e != cudaSuccess) return cuda_fail(e, "stream synchronise");
+  int32_t w[2] = {0, 0};
+  e = cudaMemcpyAsync(w, err, sizeof(w), cudaMemcpyDeviceToHost, stream);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
+  if (e != cudaSuccess) return cuda_fail(e, "reading the error words");
+  if (w[0] == 0) return GDN_OK;
+  e = cudaMemsetAsync(err, 0, sizeof(w), stream);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
+  if (e != cudaSuccess) return cuda_fail(e, "clearing the error words");
+  if (w[0] & GDN_DEVERR_INVALID_PATH)
+    return fail(GDN_ERR_INVALID_PATH, "accepted path of request %d is not a root path of its tree; nothing was "
+                "committed for it", w[1] - 1);
+  if (w[0] & GDN_DEVERR_TIMEOUT)
+    return fail(GDN_ERR_TIMEOUT, "an asynchronous copy of request %d did not complete within the bounded wait; "
+                "its outputs are incomplete", w[1] - 1);
+  if (w[0] & GDN_DEVERR_SCHEDULE)
+    return fail(GDN_ERR_SCHEDULE, "packed schedule of request %d is out of range (n, chains, boundary slots); "
+                "the offending accesses were skipped", w[1] - 1);
+  if (w[0] & GDN_DEVERR_CACHE)
+    return fail(GDN_ERR_CACHE, "4-bit cache of request %d: a length, page number, path entry or row count is out of "
+                "range; the offending accesses were skipped", w[1] - 1);
+  if (w[0] & GDN_DEVERR_LOGITS)
+    return fail(GDN_ERR_LOGITS, "request %d: a visited logits row holds no distribution, or its temperature is "
+                "negative or not finite; the walk stopped there", w[1] - 1);
+  return fail(GDN_ERR_CUDA, "unknown device error word 0x%x", w[0]);
+}
+
+constexpr int kMaxAppendRows = 1 << 21;
+
+int pages_of(int tokens) { return tokens / GDN_KV4_PAGE + (tokens % GDN_KV4_PAGE ? 1 : 0); }
+
+gdn_status check_attn_dims(const gdn_attn_dims* d) {
+  if (!d) return fail(GDN_ERR_INVALID_ARG, "dims is NULL");
+  if (d->Hq < 1 || d->Hkv < 1 || d->Hq % d->Hkv != 0)
+    return fail(GDN_ERR_INVALID_ARG, "heads Hq = %d, Hkv = %d: need Hkv >= 1 and Hq a multiple of Hkv", d->Hq, d->Hkv);
+  if (d->Hq > 1024) return fail(GDN_ERR_UNSUPPORTED, "Hq = %d above 1024", d->Hq);
+  if (d->D != 64 && d->D != 128 && d->D != 256)
+    return fail(GDN_ERR_UNSUPPORTED, "head size D = %d: supported are 64, 128 and 256", d->D);
+  if (d->dtype != GDN_DTYPE_F32 && d->dtype != GDN_DTYPE_BF16) return fail(GDN_ERR_INVALID_ARG, "dtype = %d", d->dtype);
+  if (!std::isfinite(d->scale)) return fail(GDN_ERR_INVALID_ARG, "scale is not finite");
+  const int vec = d->dtype == GDN_DTYPE_F32 ? 4 : 8;
+  if (d->q_row != 0 && (d->q_row < d->Hq * d->D || d->q_row % vec))
+    return fail(GDN_ERR_INVALID_ARG, "q_row = %d: below Hq * D or not a multiple of 16 bytes", d->q_row);
+  if (d->kv_row != 0 && (d->kv_row < d->Hkv * d->D || d->kv_row % vec))
+    return fail(GDN_ERR_INVALID_ARG, "kv_row = %d: below Hkv * D or not a multiple of 16 bytes", d->kv_row);
+  return GDN_OK;
+}
+
+gdn_status check_cache(const gdn_kv4_cache* c, int layers) {
+  if (!c) return fail(GDN_ERR_INVALID_ARG, "cache is NULL");
+  if (c->B < 1 || c->layers < 1 || c->pages_max < 1 || c->n_pages < 1)
+    return fail(GDN_ERR_INVALID_ARG, "cache B = %d, layers = %d, pages_max = %d, n_pages = %lld", c->B, c->layers,
+                c->pages_max, static_cast<long long>(c->n_pages));
+  if (c->pages_max > (INT32_MAX - GDN_KV4_PAGE) / GDN_KV4_PAGE || c->n_pages > INT32_MAX)
+    return fail(GDN_ERR_UNSUPPORTED, "pages_max = %d, n_pages = %lld: lengths and page numbers are 32-bit", c->pages_max,
+                static_cast<long long>(c->n_pages));
+  if (c->layers != layers) return fail(GDN_ERR_CAPACITY, "cache of %d layers, call of %d", c->layers, layers);
+  if (static_cast<long long>(c->B) * layers > INT32_MAX / 1024)
+    return fail(GDN_ERR_UNSUPPORTED, "B * layers = %lld", static_cast<long long>(c->B) * layers);
+  GDN_CHECK_PTR(c->pool, "cache.pool");
+  GDN_CHECK_PTR(c->page_table, "cache.page_table");
+  GDN_CHECK_PTR(c->seq_len, "cache.seq_len");
+  GDN_CHECK_PTR(c->ticket, "cache.ticket");
+  GDN_CHECK_PTR(c->err, "cache.err");
+  return GDN_OK;
+}
+
+gdn::KvCacheView cache_view(const gdn_kv4_cache* c) {
+  gdn::KvCacheView v{};
+  v.pool = static_cast<char*>(c->pool);
+  v.page_table = c->page_table; v.seq_len = c->seq_len; v.ticket = c->ticket; v.err = c->err;
+  v.B = c->B; v.layers = c->layers; v.pages_max = c->pages_max; v.n_pages = c->n_pages;
+  return v;
 }
 
 }  // namespace
@@ -330,26 +411,160 @@ gdn_status gdn_selftest_wait_timeout(gdn_banks* banks, cudaStream_t stream) {
 gdn_status gdn_check_error(gdn_banks* banks, cudaStream_t stream) {
   gdn::clear_error();
   if (!banks || !banks->err) return fail(GDN_ERR_INVALID_ARG, "banks / banks.err is NULL");
-  cudaError_t e = cudaStreamSynchronize(stream);
-  if (e != cudaSuccess) return cuda_fail(e, "stream synchronise");
-  int32_t w[2] = {0, 0};
-  e = cudaMemcpyAsync(w, banks->err, sizeof(w), cudaMemcpyDeviceToHost, stream);
-  if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
-  if (e != cudaSuccess) return cuda_fail(e, "reading the error words");
-  if (w[0] == 0) return GDN_OK;
-  e = cudaMemsetAsync(banks->err, 0, sizeof(w), stream);
-  if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
-  if (e != cudaSuccess) return cuda_fail(e, "clearing the error words");
-  if (w[0] & GDN_DEVERR_INVALID_PATH)
-    return fail(GDN_ERR_INVALID_PATH, "accepted path of request %d is not a root path of its tree; nothing was "
-                "committed for it", w[1] - 1);
-  if (w[0] & GDN_DEVERR_TIMEOUT)
-    return fail(GDN_ERR_TIMEOUT, "an asynchronous copy of request %d did not complete within the bounded wait; "
-                "its outputs are incomplete", w[1] - 1);
-  if (w[0] & GDN_DEVERR_SCHEDULE)
-    return fail(GDN_ERR_SCHEDULE, "packed schedule of request %d is out of range (n, chains, boundary slots); "
-                "the offending accesses were skipped", w[1] - 1);
-  return fail(GDN_ERR_CUDA, "unknown device error word 0x%x", w[0]);
+  return read_error_words(banks->err, stream);
+}
+
+gdn_status gdn_check_error_words(int32_t* err, cudaStream_t stream) {
+  gdn::clear_error();
+  GDN_CHECK_PTR(err, "err");
+  return read_error_words(err, stream);
+}
+
+// ---- 4-bit key/value cache and its attention ----
+
+size_t gdn_kv4_pool_bytes(const gdn_attn_dims* d, int32_t layers, int64_t n_pages) {
+  if (check_attn_dims(d) != GDN_OK || layers < 1 || n_pages < 1) return 0;
+  return static_cast<size_t>(layers) * static_cast<size_t>(n_pages) * d->Hkv * 72 * d->D;
+}
+
+gdn_status gdn_kv4_append(const gdn_attn_dims* d, int32_t layers, int32_t n_rows, const void* k_new,
+                          const void* v_new, const int32_t* path, const int32_t* count, gdn_kv4_cache* cache,
+                          cudaStream_t stream) {
+  gdn::clear_error();
+  GDN_TRY(check_attn_dims(d));
+  GDN_TRY(check_cache(cache, layers));
+  if (n_rows < 1 || n_rows > kMaxAppendRows)
+    return fail(GDN_ERR_INVALID_ARG, "n_rows = %d outside 1..%d", n_rows, kMaxAppendRows);
+  GDN_CHECK_PTR(k_new, "k_new");
+  GDN_CHECK_PTR(v_new, "v_new");
+  GDN_CHECK_PTR(count, "count");
+  if (path) GDN_CHECK_PTR(path, "path");
+  gdn::KvAppendParams p{};
+  p.c = cache_view(cache);
+  p.Hkv = d->Hkv; p.D = d->D; p.dtype = d->dtype; p.n_rows = n_rows;
+  p.kv_row = d->kv_row ? d->kv_row : d->Hkv * d->D;
+  p.k_new = k_new; p.v_new = v_new; p.path = path; p.count = count;
+  cudaError_t e = gdn::launch_kv4_append(p, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "cache append launch");
+  return GDN_OK;
+}
+
+gdn_status gdn_kv4_read(const gdn_attn_dims* d, int32_t layers, int32_t n_rows, const int32_t* start,
+                        int32_t out_dtype, void* k_out, void* v_out, const gdn_kv4_cache* cache,
+                        cudaStream_t stream) {
+  gdn::clear_error();
+  GDN_TRY(check_attn_dims(d));
+  GDN_TRY(check_cache(cache, layers));
+  if (n_rows < 1 || n_rows > kMaxAppendRows)
+    return fail(GDN_ERR_INVALID_ARG, "n_rows = %d outside 1..%d", n_rows, kMaxAppendRows);
+  if (out_dtype != GDN_DTYPE_F32 && out_dtype != GDN_DTYPE_BF16)
+    return fail(GDN_ERR_INVALID_ARG, "out_dtype = %d", out_dtype);
+  GDN_CHECK_PTR(k_out, "k_out");
+  GDN_CHECK_PTR(v_out, "v_out");
+  if (start) GDN_CHECK_PTR(start, "start");
+  gdn::KvReadParams p{};
+  p.c = cache_view(cache);
+  p.Hkv = d->Hkv; p.D = d->D; p.out_dtype = out_dtype; p.n_rows = n_rows;
+  p.start = start; p.k_out = k_out; p.v_out = v_out;
+  cudaError_t e = gdn::launch_kv4_read(p, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "cache read launch");
+  return GDN_OK;
+}
+
+size_t gdn_kv4_workspace_bytes(const gdn_attn_dims* d, int32_t B, int32_t layers, int32_t n_max, int32_t max_len) {
+  if (check_attn_dims(d) != GDN_OK || B < 1 || layers < 1 || n_max < 1 || n_max > GDN_MAX_NODES || max_len < 0)
+    return 0;
+  return gdn::plan_kv4_attention(d->Hq, d->Hkv, d->D, d->dtype, B, layers, n_max, pages_of(max_len)).bytes;
+}
+
+gdn_status gdn_kv4_attention(const gdn_attn_dims* d, int32_t layers, const gdn_batch_schedule* sched, const void* q,
+                             const void* k_new, const void* v_new, void* out, const gdn_kv4_cache* cache,
+                             int32_t max_len, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  gdn::clear_error();
+  GDN_TRY(check_attn_dims(d));
+  GDN_TRY(check_cache(cache, layers));
+  if (sched) {
+    GDN_TRY(check_sched(sched));
+    if (sched->B != cache->B)
+      return fail(GDN_ERR_CAPACITY, "schedule of %d requests, cache of %d", sched->B, cache->B);
+  }
+  GDN_CHECK_PTR(q, "q");
+  GDN_CHECK_PTR(out, "out");
+  if ((k_new == nullptr) != (v_new == nullptr))
+    return fail(GDN_ERR_INVALID_ARG, "k_new and v_new: both or neither");
+  if (k_new) {
+    GDN_CHECK_PTR(k_new, "k_new");
+    GDN_CHECK_PTR(v_new, "v_new");
+  }
+  if (max_len < 0) return fail(GDN_ERR_INVALID_ARG, "max_len = %d", max_len);
+  GDN_CHECK_PTR(workspace, "workspace");
+  const int n_max = sched ? sched->n_max : 1;
+  const int most = max_len ? std::min(pages_of(max_len), cache->pages_max) : cache->pages_max;
+  const gdn::KvAttnPlan pl =
+      gdn::plan_kv4_attention(d->Hq, d->Hkv, d->D, d->dtype, cache->B, layers, n_max, most);
+  if (workspace_bytes < pl.bytes)
+    return fail(GDN_ERR_CAPACITY, "workspace holds %zu bytes, the call needs %zu", workspace_bytes, pl.bytes);
+  gdn::KvAttnParams p{};
+  p.c = cache_view(cache);
+  p.layers = layers; p.n_max = n_max; p.Hq = d->Hq; p.Hkv = d->Hkv; p.D = d->D; p.dtype = d->dtype;
+  p.G = d->Hq / d->Hkv; p.scale = d->scale;
+  p.q_row = d->q_row ? d->q_row : static_cast<long long>(d->Hq) * d->D;
+  p.kv_row = d->kv_row ? d->kv_row : static_cast<long long>(d->Hkv) * d->D;
+  p.words = sched ? sched->words : nullptr;
+  p.q = q; p.k_new = k_new; p.v_new = v_new; p.out = out;
+  p.row_tiles = pl.row_tiles; p.chunks = pl.chunks; p.chunk_pages = pl.chunk_pages;
+  p.done = static_cast<int32_t*>(workspace);
+  p.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + pl.done_bytes);
+  cudaError_t e = gdn::launch_kv4_attention_simt(p, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "cache attention launch");
+  return GDN_OK;
+}
+
+// ---- acceptance of drafted tokens ----
+
+size_t gdn_accept_workspace_bytes(int32_t B, int32_t n_max, int32_t V) {
+  if (B < 1 || n_max < 1 || n_max > GDN_MAX_NODES || V < 1) return 0;
+  return kAlign;
+}
+
+gdn_status gdn_tree_accept(const gdn_batch_schedule* sched, int32_t V, int32_t v_stride, int32_t logits_dtype,
+                           const void* logits, const int32_t* tokens, const void* draft_probs, int32_t draft_dtype,
+                           const float* uniform, const float* gumbel, const float* temperature, int32_t* path,
+                           int32_t* len, int32_t* next, int32_t* err, void* workspace, size_t workspace_bytes,
+                           cudaStream_t stream) {
+  gdn::clear_error();
+  GDN_TRY(check_sched(sched));
+  if (V < 1) return fail(GDN_ERR_INVALID_ARG, "V = %d", V);
+  if (v_stride != 0 && v_stride < V) return fail(GDN_ERR_INVALID_ARG, "v_stride = %d, V = %d", v_stride, V);
+  if (logits_dtype != GDN_DTYPE_F32 && logits_dtype != GDN_DTYPE_BF16)
+    return fail(GDN_ERR_INVALID_ARG, "logits_dtype = %d", logits_dtype);
+  if (draft_probs && draft_dtype != GDN_DTYPE_F32 && draft_dtype != GDN_DTYPE_BF16)
+    return fail(GDN_ERR_INVALID_ARG, "draft_dtype = %d", draft_dtype);
+  GDN_CHECK_PTR(logits, "logits");
+  GDN_CHECK_PTR(tokens, "tokens");
+  if (draft_probs) GDN_CHECK_PTR(draft_probs, "draft_probs");
+  if (temperature) {
+    GDN_CHECK_PTR(temperature, "temperature");
+    GDN_CHECK_PTR(uniform, "uniform");
+    GDN_CHECK_PTR(gumbel, "gumbel");
+  }
+  GDN_CHECK_PTR(path, "path");
+  GDN_CHECK_PTR(len, "len");
+  GDN_CHECK_PTR(next, "next");
+  GDN_CHECK_PTR(err, "err");
+  GDN_CHECK_PTR(workspace, "workspace");
+  const size_t need = gdn_accept_workspace_bytes(sched->B, sched->n_max, V);
+  if (workspace_bytes < need)
+    return fail(GDN_ERR_CAPACITY, "workspace holds %zu bytes, the call needs %zu", workspace_bytes, need);
+  gdn::AcceptParams p{};
+  p.B = sched->B; p.n_max = sched->n_max; p.V = V; p.logits_dtype = logits_dtype; p.draft_dtype = draft_dtype;
+  p.v_stride = v_stride ? v_stride : V;
+  p.words = sched->words; p.logits = logits; p.tokens = tokens; p.draft = draft_probs;
+  p.uniform = uniform; p.gumbel = gumbel; p.temperature = temperature;
+  p.path = path; p.len = len; p.next = next; p.err = err;
+  cudaError_t e = gdn::launch_accept(p, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "acceptance launch");
+  return GDN_OK;
 }
 
 }  // extern "C"

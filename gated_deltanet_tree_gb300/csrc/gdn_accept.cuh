@@ -1,0 +1,24 @@
+// Parameters of the acceptance kernels.
+#pragma once
+#include "gdn_internal.h"
+
+namespace gdn {
+
+struct AcceptParams {
+  int B, n_max, V, logits_dtype, draft_dtype;
+  long long v_stride;
+  const int32_t* words;
+  const void* logits;
+  const int32_t* tokens;
+  const void* draft;           // nullptr: the drafted tokens were chosen, not sampled
+  const float* uniform;
+  const float* gumbel;
+  const float* temperature;    // nullptr: all 0
+  int32_t* path;
+  int32_t* len;
+  int32_t* next;
+  int32_t* err;
+};
+cudaError_t launch_accept(const AcceptParams& p, cudaStream_t s);
+
+}  // namespace gdn

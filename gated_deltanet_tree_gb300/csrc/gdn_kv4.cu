@@ -1,0 +1,268 @@
+// Append to and read from the paged 4-bit key/value cache (format: gdn_tree.h).
+//
+// Append.  One CTA per (request and layer, page it touches, kv head): it owns
+// every word of that page's block, so the value words -- eight tokens of one
+// channel each -- are merged with tokens written earlier without atomics.  Four
+// lanes share a group of 32 channels: eight channels each, the group's largest
+// magnitude by two shuffles, one code word per lane.  Keys go straight to their
+// words; value codes pass through shared memory ([token][channel] bytes) and are
+// regrouped into words of eight tokens.  The work is the rows read once and
+// 1.125 D bytes a row and head written.
+//
+// The lengths are read by every CTA and advanced by the request's last one to
+// finish (a ticket per request), so a call is one launch.
+#include "gdn_kv4.cuh"
+
+namespace gdn {
+namespace {
+
+constexpr int kAppendThreads = 128;
+
+// Eight consecutive elements as fp32.
+__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
+  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+  x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+}
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&x)[8]) {
+  const uint4 u = *reinterpret_cast<const uint4*>(p);
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(w[i] << 16);
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
+}
+
+// Quantises a group held by four adjacent lanes (eight channels each): codes 0..15 of this lane's channels
+// and the group's scale.  All 32 lanes of the warp call it.
+__device__ __forceinline__ __half quantise8(const float (&x)[8], uint32_t (&code)[8]) {
+  float big = 0.f, m = 0.f;
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float a = fabsf(x[i]);
+    bad |= !(a <= 3.402823466e38f);
+    if (a > big) { big = a; m = x[i]; }        // the first of equals stays
+  }
+#pragma unroll
+  for (int o = 1; o < 4; o <<= 1) {
+    const float ob = __shfl_xor_sync(0xffffffffu, big, o), om = __shfl_xor_sync(0xffffffffu, m, o);
+    const bool other_first = (threadIdx.x & o) != 0;   // the partner holds the lower channels
+    if (ob > big || (ob == big && other_first)) { big = ob; m = om; }
+  }
+  const unsigned quad = 0xFu << (threadIdx.x & 28);
+  bad = (__ballot_sync(0xffffffffu, bad) & quad) != 0;
+  float d = __bfloat162float(__float2bfloat16_rn(m * -0.125f));
+  d = fminf(fmaxf(d, -kScaleMax), kScaleMax);
+  const __half h = __float2half_rn(d);
+  d = __half2float(h);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float r = (bad || d == 0.f) ? 0.f : rintf(__fdiv_rn(x[i], d));
+    code[i] = static_cast<uint32_t>(static_cast<int>(fminf(fmaxf(r, -8.f), 7.f)) + 8);
+  }
+  return bad ? __ushort_as_half(0x7FFF) : h;
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kAppendThreads) kv4_append_kernel(KvAppendParams p) {
+  using Blk = KvBlock<D>;
+  constexpr int kLanesPerRow = D / 8;                       // lanes that hold one row
+  constexpr int kRowsPerPass = kAppendThreads / kLanesPerRow;
+  __shared__ __align__(16) uint8_t codes[kPage][D];         // value codes of the rows written here
+  const int bl = blockIdx.x, b = bl / p.c.layers, l = bl % p.c.layers;
+  const int h = blockIdx.z, tid = threadIdx.x;
+
+  const int len = p.c.seq_len[b], cnt = p.count[b];
+  const long long cap = static_cast<long long>(p.c.pages_max) * kPage;
+  bool ok = len >= 0 && cnt >= 0 && cnt <= p.n_rows && len + static_cast<long long>(cnt) <= cap;
+  const int32_t* table = p.c.page_table + static_cast<size_t>(b) * p.c.pages_max;
+  const int32_t* path = p.path ? p.path + static_cast<size_t>(b) * p.n_rows : nullptr;
+  const int page0 = len / kPage;
+  if (ok && cnt > 0) {
+    const int pages = (len + cnt - 1) / kPage - page0 + 1;
+    bool mine = true;
+    for (int i = tid; i < pages; i += kAppendThreads) {
+      const int g = table[page0 + i];
+      mine = mine && g >= 0 && g < p.c.n_pages;
+    }
+    if (path)
+      for (int i = tid; i < cnt; i += kAppendThreads) mine = mine && path[i] >= 0 && path[i] < p.n_rows;
+    ok = __syncthreads_and(mine);
+  }
+  if (!ok && tid == 0) device_error(p.c.err, GDN_DEVERR_CACHE, b);
+
+  // rows [lo, hi) of the page are written; row r holds appended row first + r
+  const int first = (page0 + static_cast<int>(blockIdx.y)) * kPage - len;
+  const int lo = max(0, -first), hi = ok ? min(kPage, cnt - first) : 0;
+  if (lo < hi) {
+    char* blk = kv_block<D>(p.c, p.Hkv, table[page0 + blockIdx.y], l, h);
+    const size_t row0 = static_cast<size_t>(bl) * p.n_rows;
+    const T* kn = static_cast<const T*>(p.k_new) + h * D;
+    const T* vn = static_cast<const T*>(p.v_new) + h * D;
+    const int w = tid % kLanesPerRow;                       // word of the row this lane holds
+    const int rounds = (hi - lo + kRowsPerPass - 1) / kRowsPerPass;
+    for (int i = 0; i < rounds; ++i) {
+      const int r = lo + i * kRowsPerPass + tid / kLanesPerRow;
+      const bool in = r < hi;
+      const int src = in ? (path ? path[first + r] : first + r) : 0;
+      const size_t at = (row0 + src) * p.kv_row + 8 * w;
+      float x[8], y[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = y[e] = 0.f;
+      if (in) {
+        load8(kn + at, x);
+        load8(vn + at, y);
+      }
+      uint32_t c[8];
+      const __half dk = quantise8(x, c);
+      uint32_t word = 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) word |= c[e] << (4 * nibble_of(e));
+      const __half dv = quantise8(y, c);
+      if (in) {
+        reinterpret_cast<uint32_t*>(blk)[Blk::key_word(r, w)] = word;
+        *reinterpret_cast<uint2*>(&codes[r][8 * w]) =
+            make_uint2(c[0] | c[1] << 8 | c[2] << 16 | c[3] << 24, c[4] | c[5] << 8 | c[6] << 16 | c[7] << 24);
+        if ((w & 3) == 0) {
+          reinterpret_cast<__half*>(blk + Blk::kKeyScales)[r * Blk::kGroups + (w >> 2)] = dk;
+          reinterpret_cast<__half*>(blk + Blk::kValScales)[(w >> 2) * kPage + r] = dv;
+        }
+      }
+    }
+    __syncthreads();
+    // value words: (four channels, eight tokens) per thread and step
+    const int o_lo = lo >> 3, o_hi = (hi + 7) >> 3;
+    uint4* out = reinterpret_cast<uint4*>(blk + Blk::kValCodes);
+    for (int i = tid; i < (o_hi - o_lo) * (D / 4); i += kAppendThreads) {
+      const int cq = i % (D / 4), o = o_lo + i / (D / 4);
+      uint32_t v[4] = {0, 0, 0, 0}, keep = 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int r = 8 * o + e;
+        if (r < lo || r >= hi) {
+          keep |= 0xFu << (4 * nibble_of(e));
+          continue;
+        }
+        const uint32_t q = *reinterpret_cast<const uint32_t*>(&codes[r][4 * cq]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) v[c] |= ((q >> (8 * c)) & 15u) << (4 * nibble_of(e));
+      }
+      uint4* dst = out + Blk::val_word(4 * cq, o) / 4;
+      if (keep) {
+        const uint4 old = *dst;
+        v[0] |= old.x & keep;
+        v[1] |= old.y & keep;
+        v[2] |= old.z & keep;
+        v[3] |= old.w & keep;
+      }
+      *dst = make_uint4(v[0], v[1], v[2], v[3]);
+    }
+  }
+  // the request's last CTA advances its length: every other one has read it before taking its ticket
+  __syncthreads();
+  if (tid == 0) {
+    __threadfence();
+    const int all = static_cast<int>(gridDim.y * gridDim.z) * p.c.layers;
+    if (atomicAdd(&p.c.ticket[b], 1) == all - 1) {
+      p.c.ticket[b] = 0;
+      if (ok) p.c.seq_len[b] = len + cnt;
+    }
+  }
+}
+
+__device__ __forceinline__ void store_out(float* p, float x) { *p = x; }
+__device__ __forceinline__ void store_out(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
+
+// One CTA per (request and layer, page of the range, kv head); a thread takes one word at a time.
+template <typename T, int D>
+__global__ void __launch_bounds__(kAppendThreads) kv4_read_kernel(KvReadParams p) {
+  using Blk = KvBlock<D>;
+  const int bl = blockIdx.x, b = bl / p.c.layers, l = bl % p.c.layers;
+  const int h = blockIdx.z, tid = threadIdx.x;
+  const int len = p.c.seq_len[b], t0 = p.start ? p.start[b] : 0;
+  const bool ok = t0 >= 0 && len >= 0 && len <= static_cast<long long>(p.c.pages_max) * kPage;
+  if (!ok && tid == 0) device_error(p.c.err, GDN_DEVERR_CACHE, b);
+  // tokens of this page, as offsets from t0: [lo, hi); those past the length are zeros
+  const long long base = (ok ? t0 / kPage + static_cast<long long>(blockIdx.y) : blockIdx.y) * kPage;
+  const long long first = base - (ok ? t0 : 0);
+  const int lo = static_cast<int>(max(0ll, first)) , hi = static_cast<int>(min(static_cast<long long>(p.n_rows), first + kPage));
+  if (lo >= hi) return;
+  const int rl = static_cast<int>(lo - first), rh = static_cast<int>(hi - first);   // rows of the page
+  int live = ok && len > base ? static_cast<int>(min(static_cast<long long>(kPage), len - base)) : 0;
+  const char* blk = nullptr;
+  if (live > 0) {
+    const int g = p.c.page_table[static_cast<size_t>(b) * p.c.pages_max + base / kPage];
+    if (g >= 0 && g < p.c.n_pages) {
+      blk = kv_block<D>(p.c, p.Hkv, g, l, h);
+    } else {
+      if (tid == 0) device_error(p.c.err, GDN_DEVERR_CACHE, b);
+      live = 0;
+    }
+  }
+  const size_t row = static_cast<size_t>(p.Hkv) * D;
+  const size_t out0 = (static_cast<size_t>(bl) * p.n_rows) * row + static_cast<size_t>(h) * D;
+  T* ko = static_cast<T*>(p.k_out) + out0;
+  T* vo = static_cast<T*>(p.v_out) + out0;
+  for (int i = tid; i < (rh - rl) * (D / 8); i += kAppendThreads) {
+    const int r = rl + i / (D / 8), w = i % (D / 8);
+    float x[8];
+    uint32_t word = 0;
+    float d = 0.f;
+    if (r < live) {
+      word = reinterpret_cast<const uint32_t*>(blk)[Blk::key_word(r, w)];
+      d = __half2float(reinterpret_cast<const __half*>(blk + Blk::kKeyScales)[r * Blk::kGroups + (w >> 2)]);
+    }
+    T* dst = ko + (first + r) * static_cast<long long>(row) + 8 * w;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      x[e] = r < live ? static_cast<float>(static_cast<int>((word >> (4 * nibble_of(e))) & 15u) - 8) * d : 0.f;
+      store_out(dst + e, x[e]);
+    }
+  }
+  for (int i = tid; i < 8 * D; i += kAppendThreads) {
+    const int c = i % D, o = i / D;
+    if (8 * o + 8 <= rl || 8 * o >= rh) continue;
+    const uint32_t word =
+        8 * o < live ? reinterpret_cast<const uint32_t*>(blk + Blk::kValCodes)[Blk::val_word(c, o)] : 0u;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int r = 8 * o + e;
+      if (r < rl || r >= rh) continue;
+      float x = 0.f;
+      if (r < live)
+        x = static_cast<float>(static_cast<int>((word >> (4 * nibble_of(e))) & 15u) - 8) *
+            __half2float(reinterpret_cast<const __half*>(blk + Blk::kValScales)[(c / kGroup) * kPage + r]);
+      store_out(vo + (first + r) * static_cast<long long>(row) + c, x);
+    }
+  }
+}
+
+template <typename T, int D>
+cudaError_t append_t(const KvAppendParams& p, cudaStream_t s) {
+  // pages that n_rows rows can touch, at any offset
+  const dim3 grid(p.c.B * p.c.layers, (p.n_rows + kPage - 2) / kPage + 1, p.Hkv);
+  kv4_append_kernel<T, D><<<grid, kAppendThreads, 0, s>>>(p);
+  return cudaGetLastError();
+}
+template <typename T, int D>
+cudaError_t read_t(const KvReadParams& p, cudaStream_t s) {
+  const dim3 grid(p.c.B * p.c.layers, (p.n_rows + kPage - 2) / kPage + 1, p.Hkv);
+  kv4_read_kernel<T, D><<<grid, kAppendThreads, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+#define GDN_KV4_BY_SIZE(fn, T, p, s) \
+  ((p).D == 256 ? fn<T, 256>(p, s) : (p).D == 128 ? fn<T, 128>(p, s) : fn<T, 64>(p, s))
+
+cudaError_t launch_kv4_append(const KvAppendParams& p, cudaStream_t s) {
+  return p.dtype == GDN_DTYPE_BF16 ? GDN_KV4_BY_SIZE(append_t, __nv_bfloat16, p, s) : GDN_KV4_BY_SIZE(append_t, float, p, s);
+}
+cudaError_t launch_kv4_read(const KvReadParams& p, cudaStream_t s) {
+  return p.out_dtype == GDN_DTYPE_BF16 ? GDN_KV4_BY_SIZE(read_t, __nv_bfloat16, p, s) : GDN_KV4_BY_SIZE(read_t, float, p, s);
+}
+
+}  // namespace gdn

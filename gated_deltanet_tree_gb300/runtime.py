@@ -128,3 +128,200 @@ def paths_tensor(paths: Sequence[Sequence[int]], n_max: int, device) -> tuple:
         P[b, :len(p)] = p
         L[b] = len(p)
     return torch.from_numpy(P).to(device), torch.from_numpy(L).to(device)
+
+
+def _dtype_code(dtype: torch.dtype, what: str) -> int:
+    codes = {torch.float32: N.GDN_DTYPE_F32, torch.bfloat16: N.GDN_DTYPE_BF16}
+    if dtype not in codes:
+        raise TypeError(f"{what} is {dtype}: fp32 and bf16 are supported")
+    return codes[dtype]
+
+
+def make_attn_dims(Hq: int, Hkv: int, D: int, dtype: torch.dtype = torch.bfloat16,
+                   scale: Optional[float] = None) -> N.gdn_attn_dims:
+    """Shapes of one full-attention layer; scale defaults to 1 / sqrt(D)."""
+    return N.gdn_attn_dims(Hq=Hq, Hkv=Hkv, D=D, dtype=_dtype_code(dtype, "dtype"),
+                           scale=D ** -0.5 if scale is None else scale, q_row=0, kv_row=0)
+
+
+def _row_stride(t: torch.Tensor, name: str, shape: tuple) -> int:
+    """Elements from one node's row of t [B, layers, n, heads, D] to the next; rows of a fused projection (a slice of
+    wider rows) are taken as they lie."""
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, the call needs {shape}")
+    B, L, n, H, D = shape
+    row = t.stride(2) if n > 1 else (t.stride(1) if L > 1 else t.stride(0) if B > 1 else H * D)
+    want = (L * n * row, n * row, row, D, 1)
+    for size, got, need in zip(shape, t.stride(), want):
+        if size > 1 and got != need:
+            raise ValueError(f"{name} has strides {t.stride()}: rows need one stride, heads and channels contiguous")
+    return row
+
+
+class KV4Cache:
+    """The paged 4-bit key/value cache of a stack of full-attention layers: the pool, page table and lengths the
+    caller gives (or empty() makes) and the counters and workspace of the calls on them."""
+
+    def __init__(self, dims: N.gdn_attn_dims, pool: torch.Tensor, page_table: torch.Tensor, seq_len: torch.Tensor):
+        if pool.dim() != 4 or pool.dtype != torch.uint8 or tuple(pool.shape[2:]) != (dims.Hkv, 72 * dims.D):
+            raise ValueError(f"pool is [layers, n_pages, Hkv, 72 D] uint8, got {tuple(pool.shape)} {pool.dtype}")
+        for t, name, nd in ((page_table, "page_table", 2), (seq_len, "seq_len", 1)):
+            if t.dtype != torch.int32 or t.dim() != nd:
+                raise ValueError(f"{name} is int32 with {nd} dimensions, got {tuple(t.shape)} {t.dtype}")
+        if page_table.shape[0] != seq_len.shape[0]:
+            raise ValueError("page_table and seq_len disagree on the number of requests")
+        for t in (pool, page_table, seq_len):
+            if not t.is_contiguous() or t.device != pool.device:
+                raise ValueError("pool, page_table and seq_len are contiguous tensors of one device")
+        self.dims = N.gdn_attn_dims.from_buffer_copy(dims)     # its row strides follow each call's tensors
+        self.pool, self.page_table, self.seq_len = pool, page_table, seq_len
+        self.device = pool.device
+        self.B, self.layers, self.pages_max = seq_len.shape[0], pool.shape[0], page_table.shape[1]
+        self.ticket = torch.zeros(self.B, dtype=torch.int32, device=self.device)
+        self.err = torch.zeros(4, dtype=torch.int32, device=self.device)
+        self.workspace: Optional[torch.Tensor] = None
+        self.ws_bytes: dict = {}
+        self.struct = N.gdn_kv4_cache(pool=pool.data_ptr(), page_table=page_table.data_ptr(),
+                                      seq_len=seq_len.data_ptr(), ticket=self.ticket.data_ptr(),
+                                      err=self.err.data_ptr(), B=self.B, layers=self.layers,
+                                      pages_max=self.pages_max, n_pages=pool.shape[1])
+
+    @classmethod
+    def empty(cls, dims: N.gdn_attn_dims, B: int, layers: int, pages_max: int, device="cuda") -> "KV4Cache":
+        """A cache of pages_max pages (of 64 tokens) a request, each request's pages consecutive, all lengths 0."""
+        pool = torch.zeros(layers, B * pages_max, dims.Hkv, 72 * dims.D, dtype=torch.uint8, device=device)
+        table = torch.arange(B * pages_max, dtype=torch.int32, device=device).view(B, pages_max)
+        return cls(dims, pool, table, torch.zeros(B, dtype=torch.int32, device=device))
+
+    def _check_type(self, t: torch.Tensor, name: str):
+        if _dtype_code(t.dtype, name) != self.dims.dtype or t.device != self.device:
+            raise ValueError(f"{name} is {t.dtype} on {t.device}: not the cache's type or device")
+
+    def _check_i32(self, t: torch.Tensor, name: str, shape: tuple):
+        if t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous() or t.device != self.device:
+            raise ValueError(f"{name} is a contiguous int32 tensor {shape} on {self.device}, got {tuple(t.shape)} "
+                             f"{t.dtype} on {t.device}")
+
+    def _rows(self, k: torch.Tensor, v: torch.Tensor) -> int:
+        d = self.dims
+        if k.dim() != 5:
+            raise ValueError(f"k_new is [B, layers, n, Hkv, D], got {tuple(k.shape)}")
+        n = k.shape[2]
+        row = 0
+        for t, name in ((k, "k_new"), (v, "v_new")):
+            self._check_type(t, name)
+            row = _row_stride(t, name, (self.B, self.layers, n, d.Hkv, d.D))
+            d.kv_row = row if name == "k_new" else d.kv_row
+        if row != d.kv_row:
+            raise ValueError("k_new and v_new have different row strides")
+        return n
+
+    def append(self, k_new: torch.Tensor, v_new: torch.Tensor, count: torch.Tensor,
+               path: Optional[torch.Tensor] = None, stream=None):
+        """Quantise rows k_new, v_new [B, layers, n, Hkv, D] into the cache: the first count[b], or the rows path[b]
+        names, and advance the lengths (on the device)."""
+        n = self._rows(k_new, v_new)
+        self._check_i32(count, "count", (self.B,))
+        if path is not None:
+            self._check_i32(path, "path", (self.B, n))
+        N.gdn_kv4_append(self.dims, self.layers, n, k_new, v_new, path, count, self.struct, stream)
+
+    def read(self, start: Optional[torch.Tensor], n: int, dtype: torch.dtype = torch.float32, stream=None):
+        """Values of tokens start[b] .. start[b] + n - 1 (None: from 0) -> k, v [B, layers, n, Hkv, D]; zeros past a
+        request's length."""
+        if start is not None:
+            self._check_i32(start, "start", (self.B,))
+        shape = (self.B, self.layers, n, self.dims.Hkv, self.dims.D)
+        k = torch.empty(shape, dtype=dtype, device=self.device)
+        v = torch.empty(shape, dtype=dtype, device=self.device)
+        N.gdn_kv4_read(self.dims, self.layers, n, start, _dtype_code(dtype, "dtype"), k, v, self.struct, stream)
+        return k, v
+
+    def _workspace(self, n_max: int, max_len: int):
+        need = self.ws_bytes.get((n_max, max_len))
+        if need is None:
+            most = max_len if max_len else self.pages_max * N.GDN_KV4_PAGE
+            need = N.gdn_kv4_workspace_bytes(self.dims, self.B, self.layers, n_max,
+                                             min(most, self.pages_max * N.GDN_KV4_PAGE))
+            self.ws_bytes[(n_max, max_len)] = need
+        if self.workspace is None or self.workspace.numel() < need:
+            self.workspace = torch.zeros(max(need, 256), dtype=torch.uint8, device=self.device)
+        return need
+
+    def attention(self, q: torch.Tensor, k_new: Optional[torch.Tensor], v_new: Optional[torch.Tensor],
+                  out: torch.Tensor, sched: Optional[DeviceSchedule] = None, max_len: int = 0, stream=None):
+        """Nodes q [B, layers, n_max, Hq, D] attend to the cached tokens and (with k_new, v_new) to their ancestors'
+        and their own rows; sched None: one node a request.  max_len bounds the lengths where the host knows it."""
+        d = self.dims
+        n = 1 if sched is None else sched.struct.n_max
+        self._check_type(q, "q")
+        self._check_type(out, "out")
+        d.q_row = _row_stride(q, "q", (self.B, self.layers, n, d.Hq, d.D))
+        if tuple(out.shape) != tuple(q.shape) or not out.is_contiguous():
+            raise ValueError("out is contiguous with the shape of q")
+        if (k_new is None) != (v_new is None):
+            raise ValueError("k_new and v_new: both or neither")
+        if k_new is not None and self._rows(k_new, v_new) != n:
+            raise ValueError("k_new and q have different node counts")
+        self._workspace(n, max_len)
+        N.gdn_kv4_attention(d, self.layers, None if sched is None else sched.struct, q, k_new, v_new, out, self.struct,
+                            max_len, self.workspace, self.workspace.numel(), stream)
+
+    def check_error(self, stream=None):
+        N.gdn_check_error_words(self.err, stream)
+
+
+class TreeAcceptor:
+    """Outputs, error words and workspace of the acceptance of drafted tokens for one batch shape."""
+
+    def __init__(self, B: int, n_max: int, V: int, device="cuda"):
+        self.B, self.n_max, self.V = B, n_max, V
+        self.device = torch.device(device)
+        i32 = dict(dtype=torch.int32, device=self.device)
+        self.path = torch.full((B, n_max), -1, **i32)
+        self.len = torch.zeros(B, **i32)
+        self.next = torch.zeros(B, **i32)
+        self.err = torch.zeros(4, **i32)
+        self.ws_bytes = N.gdn_accept_workspace_bytes(B, n_max, V)
+        self.workspace = torch.zeros(max(self.ws_bytes, 256), dtype=torch.uint8, device=self.device)
+
+    def _rows(self, t: torch.Tensor, name: str) -> int:
+        want = (self.B, self.n_max, self.V)
+        if tuple(t.shape) != want or t.device.type != self.device.type:
+            raise ValueError(f"{name} is {want} on {self.device}, got {tuple(t.shape)} on {t.device}")
+        row = t.stride(1) if self.n_max > 1 else t.stride(0) if self.B > 1 else self.V
+        if (self.V > 1 and t.stride(2) != 1) or (self.B > 1 and t.stride(0) != self.n_max * row):
+            raise ValueError(f"{name} has strides {t.stride()}: rows need one stride and contiguous values")
+        return row
+
+    def _small(self, t: Optional[torch.Tensor], name: str, shape: tuple, dtype: torch.dtype):
+        if t is None:
+            raise ValueError(f"{name} is needed where a temperature is given")
+        if tuple(t.shape) != shape or t.dtype != dtype or not t.is_contiguous():
+            raise ValueError(f"{name} is a contiguous {dtype} tensor {shape}, got {tuple(t.shape)} {t.dtype}")
+
+    def accept(self, sched: DeviceSchedule, logits: torch.Tensor, tokens: torch.Tensor,
+               uniform: Optional[torch.Tensor] = None, gumbel: Optional[torch.Tensor] = None,
+               temperature: Optional[torch.Tensor] = None, draft_probs: Optional[torch.Tensor] = None, stream=None):
+        """Walk every request's tree -> (path [B, n_max] padded with -1, len [B], next [B]), this object's buffers;
+        path and len go into TreeVerifier.commit and KV4Cache.append as they are.  temperature None: greedy."""
+        row = self._rows(logits, "logits")
+        self._small(tokens, "tokens", (self.B, self.n_max), torch.int32)
+        if sched.struct.B != self.B or sched.struct.n_max != self.n_max:
+            raise ValueError("the schedule's batch is not this object's")
+        if temperature is not None:
+            self._small(temperature, "temperature", (self.B,), torch.float32)
+            self._small(uniform, "uniform", (self.B, self.n_max), torch.float32)
+            self._small(gumbel, "gumbel", (self.B, self.V), torch.float32)
+        draft = N.GDN_DTYPE_F32
+        if draft_probs is not None:
+            draft = _dtype_code(draft_probs.dtype, "draft_probs")
+            if self._rows(draft_probs, "draft_probs") != row:
+                raise ValueError("draft_probs and logits have different row strides")
+        N.gdn_tree_accept(sched.struct, self.V, row, _dtype_code(logits.dtype, "logits"), logits, tokens, draft_probs,
+                          draft, uniform, gumbel, temperature, self.path, self.len, self.next, self.err,
+                          self.workspace, self.workspace.numel(), stream)
+        return self.path, self.len, self.next
+
+    def check_error(self, stream=None):
+        N.gdn_check_error_words(self.err, stream)

@@ -52,7 +52,7 @@
 extern "C" {
 #endif
 
-#define GDN_ABI_VERSION 2
+#define GDN_ABI_VERSION 3
 #define GDN_MAX_NODES 64   /* largest tree (n_max) the kernels accept */
 #define GDN_MAX_TAPS 8     /* largest conv kernel K */
 
@@ -66,7 +66,9 @@ typedef enum {
   GDN_ERR_TIMEOUT = -6,       /* (device) a bounded wait on an asynchronous copy or MMA gave up */
   GDN_ERR_CAPACITY = -7,      /* a buffer is smaller than the call needs */
   GDN_ERR_STATE = -8,         /* calls out of order (commit without a verify) */
-  GDN_ERR_SCHEDULE = -9       /* (device) packed schedule words out of range */
+  GDN_ERR_SCHEDULE = -9,      /* (device) packed schedule words out of range */
+  GDN_ERR_CACHE = -10,        /* (device) a cache length, page number or row count is out of range */
+  GDN_ERR_LOGITS = -11        /* (device) a visited logits row holds no distribution, or a temperature is negative or not finite */
 } gdn_status;
 
 typedef enum { GDN_DTYPE_F32 = 0, GDN_DTYPE_BF16 = 1 } gdn_dtype;
@@ -75,6 +77,8 @@ typedef enum { GDN_DTYPE_F32 = 0, GDN_DTYPE_BF16 = 1 } gdn_dtype;
 #define GDN_DEVERR_INVALID_PATH 1  /* an accepted path is not a root path; nothing committed */
 #define GDN_DEVERR_SCHEDULE 2      /* packed schedule words out of range; the access was skipped */
 #define GDN_DEVERR_TIMEOUT 4       /* an asynchronous copy or MMA did not complete in time; the CTA stopped */
+#define GDN_DEVERR_CACHE 8         /* 4-bit cache: length, page number or row count out of range; the access was skipped */
+#define GDN_DEVERR_LOGITS 16       /* acceptance: a visited row has a NaN, a +inf or no finite logit; the walk stopped there */
 
 /* Shapes and modes of one GDN layer stack. */
 typedef struct {
@@ -363,6 +367,157 @@ gdn_status gdn_commit_fold(const gdn_dims* d, int32_t layers, const gdn_batch_sc
  * ------------------------------------------------------------------------- */
 gdn_status gdn_finish(const gdn_dims* d, int32_t B, int32_t layers, float* state, float* conv_state,
                       gdn_banks* banks, cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Paged 4-bit key/value cache of the full-attention layers between the GDN ones
+ * (Luce DFlash README, "Architecture note": every fourth qwen35 layer is full
+ * softmax attention; its flag table holds such caches in blocks of 4-bit codes).
+ *
+ * A head's key or value row of D channels is held as D / 32 groups.  With m the
+ * group's element of largest magnitude (the lowest channel on ties),
+ *   d = fp16(bf16(-m / 8)), saturated to +-2720,  code = clamp(rint(x / d), -8, 7),
+ * the element stands for code * d; m itself is code -8 (of a bf16 m, exactly).
+ * With eight significant bits and that limit, code * d and the 16 d and 24 d that
+ * unpacking it takes are exact in fp16.  A zero group has d = 0.
+ * A group with a NaN or an infinity has d = NaN: all its elements read as NaN.
+ *
+ * Pages hold GDN_KV4_PAGE tokens.  pool is [layers][n_pages][Hkv][72 D bytes];
+ * page_table[b][p] is the page of tokens 64 p .. 64 p + 63 of request b, in every
+ * layer.  One 72 D-byte block (token r of the page, channel c, codes + 8):
+ *   [0, 32 D)      key codes: token r has D / 32 chunks of 16 bytes (chunk c/32 =
+ *                  its group), D / 2 bytes a token; chunk j is stored at place
+ *                  j ^ x(r), x(r) = ((r & 1) << 2) | ((r >> 1) & 3) for D = 256,
+ *                  (r >> 1) & 3 for D = 128, (r >> 2) & 1 for D = 64, which spreads
+ *                  the same chunk of eight adjacent tokens over all banks
+ *   [32 D, 36 D)   key scales d, fp16 [64][D / 32]
+ *   [36 D, 68 D)   value codes, tokens along the words: word (c, r / 8) is number
+ *                  ((r/32 * D/4 + c/4) * 4 + r/8 % 4) * 4 + c % 4
+ *   [68 D, 72 D)   value scales d, fp16 [D / 32][64]
+ * A word holds eight codes (eight channels of a key, eight tokens of a value
+ * channel): element 2p in nibble p, element 2p + 1 in nibble p + 4.
+ * ------------------------------------------------------------------------- */
+#define GDN_KV4_PAGE 64
+
+typedef struct {
+  int32_t Hq, Hkv;     /* query and key/value heads; Hq % Hkv == 0; query head h reads kv head h / (Hq / Hkv) */
+  int32_t D;           /* head size: 64, 128 or 256 */
+  int32_t dtype;       /* gdn_dtype of q, k_new, v_new and out */
+  float scale;         /* multiplies q . k before the softmax */
+  int32_t q_row;       /* elements from one node's q row to the next; 0: Hq * D (rows of a fused projection: its width) */
+  int32_t kv_row;      /* the same of k_new and v_new; 0: Hkv * D.  Row strides are multiples of 16 bytes */
+} gdn_attn_dims;
+
+typedef struct {
+  void* pool;                 /* device, [layers][n_pages][Hkv][72 D] bytes */
+  const int32_t* page_table;  /* device, [B][pages_max] */
+  int32_t* seq_len;           /* device, [B]: committed tokens, advanced by gdn_kv4_append */
+  int32_t* ticket;            /* device, [B]: zeroed by the caller before first use, zero again after every call */
+  int32_t* err;               /* device, [4]: error words as gdn_banks.err, zeroed before first use */
+  int32_t B, layers, pages_max;
+  int64_t n_pages;
+} gdn_kv4_cache;
+
+/* Bytes of a pool of n_pages pages (0 on invalid arguments). */
+size_t gdn_kv4_pool_bytes(const gdn_attn_dims* d, int32_t layers, int64_t n_pages);
+
+/* ---------------------------------------------------------------------------
+ * gdn_kv4_append -- quantise rows into the cache and advance the lengths.
+ *   k_new, v_new [B][layers][n_rows][Hkv][D]  dtype (row stride d->kv_row)
+ *   count [B] device int32: rows of request b to append, 0..n_rows
+ *   path  [B][n_rows] device int32: row i appended is k_new[path[i]] (an accepted
+ *         path, as gdn_commit_fold takes it); NULL: rows 0, 1, .. count - 1
+ * The lengths are read and advanced on the device, so acceptance needs no host
+ * round trip.  A request whose length, count, path entries or page numbers are
+ * out of range, or whose pages are too few, appends nothing and sets
+ * GDN_DEVERR_CACHE.  Several calls appending to one cache must not overlap.
+ * ------------------------------------------------------------------------- */
+gdn_status gdn_kv4_append(const gdn_attn_dims* d, int32_t layers, int32_t n_rows, const void* k_new,
+                          const void* v_new, const int32_t* path, const int32_t* count, gdn_kv4_cache* cache,
+                          cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * gdn_kv4_read -- the values of cached rows (export, checkpoints, tests).
+ *   start [B] device int32 (NULL: 0): first token of request b
+ *   k_out, v_out [B][layers][n_rows][Hkv][D] out_dtype: tokens start .. start +
+ *   n_rows - 1; rows at or past the request's length are written as zeros.
+ * ------------------------------------------------------------------------- */
+gdn_status gdn_kv4_read(const gdn_attn_dims* d, int32_t layers, int32_t n_rows, const int32_t* start,
+                        int32_t out_dtype, void* k_out, void* v_out, const gdn_kv4_cache* cache,
+                        cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * gdn_kv4_attention -- softmax attention of drafted nodes (or single tokens)
+ * over the cached tokens and the draft's own rows.
+ *   out[i] = sum_t w_t v_t,  w = softmax(scale * q_i . k_t)
+ * over the request's seq_len committed tokens and, where k_new is given, the
+ * nodes on the root path of node i (itself included), read from k_new / v_new
+ * unquantised.  A row that sees nothing (no token cached, k_new NULL) is zero.
+ * What a row does not see does not reach it, NaN and infinities included.
+ *   sched  the batch's packed schedule; NULL: one node per request (n_max = 1)
+ *   q      [B][layers][n_max][Hq][D]  dtype (row stride d->q_row)
+ *   k_new, v_new [B][layers][n_max][Hkv][D] dtype (row stride d->kv_row), or both
+ *          NULL: attend to the cache alone (rows appended before the call)
+ *   out    [B][layers][n_max][Hq][D]  dtype, contiguous; rows of nodes >= n[b]
+ *          are neither read nor written
+ *   max_len  upper bound of the requests' lengths known to the host, 0: unknown.
+ *          It only sizes the split of the work: a longer request is still correct.
+ *   workspace  >= gdn_kv4_workspace_bytes(...) bytes of device memory, zeroed by
+ *          the caller before its first use (its counters are zero after each call)
+ * bf16 products run on the tensor cores in fp16 with fp32 accumulation: codes
+ * times scales are exact in fp16, q is scaled per row to fp16's range (a power of
+ * two) and the weights are rounded to fp16.  fp32 calls stay in fp32 throughout.
+ * ------------------------------------------------------------------------- */
+size_t gdn_kv4_workspace_bytes(const gdn_attn_dims* d, int32_t B, int32_t layers, int32_t n_max, int32_t max_len);
+gdn_status gdn_kv4_attention(const gdn_attn_dims* d, int32_t layers, const gdn_batch_schedule* sched, const void* q,
+                             const void* k_new, const void* v_new, void* out, const gdn_kv4_cache* cache,
+                             int32_t max_len, void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * gdn_tree_accept -- which drafted nodes the target accepts, from given random
+ * numbers (SpecLA article, "延迟融合提交": the accepted path the commit takes; the
+ * pages leave acceptance to the engine).
+ *
+ * The walk starts at the root.  At a node, p = softmax(logits / temperature) is
+ * the target's distribution of the next token; the children are tried in index
+ * order and the first accepted one is descended to, until none is.
+ *  - draft_probs NULL: the drafted tokens were chosen, not sampled.  Child j is
+ *    accepted if u_j * (1 - sum of p over tokens tried before) < p(t_j); a
+ *    repeated token is not accepted again.
+ *  - draft_probs given (siblings drawn independently from q = the node's row):
+ *    child j is accepted if u_j * q(t_j) < (p(t_j) - c_j q(t_j))+ / N_j, with
+ *    c_0 = 0, N_0 = 1, c_{j+1} = c_j + N_j, N_{j+1} = sum (p - c_{j+1} q)+.
+ * The next token is then drawn from what is left at the node -- p without the
+ * tried tokens, or (p - c q)+ with the c after the last rejection (p itself where
+ * nothing is left) -- as the lowest index of the largest log weight + gumbel.
+ * Either way the tokens are distributed as the target's own samples.  With
+ * temperature 0 a child is accepted if its token is the lowest index of the
+ * row's largest logit, which is also the next token.
+ *   logits  [B][n_max] rows of V values, logits_dtype, v_stride elements apart
+ *           (0: V); -inf masks a token.  Rows may have any alignment
+ *   tokens  [B][n_max] int32: each node's token (the root's is not read); one
+ *           outside [0, V) is never accepted
+ *   draft_probs [B][n_max] rows as logits, draft_dtype; NULL as above
+ *   uniform [B][n_max] fp32 in [0, 1); gumbel [B][V] fp32, independent standard
+ *           Gumbel numbers; temperature [B] fp32.  temperature NULL: all 0, and
+ *           then uniform and gumbel may be NULL
+ *   path    [B][n_max] int32 out: the accepted nodes, root first, then -1
+ *   len     [B] int32 out (>= 1);  next [B] int32 out: the token after the path
+ * path and len are what gdn_commit_fold and gdn_kv4_append take.  A visited row
+ * with a NaN, a +inf or no finite logit, or a temperature that is negative or not finite,
+ * sets GDN_DEVERR_LOGITS in err (int32 [4], as gdn_banks.err), ends the request's
+ * walk and gives next = -1.
+ *   workspace >= gdn_accept_workspace_bytes(B, n_max, V) bytes
+ * ------------------------------------------------------------------------- */
+size_t gdn_accept_workspace_bytes(int32_t B, int32_t n_max, int32_t V);
+gdn_status gdn_tree_accept(const gdn_batch_schedule* sched, int32_t V, int32_t v_stride, int32_t logits_dtype,
+                           const void* logits, const int32_t* tokens, const void* draft_probs, int32_t draft_dtype,
+                           const float* uniform, const float* gumbel, const float* temperature, int32_t* path,
+                           int32_t* len, int32_t* next, int32_t* err, void* workspace, size_t workspace_bytes,
+                           cudaStream_t stream);
+
+/* Synchronise the stream, read and clear a caller's error words (int32 [4]) as
+ * gdn_check_error does for banks->err: of a gdn_kv4_cache or of gdn_tree_accept. */
+gdn_status gdn_check_error_words(int32_t* err, cudaStream_t stream);
 
 /* Synchronise the stream, read and clear banks->err.  Returns GDN_OK or the
  * status of a device error: GDN_ERR_INVALID_PATH, GDN_ERR_TIMEOUT or
