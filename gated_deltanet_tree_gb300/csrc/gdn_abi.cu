@@ -515,7 +515,8 @@ gdn_status gdn_kv4_attention(const gdn_attn_dims* d, int32_t layers, const gdn_b
   p.row_tiles = pl.row_tiles; p.chunks = pl.chunks; p.chunk_pages = pl.chunk_pages;
   p.done = static_cast<int32_t*>(workspace);
   p.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + pl.done_bytes);
-  cudaError_t e = gdn::launch_kv4_attention_simt(p, stream);
+  cudaError_t e = pl.kernel == gdn::kKvDec ? gdn::launch_kv4_attention_dec(p, stream)
+                                           : gdn::launch_kv4_attention_simt(p, stream);
   if (e != cudaSuccess) return cuda_fail(e, "cache attention launch");
   return GDN_OK;
 }

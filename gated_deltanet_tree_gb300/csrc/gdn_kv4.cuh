@@ -98,11 +98,14 @@ struct KvAttnPlan {
   int tile_rows, row_tiles, chunks, chunk_pages;
   size_t done_bytes, bytes;    // workspace: counters, then partial results
 };
-constexpr int kKvSimt = 0;
+constexpr int kKvSimt = 0;      // CUDA cores: fp32 calls, and what the others do not take
+constexpr int kKvDec = 1;       // at most kKvDecRows rows a kv head
+constexpr int kKvDecRows = 8;
 // Counters lead every workspace at a fixed size, so that one workspace serves calls of different shapes; with
 // more tiles than this the GPU is full without splitting the tokens.
 constexpr int kKvCounters = 16384;
 KvAttnPlan plan_kv4_attention(int Hq, int Hkv, int D, int dtype, int B, int layers, int n_max, int pages);
 cudaError_t launch_kv4_attention_simt(const KvAttnParams& p, cudaStream_t s);
+cudaError_t launch_kv4_attention_dec(const KvAttnParams& p, cudaStream_t s);
 
 }  // namespace gdn

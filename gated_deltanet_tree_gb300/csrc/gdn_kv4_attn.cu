@@ -60,7 +60,7 @@ __global__ void __launch_bounds__(kThreads) kv4_attn_simt_kernel(KvAttnParams p)
   const T* q = static_cast<const T*>(p.q);
   for (int i = tid; i < kRows * D; i += kThreads) {
     const int r = i / D, d = i % D, row = row0 + r;
-    qs[i] = r < rows ? to_f(q[(node0 + row / p.G) * p.q_row + (it.h * p.G + row % p.G) * D + d]) * p.scale : 0.f;
+    qs[i] = r < rows ? to_f(q[(node0 + row / p.G) * p.q_row + (it.h * p.G + row % p.G) * D + d]) * (p.scale * 1.4426950408889634f) : 0.f;
   }
   if (tid < kRows) {
     st_m[tid] = -INFINITY;
@@ -110,12 +110,12 @@ __global__ void __launch_bounds__(kThreads) kv4_attn_simt_kernel(KvAttnParams p)
       // a NaN score has to reach the result: fmaxf drops it, so it is carried by the weight below
       for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
       const float m0 = st_m[r], m1 = fmaxf(m0, mx);
-      const float w = (x == -INFINITY) ? 0.f : expf(x - m1);
+      const float w = (x == -INFINITY) ? 0.f : exp2f(x - m1);
       float sum = w;
       for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
       pt[lane * kRows + r] = w;
       if (lane == 0) {
-        const float c = m0 == -INFINITY ? 0.f : expf(m0 - m1);
+        const float c = m0 == -INFINITY ? 0.f : exp2f(m0 - m1);
         st_m[r] = m1;
         st_l[r] = st_l[r] * c + sum;
         st_s[r] = c;
@@ -240,18 +240,30 @@ cudaError_t simt_t(const KvAttnParams& p, cudaStream_t s) {
 
 }  // namespace
 
-// Chunks: enough CTAs for a few waves of the GPU, and no chunk shorter than two pages.
+// Which kernel takes a call, and how its tokens are split.  Up to eight rows a kv head in bf16 the cache's bytes are
+// the bound and kv4_attn_dec_kernel moves them best; everything else goes to the CUDA cores.
+//
+// Chunks: as many as fill the GPU, so that a lone request is spread over it, but none so short that
+// its own start and join cost more than its pages.
 KvAttnPlan plan_kv4_attention(int Hq, int Hkv, int D, int dtype, int B, int layers, int n_max, int pages) {
-  (void)dtype;
   KvAttnPlan pl{};
-  pl.kernel = kKvSimt;
-  pl.tile_rows = kRows;
   const long long rows = static_cast<long long>(n_max) * (Hq / Hkv);
-  pl.row_tiles = static_cast<int>((rows + kRows - 1) / kRows);
+  int want, least;                 // CTAs that fill the GPU; pages a chunk has at least
+  if (dtype == GDN_DTYPE_BF16 && rows <= kKvDecRows) {
+    pl.kernel = kKvDec;
+    pl.tile_rows = kKvDecRows;
+    want = 152 * (D == 256 ? 2 : 4) * 2;
+    least = 4;
+  } else {
+    pl.kernel = kKvSimt;
+    pl.tile_rows = kRows;
+    want = 152 * 6;
+    least = 2;
+  }
+  pl.row_tiles = static_cast<int>((rows + pl.tile_rows - 1) / pl.tile_rows);
   const long long tiles = static_cast<long long>(B) * layers * Hkv * pl.row_tiles;
-  const long long want = 152 * 6;
   long long chunks = (want + tiles - 1) / tiles;
-  const long long most = (pages + 1) / 2;
+  const long long most = (pages + least - 1) / least;
   chunks = tiles > kKvCounters ? 1 : chunks > most ? most : chunks;
   chunks = chunks < 1 ? 1 : chunks;
   pl.chunk_pages = static_cast<int>((pages + chunks - 1) / chunks);
@@ -259,7 +271,7 @@ KvAttnPlan plan_kv4_attention(int Hq, int Hkv, int D, int dtype, int B, int laye
   pl.chunks = static_cast<int>(chunks);
   pl.done_bytes = kKvCounters * sizeof(int32_t);
   pl.bytes = pl.done_bytes;
-  if (chunks > 1) pl.bytes += static_cast<size_t>(tiles) * chunks * kRows * (D + 2) * sizeof(float);
+  if (chunks > 1) pl.bytes += static_cast<size_t>(tiles) * chunks * pl.tile_rows * (D + 2) * sizeof(float);
   return pl;
 }
 

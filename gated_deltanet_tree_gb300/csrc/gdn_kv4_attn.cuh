@@ -81,7 +81,8 @@ __device__ __forceinline__ bool kv_last_chunk(const KvAttnParams& p, size_t tile
 __device__ __forceinline__ void kv_store(float* p, float x) { *p = x; }
 __device__ __forceinline__ void kv_store(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
 
-// One warp joins a row's chunks, in chunk order: out = sum_c e^{m_c - m} O_c / sum_c e^{m_c - m} l_c.
+// One warp joins a row's chunks, in chunk order: out = sum_c 2^{m_c - m} O_c / sum_c 2^{m_c - m} l_c (maxima are
+// kept in base 2).
 template <typename T, int D>
 __device__ __forceinline__ void kv_join_row(const KvAttnParams& p, size_t tile, int chunks, int tile_rows, int r, T* out) {
   const int lane = threadIdx.x & 31;
@@ -95,7 +96,7 @@ __device__ __forceinline__ void kv_join_row(const KvAttnParams& p, size_t tile, 
     const float* part = kv_part(p, tile, c, tile_rows, D) + r * (D + 2);
     const float2 ml = __ldcg(reinterpret_cast<const float2*>(part + D));
     if (ml.x == -INFINITY && ml.y == 0.f) continue;         // the chunk held nothing this row sees
-    const float w = expf(ml.x - m);
+    const float w = exp2f(ml.x - m);
     sum = fmaf(w, ml.y, sum);
 #pragma unroll
     for (int i = 0; i < D / 64; ++i) {

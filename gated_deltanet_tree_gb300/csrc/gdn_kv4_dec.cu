@@ -1,0 +1,450 @@
+// Attention over the paged 4-bit cache for few rows: at most eight (node, query
+// head) pairs share a kv head -- plain decoding, and small trees of models with
+// few query heads per kv head.  bf16 calls.
+//
+// With so few rows the cache's bytes are the bound, so the kernel is built around
+// moving and unpacking them.  A pair of warps takes a page: one bulk copy brings
+// its block (72 D bytes) into a ring of stages, each warp takes 32 of its tokens.
+// The products run on mma.m16n8k16 with the cache on the 16-wide side, which
+// wastes nothing on absent rows: S^T = K Q^T (tokens x 8 rows) and O^T = V^T P^T
+// (channels x 8 rows).  A code pair becomes two fp16 values by one mask-or -- the
+// four code bits as the top mantissa bits of 1 + n/16 -- and one fused
+// multiply-add with 16 d and -24 d, which gives (n - 8) d exactly.  The page
+// format puts a lane's codes of 32 channels (keys) or 4 channels x 8 tokens
+// (values) into one 16-byte word, in the order the fragments want; the order of
+// the tokens inside 32 is the values' and the keys follow it.
+//
+// Every warp keeps its own maximum, sum and output (fp32) and the CTA's warps
+// meet once, at the end, where the nodes' own rows are added in fp32 from
+// each row's ancestor list.  Weights are carried as 2^(x - m + 10): the offset
+// keeps weights down to 2^-34 of the largest above fp16's smallest value.
+#include "gdn_kv4_attn.cuh"
+
+namespace gdn {
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kPairs = kWarps / 2;
+constexpr int kStages = 3;
+constexpr int kRows = kKvDecRows;
+constexpr float kLift = 10.f;         // weights are scaled by 2^kLift
+constexpr float kLog2e = 1.4426950408889634f;
+
+template <int D>
+struct Smem {
+  static constexpr int kStage = KvBlock<D>::kBytes;
+  static constexpr int kQ = kPairs * kStages * kStage;             // fp16 [8][D + 8]
+  static constexpr int kQRow = D + 8;
+  static constexpr int kStat = kQ + kRows * kQRow * 2;             // float [kWarps][8][2], scale [8]
+  static constexpr int kSee = kStat + (kWarps * kRows * 2 + kRows) * 4;
+  static constexpr int kBar = kSee + GDN_MAX_NODES * 8;            // full, empty [kPairs][kStages]
+  static constexpr int kTotal = kBar + 2 * kPairs * kStages * 8 + 16;
+};
+
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+__device__ __forceinline__ uint32_t h2u(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
+__device__ __forceinline__ __half2 u2h(uint32_t u) { return *reinterpret_cast<__half2*>(&u); }
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, D == 256 ? 2 : 4) kv4_attn_dec_kernel(KvAttnParams p) {
+  using Blk = KvBlock<D>;
+  using Sm = Smem<D>;
+  extern __shared__ __align__(128) char smem_dec[];
+  __shared__ int last;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, pair = warp >> 1, kb = warp & 1;
+  const int m8 = lane >> 2, j = lane & 3;
+  const KvItem it = kv_item(p, blockIdx.x);
+  const int chunk = blockIdx.y;
+  const KvSpan sp = kv_span(p, it, chunk);
+  if (!sp.ok) {
+    if (tid == 0 && chunk == 0) device_error(p.c.err, sp.bit, it.b);
+    return;
+  }
+  if (chunk >= sp.chunks || __syncthreads_or(launch_aborted(p.c.err))) return;
+  const int rows = sp.n * p.G;
+
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem_dec + Sm::kBar);
+  uint64_t* empty = full + kPairs * kStages;
+  if (tid == 0) {
+    for (int i = 0; i < kPairs * kStages; ++i) {
+      mbar_init(&full[i]);
+      asm volatile("mbarrier.init.shared::cta.b64 [%0], 2;" ::"r"(smem_addr(&empty[i])) : "memory");
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  __syncthreads();
+
+  // this pair's pages: page_lo + pair, + kPairs, ...; a lane holds the page numbers of 32 of them at a time
+  const int pages = sp.page_hi - sp.page_lo;
+  const int mine = pages > pair ? (pages - pair + kPairs - 1) / kPairs : 0;
+  const int32_t* table = p.c.page_table + static_cast<size_t>(it.b) * p.c.pages_max + sp.page_lo + pair;
+  auto page_no = [&](int i) { return i < mine ? table[i * kPairs] : -1; };
+  int tbl = page_no(lane), tbl_next = page_no(32 + lane);       // iterations [32 k, 32 k + 32) and the next 32
+  char* stages = smem_dec + pair * kStages * Sm::kStage;
+  auto valid = [&](int g) { return g >= 0 && g < p.c.n_pages; };
+  // one lane: page of iteration i into its stage; a page number out of range completes the stage with nothing,
+  // so that stage i % kStages is in phase i / kStages whatever the pages are
+  auto fetch = [&](int i, int g) {
+    const int st = i % kStages;
+    uint64_t* bar = &full[pair * kStages + st];
+    if (valid(g)) {
+      mbar_expect(bar, Sm::kStage);
+      bulk_g2s(stages + st * Sm::kStage, kv_block<D>(p.c, p.Hkv, g, it.l, it.h), Sm::kStage, bar);
+    } else {
+      mbar_arrive(bar);
+      device_error(p.c.err, GDN_DEVERR_CACHE, it.b);
+    }
+  };
+  if (kb == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      const int g = __shfl_sync(0xffffffffu, tbl, i);
+      if (lane == 0 && i < mine) fetch(i, g);
+    }
+  }
+
+  // queries: fp16, each row scaled by a power of two that brings its largest value to [2^13, 2^14)
+  __half* qs = reinterpret_cast<__half*>(smem_dec + Sm::kQ);
+  float* st_ml = reinterpret_cast<float*>(smem_dec + Sm::kStat);
+  float* st_c = st_ml + kWarps * kRows * 2;
+  unsigned long long* see = reinterpret_cast<unsigned long long*>(smem_dec + Sm::kSee);
+  const size_t node0 = static_cast<size_t>(it.bl) * p.n_max;
+  const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q);
+  auto q_row = [&](int r) { return q + (node0 + r / p.G) * p.q_row + static_cast<size_t>(it.h * p.G + r % p.G) * D; };
+  for (int r = warp; r < kRows; r += kWarps) {
+    float x[D / 32], big = 0.f;
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i) {
+      const __nv_bfloat162 v = r < rows ? *reinterpret_cast<const __nv_bfloat162*>(q_row(r) + 64 * i + 2 * lane)
+                                        : __nv_bfloat162(__float2bfloat16(0.f), __float2bfloat16(0.f));
+      x[2 * i] = __low2float(v);
+      x[2 * i + 1] = __high2float(v);
+      big = fmaxf(big, fmaxf(fabsf(x[2 * i]), fabsf(x[2 * i + 1])));
+    }
+    for (int o = 16; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+    int e = 0;
+    if (big > 0.f && big < INFINITY) {
+      frexpf(big, &e);
+      e -= 14;
+    }
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i)
+      *reinterpret_cast<__half2*>(qs + r * Sm::kQRow + 64 * i + 2 * lane) =
+          __floats2half2_rn(ldexpf(x[2 * i], -e), ldexpf(x[2 * i + 1], -e));
+    if (lane == 0) st_c[r] = ldexpf(p.scale * kLog2e, e);
+  }
+  if (chunk == 0 && p.k_new) {
+    if (!kv_ancestors(p, it.b, sp.n, see) && tid == 0) device_error(p.c.err, GDN_DEVERR_SCHEDULE, it.b);
+  } else {
+    __syncthreads();
+  }
+  // B fragments of Q^T: step (hh, w, u) holds channels 128 hh + 32 j + 8 w + 4 u + {0,1} and {2,3} of row m8
+  constexpr int kHalves = D == 256 ? 2 : 1;
+  constexpr int kWords = D == 64 ? 2 : 4;        // words of a key chunk that this lane takes
+  uint32_t qf[kHalves][kWords][2][2];
+#pragma unroll
+  for (int hh = 0; hh < kHalves; ++hh)
+#pragma unroll
+    for (int w = 0; w < kWords; ++w)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int c = D == 64 ? 16 * j + 8 * w + 4 * u : 128 * hh + 32 * j + 8 * w + 4 * u;
+        const uint2 v = *reinterpret_cast<const uint2*>(qs + m8 * Sm::kQRow + c);
+        qf[hh][w][u][0] = v.x;
+        qf[hh][w][u][1] = v.y;
+      }
+  const float c0 = st_c[2 * j], c1 = st_c[2 * j + 1];    // of rows 2j and 2j + 1, whose scores this lane holds
+
+  float o[D / 32][2][4];
+#pragma unroll
+  for (int g = 0; g < D / 32; ++g)
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[g][x][i] = 0.f;
+  float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+  bool alive = true;
+  const __half2 k16 = __float2half2_rn(16.f), k24 = __float2half2_rn(-24.f);
+  // a word's pair i (0..3) as values: code bits at 6..9 of each half
+  auto pair_of = [&](uint32_t w, int i, __half2 a, __half2 b) {
+    const uint32_t s = i == 0 ? w << 6 : i == 1 ? w << 2 : i == 2 ? w >> 2 : w >> 6;
+    return h2u(__hfma2(u2h((s & 0x03C003C0u) | 0x3C003C00u), a, b));
+  };
+
+  for (int i = 0; i < mine && alive; ++i) {
+    if (i > 0 && (i & 31) == 0) {
+      tbl = tbl_next;
+      tbl_next = page_no(i + 32 + lane);
+    }
+    const int g = __shfl_sync(0xffffffffu, tbl, i & 31);
+    const int st = i % kStages;
+    const int toks = min(32, sp.len - (sp.page_lo + pair + i * kPairs) * kPage - 32 * kb);
+    if (!__all_sync(0xffffffffu, mbar_wait(&full[pair * kStages + st], (i / kStages) & 1))) {
+      alive = false;
+      break;
+    }
+    if (valid(g) && toks > 0) {
+      const char* blk = stages + st * Sm::kStage;
+      const uint32_t* kw = reinterpret_cast<const uint32_t*>(blk);
+      const __half* kd = reinterpret_cast<const __half*>(blk + Blk::kKeyScales);
+      // ---- S^T: M tile u holds tokens tok(2u, m8) in rows 0-7 and tok(2u + 1, m8) in rows 8-15
+      auto tok = [&](int t) { return 32 * kb + 8 * (m8 >> 1) + 2 * t + (m8 & 1); };
+      float s[2][4];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int ta = tok(2 * u), tb = tok(2 * u + 1);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) s[u][x] = 0.f;
+#pragma unroll
+        for (int hh = 0; hh < kHalves; ++hh) {
+          uint32_t wa[kWords], wb[kWords];
+          int grp;
+          if constexpr (D == 64) {
+            const uint2 va = *reinterpret_cast<const uint2*>(kw + Blk::key_word(ta, 2 * j));
+            const uint2 vb = *reinterpret_cast<const uint2*>(kw + Blk::key_word(tb, 2 * j));
+            wa[0] = va.x; wa[1] = va.y;
+            wb[0] = vb.x; wb[1] = vb.y;
+            grp = j >> 1;
+          } else {
+            const uint4 va = *reinterpret_cast<const uint4*>(kw + Blk::key_word(ta, 16 * hh + 4 * j));
+            const uint4 vb = *reinterpret_cast<const uint4*>(kw + Blk::key_word(tb, 16 * hh + 4 * j));
+            wa[0] = va.x; wa[1] = va.y; wa[2] = va.z; wa[3] = va.w;
+            wb[0] = vb.x; wb[1] = vb.y; wb[2] = vb.z; wb[3] = vb.w;
+            grp = 4 * hh + j;
+          }
+          const __half2 da = __half2half2(kd[ta * Blk::kGroups + grp]), db = __half2half2(kd[tb * Blk::kGroups + grp]);
+          const __half2 a16 = __hmul2(da, k16), a24 = __hmul2(da, k24), b16 = __hmul2(db, k16), b24 = __hmul2(db, k24);
+#pragma unroll
+          for (int w = 0; w < kWords; ++w)
+#pragma unroll
+            for (int v = 0; v < 2; ++v)
+              mma16816(s[u], pair_of(wa[w], 2 * v, a16, a24), pair_of(wb[w], 2 * v, b16, b24),
+                       pair_of(wa[w], 2 * v + 1, a16, a24), pair_of(wb[w], 2 * v + 1, b16, b24), qf[hh][w][v][0],
+                       qf[hh][w][v][1]);
+        }
+      }
+      // ---- weights: this lane holds rows 2j (x = 0, 2) and 2j + 1 (x = 1, 3)
+      float n0 = m0, n1 = m1;
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          float v = s[u][x] * ((x & 1) ? c1 : c0);
+          if (toks < 32 && tok(2 * u + (x >> 1)) - 32 * kb >= toks) v = -INFINITY;
+          s[u][x] = v;
+          if (x & 1) n1 = fmaxf(n1, v); else n0 = fmaxf(n0, v);
+        }
+#pragma unroll
+      for (int off = 4; off < 32; off <<= 1) {
+        n0 = fmaxf(n0, __shfl_xor_sync(0xffffffffu, n0, off));
+        n1 = fmaxf(n1, __shfl_xor_sync(0xffffffffu, n1, off));
+      }
+      if (__any_sync(0xffffffffu, n0 > m0 || n1 > m1)) {
+        const float f0 = m0 == -INFINITY ? 0.f : exp2f(m0 - n0), f1 = m1 == -INFINITY ? 0.f : exp2f(m1 - n1);
+        m0 = n0;
+        m1 = n1;
+        l0 *= f0;
+        l1 *= f1;
+#pragma unroll
+        for (int gg = 0; gg < D / 32; ++gg)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            o[gg][x][0] *= f0;
+            o[gg][x][1] *= f1;
+            o[gg][x][2] *= f0;
+            o[gg][x][3] *= f1;
+          }
+      }
+      // a row whose scores so far are all -inf keeps weight 0 (its maximum is not subtracted)
+      const float r0 = m0 == -INFINITY ? kLift : kLift - m0, r1 = m1 == -INFINITY ? kLift : kLift - m1;
+      uint32_t pf[2][2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x) s[u][x] = exp2f(s[u][x] + ((x & 1) ? r1 : r0));
+        l0 += s[u][0] + s[u][2];
+        l1 += s[u][1] + s[u][3];
+        pf[u][0] = transpose8x8(h2u(__floats2half2_rn(s[u][0], s[u][1])));
+        pf[u][1] = transpose8x8(h2u(__floats2half2_rn(s[u][2], s[u][3])));
+      }
+      // ---- O^T: tile (gg, x) holds channel 32 gg + 4 m8 + 2x in rows 0-7 and the next one in rows 8-15; step u
+      // takes tokens 8j + 4u .. + 3 of the 32
+      const uint4* vw = reinterpret_cast<const uint4*>(blk + Blk::kValCodes) + kb * D;
+      const __half* vd = reinterpret_cast<const __half*>(blk + Blk::kValScales) + 32 * kb + 8 * j;
+#pragma unroll
+      for (int gg = 0; gg < D / 32; ++gg) {
+        const uint4 wv = vw[(8 * gg + m8) * 4 + j];
+        uint4 dv = *reinterpret_cast<const uint4*>(vd + gg * kPage);
+        uint32_t dd[4] = {dv.x, dv.y, dv.z, dv.w};
+        if (toks < 32) {                        // scales past the length are whatever the page held
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int left = toks - (8 * j + 2 * x);
+            dd[x] = left <= 0 ? 0u : left == 1 ? dd[x] & 0xFFFFu : dd[x];
+          }
+        }
+        const uint32_t ww[4] = {wv.x, wv.y, wv.z, wv.w};
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const __half2 e0 = u2h(dd[2 * u]), e1 = u2h(dd[2 * u + 1]);
+          const __half2 a0 = __hmul2(e0, k16), b0 = __hmul2(e0, k24), a1 = __hmul2(e1, k16), b1 = __hmul2(e1, k24);
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+            mma16816(o[gg][x], pair_of(ww[2 * x], 2 * u, a0, b0), pair_of(ww[2 * x + 1], 2 * u, a0, b0),
+                     pair_of(ww[2 * x], 2 * u + 1, a1, b1), pair_of(ww[2 * x + 1], 2 * u + 1, a1, b1), pf[u][0],
+                     pf[u][1]);
+        }
+      }
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&empty[pair * kStages + st]);
+    // refill the stage of the iteration before this one: the pair's other warp has most likely left it
+    const int next = i - 1 + kStages;
+    if (kb == 0 && i > 0 && next < mine) {
+      // (32 k + 31) + 2 is the furthest this looks: within the two tables held
+      const int at = next - (i & ~31);
+      const int ga = __shfl_sync(0xffffffffu, tbl, at & 31), gb = __shfl_sync(0xffffffffu, tbl_next, at & 31);
+      if (lane == 0) {
+        if (mbar_wait(&empty[pair * kStages + (i - 1) % kStages], ((i - 1) / kStages) & 1))
+          fetch(next, at < 32 ? ga : gb);
+        else
+          alive = false;
+      }
+      alive = __shfl_sync(0xffffffffu, alive, 0);
+    }
+  }
+  if (!alive) {
+    if (lane == 0) device_error(p.c.err, GDN_DEVERR_TIMEOUT, it.b);
+    // let this pair's copies land before the CTA exits
+    for (int st = 0; st < kStages; ++st)
+      for (int par = 0; par < 2; ++par) mbar_wait(&full[pair * kStages + st], par);
+  }
+#pragma unroll
+  for (int off = 4; off < 32; off <<= 1) {
+    l0 += __shfl_xor_sync(0xffffffffu, l0, off);
+    l1 += __shfl_xor_sync(0xffffffffu, l1, off);
+  }
+  // ---- the CTA's warps meet: outputs [warp][row][D] over the stages, maxima and sums beside them
+  __syncthreads();
+  float* po = reinterpret_cast<float*>(smem_dec);
+#pragma unroll
+  for (int gg = 0; gg < D / 32; ++gg)
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int c = 32 * gg + 4 * m8 + 2 * x;
+      *reinterpret_cast<float2*>(po + (warp * kRows + 2 * j) * D + c) = make_float2(o[gg][x][0], o[gg][x][2]);
+      *reinterpret_cast<float2*>(po + (warp * kRows + 2 * j + 1) * D + c) = make_float2(o[gg][x][1], o[gg][x][3]);
+    }
+  if (lane < 4) {
+    *reinterpret_cast<float2*>(st_ml + (warp * kRows + 2 * j) * 2) = make_float2(m0, l0);
+    *reinterpret_cast<float2*>(st_ml + (warp * kRows + 2 * j + 1) * 2) = make_float2(m1, l1);
+  }
+  __syncthreads();
+
+  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out);
+  auto out_row = [&](int r) {
+    return out + (node0 + r / p.G) * (static_cast<size_t>(p.Hq) * D) + static_cast<size_t>(it.h * p.G + r % p.G) * D;
+  };
+  float* part = sp.chunks > 1 ? kv_part(p, blockIdx.x, chunk, kRows, D) : nullptr;
+  const bool with_new = chunk == 0 && p.k_new;
+  for (int r = warp; r < rows; r += kWarps) {
+    float m = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) m = fmaxf(m, st_ml[(w * kRows + r) * 2]);
+    float acc[D / 32], l = 0.f;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) acc[i] = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float mw = st_ml[(w * kRows + r) * 2], lw = st_ml[(w * kRows + r) * 2 + 1];
+      if (mw == -INFINITY && lw == 0.f) continue;
+      const float f = exp2f(mw - m);
+      l = fmaf(f, lw, l);
+#pragma unroll
+      for (int i = 0; i < D / 64; ++i) {
+        const float2 v = *reinterpret_cast<const float2*>(po + (w * kRows + r) * D + 64 * i + 2 * lane);
+        acc[2 * i] = fmaf(f, v.x, acc[2 * i]);
+        acc[2 * i + 1] = fmaf(f, v.y, acc[2 * i + 1]);
+      }
+    }
+    if (with_new) {
+      // the row's own ancestors, one at a time in fp32: what it does not see is not read
+      const __nv_bfloat16* kn = static_cast<const __nv_bfloat16*>(p.k_new) + static_cast<size_t>(it.h) * D + 2 * lane;
+      const __nv_bfloat16* vn = static_cast<const __nv_bfloat16*>(p.v_new) + static_cast<size_t>(it.h) * D + 2 * lane;
+      float2 qv[D / 64];
+#pragma unroll
+      for (int i = 0; i < D / 64; ++i)
+        qv[i] = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(q_row(r) + 64 * i + 2 * lane));
+      unsigned long long left = see[r / p.G];
+      while (left) {
+        const int t = __ffsll(static_cast<long long>(left)) - 1;
+        left &= left - 1;
+        const size_t at = (node0 + t) * p.kv_row;
+        float x = 0.f;
+        float2 vv[D / 64];
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i) {
+          const float2 kv = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(kn + at + 64 * i));
+          vv[i] = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(vn + at + 64 * i));
+          x = fmaf(qv[i].x, kv.x, fmaf(qv[i].y, kv.y, x));
+        }
+        for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+        x *= p.scale * kLog2e;
+        const float mn = fmaxf(m, x);
+        const float f = m == -INFINITY ? 0.f : exp2f(m - mn);
+        const float wt = x == -INFINITY ? 0.f : exp2f(x - mn + kLift);
+        m = mn;
+        l = fmaf(l, f, wt);
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i) {
+          acc[2 * i] = fmaf(acc[2 * i], f, wt == 0.f ? 0.f : wt * vv[i].x);
+          acc[2 * i + 1] = fmaf(acc[2 * i + 1], f, wt == 0.f ? 0.f : wt * vv[i].y);
+        }
+      }
+    }
+    if (part) {
+#pragma unroll
+      for (int i = 0; i < D / 64; ++i)
+        *reinterpret_cast<float2*>(part + r * (D + 2) + 64 * i + 2 * lane) = make_float2(acc[2 * i], acc[2 * i + 1]);
+      if (lane == 0) *reinterpret_cast<float2*>(part + r * (D + 2) + D) = make_float2(m, l);
+    } else {
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+      for (int i = 0; i < D / 64; ++i)
+        *reinterpret_cast<__nv_bfloat162*>(out_row(r) + 64 * i + 2 * lane) =
+            __floats2bfloat162_rn(acc[2 * i] * inv, acc[2 * i + 1] * inv);
+    }
+  }
+  if (!part || !kv_last_chunk(p, blockIdx.x, sp.chunks, &last)) return;
+  for (int r = warp; r < rows; r += kWarps)
+    kv_join_row<__nv_bfloat16, D>(p, blockIdx.x, sp.chunks, kRows, r, out_row(r));
+}
+
+template <int D>
+cudaError_t dec_t(const KvAttnParams& p, cudaStream_t s) {
+  auto k = kv4_attn_dec_kernel<D>;
+  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::kTotal);
+  if (e != cudaSuccess) return e;
+  const dim3 grid(static_cast<unsigned>(p.c.B) * p.layers * p.Hkv, p.chunks);
+  k<<<grid, kThreads, Smem<D>::kTotal, s>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_kv4_attention_dec(const KvAttnParams& p, cudaStream_t s) {
+  return p.D == 256 ? dec_t<256>(p, s) : p.D == 128 ? dec_t<128>(p, s) : dec_t<64>(p, s);
+}
+
+}  // namespace gdn

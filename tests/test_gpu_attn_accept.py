@@ -559,3 +559,15 @@ def test_wrapper_refusals():
                 lambda: R.make_attn_dims(4, 2, 64, dtype=torch.float16)):
         with pytest.raises((ValueError, TypeError)):
             bad()
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,n", [(4, 4, 256, 8), (2, 1, 256, 4), (8, 8, 128, 7), (8, 2, 128, 2), (2, 2, 64, 8),
+                                        (8, 4, 64, 4)])
+def test_attention_small_trees(Hq, Hkv, D, n):
+    """Trees of at most eight rows a kv head, some of them long enough to be split, with unseen NaN and infinite rows."""
+    rng = np.random.default_rng(Hq + D + n)
+    trees = [S.random_tree(m, rng) for m in (n, 1, max(1, n // 2), n, n)]
+    run_case(rng, Hq, Hkv, D, [0, 1, 65, 130, 3000], trees, "bf16")
+    run_case(rng, Hq, Hkv, D, [40, 64, 2300], [np.array([-1] + [0] * (n - 1))] * 3, "bf16", layers=2,
+             poison=[(0, n - 1), (2, 1)])
+    run_case(rng, Hq, Hkv, D, [0, 600], [S.chain_tree(n)] * 2, "bf16", new=False)
