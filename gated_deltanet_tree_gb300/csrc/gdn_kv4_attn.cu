@@ -252,7 +252,7 @@ KvAttnPlan plan_kv4_attention(int Hq, int Hkv, int D, int dtype, int B, int laye
   if (dtype == GDN_DTYPE_BF16 && rows <= kKvDecRows) {
     pl.kernel = kKvDec;
     pl.tile_rows = kKvDecRows;
-    want = 152 * (D == 256 ? 2 : 4) * 2;
+    want = 152 * 2 * 2;
     least = 4;
   } else {
     pl.kernel = kKvSimt;

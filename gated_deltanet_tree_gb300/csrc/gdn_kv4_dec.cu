@@ -23,22 +23,24 @@
 namespace gdn {
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kThreads = 32 * kWarps;
-constexpr int kPairs = kWarps / 2;
-constexpr int kStages = 3;
+constexpr int kStages = 2;
+// Warps of a CTA; two CTAs share an SM, so that one computes while the other starts or ends.  The register file
+// holds 12 warps with the 160 registers D = 256 takes, or 16 with 128.
+template <int D>
+constexpr int kWarpsOf = D == 256 ? 6 : 8;
 constexpr int kRows = kKvDecRows;
 constexpr float kLift = 10.f;         // weights are scaled by 2^kLift
 constexpr float kLog2e = 1.4426950408889634f;
 
 template <int D>
-struct Smem {
+struct Smem {   // twice this fits the 228 KB of an SM
+  static constexpr int kWarps = kWarpsOf<D>, kPairs = kWarps / 2;
   static constexpr int kStage = KvBlock<D>::kBytes;
   static constexpr int kQ = kPairs * kStages * kStage;             // fp16 [8][D + 8]
   static constexpr int kQRow = D + 8;
   static constexpr int kStat = kQ + kRows * kQRow * 2;             // float [kWarps][8][2], scale [8]
   static constexpr int kSee = kStat + (kWarps * kRows * 2 + kRows) * 4;
-  static constexpr int kBar = kSee + GDN_MAX_NODES * 8;            // full, empty [kPairs][kStages]
+  static constexpr int kBar = kSee + kRows * 8;                    // at most as many nodes as rows            // full, empty [kPairs][kStages]
   static constexpr int kTotal = kBar + 2 * kPairs * kStages * 8 + 16;
 };
 
@@ -58,9 +60,10 @@ __device__ __forceinline__ uint32_t h2u(__half2 h) { return *reinterpret_cast<ui
 __device__ __forceinline__ __half2 u2h(uint32_t u) { return *reinterpret_cast<__half2*>(&u); }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, D == 256 ? 2 : 4) kv4_attn_dec_kernel(KvAttnParams p) {
+__global__ void __launch_bounds__(32 * kWarpsOf<D>, 2) kv4_attn_dec_kernel(KvAttnParams p) {
   using Blk = KvBlock<D>;
   using Sm = Smem<D>;
+  constexpr int kWarps = Sm::kWarps, kPairs = Sm::kPairs;
   extern __shared__ __align__(128) char smem_dec[];
   __shared__ int last;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, pair = warp >> 1, kb = warp & 1;
@@ -152,18 +155,10 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : 4) kv4_attn_dec_kerne
   // B fragments of Q^T: step (hh, w, u) holds channels 128 hh + 32 j + 8 w + 4 u + {0,1} and {2,3} of row m8
   constexpr int kHalves = D == 256 ? 2 : 1;
   constexpr int kWords = D == 64 ? 2 : 4;        // words of a key chunk that this lane takes
-  uint32_t qf[kHalves][kWords][2][2];
-#pragma unroll
-  for (int hh = 0; hh < kHalves; ++hh)
-#pragma unroll
-    for (int w = 0; w < kWords; ++w)
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int c = D == 64 ? 16 * j + 8 * w + 4 * u : 128 * hh + 32 * j + 8 * w + 4 * u;
-        const uint2 v = *reinterpret_cast<const uint2*>(qs + m8 * Sm::kQRow + c);
-        qf[hh][w][u][0] = v.x;
-        qf[hh][w][u][1] = v.y;
-      }
+  auto query = [&](int hh, int w, int u) {       // read where they are used: registers go to the output
+    const int c = D == 64 ? 16 * j + 8 * w + 4 * u : 128 * hh + 32 * j + 8 * w + 4 * u;
+    return *reinterpret_cast<const uint2*>(qs + m8 * Sm::kQRow + c);
+  };
   const float c0 = st_c[2 * j], c1 = st_c[2 * j + 1];    // of rows 2j and 2j + 1, whose scores this lane holds
 
   float o[D / 32][2][4];
@@ -194,6 +189,19 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : 4) kv4_attn_dec_kerne
       alive = false;
       break;
     }
+    // refill the stage of the iteration before this one: the pair's other warp has most likely left it
+    const int next = i - 1 + kStages;
+    if (kb == 0 && i > 0 && next < mine) {
+      const int at = next - (i & ~31);      // 32 at most: within the two tables held
+      const int ga = __shfl_sync(0xffffffffu, tbl, at & 31), gb = __shfl_sync(0xffffffffu, tbl_next, at & 31);
+      if (lane == 0) {
+        if (mbar_wait(&empty[pair * kStages + (i - 1) % kStages], ((i - 1) / kStages) & 1))
+          fetch(next, at < 32 ? ga : gb);
+        else
+          alive = false;
+      }
+      alive = __shfl_sync(0xffffffffu, alive, 0);
+    }
     if (valid(g) && toks > 0) {
       const char* blk = stages + st * Sm::kStage;
       const uint32_t* kw = reinterpret_cast<const uint32_t*>(blk);
@@ -202,37 +210,41 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : 4) kv4_attn_dec_kerne
       auto tok = [&](int t) { return 32 * kb + 8 * (m8 >> 1) + 2 * t + (m8 & 1); };
       float s[2][4];
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int ta = tok(2 * u), tb = tok(2 * u + 1);
+      for (int u = 0; u < 2; ++u)
 #pragma unroll
         for (int x = 0; x < 4; ++x) s[u][x] = 0.f;
 #pragma unroll
-        for (int hh = 0; hh < kHalves; ++hh) {
-          uint32_t wa[kWords], wb[kWords];
+      for (int hh = 0; hh < kHalves; ++hh) {
+        uint32_t ww[4][kWords];
+        __half2 d16[4], d24[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
           int grp;
           if constexpr (D == 64) {
-            const uint2 va = *reinterpret_cast<const uint2*>(kw + Blk::key_word(ta, 2 * j));
-            const uint2 vb = *reinterpret_cast<const uint2*>(kw + Blk::key_word(tb, 2 * j));
-            wa[0] = va.x; wa[1] = va.y;
-            wb[0] = vb.x; wb[1] = vb.y;
+            const uint2 v = *reinterpret_cast<const uint2*>(kw + Blk::key_word(tok(t), 2 * j));
+            ww[t][0] = v.x; ww[t][1] = v.y;
             grp = j >> 1;
           } else {
-            const uint4 va = *reinterpret_cast<const uint4*>(kw + Blk::key_word(ta, 16 * hh + 4 * j));
-            const uint4 vb = *reinterpret_cast<const uint4*>(kw + Blk::key_word(tb, 16 * hh + 4 * j));
-            wa[0] = va.x; wa[1] = va.y; wa[2] = va.z; wa[3] = va.w;
-            wb[0] = vb.x; wb[1] = vb.y; wb[2] = vb.z; wb[3] = vb.w;
+            const uint4 v = *reinterpret_cast<const uint4*>(kw + Blk::key_word(tok(t), 16 * hh + 4 * j));
+            ww[t][0] = v.x; ww[t][1] = v.y; ww[t][2] = v.z; ww[t][3] = v.w;
             grp = 4 * hh + j;
           }
-          const __half2 da = __half2half2(kd[ta * Blk::kGroups + grp]), db = __half2half2(kd[tb * Blk::kGroups + grp]);
-          const __half2 a16 = __hmul2(da, k16), a24 = __hmul2(da, k24), b16 = __hmul2(db, k16), b24 = __hmul2(db, k24);
-#pragma unroll
-          for (int w = 0; w < kWords; ++w)
-#pragma unroll
-            for (int v = 0; v < 2; ++v)
-              mma16816(s[u], pair_of(wa[w], 2 * v, a16, a24), pair_of(wb[w], 2 * v, b16, b24),
-                       pair_of(wa[w], 2 * v + 1, a16, a24), pair_of(wb[w], 2 * v + 1, b16, b24), qf[hh][w][v][0],
-                       qf[hh][w][v][1]);
+          const __half2 d = __half2half2(kd[tok(t) * Blk::kGroups + grp]);
+          d16[t] = __hmul2(d, k16);
+          d24[t] = __hmul2(d, k24);
         }
+#pragma unroll
+        for (int w = 0; w < kWords; ++w)
+#pragma unroll
+          for (int v = 0; v < 2; ++v) {
+            const uint2 qv = query(hh, w, v);
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+              mma16816(s[u], pair_of(ww[2 * u][w], 2 * v, d16[2 * u], d24[2 * u]),
+                       pair_of(ww[2 * u + 1][w], 2 * v, d16[2 * u + 1], d24[2 * u + 1]),
+                       pair_of(ww[2 * u][w], 2 * v + 1, d16[2 * u], d24[2 * u]),
+                       pair_of(ww[2 * u + 1][w], 2 * v + 1, d16[2 * u + 1], d24[2 * u + 1]), qv.x, qv.y);
+          }
       }
       // ---- weights: this lane holds rows 2j (x = 0, 2) and 2j + 1 (x = 1, 3)
       float n0 = m0, n1 = m1;
@@ -309,20 +321,6 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : 4) kv4_attn_dec_kerne
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(&empty[pair * kStages + st]);
-    // refill the stage of the iteration before this one: the pair's other warp has most likely left it
-    const int next = i - 1 + kStages;
-    if (kb == 0 && i > 0 && next < mine) {
-      // (32 k + 31) + 2 is the furthest this looks: within the two tables held
-      const int at = next - (i & ~31);
-      const int ga = __shfl_sync(0xffffffffu, tbl, at & 31), gb = __shfl_sync(0xffffffffu, tbl_next, at & 31);
-      if (lane == 0) {
-        if (mbar_wait(&empty[pair * kStages + (i - 1) % kStages], ((i - 1) / kStages) & 1))
-          fetch(next, at < 32 ? ga : gb);
-        else
-          alive = false;
-      }
-      alive = __shfl_sync(0xffffffffu, alive, 0);
-    }
   }
   if (!alive) {
     if (lane == 0) device_error(p.c.err, GDN_DEVERR_TIMEOUT, it.b);
@@ -437,7 +435,7 @@ cudaError_t dec_t(const KvAttnParams& p, cudaStream_t s) {
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::kTotal);
   if (e != cudaSuccess) return e;
   const dim3 grid(static_cast<unsigned>(p.c.B) * p.layers * p.Hkv, p.chunks);
-  k<<<grid, kThreads, Smem<D>::kTotal, s>>>(p);
+  k<<<grid, 32 * kWarpsOf<D>, Smem<D>::kTotal, s>>>(p);
   return cudaGetLastError();
 }
 
