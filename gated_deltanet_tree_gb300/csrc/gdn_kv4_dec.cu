@@ -16,8 +16,10 @@
 //
 // Every warp keeps its own maximum, sum and output (fp32) and the CTA's warps
 // meet once, at the end, where the nodes' own rows are added in fp32 from
-// each row's ancestor list.  Weights are carried as 2^(x - m + 10): the offset
-// keeps weights down to 2^-34 of the largest above fp16's smallest value.
+// each row's ancestor list.  Weights are carried as 2^(x - m + 6), m the largest
+// score when the output was last rescaled, which happens only where a score passes
+// it by more than 8: weights down to 2^-30 of the largest stay above fp16's
+// smallest value and none passes its largest.
 #include "gdn_kv4_attn.cuh"
 
 namespace gdn {
@@ -29,7 +31,8 @@ constexpr int kStages = 2;
 template <int D>
 constexpr int kWarpsOf = D == 256 ? 6 : 8;
 constexpr int kRows = kKvDecRows;
-constexpr float kLift = 10.f;         // weights are scaled by 2^kLift
+constexpr float kLift = 6.f;          // weights are scaled by 2^kLift ...
+constexpr float kSlack = 8.f;         // ... against a maximum that may lag by up to 2^kSlack: 2^14 at most in fp16
 constexpr float kLog2e = 1.4426950408889634f;
 
 template <int D>
@@ -55,6 +58,11 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
   uint32_t d;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
   return d;
+}
+__device__ __forceinline__ float exp2_fast(float x) {   // results below 2^-126 are zero
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 __device__ __forceinline__ uint32_t h2u(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
 __device__ __forceinline__ __half2 u2h(uint32_t u) { return *reinterpret_cast<__half2*>(&u); }
@@ -174,7 +182,9 @@ __global__ void __launch_bounds__(32 * kWarpsOf<D>, 2) kv4_attn_dec_kernel(KvAtt
   // a word's pair i (0..3) as values: code bits at 6..9 of each half
   auto pair_of = [&](uint32_t w, int i, __half2 a, __half2 b) {
     const uint32_t s = i == 0 ? w << 6 : i == 1 ? w << 2 : i == 2 ? w >> 2 : w >> 6;
-    return h2u(__hfma2(u2h((s & 0x03C003C0u) | 0x3C003C00u), a, b));
+    uint32_t v;                               // (s & mask) | one, in one operation
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(v) : "r"(s), "r"(0x03C003C0u), "r"(0x3C003C00u));
+    return h2u(__hfma2(u2h(v), a, b));
   };
 
   for (int i = 0; i < mine && alive; ++i) {
@@ -251,18 +261,25 @@ __global__ void __launch_bounds__(32 * kWarpsOf<D>, 2) kv4_attn_dec_kernel(KvAtt
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          float v = s[u][x] * ((x & 1) ? c1 : c0);
-          if (toks < 32 && tok(2 * u + (x >> 1)) - 32 * kb >= toks) v = -INFINITY;
-          s[u][x] = v;
-          if (x & 1) n1 = fmaxf(n1, v); else n0 = fmaxf(n0, v);
-        }
+        for (int x = 0; x < 4; ++x) s[u][x] *= (x & 1) ? c1 : c0;
+      if (toks < 32) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            if (tok(2 * u + (x >> 1)) - 32 * kb >= toks) s[u][x] = -INFINITY;
+      }
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        n0 = fmaxf(n0, fmaxf(s[u][0], s[u][2]));
+        n1 = fmaxf(n1, fmaxf(s[u][1], s[u][3]));
+      }
 #pragma unroll
       for (int off = 4; off < 32; off <<= 1) {
         n0 = fmaxf(n0, __shfl_xor_sync(0xffffffffu, n0, off));
         n1 = fmaxf(n1, __shfl_xor_sync(0xffffffffu, n1, off));
       }
-      if (__any_sync(0xffffffffu, n0 > m0 || n1 > m1)) {
+      if (__any_sync(0xffffffffu, n0 > m0 + kSlack || n1 > m1 + kSlack)) {
         const float f0 = m0 == -INFINITY ? 0.f : exp2f(m0 - n0), f1 = m1 == -INFINITY ? 0.f : exp2f(m1 - n1);
         m0 = n0;
         m1 = n1;
@@ -284,7 +301,7 @@ __global__ void __launch_bounds__(32 * kWarpsOf<D>, 2) kv4_attn_dec_kernel(KvAtt
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
 #pragma unroll
-        for (int x = 0; x < 4; ++x) s[u][x] = exp2f(s[u][x] + ((x & 1) ? r1 : r0));
+        for (int x = 0; x < 4; ++x) s[u][x] = exp2_fast(s[u][x] + ((x & 1) ? r1 : r0));
         l0 += s[u][0] + s[u][2];
         l1 += s[u][1] + s[u][3];
         pf[u][0] = transpose8x8(h2u(__floats2half2_rn(s[u][0], s[u][1])));
