@@ -512,7 +512,7 @@ gdn_status gdn_kv4_attention(const gdn_attn_dims* d, int32_t layers, const gdn_b
   p.kv_row = d->kv_row ? d->kv_row : static_cast<long long>(d->Hkv) * d->D;
   p.words = sched ? sched->words : nullptr;
   p.q = q; p.k_new = k_new; p.v_new = v_new; p.out = out;
-  p.row_tiles = pl.row_tiles; p.chunks = pl.chunks; p.chunk_pages = pl.chunk_pages;
+  p.ctas = pl.ctas; p.least = pl.least; p.row_tiles = pl.row_tiles; p.chunks = pl.chunks; p.chunk_pages = pl.chunk_pages;
   p.done = static_cast<int32_t*>(workspace);
   p.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + pl.done_bytes);
   cudaError_t e = pl.kernel == gdn::kKvDec ? gdn::launch_kv4_attention_dec(p, stream)

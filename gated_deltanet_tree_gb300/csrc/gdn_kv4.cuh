@@ -87,14 +87,18 @@ struct KvAttnParams {
   const void* k_new;           // nullptr: the cache alone
   const void* v_new;
   void* out;
-  int row_tiles;               // row tiles of an item (grid)
+  int b0, bn;                  // requests of this launch (the kernels that take units)
+  int ctas, least;             // CTAs launched, and the units one takes at least where there are few
+  int each;                    // CTAs an item of a lone request can have: ctas / (layers * Hkv * row_tiles)
+  int row_tiles;               // row tiles of an item, at most
   int chunks;                  // token chunks of an item (grid)
   int chunk_pages;             // pages of a chunk, where the request is no longer than the host expects
-  float* part;                 // [items * row_tiles][chunks][tile rows][D + 2] unnormalised output, max, sum
+  float* part;                 // partial results, rows of D + 2: unnormalised output, maximum (base 2), sum
   int32_t* done;               // [kKvCounters] chunks finished of each row tile, zero between calls
 };
 struct KvAttnPlan {
   int kernel;                  // kKvSimt, ...
+  int ctas, least;
   int tile_rows, row_tiles, chunks, chunk_pages;
   size_t done_bytes, bytes;    // workspace: counters, then partial results
 };

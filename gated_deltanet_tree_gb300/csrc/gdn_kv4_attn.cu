@@ -243,23 +243,25 @@ cudaError_t simt_t(const KvAttnParams& p, cudaStream_t s) {
 // Which kernel takes a call, and how its tokens are split.  Up to eight rows a kv head in bf16 the cache's bytes are
 // the bound and kv4_attn_dec_kernel moves them best; everything else goes to the CUDA cores.
 //
-// Chunks: as many as fill the GPU, so that a lone request is spread over it, but none so short that
-// its own start and join cost more than its pages.
+// On the CUDA cores the tokens are split in as many chunks as fill the GPU, so that a lone request is spread over it,
+// but none so short that its own start and join cost more than its pages.
 KvAttnPlan plan_kv4_attention(int Hq, int Hkv, int D, int dtype, int B, int layers, int n_max, int pages) {
   KvAttnPlan pl{};
   const long long rows = static_cast<long long>(n_max) * (Hq / Hkv);
-  int want, least;                 // CTAs that fill the GPU; pages a chunk has at least
-  if (dtype == GDN_DTYPE_BF16 && rows <= kKvDecRows) {
+  pl.done_bytes = kKvCounters * sizeof(int32_t);
+  if (dtype == GDN_DTYPE_BF16 && rows <= kKvDecRows && static_cast<long long>(layers) * Hkv <= kKvCounters) {
+    // units: two CTAs an SM, and at least a page for each of a CTA's pairs of warps
     pl.kernel = kKvDec;
     pl.tile_rows = kKvDecRows;
-    want = 152 * 2 * 2;
-    least = 4;
-  } else {
-    pl.kernel = kKvSimt;
-    pl.tile_rows = kRows;
-    want = 152 * 6;
-    least = 2;
+    pl.row_tiles = 1;
+    pl.least = D == 256 ? 3 : 4;
+    pl.ctas = 152 * 2;
+    pl.bytes = pl.done_bytes + static_cast<size_t>(pl.ctas) * 2 * pl.tile_rows * (D + 2) * sizeof(float);
+    return pl;
   }
+  pl.kernel = kKvSimt;
+  pl.tile_rows = kRows;
+  const int want = 152 * 6, least = 2;      // CTAs that fill the GPU; pages a chunk has at least
   pl.row_tiles = static_cast<int>((rows + pl.tile_rows - 1) / pl.tile_rows);
   const long long tiles = static_cast<long long>(B) * layers * Hkv * pl.row_tiles;
   long long chunks = (want + tiles - 1) / tiles;
@@ -269,7 +271,6 @@ KvAttnPlan plan_kv4_attention(int Hq, int Hkv, int D, int dtype, int B, int laye
   pl.chunk_pages = static_cast<int>((pages + chunks - 1) / chunks);
   pl.chunk_pages = pl.chunk_pages < 1 ? 1 : pl.chunk_pages;
   pl.chunks = static_cast<int>(chunks);
-  pl.done_bytes = kKvCounters * sizeof(int32_t);
   pl.bytes = pl.done_bytes;
   if (chunks > 1) pl.bytes += static_cast<size_t>(tiles) * chunks * pl.tile_rows * (D + 2) * sizeof(float);
   return pl;
