@@ -515,8 +515,10 @@ gdn_status gdn_kv4_attention(const gdn_attn_dims* d, int32_t layers, const gdn_b
   p.ctas = pl.ctas; p.least = pl.least; p.row_tiles = pl.row_tiles; p.chunks = pl.chunks; p.chunk_pages = pl.chunk_pages;
   p.done = static_cast<int32_t*>(workspace);
   p.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + pl.done_bytes);
-  cudaError_t e = pl.kernel == gdn::kKvDec ? gdn::launch_kv4_attention_dec(p, stream)
-                                           : gdn::launch_kv4_attention_simt(p, stream);
+  p.desc = reinterpret_cast<int4*>(p.done + gdn::kKvCounters);
+  cudaError_t e = pl.kernel == gdn::kKvDec    ? gdn::launch_kv4_attention_dec(p, stream)
+                  : pl.kernel == gdn::kKvTree ? gdn::launch_kv4_attention_tree(p, stream)
+                                              : gdn::launch_kv4_attention_simt(p, stream);
   if (e != cudaSuccess) return cuda_fail(e, "cache attention launch");
   return GDN_OK;
 }

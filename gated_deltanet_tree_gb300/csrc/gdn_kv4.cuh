@@ -94,6 +94,7 @@ struct KvAttnParams {
   int chunks;                  // token chunks of an item (grid)
   int chunk_pages;             // pages of a chunk, where the request is no longer than the host expects
   float* part;                 // partial results, rows of D + 2: unnormalised output, maximum (base 2), sum
+  int4* desc;                  // [kKvItems] what the join of an item reads (tree kernel)
   int32_t* done;               // [kKvCounters] chunks finished of each row tile, zero between calls
 };
 struct KvAttnPlan {
@@ -105,11 +106,15 @@ struct KvAttnPlan {
 constexpr int kKvSimt = 0;      // CUDA cores: fp32 calls, and what the others do not take
 constexpr int kKvDec = 1;       // at most kKvDecRows rows a kv head
 constexpr int kKvDecRows = 8;
+constexpr int kKvTree = 2;      // tiles of kKvTreeRows rows
+constexpr int kKvTreeRows = 128;
 // Counters lead every workspace at a fixed size, so that one workspace serves calls of different shapes; with
 // more tiles than this the GPU is full without splitting the tokens.
 constexpr int kKvCounters = 16384;
+constexpr int kKvItems = 4096;  // items of a launch of the tree kernel; their join records follow the counters
 KvAttnPlan plan_kv4_attention(int Hq, int Hkv, int D, int dtype, int B, int layers, int n_max, int pages);
 cudaError_t launch_kv4_attention_simt(const KvAttnParams& p, cudaStream_t s);
 cudaError_t launch_kv4_attention_dec(const KvAttnParams& p, cudaStream_t s);
+cudaError_t launch_kv4_attention_tree(const KvAttnParams& p, cudaStream_t s);
 
 }  // namespace gdn

@@ -241,14 +241,15 @@ cudaError_t simt_t(const KvAttnParams& p, cudaStream_t s) {
 }  // namespace
 
 // Which kernel takes a call, and how its tokens are split.  Up to eight rows a kv head in bf16 the cache's bytes are
-// the bound and kv4_attn_dec_kernel moves them best; everything else goes to the CUDA cores.
+// the bound and kv4_attn_dec_kernel moves them best; with more rows kv4_attn_tree_kernel shares the unpacking among
+// them.  fp32 calls (and more layers and heads than a launch has records for) go to the CUDA cores.
 //
 // On the CUDA cores the tokens are split in as many chunks as fill the GPU, so that a lone request is spread over it,
 // but none so short that its own start and join cost more than its pages.
 KvAttnPlan plan_kv4_attention(int Hq, int Hkv, int D, int dtype, int B, int layers, int n_max, int pages) {
   KvAttnPlan pl{};
   const long long rows = static_cast<long long>(n_max) * (Hq / Hkv);
-  pl.done_bytes = kKvCounters * sizeof(int32_t);
+  pl.done_bytes = kKvCounters * sizeof(int32_t) + kKvItems * sizeof(int4);
   if (dtype == GDN_DTYPE_BF16 && rows <= kKvDecRows && static_cast<long long>(layers) * Hkv <= kKvCounters) {
     // units: two CTAs an SM, and at least a page for each of a CTA's pairs of warps
     pl.kernel = kKvDec;
@@ -256,6 +257,15 @@ KvAttnPlan plan_kv4_attention(int Hq, int Hkv, int D, int dtype, int B, int laye
     pl.row_tiles = 1;
     pl.least = D == 256 ? 3 : 4;
     pl.ctas = 152 * 2;
+    pl.bytes = pl.done_bytes + static_cast<size_t>(pl.ctas) * 2 * pl.tile_rows * (D + 2) * sizeof(float);
+    return pl;
+  }
+  pl.tile_rows = kKvTreeRows;
+  pl.row_tiles = static_cast<int>((rows + pl.tile_rows - 1) / pl.tile_rows);
+  if (dtype == GDN_DTYPE_BF16 && static_cast<long long>(layers) * Hkv * pl.row_tiles <= kKvItems) {
+    pl.kernel = kKvTree;
+    pl.least = 2;
+    pl.ctas = 152;
     pl.bytes = pl.done_bytes + static_cast<size_t>(pl.ctas) * 2 * pl.tile_rows * (D + 2) * sizeof(float);
     return pl;
   }

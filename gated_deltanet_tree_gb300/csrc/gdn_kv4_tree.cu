@@ -1,0 +1,681 @@
+// Attention over the paged 4-bit cache for trees: up to 128 (node, query head)
+// pairs that share a kv head per tile, on tcgen05.  bf16 calls.
+//
+// With tens of rows per kv head the two products are the bound (4 D operations a
+// row and token), so the rows fill a 128-row tile and the cache is unpacked to
+// fp16 in shared memory for the fifth-generation tensor cores, one page (64
+// tokens) a step.  Tensor memory (512 columns) holds everything else: the output
+// O[128][D] in fp32, the queries as the A operand of S = Q K^T, and two score
+// buffers of 64 columns; the weights overwrite the scores they came from and are
+// the A operand of O += P V.  The scores of one page are computed while the page
+// before it goes through the softmax.
+//
+// Roles (14 warps, one CTA an SM): four softmax warps, a thread a row; eight
+// unpacking warps (codes to fp16: see gdn_kv4_dec.cu); one warp issues the bulk
+// copies of the pages, one the MMAs.  They meet at mbarriers only; every wait is
+// bounded.  CTAs take equal runs of the requests' pages (KvPlace); items that two
+// or more CTAs share are joined by a second kernel, spread over the GPU.
+//
+// The nodes' own rows are one more step at the start of an item: fp16 like the
+// rest, each key row scaled to fp16's range by a power of two, the row's ancestors
+// as its mask.  A masked weight is 0, which would still turn a NaN or an infinity
+// in an unseen row into NaN inside a product; if any such value (or one beyond
+// fp16) is among the rows, that step is left out of the products and each row adds
+// its own ancestors in fp32 at the end.
+#include "gdn_kv4_attn.cuh"
+#include "gdn_umma.cuh"
+
+namespace gdn {
+namespace {
+
+constexpr int kSoftWarps = 4, kUnpackWarps = 8;
+constexpr int kCopyWarp = kSoftWarps + kUnpackWarps, kMmaWarp = kCopyWarp + 1;
+constexpr int kThreads = 32 * (kMmaWarp + 1);
+constexpr int kRows = kKvTreeRows;
+constexpr int kStages = 3;
+constexpr float kLift = 6.f;          // weights are scaled by 2^kLift ...
+constexpr float kSlack = 8.f;         // ... against a maximum that may lag by up to 2^kSlack
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kTooLarge = 6.0e4f;   // new values beyond this take the fp32 path
+
+enum Bar { kStFull = 0, kStEmpty = 3, kKFull = 6, kKEmpty = 8, kVFull = 10, kVEmpty = 12, kSFull = 14, kPFull = 16,
+           kODone = 18, kOFree = 19, kQReady = 20, kNewFull = 21, kDrain = 22, kBars = 23 };
+
+template <int D>
+struct Smem {
+  static constexpr int kStage = KvBlock<D>::kBytes;
+  // operands without swizzle: 8 rows x 16 bytes contiguous; adjacent row groups 128 bytes apart, adjacent groups of
+  // eight elements along K `kKeyK` / `kValK` bytes (the values' 16 bytes more spread the unpackers' stores over all banks)
+  static constexpr int kKeyK = kPage * 16, kValK = D * 16 + 16;
+  static constexpr int kKeyTile = (D / 8) * kKeyK, kValTile = (kPage / 8) * kValK;
+  static constexpr int kKeys = kStages * kStage;
+  static constexpr int kVals = kKeys + 2 * kKeyTile;
+  static constexpr int kSee = kVals + 2 * kValTile;                // u64 [64]
+  static constexpr int kColScale = kSee + GDN_MAX_NODES * 8;       // float [64]
+  static constexpr int kBar = kColScale + GDN_MAX_NODES * 4;
+  static constexpr int kTmem = kBar + kBars * 8;                   // tensor-memory address, flags
+  static constexpr int kTotal = kTmem + 32;
+  // tensor-memory columns
+  static constexpr int kO = 0, kQ = D, kS = D + D / 2;
+  static constexpr int kCols = D == 256 ? 512 : D == 128 ? 512 : 256;
+};
+
+__host__ __device__ constexpr uint32_t idesc_f16(int m, int n) {
+  return (1u << 4) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
+}
+// D (+)= A B^T, kind::f16 (K = 16), A in tensor memory.
+__device__ __forceinline__ void umma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, int accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld32(uint32_t ta, float (&v)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+        "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]),
+        "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]),
+        "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+      : "r"(ta)
+      : "memory");
+}
+__device__ __forceinline__ uint32_t h2u(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
+__device__ __forceinline__ __half2 u2h(uint32_t u) { return *reinterpret_cast<__half2*>(&u); }
+__device__ __forceinline__ float exp2i(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// Exponent that brings 2^e <= big < 2^(e + 1) to [2^13, 2^14); 0 for zero and non-finite rows.
+__device__ __forceinline__ int row_exponent(float big) {
+  const int ex = static_cast<int>(__float_as_uint(big) >> 23);
+  return (big > 0.f && ex < 255) ? ex - 127 - 13 : 0;
+}
+// Eight codes as fp16: pairs (elements 2i, 2i + 1) with scale constants 16 d and -24 d of each pair.
+__device__ __forceinline__ uint32_t pair_of(uint32_t w, int i, __half2 a, __half2 b) {
+  const uint32_t s = i == 0 ? w << 6 : i == 1 ? w << 2 : i == 2 ? w >> 2 : w >> 6;
+  uint32_t v;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(v) : "r"(s), "r"(0x03C003C0u), "r"(0x3C003C00u));
+  return h2u(__hfma2(u2h(v), a, b));
+}
+__device__ __forceinline__ void unpack8(float (&x)[8], uint4 u) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(w[i] << 16);
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) kv4_attn_tree_kernel(KvAttnParams p) {
+  using Blk = KvBlock<D>;
+  using Sm = Smem<D>;
+  extern __shared__ __align__(1024) char sm[];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const bool aborted = launch_aborted(p.c.err);
+  const KvPlace place = kv_place(p, kRows, reinterpret_cast<long long*>(sm));
+  if (__syncthreads_or(aborted) || place.at == place.end) return;
+
+  uint64_t* bar = reinterpret_cast<uint64_t*>(sm + Sm::kBar);
+  volatile int* gave_up = reinterpret_cast<volatile int*>(sm + Sm::kTmem + 8);
+  volatile int* odd = reinterpret_cast<volatile int*>(sm + Sm::kTmem + 12);
+  unsigned long long* see = reinterpret_cast<unsigned long long*>(sm + Sm::kSee);
+  float* colscale = reinterpret_cast<float*>(sm + Sm::kColScale);
+  if (tid == 0) {
+    auto init = [&](int i, int count) {
+      asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(&bar[i])), "r"(count) : "memory");
+    };
+    for (int i = 0; i < kBars; ++i) init(i, 1);
+    for (int i = 0; i < kStages; ++i) init(kStEmpty + i, kUnpackWarps);
+    for (int i = 0; i < 2; ++i) {
+      init(kKFull + i, kUnpackWarps);
+      init(kVFull + i, kUnpackWarps);
+      init(kPFull + i, kSoftWarps);
+    }
+    init(kOFree, kSoftWarps);
+    init(kQReady, kSoftWarps);
+    init(kNewFull, kUnpackWarps);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    *gave_up = 0;
+    *odd = 0;
+  }
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + Sm::kTmem);
+  if (warp == kMmaWarp) {
+    tmem_alloc(tslot, Sm::kCols);
+    tmem_relinquish();
+  }
+  fence_proxy_async();
+  tmem_fence_before();
+  __syncthreads();
+  tmem_fence_after();
+  const uint32_t tmem = *tslot;
+
+  // Bounded wait; once any wait of the CTA has given up, all of them return at once.
+  auto wait = [&](int b, uint32_t parity) {
+    if (*gave_up) return false;
+    if (mbar_wait(&bar[b], parity & 1)) return true;
+    *gave_up = 1;
+    device_error(p.c.err, GDN_DEVERR_TIMEOUT, place.b);
+    return false;
+  };
+  auto wait_all = [&](int b, uint32_t parity) { return __all_sync(0xffffffffu, wait(b, parity)) != 0; };   // by a whole warp
+  auto arrive_warp = [&](int b) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bar[b]);
+  };
+
+  long long at = place.at;
+  KvPlace where = place;
+  int step = 0, pages = 0, segs = 0, news = 0;      // steps, pages, segments with steps and new-row steps so far
+  bool alive = true;
+  while (at < place.end && alive) {
+    const KvSegment it = kv_segment(p, kRows, at, place.end, where, &at);
+    if (!it.r.ok) {
+      if (tid == 0 && it.first) {
+        device_error(p.c.err, it.r.n < 1 || it.r.n > p.n_max ? GDN_DEVERR_SCHEDULE : GDN_DEVERR_CACHE, it.b);
+        for (int t = 0; t < p.row_tiles; ++t) p.desc[it.item + t] = make_int4(0, 0, 0, 0);
+      }
+      continue;
+    }
+    const bool with_new = it.first && p.k_new;
+    const int lead = with_new ? 1 : 0, steps = lead + it.pages;
+    const int row0 = it.tile * kRows, rows = min(kRows, it.r.n * p.G - row0);
+    const size_t node0 = static_cast<size_t>(it.bl) * p.n_max;
+
+    if (warp < kSoftWarps) {
+      // ================= softmax: thread tid is row tid of the tile, lane tid of tensor memory
+      const uint32_t lanes = tmem + (static_cast<uint32_t>(warp) << 21);
+      const bool busy = 32 * warp < rows;                  // a warp without rows only keeps the barriers going
+      const int row = row0 + min(tid, rows - 1);           // rows past the tile repeat its last one
+      const int node = row / p.G, head = it.h * p.G + row % p.G;
+      const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + (node0 + node) * p.q_row + static_cast<size_t>(head) * D;
+      float c = 0.f;
+      if (busy) {
+        float big = 0.f;
+#pragma unroll 4
+        for (int i = 0; i < D / 8; ++i) {
+          float x[8];
+          unpack8(x, __ldg(reinterpret_cast<const uint4*>(q) + i));
+#pragma unroll
+          for (int e = 0; e < 8; ++e) big = fmaxf(big, fabsf(x[e]));
+        }
+        const int e = row_exponent(big);
+        const float f0 = exp2i(-(e / 2)), f1 = (p.scale < 0.f ? -1.f : 1.f) * exp2i(-(e - e / 2));
+        // the scores' factor; never 0, so that a masked score stays -inf
+        c = fmaxf(fabsf(p.scale) * kLog2e * exp2i(e / 2) * exp2i(e - e / 2), 1.2e-38f);
+#pragma unroll 1
+        for (int i = 0; i < D / 32; ++i) {
+          float w[16];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            float x[8];
+            unpack8(x, __ldg(reinterpret_cast<const uint4*>(q) + 4 * i + k));
+#pragma unroll
+            for (int e2 = 0; e2 < 4; ++e2)
+              w[4 * k + e2] = __uint_as_float(h2u(__floats2half2_rn(x[2 * e2] * f0 * f1, x[2 * e2 + 1] * f0 * f1)));
+          }
+          tmem_st16(lanes + Sm::kQ + 16 * i, w);
+        }
+        tmem_wait_st();
+      }
+      if (steps > 0) {
+        tmem_fence_before();
+        arrive_warp(kQReady);
+      }
+      float m = -INFINITY, l = 0.f;
+      bool own = false;                                    // the row adds its own ancestors at the end
+      for (int i = 0; i < steps && alive; ++i) {
+        const int k = step + i, buf = k & 1;
+        alive = wait_all(kSFull + buf, k >> 1);
+        if (alive && i < lead) alive = wait_all(kNewFull, news);
+        if (!alive) break;
+        tmem_fence_after();
+        if (busy) {
+          const uint32_t ts = lanes + Sm::kS + 64 * buf;
+          float s[2][32];
+          tmem_ld32(ts, s[0]);
+          tmem_ld32(ts + 32, s[1]);
+          tmem_wait_ld();
+          unsigned long long vis = ~0ull;
+          if (i < lead) {
+            own = *odd != 0;
+            vis = own ? 0ull : see[node];
+#pragma unroll
+            for (int x = 0; x < 64; ++x) s[x >> 5][x & 31] *= colscale[x];
+          } else {
+            const int toks = it.r.len - (it.page_lo + i - lead) * kPage;
+            if (toks < kPage) vis = (1ull << toks) - 1;
+          }
+          if (vis != ~0ull) {
+#pragma unroll
+            for (int x = 0; x < 64; ++x)
+              if (!((vis >> x) & 1)) s[x >> 5][x & 31] = -INFINITY;
+          }
+          float t0 = s[0][0], t1 = s[0][1], t2 = s[1][0], t3 = s[1][1];
+#pragma unroll
+          for (int x = 2; x < 32; x += 2) {
+            t0 = fmaxf(t0, s[0][x]);
+            t1 = fmaxf(t1, s[0][x + 1]);
+            t2 = fmaxf(t2, s[1][x]);
+            t3 = fmaxf(t3, s[1][x + 1]);
+          }
+          // rounded up: no score times c passes it, however large the scores
+          const float top = __fmul_ru(fmaxf(fmaxf(t0, t1), fmaxf(t2, t3)), c);
+          if (__any_sync(0xffffffffu, top > m + kSlack)) {
+            const float mn = top > m + kSlack ? top : m;
+            const float f = m == -INFINITY ? 0.f : mn == m ? 1.f : exp2f(m - mn);
+            m = mn;
+            l *= f;
+            // rescale the output: the product of the step before has to be in it first
+            if (i > 0) {
+              alive = wait_all(kODone, k - 1);
+              tmem_fence_after();
+#pragma unroll 1
+              for (int x = 0; x < D; x += 16) {
+                float o[16];
+                tmem_ld16(lanes + Sm::kO + x, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int y = 0; y < 16; ++y) o[y] *= f;
+                tmem_st16(lanes + Sm::kO + x, o);
+              }
+              tmem_wait_st();
+            }
+          }
+          const float r = m == -INFINITY ? kLift : kLift - m;
+          float l0 = 0.f, l1 = 0.f;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float w[16];
+#pragma unroll
+            for (int x = 0; x < 16; ++x) {
+              const float a = exp2_fast(fmaf(s[h][2 * x], c, r)), b = exp2_fast(fmaf(s[h][2 * x + 1], c, r));
+              l0 += a;
+              l1 += b;
+              w[x] = __uint_as_float(h2u(__floats2half2_rn(a, b)));
+            }
+            tmem_st16(ts + 16 * h, w);
+          }
+          l += l0 + l1;
+          tmem_wait_st();
+        }
+        tmem_fence_before();
+        arrive_warp(kPFull + buf);
+      }
+      // ---- the item's rows (or this CTA's part of them)
+      if (steps > 0 && alive) {
+        // the last product; the one before it first, so that its phase cannot be mistaken for this one's
+        alive = wait_all(kODone, step + steps - 2) && wait_all(kODone, step + steps - 1);
+        tmem_fence_after();
+      }
+      if (alive && busy) {
+        const bool mine = tid < rows;
+        float f = 1.f;
+        float* ps = reinterpret_cast<float*>(sm + Sm::kKeys) + tid * GDN_MAX_NODES;
+        unsigned long long anc = own ? see[node] : 0ull;
+        if (own) {
+          // scores of the ancestors in fp32, kept in the operands' space (every product has completed)
+          const float sc = p.scale * kLog2e;
+          float mn = m;
+          for (unsigned long long left = anc; left; left &= left - 1) {
+            const int t = __ffsll(static_cast<long long>(left)) - 1;
+            const __nv_bfloat16* kr = static_cast<const __nv_bfloat16*>(p.k_new) + (node0 + t) * p.kv_row + static_cast<size_t>(it.h) * D;
+            float x = 0.f;
+            for (int i = 0; i < D / 8; ++i) {
+              float a[8], b[8];
+              unpack8(a, __ldg(reinterpret_cast<const uint4*>(q) + i));
+              unpack8(b, __ldg(reinterpret_cast<const uint4*>(kr) + i));
+#pragma unroll
+              for (int e = 0; e < 8; ++e) x = fmaf(a[e], b[e], x);
+            }
+            x *= sc;
+            ps[t] = x;
+            mn = fmaxf(mn, x);
+          }
+          f = m == -INFINITY ? 0.f : exp2f(m - mn);
+          l *= f;
+          m = mn;
+          for (unsigned long long left = anc; left; left &= left - 1) {
+            const int t = __ffsll(static_cast<long long>(left)) - 1;
+            const float w = ps[t] == -INFINITY ? 0.f : exp2f(ps[t] - m + kLift);
+            ps[t] = w;
+            l += w;
+          }
+        }
+        float* part = it.whole ? nullptr : kv_stream_part(p, blockIdx.x, it.start > place.at, kRows, D);
+        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + (node0 + node) * (static_cast<size_t>(p.Hq) * D) + static_cast<size_t>(head) * D;
+        const float inv = part ? 1.f : (l == 0.f ? 0.f : 1.f / l);
+#pragma unroll 1
+        for (int x = 0; x < D; x += 32) {
+          float o[32];
+          if (steps > 0) {
+            tmem_ld32(lanes + Sm::kO + x, o);
+            tmem_wait_ld();
+          } else {
+#pragma unroll
+            for (int y = 0; y < 32; ++y) o[y] = 0.f;
+          }
+          if (own) {
+#pragma unroll
+            for (int y = 0; y < 32; ++y) o[y] = f == 0.f ? 0.f : o[y] * f;
+            for (unsigned long long left = anc; left; left &= left - 1) {
+              const int t = __ffsll(static_cast<long long>(left)) - 1;
+              if (ps[t] == 0.f) continue;
+              const __nv_bfloat16* vr = static_cast<const __nv_bfloat16*>(p.v_new) + (node0 + t) * p.kv_row + static_cast<size_t>(it.h) * D + x;
+#pragma unroll
+              for (int y = 0; y < 32; ++y) o[y] = fmaf(ps[t], __bfloat162float(vr[y]), o[y]);
+            }
+          }
+          if (!mine) continue;
+          if (part) {
+#pragma unroll
+            for (int y = 0; y < 32; y += 4)
+              *reinterpret_cast<float4*>(part + static_cast<size_t>(tid) * D + x + y) = make_float4(o[y], o[y + 1], o[y + 2], o[y + 3]);
+          } else {
+#pragma unroll
+            for (int y = 0; y < 32; y += 8) {
+              uint4 v;
+              __nv_bfloat162 b[4];
+#pragma unroll
+              for (int z = 0; z < 4; ++z) b[z] = __floats2bfloat162_rn(o[y + 2 * z] * inv, o[y + 2 * z + 1] * inv);
+              v.x = *reinterpret_cast<uint32_t*>(&b[0]);
+              v.y = *reinterpret_cast<uint32_t*>(&b[1]);
+              v.z = *reinterpret_cast<uint32_t*>(&b[2]);
+              v.w = *reinterpret_cast<uint32_t*>(&b[3]);
+              *reinterpret_cast<uint4*>(out + x + y) = v;
+            }
+          }
+        }
+        if (part && mine) *reinterpret_cast<float2*>(part + kRows * D + 2 * tid) = make_float2(m, l);
+      }
+      if (tid == 0 && it.first) {
+        const int c0 = kv_cta_of(it.start, place.total, place.ctas);
+        const int c1 = kv_cta_of(it.start + it.r.units - 1, place.total, place.ctas);
+        // what the join reads: first CTA, CTAs (none to join: 0), whether the item starts inside the first, rows
+        p.desc[it.item] = make_int4(c0, it.whole ? 0 : c1 - c0 + 1, it.start > kv_unit_of(c0, place.total, place.ctas), rows);
+        if (it.tile == 0)          // tiles that this request does not fill
+          for (int t = it.r.tiles; t < p.row_tiles; ++t) p.desc[it.item + t] = make_int4(0, 0, 0, 0);
+      }
+      if (tid == 0 && with_new) *odd = 0;      // every warp has read it: their weights are in the last product
+      if (steps > 0) {
+        tmem_fence_before();
+        arrive_warp(kOFree);
+      }
+    } else if (warp < kCopyWarp) {
+      // ================= unpacking: keys, then values, of each step
+      const int uw = warp - kSoftWarps;
+      // the operands' space, the ancestor masks and the scales belong to the item before until its output is released
+      if (steps > 0) alive = wait_all(kOFree, segs + 1);
+      for (int i = 0; i < steps && alive; ++i) {
+        const int k = step + i, buf = k & 1;
+        char* kt = sm + Sm::kKeys + buf * Sm::kKeyTile;
+        char* vt = sm + Sm::kVals + buf * Sm::kValTile;
+        alive = wait_all(kKEmpty + buf, (k >> 1) + 1);
+        if (!alive) break;
+        if (i < lead) {
+          // the nodes' own rows, straight from global memory
+          const int32_t* parent = p.words ? p.words + static_cast<size_t>(it.b) * SchedLayout{p.n_max}.words() + SchedLayout{p.n_max}.parent() : nullptr;
+          const int ut = tid - 32 * kSoftWarps;
+          if (ut < it.r.n) {
+            unsigned long long mask = 1ull << ut;
+            int a = parent ? parent[ut] : -1, prev = ut;
+            while (a >= 0 && a < prev) {
+              mask |= 1ull << a;
+              prev = a;
+              a = parent[a];
+            }
+            if (a >= 0) device_error(p.c.err, GDN_DEVERR_SCHEDULE, it.b);
+            see[ut] = mask;
+          }
+          bool strange = false;
+          for (int t = uw; t < kPage; t += kUnpackWarps) {           // keys: a warp a row, eight channels a lane
+            const bool in = t < it.r.n && lane < D / 8;
+            uint4 raw = make_uint4(0, 0, 0, 0);
+            if (in)
+              raw = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.k_new) + (node0 + t) * p.kv_row + static_cast<size_t>(it.h) * D) + lane);
+            float x[8], big = 0.f;
+            unpack8(x, raw);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              strange = strange || !(fabsf(x[e]) < INFINITY);
+              big = fmaxf(big, fabsf(x[e]));
+            }
+            for (int o = 16; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+            const int e = row_exponent(big);
+            const float f0 = exp2i(-(e / 2)), f1 = exp2i(-(e - e / 2));
+            if (lane == 0) colscale[t] = exp2i(e / 2) * exp2i(e - e / 2);
+            uint32_t w[4];
+#pragma unroll
+            for (int z = 0; z < 4; ++z) w[z] = h2u(__floats2half2_rn(x[2 * z] * f0 * f1, x[2 * z + 1] * f0 * f1));
+            if (lane < D / 8)
+              *reinterpret_cast<uint4*>(kt + lane * Sm::kKeyK + (t >> 3) * 128 + (t & 7) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+          fence_proxy_async();
+          arrive_warp(kKFull + buf);
+          alive = wait_all(kVEmpty + buf, (k >> 1) + 1);
+          if (!alive) break;
+          for (int x = ut; x < 8 * D; x += 32 * kUnpackWarps) {      // values: eight tokens of a channel
+            const int ch = x % D, o = x / D;
+            float y[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const int t = 8 * o + e;
+              y[e] = t < it.r.n ? __bfloat162float(static_cast<const __nv_bfloat16*>(p.v_new)[(node0 + t) * p.kv_row + static_cast<size_t>(it.h) * D + ch]) : 0.f;
+              if (!(fabsf(y[e]) < kTooLarge)) {
+                strange = true;
+                y[e] = 0.f;
+              }
+            }
+            uint32_t w[4];
+#pragma unroll
+            for (int z = 0; z < 4; ++z) w[z] = h2u(__floats2half2_rn(y[2 * z], y[2 * z + 1]));
+            *reinterpret_cast<uint4*>(vt + o * Sm::kValK + (ch >> 3) * 128 + (ch & 7) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+          if (strange) *odd = 1;
+          fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&bar[kVFull + buf]);
+            mbar_arrive(&bar[kNewFull]);
+          }
+          continue;
+        }
+        const int pg = pages + i - lead, st = pg % kStages;
+        alive = wait_all(kStFull + st, pg / kStages);
+        if (!alive) break;
+        const char* blk = sm + st * Sm::kStage;
+        const int toks = it.r.len - (it.page_lo + i - lead) * kPage;     // tokens past the length read as zeros
+        const __half2 k16 = __float2half2_rn(16.f), k24 = __float2half2_rn(-24.f);
+        for (int x = uw; x < D / 16; x += kUnpackWarps) {                // a chunk of 32 channels of 32 tokens
+          const int t = 32 * (x & 1) + lane, ch = x >> 1;
+          const uint4 v = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint32_t*>(blk) + Blk::key_word(t, 4 * ch));
+          __half d = reinterpret_cast<const __half*>(blk + Blk::kKeyScales)[t * Blk::kGroups + ch];
+          if (t >= toks) d = __ushort_as_half(0);
+          const __half2 d2 = __half2half2(d), a = __hmul2(d2, k16), b = __hmul2(d2, k24);
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+          char* dst = kt + 4 * ch * Sm::kKeyK + (t >> 3) * 128 + (t & 7) * 16;
+#pragma unroll
+          for (int z = 0; z < 4; ++z)
+            *reinterpret_cast<uint4*>(dst + z * Sm::kKeyK) =
+                make_uint4(pair_of(w[z], 0, a, b), pair_of(w[z], 1, a, b), pair_of(w[z], 2, a, b), pair_of(w[z], 3, a, b));
+        }
+        fence_proxy_async();
+        arrive_warp(kKFull + buf);
+        alive = wait_all(kVEmpty + buf, (k >> 1) + 1);
+        if (!alive) break;
+        for (int x = uw; x < D / 16; x += kUnpackWarps) {                // four channels, eight tokens a lane
+          const int u = 32 * x + lane, o = (u / D) * 4 + (u & 3), cq = (u % D) >> 2;
+          const uint4 v = *(reinterpret_cast<const uint4*>(blk + Blk::kValCodes) + u);
+          const uint4 dv = *reinterpret_cast<const uint4*>(reinterpret_cast<const __half*>(blk + Blk::kValScales) + (cq >> 3) * kPage + 8 * o);
+          uint32_t dd[4] = {dv.x, dv.y, dv.z, dv.w};
+          __half2 a[4], b[4];
+#pragma unroll
+          for (int z = 0; z < 4; ++z) {
+            const int left = toks - (8 * o + 2 * z);
+            if (left < 2) dd[z] = left == 1 ? dd[z] & 0xFFFFu : 0u;
+            a[z] = __hmul2(u2h(dd[z]), k16);
+            b[z] = __hmul2(u2h(dd[z]), k24);
+          }
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+          char* dst = vt + o * Sm::kValK + (cq >> 1) * 128 + (cq & 1) * 64;
+#pragma unroll
+          for (int z = 0; z < 4; ++z)
+            *reinterpret_cast<uint4*>(dst + 16 * z) = make_uint4(pair_of(w[z], 0, a[0], b[0]), pair_of(w[z], 1, a[1], b[1]),
+                                                                 pair_of(w[z], 2, a[2], b[2]), pair_of(w[z], 3, a[3], b[3]));
+        }
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&bar[kVFull + buf]);
+          mbar_arrive(&bar[kStEmpty + st]);
+        }
+      }
+    } else if (warp == kCopyWarp) {
+      // ================= bulk copies of the pages; a lane holds the numbers of 32 of them at a time
+      const int32_t* table = p.c.page_table + static_cast<size_t>(it.b) * p.c.pages_max + it.page_lo;
+      for (int base = 0; base < it.pages && alive; base += 32) {
+        const int mine = base + lane < it.pages ? table[base + lane] : -1;
+        for (int i = base; i < min(it.pages, base + 32) && alive; ++i) {
+          const int g = __shfl_sync(0xffffffffu, mine, i - base);
+          const int pg = pages + i, st = pg % kStages;
+          if (lane == 0) {
+            alive = wait(kStEmpty + st, pg / kStages + 1);
+            if (alive) {
+              if (g >= 0 && g < p.c.n_pages) {
+                mbar_expect(&bar[kStFull + st], Sm::kStage);
+                bulk_g2s(sm + st * Sm::kStage, kv_block<D>(p.c, p.Hkv, g, it.l, it.h), Sm::kStage, &bar[kStFull + st]);
+              } else {       // whatever the stage holds is unpacked in its place; the request is reported
+                device_error(p.c.err, GDN_DEVERR_CACHE, it.b);
+                mbar_arrive(&bar[kStFull + st]);
+              }
+            }
+          }
+          alive = __shfl_sync(0xffffffffu, alive, 0);
+        }
+      }
+      if (!alive && lane == 0)          // let the copies in flight land before the CTA exits
+        for (int st = 0; st < kStages; ++st)
+          for (int par = 0; par < 2; ++par) mbar_wait(&bar[kStFull + st], par);
+    } else if (lane == 0 && steps > 0) {
+      // ================= MMAs, one thread: scores of step i, then the product of step i - 1
+      alive = wait(kQReady, segs);
+      tmem_fence_after();
+      for (int i = 0; i <= steps && alive; ++i) {
+        if (i < steps) {
+          const int k = step + i, buf = k & 1;
+          alive = wait(kKFull + buf, k >> 1);
+          if (!alive) break;
+          tmem_fence_after();
+          const uint64_t b0 = umma_desc(smem_addr(sm + Sm::kKeys + buf * Sm::kKeyTile), Sm::kKeyK, 128);
+          const uint32_t d = tmem + Sm::kS + 64 * buf;
+#pragma unroll 4
+          for (int x = 0; x < D / 16; ++x)
+            umma_f16_ts(d, tmem + Sm::kQ + 8 * x, b0 + static_cast<uint64_t>(x) * (2 * Sm::kKeyK / 16), idesc_f16(128, kPage), x > 0);
+          umma_commit(&bar[kKEmpty + buf]);
+          umma_commit(&bar[kSFull + buf]);
+        }
+        if (i > 0) {
+          const int k = step + i - 1, buf = k & 1;
+          // the first product of an item overwrites the output of the one before it
+          alive = (i > 1 || wait(kOFree, segs + 1)) && wait(kPFull + buf, k >> 1) && wait(kVFull + buf, k >> 1);
+          if (!alive) break;
+          tmem_fence_after();
+          const uint64_t b0 = umma_desc(smem_addr(sm + Sm::kVals + buf * Sm::kValTile), Sm::kValK, 128);
+#pragma unroll
+          for (int x = 0; x < kPage / 16; ++x)
+            umma_f16_ts(tmem + Sm::kO, tmem + Sm::kS + 64 * buf + 8 * x, b0 + static_cast<uint64_t>(x) * (2 * Sm::kValK / 16),
+                        idesc_f16(128, D), i > 1 || x > 0);
+          umma_commit(&bar[kVEmpty + buf]);
+          umma_commit(&bar[kODone]);
+        }
+      }
+      if (!alive) {                     // MMAs in flight read shared and tensor memory: wait for them
+        umma_commit(&bar[kDrain]);
+        mbar_wait(&bar[kDrain], 0);
+      }
+    }
+    step += steps;
+    pages += it.pages;
+    segs += steps > 0 ? 1 : 0;
+    news += lead;
+    alive = __shfl_sync(0xffffffffu, alive, 0);
+  }
+  tmem_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) tmem_dealloc(tmem, Sm::kCols);
+}
+
+// Joins the items that several CTAs share: a warp a row.
+template <int D>
+__global__ void __launch_bounds__(128) kv4_join_kernel(KvAttnParams p) {
+  if (launch_aborted(p.c.err)) return;  // the counts may be an earlier call's
+  const int item = blockIdx.x, r = blockIdx.y * 4 + (threadIdx.x >> 5);
+  const int4 t = p.desc[item];          // first CTA, CTAs, starts inside, rows
+  if (t.y < 2 || r >= t.w) return;
+  const size_t size = static_cast<size_t>(kRows) * (D + 2);
+  const int lane = threadIdx.x & 31, tile = item % p.row_tiles;
+  const int lh = item / p.row_tiles, h = lh % p.Hkv, bl = p.b0 * p.layers + lh / p.Hkv;
+  const int row = tile * kRows + r;
+  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) +
+                       ((static_cast<size_t>(bl) * p.n_max + row / p.G) * p.Hq + h * p.G + row % p.G) * D;
+  auto part_of = [&](int c) { return p.part + (2 * static_cast<size_t>(t.x + c) + (c == 0 && t.z ? 1 : 0)) * size; };
+  float m = -INFINITY, sum = 0.f;
+  for (int b = 0; b < t.y; b += 32) {
+    const float mc = b + lane < t.y ? part_of(b + lane)[kRows * D + 2 * r] : -INFINITY;
+    float top = fmaxf(m, mc);
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    m = top;
+  }
+  float acc[D / 32];
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) acc[i] = 0.f;
+#pragma unroll 4
+  for (int c = 0; c < t.y; ++c) {
+    const float* part = part_of(c);
+    const float2 ml = *reinterpret_cast<const float2*>(part + kRows * D + 2 * r);
+    // a part that held nothing this row sees has maximum -inf, sum 0 and zeros
+    const float w = (ml.x == -INFINITY && ml.y == 0.f) ? 0.f : exp2f(ml.x - m);
+    sum = fmaf(w, ml.y, sum);
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i) {
+      const float2 v = *reinterpret_cast<const float2*>(part + static_cast<size_t>(r) * D + 64 * i + 2 * lane);
+      acc[2 * i] = fmaf(w, v.x, acc[2 * i]);
+      acc[2 * i + 1] = fmaf(w, v.y, acc[2 * i + 1]);
+    }
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+  for (int i = 0; i < D / 64; ++i)
+    *reinterpret_cast<__nv_bfloat162*>(out + 64 * i + 2 * lane) = __floats2bfloat162_rn(acc[2 * i] * inv, acc[2 * i + 1] * inv);
+}
+
+template <int D>
+cudaError_t tree_t(KvAttnParams p, cudaStream_t s) {
+  auto k = kv4_attn_tree_kernel<D>;
+  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::kTotal);
+  if (e != cudaSuccess) return e;
+  const int items = p.layers * p.Hkv * p.row_tiles, per = kKvItems / items;      // requests a launch
+  p.each = p.ctas / items;
+  for (p.b0 = 0; p.b0 < p.c.B; p.b0 += per) {
+    p.bn = p.c.B - p.b0 < per ? p.c.B - p.b0 : per;
+    k<<<p.ctas, kThreads, Smem<D>::kTotal, s>>>(p);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    kv4_join_kernel<D><<<dim3(p.bn * items, kRows / 4), 128, 0, s>>>(p);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+}  // namespace
+
+cudaError_t launch_kv4_attention_tree(const KvAttnParams& p, cudaStream_t s) {
+  return p.D == 256 ? tree_t<256>(p, s) : p.D == 128 ? tree_t<128>(p, s) : tree_t<64>(p, s);
+}
+
+}  // namespace gdn
