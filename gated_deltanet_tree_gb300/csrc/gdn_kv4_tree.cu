@@ -38,8 +38,10 @@ constexpr float kSlack = 8.f;         // ... against a maximum that may lag by u
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kTooLarge = 6.0e4f;   // new values beyond this take the fp32 path
 
-enum Bar { kStFull = 0, kStEmpty = 3, kKFull = 6, kKEmpty = 8, kVFull = 10, kVEmpty = 12, kSFull = 14, kPFull = 16,
-           kODone = 18, kOFree = 19, kQReady = 20, kNewFull = 21, kDrain = 22, kBars = 23 };
+// kScored: scores written, which also frees the key operand; kAdded: product added to the output, which also frees the
+// value operand (a commit costs the issuing thread some two hundred cycles, so there is one for each)
+enum Bar { kStFull = 0, kStEmpty = 3, kKFull = 6, kVFull = 8, kScored = 10, kPFull = 12, kAdded = 14, kOFree = 16,
+           kQReady = 17, kNewFull = 18, kDrain = 19, kBars = 20 };
 
 template <int D>
 struct Smem {
@@ -63,13 +65,20 @@ struct Smem {
 __host__ __device__ constexpr uint32_t idesc_f16(int m, int n) {
   return (1u << 4) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
 }
-// D (+)= A B^T, kind::f16 (K = 16), A in tensor memory.
-__device__ __forceinline__ void umma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, int accumulate) {
+// D = A B^T or D += A B^T, kind::f16 (K = 16), A in tensor memory.
+template <bool kAdd>
+__device__ __forceinline__ void umma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc) {
   asm volatile(
       "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      "r"(a), "l"(b), "r"(idesc), "n"(kAdd ? 1 : 0)
       : "memory");
 }
+__device__ __forceinline__ bool elect_one() {
+  uint32_t yes;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(yes));
+  return yes != 0;
+}
+// 32 columns of this thread's lane; defined after tmem_wait_ld().
 __device__ __forceinline__ void tmem_ld32(uint32_t ta, float (&v)[32]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
@@ -80,6 +89,11 @@ __device__ __forceinline__ void tmem_ld32(uint32_t ta, float (&v)[32]) {
         "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
       : "r"(ta)
       : "memory");
+}
+__device__ __forceinline__ u64 add2(u64 a, u64 b) {
+  u64 d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
 }
 __device__ __forceinline__ uint32_t h2u(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
 __device__ __forceinline__ __half2 u2h(uint32_t u) { return *reinterpret_cast<__half2*>(&u); }
@@ -156,6 +170,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tree_kernel(KvAttnParams
 
   // Bounded wait; once any wait of the CTA has given up, all of them return at once.
   auto wait = [&](int b, uint32_t parity) {
+    if (mbar_ready(&bar[b], parity & 1)) return true;
     if (*gave_up) return false;
     if (mbar_wait(&bar[b], parity & 1)) return true;
     *gave_up = 1;
@@ -230,7 +245,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tree_kernel(KvAttnParams
       bool own = false;                                    // the row adds its own ancestors at the end
       for (int i = 0; i < steps && alive; ++i) {
         const int k = step + i, buf = k & 1;
-        alive = wait_all(kSFull + buf, k >> 1);
+        alive = wait_all(kScored + buf, k >> 1);
         if (alive && i < lead) alive = wait_all(kNewFull, news);
         if (!alive) break;
         tmem_fence_after();
@@ -257,11 +272,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tree_kernel(KvAttnParams
           }
           float t0 = s[0][0], t1 = s[0][1], t2 = s[1][0], t3 = s[1][1];
 #pragma unroll
-          for (int x = 2; x < 32; x += 2) {
-            t0 = fmaxf(t0, s[0][x]);
-            t1 = fmaxf(t1, s[0][x + 1]);
-            t2 = fmaxf(t2, s[1][x]);
-            t3 = fmaxf(t3, s[1][x + 1]);
+          for (int x = 2; x < 32; x += 2) {          // (three-input maxima)
+            t0 = fmaxf(t0, fmaxf(s[0][x], s[0][x + 1]));
+            t2 = fmaxf(t2, fmaxf(s[1][x], s[1][x + 1]));
           }
           // rounded up: no score times c passes it, however large the scores
           const float top = __fmul_ru(fmaxf(fmaxf(t0, t1), fmaxf(t2, t3)), c);
@@ -272,7 +285,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tree_kernel(KvAttnParams
             l *= f;
             // rescale the output: the product of the step before has to be in it first
             if (i > 0) {
-              alive = wait_all(kODone, k - 1);
+              alive = wait_all(kAdded + (buf ^ 1), (k - 1) >> 1);
               tmem_fence_after();
 #pragma unroll 1
               for (int x = 0; x < D; x += 16) {
@@ -287,20 +300,22 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tree_kernel(KvAttnParams
             }
           }
           const float r = m == -INFINITY ? kLift : kLift - m;
-          float l0 = 0.f, l1 = 0.f;
+          const u64 c2 = pack2(c, c), r2 = pack2(r, r);
+          u64 sum[2] = {0, 0};
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             float w[16];
 #pragma unroll
             for (int x = 0; x < 16; ++x) {
-              const float a = exp2_fast(fmaf(s[h][2 * x], c, r)), b = exp2_fast(fmaf(s[h][2 * x + 1], c, r));
-              l0 += a;
-              l1 += b;
+              const float2 y = unpack2(fma2(pack2(s[h][2 * x], s[h][2 * x + 1]), c2, r2));
+              const float a = exp2_fast(y.x), b = exp2_fast(y.y);
+              sum[x & 1] = add2(sum[x & 1], pack2(a, b));
               w[x] = __uint_as_float(h2u(__floats2half2_rn(a, b)));
             }
             tmem_st16(ts + 16 * h, w);
           }
-          l += l0 + l1;
+          const float2 total = unpack2(add2(sum[0], sum[1]));
+          l += total.x + total.y;
           tmem_wait_st();
         }
         tmem_fence_before();
@@ -308,8 +323,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tree_kernel(KvAttnParams
       }
       // ---- the item's rows (or this CTA's part of them)
       if (steps > 0 && alive) {
-        // the last product; the one before it first, so that its phase cannot be mistaken for this one's
-        alive = wait_all(kODone, step + steps - 2) && wait_all(kODone, step + steps - 1);
+        const int k = step + steps - 1;
+        alive = wait_all(kAdded + (k & 1), k >> 1);
         tmem_fence_after();
       }
       if (alive && busy) {
@@ -414,7 +429,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tree_kernel(KvAttnParams
         const int k = step + i, buf = k & 1;
         char* kt = sm + Sm::kKeys + buf * Sm::kKeyTile;
         char* vt = sm + Sm::kVals + buf * Sm::kValTile;
-        alive = wait_all(kKEmpty + buf, (k >> 1) + 1);
+        alive = wait_all(kScored + buf, (k >> 1) + 1);
         if (!alive) break;
         if (i < lead) {
           // the nodes' own rows, straight from global memory
@@ -456,7 +471,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tree_kernel(KvAttnParams
           }
           fence_proxy_async();
           arrive_warp(kKFull + buf);
-          alive = wait_all(kVEmpty + buf, (k >> 1) + 1);
+          alive = wait_all(kAdded + buf, (k >> 1) + 1);
           if (!alive) break;
           for (int x = ut; x < 8 * D; x += 32 * kUnpackWarps) {      // values: eight tokens of a channel
             const int ch = x % D, o = x / D;
@@ -490,49 +505,72 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tree_kernel(KvAttnParams
         const char* blk = sm + st * Sm::kStage;
         const int toks = it.r.len - (it.page_lo + i - lead) * kPage;     // tokens past the length read as zeros
         const __half2 k16 = __float2half2_rn(16.f), k24 = __float2half2_rn(-24.f);
-        for (int x = uw; x < D / 16; x += kUnpackWarps) {                // a chunk of 32 channels of 32 tokens
-          const int t = 32 * (x & 1) + lane, ch = x >> 1;
-          const uint4 v = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint32_t*>(blk) + Blk::key_word(t, 4 * ch));
-          __half d = reinterpret_cast<const __half*>(blk + Blk::kKeyScales)[t * Blk::kGroups + ch];
-          if (t >= toks) d = __ushort_as_half(0);
-          const __half2 d2 = __half2half2(d), a = __hmul2(d2, k16), b = __hmul2(d2, k24);
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-          char* dst = kt + 4 * ch * Sm::kKeyK + (t >> 3) * 128 + (t & 7) * 16;
+        // everything of this warp's share is loaded first: the unpacking then waits for nothing
+        constexpr int kShare = (D / 16 + kUnpackWarps - 1) / kUnpackWarps;
+        const bool busy = uw < D / 16;
+        uint4 kw[kShare], vw[kShare], vd[kShare];
+        __half kd[kShare];
 #pragma unroll
-          for (int z = 0; z < 4; ++z)
-            *reinterpret_cast<uint4*>(dst + z * Sm::kKeyK) =
-                make_uint4(pair_of(w[z], 0, a, b), pair_of(w[z], 1, a, b), pair_of(w[z], 2, a, b), pair_of(w[z], 3, a, b));
-        }
-        fence_proxy_async();
-        arrive_warp(kKFull + buf);
-        alive = wait_all(kVEmpty + buf, (k >> 1) + 1);
-        if (!alive) break;
-        for (int x = uw; x < D / 16; x += kUnpackWarps) {                // four channels, eight tokens a lane
-          const int u = 32 * x + lane, o = (u / D) * 4 + (u & 3), cq = (u % D) >> 2;
-          const uint4 v = *(reinterpret_cast<const uint4*>(blk + Blk::kValCodes) + u);
-          const uint4 dv = *reinterpret_cast<const uint4*>(reinterpret_cast<const __half*>(blk + Blk::kValScales) + (cq >> 3) * kPage + 8 * o);
-          uint32_t dd[4] = {dv.x, dv.y, dv.z, dv.w};
-          __half2 a[4], b[4];
+        for (int y = 0; y < kShare; ++y) {
+          const int x = busy ? uw + y * kUnpackWarps : 0;
+          // keys: a chunk of 32 channels of a token a lane; values: four channels, eight tokens a lane
+          const int t = 32 * (x & 1) + lane, ch = x >> 1, u = 32 * x + lane, o = (u / D) * 4 + (u & 3), cq = (u % D) >> 2;
+          kw[y] = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint32_t*>(blk) + Blk::key_word(t, 4 * ch));
+          kd[y] = reinterpret_cast<const __half*>(blk + Blk::kKeyScales)[t * Blk::kGroups + ch];
+          vw[y] = *(reinterpret_cast<const uint4*>(blk + Blk::kValCodes) + u);
+          vd[y] = *reinterpret_cast<const uint4*>(reinterpret_cast<const __half*>(blk + Blk::kValScales) + (cq >> 3) * kPage + 8 * o);
+          if (toks < kPage) {          // scales past the length are whatever the page held
+            if (t >= toks) kd[y] = __ushort_as_half(0);
+            uint32_t* dd = reinterpret_cast<uint32_t*>(&vd[y]);
 #pragma unroll
-          for (int z = 0; z < 4; ++z) {
-            const int left = toks - (8 * o + 2 * z);
-            if (left < 2) dd[z] = left == 1 ? dd[z] & 0xFFFFu : 0u;
-            a[z] = __hmul2(u2h(dd[z]), k16);
-            b[z] = __hmul2(u2h(dd[z]), k24);
+            for (int z = 0; z < 4; ++z) {
+              const int left = toks - (8 * o + 2 * z);
+              if (left < 2) dd[z] = left == 1 ? dd[z] & 0xFFFFu : 0u;
+            }
           }
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-          char* dst = vt + o * Sm::kValK + (cq >> 1) * 128 + (cq & 1) * 64;
+        }
+        if (busy) {
 #pragma unroll
-          for (int z = 0; z < 4; ++z)
-            *reinterpret_cast<uint4*>(dst + 16 * z) = make_uint4(pair_of(w[z], 0, a[0], b[0]), pair_of(w[z], 1, a[1], b[1]),
-                                                                 pair_of(w[z], 2, a[2], b[2]), pair_of(w[z], 3, a[3], b[3]));
+          for (int y = 0; y < kShare; ++y) {
+            const int x = uw + y * kUnpackWarps, t = 32 * (x & 1) + lane, ch = x >> 1;
+            const __half2 d2 = __half2half2(kd[y]), a = __hmul2(d2, k16), b = __hmul2(d2, k24);
+            const uint32_t w[4] = {kw[y].x, kw[y].y, kw[y].z, kw[y].w};
+            char* dst = kt + 4 * ch * Sm::kKeyK + (t >> 3) * 128 + (t & 7) * 16;
+#pragma unroll
+            for (int z = 0; z < 4; ++z)
+              *reinterpret_cast<uint4*>(dst + z * Sm::kKeyK) =
+                  make_uint4(pair_of(w[z], 0, a, b), pair_of(w[z], 1, a, b), pair_of(w[z], 2, a, b), pair_of(w[z], 3, a, b));
+          }
         }
         fence_proxy_async();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(&bar[kVFull + buf]);
+          mbar_arrive(&bar[kKFull + buf]);
           mbar_arrive(&bar[kStEmpty + st]);
         }
+        alive = wait_all(kAdded + buf, (k >> 1) + 1);
+        if (!alive) break;
+        if (busy) {
+#pragma unroll
+          for (int y = 0; y < kShare; ++y) {
+            const int u = 32 * (uw + y * kUnpackWarps) + lane, o = (u / D) * 4 + (u & 3), cq = (u % D) >> 2;
+            const uint32_t dd[4] = {vd[y].x, vd[y].y, vd[y].z, vd[y].w};
+            __half2 a[4], b[4];
+#pragma unroll
+            for (int z = 0; z < 4; ++z) {
+              a[z] = __hmul2(u2h(dd[z]), k16);
+              b[z] = __hmul2(u2h(dd[z]), k24);
+            }
+            const uint32_t w[4] = {vw[y].x, vw[y].y, vw[y].z, vw[y].w};
+            char* dst = vt + o * Sm::kValK + (cq >> 1) * 128 + (cq & 1) * 64;
+#pragma unroll
+            for (int z = 0; z < 4; ++z)
+              *reinterpret_cast<uint4*>(dst + 16 * z) = make_uint4(pair_of(w[z], 0, a[0], b[0]), pair_of(w[z], 1, a[1], b[1]),
+                                                                   pair_of(w[z], 2, a[2], b[2]), pair_of(w[z], 3, a[3], b[3]));
+          }
+        }
+        fence_proxy_async();
+        arrive_warp(kVFull + buf);
       }
     } else if (warp == kCopyWarp) {
       // ================= bulk copies of the pages; a lane holds the numbers of 32 of them at a time
@@ -560,42 +598,59 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tree_kernel(KvAttnParams
       if (!alive && lane == 0)          // let the copies in flight land before the CTA exits
         for (int st = 0; st < kStages; ++st)
           for (int par = 0; par < 2; ++par) mbar_wait(&bar[kStFull + st], par);
-    } else if (lane == 0 && steps > 0) {
-      // ================= MMAs, one thread: scores of step i, then the product of step i - 1
-      alive = wait(kQReady, segs);
+    } else if (steps > 0) {
+      // ================= MMAs: scores of step i, then the product of step i - 1.  The warp runs the loop together
+      // and one elected thread issues: operand descriptors stay in uniform registers that way, and an issue takes a
+      // few instructions (in a lane-0 branch the 20 issues of a step took three times as long as the MMAs themselves)
+      const bool leader = elect_one();
+      alive = wait_all(kQReady, segs);
       tmem_fence_after();
       for (int i = 0; i <= steps && alive; ++i) {
         if (i < steps) {
           const int k = step + i, buf = k & 1;
-          alive = wait(kKFull + buf, k >> 1);
+          alive = wait_all(kKFull + buf, k >> 1);
           if (!alive) break;
           tmem_fence_after();
           const uint64_t b0 = umma_desc(smem_addr(sm + Sm::kKeys + buf * Sm::kKeyTile), Sm::kKeyK, 128);
           const uint32_t d = tmem + Sm::kS + 64 * buf;
-#pragma unroll 4
-          for (int x = 0; x < D / 16; ++x)
-            umma_f16_ts(d, tmem + Sm::kQ + 8 * x, b0 + static_cast<uint64_t>(x) * (2 * Sm::kKeyK / 16), idesc_f16(128, kPage), x > 0);
-          umma_commit(&bar[kKEmpty + buf]);
-          umma_commit(&bar[kSFull + buf]);
+          if (leader) {
+            umma_f16_ts<false>(d, tmem + Sm::kQ, b0, idesc_f16(128, kPage));
+#pragma unroll
+            for (int x = 1; x < D / 16; ++x)
+              umma_f16_ts<true>(d, tmem + Sm::kQ + 8 * x, b0 + static_cast<uint64_t>(x) * (2 * Sm::kKeyK / 16),
+                                idesc_f16(128, kPage));
+            umma_commit(&bar[kScored + buf]);
+          }
+          __syncwarp();
         }
         if (i > 0) {
           const int k = step + i - 1, buf = k & 1;
           // the first product of an item overwrites the output of the one before it
-          alive = (i > 1 || wait(kOFree, segs + 1)) && wait(kPFull + buf, k >> 1) && wait(kVFull + buf, k >> 1);
+          alive = (i > 1 || wait_all(kOFree, segs + 1)) && wait_all(kPFull + buf, k >> 1) && wait_all(kVFull + buf, k >> 1);
           if (!alive) break;
           tmem_fence_after();
           const uint64_t b0 = umma_desc(smem_addr(sm + Sm::kVals + buf * Sm::kValTile), Sm::kValK, 128);
+          const uint32_t a0 = tmem + Sm::kS + 64 * buf;
+          if (leader) {
+            if (i == 1)
+              umma_f16_ts<false>(tmem + Sm::kO, a0, b0, idesc_f16(128, D));
+            else
+              umma_f16_ts<true>(tmem + Sm::kO, a0, b0, idesc_f16(128, D));
 #pragma unroll
-          for (int x = 0; x < kPage / 16; ++x)
-            umma_f16_ts(tmem + Sm::kO, tmem + Sm::kS + 64 * buf + 8 * x, b0 + static_cast<uint64_t>(x) * (2 * Sm::kValK / 16),
-                        idesc_f16(128, D), i > 1 || x > 0);
-          umma_commit(&bar[kVEmpty + buf]);
-          umma_commit(&bar[kODone]);
+            for (int x = 1; x < kPage / 16; ++x)
+              umma_f16_ts<true>(tmem + Sm::kO, a0 + 8 * x, b0 + static_cast<uint64_t>(x) * (2 * Sm::kValK / 16),
+                                idesc_f16(128, D));
+            umma_commit(&bar[kAdded + buf]);
+          }
+          __syncwarp();
         }
       }
       if (!alive) {                     // MMAs in flight read shared and tensor memory: wait for them
-        umma_commit(&bar[kDrain]);
-        mbar_wait(&bar[kDrain], 0);
+        if (leader) {
+          umma_commit(&bar[kDrain]);
+          mbar_wait(&bar[kDrain], 0);
+        }
+        __syncwarp();
       }
     }
     step += steps;
