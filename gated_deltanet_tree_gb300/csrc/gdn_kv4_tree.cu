@@ -10,9 +10,11 @@
 // the A operand of O += P V.  The scores of one page are computed while the page
 // before it goes through the softmax.
 //
-// Roles (14 warps, one CTA an SM): four softmax warps, a thread a row; eight
-// unpacking warps (codes to fp16: see gdn_kv4_dec.cu); one warp issues the bulk
-// copies of the pages, one the MMAs.  They meet at mbarriers only; every wait is
+// Roles (18 warps, one CTA an SM): eight softmax warps, two threads a row that take
+// the pages in turn and hand each other the row's reference maximum; four warps
+// unpack keys and four values (codes to
+// fp16: see gdn_kv4_dec.cu); one warp issues the bulk copies of the pages, one the
+// MMAs.  They meet at mbarriers only; every wait is
 // bounded.  CTAs take equal runs of the requests' pages (KvPlace); items that two
 // or more CTAs share are joined by a second kernel, spread over the GPU.
 //
@@ -28,7 +30,7 @@
 namespace gdn {
 namespace {
 
-constexpr int kSoftWarps = 4, kUnpackWarps = 8;
+constexpr int kSoftWarps = 8, kKeyWarps = 4, kUnpackWarps = 8;      // of the latter, kKeyWarps for the keys
 constexpr int kCopyWarp = kSoftWarps + kUnpackWarps, kMmaWarp = kCopyWarp + 1;
 constexpr int kThreads = 32 * (kMmaWarp + 1);
 constexpr int kRows = kKvTreeRows;
@@ -41,7 +43,7 @@ constexpr float kTooLarge = 6.0e4f;   // new values beyond this take the fp32 pa
 // kScored: scores written, which also frees the key operand; kAdded: product added to the output, which also frees the
 // value operand (a commit costs the issuing thread some two hundred cycles, so there is one for each)
 enum Bar { kStFull = 0, kStEmpty = 3, kKFull = 6, kVFull = 8, kScored = 10, kPFull = 12, kAdded = 14, kOFree = 16,
-           kQReady = 17, kNewFull = 18, kDrain = 19, kBars = 20 };
+           kQReady = 17, kNewFull = 18, kDrain = 19, kPair = 20, kDecided = 24, kItem = 28, kBars = 29 };
 
 template <int D>
 struct Smem {
@@ -56,7 +58,9 @@ struct Smem {
   static constexpr int kColScale = kSee + GDN_MAX_NODES * 8;       // float [64]
   static constexpr int kBar = kColScale + GDN_MAX_NODES * 4;
   static constexpr int kTmem = kBar + kBars * 8;                   // tensor-memory address, flags
-  static constexpr int kTotal = kTmem + 32;
+  static constexpr int kSwap = kTmem + 32;                         // float [2][2][128]: what the two threads of a row tell each other
+  static constexpr int kRef = kSwap + 4 * kRows * 4;               // float [128]: each row's reference maximum
+  static constexpr int kTotal = kRef + kRows * 4;
   // tensor-memory columns
   static constexpr int kO = 0, kQ = D, kS = D + D / 2;
   static constexpr int kCols = D == 256 ? 512 : D == 128 ? 512 : 256;
@@ -136,7 +140,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tree_kernel(KvAttnParams
 
   uint64_t* bar = reinterpret_cast<uint64_t*>(sm + Sm::kBar);
   volatile int* gave_up = reinterpret_cast<volatile int*>(sm + Sm::kTmem + 8);
-  volatile int* odd = reinterpret_cast<volatile int*>(sm + Sm::kTmem + 12);
+  volatile int* odd = reinterpret_cast<volatile int*>(sm + Sm::kTmem + 16);      // [2], alternating by new-row step
   unsigned long long* see = reinterpret_cast<unsigned long long*>(sm + Sm::kSee);
   float* colscale = reinterpret_cast<float*>(sm + Sm::kColScale);
   if (tid == 0) {
@@ -146,16 +150,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tree_kernel(KvAttnParams
     for (int i = 0; i < kBars; ++i) init(i, 1);
     for (int i = 0; i < kStages; ++i) init(kStEmpty + i, kUnpackWarps);
     for (int i = 0; i < 2; ++i) {
-      init(kKFull + i, kUnpackWarps);
-      init(kVFull + i, kUnpackWarps);
-      init(kPFull + i, kSoftWarps);
+      init(kKFull + i, kKeyWarps);
+      init(kVFull + i, kUnpackWarps - kKeyWarps);
+      init(kPFull + i, kSoftWarps / 2);
     }
     init(kOFree, kSoftWarps);
     init(kQReady, kSoftWarps);
     init(kNewFull, kUnpackWarps);
+    for (int i = 0; i < 4; ++i) init(kPair + i, 2);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     *gave_up = 0;
-    *odd = 0;
+    odd[0] = odd[1] = 0;
   }
   uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + Sm::kTmem);
   if (warp == kMmaWarp) {
@@ -171,8 +176,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tree_kernel(KvAttnParams
   // Bounded wait; once any wait of the CTA has given up, all of them return at once.
   auto wait = [&](int b, uint32_t parity) {
     if (mbar_ready(&bar[b], parity & 1)) return true;
+    const long long t0 = clock64();
+    while (!*gave_up && clock64() - t0 <= kWaitCycles)
+      if (mbar_ready(&bar[b], parity & 1)) return true;
     if (*gave_up) return false;
-    if (mbar_wait(&bar[b], parity & 1)) return true;
     *gave_up = 1;
     device_error(p.c.err, GDN_DEVERR_TIMEOUT, place.b);
     return false;
@@ -186,6 +193,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tree_kernel(KvAttnParams
   long long at = place.at;
   KvPlace where = place;
   int step = 0, pages = 0, segs = 0, news = 0;      // steps, pages, segments with steps and new-row steps so far
+  int swaps = 0, decisions = 0;                     // exchanges between the two threads of a row, reference maxima so far
   bool alive = true;
   while (at < place.end && alive) {
     const KvSegment it = kv_segment(p, kRows, at, place.end, where, &at);
@@ -202,38 +210,59 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tree_kernel(KvAttnParams
     const size_t node0 = static_cast<size_t>(it.bl) * p.n_max;
 
     if (warp < kSoftWarps) {
-      // ================= softmax: thread tid is row tid of the tile, lane tid of tensor memory
-      const uint32_t lanes = tmem + (static_cast<uint32_t>(warp) << 21);
-      const bool busy = 32 * warp < rows;                  // a warp without rows only keeps the barriers going
-      const int row = row0 + min(tid, rows - 1);           // rows past the tile repeat its last one
+      // ================= softmax: two threads a row take steps in turn (half = step & 1), so that the latencies of one
+      // step run beside those of the next, and half of the channels each of queries and output
+      const int quarter = warp & 3, half = warp >> 2, r = 32 * quarter + lane;     // lane r of tensor memory
+      const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter) << 21);
+      const bool busy = 32 * quarter < rows;               // a warp without rows only keeps the barriers going
+      const int row = row0 + min(r, rows - 1);             // rows past the tile repeat its last one
       const int node = row / p.G, head = it.h * p.G + row % p.G;
       const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + (node0 + node) * p.q_row + static_cast<size_t>(head) * D;
+      float* swap = reinterpret_cast<float*>(sm + Sm::kSwap);
+      // a value to the row's other thread, and its value
+      auto exchange = [&](float x, bool* ok) {
+        float* to = swap + (swaps & 1) * 2 * kRows;
+        to[half * kRows + r] = x;
+        arrive_warp(kPair + quarter);
+        *ok = wait_all(kPair + quarter, swaps);
+        ++swaps;
+        return to[(half ^ 1) * kRows + r];
+      };
       float c = 0.f;
       if (busy) {
+        constexpr int kAhead = D / 16 < 8 ? D / 16 : 8;      // 16-byte loads in flight
+        const uint4* qv = reinterpret_cast<const uint4*>(q + half * (D / 2));
         float big = 0.f;
-#pragma unroll 4
-        for (int i = 0; i < D / 8; ++i) {
-          float x[8];
-          unpack8(x, __ldg(reinterpret_cast<const uint4*>(q) + i));
+#pragma unroll 1
+        for (int i = 0; i < D / 16; i += kAhead) {
+          uint4 raw[kAhead];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) big = fmaxf(big, fabsf(x[e]));
+          for (int k = 0; k < kAhead; ++k) raw[k] = __ldg(qv + i + k);
+#pragma unroll
+          for (int k = 0; k < kAhead; ++k) {
+            float x[8];
+            unpack8(x, raw[k]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) big = fmaxf(big, fabsf(x[e]));
+          }
         }
+        big = fmaxf(big, exchange(big, &alive));
         const int e = row_exponent(big);
         const float f0 = exp2i(-(e / 2)), f1 = (p.scale < 0.f ? -1.f : 1.f) * exp2i(-(e - e / 2));
         // the scores' factor; never 0, so that a masked score stays -inf
         c = fmaxf(fabsf(p.scale) * kLog2e * exp2i(e / 2) * exp2i(e - e / 2), 1.2e-38f);
 #pragma unroll 1
-        for (int i = 0; i < D / 32; ++i) {
+        for (int i = 0; i < D / 64; ++i) {
           float w[16];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             float x[8];
-            unpack8(x, __ldg(reinterpret_cast<const uint4*>(q) + 4 * i + k));
+            unpack8(x, __ldg(qv + 4 * i + k));
 #pragma unroll
-            for (int e2 = 0; e2 < 4; ++e2)
-              w[4 * k + e2] = __uint_as_float(h2u(__floats2half2_rn(x[2 * e2] * f0 * f1, x[2 * e2 + 1] * f0 * f1)));
+            for (int z = 0; z < 4; ++z)
+              w[4 * k + z] = __uint_as_float(h2u(__floats2half2_rn(x[2 * z] * f0 * f1, x[2 * z + 1] * f0 * f1)));
           }
-          tmem_st16(lanes + Sm::kQ + 16 * i, w);
+          tmem_st16(lanes + Sm::kQ + half * (D / 4) + 16 * i, w);
         }
         tmem_wait_st();
       }
@@ -241,78 +270,108 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tree_kernel(KvAttnParams
         tmem_fence_before();
         arrive_warp(kQReady);
       }
-      float m = -INFINITY, l = 0.f;
-      bool own = false;                                    // the row adds its own ancestors at the end
+      float m = -INFINITY, l = 0.f;      // l is relative to m, the row's reference when this thread last looked
+      float* ref = reinterpret_cast<float*>(sm + Sm::kRef) + r;
+      // the row's reference after decision n, and l in its terms
+      auto follow = [&](float mn) {
+        if (mn != m) l *= m == -INFINITY ? 0.f : exp2f(m - mn);
+        m = mn;
+      };
       for (int i = 0; i < steps && alive; ++i) {
         const int k = step + i, buf = k & 1;
+        if (buf != half) continue;
         alive = wait_all(kScored + buf, k >> 1);
         if (alive && i < lead) alive = wait_all(kNewFull, news);
         if (!alive) break;
         tmem_fence_after();
         if (busy) {
           const uint32_t ts = lanes + Sm::kS + 64 * buf;
-          float s[2][32];
-          tmem_ld32(ts, s[0]);
-          tmem_ld32(ts + 32, s[1]);
-          tmem_wait_ld();
+          const bool is_new = i < lead;
           unsigned long long vis = ~0ull;
-          if (i < lead) {
-            own = *odd != 0;
-            vis = own ? 0ull : see[node];
-#pragma unroll
-            for (int x = 0; x < 64; ++x) s[x >> 5][x & 31] *= colscale[x];
+          if (is_new) {
+            vis = odd[news & 1] ? 0ull : see[node];
           } else {
             const int toks = it.r.len - (it.page_lo + i - lead) * kPage;
             if (toks < kPage) vis = (1ull << toks) - 1;
           }
-          if (vis != ~0ull) {
+          if (is_new || vis != ~0ull) {
+            // scale and mask in place, apart from the common path (whose code is better small: the roles of an SM share
+            // its instruction caches)
+#pragma unroll 1
+            for (int x = 0; x < 64; x += 16) {
+              float t[16];
+              tmem_ld16(ts + x, t);
+              tmem_wait_ld();
 #pragma unroll
-            for (int x = 0; x < 64; ++x)
-              if (!((vis >> x) & 1)) s[x >> 5][x & 31] = -INFINITY;
+              for (int y = 0; y < 16; ++y) {
+                if (is_new) t[y] *= colscale[x + y];
+                if (!((vis >> (x + y)) & 1)) t[y] = -INFINITY;
+              }
+              tmem_st16(ts + x, t);
+            }
+            tmem_wait_st();
           }
-          float t0 = s[0][0], t1 = s[0][1], t2 = s[1][0], t3 = s[1][1];
+          float top = -INFINITY;
+#pragma unroll 1
+          for (int h = 0; h < 64; h += 32) {
+            float x[32];
+            tmem_ld32(ts + h, x);
+            tmem_wait_ld();
+            float t0 = x[0], t1 = x[1];
 #pragma unroll
-          for (int x = 2; x < 32; x += 2) {          // (three-input maxima)
-            t0 = fmaxf(t0, fmaxf(s[0][x], s[0][x + 1]));
-            t2 = fmaxf(t2, fmaxf(s[1][x], s[1][x + 1]));
+            for (int y = 2; y < 32; y += 4) {          // (three-input maxima)
+              t0 = fmaxf(t0, fmaxf(x[y], x[y + 1]));
+              if (y + 3 < 32) t1 = fmaxf(t1, fmaxf(x[y + 2], x[y + 3]));
+            }
+            top = fmaxf(top, fmaxf(t0, t1));
           }
           // rounded up: no score times c passes it, however large the scores
-          const float top = __fmul_ru(fmaxf(fmaxf(t0, t1), fmaxf(t2, t3)), c);
-          if (__any_sync(0xffffffffu, top > m + kSlack)) {
-            const float mn = top > m + kSlack ? top : m;
-            const float f = m == -INFINITY ? 0.f : mn == m ? 1.f : exp2f(m - mn);
-            m = mn;
-            l *= f;
-            // rescale the output: the product of the step before has to be in it first
-            if (i > 0) {
-              alive = wait_all(kAdded + (buf ^ 1), (k - 1) >> 1);
-              tmem_fence_after();
-#pragma unroll 1
-              for (int x = 0; x < D; x += 16) {
-                float o[16];
-                tmem_ld16(lanes + Sm::kO + x, o);
-                tmem_wait_ld();
-#pragma unroll
-                for (int y = 0; y < 16; ++y) o[y] *= f;
-                tmem_st16(lanes + Sm::kO + x, o);
-              }
-              tmem_wait_st();
-            }
+          top = __fmul_ru(top, c);
+          // the reference: the other thread's of the page before, raised where this page passes it by too much
+          float before = -INFINITY;
+          if (i > 0) {
+            alive = wait_all(kDecided + quarter, decisions + i - 1);
+            if (!alive) break;
+            before = *const_cast<volatile float*>(ref);
           }
-          const float r = m == -INFINITY ? kLift : kLift - m;
-          const u64 c2 = pack2(c, c), r2 = pack2(r, r);
-          u64 sum[2] = {0, 0};
+          const float now = top > before + kSlack ? top : before;
+          *ref = now;
+          arrive_warp(kDecided + quarter);
+          follow(now);
+          if (i > 0 && __any_sync(0xffffffffu, now != before)) {
+            // rescale the output: the product of the step before has to be in it first
+            const float f = before == -INFINITY ? 0.f : exp2f(before - now);
+            alive = wait_all(kAdded + (buf ^ 1), (k - 1) >> 1);
+            if (!alive) break;
+            tmem_fence_after();
+#pragma unroll 1
+            for (int x = 0; x < D; x += 16) {
+              float o[16];
+              tmem_ld16(lanes + Sm::kO + x, o);
+              tmem_wait_ld();
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            float w[16];
-#pragma unroll
-            for (int x = 0; x < 16; ++x) {
-              const float2 y = unpack2(fma2(pack2(s[h][2 * x], s[h][2 * x + 1]), c2, r2));
-              const float a = exp2_fast(y.x), b = exp2_fast(y.y);
-              sum[x & 1] = add2(sum[x & 1], pack2(a, b));
-              w[x] = __uint_as_float(h2u(__floats2half2_rn(a, b)));
+              for (int y = 0; y < 16; ++y) o[y] *= f;
+              tmem_st16(lanes + Sm::kO + x, o);
             }
-            tmem_st16(ts + 16 * h, w);
+            tmem_wait_st();
+          }
+          const float base = m == -INFINITY ? kLift : kLift - m;
+          const u64 c2 = pack2(c, c), b2 = pack2(base, base);
+          u64 sum[2] = {0, 0};
+#pragma unroll 1
+          for (int h = 0; h < 64; h += 32) {
+            float x[32], w[16];
+            tmem_ld32(ts + h, x);
+            tmem_wait_ld();
+#pragma unroll
+            for (int y = 0; y < 16; ++y) {
+              const float2 e = unpack2(fma2(pack2(x[2 * y], x[2 * y + 1]), c2, b2));
+              const float e0 = exp2_fast(e.x), e1 = exp2_fast(e.y);
+              sum[y & 1] = add2(sum[y & 1], pack2(e0, e1));
+              w[y] = __uint_as_float(h2u(__floats2half2_rn(e0, e1)));
+            }
+            // the weights of 32 tokens go over the scores they came from: columns h .. h + 15
+            tmem_st16(ts + h, w);
           }
           const float2 total = unpack2(add2(sum[0], sum[1]));
           l += total.x + total.y;
@@ -322,77 +381,94 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tree_kernel(KvAttnParams
         arrive_warp(kPFull + buf);
       }
       // ---- the item's rows (or this CTA's part of them)
+      bool own = false;                                    // the row adds its own ancestors
       if (steps > 0 && alive) {
-        const int k = step + steps - 1;
-        alive = wait_all(kAdded + (k & 1), k >> 1);
+        // every product of the item (a barrier of its own, once an item: a wait tells a phase from the one before and
+        // the one after only)
+        alive = wait_all(kItem, segs);
         tmem_fence_after();
+        if (alive && busy) {
+          alive = wait_all(kDecided + quarter, decisions + steps - 1);
+          follow(*ref);
+          own = with_new && odd[news & 1];
+        }
       }
+      if (busy) decisions += steps;
       if (alive && busy) {
-        const bool mine = tid < rows;
+        const bool mine = r < rows;
         float f = 1.f;
-        float* ps = reinterpret_cast<float*>(sm + Sm::kKeys) + tid * GDN_MAX_NODES;
-        unsigned long long anc = own ? see[node] : 0ull;
+        // the row's ancestors' weights, in the operands' space (every product has completed)
+        float* ps = reinterpret_cast<float*>(sm + Sm::kKeys) + r * GDN_MAX_NODES;
+        const unsigned long long anc = own ? see[node] : 0ull;
         if (own) {
-          // scores of the ancestors in fp32, kept in the operands' space (every product has completed)
-          const float sc = p.scale * kLog2e;
-          float mn = m;
-          for (unsigned long long left = anc; left; left &= left - 1) {
-            const int t = __ffsll(static_cast<long long>(left)) - 1;
-            const __nv_bfloat16* kr = static_cast<const __nv_bfloat16*>(p.k_new) + (node0 + t) * p.kv_row + static_cast<size_t>(it.h) * D;
-            float x = 0.f;
-            for (int i = 0; i < D / 8; ++i) {
-              float a[8], b[8];
-              unpack8(a, __ldg(reinterpret_cast<const uint4*>(q) + i));
-              unpack8(b, __ldg(reinterpret_cast<const uint4*>(kr) + i));
+          if (half == 0) {
+            const float sc = p.scale * kLog2e;
+            float mn = m;
+            for (unsigned long long left = anc; left; left &= left - 1) {
+              const int t = __ffsll(static_cast<long long>(left)) - 1;
+              const __nv_bfloat16* kr = static_cast<const __nv_bfloat16*>(p.k_new) + (node0 + t) * p.kv_row + static_cast<size_t>(it.h) * D;
+              float x = 0.f;
+#pragma unroll 1
+              for (int i = 0; i < D / 8; ++i) {
+                float a[8], b[8];
+                unpack8(a, __ldg(reinterpret_cast<const uint4*>(q) + i));
+                unpack8(b, __ldg(reinterpret_cast<const uint4*>(kr) + i));
 #pragma unroll
-              for (int e = 0; e < 8; ++e) x = fmaf(a[e], b[e], x);
+                for (int e = 0; e < 8; ++e) x = fmaf(a[e], b[e], x);
+              }
+              x *= sc;
+              ps[t] = x;
+              mn = fmaxf(mn, x);
             }
-            x *= sc;
-            ps[t] = x;
-            mn = fmaxf(mn, x);
+            f = m == -INFINITY ? 0.f : exp2f(m - mn);
+            m = mn;
+            l *= f;
+            for (unsigned long long left = anc; left; left &= left - 1) {
+              const int t = __ffsll(static_cast<long long>(left)) - 1;
+              const float w = ps[t] == -INFINITY ? 0.f : exp2f(ps[t] - m + kLift);
+              ps[t] = w;
+              l += w;
+            }
           }
-          f = m == -INFINITY ? 0.f : exp2f(m - mn);
-          l *= f;
-          m = mn;
-          for (unsigned long long left = anc; left; left &= left - 1) {
-            const int t = __ffsll(static_cast<long long>(left)) - 1;
-            const float w = ps[t] == -INFINITY ? 0.f : exp2f(ps[t] - m + kLift);
-            ps[t] = w;
-            l += w;
+          const float g = exchange(f, &alive);      // and the weights with it
+          if (half == 1) {
+            f = g;
+            l *= f;
           }
         }
+        l += exchange(l, &alive);
         float* part = it.whole ? nullptr : kv_stream_part(p, blockIdx.x, it.start > place.at, kRows, D);
         __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + (node0 + node) * (static_cast<size_t>(p.Hq) * D) + static_cast<size_t>(head) * D;
         const float inv = part ? 1.f : (l == 0.f ? 0.f : 1.f / l);
 #pragma unroll 1
-        for (int x = 0; x < D; x += 32) {
-          float o[32];
+        for (int x = half * (D / 2); x < (half + 1) * (D / 2); x += 16) {
+          float o[16];
           if (steps > 0) {
-            tmem_ld32(lanes + Sm::kO + x, o);
+            tmem_ld16(lanes + Sm::kO + x, o);
             tmem_wait_ld();
           } else {
 #pragma unroll
-            for (int y = 0; y < 32; ++y) o[y] = 0.f;
+            for (int y = 0; y < 16; ++y) o[y] = 0.f;
           }
           if (own) {
 #pragma unroll
-            for (int y = 0; y < 32; ++y) o[y] = f == 0.f ? 0.f : o[y] * f;
+            for (int y = 0; y < 16; ++y) o[y] = f == 0.f ? 0.f : o[y] * f;
             for (unsigned long long left = anc; left; left &= left - 1) {
               const int t = __ffsll(static_cast<long long>(left)) - 1;
               if (ps[t] == 0.f) continue;
               const __nv_bfloat16* vr = static_cast<const __nv_bfloat16*>(p.v_new) + (node0 + t) * p.kv_row + static_cast<size_t>(it.h) * D + x;
 #pragma unroll
-              for (int y = 0; y < 32; ++y) o[y] = fmaf(ps[t], __bfloat162float(vr[y]), o[y]);
+              for (int y = 0; y < 16; ++y) o[y] = fmaf(ps[t], __bfloat162float(vr[y]), o[y]);
             }
           }
           if (!mine) continue;
           if (part) {
 #pragma unroll
-            for (int y = 0; y < 32; y += 4)
-              *reinterpret_cast<float4*>(part + static_cast<size_t>(tid) * D + x + y) = make_float4(o[y], o[y + 1], o[y + 2], o[y + 3]);
+            for (int y = 0; y < 16; y += 4)
+              *reinterpret_cast<float4*>(part + static_cast<size_t>(r) * D + x + y) = make_float4(o[y], o[y + 1], o[y + 2], o[y + 3]);
           } else {
 #pragma unroll
-            for (int y = 0; y < 32; y += 8) {
+            for (int y = 0; y < 16; y += 8) {
               uint4 v;
               __nv_bfloat162 b[4];
 #pragma unroll
@@ -405,7 +481,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tree_kernel(KvAttnParams
             }
           }
         }
-        if (part && mine) *reinterpret_cast<float2*>(part + kRows * D + 2 * tid) = make_float2(m, l);
+        if (part && mine && half == 0) *reinterpret_cast<float2*>(part + kRows * D + 2 * r) = make_float2(m, l);
       }
       if (tid == 0 && it.first) {
         const int c0 = kv_cta_of(it.start, place.total, place.ctas);
@@ -415,86 +491,98 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tree_kernel(KvAttnParams
         if (it.tile == 0)          // tiles that this request does not fill
           for (int t = it.r.tiles; t < p.row_tiles; ++t) p.desc[it.item + t] = make_int4(0, 0, 0, 0);
       }
-      if (tid == 0 && with_new) *odd = 0;      // every warp has read it: their weights are in the last product
       if (steps > 0) {
         tmem_fence_before();
         arrive_warp(kOFree);
       }
     } else if (warp < kCopyWarp) {
-      // ================= unpacking: keys, then values, of each step
-      const int uw = warp - kSoftWarps;
+      // ================= unpacking: four warps the keys, four the values
+      // (warps of one kind on two of the four schedulers: warp % 4 is a warp's scheduler, with instruction caches of its own)
+      const bool keys = (warp & 2) == 0;
+      const int uw = (warp & 1) + 2 * ((warp - kSoftWarps) >> 2);
+      // 32 x 16-byte units of a page's keys, and of its values; a warp takes units uw, uw + 4, ...
+      constexpr int kUnits = D / 16, kShare = kUnits / kKeyWarps;
+      static_assert(kKeyWarps == 4 && kUnpackWarps == 8, "units are dealt to four warps");
+      const __half2 k16 = __float2half2_rn(16.f), k24 = __float2half2_rn(-24.f);
+      // keys: unit uw + 4 y is chunk uw / 2 + 2 y of token 32 (uw & 1) + lane
+      const int kt_tok = 32 * (uw & 1) + lane, kt_turn = Blk::turn(kt_tok);
+      // values: unit uw + 4 y holds units (of 16 bytes) 32 uw + lane + 128 y; the first one's octet and channel quad
+      const int vt_unit = 32 * uw + lane, vt_oct = (vt_unit / D) * 4 + (vt_unit & 3), vt_quad = (vt_unit % D) >> 2;
       // the operands' space, the ancestor masks and the scales belong to the item before until its output is released
       if (steps > 0) alive = wait_all(kOFree, segs + 1);
       for (int i = 0; i < steps && alive; ++i) {
         const int k = step + i, buf = k & 1;
         char* kt = sm + Sm::kKeys + buf * Sm::kKeyTile;
         char* vt = sm + Sm::kVals + buf * Sm::kValTile;
-        alive = wait_all(kScored + buf, (k >> 1) + 1);
-        if (!alive) break;
+        const int free_bar = keys ? kScored + buf : kAdded + buf, full_bar = keys ? kKFull + buf : kVFull + buf;
         if (i < lead) {
           // the nodes' own rows, straight from global memory
-          const int32_t* parent = p.words ? p.words + static_cast<size_t>(it.b) * SchedLayout{p.n_max}.words() + SchedLayout{p.n_max}.parent() : nullptr;
-          const int ut = tid - 32 * kSoftWarps;
-          if (ut < it.r.n) {
-            unsigned long long mask = 1ull << ut;
-            int a = parent ? parent[ut] : -1, prev = ut;
-            while (a >= 0 && a < prev) {
-              mask |= 1ull << a;
-              prev = a;
-              a = parent[a];
-            }
-            if (a >= 0) device_error(p.c.err, GDN_DEVERR_SCHEDULE, it.b);
-            see[ut] = mask;
-          }
-          bool strange = false;
-          for (int t = uw; t < kPage; t += kUnpackWarps) {           // keys: a warp a row, eight channels a lane
-            const bool in = t < it.r.n && lane < D / 8;
-            uint4 raw = make_uint4(0, 0, 0, 0);
-            if (in)
-              raw = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.k_new) + (node0 + t) * p.kv_row + static_cast<size_t>(it.h) * D) + lane);
-            float x[8], big = 0.f;
-            unpack8(x, raw);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              strange = strange || !(fabsf(x[e]) < INFINITY);
-              big = fmaxf(big, fabsf(x[e]));
-            }
-            for (int o = 16; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
-            const int e = row_exponent(big);
-            const float f0 = exp2i(-(e / 2)), f1 = exp2i(-(e - e / 2));
-            if (lane == 0) colscale[t] = exp2i(e / 2) * exp2i(e - e / 2);
-            uint32_t w[4];
-#pragma unroll
-            for (int z = 0; z < 4; ++z) w[z] = h2u(__floats2half2_rn(x[2 * z] * f0 * f1, x[2 * z + 1] * f0 * f1));
-            if (lane < D / 8)
-              *reinterpret_cast<uint4*>(kt + lane * Sm::kKeyK + (t >> 3) * 128 + (t & 7) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
-          }
-          fence_proxy_async();
-          arrive_warp(kKFull + buf);
-          alive = wait_all(kAdded + buf, (k >> 1) + 1);
+          alive = wait_all(free_bar, (k >> 1) + 1);
           if (!alive) break;
-          for (int x = ut; x < 8 * D; x += 32 * kUnpackWarps) {      // values: eight tokens of a channel
-            const int ch = x % D, o = x / D;
-            float y[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const int t = 8 * o + e;
-              y[e] = t < it.r.n ? __bfloat162float(static_cast<const __nv_bfloat16*>(p.v_new)[(node0 + t) * p.kv_row + static_cast<size_t>(it.h) * D + ch]) : 0.f;
-              if (!(fabsf(y[e]) < kTooLarge)) {
-                strange = true;
-                y[e] = 0.f;
+          if (keys && uw == 0 && lane == 0) odd[(news + 1) & 1] = 0;      // the next one's, which nobody uses now
+          bool strange = false;
+          if (keys) {
+            const int32_t* parent = p.words ? p.words + static_cast<size_t>(it.b) * SchedLayout{p.n_max}.words() + SchedLayout{p.n_max}.parent() : nullptr;
+            const int ut = 32 * uw + lane;
+            if (ut < it.r.n) {
+              unsigned long long mask = 1ull << ut;
+              int a = parent ? parent[ut] : -1, prev = ut;
+              while (a >= 0 && a < prev) {
+                mask |= 1ull << a;
+                prev = a;
+                a = parent[a];
               }
+              if (a >= 0) device_error(p.c.err, GDN_DEVERR_SCHEDULE, it.b);
+              see[ut] = mask;
             }
-            uint32_t w[4];
+#pragma unroll 1
+            for (int t = uw; t < kPage; t += kKeyWarps) {            // a warp a row, eight channels a lane
+              const bool in = t < it.r.n && lane < D / 8;
+              uint4 raw = make_uint4(0, 0, 0, 0);
+              if (in)
+                raw = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.k_new) + (node0 + t) * p.kv_row + static_cast<size_t>(it.h) * D) + lane);
+              float x[8], big = 0.f;
+              unpack8(x, raw);
 #pragma unroll
-            for (int z = 0; z < 4; ++z) w[z] = h2u(__floats2half2_rn(y[2 * z], y[2 * z + 1]));
-            *reinterpret_cast<uint4*>(vt + o * Sm::kValK + (ch >> 3) * 128 + (ch & 7) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+              for (int e = 0; e < 8; ++e) {
+                strange = strange || !(fabsf(x[e]) < INFINITY);
+                big = fmaxf(big, fabsf(x[e]));
+              }
+              for (int o = 16; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+              const int e = row_exponent(big);
+              const float f0 = exp2i(-(e / 2)), f1 = exp2i(-(e - e / 2));
+              if (lane == 0) colscale[t] = exp2i(e / 2) * exp2i(e - e / 2);
+              uint32_t w[4];
+#pragma unroll
+              for (int z = 0; z < 4; ++z) w[z] = h2u(__floats2half2_rn(x[2 * z] * f0 * f1, x[2 * z + 1] * f0 * f1));
+              if (lane < D / 8)
+                *reinterpret_cast<uint4*>(kt + lane * Sm::kKeyK + (t >> 3) * 128 + (t & 7) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          } else {
+#pragma unroll 1
+            for (int x = 32 * uw + lane; x < 8 * D; x += 32 * (kUnpackWarps - kKeyWarps)) {      // eight tokens of a channel
+              const int ch = x % D, o = x / D;
+              float y[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const int t = 8 * o + e;
+                y[e] = t < it.r.n ? __bfloat162float(static_cast<const __nv_bfloat16*>(p.v_new)[(node0 + t) * p.kv_row + static_cast<size_t>(it.h) * D + ch]) : 0.f;
+                if (!(fabsf(y[e]) < kTooLarge)) {
+                  strange = true;
+                  y[e] = 0.f;
+                }
+              }
+              uint32_t w[4];
+#pragma unroll
+              for (int z = 0; z < 4; ++z) w[z] = h2u(__floats2half2_rn(y[2 * z], y[2 * z + 1]));
+              *reinterpret_cast<uint4*>(vt + o * Sm::kValK + (ch >> 3) * 128 + (ch & 7) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
           }
-          if (strange) *odd = 1;
+          if (strange) odd[news & 1] = 1;
           fence_proxy_async();
           __syncwarp();
           if (lane == 0) {
-            mbar_arrive(&bar[kVFull + buf]);
+            mbar_arrive(&bar[full_bar]);
             mbar_arrive(&bar[kNewFull]);
           }
           continue;
@@ -504,73 +592,83 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tree_kernel(KvAttnParams
         if (!alive) break;
         const char* blk = sm + st * Sm::kStage;
         const int toks = it.r.len - (it.page_lo + i - lead) * kPage;     // tokens past the length read as zeros
-        const __half2 k16 = __float2half2_rn(16.f), k24 = __float2half2_rn(-24.f);
-        // everything of this warp's share is loaded first: the unpacking then waits for nothing
-        constexpr int kShare = (D / 16 + kUnpackWarps - 1) / kUnpackWarps;
-        const bool busy = uw < D / 16;
-        uint4 kw[kShare], vw[kShare], vd[kShare];
-        __half kd[kShare];
-#pragma unroll
-        for (int y = 0; y < kShare; ++y) {
-          const int x = busy ? uw + y * kUnpackWarps : 0;
-          // keys: a chunk of 32 channels of a token a lane; values: four channels, eight tokens a lane
-          const int t = 32 * (x & 1) + lane, ch = x >> 1, u = 32 * x + lane, o = (u / D) * 4 + (u & 3), cq = (u % D) >> 2;
-          kw[y] = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint32_t*>(blk) + Blk::key_word(t, 4 * ch));
-          kd[y] = reinterpret_cast<const __half*>(blk + Blk::kKeyScales)[t * Blk::kGroups + ch];
-          vw[y] = *(reinterpret_cast<const uint4*>(blk + Blk::kValCodes) + u);
-          vd[y] = *reinterpret_cast<const uint4*>(reinterpret_cast<const __half*>(blk + Blk::kValScales) + (cq >> 3) * kPage + 8 * o);
-          if (toks < kPage) {          // scales past the length are whatever the page held
-            if (t >= toks) kd[y] = __ushort_as_half(0);
-            uint32_t* dd = reinterpret_cast<uint32_t*>(&vd[y]);
-#pragma unroll
-            for (int z = 0; z < 4; ++z) {
-              const int left = toks - (8 * o + 2 * z);
-              if (left < 2) dd[z] = left == 1 ? dd[z] & 0xFFFFu : 0u;
-            }
-          }
-        }
-        if (busy) {
-#pragma unroll
+        // rolled loops: the roles of an SM share its instruction caches, and unrolled they do not fit
+        if (keys) {                    // a unit: a chunk of 32 channels of a token a lane
+          const char* from = blk + kt_tok * (D / 2);
+          const __half* scale = reinterpret_cast<const __half*>(blk + Blk::kKeyScales) + kt_tok * Blk::kGroups + (uw >> 1);
+          char* dst = kt + 4 * (uw >> 1) * Sm::kKeyK + (kt_tok >> 3) * 128 + (kt_tok & 7) * 16;
+          int ch = uw >> 1;
+          uint4 cw = *reinterpret_cast<const uint4*>(from + ((ch ^ kt_turn) << 4));
+          __half d = *scale;
+          alive = wait_all(free_bar, (k >> 1) + 1);
+          if (!alive) break;
+#pragma unroll 1
           for (int y = 0; y < kShare; ++y) {
-            const int x = uw + y * kUnpackWarps, t = 32 * (x & 1) + lane, ch = x >> 1;
-            const __half2 d2 = __half2half2(kd[y]), a = __hmul2(d2, k16), b = __hmul2(d2, k24);
-            const uint32_t w[4] = {kw[y].x, kw[y].y, kw[y].z, kw[y].w};
-            char* dst = kt + 4 * ch * Sm::kKeyK + (t >> 3) * 128 + (t & 7) * 16;
+            if (kt_tok >= toks) d = __ushort_as_half(0);            // scales past the length are whatever the page held
+            const __half2 d2 = __half2half2(d), a = __hmul2(d2, k16), b = __hmul2(d2, k24);
+            const uint32_t w[4] = {cw.x, cw.y, cw.z, cw.w};
+            ch += 2;
+            scale += 2;
+            if (y + 1 < kShare) {
+              cw = *reinterpret_cast<const uint4*>(from + ((ch ^ kt_turn) << 4));
+              d = *scale;
+            }
 #pragma unroll
             for (int z = 0; z < 4; ++z)
               *reinterpret_cast<uint4*>(dst + z * Sm::kKeyK) =
                   make_uint4(pair_of(w[z], 0, a, b), pair_of(w[z], 1, a, b), pair_of(w[z], 2, a, b), pair_of(w[z], 3, a, b));
+            dst += 8 * Sm::kKeyK;
           }
-        }
-        fence_proxy_async();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&bar[kKFull + buf]);
-          mbar_arrive(&bar[kStEmpty + st]);
-        }
-        alive = wait_all(kAdded + buf, (k >> 1) + 1);
-        if (!alive) break;
-        if (busy) {
-#pragma unroll
+        } else {                       // a unit: four channels, eight tokens a lane
+          const char* from = blk + Blk::kValCodes + 16 * vt_unit;
+          const char* scale = blk + Blk::kValScales + (vt_quad >> 3) * (2 * kPage) + 16 * vt_oct;
+          char* dst = vt + vt_oct * Sm::kValK + (vt_quad >> 1) * 128 + (vt_quad & 1) * 64;
+          int left = toks - 8 * vt_oct;                             // tokens of the octet inside the length
+          uint4 cw = *reinterpret_cast<const uint4*>(from), sd = *reinterpret_cast<const uint4*>(scale);
+          alive = wait_all(free_bar, (k >> 1) + 1);
+          if (!alive) break;
+#pragma unroll 1
           for (int y = 0; y < kShare; ++y) {
-            const int u = 32 * (uw + y * kUnpackWarps) + lane, o = (u / D) * 4 + (u & 3), cq = (u % D) >> 2;
-            const uint32_t dd[4] = {vd[y].x, vd[y].y, vd[y].z, vd[y].w};
+            const uint32_t w[4] = {cw.x, cw.y, cw.z, cw.w};
+            uint32_t dd[4] = {sd.x, sd.y, sd.z, sd.w};
+            if (left < 8) {
+#pragma unroll
+              for (int z = 0; z < 4; ++z)
+                if (left - 2 * z < 2) dd[z] = left - 2 * z == 1 ? dd[z] & 0xFFFFu : 0u;
+            }
             __half2 a[4], b[4];
 #pragma unroll
             for (int z = 0; z < 4; ++z) {
               a[z] = __hmul2(u2h(dd[z]), k16);
               b[z] = __hmul2(u2h(dd[z]), k24);
             }
-            const uint32_t w[4] = {vw[y].x, vw[y].y, vw[y].z, vw[y].w};
-            char* dst = vt + o * Sm::kValK + (cq >> 1) * 128 + (cq & 1) * 64;
+            char* to = dst;
+            // the next unit is 128 units on: 128 channels further (D = 256, odd steps), or the next 32 tokens
+            from += 128 * 16;
+            if (D == 256 && (y & 1) == 0) {
+              scale += 4 * (2 * kPage);
+              dst += 16 * 128;
+            } else {
+              scale += 64 - (D == 256 ? 4 * (2 * kPage) : 0);
+              dst += 4 * Sm::kValK - (D == 256 ? 16 * 128 : 0);
+              left -= 32;
+            }
+            if (y + 1 < kShare) {
+              cw = *reinterpret_cast<const uint4*>(from);
+              sd = *reinterpret_cast<const uint4*>(scale);
+            }
 #pragma unroll
             for (int z = 0; z < 4; ++z)
-              *reinterpret_cast<uint4*>(dst + 16 * z) = make_uint4(pair_of(w[z], 0, a[0], b[0]), pair_of(w[z], 1, a[1], b[1]),
-                                                                   pair_of(w[z], 2, a[2], b[2]), pair_of(w[z], 3, a[3], b[3]));
+              *reinterpret_cast<uint4*>(to + 16 * z) = make_uint4(pair_of(w[z], 0, a[0], b[0]), pair_of(w[z], 1, a[1], b[1]),
+                                                                  pair_of(w[z], 2, a[2], b[2]), pair_of(w[z], 3, a[3], b[3]));
           }
         }
         fence_proxy_async();
-        arrive_warp(kVFull + buf);
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&bar[full_bar]);
+          mbar_arrive(&bar[kStEmpty + st]);
+        }
       }
     } else if (warp == kCopyWarp) {
       // ================= bulk copies of the pages; a lane holds the numbers of 32 of them at a time
@@ -630,7 +728,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tree_kernel(KvAttnParams
           if (!alive) break;
           tmem_fence_after();
           const uint64_t b0 = umma_desc(smem_addr(sm + Sm::kVals + buf * Sm::kValTile), Sm::kValK, 128);
-          const uint32_t a0 = tmem + Sm::kS + 64 * buf;
+          const uint32_t a0 = tmem + Sm::kS + 64 * buf;      // weights of 16 tokens in columns 0, 8, 32 and 40
           if (leader) {
             if (i == 1)
               umma_f16_ts<false>(tmem + Sm::kO, a0, b0, idesc_f16(128, D));
@@ -638,9 +736,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tree_kernel(KvAttnParams
               umma_f16_ts<true>(tmem + Sm::kO, a0, b0, idesc_f16(128, D));
 #pragma unroll
             for (int x = 1; x < kPage / 16; ++x)
-              umma_f16_ts<true>(tmem + Sm::kO, a0 + 8 * x, b0 + static_cast<uint64_t>(x) * (2 * Sm::kValK / 16),
+              umma_f16_ts<true>(tmem + Sm::kO, a0 + 16 * x - 8 * (x & 1), b0 + static_cast<uint64_t>(x) * (2 * Sm::kValK / 16),
                                 idesc_f16(128, D));
             umma_commit(&bar[kAdded + buf]);
+            if (i == steps) umma_commit(&bar[kItem]);
           }
           __syncwarp();
         }
