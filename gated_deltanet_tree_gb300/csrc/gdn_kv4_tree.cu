@@ -535,47 +535,67 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tree_kernel(KvAttnParams
               if (a >= 0) device_error(p.c.err, GDN_DEVERR_SCHEDULE, it.b);
               see[ut] = mask;
             }
+            // a warp a row, eight channels a lane, four rows in flight; rows past the tree are zeros
+            const __nv_bfloat16* kn = static_cast<const __nv_bfloat16*>(p.k_new) + node0 * p.kv_row + static_cast<size_t>(it.h) * D + 8 * lane;
+            char* to = kt + lane * Sm::kKeyK;
+            const bool in = lane < D / 8;
 #pragma unroll 1
-            for (int t = uw; t < kPage; t += kKeyWarps) {            // a warp a row, eight channels a lane
-              const bool in = t < it.r.n && lane < D / 8;
-              uint4 raw = make_uint4(0, 0, 0, 0);
-              if (in)
-                raw = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.k_new) + (node0 + t) * p.kv_row + static_cast<size_t>(it.h) * D) + lane);
-              float x[8], big = 0.f;
-              unpack8(x, raw);
+            for (int t0 = uw; t0 < kPage; t0 += 4 * kKeyWarps) {
+              uint4 raw[4];
 #pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                strange = strange || !(fabsf(x[e]) < INFINITY);
-                big = fmaxf(big, fabsf(x[e]));
+              for (int y = 0; y < 4; ++y) {
+                const int t = t0 + y * kKeyWarps;
+                raw[y] = in && t < it.r.n ? __ldg(reinterpret_cast<const uint4*>(kn + t * p.kv_row)) : make_uint4(0, 0, 0, 0);
               }
-              for (int o = 16; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
-              const int e = row_exponent(big);
-              const float f0 = exp2i(-(e / 2)), f1 = exp2i(-(e - e / 2));
-              if (lane == 0) colscale[t] = exp2i(e / 2) * exp2i(e - e / 2);
-              uint32_t w[4];
 #pragma unroll
-              for (int z = 0; z < 4; ++z) w[z] = h2u(__floats2half2_rn(x[2 * z] * f0 * f1, x[2 * z + 1] * f0 * f1));
-              if (lane < D / 8)
-                *reinterpret_cast<uint4*>(kt + lane * Sm::kKeyK + (t >> 3) * 128 + (t & 7) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+              for (int y = 0; y < 4; ++y) {
+                const int t = t0 + y * kKeyWarps;
+                float x[8], big = 0.f;
+                unpack8(x, raw[y]);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                  strange = strange || !(fabsf(x[e]) < INFINITY);
+                  big = fmaxf(big, fabsf(x[e]));
+                }
+                for (int o = 16; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+                const int e = row_exponent(big);
+                const float f0 = exp2i(-(e / 2)), f1 = exp2i(-(e - e / 2));
+                if (lane == 0) colscale[t] = exp2i(e / 2) * exp2i(e - e / 2);
+                uint32_t w[4];
+#pragma unroll
+                for (int z = 0; z < 4; ++z) w[z] = h2u(__floats2half2_rn(x[2 * z] * f0 * f1, x[2 * z + 1] * f0 * f1));
+                if (in) *reinterpret_cast<uint4*>(to + (t >> 3) * 128 + (t & 7) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+              }
             }
           } else {
+            // eight tokens of two channels a thread
+            const __nv_bfloat16* vn = static_cast<const __nv_bfloat16*>(p.v_new) + node0 * p.kv_row + static_cast<size_t>(it.h) * D;
 #pragma unroll 1
-            for (int x = 32 * uw + lane; x < 8 * D; x += 32 * (kUnpackWarps - kKeyWarps)) {      // eight tokens of a channel
-              const int ch = x % D, o = x / D;
-              float y[8];
+            for (int x = 32 * uw + lane; x < 4 * D; x += 32 * (kUnpackWarps - kKeyWarps)) {
+              const int ch = 2 * (x % (D / 2)), o = x / (D / 2);
+              uint32_t raw[8], w[2][4];
 #pragma unroll
               for (int e = 0; e < 8; ++e) {
                 const int t = 8 * o + e;
-                y[e] = t < it.r.n ? __bfloat162float(static_cast<const __nv_bfloat16*>(p.v_new)[(node0 + t) * p.kv_row + static_cast<size_t>(it.h) * D + ch]) : 0.f;
-                if (!(fabsf(y[e]) < kTooLarge)) {
-                  strange = true;
-                  y[e] = 0.f;
-                }
+                raw[e] = t < it.r.n ? __ldg(reinterpret_cast<const uint32_t*>(vn + t * p.kv_row + ch)) : 0u;
               }
-              uint32_t w[4];
 #pragma unroll
-              for (int z = 0; z < 4; ++z) w[z] = h2u(__floats2half2_rn(y[2 * z], y[2 * z + 1]));
-              *reinterpret_cast<uint4*>(vt + o * Sm::kValK + (ch >> 3) * 128 + (ch & 7) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+              for (int c2 = 0; c2 < 2; ++c2) {
+                float y[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                  y[e] = __uint_as_float(c2 ? raw[e] & 0xFFFF0000u : raw[e] << 16);
+                  if (!(fabsf(y[e]) < kTooLarge)) {
+                    strange = true;
+                    y[e] = 0.f;
+                  }
+                }
+#pragma unroll
+                for (int z = 0; z < 4; ++z) w[c2][z] = h2u(__floats2half2_rn(y[2 * z], y[2 * z + 1]));
+              }
+              char* to = vt + o * Sm::kValK + (ch >> 3) * 128 + (ch & 7) * 16;
+              *reinterpret_cast<uint4*>(to) = make_uint4(w[0][0], w[0][1], w[0][2], w[0][3]);
+              *reinterpret_cast<uint4*>(to + 16) = make_uint4(w[1][0], w[1][1], w[1][2], w[1][3]);
             }
           }
           if (strange) odd[news & 1] = 1;
