@@ -43,7 +43,7 @@ constexpr float kTooLarge = 6.0e4f;   // new values beyond this take the fp32 pa
 // kScored: scores written, which also frees the key operand; kAdded: product added to the output, which also frees the
 // value operand (a commit costs the issuing thread some two hundred cycles, so there is one for each)
 enum Bar { kStFull = 0, kStEmpty = 3, kKFull = 6, kVFull = 8, kScored = 10, kPFull = 12, kAdded = 14, kOFree = 16,
-           kQReady = 17, kNewFull = 18, kDrain = 19, kPair = 20, kDecided = 24, kItem = 28, kBars = 29 };
+           kQReady = 17, kNewFull = 18, kDrain = 19, kPair = 20, kDecided = 24, kItem = 28, kSoft = 29, kKeyMeet = 30, kValMeet = 31, kBars = 32 };
 
 template <int D>
 struct Smem {
@@ -77,6 +77,13 @@ __device__ __forceinline__ void umma_f16_ts(uint32_t d, uint32_t a, uint64_t b, 
       "r"(a), "l"(b), "r"(idesc), "n"(kAdd ? 1 : 0)
       : "memory");
 }
+// Sixteen bytes of global memory to shared memory, asynchronously; complete after copy16_wait() in the thread that issued
+// it.  Code that runs once an item is kept small -- rolled loops of such copies instead of loads unrolled into registers:
+// an SM fetches cold code at some twenty cycles an instruction.
+__device__ __forceinline__ void copy16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy16_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 __device__ __forceinline__ bool elect_one() {
   uint32_t yes;
   asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(yes));
@@ -93,6 +100,11 @@ __device__ __forceinline__ void tmem_ld32(uint32_t ta, float (&v)[32]) {
         "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
       : "r"(ta)
       : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t ta, const float (&v)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(ta), "f"(v[0]),
+               "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+               : "memory");
 }
 __device__ __forceinline__ u64 add2(u64 a, u64 b) {
   u64 d;
@@ -158,6 +170,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tree_kernel(KvAttnParams
     init(kQReady, kSoftWarps);
     init(kNewFull, kUnpackWarps);
     for (int i = 0; i < 4; ++i) init(kPair + i, 2);
+    init(kSoft, kSoftWarps);
+    init(kKeyMeet, kKeyWarps);
+    init(kValMeet, kUnpackWarps - kKeyWarps);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     *gave_up = 0;
     odd[0] = odd[1] = 0;
@@ -194,6 +209,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tree_kernel(KvAttnParams
   KvPlace where = place;
   int step = 0, pages = 0, segs = 0, news = 0;      // steps, pages, segments with steps and new-row steps so far
   int swaps = 0, decisions = 0;                     // exchanges between the two threads of a row, reference maxima so far
+  int meets = 0;                                    // meetings of the softmax warps so far
   bool alive = true;
   while (at < place.end && alive) {
     const KvSegment it = kv_segment(p, kRows, at, place.end, where, &at);
@@ -228,23 +244,40 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tree_kernel(KvAttnParams
         ++swaps;
         return to[(half ^ 1) * kRows + r];
       };
+      // the softmax warps' meeting point; what they wrote to shared memory before it is seen by all of them
+      auto meet = [&]() {
+        arrive_warp(kSoft);
+        const bool ok = wait_all(kSoft, meets);
+        ++meets;
+        return ok;
+      };
+      // 16-byte chunk i of row x in a staging tile of `chunks` chunks a row, spread over the banks
+      char* stage = sm + Sm::kKeys;
+      auto staged = [&](int x, int i, int chunks) { return reinterpret_cast<uint4*>(stage) + x * chunks + (i ^ (x & 7)); };
       float c = 0.f;
-      if (busy) {
-        constexpr int kAhead = D / 16 < 8 ? D / 16 : 8;      // 16-byte loads in flight
-        const uint4* qv = reinterpret_cast<const uint4*>(q + half * (D / 2));
-        float big = 0.f;
+      if (steps > 0) {
+        // the rows' queries, whole rows at a time, into the operands' space, which is free once the item before is out
+        alive = wait_all(kOFree, segs + 1);
+        constexpr int kChunks = D / 8;
+        const __nv_bfloat16* q0 = static_cast<const __nv_bfloat16*>(p.q) + node0 * p.q_row + static_cast<size_t>(it.h) * p.G * D;
 #pragma unroll 1
-        for (int i = 0; i < D / 16; i += kAhead) {
-          uint4 raw[kAhead];
+        for (int i = tid; alive && i < rows * kChunks; i += 32 * kSoftWarps) {
+          const int x = row0 + i / kChunks, nd = x / p.G;
+          copy16(staged(i / kChunks, i % kChunks, kChunks), q0 + nd * p.q_row + (x - nd * p.G) * D + 8 * (i % kChunks));
+        }
+        copy16_wait();
+        alive = alive && meet();
+      }
+      if (busy && steps > 0 && alive) {
+        // a thread half a row: largest value, then fp16, scaled by a power of two, in tensor memory
+        const int x0 = min(r, rows - 1);
+        float big = 0.f;
+#pragma unroll 2
+        for (int i = 0; i < D / 16; ++i) {
+          float x[8];
+          unpack8(x, *staged(x0, half * (D / 16) + i, D / 8));
 #pragma unroll
-          for (int k = 0; k < kAhead; ++k) raw[k] = __ldg(qv + i + k);
-#pragma unroll
-          for (int k = 0; k < kAhead; ++k) {
-            float x[8];
-            unpack8(x, raw[k]);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) big = fmaxf(big, fabsf(x[e]));
-          }
+          for (int e = 0; e < 8; ++e) big = fmaxf(big, fabsf(x[e]));
         }
         big = fmaxf(big, exchange(big, &alive));
         const int e = row_exponent(big);
@@ -252,17 +285,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tree_kernel(KvAttnParams
         // the scores' factor; never 0, so that a masked score stays -inf
         c = fmaxf(fabsf(p.scale) * kLog2e * exp2i(e / 2) * exp2i(e - e / 2), 1.2e-38f);
 #pragma unroll 1
-        for (int i = 0; i < D / 64; ++i) {
-          float w[16];
+        for (int i = 0; i < D / 32; ++i) {
+          float w[8];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
+          for (int k = 0; k < 2; ++k) {
             float x[8];
-            unpack8(x, __ldg(qv + 4 * i + k));
+            unpack8(x, *staged(x0, half * (D / 16) + 2 * i + k, D / 8));
 #pragma unroll
             for (int z = 0; z < 4; ++z)
               w[4 * k + z] = __uint_as_float(h2u(__floats2half2_rn(x[2 * z] * f0 * f1, x[2 * z + 1] * f0 * f1)));
           }
-          tmem_st16(lanes + Sm::kQ + half * (D / 4) + 16 * i, w);
+          tmem_st8(lanes + Sm::kQ + half * (D / 4) + 8 * i, w);
         }
         tmem_wait_st();
       }
@@ -387,13 +420,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tree_kernel(KvAttnParams
         // the one after only)
         alive = wait_all(kItem, segs);
         tmem_fence_after();
+        own = with_new && odd[news & 1];
         if (alive && busy) {
           alive = wait_all(kDecided + quarter, decisions + steps - 1);
           follow(*ref);
-          own = with_new && odd[news & 1];
         }
       }
       if (busy) decisions += steps;
+      float* part = it.whole ? nullptr : kv_stream_part(p, blockIdx.x, it.start > place.at, kRows, D);
       if (alive && busy) {
         const bool mine = r < rows;
         float f = 1.f;
@@ -437,51 +471,78 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tree_kernel(KvAttnParams
           }
         }
         l += exchange(l, &alive);
-        float* part = it.whole ? nullptr : kv_stream_part(p, blockIdx.x, it.start > place.at, kRows, D);
+        const float inv = !it.whole ? 1.f : (l == 0.f ? 0.f : 1.f / l);
         __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + (node0 + node) * (static_cast<size_t>(p.Hq) * D) + static_cast<size_t>(head) * D;
-        const float inv = part ? 1.f : (l == 0.f ? 0.f : 1.f / l);
+        if (!own && steps > 0) {
 #pragma unroll 1
-        for (int x = half * (D / 2); x < (half + 1) * (D / 2); x += 16) {
-          float o[16];
-          if (steps > 0) {
-            tmem_ld16(lanes + Sm::kO + x, o);
+          for (int x = half * (D / 2); x < (half + 1) * (D / 2); x += 32) {
+            float o[32];
+            tmem_ld32(lanes + Sm::kO + x, o);
             tmem_wait_ld();
-          } else {
+            if (part) {
 #pragma unroll
-            for (int y = 0; y < 16; ++y) o[y] = 0.f;
-          }
-          if (own) {
+              for (int y = 0; y < 8; ++y)
+                *reinterpret_cast<float4*>(staged(r, x / 4 + y, D / 4)) = make_float4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
+            } else {
 #pragma unroll
-            for (int y = 0; y < 16; ++y) o[y] = f == 0.f ? 0.f : o[y] * f;
-            for (unsigned long long left = anc; left; left &= left - 1) {
-              const int t = __ffsll(static_cast<long long>(left)) - 1;
-              if (ps[t] == 0.f) continue;
-              const __nv_bfloat16* vr = static_cast<const __nv_bfloat16*>(p.v_new) + (node0 + t) * p.kv_row + static_cast<size_t>(it.h) * D + x;
+              for (int y = 0; y < 4; ++y) {
+                __nv_bfloat162 b[4];
 #pragma unroll
-              for (int y = 0; y < 16; ++y) o[y] = fmaf(ps[t], __bfloat162float(vr[y]), o[y]);
+                for (int z = 0; z < 4; ++z) b[z] = __floats2bfloat162_rn(o[8 * y + 2 * z] * inv, o[8 * y + 2 * z + 1] * inv);
+                *staged(r, x / 8 + y, D / 8) = *reinterpret_cast<uint4*>(b);
+              }
             }
           }
-          if (!mine) continue;
-          if (part) {
+        } else {                       // rare: straight to global memory (the loads of tensor memory take the whole warp)
+#pragma unroll 1
+          for (int x = half * (D / 2); x < (half + 1) * (D / 2); x += 4) {
+            float o[4] = {0.f, 0.f, 0.f, 0.f};
+            __syncwarp();
+            if (own) {
+              tmem_ld4(lanes + Sm::kO + x, o);
+              tmem_wait_ld();
 #pragma unroll
-            for (int y = 0; y < 16; y += 4)
-              *reinterpret_cast<float4*>(part + static_cast<size_t>(r) * D + x + y) = make_float4(o[y], o[y + 1], o[y + 2], o[y + 3]);
-          } else {
+              for (int y = 0; y < 4; ++y) o[y] = f == 0.f ? 0.f : o[y] * f;
+              for (unsigned long long left = mine ? anc : 0ull; left; left &= left - 1) {
+                const int t = __ffsll(static_cast<long long>(left)) - 1;
+                if (ps[t] == 0.f) continue;
+                const __nv_bfloat16* vr = static_cast<const __nv_bfloat16*>(p.v_new) + (node0 + t) * p.kv_row + static_cast<size_t>(it.h) * D + x;
 #pragma unroll
-            for (int y = 0; y < 16; y += 8) {
-              uint4 v;
-              __nv_bfloat162 b[4];
-#pragma unroll
-              for (int z = 0; z < 4; ++z) b[z] = __floats2bfloat162_rn(o[y + 2 * z] * inv, o[y + 2 * z + 1] * inv);
-              v.x = *reinterpret_cast<uint32_t*>(&b[0]);
-              v.y = *reinterpret_cast<uint32_t*>(&b[1]);
-              v.z = *reinterpret_cast<uint32_t*>(&b[2]);
-              v.w = *reinterpret_cast<uint32_t*>(&b[3]);
-              *reinterpret_cast<uint4*>(out + x + y) = v;
+                for (int y = 0; y < 4; ++y) o[y] = fmaf(ps[t], __bfloat162float(vr[y]), o[y]);
+              }
             }
+            if (mine && part) {
+              *(reinterpret_cast<float4*>(part) + r * (D / 4) + ((x / 4) ^ (r & 7))) = make_float4(o[0], o[1], o[2], o[3]);
+            } else if (mine) {
+              *reinterpret_cast<__nv_bfloat162*>(out + x) = __floats2bfloat162_rn(o[0] * inv, o[1] * inv);
+              *reinterpret_cast<__nv_bfloat162*>(out + x + 2) = __floats2bfloat162_rn(o[2] * inv, o[3] * inv);
+            }
+            __syncwarp();
           }
         }
         if (part && mine && half == 0) *reinterpret_cast<float2*>(part + kRows * D + 2 * r) = make_float2(m, l);
+      }
+      if (steps > 0 && alive && !own) {
+        // from the staging tile to global memory, whole rows at a time
+        if (part) fence_proxy_async();
+        alive = meet();
+        if (alive && part && tid == 0) {
+          asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(part), "r"(smem_addr(stage)),
+                       "r"(static_cast<uint32_t>(rows * D * 4))
+                       : "memory");
+          asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+          asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+        }
+        if (alive && !part) {
+          constexpr int kChunks = D / 8;
+          __nv_bfloat16* o0 = static_cast<__nv_bfloat16*>(p.out) + (node0 * p.Hq + it.h * p.G) * D;
+#pragma unroll 4
+          for (int i = tid; i < rows * kChunks; i += 32 * kSoftWarps) {
+            const int x = row0 + i / kChunks;
+            *(reinterpret_cast<uint4*>(o0 + static_cast<size_t>(x / p.G) * p.Hq * D + (x % p.G) * D) + i % kChunks) =
+                *staged(i / kChunks, i % kChunks, kChunks);
+          }
+        }
       }
       if (tid == 0 && it.first) {
         const int c0 = kv_cta_of(it.start, place.total, place.ctas);
@@ -509,7 +570,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tree_kernel(KvAttnParams
       // values: unit uw + 4 y holds units (of 16 bytes) 32 uw + lane + 128 y; the first one's octet and channel quad
       const int vt_unit = 32 * uw + lane, vt_oct = (vt_unit / D) * 4 + (vt_unit & 3), vt_quad = (vt_unit % D) >> 2;
       // the operands' space, the ancestor masks and the scales belong to the item before until its output is released
-      if (steps > 0) alive = wait_all(kOFree, segs + 1);
+      // (and to this one's queries, on their way to tensor memory)
+      if (steps > 0) alive = wait_all(kOFree, segs + 1) && wait_all(kQReady, segs);
       for (int i = 0; i < steps && alive; ++i) {
         const int k = step + i, buf = k & 1;
         char* kt = sm + Sm::kKeys + buf * Sm::kKeyTile;
@@ -535,67 +597,69 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tree_kernel(KvAttnParams
               if (a >= 0) device_error(p.c.err, GDN_DEVERR_SCHEDULE, it.b);
               see[ut] = mask;
             }
-            // a warp a row, eight channels a lane, four rows in flight; rows past the tree are zeros
-            const __nv_bfloat16* kn = static_cast<const __nv_bfloat16*>(p.k_new) + node0 * p.kv_row + static_cast<size_t>(it.h) * D + 8 * lane;
-            char* to = kt + lane * Sm::kKeyK;
-            const bool in = lane < D / 8;
+          }
+          // the raw rows, into the space of the other operand buffer, which is unpacked after this step's
+          char* raw = keys ? sm + Sm::kKeys + (buf ^ 1) * Sm::kKeyTile : sm + Sm::kVals + (buf ^ 1) * Sm::kValTile;
+          {
+            const __nv_bfloat16* from = static_cast<const __nv_bfloat16*>(keys ? p.k_new : p.v_new) + node0 * p.kv_row + static_cast<size_t>(it.h) * D;
 #pragma unroll 1
-            for (int t0 = uw; t0 < kPage; t0 += 4 * kKeyWarps) {
-              uint4 raw[4];
+            for (int x = 32 * uw + lane; x < it.r.n * (D / 8); x += 32 * kKeyWarps) {
+              const int t = x / (D / 8), ch = x % (D / 8);
+              copy16(raw + t * (2 * D) + 16 * (ch ^ (t & 7)), from + t * p.kv_row + 8 * ch);
+            }
+            copy16_wait();
+            arrive_warp(keys ? kKeyMeet : kValMeet);
+            alive = wait_all(keys ? kKeyMeet : kValMeet, 2 * news);
+            if (!alive) break;
+          }
+          if (keys) {
+            // two threads a row: its largest value, then fp16, scaled by a power of two
+            const int ut = 32 * uw + lane, t = ut >> 1, part = ut & 1;
+            const bool in = t < it.r.n;
+            float big = 0.f, sum = 0.f;
+#pragma unroll 2
+            for (int ch = part * (D / 16); ch < (part + 1) * (D / 16); ++ch) {
+              float x[8];
+              unpack8(x, in ? *reinterpret_cast<const uint4*>(raw + t * (2 * D) + 16 * (ch ^ (t & 7))) : make_uint4(0, 0, 0, 0));
 #pragma unroll
-              for (int y = 0; y < 4; ++y) {
-                const int t = t0 + y * kKeyWarps;
-                raw[y] = in && t < it.r.n ? __ldg(reinterpret_cast<const uint4*>(kn + t * p.kv_row)) : make_uint4(0, 0, 0, 0);
-              }
-#pragma unroll
-              for (int y = 0; y < 4; ++y) {
-                const int t = t0 + y * kKeyWarps;
-                float x[8], big = 0.f;
-                unpack8(x, raw[y]);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                  strange = strange || !(fabsf(x[e]) < INFINITY);
-                  big = fmaxf(big, fabsf(x[e]));
-                }
-                for (int o = 16; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
-                const int e = row_exponent(big);
-                const float f0 = exp2i(-(e / 2)), f1 = exp2i(-(e - e / 2));
-                if (lane == 0) colscale[t] = exp2i(e / 2) * exp2i(e - e / 2);
-                uint32_t w[4];
-#pragma unroll
-                for (int z = 0; z < 4; ++z) w[z] = h2u(__floats2half2_rn(x[2 * z] * f0 * f1, x[2 * z + 1] * f0 * f1));
-                if (in) *reinterpret_cast<uint4*>(to + (t >> 3) * 128 + (t & 7) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+              for (int e = 0; e < 8; ++e) {
+                big = fmaxf(big, fabsf(x[e]));
+                sum = fmaf(0.f, x[e], sum);
               }
             }
+            strange = sum != 0.f;                    // a NaN or infinity times 0 is NaN
+            big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+            const int e = row_exponent(big);
+            const float f0 = exp2i(-(e / 2)), f1 = exp2i(-(e - e / 2));
+            if (part == 0) colscale[t] = exp2i(e / 2) * exp2i(e - e / 2);
+#pragma unroll 2
+            for (int ch = part * (D / 16); ch < (part + 1) * (D / 16); ++ch) {
+              float x[8];
+              uint32_t w[4];
+              unpack8(x, in ? *reinterpret_cast<const uint4*>(raw + t * (2 * D) + 16 * (ch ^ (t & 7))) : make_uint4(0, 0, 0, 0));
+#pragma unroll
+              for (int z = 0; z < 4; ++z) w[z] = h2u(__floats2half2_rn(x[2 * z] * f0 * f1, x[2 * z + 1] * f0 * f1));
+              *reinterpret_cast<uint4*>(kt + ch * Sm::kKeyK + (t >> 3) * 128 + (t & 7) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
           } else {
-            // eight tokens of two channels a thread
-            const __nv_bfloat16* vn = static_cast<const __nv_bfloat16*>(p.v_new) + node0 * p.kv_row + static_cast<size_t>(it.h) * D;
+            // eight tokens of a channel a thread
 #pragma unroll 1
-            for (int x = 32 * uw + lane; x < 4 * D; x += 32 * (kUnpackWarps - kKeyWarps)) {
-              const int ch = 2 * (x % (D / 2)), o = x / (D / 2);
-              uint32_t raw[8], w[2][4];
+            for (int x = 32 * uw + lane; x < 8 * D; x += 32 * (kUnpackWarps - kKeyWarps)) {
+              const int ch = x % D, o = x / D;
+              float y[8], sum = 0.f, big = 0.f;
 #pragma unroll
               for (int e = 0; e < 8; ++e) {
                 const int t = 8 * o + e;
-                raw[e] = t < it.r.n ? __ldg(reinterpret_cast<const uint32_t*>(vn + t * p.kv_row + ch)) : 0u;
+                y[e] = t < it.r.n ? __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(raw + t * (2 * D) + 16 * ((ch >> 3) ^ e) + 2 * (ch & 7))) : 0.f;
+                sum = fmaf(0.f, y[e], sum);
+                big = fmaxf(big, fabsf(y[e]));
               }
+              const bool bad = sum != 0.f || big > kTooLarge;
+              strange = strange || bad;
+              uint32_t w[4];
 #pragma unroll
-              for (int c2 = 0; c2 < 2; ++c2) {
-                float y[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                  y[e] = __uint_as_float(c2 ? raw[e] & 0xFFFF0000u : raw[e] << 16);
-                  if (!(fabsf(y[e]) < kTooLarge)) {
-                    strange = true;
-                    y[e] = 0.f;
-                  }
-                }
-#pragma unroll
-                for (int z = 0; z < 4; ++z) w[c2][z] = h2u(__floats2half2_rn(y[2 * z], y[2 * z + 1]));
-              }
-              char* to = vt + o * Sm::kValK + (ch >> 3) * 128 + (ch & 7) * 16;
-              *reinterpret_cast<uint4*>(to) = make_uint4(w[0][0], w[0][1], w[0][2], w[0][3]);
-              *reinterpret_cast<uint4*>(to + 16) = make_uint4(w[1][0], w[1][1], w[1][2], w[1][3]);
+              for (int z = 0; z < 4; ++z) w[z] = bad ? 0u : h2u(__floats2half2_rn(y[2 * z], y[2 * z + 1]));
+              *reinterpret_cast<uint4*>(vt + o * Sm::kValK + (ch >> 3) * 128 + (ch & 7) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
             }
           }
           if (strange) odd[news & 1] = 1;
@@ -604,7 +668,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tree_kernel(KvAttnParams
           if (lane == 0) {
             mbar_arrive(&bar[full_bar]);
             mbar_arrive(&bar[kNewFull]);
+            mbar_arrive(&bar[keys ? kKeyMeet : kValMeet]);
           }
+          // the raw rows' space is the next step's operand: every warp has to be done with them
+          alive = wait_all(keys ? kKeyMeet : kValMeet, 2 * news + 1);
           continue;
         }
         const int pg = pages + i - lead, st = pg % kStages;
@@ -778,53 +845,72 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tree_kernel(KvAttnParams
     news += lead;
     alive = __shfl_sync(0xffffffffu, alive, 0);
   }
+  if (tid == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   tmem_fence_before();
   __syncthreads();
   if (warp == kMmaWarp) tmem_dealloc(tmem, Sm::kCols);
 }
 
-// Joins the items that several CTAs share: a warp a row.
+// Joins the items that several CTAs share: a thread four channels of a row, the parts' loads in flight together.
+constexpr int kJoinThreads = 128;
 template <int D>
-__global__ void __launch_bounds__(128) kv4_join_kernel(KvAttnParams p) {
+__global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(KvAttnParams p) {
+  constexpr int kQuads = D / 4, kAhead = 8;
+  asm volatile("griddepcontrol.wait;" ::: "memory");      // launched ahead: everything below reads the first kernel's results
   if (launch_aborted(p.c.err)) return;  // the counts may be an earlier call's
-  const int item = blockIdx.x, r = blockIdx.y * 4 + (threadIdx.x >> 5);
+  const int item = blockIdx.x, lane = threadIdx.x & 31;
+  const int r = blockIdx.y * (kJoinThreads / kQuads) + threadIdx.x / kQuads, i = threadIdx.x % kQuads;
   const int4 t = p.desc[item];          // first CTA, CTAs, starts inside, rows
-  if (t.y < 2 || r >= t.w) return;
+  if (t.y < 2) return;
+  const bool mine = r < t.w;
   const size_t size = static_cast<size_t>(kRows) * (D + 2);
-  const int lane = threadIdx.x & 31, tile = item % p.row_tiles;
+  const int tile = item % p.row_tiles;
   const int lh = item / p.row_tiles, h = lh % p.Hkv, bl = p.b0 * p.layers + lh / p.Hkv;
   const int row = tile * kRows + r;
-  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) +
-                       ((static_cast<size_t>(bl) * p.n_max + row / p.G) * p.Hq + h * p.G + row % p.G) * D;
   auto part_of = [&](int c) { return p.part + (2 * static_cast<size_t>(t.x + c) + (c == 0 && t.z ? 1 : 0)) * size; };
+  // maxima and sums of 32 parts a time, a lane a part (the lanes of a warp share a row, or, for D = 64, two rows: a
+  // half-warp then takes 16 parts a time)
+  constexpr int kLanes = kQuads < 32 ? kQuads : 32;
+  const int sub = lane % kLanes;
   float m = -INFINITY, sum = 0.f;
-  for (int b = 0; b < t.y; b += 32) {
-    const float mc = b + lane < t.y ? part_of(b + lane)[kRows * D + 2 * r] : -INFINITY;
+  for (int b = 0; b < t.y; b += kLanes) {
+    const float mc = mine && b + sub < t.y ? part_of(b + sub)[kRows * D + 2 * r] : -INFINITY;
     float top = fmaxf(m, mc);
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    for (int o = kLanes / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     m = top;
   }
-  float acc[D / 32];
-#pragma unroll
-  for (int i = 0; i < D / 32; ++i) acc[i] = 0.f;
-#pragma unroll 4
-  for (int c = 0; c < t.y; ++c) {
-    const float* part = part_of(c);
-    const float2 ml = *reinterpret_cast<const float2*>(part + kRows * D + 2 * r);
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int b = 0; b < t.y; b += kLanes) {
+    float2 ml = make_float2(-INFINITY, 0.f);
+    if (mine && b + sub < t.y) ml = *reinterpret_cast<const float2*>(part_of(b + sub) + kRows * D + 2 * r);
     // a part that held nothing this row sees has maximum -inf, sum 0 and zeros
-    const float w = (ml.x == -INFINITY && ml.y == 0.f) ? 0.f : exp2f(ml.x - m);
-    sum = fmaf(w, ml.y, sum);
+    const float wt = (ml.x == -INFINITY && ml.y == 0.f) ? 0.f : exp2f(ml.x - m);
+    const float wl = wt * ml.y;
+    for (int c0 = b; c0 < min(t.y, b + kLanes); c0 += kAhead) {
+      float4 v[kAhead];
 #pragma unroll
-    for (int i = 0; i < D / 64; ++i) {
-      const float2 v = *reinterpret_cast<const float2*>(part + static_cast<size_t>(r) * D + 64 * i + 2 * lane);
-      acc[2 * i] = fmaf(w, v.x, acc[2 * i]);
-      acc[2 * i + 1] = fmaf(w, v.y, acc[2 * i + 1]);
+      for (int k = 0; k < kAhead; ++k)
+        if (mine && c0 + k < t.y)
+          v[k] = *(reinterpret_cast<const float4*>(part_of(c0 + k)) + static_cast<size_t>(r) * kQuads + (i ^ (r & 7)));
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const float w = __shfl_sync(0xffffffffu, wt, c0 + k - b, kLanes), s = __shfl_sync(0xffffffffu, wl, c0 + k - b, kLanes);
+        if (mine && c0 + k < t.y) {
+          sum += s;
+          acc.x = fmaf(w, v[k].x, acc.x);
+          acc.y = fmaf(w, v[k].y, acc.y);
+          acc.z = fmaf(w, v[k].z, acc.z);
+          acc.w = fmaf(w, v[k].w, acc.w);
+        }
+      }
     }
   }
+  if (!mine) return;
+  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) +
+                       ((static_cast<size_t>(bl) * p.n_max + row / p.G) * p.Hq + h * p.G + row % p.G) * D + 4 * i;
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
-#pragma unroll
-  for (int i = 0; i < D / 64; ++i)
-    *reinterpret_cast<__nv_bfloat162*>(out + 64 * i + 2 * lane) = __floats2bfloat162_rn(acc[2 * i] * inv, acc[2 * i + 1] * inv);
+  *reinterpret_cast<__nv_bfloat162*>(out) = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
+  *reinterpret_cast<__nv_bfloat162*>(out + 2) = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
 }
 
 template <int D>
@@ -839,8 +925,16 @@ cudaError_t tree_t(KvAttnParams p, cudaStream_t s) {
     k<<<p.ctas, kThreads, Smem<D>::kTotal, s>>>(p);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    kv4_join_kernel<D><<<dim3(p.bn * items, kRows / 4), 128, 0, s>>>(p);
-    e = cudaGetLastError();
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(p.bn * items), static_cast<unsigned>(kRows / (kJoinThreads / (D / 4))));
+    cfg.blockDim = dim3(kJoinThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, kv4_join_kernel<D>, p);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
