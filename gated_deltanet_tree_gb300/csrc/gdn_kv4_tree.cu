@@ -18,7 +18,7 @@
 // bounded.  CTAs take equal runs of the requests' pages (KvPlace); items that two
 // or more CTAs share are joined by a second kernel, spread over the GPU.
 //
-// The nodes' own rows are one more step at the start of an item: fp16 like the
+// The nodes' own rows are one more step of an item: fp16 like the
 // rest, each key row scaled to fp16's range by a power of two, the row's ancestors
 // as its mask.  A masked weight is 0, which would still turn a NaN or an infinity
 // in an unseen row into NaN inside a product; if any such value (or one beyond
@@ -35,8 +35,8 @@ constexpr int kCopyWarp = kSoftWarps + kUnpackWarps, kMmaWarp = kCopyWarp + 1;
 constexpr int kThreads = 32 * (kMmaWarp + 1);
 constexpr int kRows = kKvTreeRows;
 constexpr int kStages = 3;
-constexpr float kLift = 6.f;          // weights are scaled by 2^kLift ...
-constexpr float kSlack = 8.f;         // ... against a maximum that may lag by up to 2^kSlack
+constexpr float kLift = 2.f;          // weights are scaled by 2^kLift ...
+constexpr float kSlack = 13.f;        // ... against a reference that the largest may pass by 2^kSlack: 2^15 at most in fp16
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kTooLarge = 6.0e4f;   // new values beyond this take the fp32 path
 
@@ -99,6 +99,16 @@ __device__ __forceinline__ void tmem_ld32(uint32_t ta, float (&v)[32]) {
         "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]),
         "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
       : "r"(ta)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t ta, const float (&v)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(ta),
+      "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]), "f"(v[9]),
+      "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15]), "f"(v[16]), "f"(v[17]), "f"(v[18]),
+      "f"(v[19]), "f"(v[20]), "f"(v[21]), "f"(v[22]), "f"(v[23]), "f"(v[24]), "f"(v[25]), "f"(v[26]), "f"(v[27]),
+      "f"(v[28]), "f"(v[29]), "f"(v[30]), "f"(v[31])
       : "memory");
 }
 __device__ __forceinline__ void tmem_st8(uint32_t ta, const float (&v)[8]) {
@@ -221,7 +231,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tree_kernel(KvAttnParams
       continue;
     }
     const bool with_new = it.first && p.k_new;
-    const int lead = with_new ? 1 : 0, steps = lead + it.pages;
+    const int steps = it.pages + (with_new ? 1 : 0);      // the new rows last: a page sets better first references
     const int row0 = it.tile * kRows, rows = min(kRows, it.r.n * p.G - row0);
     const size_t node0 = static_cast<size_t>(it.bl) * p.n_max;
 
@@ -314,17 +324,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tree_kernel(KvAttnParams
         const int k = step + i, buf = k & 1;
         if (buf != half) continue;
         alive = wait_all(kScored + buf, k >> 1);
-        if (alive && i < lead) alive = wait_all(kNewFull, news);
+        if (alive && i == it.pages) alive = wait_all(kNewFull, news);
         if (!alive) break;
         tmem_fence_after();
         if (busy) {
           const uint32_t ts = lanes + Sm::kS + 64 * buf;
-          const bool is_new = i < lead;
+          const bool is_new = i == it.pages;
           unsigned long long vis = ~0ull;
           if (is_new) {
             vis = odd[news & 1] ? 0ull : see[node];
           } else {
-            const int toks = it.r.len - (it.page_lo + i - lead) * kPage;
+            const int toks = it.r.len - (it.page_lo + i) * kPage;
             if (toks < kPage) vis = (1ull << toks) - 1;
           }
           if (is_new || vis != ~0ull) {
@@ -378,13 +388,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tree_kernel(KvAttnParams
             if (!alive) break;
             tmem_fence_after();
 #pragma unroll 1
-            for (int x = 0; x < D; x += 16) {
-              float o[16];
-              tmem_ld16(lanes + Sm::kO + x, o);
+            for (int x = 0; x < D; x += 32) {
+              float o[32];
+              tmem_ld32(lanes + Sm::kO + x, o);
               tmem_wait_ld();
 #pragma unroll
-              for (int y = 0; y < 16; ++y) o[y] *= f;
-              tmem_st16(lanes + Sm::kO + x, o);
+              for (int y = 0; y < 32; ++y) o[y] *= f;
+              tmem_st32(lanes + Sm::kO + x, o);
             }
             tmem_wait_st();
           }
@@ -577,9 +587,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tree_kernel(KvAttnParams
         char* kt = sm + Sm::kKeys + buf * Sm::kKeyTile;
         char* vt = sm + Sm::kVals + buf * Sm::kValTile;
         const int free_bar = keys ? kScored + buf : kAdded + buf, full_bar = keys ? kKFull + buf : kVFull + buf;
-        if (i < lead) {
+        if (i == it.pages) {
           // the nodes' own rows, straight from global memory
           alive = wait_all(free_bar, (k >> 1) + 1);
+          // the rows pass through the space of the other operand buffer: the step before has to be done with it
+          if (alive && k > 0) alive = wait_all(keys ? kScored + (buf ^ 1) : kAdded + (buf ^ 1), (k - 1) >> 1);
           if (!alive) break;
           if (keys && uw == 0 && lane == 0) odd[(news + 1) & 1] = 0;      // the next one's, which nobody uses now
           bool strange = false;
@@ -598,7 +610,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tree_kernel(KvAttnParams
               see[ut] = mask;
             }
           }
-          // the raw rows, into the space of the other operand buffer, which is unpacked after this step's
           char* raw = keys ? sm + Sm::kKeys + (buf ^ 1) * Sm::kKeyTile : sm + Sm::kVals + (buf ^ 1) * Sm::kValTile;
           {
             const __nv_bfloat16* from = static_cast<const __nv_bfloat16*>(keys ? p.k_new : p.v_new) + node0 * p.kv_row + static_cast<size_t>(it.h) * D;
@@ -674,11 +685,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tree_kernel(KvAttnParams
           alive = wait_all(keys ? kKeyMeet : kValMeet, 2 * news + 1);
           continue;
         }
-        const int pg = pages + i - lead, st = pg % kStages;
+        const int pg = pages + i, st = pg % kStages;
         alive = wait_all(kStFull + st, pg / kStages);
         if (!alive) break;
         const char* blk = sm + st * Sm::kStage;
-        const int toks = it.r.len - (it.page_lo + i - lead) * kPage;     // tokens past the length read as zeros
+        const int toks = it.r.len - (it.page_lo + i) * kPage;     // tokens past the length read as zeros
         // rolled loops: the roles of an SM share its instruction caches, and unrolled they do not fit
         if (keys) {                    // a unit: a chunk of 32 channels of a token a lane
           const char* from = blk + kt_tok * (D / 2);
@@ -842,7 +853,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tree_kernel(KvAttnParams
     step += steps;
     pages += it.pages;
     segs += steps > 0 ? 1 : 0;
-    news += lead;
+    news += with_new ? 1 : 0;
     alive = __shfl_sync(0xffffffffu, alive, 0);
   }
   if (tid == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
