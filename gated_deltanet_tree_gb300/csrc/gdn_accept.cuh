@@ -18,7 +18,11 @@ struct AcceptParams {
   int32_t* len;
   int32_t* next;
   int32_t* err;
+  int n_slices;                // > 0: every row is reduced at once, in this many slices
+  void* slices;                // [B][n_max][n_slices] partial results of 16 bytes (workspace)
 };
+constexpr double kRowsAtOnceBytes = 128.0 * (1 << 20);
+int accept_slices(int B, int n_max, int V);
 cudaError_t launch_accept(const AcceptParams& p, cudaStream_t s);
 
 }  // namespace gdn
