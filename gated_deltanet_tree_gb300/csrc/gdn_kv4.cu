@@ -18,15 +18,28 @@ namespace {
 
 constexpr int kAppendThreads = 128;
 
-// Eight consecutive elements as fp32.
-__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
-  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-  x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+// Eight consecutive elements, as they lie and as fp32.
+template <typename T>
+struct Raw8;
+template <>
+struct Raw8<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = __ldg(reinterpret_cast<const float4*>(p));
+    b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+  }
+};
+template <>
+struct Raw8<__nv_bfloat16> {
+  uint4 u;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { u = __ldg(reinterpret_cast<const uint4*>(p)); }
+};
+__device__ __forceinline__ void unpack(const Raw8<float>& r, float (&x)[8]) {
+  x[0] = r.a.x; x[1] = r.a.y; x[2] = r.a.z; x[3] = r.a.w;
+  x[4] = r.b.x; x[5] = r.b.y; x[6] = r.b.z; x[7] = r.b.w;
 }
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&x)[8]) {
-  const uint4 u = *reinterpret_cast<const uint4*>(p);
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+__device__ __forceinline__ void unpack(const Raw8<__nv_bfloat16>& r, float (&x)[8]) {
+  const uint32_t w[4] = {r.u.x, r.u.y, r.u.z, r.u.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     x[2 * i] = __uint_as_float(w[i] << 16);
@@ -36,6 +49,11 @@ __device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&x)[8]) {
 
 // Quantises a group held by four adjacent lanes (eight channels each): codes 0..15 of this lane's channels
 // and the group's scale.  All 32 lanes of the warp call it.
+//
+// code = rint(x / d) + 8.  Of bf16 elements x and d have eight significant bits, so x / d is a tie or at least 2^-11
+// away from one: a product with 1 / d, corrected once by its remainder (which makes ties exact), rounds alike at a
+// third of the division's instructions.  fp32 elements are divided.
+template <bool kDivide>
 __device__ __forceinline__ __half quantise8(const float (&x)[8], uint32_t (&code)[8]) {
   float big = 0.f, m = 0.f;
   bool bad = false;
@@ -57,10 +75,19 @@ __device__ __forceinline__ __half quantise8(const float (&x)[8], uint32_t (&code
   d = fminf(fmaxf(d, -kScaleMax), kScaleMax);
   const __half h = __float2half_rn(d);
   d = __half2float(h);
+  const bool none = bad || d == 0.f;
+  const float inv = none ? 0.f : __frcp_rn(d);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float r = (bad || d == 0.f) ? 0.f : rintf(__fdiv_rn(x[i], d));
-    code[i] = static_cast<uint32_t>(static_cast<int>(fminf(fmaxf(r, -8.f), 7.f)) + 8);
+    float q;
+    if (kDivide) {
+      q = none ? 0.f : __fdiv_rn(x[i], d);
+    } else {
+      q = x[i] * inv;
+      q = fmaf(fmaf(-q, d, x[i]), inv, q);
+    }
+    // adding 1.5 2^23 rounds to an integer, ties to even, in the low bits; 8 more makes it the code
+    code[i] = __float_as_uint(fminf(fmaxf(q, -8.f), 7.f) + 12582920.f) & 15u;
   }
   return bad ? __ushort_as_half(0x7FFF) : h;
 }
@@ -102,32 +129,37 @@ __global__ void __launch_bounds__(kAppendThreads) kv4_append_kernel(KvAppendPara
     const T* kn = static_cast<const T*>(p.k_new) + h * D;
     const T* vn = static_cast<const T*>(p.v_new) + h * D;
     const int w = tid % kLanesPerRow;                       // word of the row this lane holds
-    const int rounds = (hi - lo + kRowsPerPass - 1) / kRowsPerPass;
-    for (int i = 0; i < rounds; ++i) {
-      const int r = lo + i * kRowsPerPass + tid / kLanesPerRow;
-      const bool in = r < hi;
-      const int src = in ? (path ? path[first + r] : first + r) : 0;
-      const size_t at = (row0 + src) * p.kv_row + 8 * w;
-      float x[8], y[8];
+    constexpr int kAhead = sizeof(T) == 2 ? 4 : 2;          // rows in flight
+#pragma unroll 1
+    for (int r0 = lo + tid / kLanesPerRow; r0 - tid / kLanesPerRow < hi; r0 += kAhead * kRowsPerPass) {
+      Raw8<T> rk[kAhead], rv[kAhead];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = y[e] = 0.f;
-      if (in) {
-        load8(kn + at, x);
-        load8(vn + at, y);
+      for (int k = 0; k < kAhead; ++k) {
+        const int r = min(r0 + k * kRowsPerPass, hi - 1);   // (rows past the last repeat it and are not stored)
+        const size_t at = (row0 + (path ? path[first + r] : first + r)) * p.kv_row + 8 * w;
+        rk[k].load(kn + at);
+        rv[k].load(vn + at);
       }
-      uint32_t c[8];
-      const __half dk = quantise8(x, c);
-      uint32_t word = 0;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) word |= c[e] << (4 * nibble_of(e));
-      const __half dv = quantise8(y, c);
-      if (in) {
-        reinterpret_cast<uint32_t*>(blk)[Blk::key_word(r, w)] = word;
-        *reinterpret_cast<uint2*>(&codes[r][8 * w]) =
-            make_uint2(c[0] | c[1] << 8 | c[2] << 16 | c[3] << 24, c[4] | c[5] << 8 | c[6] << 16 | c[7] << 24);
-        if ((w & 3) == 0) {
-          reinterpret_cast<__half*>(blk + Blk::kKeyScales)[r * Blk::kGroups + (w >> 2)] = dk;
-          reinterpret_cast<__half*>(blk + Blk::kValScales)[(w >> 2) * kPage + r] = dv;
+      for (int k = 0; k < kAhead; ++k) {
+        const int r = r0 + k * kRowsPerPass;
+        float x[8];
+        uint32_t c[8];
+        unpack(rk[k], x);
+        const __half dk = quantise8<sizeof(T) == 4>(x, c);
+        uint32_t word = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) word |= c[e] << (4 * nibble_of(e));
+        unpack(rv[k], x);
+        const __half dv = quantise8<sizeof(T) == 4>(x, c);
+        if (r < hi) {
+          reinterpret_cast<uint32_t*>(blk)[Blk::key_word(r, w)] = word;
+          *reinterpret_cast<uint2*>(&codes[r][8 * w]) =
+              make_uint2(c[0] | c[1] << 8 | c[2] << 16 | c[3] << 24, c[4] | c[5] << 8 | c[6] << 16 | c[7] << 24);
+          if ((w & 3) == 0) {
+            reinterpret_cast<__half*>(blk + Blk::kKeyScales)[r * Blk::kGroups + (w >> 2)] = dk;
+            reinterpret_cast<__half*>(blk + Blk::kValScales)[(w >> 2) * kPage + r] = dv;
+          }
         }
       }
     }
@@ -174,8 +206,15 @@ __global__ void __launch_bounds__(kAppendThreads) kv4_append_kernel(KvAppendPara
 
 __device__ __forceinline__ void store_out(float* p, float x) { *p = x; }
 __device__ __forceinline__ void store_out(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
+__device__ __forceinline__ void store4(float* p, const float (&x)[4]) {
+  __stcs(reinterpret_cast<float4*>(p), make_float4(x[0], x[1], x[2], x[3]));
+}
+__device__ __forceinline__ void store4(__nv_bfloat16* p, const float (&x)[4]) {
+  reinterpret_cast<__nv_bfloat162*>(p)[0] = __floats2bfloat162_rn(x[0], x[1]);
+  reinterpret_cast<__nv_bfloat162*>(p)[1] = __floats2bfloat162_rn(x[2], x[3]);
+}
 
-// One CTA per (request and layer, page of the range, kv head); a thread takes one word at a time.
+// One CTA per (request and layer, page of the range, kv head).
 template <typename T, int D>
 __global__ void __launch_bounds__(kAppendThreads) kv4_read_kernel(KvReadParams p) {
   using Blk = KvBlock<D>;
@@ -205,22 +244,20 @@ __global__ void __launch_bounds__(kAppendThreads) kv4_read_kernel(KvReadParams p
   const size_t out0 = (static_cast<size_t>(bl) * p.n_rows) * row + static_cast<size_t>(h) * D;
   T* ko = static_cast<T*>(p.k_out) + out0;
   T* vo = static_cast<T*>(p.v_out) + out0;
-  for (int i = tid; i < (rh - rl) * (D / 8); i += kAppendThreads) {
-    const int r = rl + i / (D / 8), w = i % (D / 8);
-    float x[8];
-    uint32_t word = 0;
-    float d = 0.f;
+  // four channels a lane: half a word of codes, 16 (or 8) adjacent bytes out
+#pragma unroll 4
+  for (int i = tid; i < (rh - rl) * (D / 4); i += kAppendThreads) {
+    const int r = rl + i / (D / 4), q = i % (D / 4);
+    float x[4] = {0.f, 0.f, 0.f, 0.f};
     if (r < live) {
-      word = reinterpret_cast<const uint32_t*>(blk)[Blk::key_word(r, w)];
-      d = __half2float(reinterpret_cast<const __half*>(blk + Blk::kKeyScales)[r * Blk::kGroups + (w >> 2)]);
-    }
-    T* dst = ko + (first + r) * static_cast<long long>(row) + 8 * w;
+      const uint32_t word = reinterpret_cast<const uint32_t*>(blk)[Blk::key_word(r, q >> 1)] >> (8 * (q & 1));
+      const float d = __half2float(reinterpret_cast<const __half*>(blk + Blk::kKeyScales)[r * Blk::kGroups + (q >> 3)]);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      x[e] = r < live ? static_cast<float>(static_cast<int>((word >> (4 * nibble_of(e))) & 15u) - 8) * d : 0.f;
-      store_out(dst + e, x[e]);
+      for (int e = 0; e < 4; ++e) x[e] = static_cast<float>(static_cast<int>((word >> (4 * nibble_of(e))) & 15u) - 8) * d;
     }
+    store4(ko + (first + r) * static_cast<long long>(row) + 4 * q, x);
   }
+#pragma unroll 2
   for (int i = tid; i < 8 * D; i += kAppendThreads) {
     const int c = i % D, o = i / D;
     if (8 * o + 8 <= rl || 8 * o >= rh) continue;
