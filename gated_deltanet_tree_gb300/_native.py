@@ -163,6 +163,15 @@ def _stream(stream) -> Optional[int]:
     return stream.cuda_stream
 
 
+def _stream_of(stream, device_index: int) -> Optional[int]:
+    """The given stream, or the device's current one (by torch's raw query, which makes no stream object)."""
+    if stream is None:
+        import torch
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        return raw(device_index) if raw is not None else torch.cuda.current_stream(device_index).cuda_stream
+    return _stream(stream)
+
+
 def gdn_abi_version() -> int:
     return lib().gdn_abi_version()
 

@@ -204,8 +204,6 @@ __global__ void __launch_bounds__(kAppendThreads) kv4_append_kernel(KvAppendPara
   }
 }
 
-__device__ __forceinline__ void store_out(float* p, float x) { *p = x; }
-__device__ __forceinline__ void store_out(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
 __device__ __forceinline__ void store4(float* p, const float (&x)[4]) {
   __stcs(reinterpret_cast<float4*>(p), make_float4(x[0], x[1], x[2], x[3]));
 }
@@ -257,21 +255,27 @@ __global__ void __launch_bounds__(kAppendThreads) kv4_read_kernel(KvReadParams p
     }
     store4(ko + (first + r) * static_cast<long long>(row) + 4 * q, x);
   }
-#pragma unroll 2
-  for (int i = tid; i < 8 * D; i += kAppendThreads) {
-    const int c = i % D, o = i / D;
+  // values: four channels, eight tokens a lane
+#pragma unroll 1
+  for (int i = tid; i < 2 * D; i += kAppendThreads) {
+    const int cq = i % (D / 4), o = i / (D / 4);
     if (8 * o + 8 <= rl || 8 * o >= rh) continue;
-    const uint32_t word =
-        8 * o < live ? reinterpret_cast<const uint32_t*>(blk + Blk::kValCodes)[Blk::val_word(c, o)] : 0u;
+    uint4 word = make_uint4(0, 0, 0, 0), scale = make_uint4(0, 0, 0, 0);
+    if (8 * o < live) {
+      word = *(reinterpret_cast<const uint4*>(blk + Blk::kValCodes) + Blk::val_word(4 * cq, o) / 4);
+      scale = *reinterpret_cast<const uint4*>(blk + Blk::kValScales + 2 * ((cq >> 3) * kPage + 8 * o));
+    }
+    const uint32_t w[4] = {word.x, word.y, word.z, word.w}, sc[4] = {scale.x, scale.y, scale.z, scale.w};
+    T* dst = vo + (first + 8 * o) * static_cast<long long>(row) + 4 * cq;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const int r = 8 * o + e;
-      if (r < rl || r >= rh) continue;
-      float x = 0.f;
-      if (r < live)
-        x = static_cast<float>(static_cast<int>((word >> (4 * nibble_of(e))) & 15u) - 8) *
-            __half2float(reinterpret_cast<const __half*>(blk + Blk::kValScales)[(c / kGroup) * kPage + r]);
-      store_out(vo + (first + r) * static_cast<long long>(row) + c, x);
+      const float d = __half2float(__ushort_as_half(static_cast<unsigned short>(sc[e >> 1] >> (16 * (e & 1)))));
+      float x[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        x[c] = r < live ? static_cast<float>(static_cast<int>((w[c] >> (4 * nibble_of(e))) & 15u) - 8) * d : 0.f;
+      if (r >= rl && r < rh) store4(dst + e * static_cast<long long>(row), x);
     }
   }
 }

@@ -5,6 +5,7 @@ libgdn_tree.so through the ctypes binding.
 """
 from __future__ import annotations
 
+import ctypes
 from typing import Optional, Sequence
 
 import numpy as np
@@ -130,11 +131,14 @@ def paths_tensor(paths: Sequence[Sequence[int]], n_max: int, device) -> tuple:
     return torch.from_numpy(P).to(device), torch.from_numpy(L).to(device)
 
 
+_DTYPES = {torch.float32: N.GDN_DTYPE_F32, torch.bfloat16: N.GDN_DTYPE_BF16}
+
+
 def _dtype_code(dtype: torch.dtype, what: str) -> int:
-    codes = {torch.float32: N.GDN_DTYPE_F32, torch.bfloat16: N.GDN_DTYPE_BF16}
-    if dtype not in codes:
+    code = _DTYPES.get(dtype)
+    if code is None:
         raise TypeError(f"{what} is {dtype}: fp32 and bf16 are supported")
-    return codes[dtype]
+    return code
 
 
 def make_attn_dims(Hq: int, Hkv: int, D: int, dtype: torch.dtype = torch.bfloat16,
@@ -147,9 +151,11 @@ def make_attn_dims(Hq: int, Hkv: int, D: int, dtype: torch.dtype = torch.bfloat1
 def _row_stride(t: torch.Tensor, name: str, shape: tuple) -> int:
     """Elements from one node's row of t [B, layers, n, heads, D] to the next; rows of a fused projection (a slice of
     wider rows) are taken as they lie."""
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, the call needs {shape}")
     B, L, n, H, D = shape
+    if t.is_contiguous():
+        return H * D
     row = t.stride(2) if n > 1 else (t.stride(1) if L > 1 else t.stride(0) if B > 1 else H * D)
     want = (L * n * row, n * row, row, D, 1)
     for size, got, need in zip(shape, t.stride(), want):
@@ -185,6 +191,11 @@ class KV4Cache:
                                       seq_len=seq_len.data_ptr(), ticket=self.ticket.data_ptr(),
                                       err=self.err.data_ptr(), B=self.B, layers=self.layers,
                                       pages_max=self.pages_max, n_pages=pool.shape[1])
+        # what every call passes, once (a call's own time on the host is what a small one costs)
+        self._type = torch.bfloat16 if dims.dtype == N.GDN_DTYPE_BF16 else torch.float32
+        self._index = pool.get_device()
+        self._refs = (ctypes.byref(self.dims), ctypes.byref(self.struct))
+        self._heads = (dims.Hq, dims.Hkv, dims.D)
 
     @classmethod
     def empty(cls, dims: N.gdn_attn_dims, B: int, layers: int, pages_max: int, device="cuda") -> "KV4Cache":
@@ -194,26 +205,27 @@ class KV4Cache:
         return cls(dims, pool, table, torch.zeros(B, dtype=torch.int32, device=device))
 
     def _check_type(self, t: torch.Tensor, name: str):
-        if _dtype_code(t.dtype, name) != self.dims.dtype or t.device != self.device:
+        if t.dtype is not self._type or t.get_device() != self._index:
+            _dtype_code(t.dtype, name)
             raise ValueError(f"{name} is {t.dtype} on {t.device}: not the cache's type or device")
 
     def _check_i32(self, t: torch.Tensor, name: str, shape: tuple):
-        if t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous() or t.device != self.device:
+        if t.dtype is not torch.int32 or t.shape != shape or not t.is_contiguous() or t.get_device() != self._index:
             raise ValueError(f"{name} is a contiguous int32 tensor {shape} on {self.device}, got {tuple(t.shape)} "
                              f"{t.dtype} on {t.device}")
 
     def _rows(self, k: torch.Tensor, v: torch.Tensor) -> int:
-        d = self.dims
         if k.dim() != 5:
             raise ValueError(f"k_new is [B, layers, n, Hkv, D], got {tuple(k.shape)}")
         n = k.shape[2]
-        row = 0
-        for t, name in ((k, "k_new"), (v, "v_new")):
-            self._check_type(t, name)
-            row = _row_stride(t, name, (self.B, self.layers, n, d.Hkv, d.D))
-            d.kv_row = row if name == "k_new" else d.kv_row
-        if row != d.kv_row:
+        _, Hkv, D = self._heads
+        want = (self.B, self.layers, n, Hkv, D)
+        self._check_type(k, "k_new")
+        self._check_type(v, "v_new")
+        row = _row_stride(k, "k_new", want)
+        if row != _row_stride(v, "v_new", want):
             raise ValueError("k_new and v_new have different row strides")
+        self.dims.kv_row = row
         return n
 
     def append(self, k_new: torch.Tensor, v_new: torch.Tensor, count: torch.Tensor,
@@ -224,17 +236,22 @@ class KV4Cache:
         self._check_i32(count, "count", (self.B,))
         if path is not None:
             self._check_i32(path, "path", (self.B, n))
-        N.gdn_kv4_append(self.dims, self.layers, n, k_new, v_new, path, count, self.struct, stream)
+        dims, cache = self._refs
+        N._check(N.lib().gdn_kv4_append(dims, self.layers, n, k_new.data_ptr(), v_new.data_ptr(),
+                                        None if path is None else path.data_ptr(), count.data_ptr(), cache,
+                                        N._stream_of(stream, self._index)))
 
     def read(self, start: Optional[torch.Tensor], n: int, dtype: torch.dtype = torch.float32, stream=None):
         """Values of tokens start[b] .. start[b] + n - 1 (None: from 0) -> k, v [B, layers, n, Hkv, D]; zeros past a
         request's length."""
         if start is not None:
             self._check_i32(start, "start", (self.B,))
-        shape = (self.B, self.layers, n, self.dims.Hkv, self.dims.D)
-        k = torch.empty(shape, dtype=dtype, device=self.device)
-        v = torch.empty(shape, dtype=dtype, device=self.device)
-        N.gdn_kv4_read(self.dims, self.layers, n, start, _dtype_code(dtype, "dtype"), k, v, self.struct, stream)
+        code = _dtype_code(dtype, "dtype")
+        kv = torch.empty((2, self.B, self.layers, n, *self._heads[1:]), dtype=dtype, device=self.device)
+        k, v = kv.unbind(0)
+        dims, cache = self._refs
+        N._check(N.lib().gdn_kv4_read(dims, self.layers, n, None if start is None else start.data_ptr(), code,
+                                      k.data_ptr(), v.data_ptr(), cache, N._stream_of(stream, self._index)))
         return k, v
 
     def _workspace(self, n_max: int, max_len: int):
@@ -252,20 +269,24 @@ class KV4Cache:
                   out: torch.Tensor, sched: Optional[DeviceSchedule] = None, max_len: int = 0, stream=None):
         """Nodes q [B, layers, n_max, Hq, D] attend to the cached tokens and (with k_new, v_new) to their ancestors'
         and their own rows; sched None: one node a request.  max_len bounds the lengths where the host knows it."""
-        d = self.dims
         n = 1 if sched is None else sched.struct.n_max
+        Hq, _, D = self._heads
         self._check_type(q, "q")
         self._check_type(out, "out")
-        d.q_row = _row_stride(q, "q", (self.B, self.layers, n, d.Hq, d.D))
-        if tuple(out.shape) != tuple(q.shape) or not out.is_contiguous():
+        self.dims.q_row = _row_stride(q, "q", (self.B, self.layers, n, Hq, D))
+        if out.shape != q.shape or not out.is_contiguous():
             raise ValueError("out is contiguous with the shape of q")
         if (k_new is None) != (v_new is None):
             raise ValueError("k_new and v_new: both or neither")
         if k_new is not None and self._rows(k_new, v_new) != n:
             raise ValueError("k_new and q have different node counts")
         self._workspace(n, max_len)
-        N.gdn_kv4_attention(d, self.layers, None if sched is None else sched.struct, q, k_new, v_new, out, self.struct,
-                            max_len, self.workspace, self.workspace.numel(), stream)
+        dims, cache = self._refs
+        N._check(N.lib().gdn_kv4_attention(dims, self.layers, None if sched is None else ctypes.byref(sched.struct),
+                                           q.data_ptr(), None if k_new is None else k_new.data_ptr(),
+                                           None if v_new is None else v_new.data_ptr(), out.data_ptr(), cache, max_len,
+                                           self.workspace.data_ptr(), self.workspace.numel(),
+                                           N._stream_of(stream, self._index)))
 
     def check_error(self, stream=None):
         N.gdn_check_error_words(self.err, stream)
@@ -284,21 +305,28 @@ class TreeAcceptor:
         self.err = torch.zeros(4, **i32)
         self.ws_bytes = N.gdn_accept_workspace_bytes(B, n_max, V)
         self.workspace = torch.zeros(max(self.ws_bytes, 256), dtype=torch.uint8, device=self.device)
+        self._index = self.path.get_device()
+        self._out = (self.path.data_ptr(), self.len.data_ptr(), self.next.data_ptr(), self.err.data_ptr(),
+                     self.workspace.data_ptr(), self.workspace.numel())
 
     def _rows(self, t: torch.Tensor, name: str) -> int:
         want = (self.B, self.n_max, self.V)
-        if tuple(t.shape) != want or t.device.type != self.device.type:
+        if t.shape != want or t.get_device() != self._index:
             raise ValueError(f"{name} is {want} on {self.device}, got {tuple(t.shape)} on {t.device}")
+        if t.is_contiguous():
+            return self.V
         row = t.stride(1) if self.n_max > 1 else t.stride(0) if self.B > 1 else self.V
         if (self.V > 1 and t.stride(2) != 1) or (self.B > 1 and t.stride(0) != self.n_max * row):
             raise ValueError(f"{name} has strides {t.stride()}: rows need one stride and contiguous values")
         return row
 
-    def _small(self, t: Optional[torch.Tensor], name: str, shape: tuple, dtype: torch.dtype):
+    def _small(self, t: Optional[torch.Tensor], name: str, shape: tuple, dtype: torch.dtype) -> int:
         if t is None:
             raise ValueError(f"{name} is needed where a temperature is given")
-        if tuple(t.shape) != shape or t.dtype != dtype or not t.is_contiguous():
-            raise ValueError(f"{name} is a contiguous {dtype} tensor {shape}, got {tuple(t.shape)} {t.dtype}")
+        if t.shape != shape or t.dtype is not dtype or not t.is_contiguous() or t.get_device() != self._index:
+            raise ValueError(f"{name} is a contiguous {dtype} tensor {shape} on {self.device}, got {tuple(t.shape)} "
+                             f"{t.dtype} on {t.device}")
+        return t.data_ptr()
 
     def accept(self, sched: DeviceSchedule, logits: torch.Tensor, tokens: torch.Tensor,
                uniform: Optional[torch.Tensor] = None, gumbel: Optional[torch.Tensor] = None,
@@ -306,21 +334,23 @@ class TreeAcceptor:
         """Walk every request's tree -> (path [B, n_max] padded with -1, len [B], next [B]), this object's buffers;
         path and len go into TreeVerifier.commit and KV4Cache.append as they are.  temperature None: greedy."""
         row = self._rows(logits, "logits")
-        self._small(tokens, "tokens", (self.B, self.n_max), torch.int32)
+        tok = self._small(tokens, "tokens", (self.B, self.n_max), torch.int32)
         if sched.struct.B != self.B or sched.struct.n_max != self.n_max:
             raise ValueError("the schedule's batch is not this object's")
+        u = g = t = dp = None
         if temperature is not None:
-            self._small(temperature, "temperature", (self.B,), torch.float32)
-            self._small(uniform, "uniform", (self.B, self.n_max), torch.float32)
-            self._small(gumbel, "gumbel", (self.B, self.V), torch.float32)
+            t = self._small(temperature, "temperature", (self.B,), torch.float32)
+            u = self._small(uniform, "uniform", (self.B, self.n_max), torch.float32)
+            g = self._small(gumbel, "gumbel", (self.B, self.V), torch.float32)
         draft = N.GDN_DTYPE_F32
         if draft_probs is not None:
             draft = _dtype_code(draft_probs.dtype, "draft_probs")
             if self._rows(draft_probs, "draft_probs") != row:
                 raise ValueError("draft_probs and logits have different row strides")
-        N.gdn_tree_accept(sched.struct, self.V, row, _dtype_code(logits.dtype, "logits"), logits, tokens, draft_probs,
-                          draft, uniform, gumbel, temperature, self.path, self.len, self.next, self.err,
-                          self.workspace, self.workspace.numel(), stream)
+            dp = draft_probs.data_ptr()
+        N._check(N.lib().gdn_tree_accept(ctypes.byref(sched.struct), self.V, row, _dtype_code(logits.dtype, "logits"),
+                                         logits.data_ptr(), tok, dp, draft, u, g, t, *self._out,
+                                         N._stream_of(stream, self._index)))
         return self.path, self.len, self.next
 
     def check_error(self, stream=None):
