@@ -499,9 +499,11 @@ gdn_status gdn_kv4_attention(const gdn_attn_dims* d, int32_t layers, const gdn_b
   if (max_len < 0) return fail(GDN_ERR_INVALID_ARG, "max_len = %d", max_len);
   GDN_CHECK_PTR(workspace, "workspace");
   const int n_max = sched ? sched->n_max : 1;
-  const int most = max_len ? std::min(pages_of(max_len), cache->pages_max) : cache->pages_max;
   const gdn::KvAttnPlan pl =
-      gdn::plan_kv4_attention(d->Hq, d->Hkv, d->D, d->dtype, cache->B, layers, n_max, most);
+      gdn::plan_kv4_attention(d->Hq, d->Hkv, d->D, d->dtype, cache->B, layers, n_max, pages_of(max_len));
+  if (!pl.kernel)
+    return fail(GDN_ERR_UNSUPPORTED, "layers = %d, Hkv = %d, n_max = %d: above %d tiles of %d rows a request", layers, d->Hkv,
+                n_max, gdn::kKvCounters, gdn::kKvDecRows);
   if (workspace_bytes < pl.bytes)
     return fail(GDN_ERR_CAPACITY, "workspace holds %zu bytes, the call needs %zu", workspace_bytes, pl.bytes);
   gdn::KvAttnParams p{};
@@ -512,13 +514,12 @@ gdn_status gdn_kv4_attention(const gdn_attn_dims* d, int32_t layers, const gdn_b
   p.kv_row = d->kv_row ? d->kv_row : static_cast<long long>(d->Hkv) * d->D;
   p.words = sched ? sched->words : nullptr;
   p.q = q; p.k_new = k_new; p.v_new = v_new; p.out = out;
-  p.ctas = pl.ctas; p.least = pl.least; p.row_tiles = pl.row_tiles; p.chunks = pl.chunks; p.chunk_pages = pl.chunk_pages;
+  p.ctas = pl.ctas; p.least = pl.least; p.row_tiles = pl.row_tiles;
   p.done = static_cast<int32_t*>(workspace);
   p.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + pl.done_bytes);
   p.desc = reinterpret_cast<int4*>(p.done + gdn::kKvCounters);
-  cudaError_t e = pl.kernel == gdn::kKvDec    ? gdn::launch_kv4_attention_dec(p, stream)
-                  : pl.kernel == gdn::kKvTree ? gdn::launch_kv4_attention_tree(p, stream)
-                                              : gdn::launch_kv4_attention_simt(p, stream);
+  cudaError_t e =
+      pl.kernel == gdn::kKvDec ? gdn::launch_kv4_attention_dec(p, stream) : gdn::launch_kv4_attention_tree(p, stream);
   if (e != cudaSuccess) return cuda_fail(e, "cache attention launch");
   return GDN_OK;
 }

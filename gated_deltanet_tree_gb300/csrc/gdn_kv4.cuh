@@ -75,8 +75,8 @@ __device__ __forceinline__ char* kv_block(const KvCacheView& c, int Hkv, long lo
 }
 #endif
 
-// The attention call, whichever kernel takes it.  A work item is (request, layer, kv head); its rows are
-// (node, query head of the group), row = node * G + g, taken in tiles; its tokens are split in chunks of pages.
+// The attention call, whichever kernel takes it.  The rows of a (request, layer, kv head) are its (node, query head of
+// the group) pairs, row = node * G + g, taken in tiles.
 struct KvAttnParams {
   KvCacheView c;
   int layers, n_max, Hq, Hkv, D, dtype, G;
@@ -90,30 +90,25 @@ struct KvAttnParams {
   int b0, bn;                  // requests of this launch (the kernels that take units)
   int ctas, least;             // CTAs launched, and the units one takes at least where there are few
   int each;                    // CTAs an item of a lone request can have: ctas / (layers * Hkv * row_tiles)
-  int row_tiles;               // row tiles of an item, at most
-  int chunks;                  // token chunks of an item (grid)
-  int chunk_pages;             // pages of a chunk, where the request is no longer than the host expects
+  int row_tiles;               // row tiles of a (request, layer, kv head), at most
   float* part;                 // partial results, rows of D + 2: unnormalised output, maximum (base 2), sum
   int4* desc;                  // [kKvItems] what the join of an item reads (tree kernel)
-  int32_t* done;               // [kKvCounters] chunks finished of each row tile, zero between calls
+  int32_t* done;               // [kKvCounters] CTAs that have finished an item, zero between calls
 };
 struct KvAttnPlan {
-  int kernel;                  // kKvSimt, ...
+  int kernel;                  // kKvDec or kKvTree; 0: no kernel takes the call
   int ctas, least;
-  int tile_rows, row_tiles, chunks, chunk_pages;
-  size_t done_bytes, bytes;    // workspace: counters, then partial results
+  int tile_rows, row_tiles;
+  size_t done_bytes, bytes;    // workspace: counters and records, then partial results
 };
-constexpr int kKvSimt = 0;      // CUDA cores: fp32 calls, and what the others do not take
-constexpr int kKvDec = 1;       // at most kKvDecRows rows a kv head
+constexpr int kKvDec = 1;       // tiles of kKvDecRows rows
 constexpr int kKvDecRows = 8;
 constexpr int kKvTree = 2;      // tiles of kKvTreeRows rows
 constexpr int kKvTreeRows = 128;
-// Counters lead every workspace at a fixed size, so that one workspace serves calls of different shapes; with
-// more tiles than this the GPU is full without splitting the tokens.
+// Counters lead every workspace at a fixed size, so that one workspace serves calls of different shapes.
 constexpr int kKvCounters = 16384;
 constexpr int kKvItems = 4096;  // items of a launch of the tree kernel; their join records follow the counters
-KvAttnPlan plan_kv4_attention(int Hq, int Hkv, int D, int dtype, int B, int layers, int n_max, int pages);
-cudaError_t launch_kv4_attention_simt(const KvAttnParams& p, cudaStream_t s);
+KvAttnPlan plan_kv4_attention(int Hq, int Hkv, int D, int dtype, int B, int layers, int n_max, int max_pages);
 cudaError_t launch_kv4_attention_dec(const KvAttnParams& p, cudaStream_t s);
 cudaError_t launch_kv4_attention_tree(const KvAttnParams& p, cudaStream_t s);
 

@@ -1,46 +1,11 @@
 // Parts the attention kernels over the 4-bit cache share: which rows and pages a
-// CTA takes, the nodes' ancestor masks, and the join of the chunks' results.
+// CTA takes, the nodes' root paths, and the join of partial results.
 #pragma once
 #include <cmath>
 
 #include "gdn_kv4.cuh"
 
 namespace gdn {
-
-struct KvItem {
-  int b, l, h, bl, tile;
-};
-__device__ __forceinline__ KvItem kv_item(const KvAttnParams& p, unsigned x) {
-  KvItem it;
-  it.tile = x % p.row_tiles;
-  x /= p.row_tiles;
-  it.h = x % p.Hkv;
-  it.bl = x / p.Hkv;
-  it.b = it.bl / p.layers;
-  it.l = it.bl % p.layers;
-  return it;
-}
-
-// The request's nodes and length, and the pages of one chunk.  Every chunk has the planned number of pages;
-// a request longer than the host expected gets longer chunks instead of more.
-struct KvSpan {
-  bool ok;
-  int bit;                     // error bit where not ok
-  int n, len, chunks, page_lo, page_hi;
-};
-__device__ __forceinline__ KvSpan kv_span(const KvAttnParams& p, const KvItem& it, int chunk) {
-  KvSpan s{};
-  s.n = p.words ? p.words[static_cast<size_t>(it.b) * SchedLayout{p.n_max}.words()] : 1;
-  s.len = p.c.seq_len[it.b];
-  s.bit = (s.n < 1 || s.n > p.n_max) ? GDN_DEVERR_SCHEDULE : GDN_DEVERR_CACHE;
-  s.ok = s.n >= 1 && s.n <= p.n_max && s.len >= 0 && s.len <= static_cast<long long>(p.c.pages_max) * kPage;
-  const int pages = (s.len + kPage - 1) / kPage;
-  const int each = max(p.chunk_pages, (pages + p.chunks - 1) / p.chunks);
-  s.chunks = max(1, (pages + each - 1) / each);
-  s.page_lo = min(pages, chunk * each);
-  s.page_hi = min(pages, s.page_lo + each);
-  return s;
-}
 
 // ---- A schedule without waves.  The pages of all work items, one after another, are one sequence of units; CTA c
 // of N takes units [c T / N, (c + 1) T / N), whatever items they belong to, so that ragged lengths cost no idle
@@ -189,37 +154,32 @@ __device__ __forceinline__ float* kv_stream_part(const KvAttnParams& p, int c, b
   return p.part + (2 * static_cast<size_t>(c) + (starts_inside ? 1 : 0)) * tile_rows * (D + 2);
 }
 
-// see[i], bit j: node j is i or an ancestor of i.  The CTA's threads call it; false if the parents are no tree.
-__device__ __forceinline__ bool kv_ancestors(const KvAttnParams& p, int b, int n, unsigned long long* see) {
-  bool ok = true;
-  const int32_t* parent = p.words ? p.words + static_cast<size_t>(b) * SchedLayout{p.n_max}.words() + SchedLayout{p.n_max}.parent()
-                                  : nullptr;
-  for (int i = threadIdx.x; i < n; i += blockDim.x) {
-    unsigned long long m = 1ull << i;
-    int a = parent ? parent[i] : -1, prev = i;
-    while (a >= 0 && a < prev) {
-      m |= 1ull << a;
-      prev = a;
-      a = parent[a];
-    }
-    ok = ok && a < 0;
-    see[i] = m;
+// The request's parents, and the nodes on the root path of node i (itself included) as a bit mask; false if the
+// parents are no tree (the mask then ends at the fault).
+__device__ __forceinline__ const int32_t* kv_parents(const KvAttnParams& p, int b) {
+  const SchedLayout lay{p.n_max};
+  return p.words + static_cast<size_t>(b) * lay.words() + lay.parent();
+}
+__device__ __forceinline__ bool kv_root_path(const int32_t* parent, int i, unsigned long long* mask) {
+  unsigned long long m = 1ull << i;
+  int a = parent ? parent[i] : -1, prev = i;
+  while (a >= 0 && a < prev) {
+    m |= 1ull << a;
+    prev = a;
+    a = parent[a];
   }
-  return __syncthreads_and(ok);
+  *mask = m;
+  return a < 0;
 }
 
-// Partial result of a row tile over one chunk: rows of D outputs, maximum, sum.
-__device__ __forceinline__ float* kv_part(const KvAttnParams& p, size_t tile, int chunk, int tile_rows, int D) {
-  return p.part + (tile * p.chunks + chunk) * static_cast<size_t>(tile_rows) * (D + 2);
-}
-// True in the CTA that finishes the tile's chunks last, with every chunk's partial result visible.
-__device__ __forceinline__ bool kv_last_chunk(const KvAttnParams& p, size_t tile, int chunks, int* flag) {
+// True in the CTA that finishes an item last of `count`, with every partial result visible.
+__device__ __forceinline__ bool kv_last(const KvAttnParams& p, size_t item, int count, int* flag) {
   __threadfence();
   __syncthreads();
   if (threadIdx.x == 0) {
-    const int prev = atomicAdd(&p.done[tile], 1);
-    *flag = prev == chunks - 1;
-    if (prev == chunks - 1) p.done[tile] = 0;
+    const int prev = atomicAdd(&p.done[item], 1);
+    *flag = prev == count - 1;
+    if (prev == count - 1) p.done[item] = 0;
   }
   __syncthreads();
   __threadfence();
@@ -228,46 +188,13 @@ __device__ __forceinline__ bool kv_last_chunk(const KvAttnParams& p, size_t tile
 __device__ __forceinline__ void kv_store(float* p, float x) { *p = x; }
 __device__ __forceinline__ void kv_store(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
 
-// The join of one row's partial results, by one warp, in order: out = sum_c 2^{m_c - m} O_c / sum_c 2^{m_c - m} l_c
-// (maxima are kept in base 2).  part_of(c), c < count, is the row in partial result c.
-template <typename T, int D, typename F>
-__device__ __forceinline__ void kv_join(int count, F part_of, T* out) {
-  const int lane = threadIdx.x & 31;
-  float m = -INFINITY;
-  for (int c = lane; c < count; c += 32) m = fmaxf(m, __ldcg(part_of(c) + D));
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  float acc[D / 32], sum = 0.f;
-#pragma unroll
-  for (int i = 0; i < D / 32; ++i) acc[i] = 0.f;
-#pragma unroll 8
-  for (int c = 0; c < count; ++c) {
-    const float* part = part_of(c);
-    const float2 ml = __ldcg(reinterpret_cast<const float2*>(part + D));
-    // a part that held nothing this row sees has weight 0 and zeros
-    const float w = (ml.x == -INFINITY && ml.y == 0.f) ? 0.f : exp2f(ml.x - m);
-    sum = fmaf(w, ml.y, sum);
-#pragma unroll
-    for (int i = 0; i < D / 64; ++i) {
-      const float2 v = __ldcg(reinterpret_cast<const float2*>(part + 64 * i + 2 * lane));
-      acc[2 * i] = fmaf(w, v.x, acc[2 * i]);
-      acc[2 * i + 1] = fmaf(w, v.y, acc[2 * i + 1]);
-    }
-  }
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-#pragma unroll
-  for (int i = 0; i < D / 64; ++i) {
-    kv_store(out + 64 * i + 2 * lane, acc[2 * i] * inv);
-    kv_store(out + 64 * i + 2 * lane + 1, acc[2 * i + 1] * inv);
-  }
-}
-
-// The same for all rows of a tile by the whole CTA, from partial results with the layout of kv_stream_part.  Reads of
-// what other SMs just wrote take a microsecond and more, so the loads of a step are all in flight together: a row's
+// The join of all rows of a tile by the whole CTA, in order: out = sum_c 2^{m_c - m} O_c / sum_c 2^{m_c - m} l_c (maxima
+// are kept in base 2), from partial results with the layout of kv_stream_part.  Reads of what other SMs just wrote take a microsecond and more, so the loads of a step are all in flight together: a row's
 // maxima and sums by one warp, then four channels of a row per thread, kAhead parts at a time.  `sh` holds
-// (count + 1) * rows floats; row r of the tile is query head r % G of node r / G, counted from out0.
+// (count + 1) * rows floats; row r of the item is query head r % G of node r / G, counted from out0.
 struct KvJoin {
   int c0, count, rows, inside;     // first CTA, CTAs, rows; the item starts inside its first CTA
-  int b, l, h;
+  int b, l, h, row0;
 };
 template <typename T, int D>
 __device__ __forceinline__ void kv_join_rows(const float* part, const KvJoin& t, int tile_rows, T* out0, int G,
@@ -327,17 +254,13 @@ __device__ __forceinline__ void kv_join_rows(const float* part, const KvJoin& t,
           acc.w = fmaf(w, v[k].w, acc.w);
         }
     }
-    T* out = out0 + (r / G) * out_node + (r % G) * D + d;
+    const int x = t.row0 + r;
+    T* out = out0 + (x / G) * out_node + (x % G) * D + d;
     kv_store(out, acc.x);
     kv_store(out + 1, acc.y);
     kv_store(out + 2, acc.z);
     kv_store(out + 3, acc.w);
   }
-}
-
-template <typename T, int D>
-__device__ __forceinline__ void kv_join_row(const KvAttnParams& p, size_t tile, int chunks, int tile_rows, int r, T* out) {
-  kv_join<T, D>(chunks, [&](int c) { return kv_part(p, tile, c, tile_rows, D) + r * (D + 2); }, out);
 }
 
 }  // namespace gdn

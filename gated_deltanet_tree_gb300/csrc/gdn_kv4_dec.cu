@@ -1,6 +1,6 @@
-// Attention over the paged 4-bit cache for few rows: at most eight (node, query
-// head) pairs share a kv head -- plain decoding, and small trees of models with
-// few query heads per kv head.  bf16 calls.
+// Attention over the paged 4-bit cache for few rows: tiles of eight (node, query
+// head) pairs that share a kv head -- plain decoding, and small trees of models
+// with few query heads per kv head; and every fp32 call.
 //
 // With so few rows the cache's bytes are the bound, so the kernel is built around
 // moving and unpacking them.  A pair of warps takes a page: one bulk copy brings
@@ -20,6 +20,10 @@
 // score when the output was last rescaled, which happens only where a score passes
 // it by more than 8: weights down to 2^-30 of the largest stay above fp16's
 // smallest value and none passes its largest.
+//
+// fp32 calls run the same products on values split in two fp16 terms each: q = hi +
+// lo and the weights likewise keep 22 bits, the unpacked codes are exact as they
+// are, and a product costs two MMAs instead of one.
 #include "gdn_kv4_attn.cuh"
 #include "gdn_umma.cuh"
 
@@ -36,15 +40,16 @@ constexpr float kLift = 6.f;          // weights are scaled by 2^kLift ...
 constexpr float kSlack = 8.f;         // ... against a maximum that may lag by up to 2^kSlack: 2^14 at most in fp16
 constexpr float kLog2e = 1.4426950408889634f;
 
-template <int D>
-struct Smem {   // twice this fits the 228 KB of an SM
+template <int D, typename T>
+struct Smem {   // bf16: twice this fits the 228 KB of an SM
+  static constexpr int kTerms = sizeof(T) == 4 ? 2 : 1;            // fp16 terms of a query or a weight
   static constexpr int kWarps = kWarpsOf<D>, kPairs = kWarps / 2;
   static constexpr int kStage = KvBlock<D>::kBytes;
   static constexpr int kQ = kPairs * kStages * kStage;             // fp16 [8][D + 8]
   static constexpr int kQRow = D + 8;
-  static constexpr int kStat = kQ + kRows * kQRow * 2;             // float [kWarps][8][2], scale [8]
+  static constexpr int kStat = kQ + kTerms * kRows * kQRow * 2;    // float [kWarps][8][2], scale [8]
   static constexpr int kSee = kStat + (kWarps * kRows * 2 + kRows) * 4;
-  static constexpr int kBar = kSee + kRows * 8;    // at most as many nodes as rows; full, empty [kPairs][kStages]
+  static constexpr int kBar = kSee + kRows * 8;                    // each row's ancestors; full, empty [kPairs][kStages]
   static constexpr int kTotal = kBar + 2 * kPairs * kStages * 8 + 16;
 };
 
@@ -66,13 +71,22 @@ __device__ __forceinline__ float exp2_fast(float x) {   // results below 2^-126 
   return y;
 }
 __device__ __forceinline__ float exp2i(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }   // |e| < 127
+__device__ __forceinline__ float2 load2(const __nv_bfloat16* p) {
+  return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(p));
+}
+__device__ __forceinline__ float2 load2(const float* p) { return *reinterpret_cast<const float2*>(p); }
+__device__ __forceinline__ void store2(__nv_bfloat16* p, float x, float y) {
+  *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(x, y);
+}
+__device__ __forceinline__ void store2(float* p, float x, float y) { *reinterpret_cast<float2*>(p) = make_float2(x, y); }
 __device__ __forceinline__ uint32_t h2u(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
 __device__ __forceinline__ __half2 u2h(uint32_t u) { return *reinterpret_cast<__half2*>(&u); }
 
-template <int D>
+template <int D, typename T>
 __global__ void __launch_bounds__(32 * kWarpsOf<D>, 2) kv4_attn_dec_kernel(KvAttnParams p) {
   using Blk = KvBlock<D>;
-  using Sm = Smem<D>;
+  using Sm = Smem<D, T>;
+  constexpr int kTerms = Sm::kTerms;
   constexpr int kWarps = Sm::kWarps, kPairs = Sm::kPairs;
   extern __shared__ __align__(128) char smem_dec[];
   __shared__ int last;
@@ -105,8 +119,8 @@ __global__ void __launch_bounds__(32 * kWarpsOf<D>, 2) kv4_attn_dec_kernel(KvAtt
   unsigned long long* see = reinterpret_cast<unsigned long long*>(smem_dec + Sm::kSee);
   float* po = reinterpret_cast<float*>(smem_dec);                // the warps' outputs, over the stages
   char* stages = smem_dec + pair * kStages * Sm::kStage;
-  const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q);
-  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out);
+  const T* q = static_cast<const T*>(p.q);
+  T* out = static_cast<T*>(p.out);
   const __half2 k16 = __float2half2_rn(16.f), k24 = __float2half2_rn(-24.f);
   auto valid = [&](int g) { return g >= 0 && g < p.c.n_pages; };
   int n_joins = 0;
@@ -120,19 +134,21 @@ __global__ void __launch_bounds__(32 * kWarpsOf<D>, 2) kv4_attn_dec_kernel(KvAtt
         device_error(p.c.err, it.r.n < 1 || it.r.n > p.n_max ? GDN_DEVERR_SCHEDULE : GDN_DEVERR_CACHE, it.b);
       continue;
     }
-    const int rows = it.r.n * p.G;
+    const int row0 = it.tile * kRows, rows = min(kRows, it.r.n * p.G - row0);
     const size_t node0 = static_cast<size_t>(it.bl) * p.n_max;
-    auto q_row = [&](int r) { return q + (node0 + r / p.G) * p.q_row + static_cast<size_t>(it.h * p.G + r % p.G) * D; };
+    auto q_row = [&](int r) {
+      const int x = row0 + r;
+      return q + (node0 + x / p.G) * p.q_row + static_cast<size_t>(it.h * p.G + x % p.G) * D;
+    };
     // queries: loaded first, used below
     constexpr int kMine = (kRows + kWarps - 1) / kWarps;     // rows of a warp, loaded together
-    __nv_bfloat162 v[kMine][D / 64];
+    float2 v[kMine][D / 64];
 #pragma unroll
     for (int k = 0; k < kMine; ++k)
 #pragma unroll
       for (int i = 0; i < D / 64; ++i) {
         const int r = warp + k * kWarps;
-        v[k][i] = r < rows ? *reinterpret_cast<const __nv_bfloat162*>(q_row(r) + 64 * i + 2 * lane)
-                           : __nv_bfloat162(__float2bfloat16(0.f), __float2bfloat16(0.f));
+        v[k][i] = r < rows ? load2(q_row(r) + 64 * i + 2 * lane) : make_float2(0.f, 0.f);
       }
     // this pair's pages: page_lo + pair, + kPairs, ...; a lane holds the page numbers of 32 of them at a time
     const int mine = it.pages > pair ? (it.pages - pair + kPairs - 1) / kPairs : 0;
@@ -164,8 +180,8 @@ __global__ void __launch_bounds__(32 * kWarpsOf<D>, 2) kv4_attn_dec_kernel(KvAtt
     if (with_new && lane == 0)      // the nodes' own rows are wanted last, from nearby
       for (int t = warp; t < it.r.n; t += kWarps) {
         const size_t row = (node0 + t) * p.kv_row + static_cast<size_t>(it.h) * D;
-        prefetch_l2(static_cast<const __nv_bfloat16*>(p.k_new) + row, 2 * D);
-        prefetch_l2(static_cast<const __nv_bfloat16*>(p.v_new) + row, 2 * D);
+        prefetch_l2(static_cast<const T*>(p.k_new) + row, sizeof(T) * D);
+        prefetch_l2(static_cast<const T*>(p.v_new) + row, sizeof(T) * D);
       }
     // queries: fp16, each row scaled by a power of two that brings its largest value to [2^13, 2^14)
     {
@@ -175,30 +191,34 @@ __global__ void __launch_bounds__(32 * kWarpsOf<D>, 2) kv4_attn_dec_kernel(KvAtt
         if (r >= kRows) break;
         float big = 0.f;
 #pragma unroll
-        for (int i = 0; i < D / 64; ++i) big = fmaxf(big, fmaxf(fabsf(__low2float(v[k][i])), fabsf(__high2float(v[k][i]))));
+        for (int i = 0; i < D / 64; ++i) big = fmaxf(big, fmaxf(fabsf(v[k][i].x), fabsf(v[k][i].y)));
         for (int o = 16; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
         // 2^e <= big < 2^(e + 1); a zero or non-finite row stays as it is
         const int ex = static_cast<int>(__float_as_uint(big) >> 23);
         const int e = (big > 0.f && ex < 255) ? ex - 127 - 13 : 0;
         const float f0 = exp2i(-(e / 2)), f1 = exp2i(-(e - e / 2));
 #pragma unroll
-        for (int i = 0; i < D / 64; ++i)
-          *reinterpret_cast<__half2*>(qs + r * Sm::kQRow + 64 * i + 2 * lane) =
-              __floats2half2_rn(__low2float(v[k][i]) * f0 * f1, __high2float(v[k][i]) * f0 * f1);
+        for (int i = 0; i < D / 64; ++i) {
+          const float x = v[k][i].x * f0 * f1, y = v[k][i].y * f0 * f1;
+          const __half2 hi = __floats2half2_rn(x, y);
+          __half2* at = reinterpret_cast<__half2*>(qs + r * Sm::kQRow + 64 * i + 2 * lane);
+          at[0] = hi;
+          if (kTerms == 2) at[kRows * Sm::kQRow / 2] = __floats2half2_rn(x - __low2float(hi), y - __high2float(hi));
+        }
         if (lane == 0) st_c[r] = p.scale * kLog2e * exp2i(e / 2) * exp2i(e - e / 2);
       }
     }
-    if (with_new) {
-      if (!kv_ancestors(p, it.b, it.r.n, see) && tid == 0) device_error(p.c.err, GDN_DEVERR_SCHEDULE, it.b);
-    } else {
-      __syncthreads();
+    if (with_new && tid < rows) {
+      const int32_t* parent = p.words ? kv_parents(p, it.b) : nullptr;
+      if (!kv_root_path(parent, (row0 + tid) / p.G, &see[tid])) device_error(p.c.err, GDN_DEVERR_SCHEDULE, it.b);
     }
+    __syncthreads();
     // B fragments of Q^T: step (hh, w, u) holds channels 128 hh + 32 j + 8 w + 4 u + {0,1} and {2,3} of row m8
     constexpr int kHalves = D == 256 ? 2 : 1;
     constexpr int kWords = D == 64 ? 2 : 4;        // words of a key chunk that this lane takes
-    auto query = [&](int hh, int w, int u) {       // read where they are used: registers go to the output
+    auto query = [&](int hh, int w, int u, int term) {       // read where they are used: registers go to the output
       const int c = D == 64 ? 16 * j + 8 * w + 4 * u : 128 * hh + 32 * j + 8 * w + 4 * u;
-      return *reinterpret_cast<const uint2*>(qs + m8 * Sm::kQRow + c);
+      return *reinterpret_cast<const uint2*>(qs + (term * kRows + m8) * Sm::kQRow + c);
     };
     const float c0 = st_c[2 * j], c1 = st_c[2 * j + 1];    // of rows 2j and 2j + 1, whose scores this lane holds
 
@@ -278,13 +298,19 @@ __global__ void __launch_bounds__(32 * kWarpsOf<D>, 2) kv4_attn_dec_kernel(KvAtt
           for (int w = 0; w < kWords; ++w)
 #pragma unroll
             for (int v = 0; v < 2; ++v) {
-              const uint2 qv = query(hh, w, v);
+              const uint2 qv = query(hh, w, v, 0);
 #pragma unroll
-              for (int u = 0; u < 2; ++u)
-                mma16816(s[u], pair_of(ww[2 * u][w], 2 * v, d16[2 * u], d24[2 * u]),
-                         pair_of(ww[2 * u + 1][w], 2 * v, d16[2 * u + 1], d24[2 * u + 1]),
-                         pair_of(ww[2 * u][w], 2 * v + 1, d16[2 * u], d24[2 * u]),
-                         pair_of(ww[2 * u + 1][w], 2 * v + 1, d16[2 * u + 1], d24[2 * u + 1]), qv.x, qv.y);
+              for (int u = 0; u < 2; ++u) {
+                const uint32_t a0 = pair_of(ww[2 * u][w], 2 * v, d16[2 * u], d24[2 * u]),
+                               a1 = pair_of(ww[2 * u + 1][w], 2 * v, d16[2 * u + 1], d24[2 * u + 1]),
+                               a2 = pair_of(ww[2 * u][w], 2 * v + 1, d16[2 * u], d24[2 * u]),
+                               a3 = pair_of(ww[2 * u + 1][w], 2 * v + 1, d16[2 * u + 1], d24[2 * u + 1]);
+                mma16816(s[u], a0, a1, a2, a3, qv.x, qv.y);
+                if constexpr (kTerms == 2) {
+                  const uint2 ql = query(hh, w, v, 1);
+                  mma16816(s[u], a0, a1, a2, a3, ql.x, ql.y);
+                }
+              }
             }
         }
         // ---- weights: this lane holds rows 2j (x = 0, 2) and 2j + 1 (x = 1, 3)
@@ -328,15 +354,21 @@ __global__ void __launch_bounds__(32 * kWarpsOf<D>, 2) kv4_attn_dec_kernel(KvAtt
         }
         // a row whose scores so far are all -inf keeps weight 0 (its maximum is not subtracted)
         const float r0 = m0 == -INFINITY ? kLift : kLift - m0, r1 = m1 == -INFINITY ? kLift : kLift - m1;
-        uint32_t pf[2][2];
+        uint32_t pf[kTerms][2][2];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
 #pragma unroll
           for (int x = 0; x < 4; ++x) s[u][x] = exp2_fast(s[u][x] + ((x & 1) ? r1 : r0));
           l0 += s[u][0] + s[u][2];
           l1 += s[u][1] + s[u][3];
-          pf[u][0] = transpose8x8(h2u(__floats2half2_rn(s[u][0], s[u][1])));
-          pf[u][1] = transpose8x8(h2u(__floats2half2_rn(s[u][2], s[u][3])));
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const __half2 hi = __floats2half2_rn(s[u][2 * x], s[u][2 * x + 1]);
+            pf[0][u][x] = transpose8x8(h2u(hi));
+            if constexpr (kTerms == 2)
+              pf[1][u][x] = transpose8x8(
+                  h2u(__floats2half2_rn(s[u][2 * x] - __low2float(hi), s[u][2 * x + 1] - __high2float(hi))));
+          }
         }
         // ---- O^T: tile (gg, x) holds channel 32 gg + 4 m8 + 2x in rows 0-7 and the next one in rows 8-15; step u
         // takes tokens 8j + 4u .. + 3 of the 32
@@ -360,10 +392,12 @@ __global__ void __launch_bounds__(32 * kWarpsOf<D>, 2) kv4_attn_dec_kernel(KvAtt
             const __half2 e0 = u2h(dd[2 * u]), e1 = u2h(dd[2 * u + 1]);
             const __half2 a0 = __hmul2(e0, k16), b0 = __hmul2(e0, k24), a1 = __hmul2(e1, k16), b1 = __hmul2(e1, k24);
 #pragma unroll
-            for (int x = 0; x < 2; ++x)
-              mma16816(o[gg][x], pair_of(ww[2 * x], 2 * u, a0, b0), pair_of(ww[2 * x + 1], 2 * u, a0, b0),
-                       pair_of(ww[2 * x], 2 * u + 1, a1, b1), pair_of(ww[2 * x + 1], 2 * u + 1, a1, b1), pf[u][0],
-                       pf[u][1]);
+            for (int x = 0; x < 2; ++x) {
+              const uint32_t f0 = pair_of(ww[2 * x], 2 * u, a0, b0), f1 = pair_of(ww[2 * x + 1], 2 * u, a0, b0),
+                             f2 = pair_of(ww[2 * x], 2 * u + 1, a1, b1), f3 = pair_of(ww[2 * x + 1], 2 * u + 1, a1, b1);
+#pragma unroll
+              for (int t = 0; t < kTerms; ++t) mma16816(o[gg][x], f0, f1, f2, f3, pf[t][u][0], pf[t][u][1]);
+            }
           }
         }
       }
@@ -399,7 +433,8 @@ __global__ void __launch_bounds__(32 * kWarpsOf<D>, 2) kv4_attn_dec_kernel(KvAtt
     __syncthreads();
 
     auto out_row = [&](int r) {
-      return out + (node0 + r / p.G) * (static_cast<size_t>(p.Hq) * D) + static_cast<size_t>(it.h * p.G + r % p.G) * D;
+      const int x = row0 + r;
+      return out + (node0 + x / p.G) * (static_cast<size_t>(p.Hq) * D) + static_cast<size_t>(it.h * p.G + x % p.G) * D;
     };
     float* part = it.whole ? nullptr : kv_stream_part(p, cta, it.start > begin, kRows, D);
     for (int r = warp; r < rows; r += kWarps) {
@@ -424,13 +459,12 @@ __global__ void __launch_bounds__(32 * kWarpsOf<D>, 2) kv4_attn_dec_kernel(KvAtt
       }
       if (with_new) {
         // the row's own ancestors, one at a time in fp32: what it does not see is not read
-        const __nv_bfloat16* kn = static_cast<const __nv_bfloat16*>(p.k_new) + static_cast<size_t>(it.h) * D + 2 * lane;
-        const __nv_bfloat16* vn = static_cast<const __nv_bfloat16*>(p.v_new) + static_cast<size_t>(it.h) * D + 2 * lane;
+        const T* kn = static_cast<const T*>(p.k_new) + static_cast<size_t>(it.h) * D + 2 * lane;
+        const T* vn = static_cast<const T*>(p.v_new) + static_cast<size_t>(it.h) * D + 2 * lane;
         float2 qv[D / 64];
 #pragma unroll
-        for (int i = 0; i < D / 64; ++i)
-          qv[i] = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(q_row(r) + 64 * i + 2 * lane));
-        unsigned long long left = see[r / p.G];
+        for (int i = 0; i < D / 64; ++i) qv[i] = load2(q_row(r) + 64 * i + 2 * lane);
+        unsigned long long left = see[r];
         while (left) {
           const int t = __ffsll(static_cast<long long>(left)) - 1;
           left &= left - 1;
@@ -439,8 +473,8 @@ __global__ void __launch_bounds__(32 * kWarpsOf<D>, 2) kv4_attn_dec_kernel(KvAtt
           float2 vv[D / 64];
 #pragma unroll
           for (int i = 0; i < D / 64; ++i) {
-            const float2 kv = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(kn + at + 64 * i));
-            vv[i] = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(vn + at + 64 * i));
+            const float2 kv = load2(kn + at + 64 * i);
+            vv[i] = load2(vn + at + 64 * i);
             x = fmaf(qv[i].x, kv.x, fmaf(qv[i].y, kv.y, x));
           }
           for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
@@ -466,15 +500,14 @@ __global__ void __launch_bounds__(32 * kWarpsOf<D>, 2) kv4_attn_dec_kernel(KvAtt
         const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
         for (int i = 0; i < D / 64; ++i)
-          *reinterpret_cast<__nv_bfloat162*>(out_row(r) + 64 * i + 2 * lane) =
-              __floats2bfloat162_rn(acc[2 * i] * inv, acc[2 * i + 1] * inv);
+          store2(out_row(r) + 64 * i + 2 * lane, acc[2 * i] * inv, acc[2 * i + 1] * inv);
       }
     }
     if (part) {
       const int c0 = kv_cta_of(it.start, total, ctas), c1 = kv_cta_of(it.start + it.r.units - 1, total, ctas);
-      if (kv_last_chunk(p, it.item, c1 - c0 + 1, &last)) {     // joined after the loop: at most two
+      if (kv_last(p, it.item, c1 - c0 + 1, &last)) {     // joined after the loop: at most two
         if (tid == 0)
-          joins[n_joins] = {c0, c1 - c0 + 1, rows, it.start > kv_unit_of(c0, total, ctas), it.b, it.l, it.h};
+          joins[n_joins] = {c0, c1 - c0 + 1, rows, it.start > kv_unit_of(c0, total, ctas), it.b, it.l, it.h, row0};
         ++n_joins;
       }
     }
@@ -485,23 +518,22 @@ __global__ void __launch_bounds__(32 * kWarpsOf<D>, 2) kv4_attn_dec_kernel(KvAtt
   for (int i = 0; i < n_joins; ++i) {
     const KvJoin t = joins[i];
     const size_t node = (static_cast<size_t>(t.b) * p.layers + t.l) * p.n_max;
-    kv_join_rows<__nv_bfloat16, D>(p.part, t, kRows, out + (node * p.Hq + t.h * p.G) * D, p.G,
-                                   static_cast<long long>(p.Hq) * D, po);
+    kv_join_rows<T, D>(p.part, t, kRows, out + (node * p.Hq + t.h * p.G) * D, p.G, static_cast<long long>(p.Hq) * D, po);
     __syncthreads();
   }
 }
 
-template <int D>
+template <int D, typename T>
 cudaError_t dec_t(KvAttnParams p, cudaStream_t s) {
-  auto k = kv4_attn_dec_kernel<D>;
-  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::kTotal);
+  auto k = kv4_attn_dec_kernel<D, T>;
+  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D, T>::kTotal);
   if (e != cudaSuccess) return e;
-  p.each = p.ctas / (p.layers * p.Hkv);
   // as many requests a launch as have counters
-  const int per = kKvCounters / (p.layers * p.Hkv);
+  const int items = p.layers * p.Hkv * p.row_tiles, per = kKvCounters / items;
+  p.each = p.ctas / items;
   for (p.b0 = 0; p.b0 < p.c.B; p.b0 += per) {
     p.bn = p.c.B - p.b0 < per ? p.c.B - p.b0 : per;
-    k<<<p.ctas, 32 * kWarpsOf<D>, Smem<D>::kTotal, s>>>(p);
+    k<<<p.ctas, 32 * kWarpsOf<D>, Smem<D, T>::kTotal, s>>>(p);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
@@ -511,7 +543,11 @@ cudaError_t dec_t(KvAttnParams p, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_kv4_attention_dec(const KvAttnParams& p, cudaStream_t s) {
-  return p.D == 256 ? dec_t<256>(p, s) : p.D == 128 ? dec_t<128>(p, s) : dec_t<64>(p, s);
+  if (p.dtype == GDN_DTYPE_F32)
+    return p.D == 256 ? dec_t<256, float>(p, s) : p.D == 128 ? dec_t<128, float>(p, s) : dec_t<64, float>(p, s);
+  return p.D == 256   ? dec_t<256, __nv_bfloat16>(p, s)
+         : p.D == 128 ? dec_t<128, __nv_bfloat16>(p, s)
+                      : dec_t<64, __nv_bfloat16>(p, s);
 }
 
 }  // namespace gdn

@@ -596,17 +596,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tree_kernel(KvAttnParams
           if (keys && uw == 0 && lane == 0) odd[(news + 1) & 1] = 0;      // the next one's, which nobody uses now
           bool strange = false;
           if (keys) {
-            const int32_t* parent = p.words ? p.words + static_cast<size_t>(it.b) * SchedLayout{p.n_max}.words() + SchedLayout{p.n_max}.parent() : nullptr;
+            const int32_t* parent = p.words ? kv_parents(p, it.b) : nullptr;
             const int ut = 32 * uw + lane;
             if (ut < it.r.n) {
-              unsigned long long mask = 1ull << ut;
-              int a = parent ? parent[ut] : -1, prev = ut;
-              while (a >= 0 && a < prev) {
-                mask |= 1ull << a;
-                prev = a;
-                a = parent[a];
-              }
-              if (a >= 0) device_error(p.c.err, GDN_DEVERR_SCHEDULE, it.b);
+              unsigned long long mask;
+              if (!kv_root_path(parent, ut, &mask)) device_error(p.c.err, GDN_DEVERR_SCHEDULE, it.b);
               see[ut] = mask;
             }
           }

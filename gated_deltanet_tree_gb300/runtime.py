@@ -257,9 +257,7 @@ class KV4Cache:
     def _workspace(self, n_max: int, max_len: int):
         need = self.ws_bytes.get((n_max, max_len))
         if need is None:
-            most = max_len if max_len else self.pages_max * N.GDN_KV4_PAGE
-            need = N.gdn_kv4_workspace_bytes(self.dims, self.B, self.layers, n_max,
-                                             min(most, self.pages_max * N.GDN_KV4_PAGE))
+            need = N.gdn_kv4_workspace_bytes(self.dims, self.B, self.layers, n_max, max_len)
             self.ws_bytes[(n_max, max_len)] = need
         if self.workspace is None or self.workspace.numel() < need:
             self.workspace = torch.zeros(max(need, 256), dtype=torch.uint8, device=self.device)

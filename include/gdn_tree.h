@@ -460,12 +460,15 @@ gdn_status gdn_kv4_read(const gdn_attn_dims* d, int32_t layers, int32_t n_rows, 
  *   out    [B][layers][n_max][Hq][D]  dtype, contiguous; rows of nodes >= n[b]
  *          are neither read nor written
  *   max_len  upper bound of the requests' lengths known to the host, 0: unknown.
- *          It only sizes the split of the work: a longer request is still correct.
+ *          It only limits how much of the GPU the call takes: a longer request is still
+ *          correct.
  *   workspace  >= gdn_kv4_workspace_bytes(...) bytes of device memory, zeroed by
  *          the caller before its first use (its counters are zero after each call)
- * bf16 products run on the tensor cores in fp16 with fp32 accumulation: codes
- * times scales are exact in fp16, q is scaled per row to fp16's range (a power of
- * two) and the weights are rounded to fp16.  fp32 calls stay in fp32 throughout.
+ * The products run on the tensor cores in fp16 with fp32 accumulation: codes times
+ * scales are exact in fp16, and q is scaled per row to fp16's range by a power of
+ * two.  bf16 calls round the weights to fp16 (to 11 bits, or to 2^-26 of a row's
+ * largest); fp32 calls split q and the weights in two fp16 terms each (22 bits).
+ * GDN_ERR_UNSUPPORTED: layers * Hkv * ceil(n_max * Hq / Hkv / 8) above 16384.
  * ------------------------------------------------------------------------- */
 size_t gdn_kv4_workspace_bytes(const gdn_attn_dims* d, int32_t B, int32_t layers, int32_t n_max, int32_t max_len);
 gdn_status gdn_kv4_attention(const gdn_attn_dims* d, int32_t layers, const gdn_batch_schedule* sched, const void* q,

@@ -114,3 +114,9 @@ def test_accept_refusals(N):
 
 def test_error_words_pointer(N):
     assert status(N, N.gdn_check_error_words, None, 0) == -1
+
+
+def test_attention_with_too_many_items(N):
+    d, c = dims(N, Hq=1024, Hkv=512, dtype=N.GDN_DTYPE_F32), cache(N, layers=5)
+    assert N.gdn_kv4_workspace_bytes(d, 2, 5, 64, 100) == 0
+    assert status(N, calls(N, d, c, layers=5, s=sched(N, n_max=64))["attention"]) == -4

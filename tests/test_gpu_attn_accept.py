@@ -571,3 +571,25 @@ def test_attention_small_trees(Hq, Hkv, D, n):
     run_case(rng, Hq, Hkv, D, [40, 64, 2300], [np.array([-1] + [0] * (n - 1))] * 3, "bf16", layers=2,
              poison=[(0, n - 1), (2, 1)])
     run_case(rng, Hq, Hkv, D, [0, 600], [S.chain_tree(n)] * 2, "bf16", new=False)
+
+
+def test_attention_many_heads_and_layers():
+    """More items a request than the 128-row kernel has records for: tiles of eight rows take the call."""
+    rng = np.random.default_rng(30)
+    B, layers, Hq, Hkv, D, n = 1, 70, 256, 64, 64, 6
+    c = make_cache(Hq, Hkv, D, B, layers, 2, "bf16")
+    k = rows(rng, B, layers, 70, Hkv, D, dtype="bf16")
+    c.append(k, k, i32([70]))
+    kr, vr = c.read(None, 70)
+    tree = S.random_tree(n, rng)
+    from gated_deltanet_tree_gb300.runtime import DeviceSchedule
+    q, kn = rows(rng, B, layers, n, Hq, D, dtype="bf16"), rows(rng, B, layers, n, Hkv, D, dtype="bf16")
+    out = torch.zeros_like(q)
+    c.attention(q, kn, kn, out, sched=DeviceSchedule([tree], n, "cuda"), max_len=70)
+    c.check_error()
+    vmax = max(float(kn.abs().max()), float(vr.abs().max()))
+    for l, h in ((0, 0), (31, 40), (69, 63)):
+        G = Hq // Hkv
+        ref = K.tree_attention(f64(q[0, l, :, h * G:(h + 1) * G]), f64(kr[0, l, :, h:h + 1]), f64(vr[0, l, :, h:h + 1]),
+                               f64(kn[0, l, :, h:h + 1]), f64(kn[0, l, :, h:h + 1]), tree, c.dims.scale)
+        check(f64(out[0, l, :, h * G:(h + 1) * G]), ref, vmax, "bf16", (l, h))
