@@ -593,3 +593,19 @@ def test_attention_many_heads_and_layers():
         ref = K.tree_attention(f64(q[0, l, :, h * G:(h + 1) * G]), f64(kr[0, l, :, h:h + 1]), f64(vr[0, l, :, h:h + 1]),
                                f64(kn[0, l, :, h:h + 1]), f64(kn[0, l, :, h:h + 1]), tree, c.dims.scale)
         check(f64(out[0, l, :, h * G:(h + 1) * G]), ref, vmax, "bf16", (l, h))
+
+
+def test_example_runs_the_operators_together():
+    """The example's steps, and its last step's attention and acceptance against the oracles."""
+    import os
+    import sys
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+    import hybrid_step
+    lines = []
+    model = hybrid_step.main(steps=3, show=lines.append)
+    assert len(lines) == 4 and torch.isfinite(model.state).all()
+    for b in range(model.B):
+        L = int(model.acceptor.len[b])
+        path = model.acceptor.path[b]
+        assert 1 <= L <= model.n_max and int(path[0]) == 0 and (path[L:] == -1).all()
+        assert 0 <= int(model.acceptor.next[b]) < model.V
