@@ -9,10 +9,14 @@
 //    bytes of all rows, read once;
 //  - along the walk: a request's cluster reads the rows on its path, one after
 //    another.  Few bytes, but every step waits for a row's latency and a cluster
-//    barrier (about 3 us).
-// The first is taken while all rows are few (kRowsAtOnceBytes): a call of 22 rows
-// of 131072 bf16 entries takes 12 us against 29 us along the walk; with 64 nodes and
-// 128 requests (2.1 GB) the walk's 50 MB win.
+//    barrier.
+// The first is taken while all rows are few (kRowsAtOnceBytes).  Measured, at once
+// against along the walk: 64 chains of 9 rows of 65537 fp32 entries (counted as
+// 75 MB) 61 us against 69; 32 trees of 22 rows of 131072 bf16 entries (184 MB) 60 us
+// against 39; one such tree whose path is one node about 15 us either way, most of
+// it launches.  The walk of the 32 trees reads 44 MB in 39 us (1.1 TB/s): its bound is
+// the latency of the steps, not the bytes.  The rows' reduction reads its 151 MB at
+// 4.5 TB/s.
 //
 // One thread-block cluster walks one request.  Its CTAs share each row they read by
 // slices and exchange their partial results through distributed shared memory;

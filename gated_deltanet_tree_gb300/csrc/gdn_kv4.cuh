@@ -92,7 +92,8 @@ struct KvAttnParams {
   int each;                    // CTAs an item of a lone request can have: ctas / (layers * Hkv * row_tiles)
   int row_tiles;               // row tiles of a (request, layer, kv head), at most
   float* part;                 // partial results, rows of D + 2: unnormalised output, maximum (base 2), sum
-  int4* desc;                  // [kKvItems] what the join of an item reads (tree kernel)
+  int4* desc;                  // [kKvItems] what the join reads (tree kernel), by item or by CTA
+  int by_item;
   int32_t* done;               // [kKvCounters] CTAs that have finished an item, zero between calls
 };
 struct KvAttnPlan {

