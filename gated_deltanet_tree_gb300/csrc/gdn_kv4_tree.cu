@@ -52,16 +52,17 @@ enum Bar { kStFull = 0, kStEmpty = 3, kKFull = 6, kVFull = 8, kScored = 10, kPFu
 
 template <int D>
 struct Smem {
-  static constexpr int kStage = KvBlock<D>::kBytes;
+  static constexpr int kPages = D == 256 ? 1 : 2, kTok = kPages * kPage;      // pages and tokens of a step
+  static constexpr int kBlock = KvBlock<D>::kBytes, kStage = kPages * kBlock;
   // operands without swizzle: 8 rows x 16 bytes contiguous; adjacent row groups 128 bytes apart, adjacent groups of
   // eight elements along K `kKeyK` / `kValK` bytes (the values' 16 bytes more spread the unpackers' stores over all banks)
-  static constexpr int kKeyK = kPage * 16, kValK = D * 16 + 16;
-  static constexpr int kKeyTile = (D / 8) * kKeyK, kValTile = (kPage / 8) * kValK;
+  static constexpr int kKeyK = kTok * 16, kValK = D * 16 + 16;
+  static constexpr int kKeyTile = (D / 8) * kKeyK, kValTile = (kTok / 8) * kValK;
   static constexpr int kKeys = kStages * kStage;
   static constexpr int kVals = kKeys + 2 * kKeyTile;
   static constexpr int kSee = kVals + 2 * kValTile;                // u64 [64]
-  static constexpr int kColScale = kSee + GDN_MAX_NODES * 8;       // float [64]
-  static constexpr int kBar = kColScale + GDN_MAX_NODES * 4;
+  static constexpr int kColScale = kSee + GDN_MAX_NODES * 8;       // float [kTok]
+  static constexpr int kBar = kColScale + kTok * 4;
   static constexpr int kTmem = kBar + kBars * 8;                   // tensor-memory address, flags
   static constexpr int kSwap = kTmem + 32;                         // float [2][2][128]: what the two threads of a row tell each other
   static constexpr int kRef = kSwap + 4 * kRows * 4;               // float [128]: each row's reference maximum
@@ -69,7 +70,8 @@ struct Smem {
   static constexpr int kTotal = kRawVal + GDN_MAX_NODES * D * 2;
   // tensor-memory columns
   static constexpr int kO = 0, kQ = D, kS = D + D / 2;
-  static constexpr int kCols = D == 256 ? 512 : D == 128 ? 512 : 256;
+  static constexpr int kCols = 512;
+  static_assert(kS + 2 * kTok <= kCols, "output, queries and two score buffers");
 };
 
 __host__ __device__ constexpr uint32_t idesc_f16(int m, int n) {
@@ -160,6 +162,7 @@ template <int D>
 __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tree_kernel(KvAttnParams p) {
   using Blk = KvBlock<D>;
   using Sm = Smem<D>;
+  constexpr int kTok = Sm::kTok;
   extern __shared__ __align__(1024) char sm[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const bool aborted = launch_aborted(p.c.err);
@@ -243,7 +246,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tree_kernel(KvAttnParams
       continue;
     }
     const bool with_new = it.first && p.k_new;
-    const int steps = it.pages + (with_new ? 1 : 0);      // the new rows last: a page sets better first references
+    const int psteps = (it.pages + Sm::kPages - 1) / Sm::kPages;
+    const int steps = psteps + (with_new ? 1 : 0);        // the new rows last: a page sets better first references
+    const int seg_toks = min(it.r.len - it.page_lo * kPage, it.pages * kPage);
     const int row0 = it.tile * kRows, rows = min(kRows, it.r.n * p.G - row0);
     const size_t node0 = static_cast<size_t>(it.bl) * p.n_max;
 
@@ -338,31 +343,28 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tree_kernel(KvAttnParams
         const int k = step + i, buf = k & 1;
         if (buf != half) continue;
         alive = wait_all(kScored + buf, k >> 1);
-        if (alive && i == it.pages) alive = wait_all(kNewFull, news);
+        if (alive && i == psteps) alive = wait_all(kNewFull, news);
         if (!alive) break;
         tmem_fence_after();
         if (busy) {
-          const uint32_t ts = lanes + Sm::kS + 64 * buf;
-          const bool is_new = i == it.pages;
-          unsigned long long vis = ~0ull;
-          if (is_new) {
-            vis = odd[news & 1] ? 0ull : see[node];
-          } else {
-            const int toks = it.r.len - (it.page_lo + i) * kPage;
-            if (toks < kPage) vis = (1ull << toks) - 1;
-          }
-          if (is_new || vis != ~0ull) {
+          const uint32_t ts = lanes + Sm::kS + kTok * buf;
+          const bool is_new = i == psteps;
+          const int toks = seg_toks - i * kTok;               // tokens of this step
+          if (is_new || toks < kTok) {
             // scale and mask in place, apart from the common path (whose code is better small: the roles of an SM share
             // its instruction caches)
 #pragma unroll 1
-            for (int x = 0; x < 64; x += 16) {
+            for (int x = 0; x < kTok; x += 16) {
               float t[16];
               tmem_ld16(ts + x, t);
               tmem_wait_ld();
+              // which of the 16 columns the row sees
+              uint32_t vis = toks - x >= 16 ? 0xFFFFu : toks > x ? (1u << (toks - x)) - 1 : 0u;
+              if (is_new) vis = odd[news & 1] || x >= GDN_MAX_NODES ? 0u : static_cast<uint32_t>(see[node] >> x);
 #pragma unroll
               for (int y = 0; y < 16; ++y) {
                 if (is_new) t[y] *= colscale[x + y];
-                if (!((vis >> (x + y)) & 1)) t[y] = -INFINITY;
+                if (!((vis >> y) & 1)) t[y] = -INFINITY;
               }
               tmem_st16(ts + x, t);
             }
@@ -370,7 +372,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tree_kernel(KvAttnParams
           }
           float top = -INFINITY;
 #pragma unroll 1
-          for (int h = 0; h < 64; h += 32) {
+          for (int h = 0; h < kTok; h += 32) {
             float x[32];
             tmem_ld32(ts + h, x);
             tmem_wait_ld();
@@ -416,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tree_kernel(KvAttnParams
           const u64 c2 = pack2(c, c), b2 = pack2(base, base);
           u64 sum[2] = {0, 0};
 #pragma unroll 1
-          for (int h = 0; h < 64; h += 32) {
+          for (int h = 0; h < kTok; h += 32) {
             float x[32], w[16];
             tmem_ld32(ts + h, x);
             tmem_wait_ld();
@@ -588,13 +590,21 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tree_kernel(KvAttnParams
       const bool keys = (warp & 2) == 0;
       const int uw = (warp & 1) + 2 * ((warp - kSoftWarps) >> 2);
       // 32 x 16-byte units of a page's keys, and of its values; a warp takes units uw, uw + 4, ...
-      constexpr int kUnits = D / 16, kShare = kUnits / kKeyWarps, kValWarps = kUnpackWarps - kKeyWarps;
+      constexpr int kUnits = Sm::kPages * D / 16, kShare = kUnits / kKeyWarps, kValWarps = kUnpackWarps - kKeyWarps;
       static_assert(kKeyWarps == 4 && kUnpackWarps == 8, "units are dealt to four warps");
+      constexpr bool kTwo = Sm::kPages == 2;
       const __half2 k16 = __float2half2_rn(16.f), k24 = __float2half2_rn(-24.f);
-      // keys: unit uw + 4 y is chunk uw / 2 + 2 y of token 32 (uw & 1) + lane
-      const int kt_tok = 32 * (uw & 1) + lane, kt_turn = Blk::turn(kt_tok);
-      // values: unit uw + 4 y holds units (of 16 bytes) 32 uw + lane + 128 y; the first one's octet and channel quad
-      const int vt_unit = 32 * uw + lane, vt_oct = (vt_unit / D) * 4 + (vt_unit & 3), vt_quad = (vt_unit % D) >> 2;
+      // keys: one page: unit uw + 4 y is chunk uw / 2 + 2 y of token 32 (uw & 1) + lane; two pages: a warp takes all
+      // chunks of tokens 32 uw + lane
+      constexpr int kChunkStep = kTwo ? 1 : 2;
+      const int kt_tok = 32 * (uw & 1) + lane, kt_turn = Blk::turn(kt_tok), kt_at = kTwo ? 32 * uw + lane : kt_tok;
+      const int kt_ch = kTwo ? 0 : uw >> 1;
+      // values: one page: unit uw + 4 y holds units (of 16 bytes) 32 uw + lane + 128 y; two pages: two warps a page,
+      // 64 units apart.  The first one's octet and channel quad
+      constexpr int kUnitStep = kTwo ? 64 : 128, kPerHalf = D / kUnitStep;      // steps a half (32 tokens) of a page
+      const int vt_page = kTwo ? uw >> 1 : 0, vt_unit = 32 * (kTwo ? uw & 1 : uw) + lane;
+      const int vt_oct = (vt_unit / D) * 4 + (vt_unit & 3), vt_quad = (vt_unit % D) >> 2;
+      const int block = kTwo ? (uw >> 1) * Sm::kBlock : 0;                     // the warp's page in a stage
       // the operands' space, the ancestor masks and the scales belong to the item before until its output is released
       // (the values' also to this one's queries, on their way to tensor memory)
       if (steps > 0) alive = wait_all(kOFree, segs + 1);
@@ -614,7 +624,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tree_kernel(KvAttnParams
         char* kt = sm + Sm::kKeys + buf * Sm::kKeyTile;
         char* vt = sm + Sm::kVals + buf * Sm::kValTile;
         const int free_bar = keys ? kScored + buf : kAdded + buf, full_bar = keys ? kKFull + buf : kVFull + buf;
-        if (i == it.pages) {
+        if (i == psteps) {
           // the nodes' own rows, straight from global memory; the keys pass through the space of the other operand
           // buffer, so the step before has to be done with it
           alive = wait_all(free_bar, (k >> 1) + 1);
@@ -678,7 +688,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tree_kernel(KvAttnParams
           } else {
             // eight tokens of a channel a thread
 #pragma unroll 1
-            for (int x = 32 * uw + lane; x < 8 * D; x += 32 * kValWarps) {
+            for (int x = 32 * uw + lane; x < (kTok / 8) * D; x += 32 * kValWarps) {
               const int ch = x % D, o = x / D;
               uint32_t w[4] = {0, 0, 0, 0};
               if (8 * o < it.r.n) {
@@ -714,25 +724,25 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tree_kernel(KvAttnParams
         const int pg = pages + i, st = pg % kStages;
         alive = wait_all(kStFull + st, pg / kStages);
         if (!alive) break;
-        const char* blk = sm + st * Sm::kStage;
-        const int toks = it.r.len - (it.page_lo + i) * kPage;     // tokens past the length read as zeros
+        const char* blk = sm + st * Sm::kStage + block;
+        const int toks = seg_toks - i * kTok;                     // tokens past them read as zeros
         // rolled loops: the roles of an SM share its instruction caches, and unrolled they do not fit
         if (keys) {                    // a unit: a chunk of 32 channels of a token a lane
           const char* from = blk + kt_tok * (D / 2);
-          const __half* scale = reinterpret_cast<const __half*>(blk + Blk::kKeyScales) + kt_tok * Blk::kGroups + (uw >> 1);
-          char* dst = kt + 4 * (uw >> 1) * Sm::kKeyK + (kt_tok >> 3) * 128 + (kt_tok & 7) * 16;
-          int ch = uw >> 1;
+          const __half* scale = reinterpret_cast<const __half*>(blk + Blk::kKeyScales) + kt_tok * Blk::kGroups + kt_ch;
+          char* dst = kt + 4 * kt_ch * Sm::kKeyK + (kt_at >> 3) * 128 + (kt_at & 7) * 16;
+          int ch = kt_ch;
           uint4 cw = *reinterpret_cast<const uint4*>(from + ((ch ^ kt_turn) << 4));
           __half d = *scale;
           alive = wait_all(free_bar, (k >> 1) + 1);
           if (!alive) break;
 #pragma unroll 1
           for (int y = 0; y < kShare; ++y) {
-            if (kt_tok >= toks) d = __ushort_as_half(0);            // scales past the length are whatever the page held
+            if (kt_at >= toks) d = __ushort_as_half(0);            // scales past the length are whatever the page held
             const __half2 d2 = __half2half2(d), a = __hmul2(d2, k16), b = __hmul2(d2, k24);
             const uint32_t w[4] = {cw.x, cw.y, cw.z, cw.w};
-            ch += 2;
-            scale += 2;
+            ch += kChunkStep;
+            scale += kChunkStep;
             if (y + 1 < kShare) {
               cw = *reinterpret_cast<const uint4*>(from + ((ch ^ kt_turn) << 4));
               d = *scale;
@@ -741,13 +751,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tree_kernel(KvAttnParams
             for (int z = 0; z < 4; ++z)
               *reinterpret_cast<uint4*>(dst + z * Sm::kKeyK) =
                   make_uint4(pair_of(w[z], 0, a, b), pair_of(w[z], 1, a, b), pair_of(w[z], 2, a, b), pair_of(w[z], 3, a, b));
-            dst += 8 * Sm::kKeyK;
+            dst += 4 * kChunkStep * Sm::kKeyK;
           }
         } else {                       // a unit: four channels, eight tokens a lane
           const char* from = blk + Blk::kValCodes + 16 * vt_unit;
           const char* scale = blk + Blk::kValScales + (vt_quad >> 3) * (2 * kPage) + 16 * vt_oct;
-          char* dst = vt + vt_oct * Sm::kValK + (vt_quad >> 1) * 128 + (vt_quad & 1) * 64;
-          int left = toks - 8 * vt_oct;                             // tokens of the octet inside the length
+          char* dst = vt + (8 * vt_page + vt_oct) * Sm::kValK + (vt_quad >> 1) * 128 + (vt_quad & 1) * 64;
+          int left = toks - kPage * vt_page - 8 * vt_oct;                             // tokens of the octet inside the length
           uint4 cw = *reinterpret_cast<const uint4*>(from), sd = *reinterpret_cast<const uint4*>(scale);
           alive = wait_all(free_bar, (k >> 1) + 1);
           if (!alive) break;
@@ -767,14 +777,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tree_kernel(KvAttnParams
               b[z] = __hmul2(u2h(dd[z]), k24);
             }
             char* to = dst;
-            // the next unit is 128 units on: 128 channels further (D = 256, odd steps), or the next 32 tokens
-            from += 128 * 16;
-            if (D == 256 && (y & 1) == 0) {
-              scale += 4 * (2 * kPage);
-              dst += 16 * 128;
+            // the next unit: as many channels further (where a half page takes two steps, the odd ones), or the next
+            // 32 tokens
+            constexpr int kScaleStep = (kUnitStep / 32) * (2 * kPage), kChanStep = (kUnitStep / 8) * 128;
+            from += kUnitStep * 16;
+            if (kPerHalf == 2 && (y & 1) == 0) {
+              scale += kScaleStep;
+              dst += kChanStep;
             } else {
-              scale += 64 - (D == 256 ? 4 * (2 * kPage) : 0);
-              dst += 4 * Sm::kValK - (D == 256 ? 16 * 128 : 0);
+              scale += 64 - (kPerHalf == 2 ? kScaleStep : 0);
+              dst += 4 * Sm::kValK - (kPerHalf == 2 ? kChanStep : 0);
               left -= 32;
             }
             if (y + 1 < kShare) {
@@ -799,19 +811,33 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tree_kernel(KvAttnParams
       const int32_t* table = p.c.page_table + static_cast<size_t>(it.b) * p.c.pages_max + it.page_lo;
       for (int base = 0; base < it.pages && alive; base += 32) {
         const int mine = base + lane < it.pages ? table[base + lane] : -1;
-        for (int i = base; i < min(it.pages, base + 32) && alive; ++i) {
-          const int g = __shfl_sync(0xffffffffu, mine, i - base);
-          const int pg = pages + i, st = pg % kStages;
+        for (int i = base; i < min(it.pages, base + 32) && alive; i += Sm::kPages) {
+          const int pg = pages + i / Sm::kPages, st = pg % kStages;
+          int g[Sm::kPages];
+#pragma unroll
+          for (int x = 0; x < Sm::kPages; ++x) g[x] = __shfl_sync(0xffffffffu, mine, (i - base + x) & 31);
           if (lane == 0) {
             alive = wait(kStEmpty + st, pg / kStages + 1);
             if (alive) {
-              if (g >= 0 && g < p.c.n_pages) {
-                mbar_expect(&bar[kStFull + st], Sm::kStage);
-                bulk_g2s(sm + st * Sm::kStage, kv_block<D>(p.c, p.Hkv, g, it.l, it.h), Sm::kStage, &bar[kStFull + st]);
-              } else {       // whatever the stage holds is unpacked in its place; the request is reported
-                device_error(p.c.err, GDN_DEVERR_CACHE, it.b);
-                mbar_arrive(&bar[kStFull + st]);
+              int good = 0;
+#pragma unroll
+              for (int x = 0; x < Sm::kPages; ++x) {
+                // whatever the stage holds is unpacked in a bad page's place; the request is reported.  A page past the
+                // segment's last reads as zeros
+                const bool in = i + x < it.pages, ok = in && g[x] >= 0 && g[x] < p.c.n_pages;
+                if (in && !ok) device_error(p.c.err, GDN_DEVERR_CACHE, it.b);
+                if (!ok) g[x] = -1;
+                good += ok;
               }
+              if (good)
+                mbar_expect(&bar[kStFull + st], good * Sm::kBlock);
+              else
+                mbar_arrive(&bar[kStFull + st]);
+#pragma unroll
+              for (int x = 0; x < Sm::kPages; ++x)
+                if (g[x] >= 0)
+                  bulk_g2s(sm + st * Sm::kStage + x * Sm::kBlock, kv_block<D>(p.c, p.Hkv, g[x], it.l, it.h), Sm::kBlock,
+                           &bar[kStFull + st]);
             }
           }
           alive = __shfl_sync(0xffffffffu, alive, 0);
@@ -834,13 +860,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tree_kernel(KvAttnParams
           if (!alive) break;
           tmem_fence_after();
           const uint64_t b0 = umma_desc(smem_addr(sm + Sm::kKeys + buf * Sm::kKeyTile), Sm::kKeyK, 128);
-          const uint32_t d = tmem + Sm::kS + 64 * buf;
+          const uint32_t d = tmem + Sm::kS + kTok * buf;
           if (leader) {
-            umma_f16_ts<false>(d, tmem + Sm::kQ, b0, idesc_f16(128, kPage));
+            umma_f16_ts<false>(d, tmem + Sm::kQ, b0, idesc_f16(128, kTok));
 #pragma unroll
             for (int x = 1; x < D / 16; ++x)
               umma_f16_ts<true>(d, tmem + Sm::kQ + 8 * x, b0 + static_cast<uint64_t>(x) * (2 * Sm::kKeyK / 16),
-                                idesc_f16(128, kPage));
+                                idesc_f16(128, kTok));
             umma_commit(&bar[kScored + buf]);
           }
           __syncwarp();
@@ -852,14 +878,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tree_kernel(KvAttnParams
           if (!alive) break;
           tmem_fence_after();
           const uint64_t b0 = umma_desc(smem_addr(sm + Sm::kVals + buf * Sm::kValTile), Sm::kValK, 128);
-          const uint32_t a0 = tmem + Sm::kS + 64 * buf;      // weights of 16 tokens in columns 0, 8, 32 and 40
+          const uint32_t a0 = tmem + Sm::kS + kTok * buf;    // weights of 16 tokens in columns 0, 8, 32, 40, ...
           if (leader) {
             if (i == 1)
               umma_f16_ts<false>(tmem + Sm::kO, a0, b0, idesc_f16(128, D));
             else
               umma_f16_ts<true>(tmem + Sm::kO, a0, b0, idesc_f16(128, D));
 #pragma unroll
-            for (int x = 1; x < kPage / 16; ++x)
+            for (int x = 1; x < kTok / 16; ++x)
               umma_f16_ts<true>(tmem + Sm::kO, a0 + 16 * x - 8 * (x & 1), b0 + static_cast<uint64_t>(x) * (2 * Sm::kValK / 16),
                                 idesc_f16(128, D));
             umma_commit(&bar[kAdded + buf]);
@@ -877,7 +903,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tree_kernel(KvAttnParams
       }
     }
     step += steps;
-    pages += it.pages;
+    pages += psteps;
     segs += steps > 0 ? 1 : 0;
     news += with_new ? 1 : 0;
     alive = __shfl_sync(0xffffffffu, alive, 0);
