@@ -51,20 +51,13 @@ __device__ __forceinline__ void unpack(const Raw8<__nv_bfloat16>& r, float (&x)[
   }
 }
 
-// Quantises a group held by four adjacent lanes (eight channels each): codes 0..15 of this lane's channels
-// and the group's scale.  All 32 lanes of the warp call it.
-//
-// code = rint(x / d) + 8.  Of bf16 elements x and d have eight significant bits, so x / d is a tie or at least 2^-11
-// away from one: a product with 1 / d, corrected once by its remainder (which makes ties exact), rounds alike at a
-// third of the division's instructions.  fp32 elements are divided.
-template <bool kDivide>
-__device__ __forceinline__ __half quantise8(const float (&x)[8], uint32_t (&code)[8]) {
+// The element of largest magnitude of a group held by four adjacent lanes (eight channels each), the lowest channel's on
+// ties.  All 32 lanes of the warp call it.
+__device__ __forceinline__ float largest_of(const float (&x)[8]) {
   float big = 0.f, m = 0.f;
-  bool bad = false;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const float a = fabsf(x[i]);
-    bad |= !(a <= 3.402823466e38f);
     if (a > big) { big = a; m = x[i]; }        // the first of equals stays
   }
 #pragma unroll
@@ -73,26 +66,94 @@ __device__ __forceinline__ __half quantise8(const float (&x)[8], uint32_t (&code
     const bool other_first = (threadIdx.x & o) != 0;   // the partner holds the lower channels
     if (ob > big || (ob == big && other_first)) { big = ob; m = om; }
   }
+  return m;
+}
+// The group's scale from that element; 0 where it is left out (d: what elements are divided by).
+__device__ __forceinline__ __half scale_of(float m, float* d) {
+  const float x = fminf(fmaxf(__bfloat162float(__float2bfloat16_rn(m * -0.125f)), -kScaleMax), kScaleMax);
+  const __half h = __float2half_rn(x);
+  *d = __half2float(h);
+  return h;
+}
+
+// Quantises a group: codes 0..15 of this lane's channels 2i and 2i + 1 in the halves of code[i], and the group's scale.
+// code = rint(x / d) + 8, clamped.
+__device__ __forceinline__ __half quantise8(const Raw8<float>& r, uint32_t (&code)[4]) {
+  float x[8], d;
+  unpack(r, x);
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) bad |= !(fabsf(x[i]) <= 3.402823466e38f);
+  const float m = largest_of(x);
   const unsigned quad = 0xFu << (threadIdx.x & 28);
   bad = (__ballot_sync(0xffffffffu, bad) & quad) != 0;
-  float d = __bfloat162float(__float2bfloat16_rn(m * -0.125f));
-  d = fminf(fmaxf(d, -kScaleMax), kScaleMax);
-  const __half h = __float2half_rn(d);
-  d = __half2float(h);
+  const __half h = scale_of(m, &d);
   const bool none = bad || d == 0.f;
-  const float inv = none ? 0.f : __frcp_rn(d);
+  uint32_t c[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    float q;
-    if (kDivide) {
-      q = none ? 0.f : __fdiv_rn(x[i], d);
-    } else {
-      q = x[i] * inv;
-      q = fmaf(fmaf(-q, d, x[i]), inv, q);
-    }
+    const float q = none ? 0.f : __fdiv_rn(x[i], d);
     // adding 1.5 2^23 rounds to an integer, ties to even, in the low bits; 8 more makes it the code
-    code[i] = __float_as_uint(fminf(fmaxf(q, -8.f), 7.f) + 12582920.f) & 15u;
+    c[i] = __float_as_uint(fminf(fmaxf(q, -8.f), 7.f) + 12582920.f) & 15u;
   }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) code[i] = c[2 * i] | c[2 * i + 1] << 16;
+  return bad ? __ushort_as_half(0x7FFF) : h;
+}
+
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t min_u16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("min.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t max_s16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.s16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+// The same of bf16 elements, on as few integer instructions as the format allows: they are what bounds the kernel.
+//
+// The largest magnitude: a bf16 number's bits are its magnitude's order, so two packed maxima of the words as they lie,
+// one signed (the largest positive element) and one unsigned (the most negative one, if any), find it and its sign;
+// only where both magnitudes are equal does the order of the channels decide.  Infinities and NaN are the largest.
+//
+// x and d have eight significant bits, so x / d is a tie or at least 2^-11 away from one: a product with 1 / d, corrected
+// once by its remainder (which makes ties exact), rounds like the quotient, and so does that number over 16 plus 1/2,
+// saturated to [0, 1]: 24 bits hold a tie exactly, and move the others by 2^-21 of a code at most.
+__device__ __forceinline__ __half quantise8(const Raw8<__nv_bfloat16>& r, uint32_t (&code)[4]) {
+  float x[8], d;
+  unpack(r, x);
+  uint32_t pos = max_s16x2(max_s16x2(r.u.x, r.u.y), max_s16x2(r.u.z, r.u.w));
+  uint32_t neg = max_u16x2(max_u16x2(r.u.x, r.u.y), max_u16x2(r.u.z, r.u.w));
+#pragma unroll
+  for (int o = 1; o < 4; o <<= 1) {
+    pos = max_s16x2(pos, __shfl_xor_sync(0xffffffffu, pos, o));
+    neg = max_u16x2(neg, __shfl_xor_sync(0xffffffffu, neg, o));
+  }
+  pos = max_s16x2(pos, pos >> 16);
+  neg = max_u16x2(neg, neg >> 16);
+  const int p = static_cast<int16_t>(pos & 0xFFFFu), n = static_cast<int>(neg & 0xFFFFu) - 0x8000;   // < 0: none
+  const int big = max(p, n);
+  float m = __uint_as_float(static_cast<uint32_t>(big) << 16 | (n > max(p, 0) ? 0x80000000u : 0u));
+  if (__any_sync(0xffffffffu, p == n)) m = largest_of(x);
+  const bool bad = big >= 0x7F80;
+  const __half h = scale_of(m, &d);
+  const float inv = bad || d == 0.f ? 0.f : __frcp_rn(d);
+  uint32_t c[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float q = x[i] * inv;
+    q = fmaf(fmaf(-q, d, x[i]), inv, q);
+    // 1.5 2^23 more rounds to an integer, ties to even, in the low bits
+    c[i] = __float_as_uint(fmaf(__saturatef(fmaf(q, 0.0625f, 0.5f)), 16.f, 12582912.f));
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) code[i] = min_u16x2(__byte_perm(c[2 * i], c[2 * i + 1], 0x5410), 0x000F000Fu);
   return bad ? __ushort_as_half(0x7FFF) : h;
 }
 
@@ -147,19 +208,14 @@ __global__ void __launch_bounds__(kAppendThreads) kv4_append_kernel(KvAppendPara
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) {
         const int r = r0 + k * kRowsPerPass;
-        float x[8];
-        uint32_t c[8];
-        unpack(rk[k], x);
-        const __half dk = quantise8<sizeof(T) == 4>(x, c);
-        uint32_t word = 0;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) word |= c[e] << (4 * nibble_of(e));
-        unpack(rv[k], x);
-        const __half dv = quantise8<sizeof(T) == 4>(x, c);
+        uint32_t c[4];
+        const __half dk = quantise8(rk[k], c);
+        const uint32_t word = c[0] | c[1] << 4 | c[2] << 8 | c[3] << 12;      // nibble_of's order
+        const __half dv = quantise8(rv[k], c);
         if (r < hi) {
           reinterpret_cast<uint32_t*>(blk)[Blk::key_word(r, w)] = word;
           *reinterpret_cast<uint2*>(&codes[r][8 * w]) =
-              make_uint2(c[0] | c[1] << 8 | c[2] << 16 | c[3] << 24, c[4] | c[5] << 8 | c[6] << 16 | c[7] << 24);
+              make_uint2(__byte_perm(c[0], c[1], 0x6420), __byte_perm(c[2], c[3], 0x6420));
           if ((w & 3) == 0) {
             reinterpret_cast<__half*>(blk + Blk::kKeyScales)[r * Blk::kGroups + (w >> 2)] = dk;
             reinterpret_cast<__half*>(blk + Blk::kValScales)[(w >> 2) * kPage + r] = dv;
@@ -173,18 +229,20 @@ __global__ void __launch_bounds__(kAppendThreads) kv4_append_kernel(KvAppendPara
     uint4* out = reinterpret_cast<uint4*>(blk + Blk::kValCodes);
     for (int i = tid; i < (o_hi - o_lo) * (D / 4); i += kAppendThreads) {
       const int cq = i % (D / 4), o = o_lo + i / (D / 4);
-      uint32_t v[4] = {0, 0, 0, 0}, keep = 0;
+      uint32_t q[8], keep = 0;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const int r = 8 * o + e;
-        if (r < lo || r >= hi) {
-          keep |= 0xFu << (4 * nibble_of(e));
-          continue;
-        }
-        const uint32_t q = *reinterpret_cast<const uint32_t*>(&codes[r][4 * cq]);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) v[c] |= ((q >> (8 * c)) & 15u) << (4 * nibble_of(e));
+        const bool in = r >= lo && r < hi;
+        q[e] = in ? *reinterpret_cast<const uint32_t*>(&codes[r][4 * cq]) : 0u;
+        if (!in) keep |= 0xFu << (4 * nibble_of(e));
       }
+      // two tokens a byte, then a transpose of four by four bytes: nibble_of's order
+      const uint32_t a0 = q[0] | q[2] << 4, a1 = q[4] | q[6] << 4, a2 = q[1] | q[3] << 4, a3 = q[5] | q[7] << 4;
+      const uint32_t b0 = __byte_perm(a0, a1, 0x5140), b1 = __byte_perm(a0, a1, 0x7362);
+      const uint32_t b2 = __byte_perm(a2, a3, 0x5140), b3 = __byte_perm(a2, a3, 0x7362);
+      uint32_t v[4] = {__byte_perm(b0, b2, 0x5410), __byte_perm(b0, b2, 0x7632), __byte_perm(b1, b3, 0x5410),
+                       __byte_perm(b1, b3, 0x7632)};
       uint4* dst = out + Blk::val_word(4 * cq, o) / 4;
       if (keep) {
         const uint4 old = *dst;

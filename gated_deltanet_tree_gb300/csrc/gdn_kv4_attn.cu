@@ -2,18 +2,17 @@
 //
 // kv4_attn_dec_kernel unpacks the cache once for each tile of eight rows: while the rows of a kv head are few, the
 // cache's bytes are the bound and it moves them best.  kv4_attn_tree_kernel unpacks it once for 128 rows.  They cross
-// at (microseconds, the first kernel against the second; 16 requests of 4096 tokens | 4 of 32768):
-//   D = 256:  12 rows  60 : 65 |  87 :  89     18 rows  76 :  66 | 120 :  89
-//   D = 128:  24 rows  76 : 77 | 111 : 115     32 rows  91 :  77 | 142 : 116
-//   D =  64:  22 rows  40 : 48 |  52 :  66     (a tile more adds 10)
-// and a lone request of 4096 tokens takes 27 : 31, 21 : 28 and 17 : 26 at 12, 24 and 16 rows.  fp32 calls run in
-// kv4_attn_dec_kernel at any size.
+// at (microseconds, the first kernel against the second; 16 requests of 5000 tokens | 4 of 5000):
+//   D = 256:   8 rows  53 :  66 |  31 :  39     16 rows  72 :  68 | 44 : 39 (tiles of 12 to 16 rows: even)
+//   D = 128:  16 rows  61 :  72 |  35 :  40     24 rows  84 :  74 | 39 : 41     32 rows  96 :  74
+//   D =  64:  24 rows  61 :  66 |  31 :  36     32 rows  76 :  66 | 35 : 35
+// fp32 calls run in kv4_attn_dec_kernel at any size.
 #include "gdn_kv4_attn.cuh"
 
 namespace gdn {
 
 namespace {
-int dec_rows(int D) { return D == 256 ? 16 : D == 128 ? 24 : 32; }      // rows of a kv head
+int dec_rows(int D) { return D == 64 ? 24 : 16; }      // rows of a kv head
 }
 
 // max_pages: the longest request's pages where the host knows a bound, else 0; with it no more CTAs are launched than
