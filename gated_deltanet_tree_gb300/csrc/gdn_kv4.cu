@@ -123,7 +123,7 @@ __device__ __forceinline__ uint32_t max_s16x2(uint32_t a, uint32_t b) {
 // only where both magnitudes are equal does the order of the channels decide.  Infinities and NaN are the largest.
 //
 // x and d have eight significant bits, so x / d is a tie or at least 2^-11 away from one: a product with 1 / d, corrected
-// once by its remainder (which makes ties exact), rounds like the quotient, and so does that number over 16 plus 1/2,
+// once by its remainder (exact, and ties come out exact), rounds like the quotient, and so does that number over 16 plus 1/2,
 // saturated to [0, 1]: 24 bits hold a tie exactly, and move the others by 2^-21 of a code at most.
 __device__ __forceinline__ __half quantise8(const Raw8<__nv_bfloat16>& r, uint32_t (&code)[4]) {
   float x[8], d;
@@ -143,7 +143,9 @@ __device__ __forceinline__ __half quantise8(const Raw8<__nv_bfloat16>& r, uint32
   if (__any_sync(0xffffffffu, p == n)) m = largest_of(x);
   const bool bad = big >= 0x7F80;
   const __half h = scale_of(m, &d);
-  const float inv = bad || d == 0.f ? 0.f : __frcp_rn(d);
+  float inv;                                   // within an ulp or two: the remainder makes up for it
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(d));
+  if (bad || d == 0.f) inv = 0.f;
   uint32_t c[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
