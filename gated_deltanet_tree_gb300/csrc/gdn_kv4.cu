@@ -13,8 +13,8 @@
 // finish (a ticket per request), so a call is one launch.
 //
 // Measured: two prompts of 20001 and 15000 bf16 rows, 4 kv heads of 256, appended in
-// 69 us (the ALU, 72% busy, bounds it: every element's rounding and packing) and read
-// back to fp32 in 62 us (6.0 TB/s, 0.88 of a plain copy's rate).
+// 57 us (issue slots, 73% taken, bound it: about 19 instructions an element, most of
+// them rounding) and read back to fp32 in 62 us (6.0 TB/s, 0.88 of a plain copy's rate).
 #include "gdn_kv4.cuh"
 
 namespace gdn {
@@ -122,9 +122,9 @@ __device__ __forceinline__ uint32_t max_s16x2(uint32_t a, uint32_t b) {
 // one signed (the largest positive element) and one unsigned (the most negative one, if any), find it and its sign;
 // only where both magnitudes are equal does the order of the channels decide.  Infinities and NaN are the largest.
 //
-// x and d have eight significant bits, so x / d is a tie or at least 2^-11 away from one: a product with 1 / d, corrected
-// once by its remainder (exact, and ties come out exact), rounds like the quotient, and so does that number over 16 plus 1/2,
-// saturated to [0, 1]: 24 bits hold a tie exactly, and move the others by 2^-21 of a code at most.
+// x and d have eight significant bits, so x / d is a tie or at least 2^-11 away from one: a product with 1 / d,
+// corrected once by its remainder (exact, and ties come out exact), rounds like the quotient, and so does that number
+// over 16 plus 1/2, saturated to [0, 1]: 24 bits hold a tie exactly, and move the others by 2^-21 of a code at most.
 __device__ __forceinline__ __half quantise8(const Raw8<__nv_bfloat16>& r, uint32_t (&code)[4]) {
   float x[8], d;
   unpack(r, x);

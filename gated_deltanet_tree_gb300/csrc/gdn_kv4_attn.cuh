@@ -189,8 +189,9 @@ __device__ __forceinline__ void kv_store(float* p, float x) { *p = x; }
 __device__ __forceinline__ void kv_store(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
 
 // The join of all rows of a tile by the whole CTA, in order: out = sum_c 2^{m_c - m} O_c / sum_c 2^{m_c - m} l_c (maxima
-// are kept in base 2), from partial results with the layout of kv_stream_part.  Reads of what other SMs just wrote take a microsecond and more, so the loads of a step are all in flight together: a row's
-// maxima and sums by one warp, then four channels of a row per thread, kAhead parts at a time.  `sh` holds
+// are kept in base 2), from partial results with the layout of kv_stream_part.  Reads of what other SMs just wrote take
+// a microsecond and more, so the loads of a step are all in flight together: a row's maxima and sums by one warp, then
+// four channels of a row per thread, kAhead parts at a time.  `sh` holds
 // (count + 1) * rows floats; row r of the item is query head r % G of node r / G, counted from out0.
 struct KvJoin {
   int c0, count, rows, inside;     // first CTA, CTAs, rows; the item starts inside its first CTA
