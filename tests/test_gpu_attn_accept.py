@@ -609,3 +609,49 @@ def test_example_runs_the_operators_together():
         path = model.acceptor.path[b]
         assert 1 <= L <= model.n_max and int(path[0]) == 0 and (path[L:] == -1).all()
         assert 0 <= int(model.acceptor.next[b]) < model.V
+
+
+@pytest.mark.parametrize("Hq,Hkv,D", [(24, 4, 256), (32, 8, 128), (32, 8, 64), (42, 7, 128)])
+def test_attention_many_items_shared_between_ctas(Hq, Hkv, D):
+    """More items than a quarter of the CTAs, most of them split: odd numbers of pages, ends inside a page, unseen NaN
+    and infinite rows in split items, tiles that a request does not fill, no new rows."""
+    rng = np.random.default_rng(Hq + Hkv + D)
+    lens = [700, 65, 1, 0, 330, 129, 512, 640, 200, 64, 450, 1090]
+    trees = [S.random_tree(m, rng) for m in (22, 30, 5, 64, 22, 1, 21, 33, 8, 12, 43, 22)]
+    run_case(rng, Hq, Hkv, D, lens, trees, "bf16")
+    run_case(rng, Hq, Hkv, D, lens, trees, "bf16", poison=[(0, 21), (7, 30), (11, 1)])
+    run_case(rng, Hq, Hkv, D, lens[:8], trees[:8], "bf16", new=False, max_len=0)
+
+
+def quantised(x):
+    """Values of rows [..., D] after the cache, by the formula in 64 bits."""
+    g = x.double().reshape(*x.shape[:-1], -1, 32)
+    a = g.abs()
+    first = torch.where(a == a.amax(-1, keepdim=True), torch.arange(32, device=x.device), 99).amin(-1, keepdim=True)
+    m = g.gather(-1, first)
+    d = (m * -0.125).float().bfloat16().float().clamp(-2720, 2720).half().double()
+    n = torch.where(d == 0, 0.0, torch.clamp(torch.round(g / torch.where(d == 0, 1.0, d)), -8, 7))
+    return (n * d).reshape(x.shape).float()
+
+
+@pytest.mark.parametrize("D", [64, 256])
+def test_append_bf16_codes_are_the_quotients(D):
+    """bf16 rows of any bits over 40 exponents, and rows of a few values of both signs (ties of the largest magnitude and
+    of the rounding; zeros of both signs): every value exact."""
+    g = torch.Generator(device="cuda").manual_seed(D)
+    L = 64 * 512
+
+    def ints(lo, hi, *shape):
+        return torch.randint(lo, hi, shape, generator=g, device="cuda", dtype=torch.int32)
+
+    top = ints(100, 140, L, D // 32, 1).expand(L, D // 32, 32).reshape(L, D)
+    bits = (ints(0, 65536, L, D) & 0x807F) | ((top - ints(0, 5, L, D)) << 7)
+    some = torch.tensor([0.0, -0.0, 0.5, -0.5, 1.5, -1.5, 3.5, -3.5, 7.0, 7.5, -7.5, 8.0, -8.0], device="cuda")
+    for x in ((bits << 16).view(torch.float32).bfloat16(), some[ints(0, 13, L, D).long()].bfloat16(),
+              some[ints(0, 2, L, D).long()].bfloat16()):
+        c = make_cache(1, 1, D, 1, 1, L // 64, "bf16")
+        c.append(x.view(1, 1, L, 1, D), -x.view(1, 1, L, 1, D), i32([L]))
+        k, v = c.read(None, L)
+        c.check_error()
+        assert torch.equal(k.view(L, D), quantised(x))
+        assert torch.equal(v.view(L, D), quantised(-x))
