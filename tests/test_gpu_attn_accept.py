@@ -655,3 +655,27 @@ def test_append_bf16_codes_are_the_quotients(D):
         c.check_error()
         assert torch.equal(k.view(L, D), quantised(x))
         assert torch.equal(v.view(L, D), quantised(-x))
+
+
+@pytest.mark.parametrize("n", [1, 22])
+def test_cache_pages_beyond_four_gigabytes(n):
+    """The same call over pages at the end of a pool of 5 GB and over a small pool: equal to the last bit."""
+    from gated_deltanet_tree_gb300 import runtime as R
+    rng = np.random.default_rng(n)
+    Hq, Hkv, D, L = 24, 4, 256, 150
+    k, v = rows(rng, 1, 1, L, Hkv, D, dtype="bf16"), rows(rng, 1, 1, L, Hkv, D, dtype="bf16")
+    q, kn = rows(rng, 1, 1, n, Hq, D, dtype="bf16"), rows(rng, 1, 1, n, Hkv, D, dtype="bf16")
+    tree = S.random_tree(n, rng)
+    results = []
+    for pages in (3, 70000):
+        dims = R.make_attn_dims(Hq, Hkv, D)
+        pool = torch.zeros(1, pages, Hkv, 72 * D, dtype=torch.uint8, device="cuda")
+        c = R.KV4Cache(dims, pool, i32([[pages - 1, pages - 3, pages - 2]]), i32([0]))
+        c.append(k, v, i32([L]))
+        out = torch.zeros_like(q)
+        c.attention(q, kn, kn, out, sched=None if n == 1 else R.DeviceSchedule([tree], n, "cuda"), max_len=L)
+        c.check_error()
+        results.append((out, *c.read(None, L), pool[0, -3:].clone()))
+        assert not pool[0, :-3].any()
+    for a, b in zip(*results):
+        assert torch.equal(a, b)
