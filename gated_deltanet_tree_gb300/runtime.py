@@ -247,8 +247,9 @@ class KV4Cache:
         if start is not None:
             self._check_i32(start, "start", (self.B,))
         code = _dtype_code(dtype, "dtype")
-        kv = torch.empty((2, self.B, self.layers, n, *self._heads[1:]), dtype=dtype, device=self.device)
-        k, v = kv.unbind(0)
+        shape = (self.B, self.layers, n, *self._heads[1:])
+        k = torch.empty(shape, dtype=dtype, device=self.device)     # (two views of one tensor take twice the host time)
+        v = torch.empty(shape, dtype=dtype, device=self.device)
         dims, cache = self._refs
         N._check(N.lib().gdn_kv4_read(dims, self.layers, n, None if start is None else start.data_ptr(), code,
                                       k.data_ptr(), v.data_ptr(), cache, N._stream_of(stream, self._index)))
