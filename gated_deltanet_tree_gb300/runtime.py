@@ -161,6 +161,14 @@ def _row_stride(t: torch.Tensor, name: str, shape: tuple) -> int:
     for size, got, need in zip(shape, t.stride(), want):
         if size > 1 and got != need:
             raise ValueError(f"{name} has strides {t.stride()}: rows need one stride, heads and channels contiguous")
+    return _stride_in_range(row, H * D, name)
+
+
+def _stride_in_range(row: int, least: int, name: str) -> int:
+    """A row stride as the calls take it: 0 would stand for contiguous rows there, and 32 bits hold it."""
+    if not least <= row < 1 << 31:
+        raise ValueError(f"{name} has rows {row} elements apart: rows of {least} elements may neither overlap nor repeat "
+                         f"(a broadcast), nor lie 2^31 elements apart; make it contiguous")
     return row
 
 
@@ -317,7 +325,7 @@ class TreeAcceptor:
         row = t.stride(1) if self.n_max > 1 else t.stride(0) if self.B > 1 else self.V
         if (self.V > 1 and t.stride(2) != 1) or (self.B > 1 and t.stride(0) != self.n_max * row):
             raise ValueError(f"{name} has strides {t.stride()}: rows need one stride and contiguous values")
-        return row
+        return _stride_in_range(row, self.V, name)
 
     def _small(self, t: Optional[torch.Tensor], name: str, shape: tuple, dtype: torch.dtype) -> int:
         if t is None:

@@ -1,0 +1,112 @@
+"""What KV4Cache and TreeAcceptor pass to the library, and what they refuse (no GPU: the device calls are recorded)."""
+import ctypes
+
+import pytest
+import torch
+
+
+class Recorder:
+    """The library with its device calls replaced: each records its arguments and returns `status`."""
+
+    def __init__(self, real):
+        self.real, self.calls, self.status = real, [], 0
+
+    def __getattr__(self, name):
+        if name not in ("gdn_kv4_append", "gdn_kv4_read", "gdn_kv4_attention", "gdn_tree_accept", "gdn_check_error_words"):
+            return getattr(self.real, name)
+
+        def call(*args):
+            seen = []
+            for a in args:
+                a = getattr(a, "_obj", a)
+                seen.append(type(a).from_buffer_copy(a) if isinstance(a, ctypes.Structure) else a)
+            self.calls.append((name, seen))
+            return self.status
+        return call
+
+
+@pytest.fixture()
+def R(monkeypatch):
+    from gated_deltanet_tree_gb300.build import build
+    build()
+    from gated_deltanet_tree_gb300 import _native as N
+    from gated_deltanet_tree_gb300 import runtime
+    rec = Recorder(N.lib())
+    monkeypatch.setattr(N, "lib", lambda: rec)
+    runtime.recorder = rec
+    yield runtime
+    del runtime.recorder
+
+
+def make_cache(R, Hq=4, Hkv=2, D=64, B=2, layers=2, dtype=torch.bfloat16):
+    return R.KV4Cache.empty(R.make_attn_dims(Hq, Hkv, D, dtype=dtype), B, layers, 2, device="cpu")
+
+
+def i32(*x):
+    return torch.tensor(x, dtype=torch.int32)
+
+
+def schedule(R, B, n):
+    return R.DeviceSchedule([[-1] + list(range(n - 1))] * B, n, "cpu")
+
+
+# ---- strides --------------------------------------------------------------------------------------------------------
+
+def spread(shape, strides):
+    """A tensor of that shape and those strides without memory behind it (nothing reads it)."""
+    return torch.empty_strided(shape, strides, dtype=torch.bfloat16, device="meta")
+
+
+@pytest.mark.parametrize("B,layers,n", [(2, 2, 3), (2, 1, 1), (1, 2, 1), (1, 1, 3)])
+def test_repeated_rows_are_refused(R, B, layers, n):
+    """Rows of stride 0 (a broadcast): the calls read a stride of 0 as contiguous rows, past the end of the memory."""
+    c = make_cache(R, B=B, layers=layers)
+    one = torch.zeros(1, 1, 1, 2, 64, dtype=torch.bfloat16)
+    k = one.expand(B, layers, n, 2, 64)
+    good = k.contiguous()
+    q = torch.zeros(1, 1, 1, 4, 64, dtype=torch.bfloat16).expand(B, layers, n, 4, 64)
+    out = torch.zeros(B, layers, n, 4, 64, dtype=torch.bfloat16)
+    count, sched = i32(*[1] * B), schedule(R, B, n)
+    for bad in (lambda: c.append(k, k, count, stream=0), lambda: c.append(good, k, count, stream=0),
+                lambda: c.attention(q, good, good, out, sched=sched, stream=0),
+                lambda: c.attention(out, k, k, out, sched=sched, stream=0)):
+        with pytest.raises(ValueError, match="broadcast|row strides"):
+            bad()
+    assert not R.recorder.calls
+
+
+def test_overlapping_rows_are_refused(R):
+    c = make_cache(R, B=1, layers=1)
+    flat = torch.zeros(64 * 16, dtype=torch.bfloat16)
+    k = flat.as_strided((1, 1, 3, 2, 64), (192, 192, 64, 64, 1))
+    with pytest.raises(ValueError):
+        c.append(k, k, i32(1), stream=0)
+    assert not R.recorder.calls
+
+
+def test_far_rows_are_refused(R):
+    """A stride beyond 32 bits: ctypes would cut it to its low bits."""
+    far = (1 << 32) + 128
+    assert R._row_stride(spread((2, 1, 1, 2, 64), (640, 640, 640, 64, 1)), "k", (2, 1, 1, 2, 64)) == 640
+    with pytest.raises(ValueError):
+        R._row_stride(spread((2, 1, 1, 2, 64), (far, far, far, 64, 1)), "k", (2, 1, 1, 2, 64))
+    acc = R.TreeAcceptor(2, 1, 100, device="cpu")
+    acc._index = spread((1,), (1,)).get_device()
+    assert acc._rows(spread((2, 1, 100), (128, 128, 1)), "logits") == 128
+    with pytest.raises(ValueError):
+        acc._rows(spread((2, 1, 100), (far, far, 1)), "logits")
+
+
+@pytest.mark.parametrize("B,n", [(2, 3), (1, 3), (2, 1)])
+def test_repeated_logits_are_refused(R, B, n):
+    acc = R.TreeAcceptor(B, n, 100, device="cpu")
+    z = torch.zeros(1, 1, 100).expand(B, n, 100)
+    tokens, sched = torch.zeros(B, n, dtype=torch.int32), schedule(R, B, n)
+    args = (torch.zeros(B, n), torch.zeros(B, 100), torch.ones(B))
+    for bad in (lambda: acc.accept(sched, z, tokens, *args, stream=0),
+                lambda: acc.accept(sched, z.contiguous(), tokens, *args, draft_probs=z, stream=0)):
+        with pytest.raises(ValueError):
+            bad()
+    assert not R.recorder.calls
+    acc.accept(sched, z.contiguous(), tokens, *args, stream=0)
+    assert [name for name, _ in R.recorder.calls] == ["gdn_tree_accept"]
