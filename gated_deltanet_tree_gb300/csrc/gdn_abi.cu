@@ -527,7 +527,7 @@ gdn_status gdn_kv4_attention(const gdn_attn_dims* d, int32_t layers, const gdn_b
 // ---- acceptance of drafted tokens ----
 
 size_t gdn_accept_workspace_bytes(int32_t B, int32_t n_max, int32_t V) {
-  if (B < 1 || n_max < 1 || n_max > GDN_MAX_NODES || V < 1) return 0;
+  if (B < 1 || n_max < 1 || n_max > GDN_MAX_NODES || V < 1 || V > gdn::kMaxVocab) return 0;
   return round_up(static_cast<size_t>(B) * n_max * gdn::accept_slices(B, n_max, V) * 16 + 1, kAlign);
 }
 
@@ -539,6 +539,7 @@ gdn_status gdn_tree_accept(const gdn_batch_schedule* sched, int32_t V, int32_t v
   gdn::clear_error();
   GDN_TRY(check_sched(sched));
   if (V < 1) return fail(GDN_ERR_INVALID_ARG, "V = %d", V);
+  if (V > gdn::kMaxVocab) return fail(GDN_ERR_UNSUPPORTED, "V = %d above %d", V, gdn::kMaxVocab);
   if (v_stride != 0 && v_stride < V) return fail(GDN_ERR_INVALID_ARG, "v_stride = %d, V = %d", v_stride, V);
   if (logits_dtype != GDN_DTYPE_F32 && logits_dtype != GDN_DTYPE_BF16)
     return fail(GDN_ERR_INVALID_ARG, "logits_dtype = %d", logits_dtype);

@@ -21,6 +21,7 @@ struct AcceptParams {
   int n_slices;                // > 0: every row is reduced at once, in this many slices
   void* slices;                // [B][n_max][n_slices] partial results of 16 bytes (workspace)
 };
+constexpr int kMaxVocab = 1 << 30;   // the kernels' indices pass V by up to a cluster's step of 2^15 before they are compared with it
 constexpr double kRowsAtOnceBytes = 128.0 * (1 << 20);
 int accept_slices(int B, int n_max, int V);
 cudaError_t launch_accept(const AcceptParams& p, cudaStream_t s);

@@ -510,6 +510,7 @@ gdn_status gdn_kv4_attention(const gdn_attn_dims* d, int32_t layers, const gdn_b
  * sets GDN_DEVERR_LOGITS in err (int32 [4], as gdn_banks.err), ends the request's
  * walk and gives next = -1.
  *   workspace >= gdn_accept_workspace_bytes(B, n_max, V) bytes
+ * GDN_ERR_UNSUPPORTED: V above 2^30.
  * ------------------------------------------------------------------------- */
 size_t gdn_accept_workspace_bytes(int32_t B, int32_t n_max, int32_t V);
 gdn_status gdn_tree_accept(const gdn_batch_schedule* sched, int32_t V, int32_t v_stride, int32_t logits_dtype,

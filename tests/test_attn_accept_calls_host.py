@@ -110,3 +110,17 @@ def test_repeated_logits_are_refused(R, B, n):
     assert not R.recorder.calls
     acc.accept(sched, z.contiguous(), tokens, *args, stream=0)
     assert [name for name, _ in R.recorder.calls] == ["gdn_tree_accept"]
+
+
+# ---- sizes ----------------------------------------------------------------------------------------------------------
+
+def test_vocabularies_beyond_the_index_range_are_refused(R):
+    """The kernels' 32-bit indices run past V by a cluster's step; at 2^31 - 1 they would turn negative."""
+    from gated_deltanet_tree_gb300 import _native as N
+    P = 0x10000          # never dereferenced
+    lib, sched = R.recorder.real, N.gdn_batch_schedule(B=1, n_max=1, nb_max=0, depth_max=0, words=P)
+    for V in ((1 << 30) + 1, (1 << 31) - 1):
+        assert N.gdn_accept_workspace_bytes(1, 1, V) == 0
+        assert lib.gdn_tree_accept(ctypes.byref(sched), V, 0, 0, P, P, None, 0, P, P, P, P, P, P, P, P, 1 << 40,
+                                   0) == N.GDN_ERR_UNSUPPORTED
+    assert N.gdn_accept_workspace_bytes(1, 2, 1 << 30) > 0
