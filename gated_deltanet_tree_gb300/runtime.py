@@ -172,9 +172,18 @@ def _stride_in_range(row: int, least: int, name: str) -> int:
     return row
 
 
+def _finish_fills(device: torch.device):
+    """Waits for what the current stream has filled on a device, so that a first call on any stream finds it filled."""
+    if device.type == "cuda":
+        torch.cuda.current_stream(device).synchronize()
+
+
 class KV4Cache:
     """The paged 4-bit key/value cache of a stack of full-attention layers: the pool, page table and lengths the
-    caller gives (or empty() makes) and the counters and workspace of the calls on them."""
+    caller gives (or empty() makes) and the counters and workspace of the calls on them.
+
+    A call may go to any stream, or into a CUDA graph.  The calls on one cache share its counters and workspace, so they
+    must follow one another: order those on different streams by events."""
 
     def __init__(self, dims: N.gdn_attn_dims, pool: torch.Tensor, page_table: torch.Tensor, seq_len: torch.Tensor):
         if pool.dim() != 4 or pool.dtype != torch.uint8 or tuple(pool.shape[2:]) != (dims.Hkv, 72 * dims.D):
@@ -193,8 +202,11 @@ class KV4Cache:
         self.B, self.layers, self.pages_max = seq_len.shape[0], pool.shape[0], page_table.shape[1]
         self.ticket = torch.zeros(self.B, dtype=torch.int32, device=self.device)
         self.err = torch.zeros(4, dtype=torch.int32, device=self.device)
-        self.workspace: Optional[torch.Tensor] = None
-        self.ws_bytes: dict = {}
+        # Made for the largest call, once: a workspace that grew with the calls would be filled on another stream than the
+        # kernel's, and freed under kernels in flight and captured graphs.  Its size is bounded by the CTAs of a launch
+        self.workspace = torch.zeros(max(256, *(N.gdn_kv4_workspace_bytes(dims, self.B, self.layers, n, 0)
+                                                for n in range(1, N.GDN_MAX_NODES + 1))),
+                                     dtype=torch.uint8, device=self.device)
         self.struct = N.gdn_kv4_cache(pool=pool.data_ptr(), page_table=page_table.data_ptr(),
                                       seq_len=seq_len.data_ptr(), ticket=self.ticket.data_ptr(),
                                       err=self.err.data_ptr(), B=self.B, layers=self.layers,
@@ -204,6 +216,7 @@ class KV4Cache:
         self._index = pool.get_device()
         self._refs = (ctypes.byref(self.dims), ctypes.byref(self.struct))
         self._heads = (dims.Hq, dims.Hkv, dims.D)
+        _finish_fills(self.device)
 
     @classmethod
     def empty(cls, dims: N.gdn_attn_dims, B: int, layers: int, pages_max: int, device="cuda") -> "KV4Cache":
@@ -263,15 +276,6 @@ class KV4Cache:
                                       k.data_ptr(), v.data_ptr(), cache, N._stream_of(stream, self._index)))
         return k, v
 
-    def _workspace(self, n_max: int, max_len: int):
-        need = self.ws_bytes.get((n_max, max_len))
-        if need is None:
-            need = N.gdn_kv4_workspace_bytes(self.dims, self.B, self.layers, n_max, max_len)
-            self.ws_bytes[(n_max, max_len)] = need
-        if self.workspace is None or self.workspace.numel() < need:
-            self.workspace = torch.zeros(max(need, 256), dtype=torch.uint8, device=self.device)
-        return need
-
     def attention(self, q: torch.Tensor, k_new: Optional[torch.Tensor], v_new: Optional[torch.Tensor],
                   out: torch.Tensor, sched: Optional[DeviceSchedule] = None, max_len: int = 0, stream=None):
         """Nodes q [B, layers, n_max, Hq, D] attend to the cached tokens and (with k_new, v_new) to their ancestors'
@@ -287,7 +291,6 @@ class KV4Cache:
             raise ValueError("k_new and v_new: both or neither")
         if k_new is not None and self._rows(k_new, v_new) != n:
             raise ValueError("k_new and q have different node counts")
-        self._workspace(n, max_len)
         dims, cache = self._refs
         N._check(N.lib().gdn_kv4_attention(dims, self.layers, None if sched is None else ctypes.byref(sched.struct),
                                            q.data_ptr(), None if k_new is None else k_new.data_ptr(),
@@ -315,6 +318,7 @@ class TreeAcceptor:
         self._index = self.path.get_device()
         self._out = (self.path.data_ptr(), self.len.data_ptr(), self.next.data_ptr(), self.err.data_ptr(),
                      self.workspace.data_ptr(), self.workspace.numel())
+        _finish_fills(self.device)
 
     def _rows(self, t: torch.Tensor, name: str) -> int:
         want = (self.B, self.n_max, self.V)

@@ -124,3 +124,24 @@ def test_vocabularies_beyond_the_index_range_are_refused(R):
         assert lib.gdn_tree_accept(ctypes.byref(sched), V, 0, 0, P, P, None, 0, P, P, P, P, P, P, P, P, 1 << 40,
                                    0) == N.GDN_ERR_UNSUPPORTED
     assert N.gdn_accept_workspace_bytes(1, 2, 1 << 30) > 0
+
+
+# ---- workspace ------------------------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("Hq,Hkv,D", [(24, 4, 256), (8, 2, 128), (4, 2, 64)])
+def test_one_workspace_serves_every_call(R, Hq, Hkv, D, dtype):
+    """Single tokens, then trees and longer requests: the same memory from the first call on (a kernel in flight or a
+    captured graph may hold it), large enough for each, and nothing kept by the lengths that were passed."""
+    from gated_deltanet_tree_gb300 import _native as N
+    c = make_cache(R, Hq, Hkv, D, dtype=dtype)
+    kept = {name: value for name, value in vars(c).items()}
+    for n, max_len in ((1, 1), (1, 100), (2, 0), (8, 4096), (22, 0), (64, 1 << 20), (64, 0), (1, 7)):
+        q = torch.zeros(2, 2, n, Hq, D, dtype=dtype)
+        k = torch.zeros(2, 2, n, Hkv, D, dtype=dtype)
+        c.attention(q, k, k, torch.zeros_like(q), sched=None if n == 1 else schedule(R, 2, n), max_len=max_len, stream=0)
+        _, args = R.recorder.calls[-1]
+        assert args[9:11] == [kept["workspace"].data_ptr(), kept["workspace"].numel()]
+        assert args[10] >= N.gdn_kv4_workspace_bytes(c.dims, 2, 2, n, max_len) > 0
+    assert vars(c).keys() == kept.keys() and all(vars(c)[x] is kept[x] for x in kept)
+    assert not any(isinstance(x, dict) for x in kept.values())

@@ -1,0 +1,117 @@
+"""The cache and acceptance calls as programs make them on a GPU: streams, CUDA graphs, refusals between calls, and the
+paths of the kernels that only large batches, many launches or long contexts reach.  Tolerances as in
+test_gpu_attn_accept.py unless a test derives its own."""
+import numpy as np
+import pytest
+import torch
+
+import synthetic as S
+from oracle import accept_oracle as A
+from oracle import kv4_oracle as K
+from test_gpu_attn_accept import built, check, f64, filled, i32, rows  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+def schedule(trees, n):
+    from gated_deltanet_tree_gb300.runtime import DeviceSchedule
+    return DeviceSchedule(trees, n, "cuda")
+
+
+def tree_reference(c, q, kr, vr, kn, vn, lens, trees):
+    return [K.tree_attention(f64(q[b, 0, :len(t)]), kr[b, 0, :lens[b]], vr[b, 0, :lens[b]], f64(kn[b, 0, :len(t)]),
+                             f64(vn[b, 0, :len(t)]), t, c.dims.scale) for b, t in enumerate(trees)]
+
+
+# ---- streams and graphs ---------------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("n", [1, 6])
+def test_first_call_on_a_side_stream_while_the_current_one_is_busy(n):
+    """Items shared by several CTAs (their counters and partial results are in the workspace) in a cache's first call,
+    on another stream than the one the cache was made on, which is busy all the while."""
+    rng = np.random.default_rng(40 + n)
+    lens, trees = [3000, 1700], [S.random_tree(n, rng), S.random_tree(n, rng)]
+    filled_c, kr, vr = filled(rng, 24, 4, 256, lens, 1, "bf16")
+    q, kn, vn = (rows(rng, 2, 1, n, h, 256, dtype="bf16") for h in (24, 4, 4))
+    sched = schedule(trees, n)
+    ref = tree_reference(filled_c, q, kr, vr, kn, vn, lens, trees)
+    vmax = max(float(vn.abs().max()), float(np.abs(vr).max()))
+    from gated_deltanet_tree_gb300.runtime import KV4Cache
+    out = torch.full_like(q, 7.0)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    junk = torch.full((64 << 20,), 0xA5, dtype=torch.uint8, device="cuda")     # what an unfilled workspace would hold
+    del junk
+    torch.cuda.synchronize()
+    torch.cuda._sleep(20_000_000)                                              # ends by itself, about 10 ms
+    c = KV4Cache(filled_c.dims, filled_c.pool, filled_c.page_table, filled_c.seq_len)
+    torch.cuda._sleep(20_000_000)
+    c.attention(q, kn, vn, out, sched=sched, max_len=3000, stream=side)
+    side.synchronize()
+    got = out.clone()
+    torch.cuda.synchronize()
+    c.check_error()
+    assert not c.workspace[:65536].any()
+    for b in range(2):
+        check(f64(got[b, 0]), ref[b], vmax, "bf16", b)
+
+
+@pytest.mark.parametrize("n", [1, 22])
+def test_captured_steps_replay_after_larger_calls(n):
+    """A graph of a step (attention, acceptance, append of what was accepted) holds its buffers: larger calls on the same
+    cache in between change neither them nor its results, and a replay follows the cache's lengths."""
+    from gated_deltanet_tree_gb300 import runtime as R
+    rng = np.random.default_rng(42)
+    B, Hq, Hkv, D, V = 2, 6, 2, 128, 20001
+    c, _, _ = filled(rng, Hq, Hkv, D, [500, 90], 1, "bf16", slack=2)
+    acc = R.TreeAcceptor(B, n, V)
+    trees = [S.random_tree(n, rng) for _ in range(B)]
+    sched = schedule(trees, n)
+    q, k, v = (rows(rng, B, 1, n, h, D, dtype="bf16") for h in (Hq, Hkv, Hkv))
+    tokens = rng.integers(0, V, (B, n))
+
+    def logits():
+        z = rng.standard_normal((B, n, V)).astype(np.float32)
+        for b in range(B):
+            for i in range(1, n):
+                if rng.random() < 0.5:
+                    z[b, trees[b][i], tokens[b, i]] += 20.0
+        return torch.from_numpy(z).cuda()
+
+    z, tok, out = logits(), i32(tokens), torch.zeros_like(q)
+
+    def step():
+        c.attention(q, k, v, out, sched=sched)
+        path, length, _ = acc.accept(sched, z, tok)
+        c.append(k, v, length, path=path)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(side):
+        step()
+        side.synchronize()
+        with torch.cuda.graph(graph, stream=side):
+            step()
+    torch.cuda.current_stream().wait_stream(side)
+    big, kb = rows(rng, B, 1, 64, Hq, D, dtype="bf16"), rows(rng, B, 1, 64, Hkv, D, dtype="bf16")
+    bigger = schedule([S.random_tree(64, rng)] * B, 64)
+    for i in range(3):
+        c.attention(big, kb, kb, torch.zeros_like(big), sched=bigger, max_len=0)
+        junk = [torch.full((8 << 20,), 0xA5, dtype=torch.uint8, device="cuda") for _ in range(8)]   # freed memory's next user
+        for t in (q, k, v):
+            t.copy_(rows(rng, *t.shape, dtype="bf16"))
+        z.copy_(logits())
+        lens = c.seq_len.tolist()
+        kr, vr = (f64(t) for t in c.read(None, max(lens)))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(bool((t == 0xA5).all()) for t in junk)
+        c.check_error()
+        acc.check_error()
+        ref = tree_reference(c, q, kr, vr, k, v, lens, trees)
+        for b in range(B):
+            check(f64(out[b, 0]), ref[b], max(float(v.abs().max()), float(np.abs(vr).max())), "bf16", (i, b))
+            path, token = A.accept(trees[b].tolist(), tokens[b].tolist(), f64(z[b]), None, None, 0.0)
+            assert acc.path[b, :len(path)].tolist() == path and int(acc.next[b]) == token
+            assert int(c.seq_len[b]) == lens[b] + len(path) == lens[b] + int(acc.len[b])
