@@ -196,7 +196,8 @@ class KV4Cache:
         for t in (pool, page_table, seq_len):
             if not t.is_contiguous() or t.device != pool.device:
                 raise ValueError("pool, page_table and seq_len are contiguous tensors of one device")
-        self.dims = N.gdn_attn_dims.from_buffer_copy(dims)     # its row strides follow each call's tensors
+        self.dims = N.gdn_attn_dims.from_buffer_copy(dims)
+        self.dims.q_row = self.dims.kv_row = 0                 # contiguous rows; a call with others makes its own copy
         self.pool, self.page_table, self.seq_len = pool, page_table, seq_len
         self.device = pool.device
         self.B, self.layers, self.pages_max = seq_len.shape[0], pool.shape[0], page_table.shape[1]
@@ -204,7 +205,7 @@ class KV4Cache:
         self.err = torch.zeros(4, dtype=torch.int32, device=self.device)
         # Made for the largest call, once: a workspace that grew with the calls would be filled on another stream than the
         # kernel's, and freed under kernels in flight and captured graphs.  Its size is bounded by the CTAs of a launch
-        self.workspace = torch.zeros(max(256, *(N.gdn_kv4_workspace_bytes(dims, self.B, self.layers, n, 0)
+        self.workspace = torch.zeros(max(256, *(N.gdn_kv4_workspace_bytes(self.dims, self.B, self.layers, n, 0)
                                                 for n in range(1, N.GDN_MAX_NODES + 1))),
                                      dtype=torch.uint8, device=self.device)
         self.struct = N.gdn_kv4_cache(pool=pool.data_ptr(), page_table=page_table.data_ptr(),
@@ -235,7 +236,8 @@ class KV4Cache:
             raise ValueError(f"{name} is a contiguous int32 tensor {shape} on {self.device}, got {tuple(t.shape)} "
                              f"{t.dtype} on {t.device}")
 
-    def _rows(self, k: torch.Tensor, v: torch.Tensor) -> int:
+    def _rows(self, k: torch.Tensor, v: torch.Tensor) -> tuple:
+        """Rows a request and their stride."""
         if k.dim() != 5:
             raise ValueError(f"k_new is [B, layers, n, Hkv, D], got {tuple(k.shape)}")
         n = k.shape[2]
@@ -246,20 +248,29 @@ class KV4Cache:
         row = _row_stride(k, "k_new", want)
         if row != _row_stride(v, "v_new", want):
             raise ValueError("k_new and v_new have different row strides")
-        self.dims.kv_row = row
-        return n
+        return n, row
+
+    def _dims(self, q_row: int, kv_row: int):
+        """The cache's shapes with a call's row strides.  They are never written to the cache's own: a refused call would
+        leave them behind, and calls from two threads would take each other's."""
+        Hq, Hkv, D = self._heads
+        if q_row == Hq * D and kv_row == Hkv * D:
+            return self._refs[0]
+        d = N.gdn_attn_dims.from_buffer_copy(self.dims)
+        d.q_row, d.kv_row = q_row, kv_row
+        return ctypes.byref(d)
 
     def append(self, k_new: torch.Tensor, v_new: torch.Tensor, count: torch.Tensor,
                path: Optional[torch.Tensor] = None, stream=None):
         """Quantise rows k_new, v_new [B, layers, n, Hkv, D] into the cache: the first count[b], or the rows path[b]
         names, and advance the lengths (on the device)."""
-        n = self._rows(k_new, v_new)
+        n, row = self._rows(k_new, v_new)
         self._check_i32(count, "count", (self.B,))
         if path is not None:
             self._check_i32(path, "path", (self.B, n))
-        dims, cache = self._refs
-        N._check(N.lib().gdn_kv4_append(dims, self.layers, n, k_new.data_ptr(), v_new.data_ptr(),
-                                        None if path is None else path.data_ptr(), count.data_ptr(), cache,
+        Hq, _, D = self._heads
+        N._check(N.lib().gdn_kv4_append(self._dims(Hq * D, row), self.layers, n, k_new.data_ptr(), v_new.data_ptr(),
+                                        None if path is None else path.data_ptr(), count.data_ptr(), self._refs[1],
                                         N._stream_of(stream, self._index)))
 
     def read(self, start: Optional[torch.Tensor], n: int, dtype: torch.dtype = torch.float32, stream=None):
@@ -281,18 +292,21 @@ class KV4Cache:
         """Nodes q [B, layers, n_max, Hq, D] attend to the cached tokens and (with k_new, v_new) to their ancestors'
         and their own rows; sched None: one node a request.  max_len bounds the lengths where the host knows it."""
         n = 1 if sched is None else sched.struct.n_max
-        Hq, _, D = self._heads
+        Hq, Hkv, D = self._heads
         self._check_type(q, "q")
         self._check_type(out, "out")
-        self.dims.q_row = _row_stride(q, "q", (self.B, self.layers, n, Hq, D))
+        q_row = _row_stride(q, "q", (self.B, self.layers, n, Hq, D))
         if out.shape != q.shape or not out.is_contiguous():
             raise ValueError("out is contiguous with the shape of q")
         if (k_new is None) != (v_new is None):
             raise ValueError("k_new and v_new: both or neither")
-        if k_new is not None and self._rows(k_new, v_new) != n:
-            raise ValueError("k_new and q have different node counts")
-        dims, cache = self._refs
-        N._check(N.lib().gdn_kv4_attention(dims, self.layers, None if sched is None else ctypes.byref(sched.struct),
+        kv_row = Hkv * D
+        if k_new is not None:
+            n_new, kv_row = self._rows(k_new, v_new)
+            if n_new != n:
+                raise ValueError("k_new and q have different node counts")
+        cache = self._refs[1]
+        N._check(N.lib().gdn_kv4_attention(self._dims(q_row, kv_row), self.layers, None if sched is None else ctypes.byref(sched.struct),
                                            q.data_ptr(), None if k_new is None else k_new.data_ptr(),
                                            None if v_new is None else v_new.data_ptr(), out.data_ptr(), cache, max_len,
                                            self.workspace.data_ptr(), self.workspace.numel(),

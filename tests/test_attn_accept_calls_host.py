@@ -112,6 +112,34 @@ def test_repeated_logits_are_refused(R, B, n):
     assert [name for name, _ in R.recorder.calls] == ["gdn_tree_accept"]
 
 
+def test_row_strides_are_a_calls_own(R):
+    """Rows of a fused projection, then contiguous rows, then no new rows: each call passes its own strides, and neither
+    a served nor a refused one leaves any behind."""
+    c = make_cache(R, B=1, layers=1)
+    wide = torch.zeros(1, 1, 3, 10, 64, dtype=torch.bfloat16)
+    q, k, v = wide[..., :4, :], wide[..., 4:6, :], wide[..., 6:8, :]
+    out, count, sched = torch.zeros(1, 1, 3, 4, 64, dtype=torch.bfloat16), i32(1), schedule(R, 1, 3)
+
+    def strides(call):
+        call()
+        d = R.recorder.calls[-1][1][0]
+        assert (c.dims.q_row, c.dims.kv_row) == (0, 0)
+        return d.q_row or 4 * 64, d.kv_row or 2 * 64
+
+    kc, vc = k.contiguous(), v.contiguous()
+    assert strides(lambda: c.attention(q, k, v, out, sched=sched, stream=0)) == (640, 640)
+    assert strides(lambda: c.attention(out, k, v, out, sched=sched, stream=0)) == (256, 640)
+    assert strides(lambda: c.attention(q, None, None, out, sched=sched, stream=0)) == (640, 128)
+    assert strides(lambda: c.attention(out, kc, vc, out, sched=sched, stream=0)) == (256, 128)
+    assert strides(lambda: c.append(k, v, count, stream=0)) == (256, 640)
+    assert strides(lambda: c.append(kc, vc, count, stream=0)) == (256, 128)
+    R.recorder.status = -1                                  # (the library refuses, as it does rows of odd strides)
+    for call in (lambda: c.attention(q, k, v, out, sched=sched, stream=0), lambda: c.append(k, v, count, stream=0)):
+        with pytest.raises(R.N.GdnError):
+            call()
+        assert (c.dims.q_row, c.dims.kv_row) == (0, 0)
+
+
 # ---- sizes ----------------------------------------------------------------------------------------------------------
 
 def test_vocabularies_beyond_the_index_range_are_refused(R):

@@ -115,3 +115,32 @@ def test_captured_steps_replay_after_larger_calls(n):
             path, token = A.accept(trees[b].tolist(), tokens[b].tolist(), f64(z[b]), None, None, 0.0)
             assert acc.path[b, :len(path)].tolist() == path and int(acc.next[b]) == token
             assert int(c.seq_len[b]) == lens[b] + len(path) == lens[b] + int(acc.len[b])
+
+
+# ---- refusals between calls -----------------------------------------------------------------------------------------
+
+def test_a_refused_call_leaves_nothing_behind():
+    """Rows of a fused projection whose stride is no multiple of 16 bytes are refused; the calls after that are served."""
+    from gated_deltanet_tree_gb300 import _native as N
+    rng = np.random.default_rng(43)
+    Hq, Hkv, D, n = 8, 2, 64, 5
+    c, kr, vr = filled(rng, Hq, Hkv, D, [90], 1, "bf16", slack=1)
+    flat = rows(rng, 1, 1, n, (Hq + 2 * Hkv) * D + 4, dtype="bf16")                  # (four gate columns)
+    wide = flat[..., :-4].unflatten(-1, (Hq + 2 * Hkv, D))
+    q, k, v = wide[..., :Hq, :], wide[..., Hq:Hq + Hkv, :], wide[..., Hq + Hkv:, :]
+    tree = S.random_tree(n, rng)
+    out, sched, one = torch.zeros(1, 1, n, Hq, D, dtype=torch.bfloat16, device="cuda"), schedule([tree], n), i32([1])
+    for bad in (lambda: c.attention(q, k, v, out, sched=sched), lambda: c.attention(q, None, None, out, sched=sched),
+                lambda: c.append(k, v, one)):
+        with pytest.raises(N.GdnError) as e:
+            bad()
+        assert e.value.status == N.GDN_ERR_INVALID_ARG
+        kc, vc = k.contiguous(), v.contiguous()
+        c.attention(q.contiguous(), kc, vc, out, sched=sched)
+        ref = tree_reference(c, q, kr, vr, k, v, [90], [tree])
+        check(f64(out[0, 0]), ref[0], max(float(v.abs().max()), float(np.abs(vr).max())), "bf16", "after a refusal")
+        again = c.read(None, 90)
+        assert np.array_equal(f64(again[0]), kr) and np.array_equal(f64(again[1]), vr)
+    c.append(kc, vc, one)
+    c.check_error()
+    assert int(c.seq_len[0]) == 91
