@@ -275,13 +275,22 @@ class KV4Cache:
 
     def read(self, start: Optional[torch.Tensor], n: int, dtype: torch.dtype = torch.float32, stream=None):
         """Values of tokens start[b] .. start[b] + n - 1 (None: from 0) -> k, v [B, layers, n, Hkv, D]; zeros past a
-        request's length."""
+        request's length.  With a stream given they are complete on that one."""
         if start is not None:
             self._check_i32(start, "start", (self.B,))
         code = _dtype_code(dtype, "dtype")
         shape = (self.B, self.layers, n, *self._heads[1:])
-        k = torch.empty(shape, dtype=dtype, device=self.device)     # (two views of one tensor take twice the host time)
-        v = torch.empty(shape, dtype=dtype, device=self.device)
+        if stream is None or self.device.type != "cuda":
+            k = torch.empty(shape, dtype=dtype, device=self.device)     # (two views of one tensor take twice the host time)
+            v = torch.empty(shape, dtype=dtype, device=self.device)
+        else:
+            # memory of the stream that writes it: a block of the current stream's may still be in use there
+            writer = torch.cuda.ExternalStream(N._stream(stream), device=self.device)
+            with torch.cuda.stream(writer):
+                k = torch.empty(shape, dtype=dtype, device=self.device)
+                v = torch.empty(shape, dtype=dtype, device=self.device)
+            for t in (k, v):                                            # the current stream will read them
+                t.record_stream(torch.cuda.current_stream(self.device))
         dims, cache = self._refs
         N._check(N.lib().gdn_kv4_read(dims, self.layers, n, None if start is None else start.data_ptr(), code,
                                       k.data_ptr(), v.data_ptr(), cache, N._stream_of(stream, self._index)))

@@ -117,6 +117,25 @@ def test_captured_steps_replay_after_larger_calls(n):
             assert int(c.seq_len[b]) == lens[b] + len(path) == lens[b] + int(acc.len[b])
 
 
+def test_read_on_a_side_stream_keeps_off_the_current_streams_memory():
+    """A block that the current stream has still to write to, freed just before the read: its next user is of that stream."""
+    rng = np.random.default_rng(44)
+    c, kr, vr = filled(rng, 4, 4, 256, [2000, 1500], 2, "bf16")
+    side = torch.cuda.Stream()
+    for handle in (side, side.cuda_stream):
+        torch.cuda.synchronize()
+        blocks = [torch.empty(2, 2, 2000, 4, 256, device="cuda") for _ in range(4)]       # of the size of k and of v
+        torch.cuda._sleep(40_000_000)                # ends by itself, about 20 ms
+        for x in blocks:
+            x.fill_(77.0)
+        del blocks, x
+        k, v = c.read(None, 2000, stream=handle)
+        side.synchronize()
+        torch.cuda.synchronize()
+        assert np.array_equal(f64(k), kr) and np.array_equal(f64(v), vr)
+    c.check_error()
+
+
 # ---- refusals between calls -----------------------------------------------------------------------------------------
 
 def test_a_refused_call_leaves_nothing_behind():
