@@ -322,7 +322,14 @@ class KV4Cache:
                                            N._stream_of(stream, self._index)))
 
     def check_error(self, stream=None):
-        N.gdn_check_error_words(self.err, stream)
+        """Waits for the stream and raises what the calls reported; every call can be made again after it."""
+        try:
+            N.gdn_check_error_words(self.err, stream)
+        except N.GdnError as e:
+            if e.status == N.GDN_ERR_TIMEOUT:       # CTAs that left early have not counted themselves
+                self.workspace.zero_()
+                _finish_fills(self.device)
+            raise
 
 
 class TreeAcceptor:

@@ -463,7 +463,9 @@ gdn_status gdn_kv4_read(const gdn_attn_dims* d, int32_t layers, int32_t n_rows, 
  *          It only limits how much of the GPU the call takes: a longer request is still
  *          correct.
  *   workspace  >= gdn_kv4_workspace_bytes(...) bytes of device memory, zeroed by
- *          the caller before its first use (its counters are zero after each call).
+ *          the caller before its first use and again after GDN_ERR_TIMEOUT (else its
+ *          counters are zero after each call: CTAs that start after another has timed
+ *          out leave at once, without counting themselves).
  *          One serves calls of any shape, one after another; calls that may overlap
  *          need one each
  * The products run on the tensor cores in fp16 with fp32 accumulation: codes times

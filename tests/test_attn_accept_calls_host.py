@@ -140,6 +140,17 @@ def test_row_strides_are_a_calls_own(R):
         assert (c.dims.q_row, c.dims.kv_row) == (0, 0)
 
 
+@pytest.mark.parametrize("status,zeroed", [(-6, True), (-9, False), (-10, False)])
+def test_workspace_is_zeroed_after_a_timeout(R, status, zeroed):
+    c = make_cache(R)
+    c.check_error(stream=0)
+    c.workspace[:] = 3
+    R.recorder.status = status
+    with pytest.raises(R.N.GdnError) as e:
+        c.check_error(stream=0)
+    assert e.value.status == status and bool((c.workspace == (0 if zeroed else 3)).all())
+
+
 # ---- sizes ----------------------------------------------------------------------------------------------------------
 
 def test_vocabularies_beyond_the_index_range_are_refused(R):

@@ -163,3 +163,27 @@ def test_a_refused_call_leaves_nothing_behind():
     c.append(kc, vc, one)
     c.check_error()
     assert int(c.seq_len[0]) == 91
+
+
+@pytest.mark.parametrize("n", [1, 6])
+def test_calls_after_a_timeout(n):
+    """The counters as a launch leaves them whose later CTAs saw the time-out flag: some have counted, some have not.
+    While the flag is set a call does nothing; once it has been reported the next call is right."""
+    from gated_deltanet_tree_gb300 import _native as N
+    rng = np.random.default_rng(45)
+    lens, trees = [3000, 1700], [S.random_tree(n, rng), S.random_tree(n, rng)]
+    c, kr, vr = filled(rng, 24, 4, 256, lens, 1, "bf16")
+    q, kn, vn = (rows(rng, 2, 1, n, h, 256, dtype="bf16") for h in (24, 4, 4))
+    out, sched = torch.full_like(q, 7.0), schedule(trees, n)
+    c.workspace[:65536].view(torch.int32)[:64:3] = 1
+    c.err[0] = 4                                     # GDN_DEVERR_TIMEOUT
+    c.attention(q, kn, vn, out, sched=sched)
+    assert (out == 7.0).all()
+    with pytest.raises(N.GdnError) as e:
+        c.check_error()
+    assert e.value.status == N.GDN_ERR_TIMEOUT
+    c.attention(q, kn, vn, out, sched=sched)
+    c.check_error()
+    ref = tree_reference(c, q, kr, vr, kn, vn, lens, trees)
+    for b in range(2):
+        check(f64(out[b, 0]), ref[b], max(float(vn.abs().max()), float(np.abs(vr).max())), "bf16", b)
