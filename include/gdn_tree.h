@@ -470,7 +470,7 @@ gdn_status gdn_kv4_read(const gdn_attn_dims* d, int32_t layers, int32_t n_rows, 
  *          need one each
  * The products run on the tensor cores in fp16 with fp32 accumulation: codes times
  * scales are exact in fp16, and q is scaled per row to fp16's range by a power of
- * two.  bf16 calls round the weights to fp16 (to 11 bits, or to 2^-26 of a row's
+ * two.  bf16 calls round the weights to fp16 (to 11 bits, or to 2^-31 of a row's
  * largest); fp32 calls split q and the weights in two fp16 terms each (22 bits).
  * GDN_ERR_UNSUPPORTED: layers * Hkv * ceil(n_max * Hq / Hkv / 8) above 16384.
  * ------------------------------------------------------------------------- */

@@ -8,7 +8,7 @@ import torch
 import synthetic as S
 from oracle import accept_oracle as A
 from oracle import kv4_oracle as K
-from test_gpu_attn_accept import built, check, f64, filled, i32, rows  # noqa: F401
+from test_gpu_attn_accept import DT, built, check, f64, filled, i32, rows  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -187,3 +187,45 @@ def test_calls_after_a_timeout(n):
     ref = tree_reference(c, q, kr, vr, kn, vn, lens, trees)
     for b in range(2):
         check(f64(out[b, 0]), ref[b], max(float(vn.abs().max()), float(np.abs(vr).max())), "bf16", b)
+
+
+# ---- long contexts --------------------------------------------------------------------------------------------------
+
+def one_and_many(Hq, D, B, T, gap, dtype, dominant, tail):
+    """B requests of T tokens: the first with score `gap` (nats), the others with score 0; their values (a number for
+    each half of the channels, exact in the cache) -> the output and the definition's, [.., 2 halves].  Every page but
+    the first is the same one of the pool."""
+    from gated_deltanet_tree_gb300 import runtime as R
+    dims = R.make_attn_dims(Hq, 1, D, dtype=DT[dtype], scale=1.0)
+    pool = torch.zeros(1, 2, 1, 72 * D, dtype=torch.uint8, device="cuda")
+    k = torch.zeros(1, 1, 128, 1, D, device="cuda")
+    k[0, 0, 0, 0, 0] = 1.0
+    v = torch.empty_like(k)
+    for i in range(2):
+        v[..., i * D // 2:(i + 1) * D // 2] = tail[i]
+        v[0, 0, 0, 0, i * D // 2:(i + 1) * D // 2] = dominant[i]
+    first = R.KV4Cache(dims, pool, i32([[0, 1]]), i32([0]))
+    first.append(k.to(DT[dtype]), v.to(DT[dtype]), i32([128]))
+    kr, vr = first.read(None, 128)
+    first.check_error()
+    assert torch.equal(kr, k) and torch.equal(vr, v)
+    table = torch.ones(B, -(-T // 64), dtype=torch.int32, device="cuda")
+    table[:, 0] = 0
+    c = R.KV4Cache(dims, pool, table, i32([T] * B))
+    q = torch.zeros(B, 1, 1, Hq, D, dtype=DT[dtype], device="cuda")
+    q[..., 0] = gap
+    assert float(q[0, 0, 0, 0, 0]) == gap
+    out = torch.zeros_like(q)
+    c.attention(q, None, None, out, max_len=T)
+    c.check_error()
+    w = (T - 1) * np.exp(-gap)
+    return f64(out).reshape(B, Hq, 2, D // 2), (np.array(dominant) + w * np.array(tail))[:, None] / (1.0 + w)
+
+
+@pytest.mark.parametrize("Hq,D,B", [(24, 256, 152), (24, 128, 152), (32, 64, 152), (8, 256, 304)])
+def test_small_weights_of_a_long_tail_add_up(Hq, D, B):
+    """A million tokens of weight 2^-27 each behind one of weight 1, every request in one CTA: 0.7% of the output."""
+    for gap in (18.75, 15.0):
+        out, ref = one_and_many(Hq, D, B, 1 << 20, gap, "bf16", (0.0, 1.0), (1.0, 0.0))
+        tol = 2.0 ** -8 * np.abs(ref) + 2.0 ** -10
+        assert (np.abs(out - ref) <= tol)[..., 0, :].all(), (gap, float(np.abs(out - ref)[..., 0, :].max()))
