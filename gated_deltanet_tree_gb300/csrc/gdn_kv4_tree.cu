@@ -47,6 +47,11 @@ constexpr int kStages = 3;
 // often (32 22-node trees 155 -> 160 us, 64-node trees over 200k tokens 513 -> 522); 2 and 13 gains nothing over these.
 constexpr float kLift = 6.f;
 constexpr float kSlack = 9.f;
+// Additions into the output in tensor memory truncate: 16 tokens at a time, each by up to 2^-23 of what is there, which
+// a million tokens behind one that dominates make 2^-7 of the output.  A segment is therefore taken in runs of pages,
+// joined in fp32 in the place of its partial result: 131072 tokens a run leave 2^-10, and cost a start and an end
+// (some 10 us of 2 ms).
+constexpr int kRun = 2048;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kTooLarge = 6.0e4f;   // new values beyond this take the fp32 path
 
@@ -240,8 +245,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tree_kernel(KvAttnParams
   int swaps = 0, decisions = 0;                     // exchanges between the two threads of a row, reference maxima so far
   int meets = 0;                                    // meetings of the softmax warps so far
   bool alive = true;
+  int done = 0;                                     // pages of the segment in its partial result, from runs before this one
   while (at < place.end && alive) {
-    const KvSegment it = kv_segment(p, kRows, at, place.end, where, &at);
+    long long next;
+    KvSegment it = kv_segment(p, kRows, at, place.end, where, &next);
+    const bool folded = done > 0, over = it.pages - done <= kRun;
+    it.page_lo += done;
+    it.pages = min(it.pages - done, kRun);
+    done = over ? 0 : done + kRun;
+    if (over) at = next;
     if (!it.r.ok) {
       if (tid == 0 && it.first) {
         device_error(p.c.err, it.r.n < 1 || it.r.n > p.n_max ? GDN_DEVERR_SCHEDULE : GDN_DEVERR_CACHE, it.b);
@@ -251,7 +263,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tree_kernel(KvAttnParams
       if (tid == 0 && !p.by_item) p.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
       continue;
     }
-    const bool with_new = it.first && p.k_new;
+    const bool with_new = it.first && over && p.k_new;
     const int psteps = (it.pages + Sm::kPages - 1) / Sm::kPages;
     const int steps = psteps + (with_new ? 1 : 0);        // the new rows last: a page sets better first references
     const int seg_toks = min(it.r.len - it.page_lo * kPage, it.pages * kPage);
@@ -459,8 +471,50 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tree_kernel(KvAttnParams
         }
       }
       if (busy) decisions += steps;
-      float* part = it.whole ? nullptr : kv_stream_part(p, blockIdx.x, it.start > place.at, kRows, D);
-      if (alive && busy) {
+      // (an item that the CTA holds whole has no partial result of its own, and its place is free)
+      float* slot = kv_stream_part(p, blockIdx.x, it.start > place.at, kRows, D);
+      float* part = it.whole ? nullptr : slot;
+      // channels x .. x + 3 of the row in a partial result (laid out as the staging tile)
+      auto partial = [&](int x) { return reinterpret_cast<float4*>(slot) + r * (D / 4) + ((x / 4) ^ (r & 7)); };
+      if (alive && busy && (folded || !over)) {
+        // one of several runs: this one's output and the earlier ones', in the place of the partial result, in terms of
+        // their common reference; back to tensor memory from the last run
+        float fo = 1.f, fs = 0.f;
+        if (folded) {
+          const float2 before = *reinterpret_cast<const float2*>(slot + kRows * D + 2 * r);
+          const float mn = fmaxf(m, before.x);
+          fo = m == -INFINITY ? 0.f : exp2f(m - mn);
+          fs = before.x == -INFINITY ? 0.f : exp2f(before.x - mn);
+          m = mn;
+          l = fmaf(l, fo, half == 0 ? before.y * fs : 0.f);
+        }
+#pragma unroll 1
+        for (int x = half * (D / 2); x < (half + 1) * (D / 2); x += 32) {
+          float o[32];
+          tmem_ld32(lanes + Sm::kO + x, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int y = 0; y < 32; y += 4) {
+            float4* at = partial(x + y);
+            if (folded) {
+              const float4 b = *at;
+              o[y] = fmaf(o[y], fo, b.x * fs);
+              o[y + 1] = fmaf(o[y + 1], fo, b.y * fs);
+              o[y + 2] = fmaf(o[y + 2], fo, b.z * fs);
+              o[y + 3] = fmaf(o[y + 3], fo, b.w * fs);
+            }
+            if (!over) *at = make_float4(o[y], o[y + 1], o[y + 2], o[y + 3]);
+          }
+          if (over) tmem_st32(lanes + Sm::kO + x, o);
+        }
+        if (over) {
+          tmem_wait_st();
+        } else {
+          l += exchange(l, &alive);                        // (both threads of the row have read the earlier sums before)
+          if (half == 0) *reinterpret_cast<float2*>(slot + kRows * D + 2 * r) = make_float2(m, l);
+        }
+      }
+      if (alive && busy && over) {
         const bool mine = r < rows;
         float f = 1.f;
         // the row's ancestors' weights, in the operands' space (every product has completed)
@@ -544,7 +598,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tree_kernel(KvAttnParams
               }
             }
             if (mine && part) {
-              *(reinterpret_cast<float4*>(part) + r * (D / 4) + ((x / 4) ^ (r & 7))) = make_float4(o[0], o[1], o[2], o[3]);
+              *partial(x) = make_float4(o[0], o[1], o[2], o[3]);
             } else if (mine) {
               *reinterpret_cast<__nv_bfloat162*>(out + x) = __floats2bfloat162_rn(o[0] * inv, o[1] * inv);
               *reinterpret_cast<__nv_bfloat162*>(out + x + 2) = __floats2bfloat162_rn(o[2] * inv, o[3] * inv);
@@ -554,7 +608,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tree_kernel(KvAttnParams
         }
         if (part && mine && half == 0) *reinterpret_cast<float2*>(part + kRows * D + 2 * r) = make_float2(m, l);
       }
-      if (steps > 0 && alive && !own) {
+      if (steps > 0 && alive && over && !own) {
         // from the staging tile to global memory, whole rows at a time
         if (part) fence_proxy_async();
         alive = meet();

@@ -229,3 +229,54 @@ def test_small_weights_of_a_long_tail_add_up(Hq, D, B):
         out, ref = one_and_many(Hq, D, B, 1 << 20, gap, "bf16", (0.0, 1.0), (1.0, 0.0))
         tol = 2.0 ** -8 * np.abs(ref) + 2.0 ** -10
         assert (np.abs(out - ref) <= tol)[..., 0, :].all(), (gap, float(np.abs(out - ref)[..., 0, :].max()))
+
+
+@pytest.mark.parametrize("Hq,D,B", [(24, 256, 152), (24, 128, 152), (32, 64, 152), (8, 256, 304)])
+def test_a_long_tail_adds_to_a_dominating_value(Hq, D, B):
+    """The same with one value everywhere, and with opposite ones: additions to a large sum, a million of them."""
+    for gap in (18.75, 15.0):
+        out, ref = one_and_many(Hq, D, B, 1 << 20, gap, "bf16", (1.0, 1.0), (1.0, -1.0))
+        tol = 2.0 ** -8 * np.abs(ref) + 2.0 ** -10
+        assert (np.abs(out - ref) <= tol).all(), (gap, [float(np.abs(out - ref)[..., i, :].max()) for i in range(2)])
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,n", [(24, 4, 256, 3), (24, 4, 128, 4), (32, 4, 64, 5), (24, 4, 256, 22)])
+def test_attention_runs_of_pages(Hq, Hkv, D, n):
+    """Requests so long that a CTA takes thousands of an item's pages, whole items and parts of them, with new rows (some
+    not finite) at the end: against the definition in 64 bits.  The pages' numbers repeat, in random order."""
+    from gated_deltanet_tree_gb300 import runtime as R
+    rng = np.random.default_rng(D + n)
+    pages = 60
+    small, kr, vr = filled(rng, Hq, Hkv, D, [64 * pages], 1, "bf16")
+    lens = [300001] * 30 + [131072, 131073, 262144, 262145, 270000, 5, 0, 64, 140000, 290017]
+    if n > 16:
+        lens = lens[12:]                          # (two tiles of rows a head)
+    B, pages_max = len(lens), -(-max(lens) // 64)
+    pick = torch.from_numpy(rng.integers(0, pages, (B, pages_max)).astype(np.int32)).cuda()
+    table = small.page_table[0][pick.long()].contiguous()
+    c = R.KV4Cache(small.dims, small.pool, table, i32(lens))
+    trees = [S.random_tree(n, rng) for _ in range(B)]
+    q = (1.5 * rows(rng, B, 1, n, Hq, D, dtype="f32")).bfloat16()
+    kn, vn = rows(rng, B, 1, n, Hkv, D, dtype="bf16"), rows(rng, B, 1, n, Hkv, D, dtype="bf16")
+    vmax = max(float(vn.abs().max()), float(np.abs(vr).max()))
+    kn[1, 0, n - 1], vn[4, 0, n - 2] = float("nan"), float("inf")
+    out = torch.full_like(q, 7.0)
+    for _ in range(2):
+        c.attention(q, kn, vn, out, sched=schedule(trees, n), max_len=max(lens))
+    c.check_error()
+    kr, vr = torch.from_numpy(kr[0, 0]).cuda(), torch.from_numpy(vr[0, 0]).cuda()
+    G = Hq // Hkv
+    for b in (0, 1, 4, B - 10, B - 9, B - 8, B - 7, B - 6, B - 5, B - 4, B - 2, B - 1):
+        at = (64 * pick[b].long()[:, None] + torch.arange(64, device="cuda")).flatten()[:lens[b]]
+        for h in range(Hkv):
+            k, v = kr[at, h], vr[at, h]
+            for i in range(n):
+                line = K.root_path(trees[b], i)
+                qi = q[b, 0, i, h * G:(h + 1) * G].double()
+                w = torch.cat([qi @ k.T, qi @ kn[b, 0, line, h].double().T], -1) * c.dims.scale
+                w = torch.softmax(w, -1)
+                ref = w[:, :lens[b]] @ v + w[:, lens[b]:] @ vn[b, 0, line, h].double()
+                got, ref = f64(out[b, 0, i, h * G:(h + 1) * G]), f64(ref)
+                far = np.isinf(ref)
+                assert np.array_equal(got[far], ref[far])
+                check(np.where(far, 0.0, got), np.where(far, 0.0, ref), vmax, "bf16", (b, h, i))
