@@ -22,8 +22,9 @@
 // smallest value and none passes its largest.
 //
 // fp32 calls run the same products on values split in two fp16 terms each: q = hi +
-// lo and the weights likewise keep 22 bits, the unpacked codes are exact as they
-// are, and a product costs two MMAs instead of one.  An MMA's additions truncate, so
+// lo keeps 22 bits of a row's largest, hi + 2^-12 lo 22 bits of a weight, or 2^-43 of the
+// largest one, the unpacked codes are exact as they are, and a product costs two MMAs
+// instead of one.  An MMA's additions truncate, so
 // its sums are kept short -- 16 channels of a score, 32 tokens of an output -- and
 // added in fp32 outside: 24 query heads of 256 over 50000 tokens have a relative
 // error of 9e-7 that way (3.7e-6 with the sums left in the MMAs), for a tenth of the
@@ -47,6 +48,9 @@ constexpr int kWarpsOf = D == 256 ? 6 : 8;
 constexpr int kRows = kKvDecRows;
 constexpr float kLift = 6.f;          // weights are scaled by 2^kLift ...
 constexpr float kSlack = 8.f;         // ... against a maximum that may lag by up to 2^kSlack: 2^14 at most in fp16
+// (fp32) the low terms of the weights, at most 2^2, are scaled by this: unscaled, fp16's smallest value would cut them
+// off at 2^-31 of the reference, which 200,000 tokens behind one that dominates make 9e-5 of the output.
+constexpr float kLowScale = 4096.f;
 constexpr float kLog2e = 1.4426950408889634f;
 
 template <int D, typename T>
@@ -381,7 +385,7 @@ __global__ void __launch_bounds__(32 * kWarpsOf<D>, 2) kv4_attn_dec_kernel(KvAtt
             pf[0][u][x] = transpose8x8(h2u(hi));
             if constexpr (kTerms == 2)
               pf[1][u][x] = transpose8x8(
-                  h2u(__floats2half2_rn(s[u][2 * x] - __low2float(hi), s[u][2 * x + 1] - __high2float(hi))));
+                  h2u(__floats2half2_rn((s[u][2 * x] - __low2float(hi)) * kLowScale, (s[u][2 * x + 1] - __high2float(hi)) * kLowScale)));
           }
         }
         // ---- O^T: tile (gg, x) holds channel 32 gg + 4 m8 + 2x in rows 0-7 and the next one in rows 8-15; step u
@@ -401,7 +405,8 @@ __global__ void __launch_bounds__(32 * kWarpsOf<D>, 2) kv4_attn_dec_kernel(KvAtt
             }
           }
           const uint32_t ww[4] = {wv.x, wv.y, wv.z, wv.w};
-          float page[2][4] = {};                  // fp32 calls: these tokens' product, summed outside like the scores'
+          // fp32 calls: these tokens' products with the two terms of the weights, summed outside like the scores'
+          float page[2][4] = {}, low[2][4] = {};
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
             const __half2 e0 = u2h(dd[2 * u]), e1 = u2h(dd[2 * u + 1]);
@@ -413,7 +418,7 @@ __global__ void __launch_bounds__(32 * kWarpsOf<D>, 2) kv4_attn_dec_kernel(KvAtt
               if constexpr (kTerms == 1) {
                 mma16816(o[gg][x], f0, f1, f2, f3, pf[0][u][0], pf[0][u][1]);
               } else {
-                mma16816(page[x], f0, f1, f2, f3, pf[kTerms - 1][u][0], pf[kTerms - 1][u][1]);
+                mma16816(low[x], f0, f1, f2, f3, pf[kTerms - 1][u][0], pf[kTerms - 1][u][1]);
                 mma16816(page[x], f0, f1, f2, f3, pf[0][u][0], pf[0][u][1]);
               }
             }
@@ -422,7 +427,7 @@ __global__ void __launch_bounds__(32 * kWarpsOf<D>, 2) kv4_attn_dec_kernel(KvAtt
 #pragma unroll
             for (int x = 0; x < 2; ++x)
 #pragma unroll
-              for (int y = 0; y < 4; ++y) o[gg][x][y] += page[x][y];
+              for (int y = 0; y < 4; ++y) o[gg][x][y] += fmaf(low[x][y], 1.f / kLowScale, page[x][y]);
           }
         }
       }

@@ -471,7 +471,8 @@ gdn_status gdn_kv4_read(const gdn_attn_dims* d, int32_t layers, int32_t n_rows, 
  * The products run on the tensor cores in fp16 with fp32 accumulation: codes times
  * scales are exact in fp16, and q is scaled per row to fp16's range by a power of
  * two.  bf16 calls round the weights to fp16 (to 11 bits, or to 2^-31 of a row's
- * largest); fp32 calls split q and the weights in two fp16 terms each (22 bits).
+ * largest); fp32 calls split q and the weights in two fp16 terms each, which keep 22
+ * bits of a row's largest q and 22 bits of a weight, or 2^-43 of the largest weight.
  * GDN_ERR_UNSUPPORTED: layers * Hkv * ceil(n_max * Hq / Hkv / 8) above 16384.
  * ------------------------------------------------------------------------- */
 size_t gdn_kv4_workspace_bytes(const gdn_attn_dims* d, int32_t B, int32_t layers, int32_t n_max, int32_t max_len);

@@ -231,6 +231,14 @@ def test_small_weights_of_a_long_tail_add_up(Hq, D, B):
         assert (np.abs(out - ref) <= tol)[..., 0, :].all(), (gap, float(np.abs(out - ref)[..., 0, :].max()))
 
 
+@pytest.mark.parametrize("Hq,D,B", [(8, 256, 152), (8, 128, 304), (8, 64, 304)])
+def test_small_weights_of_a_long_tail_add_up_in_fp32(Hq, D, B):
+    """The same in fp32, down to 2^-31 a token, with fp32's tolerance."""
+    for gap in (21.75, 18.75, 15.0):
+        out, ref = one_and_many(Hq, D, B, 1 << 20, gap, "f32", (0.0, 1.0), (1.0, 0.0))
+        assert (np.abs(out - ref) <= 3e-5)[..., 0, :].all(), (gap, float(np.abs(out - ref)[..., 0, :].max()))
+
+
 @pytest.mark.parametrize("Hq,D,B", [(24, 256, 152), (24, 128, 152), (32, 64, 152), (8, 256, 304)])
 def test_a_long_tail_adds_to_a_dominating_value(Hq, D, B):
     """The same with one value everywhere, and with opposite ones: additions to a large sum, a million of them."""
