@@ -51,6 +51,12 @@ constexpr float kSlack = 8.f;         // ... against a maximum that may lag by u
 // (fp32) the low terms of the weights, at most 2^2, are scaled by this: unscaled, fp16's smallest value would cut them
 // off at 2^-31 of the reference, which 200,000 tokens behind one that dominates make 9e-5 of the output.
 constexpr float kLowScale = 4096.f;
+// Pages that are added to one output and one sum: a segment is taken in runs, joined in the place of its partial result.
+// fp32 sums lose up to 2^-24 an addition, one a page in each pair of warps, behind a token that dominates: 2e-5 of the
+// output at 1024 pages (1.5e-4 over a million tokens at once).  The MMAs of bf16 calls truncate, 2^-23 an addition and two
+// a page: 2^-13 at 2048.
+template <typename T>
+constexpr int kRun = sizeof(T) == 4 ? 1024 : 2048;
 constexpr float kLog2e = 1.4426950408889634f;
 
 template <int D, typename T>
@@ -139,9 +145,16 @@ __global__ void __launch_bounds__(32 * kWarpsOf<D>, 2) kv4_attn_dec_kernel(KvAtt
   int n_joins = 0;
   int used = 0;          // pages this pair has put through its stages: stage used % kStages, phase used / kStages
   bool alive = true;
+  int done = 0;          // pages of the segment in its partial result, from runs before this one
 
   while (at < end) {
-    const KvSegment it = kv_segment(p, kRows, at, end, where, &at);
+    long long next;
+    KvSegment it = kv_segment(p, kRows, at, end, where, &next);
+    const bool folded = done > 0, over = it.pages - done <= kRun<T>;
+    it.page_lo += done;
+    it.pages = min(it.pages - done, kRun<T>);
+    done = over ? 0 : done + kRun<T>;
+    if (over) at = next;
     if (!it.r.ok) {
       if (tid == 0 && it.first)
         device_error(p.c.err, it.r.n < 1 || it.r.n > p.n_max ? GDN_DEVERR_SCHEDULE : GDN_DEVERR_CACHE, it.b);
@@ -189,7 +202,7 @@ __global__ void __launch_bounds__(32 * kWarpsOf<D>, 2) kv4_attn_dec_kernel(KvAtt
       }
     }
 
-    const bool with_new = it.first && p.k_new;
+    const bool with_new = it.first && over && p.k_new;
     if (with_new && lane == 0)      // the nodes' own rows are wanted last, from nearby
       for (int t = warp; t < it.r.n; t += kWarps) {
         const size_t row = (node0 + t) * p.kv_row + static_cast<size_t>(it.h) * D;
@@ -377,8 +390,6 @@ __global__ void __launch_bounds__(32 * kWarpsOf<D>, 2) kv4_attn_dec_kernel(KvAtt
         for (int u = 0; u < 2; ++u) {
 #pragma unroll
           for (int x = 0; x < 4; ++x) s[u][x] = exp2_fast(s[u][x] + ((x & 1) ? r1 : r0));
-          l0 += s[u][0] + s[u][2];
-          l1 += s[u][1] + s[u][3];
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             const __half2 hi = __floats2half2_rn(s[u][2 * x], s[u][2 * x + 1]);
@@ -388,6 +399,8 @@ __global__ void __launch_bounds__(32 * kWarpsOf<D>, 2) kv4_attn_dec_kernel(KvAtt
                   h2u(__floats2half2_rn((s[u][2 * x] - __low2float(hi)) * kLowScale, (s[u][2 * x + 1] - __high2float(hi)) * kLowScale)));
           }
         }
+        l0 += (s[0][0] + s[0][2]) + (s[1][0] + s[1][2]);
+        l1 += (s[0][1] + s[0][3]) + (s[1][1] + s[1][3]);
         // ---- O^T: tile (gg, x) holds channel 32 gg + 4 m8 + 2x in rows 0-7 and the next one in rows 8-15; step u
         // takes tokens 8j + 4u .. + 3 of the 32
         const uint4* vw = reinterpret_cast<const uint4*>(blk + Blk::kValCodes) + kb * D;
@@ -466,7 +479,9 @@ __global__ void __launch_bounds__(32 * kWarpsOf<D>, 2) kv4_attn_dec_kernel(KvAtt
       const int x = row0 + r;
       return out + (node0 + x / p.G) * (static_cast<size_t>(p.Hq) * D) + static_cast<size_t>(it.h * p.G + x % p.G) * D;
     };
-    float* part = it.whole ? nullptr : kv_stream_part(p, cta, it.start > begin, kRows, D);
+    // (an item that the CTA holds whole has no partial result of its own, and its place is free)
+    float* slot = kv_stream_part(p, cta, it.start > begin, kRows, D);
+    float* part = it.whole && over ? nullptr : slot;
     for (int r = warp; r < rows; r += kWarps) {
       float m = -INFINITY;
 #pragma unroll
@@ -486,6 +501,20 @@ __global__ void __launch_bounds__(32 * kWarpsOf<D>, 2) kv4_attn_dec_kernel(KvAtt
           acc[2 * i] = fmaf(f, v.x, acc[2 * i]);
           acc[2 * i + 1] = fmaf(f, v.y, acc[2 * i + 1]);
         }
+      }
+      if (folded) {                      // (a warp's own rows, written by the same lanes)
+        const float2 before = *reinterpret_cast<const float2*>(slot + kRows * D + 2 * r);
+        const float mn = fmaxf(m, before.x);
+        const float fo = m == -INFINITY ? 0.f : exp2f(m - mn), fs = before.x == -INFINITY ? 0.f : exp2f(before.x - mn);
+        m = mn;
+        l = fmaf(l, fo, before.y * fs);
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i) {
+          const float2 v = *reinterpret_cast<const float2*>(slot + r * D + 64 * i + 2 * lane);
+          acc[2 * i] = fmaf(acc[2 * i], fo, v.x * fs);
+          acc[2 * i + 1] = fmaf(acc[2 * i + 1], fo, v.y * fs);
+        }
+        __syncwarp();                    // read by all lanes before one writes the sums
       }
       if (with_new) {
         // the row's own ancestors, one at a time in fp32: what it does not see is not read
@@ -533,7 +562,7 @@ __global__ void __launch_bounds__(32 * kWarpsOf<D>, 2) kv4_attn_dec_kernel(KvAtt
           store2(out_row(r) + 64 * i + 2 * lane, acc[2 * i] * inv, acc[2 * i + 1] * inv);
       }
     }
-    if (part) {
+    if (over && !it.whole) {
       const int c0 = kv_cta_of(it.start, total, ctas), c1 = kv_cta_of(it.start + it.r.units - 1, total, ctas);
       if (kv_last(p, it.item, c1 - c0 + 1, &last)) {     // joined after the loop: at most two
         if (tid == 0)

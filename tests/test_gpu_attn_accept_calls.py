@@ -248,26 +248,43 @@ def test_a_long_tail_adds_to_a_dominating_value(Hq, D, B):
         assert (np.abs(out - ref) <= tol).all(), (gap, [float(np.abs(out - ref)[..., i, :].max()) for i in range(2)])
 
 
+LONG = [300001] * 30 + [131072, 131073, 262144, 262145, 270000, 5, 0, 64, 140000, 290017]
+
+
+@pytest.mark.parametrize("Hq,D,B", [(8, 256, 152), (8, 128, 304), (8, 64, 304)])
+def test_a_long_tail_adds_to_a_dominating_value_in_fp32(Hq, D, B):
+    for gap in (21.75, 18.75, 15.0):
+        out, ref = one_and_many(Hq, D, B, 1 << 20, gap, "f32", (1.0, 1.0), (1.0, -1.0))
+        assert (np.abs(out - ref) <= 3e-5).all(), (gap, [float(np.abs(out - ref)[..., i, :].max()) for i in range(2)])
+
+
 @pytest.mark.parametrize("Hq,Hkv,D,n", [(24, 4, 256, 3), (24, 4, 128, 4), (32, 4, 64, 5), (24, 4, 256, 22)])
 def test_attention_runs_of_pages(Hq, Hkv, D, n):
     """Requests so long that a CTA takes thousands of an item's pages, whole items and parts of them, with new rows (some
     not finite) at the end: against the definition in 64 bits.  The pages' numbers repeat, in random order."""
+    runs_of_pages(Hq, Hkv, D, n, "bf16", LONG[12:] if n > 16 else LONG)       # (22 nodes: two tiles of rows a head)
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,n,dtype", [(24, 4, 256, 1, "bf16"), (8, 4, 128, 2, "bf16"), (8, 4, 64, 4, "bf16"),
+                                              (24, 4, 256, 2, "f32"), (8, 4, 128, 2, "f32"), (8, 4, 64, 5, "f32")])
+def test_attention_runs_of_pages_few_rows(Hq, Hkv, D, n, dtype):
+    runs_of_pages(Hq, Hkv, D, n, dtype, [300001] * 40 + LONG)
+
+
+def runs_of_pages(Hq, Hkv, D, n, dtype, lens):
     from gated_deltanet_tree_gb300 import runtime as R
     rng = np.random.default_rng(D + n)
     pages = 60
-    small, kr, vr = filled(rng, Hq, Hkv, D, [64 * pages], 1, "bf16")
-    lens = [300001] * 30 + [131072, 131073, 262144, 262145, 270000, 5, 0, 64, 140000, 290017]
-    if n > 16:
-        lens = lens[12:]                          # (two tiles of rows a head)
+    small, kr, vr = filled(rng, Hq, Hkv, D, [64 * pages], 1, dtype)
     B, pages_max = len(lens), -(-max(lens) // 64)
     pick = torch.from_numpy(rng.integers(0, pages, (B, pages_max)).astype(np.int32)).cuda()
     table = small.page_table[0][pick.long()].contiguous()
     c = R.KV4Cache(small.dims, small.pool, table, i32(lens))
     trees = [S.random_tree(n, rng) for _ in range(B)]
-    q = (1.5 * rows(rng, B, 1, n, Hq, D, dtype="f32")).bfloat16()
-    kn, vn = rows(rng, B, 1, n, Hkv, D, dtype="bf16"), rows(rng, B, 1, n, Hkv, D, dtype="bf16")
+    q = (1.5 * rows(rng, B, 1, n, Hq, D, dtype="f32")).to(DT[dtype])
+    kn, vn = rows(rng, B, 1, n, Hkv, D, dtype=dtype), rows(rng, B, 1, n, Hkv, D, dtype=dtype)
     vmax = max(float(vn.abs().max()), float(np.abs(vr).max()))
-    kn[1, 0, n - 1], vn[4, 0, n - 2] = float("nan"), float("inf")
+    kn[1, 0, n - 1], vn[4, 0, max(0, n - 2)] = float("nan"), float("inf")
     out = torch.full_like(q, 7.0)
     for _ in range(2):
         c.attention(q, kn, vn, out, sched=schedule(trees, n), max_len=max(lens))
@@ -287,4 +304,4 @@ def test_attention_runs_of_pages(Hq, Hkv, D, n):
                 got, ref = f64(out[b, 0, i, h * G:(h + 1) * G]), f64(ref)
                 far = np.isinf(ref)
                 assert np.array_equal(got[far], ref[far])
-                check(np.where(far, 0.0, got), np.where(far, 0.0, ref), vmax, "bf16", (b, h, i))
+                check(np.where(far, 0.0, got), np.where(far, 0.0, ref), vmax, dtype, (b, h, i))
