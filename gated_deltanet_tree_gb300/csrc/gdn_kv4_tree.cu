@@ -21,9 +21,9 @@
 // The nodes' own rows are one more step of an item, the last; their values are
 // fetched while the pages go by.  They are fp16 like the rest, each key row scaled
 // to fp16's range by a power of two, the row's ancestors as its mask.  A masked weight is 0, which would still turn a NaN or an infinity
-// in an unseen row into NaN inside a product; if any such value (or one beyond
-// fp16) is among the rows, that step is left out of the products and each row adds
-// its own ancestors in fp32 at the end.
+// in an unseen row into NaN inside a product; if any such value (or one outside
+// fp16's range) is among the rows, that step is left out of the products and each row
+// adds its own ancestors in fp32 at the end.
 //
 // Measured: trees of 64 and 48 nodes over 200001 and 150001 tokens (three tiles each),
 // 24 query and 4 kv heads of 256: 480 to 511 us from run to run, 0.94 to 1.0 PFLOP/s of
@@ -53,7 +53,8 @@ constexpr float kSlack = 9.f;
 // (some 10 us of 2 ms).
 constexpr int kRun = 2048;
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kTooLarge = 6.0e4f;   // new values beyond this take the fp32 path
+constexpr float kTooLarge = 6.0e4f;   // new values beyond this take the fp32 path,
+constexpr float kTooSmall = 0x1p-12f; // as do those that fp16 rounds (below 2^-17) where eight nodes' channel has none this large
 
 // kScored: scores written, which also frees the key operand; kAdded: product added to the output, which also frees the
 // value operand (a commit costs the issuing thread some two hundred cycles, so there is one for each)
@@ -753,6 +754,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tree_kernel(KvAttnParams
               uint32_t w[4] = {0, 0, 0, 0};
               if (8 * o < it.r.n) {
                 float y[8], sum = 0.f, big = 0.f;
+                bool cut = false;
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                   const int t = 8 * o + e;
@@ -760,8 +762,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tree_kernel(KvAttnParams
                   y[e] = t < it.r.n ? __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(at)) : 0.f;
                   sum = fmaf(0.f, y[e], sum);
                   big = fmaxf(big, fabsf(y[e]));
+                  cut = cut || __half2float(__float2half_rn(y[e])) != y[e];
                 }
-                const bool bad = sum != 0.f || big > kTooLarge;
+                const bool bad = sum != 0.f || big > kTooLarge || (cut && big < kTooSmall);
                 strange = strange || bad;
 #pragma unroll
                 for (int z = 0; z < 4; ++z) w[z] = bad ? 0u : h2u(__floats2half2_rn(y[2 * z], y[2 * z + 1]));

@@ -473,6 +473,9 @@ gdn_status gdn_kv4_read(const gdn_attn_dims* d, int32_t layers, int32_t n_rows, 
  * two.  bf16 calls round the weights to fp16 (to 11 bits, or to 2^-31 of a row's
  * largest); fp32 calls split q and the weights in two fp16 terms each, which keep 22
  * bits of a row's largest q and 22 bits of a weight, or 2^-43 of the largest weight.
+ * Many bf16 rows' k_new and v_new enter in fp16 too, k_new scaled per row like q; v_new
+ * values below 2^-17 keep 2^-25 where one of the same channel and eight nodes is 2^-12
+ * or larger, and all their bits where none is.
  * GDN_ERR_UNSUPPORTED: layers * Hkv * ceil(n_max * Hq / Hkv / 8) above 16384.
  * ------------------------------------------------------------------------- */
 size_t gdn_kv4_workspace_bytes(const gdn_attn_dims* d, int32_t B, int32_t layers, int32_t n_max, int32_t max_len);

@@ -8,7 +8,7 @@ import torch
 import synthetic as S
 from oracle import accept_oracle as A
 from oracle import kv4_oracle as K
-from test_gpu_attn_accept import DT, built, check, f64, filled, i32, rows  # noqa: F401
+from test_gpu_attn_accept import DT, built, check, f64, filled, i32, make_cache, rows  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -187,6 +187,29 @@ def test_calls_after_a_timeout(n):
     ref = tree_reference(c, q, kr, vr, kn, vn, lens, trees)
     for b in range(2):
         check(f64(out[b, 0]), ref[b], max(float(vn.abs().max()), float(np.abs(vr).max())), "bf16", b)
+
+
+# ---- values at fp16's lower end -------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("Hq,Hkv,D", [(24, 4, 256), (32, 4, 128), (32, 4, 64)])
+@pytest.mark.parametrize("size", [1e-4, 1e-6, 1e-9, 1e-30])
+def test_small_new_values_keep_their_bits(Hq, Hkv, D, size):
+    """Values that are small throughout, with and without cached ones (of the same size, as the cache reads back)."""
+    rng = np.random.default_rng(D)
+    n, lens = 22, [0, 90, 0]
+    c = make_cache(Hq, Hkv, D, 3, 1, 2, "bf16")
+    k, v = rows(rng, 3, 1, 90, Hkv, D, dtype="bf16"), rows(rng, 3, 1, 90, Hkv, D, dtype="bf16")
+    c.append(k, (size * v.float()).bfloat16(), i32(lens))
+    kr, vr = (f64(t) for t in c.read(None, 90))
+    trees = [S.random_tree(m, rng) for m in (22, 17, 9)]
+    q, kn = rows(rng, 3, 1, n, Hq, D, dtype="bf16"), rows(rng, 3, 1, n, Hkv, D, dtype="bf16")
+    vn = (size * rows(rng, 3, 1, n, Hkv, D, dtype="f32")).bfloat16()
+    out = torch.zeros_like(q)
+    c.attention(q, kn, vn, out, sched=schedule(trees, n))
+    c.check_error()
+    ref = tree_reference(c, q, kr, vr, kn, vn, lens, trees)
+    for b, t in enumerate(trees):
+        check(f64(out[b, 0, :len(t)]), ref[b], float(vn.abs().max()), "bf16", b)
 
 
 # ---- long contexts --------------------------------------------------------------------------------------------------
