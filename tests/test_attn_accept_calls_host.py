@@ -184,3 +184,16 @@ def test_one_workspace_serves_every_call(R, Hq, Hkv, D, dtype):
         assert args[10] >= N.gdn_kv4_workspace_bytes(c.dims, 2, 2, n, max_len) > 0
     assert vars(c).keys() == kept.keys() and all(vars(c)[x] is kept[x] for x in kept)
     assert not any(isinstance(x, dict) for x in kept.values())
+
+
+def test_kernel_choice_is_at_the_measured_crossings(R):
+    """Few rows a kv head leave partial results of 8 rows, 304 CTAs; more rows of 128 rows, 152 CTAs."""
+    from gated_deltanet_tree_gb300 import _native as N
+    records = 16384 * 4 + 4096 * 16
+    for D, most in ((256, 16), (128, 20), (64, 28)):
+        for rows in range(1, 65):
+            few = records + 304 * 2 * 8 * (D + 2) * 4
+            many = records + 152 * 2 * 128 * (D + 2) * 4
+            got = N.gdn_kv4_workspace_bytes(R.make_attn_dims(2, 2, D), 2, 1, rows, 0)
+            assert got == (few if rows <= most else many), (D, rows)
+            assert N.gdn_kv4_workspace_bytes(R.make_attn_dims(2, 2, D, dtype=torch.float32), 2, 1, rows, 0) == few
