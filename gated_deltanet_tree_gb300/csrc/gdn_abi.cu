@@ -528,7 +528,7 @@ gdn_status gdn_kv4_attention(const gdn_attn_dims* d, int32_t layers, const gdn_b
 
 size_t gdn_accept_workspace_bytes(int32_t B, int32_t n_max, int32_t V) {
   if (B < 1 || n_max < 1 || n_max > GDN_MAX_NODES || V < 1 || V > gdn::kMaxVocab) return 0;
-  return round_up(static_cast<size_t>(B) * n_max * gdn::accept_slices(B, n_max, V) * 16 + 1, kAlign);
+  return round_up(static_cast<size_t>(B) * n_max * gdn::accept_slices(B, n_max, V, true) * 16 + 1, kAlign);
 }
 
 gdn_status gdn_tree_accept(const gdn_batch_schedule* sched, int32_t V, int32_t v_stride, int32_t logits_dtype,
@@ -567,7 +567,7 @@ gdn_status gdn_tree_accept(const gdn_batch_schedule* sched, int32_t V, int32_t v
   p.words = sched->words; p.logits = logits; p.tokens = tokens; p.draft = draft_probs;
   p.uniform = uniform; p.gumbel = gumbel; p.temperature = temperature;
   p.path = path; p.len = len; p.next = next; p.err = err;
-  p.n_slices = gdn::accept_slices(sched->B, sched->n_max, V);
+  p.n_slices = gdn::accept_slices(sched->B, sched->n_max, V, draft_probs != nullptr);
   p.slices = workspace;
   cudaError_t e = gdn::launch_accept(p, stream);
   if (e != cudaSuccess) return cuda_fail(e, "acceptance launch");

@@ -10,13 +10,23 @@
 //  - along the walk: a request's cluster reads the rows on its path, one after
 //    another.  Few bytes, but every step waits for a row's latency and a cluster
 //    barrier.
-// The first is taken while all rows are few (kRowsAtOnceBytes).  Measured, at once
-// against along the walk: 64 chains of 9 rows of 65537 fp32 entries (counted as
-// 75 MB) 61 us against 69; 32 trees of 22 rows of 131072 bf16 entries (184 MB) 60 us
-// against 39; one such tree whose path is one node about 15 us either way, most of
-// it launches.  The walk of the 32 trees reads 44 MB in 39 us (1.1 TB/s): its bound is
-// the latency of the steps, not the bytes.  The rows' reduction reads its 151 MB at
-// 4.5 TB/s.
+// The first is taken while all rows are few (kRowsAtOnce entries, twice as many with
+// draft probabilities, where the walk's steps cost more).  Its time goes with the
+// entries, of either type; the walk's with the nodes it visits, which nothing knows
+// beforehand.  Measured (us, at once : along the walk, by nodes visited):
+//   B x n x V                  M entries   1          3          6          9
+//   4 x 22 x 131072, bf16        12     19 : 15    19 : 19    21 : 26    23 : 33
+//   8 x 22 x 131072              23     23 : 15    24 : 19    25 : 26    27 : 33
+//   12 x 22 x 131072             35     27 : 15    27 : 19    29 : 27    31 : 33
+//   24 x 22 x 131072             69     47 : 17    47 : 23    49 : 33    50 : 43
+//   64 x 22 x 32000              45     37 : 19    38 : 29    41 : 42    44 : 56
+//   chains of 9 with draft probabilities, fp32 (visited   1.7       3.5       6.5       7.5)
+//   32 x 9 x 65537               19     27 : 23    27 : 31    29 : 35    29 : 39
+//   96 x 9 x 65537               57     83 : 60    87 : 83    90 : 110   92 : 125
+// The limits lie where a walk of six nodes costs the same.  The walk of 32 trees of 22
+// such rows, 2.5 of them visited on average, reads 44 MB in 44 us (1.0 TB/s): its bound
+// is the latency of the steps, not the bytes.  The reduction of 64 chains' rows reads
+// its 151 MB at 4.5 TB/s.
 //
 // One thread-block cluster walks one request.  Its CTAs share each row they read by
 // slices and exchange their partial results through distributed shared memory;
@@ -40,6 +50,7 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kMaxCluster = 8;
 constexpr int kRowThreads = 256;
+constexpr double kRowsAtOnce = 1 << 25;      // entries
 constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ float to_f(float x) { return x; }
@@ -489,9 +500,9 @@ cudaError_t accept_t(const AcceptParams& p, cudaStream_t s) {
 }  // namespace
 
 // All rows at once while they are few; slices of 8192 entries, which a CTA of the rows' kernel reads in one go.
-int accept_slices(int B, int n_max, int V) {
-  const double bytes = 2.0 * B * n_max * V;       // (of bf16 rows)
-  if (n_max < 2 || bytes > kRowsAtOnceBytes || static_cast<long long>(B) * n_max > 65535) return 0;
+int accept_slices(int B, int n_max, int V, bool draft) {
+  const double entries = static_cast<double>(B) * n_max * V;
+  if (n_max < 2 || entries > (draft ? 2.0 : 1.0) * kRowsAtOnce || static_cast<long long>(B) * n_max > 65535) return 0;
   return (V + 8191) / 8192;
 }
 

@@ -22,8 +22,9 @@ struct AcceptParams {
   void* slices;                // [B][n_max][n_slices] partial results of 16 bytes (workspace)
 };
 constexpr int kMaxVocab = 1 << 30;   // the kernels' indices pass V by up to a cluster's step of 2^15 before they are compared with it
-constexpr double kRowsAtOnceBytes = 128.0 * (1 << 20);
-int accept_slices(int B, int n_max, int V);
+// Slices of a row where all rows are reduced at once, 0 where the walk reads the ones on its path; the most a call needs
+// is with draft probabilities.
+int accept_slices(int B, int n_max, int V, bool draft);
 cudaError_t launch_accept(const AcceptParams& p, cudaStream_t s);
 
 }  // namespace gdn

@@ -197,3 +197,13 @@ def test_kernel_choice_is_at_the_measured_crossings(R):
             got = N.gdn_kv4_workspace_bytes(R.make_attn_dims(2, 2, D), 2, 1, rows, 0)
             assert got == (few if rows <= most else many), (D, rows)
             assert N.gdn_kv4_workspace_bytes(R.make_attn_dims(2, 2, D, dtype=torch.float32), 2, 1, rows, 0) == few
+
+
+def test_acceptance_reduces_all_rows_at_once_while_they_are_few(R):
+    """The workspace holds 16 bytes for each slice of 8192 entries, up to 2^26 entries (the limit with draft
+    probabilities), and next to nothing beyond that or where there is no child."""
+    from gated_deltanet_tree_gb300 import _native as N
+    for B, n, V, slices in ((1, 22, 131072, 16), (4, 64, 131072, 16), (64, 16, 65536, 8), (64, 16, 65537, 0), (70000, 2, 100, 0),
+                            (5, 1, 1000, 0)):
+        need = B * n * slices * 16 + 1
+        assert N.gdn_accept_workspace_bytes(B, n, V) == -(-need // 256) * 256

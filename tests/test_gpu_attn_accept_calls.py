@@ -8,7 +8,7 @@ import torch
 import synthetic as S
 from oracle import accept_oracle as A
 from oracle import kv4_oracle as K
-from test_gpu_attn_accept import DT, built, check, f64, filled, i32, make_cache, rows  # noqa: F401
+from test_gpu_attn_accept import DT, accept_case, built, check, f64, filled, i32, make_cache, rows  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -328,3 +328,86 @@ def runs_of_pages(Hq, Hkv, D, n, dtype, lens):
                 far = np.isinf(ref)
                 assert np.array_equal(got[far], ref[far])
                 check(np.where(far, 0.0, got), np.where(far, 0.0, ref), vmax, dtype, (b, h, i))
+
+
+# ---- acceptance along the walk --------------------------------------------------------------------------------------
+
+def at_once(B, n, V, draft):
+    return n > 1 and B * n * V <= (2 if draft else 1) << 25
+
+
+@pytest.mark.parametrize("B,n,V,dtype", [(32, 22, 50001, "bf16"), (40, 22, 40003, "f32"), (9, 64, 65536, "bf16"),
+                                         (600, 64, 1001, "bf16"), (5, 64, 131073, "f32")])
+def test_accept_chosen_drafts_along_the_walk(B, n, V, dtype):
+    """More rows than are reduced at once: descents, rejected siblings and greedy requests through the cluster's own
+    reduction."""
+    assert not at_once(B, n, V, False)
+    rng = np.random.default_rng(B + V)
+    trees = [S.chain_tree(n) if b % 3 == 2 else S.random_tree(int(rng.integers(1, n + 1)), rng) for b in range(B)]
+    temps = [0.0 if b % 4 == 3 else 0.5 + 0.7 * b / B for b in range(B)]
+    acc, taken = accept_case(rng, B, n, V, dtype, temps, trees=trees)
+    acc.check_error()
+    assert taken > B + B // 4
+
+
+def test_accept_deep_paths_along_the_walk():
+    """Chains of 22 nodes accepted to every depth, greedy and sampled: 22 cluster joins one after another."""
+    rng = np.random.default_rng(51)
+    B, n, V = 33, 22, 60001
+    assert not at_once(B, n, V, False)
+    tokens = rng.integers(0, V, (B, n))
+    z = torch.from_numpy(rng.standard_normal((B, n, V)).astype(np.float32))
+    for b in range(B):
+        for i in range(1, n):
+            if i != b % n:                       # request b stops above node b % n
+                z[b, i - 1, tokens[b, i]] += 40.0
+    for dtype in ("bf16", "f32"):
+        acc, _ = accept_case(rng, B, n, V, dtype, [0.0 if b % 2 else 0.9 for b in range(B)], trees=[S.chain_tree(n)] * B,
+                             tokens=tokens, logits=z)
+        acc.check_error()
+        assert acc.len.tolist() == [b % n or n for b in range(B)]
+
+
+@pytest.mark.parametrize("B,n,V,dtype,draft", [(70, 16, 65537, "bf16", "f32"), (48, 22, 70000, "f32", "bf16")])
+def test_accept_sampled_drafts_along_the_walk(B, n, V, dtype, draft):
+    assert not at_once(B, n, V, True)
+    rng = np.random.default_rng(B + V)
+    trees = [S.chain_tree(n) if b % 2 else S.random_tree(n, rng) for b in range(B)]
+    trees[0] = np.array([-1] + [0] * (n - 1))
+    temps = [1.0 if b % 5 else 0.0 for b in range(B)]
+    acc, taken = accept_case(rng, B, n, V, dtype, temps, draft=draft, trees=trees)
+    acc.check_error()
+    assert taken > B
+
+
+@pytest.mark.parametrize("draft", [False, True])
+def test_accept_is_the_same_both_ways(draft):
+    """One batch along the walk, and its requests a few at a time with all rows at once."""
+    from gated_deltanet_tree_gb300 import runtime as R
+    B, n, V, few = (64, 22, 48000, 4) if draft else (64, 22, 24000, 4)
+    assert not at_once(B, n, V, draft) and at_once(few, n, V, draft)
+    rng = np.random.default_rng(50)
+    g = torch.Generator(device="cuda").manual_seed(50)
+    trees = [S.random_tree(n, rng) for _ in range(B)]
+    par = torch.from_numpy(np.stack([np.maximum(t, 0) for t in trees])).cuda()
+    z = 2.0 * torch.randn(B, n, V, generator=g, device="cuda")
+    tok = torch.randint(0, V, (B, n), generator=g, device="cuda")
+    z.view(B, -1).scatter_add_(1, par * V + tok, torch.full((B, n), float(np.log(V)) + 2.5, device="cuda"))
+    q = torch.softmax(z + 0.5 * torch.randn(B, n, V, generator=g, device="cuda"), -1) if draft else None
+    u = torch.rand(B, n, generator=g, device="cuda")
+    noise = -torch.log(-torch.log(torch.rand(B, V, generator=g, device="cuda").clamp_(1e-9, 1 - 1e-7)))
+    t = 0.6 + 0.6 * torch.rand(B, generator=g, device="cuda")
+    t[::5] = 0.0
+    z, tok = z.bfloat16(), tok.int()
+    whole = R.TreeAcceptor(B, n, V)
+    whole.accept(schedule(trees, n), z, tok, u, noise, t, draft_probs=q)
+    whole.check_error()
+    part = R.TreeAcceptor(few, n, V)
+    for b in range(0, B, few):
+        s = slice(b, b + few)
+        path, length, token = part.accept(schedule(trees[s], n), z[s], tok[s].clone(), u[s].clone(), noise[s], t[s].clone(),
+                                          draft_probs=None if q is None else q[s])
+        part.check_error()
+        assert torch.equal(path, whole.path[s]) and torch.equal(length, whole.len[s])
+        assert torch.equal(token, whole.next[s])
+    assert int(whole.len.max()) >= 4
