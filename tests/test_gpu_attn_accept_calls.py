@@ -8,7 +8,7 @@ import torch
 import synthetic as S
 from oracle import accept_oracle as A
 from oracle import kv4_oracle as K
-from test_gpu_attn_accept import DT, accept_case, built, check, f64, filled, i32, make_cache, rows  # noqa: F401
+from test_gpu_attn_accept import DT, accept_case, built, check, f64, filled, i32, make_cache, rows, run_case  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -411,3 +411,136 @@ def test_accept_is_the_same_both_ways(draft):
         assert torch.equal(path, whole.path[s]) and torch.equal(length, whole.len[s])
         assert torch.equal(token, whole.next[s])
     assert int(whole.len.max()) >= 4
+
+
+# ---- large batches and many launches --------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("Hq,Hkv,D,n,dtype", [(6, 1, 256, 1, "bf16"), (4, 1, 64, 2, "f32"), (24, 1, 256, 2, "bf16"),
+                                              (8, 1, 128, 4, "bf16")])
+def test_attention_many_short_requests(Hq, Hkv, D, n, dtype):
+    """More requests than a CTA has threads: their units are summed, and a CTA's place found, in blocks; lengths from 0,
+    more requests than CTAs and several requests a CTA."""
+    rng = np.random.default_rng(60 + n)
+    B = 1300
+    lens = rng.integers(0, 140, B)
+    lens[[0, 5, 576, 1152, B - 1]] = [0, 128, 0, 64, 131]
+    trees = None if n == 1 else [S.random_tree(int(rng.integers(1, n + 1)), rng) for _ in range(B)]
+    if trees is not None:
+        trees[0] = S.random_tree(n, rng)
+    run_case(rng, Hq, Hkv, D, lens.tolist(), trees, dtype)
+    # (requests out of range among them: nothing served but the others)
+    from gated_deltanet_tree_gb300 import _native as N
+    c, kr, vr = filled(rng, Hq, Hkv, D, lens.tolist(), 1, dtype)
+    q = rows(rng, B, 1, 1, Hq, D, dtype=dtype)
+    good, out = torch.zeros_like(q), torch.full_like(q, 7.0)
+    c.attention(q, None, None, good)
+    c.check_error()
+    bad = [1, 255, 256, 700, B - 2]
+    c.seq_len[bad] = -1
+    c.attention(q, None, None, out)
+    with pytest.raises(N.GdnError) as e:
+        c.check_error()
+    assert e.value.status == N.GDN_ERR_CACHE
+    assert (out[bad] == 7.0).all()
+    kept = np.setdiff1d(np.arange(B), bad)
+    vmax = max(1.0, float(np.abs(vr).max()))
+    check(f64(out[kept]), f64(good[kept]), vmax, dtype, "others")       # (split elsewhere: other roundings)
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,n,layers,B", [(24, 4, 64, 2, 32, 66), (24, 4, 256, 4, 16, 66), (8, 8, 64, 1, 32, 66),
+                                                 (512, 64, 64, 1, 8, 40)])
+def test_attention_in_several_launches(Hq, Hkv, D, n, layers, B):
+    """More items than a launch has counters or records for: requests of later launches, whose counters are the first
+    ones' again."""
+    some = n * (Hq // Hkv)
+    few = some <= {256: 16, 128: 20, 64: 28}[D]
+    assert (16384 if few else 4096) // (layers * Hkv * -(-some // (8 if few else 128))) < B
+    rng = np.random.default_rng(70 + n)
+    lens = rng.integers(0, 100, B)
+    lens[[0, 1, B - 1]] = [1, 99, 400]
+    trees = None if n == 1 else [S.random_tree(int(rng.integers(1, n + 1)), rng) for _ in range(B)]
+    if trees is not None:
+        trees[0] = S.random_tree(n, rng)
+    c = make_cache(Hq, Hkv, D, B, layers, 7, "bf16")
+    k, v = rows(rng, B, layers, 400, Hkv, D, dtype="bf16"), rows(rng, B, layers, 400, Hkv, D, dtype="bf16")
+    c.append(k, v, i32(lens))
+    kr, vr = c.read(None, 400)
+    q, kn, vn = (rows(rng, B, layers, n, h, D, dtype="bf16") for h in (Hq, Hkv, Hkv))
+    out = torch.full_like(q, 7.0)
+    for _ in range(2):
+        c.attention(q, kn, vn, out, sched=None if trees is None else schedule(trees, n), max_len=400)
+    c.check_error()
+    assert not c.workspace[:65536].any()
+    G, vmax = Hq // Hkv, max(float(vn.abs().max()), float(vr.abs().max()))
+    # every request's every layer and head in fp64, batched: an additive mask for what a row does not see
+    L = int(lens.max())
+    see = torch.zeros(B, n, L + n, dtype=torch.bool, device="cuda")
+    see[:, :, :L] = (torch.arange(L, device="cuda") < i32(lens)[:, None])[:, None]
+    for b in range(B):
+        t = np.array([-1]) if trees is None else trees[b]
+        for i in range(len(t)):
+            see[b, i, [L + j for j in K.root_path(t, i)]] = True
+    for l in range(layers):
+        kk = torch.cat([kr[:, l, :L], kn[:, l].float()], 1).double()                   # [B, L + n, Hkv, D]
+        vv = torch.cat([vr[:, l, :L], vn[:, l].float()], 1).double()
+        qq = q[:, l].double().unflatten(2, (Hkv, G))                                   # [B, n, Hkv, G, D]
+        a = torch.einsum("bnhgd,bthd->bnhgt", qq, kk) * c.dims.scale
+        a = a.masked_fill(~see[:, :, None, None], -float("inf"))
+        ref = torch.einsum("bnhgt,bthd->bnhgd", torch.softmax(a, -1), vv).flatten(2, 3)
+        for b in range(B):
+            m = 1 if trees is None else len(trees[b])
+            check(f64(out[b, l, :m]), f64(ref[b, :m]), vmax, "bf16", (b, l))
+            assert (out[b, l, m:] == 7.0).all()
+
+
+# ---- the example ----------------------------------------------------------------------------------------------------
+
+def test_example_step_against_the_oracles():
+    """The example's last step: its attention's output from the cache as it was before the step, its acceptance from the
+    logits and numbers it drew, and the rows its append left in the cache."""
+    import os
+    import sys
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+    import hybrid_step
+    seen = {}
+
+    class Watched(hybrid_step.HybridStack):
+        def step(self, *args):
+            before = tuple(f64(t) for t in self.cache.read(None, 64 * self.cache.pages_max)) + (self.cache.seq_len.tolist(),)
+            attention, accept = self.cache.attention, self.acceptor.accept
+
+            def look_attention(q, k, v, out, sched):
+                attention(q, k, v, out, sched=sched)
+                seen["attention"] = (before, q.clone(), k.clone(), v.clone(), out.clone(), sched)
+
+            def look_accept(sched, z, tokens, u, g, t):
+                got = accept(sched, z, tokens, u, g, t)
+                seen["accept"] = (z.clone(), tokens.clone(), u.clone(), g.clone(), t.clone(), [x.clone() for x in got])
+                return got
+
+            self.cache.attention, self.acceptor.accept = look_attention, look_accept
+            got = super().step(*args)
+            del self.cache.attention, self.acceptor.accept
+            return got
+
+    whole, hybrid_step.HybridStack = hybrid_step.HybridStack, Watched
+    try:
+        model = hybrid_step.main(steps=3, show=lambda line: None)
+    finally:
+        hybrid_step.HybridStack = whole
+    (kr, vr, lens), q, k, v, out, sched = seen["attention"]
+    z, tokens, u, g, t, (path, length, token) = seen["accept"]
+    after = [f64(x) for x in model.cache.read(None, 64 * model.cache.pages_max)]
+    for b in range(model.B):
+        m = int(sched.n[b])
+        tree = sched.parents[b, :m]
+        ref = K.tree_attention(f64(q[b, 0, :m]), kr[b, 0, :lens[b]], vr[b, 0, :lens[b]], f64(k[b, 0, :m]), f64(v[b, 0, :m]),
+                               tree, model.cache.dims.scale)
+        check(f64(out[b, 0, :m]), ref, max(float(v.abs().max()), float(np.abs(vr).max())), "bf16", b)
+        want, nxt = A.accept(tree.tolist(), tokens[b].tolist(), f64(z[b, :m]), f64(u[b]), f64(g[b]), float(t[b]))
+        L = int(length[b])
+        assert path[b, :L].tolist() == want and int(token[b]) == nxt
+        for x, new in zip(after, (k, v)):
+            rows64 = np.stack([[K.quantise_row(r) for r in f64(new[b, 0, i])] for i in want])
+            assert np.array_equal(x[b, 0, lens[b]:lens[b] + L], rows64)
+        assert int(model.cache.seq_len[b]) == lens[b] + L
