@@ -32,9 +32,11 @@
 // slices and exchange their partial results through distributed shared memory;
 // every CTA takes each decision itself from the same numbers in the same order.
 //
-// Sums and probabilities are fp32.  Scores of the next token are z / T + gumbel
-// with each operation rounded once, so that the choice does not depend on how the
-// compiler contracts it.
+// Sums and probabilities are fp32.  Exponents are (z - row's maximum) / T, the difference
+// first: z / T alone would round to steps larger than 1 at small temperatures, and a
+// product that the subtraction sees unrounded would leave that step in the exponent.
+// Scores of the next token are (z - maximum) / T + gumbel with each operation rounded
+// once, so that the choice does not depend on how the compiler contracts it.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cmath>
@@ -95,7 +97,7 @@ __device__ __forceinline__ int key_index(unsigned long long k) {
 
 // What a slice of a row contributes.
 struct __align__(16) Partial {
-  float m, s;                 // maximum (of z log2 e / T), sum of 2^(. - m)
+  float m, s;                 // maximum, sum of 2^((z - m) log2 e / T)
   unsigned long long top;     // best (value, index)
 };
 __device__ __forceinline__ Partial empty_partial() { return Partial{-INFINITY, 0.f, 0ull}; }
@@ -106,10 +108,10 @@ __device__ __forceinline__ float exp2_fast(float x) {   // results below 2^-126 
 }
 // The warp's join, the same in every lane: of maxima and sums (the sums rescaled once, to the warp's maximum), or of
 // the best entries.
-__device__ __forceinline__ Partial warp_join_sum(Partial x) {
+__device__ __forceinline__ Partial warp_join_sum(Partial x, float scale2) {
   float m = x.m;
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  float s = x.s * exp2_fast(x.m - (m == -INFINITY ? 0.f : m));
+  float s = x.s * exp2_fast((x.m - (m == -INFINITY ? 0.f : m)) * scale2);
   for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
   return Partial{m, s, 0ull};
 }
@@ -121,7 +123,11 @@ __device__ __forceinline__ Partial warp_join_top(Partial x) {
   }
   return Partial{-INFINITY, 0.f, top};
 }
-__device__ __forceinline__ Partial warp_join(Partial x, bool top) { return top ? warp_join_top(x) : warp_join_sum(x); }
+__device__ __forceinline__ Partial warp_join(Partial x, bool top, float scale2) {
+  return top ? warp_join_top(x) : warp_join_sum(x, scale2);
+}
+// log2 e / T and 1 / T, finite for the smallest temperatures too (0 times them is 0).
+__device__ __forceinline__ float over_temperature(float x, float T) { return fminf(x / T, 3.402823466e38f); }
 
 // This thread's share of part `part` of `parts` of a row: every parts * threads-th 16-byte vector, kAhead loads in
 // flight, and what the aligned vectors leave (part 0).  A NaN makes the sum NaN, or the first largest +inf.
@@ -147,11 +153,11 @@ __device__ __forceinline__ Partial scan_row(const TL* z, int V, float scale2, bo
     } else {
       float m = x.m;
 #pragma unroll
-      for (int i = 0; i < count; ++i) m = fmaxf(m, v[i] * scale2);
+      for (int i = 0; i < count; ++i) m = fmaxf(m, v[i]);
       const float ref = m == -INFINITY ? 0.f : m;
-      float s = x.s * exp2_fast(x.m - ref);
+      float s = x.s * exp2_fast((x.m - ref) * scale2);
 #pragma unroll
-      for (int i = 0; i < count; ++i) s += exp2_fast(fmaf(v[i], scale2, -ref));
+      for (int i = 0; i < count; ++i) s += exp2_fast((v[i] - ref) * scale2);
       x.m = m;
       x.s = s;
     }
@@ -203,11 +209,12 @@ __global__ void __launch_bounds__(kRowThreads) accept_rows_kernel(AcceptParams p
   if (!(T >= 0.f) || T == INFINITY) return;             // the walk reports it
   const TL* z = static_cast<const TL*>(p.logits) + static_cast<size_t>(row) * p.v_stride;
   const int lane = threadIdx.x & 31;
-  Partial x = warp_join(scan_row<TL>(z, p.V, cold ? kLog2e : kLog2e / T, cold, blockIdx.x, gridDim.x), cold);
+  const float scale2 = cold ? kLog2e : over_temperature(kLog2e, T);
+  Partial x = warp_join(scan_row<TL>(z, p.V, scale2, cold, blockIdx.x, gridDim.x), cold, scale2);
   if (lane == 0) part[threadIdx.x >> 5] = x;
   __syncthreads();
   if (threadIdx.x < 32) {
-    x = warp_join(lane < kRowThreads / 32 ? part[lane] : empty_partial(), cold);
+    x = warp_join(lane < kRowThreads / 32 ? part[lane] : empty_partial(), cold, scale2);
     if (lane == 0) static_cast<Partial*>(p.slices)[static_cast<size_t>(row) * gridDim.x + blockIdx.x] = x;
   }
 }
@@ -227,19 +234,20 @@ struct Shared {
 
 // The cluster's join of every thread's partial, known to all threads.  `step` alternates the slots: a slot is
 // written again only after the barrier of the step in between.
-__device__ __forceinline__ Partial cluster_join(cg::cluster_group& cl, Shared& sh, Partial x, int& step, bool top) {
+__device__ __forceinline__ Partial cluster_join(cg::cluster_group& cl, Shared& sh, Partial x, int& step, bool top,
+                                                float scale2) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  x = warp_join(x, top);
+  x = warp_join(x, top, scale2);
   if (lane == 0) sh.warp[warp] = x;
   __syncthreads();
   const int n = cl.num_blocks(), rank = cl.block_rank(), par = step & 1;
   if (warp == 0) {
-    const Partial t = warp_join(lane < kThreads / 32 ? sh.warp[lane] : empty_partial(), top);
+    const Partial t = warp_join(lane < kThreads / 32 ? sh.warp[lane] : empty_partial(), top, scale2);
     if (lane < n) cl.map_shared_rank(&sh, lane)->slot[par][rank] = t;
   }
   cl.sync();
   ++step;
-  return warp_join(lane < n ? sh.slot[par][lane] : empty_partial(), top);
+  return warp_join(lane < n ? sh.slot[par][lane] : empty_partial(), top, scale2);
 }
 
 // TQ: the type of the draft probabilities, void without them.
@@ -272,7 +280,7 @@ __global__ void __launch_bounds__(kThreads) accept_walk_kernel(AcceptParams p) {
   using Q = std::conditional_t<kDraft, TQ, float>;
   const Q* draft = static_cast<const Q*>(p.draft);
   const size_t row_of_b = static_cast<size_t>(b) * p.n_max;
-  const float scale2 = cold ? kLog2e : kLog2e / T;
+  const float scale2 = cold ? kLog2e : over_temperature(kLog2e, T);
   const int V = p.V;
   // everything the decisions look up, for every node at once
   if (tid < n) {
@@ -304,7 +312,7 @@ __global__ void __launch_bounds__(kThreads) accept_walk_kernel(AcceptParams p) {
       for (int k0 = 0; !bad && k0 < p.n_slices; k0 += 31) {
         const int k = k0 + lane - 1;
         if (lane > 0) x = k < p.n_slices ? slices[(row_of_b + i) * p.n_slices + k] : empty_partial();
-        x = warp_join(x, cold);
+        x = warp_join(x, cold, scale2);
       }
       if (lane == 0) sh.row[i] = x;
     }
@@ -317,7 +325,8 @@ __global__ void __launch_bounds__(kThreads) accept_walk_kernel(AcceptParams p) {
     const Q* q = kDraft ? draft + (row_of_b + node) * p.v_stride : nullptr;
     if (rank == 0 && tid == 0) path[path_len] = node;
     ++path_len;
-    const Partial x = kAtOnce ? sh.row[node] : cluster_join(cl, sh, scan_row<TL>(z, V, scale2, cold, rank, ranks), step, cold);
+    const Partial x =
+        kAtOnce ? sh.row[node] : cluster_join(cl, sh, scan_row<TL>(z, V, scale2, cold, rank, ranks), step, cold, scale2);
     const float mx = x.m, total = x.s;
     // a NaN or +inf makes the sum NaN; a row of -inf leaves it 0
     if (cold ? !(fabsf(key_value(x.top)) < INFINITY) : !(total > 0.f && total < INFINITY)) {
@@ -325,7 +334,7 @@ __global__ void __launch_bounds__(kThreads) accept_walk_kernel(AcceptParams p) {
       break;
     }
     // ---- the children, in index order: by one thread
-    auto prob = [&](float zv) { return exp2f(fmaf(zv, scale2, -mx)) / total; };
+    auto prob = [&](float zv) { return exp2f(__fmul_rn(__fsub_rn(zv, mx), scale2)) / total; };
     if (tid == 0) {
       sh.child = -1;
       sh.more = -1;
@@ -370,7 +379,7 @@ __global__ void __launch_bounds__(kThreads) accept_walk_kernel(AcceptParams p) {
         y.m = 0.f;
         for (int i = rank * kThreads + tid; i < V; i += ranks * kThreads)
           y.s += fmaxf(prob(to_f(z[i])) - c * to_f(q[i]), 0.f);
-        const float mass = cluster_join(cl, sh, y, step, false).s;
+        const float mass = cluster_join(cl, sh, y, step, false, scale2).s;
         const int t = sh.token[k];
         const float r = fmaxf(prob(sh.zc[k]) - c * sh.qc[k], 0.f);
         if (t >= 0 && t < V && sh.uniform[k] * sh.qc[k] * mass < r)
@@ -389,7 +398,7 @@ __global__ void __launch_bounds__(kThreads) accept_walk_kernel(AcceptParams p) {
       pick = key_index(x.top);
       break;
     }
-    const float rT = 1.f / T, rtotal = 1.f / total;
+    const float rT = over_temperature(1.f, T), rtotal = 1.f / total;
     for (int whole = 0; whole < 2 && pick < 0; ++whole) {   // p itself where nothing is left
       constexpr int kAhead = 8;
       Partial y = empty_partial();
@@ -422,10 +431,10 @@ __global__ void __launch_bounds__(kThreads) accept_walk_kernel(AcceptParams p) {
         for (int k = 0; k < kAhead; ++k) {
           float t, slack = 0.f;                             // the log weight from above, and how far below it may be
           if constexpr (!kDraft) {
-            t = zv[k] * rT;
+            t = (zv[k] - mx) * rT;
           } else {
             // (the difference may cancel)
-            const float pk = exp2_fast(fmaf(zv[k], scale2, -mx)) * rtotal, qk = use * qv[k];
+            const float pk = exp2_fast((zv[k] - mx) * scale2) * rtotal, qk = use * qv[k];
             const float up = fmaf(pk, 1.0001f, -0.9999f * qk), dn = fmaf(pk, 0.9999f, -1.0001f * qk);
             t = up > 0.f ? __logf(up) + 1e-3f : -INFINITY;
             slack = dn > 0.f ? t - __logf(dn) + 1e-3f : INFINITY;
@@ -445,7 +454,7 @@ __global__ void __launch_bounds__(kThreads) accept_walk_kernel(AcceptParams p) {
           const float zi = to_f(z[i]), gi = __ldg(g + i);
           float score;
           if constexpr (!kDraft) {
-            score = __fadd_rn(__fdiv_rn(zi, T), gi);
+            score = __fadd_rn(__fdiv_rn(__fsub_rn(zi, mx), T), gi);
           } else {
             const float r = prob(zi) - use * to_f(q[i]);
             score = r > 0.f ? __fadd_rn(logf(r), gi) : -INFINITY;
@@ -456,7 +465,7 @@ __global__ void __launch_bounds__(kThreads) accept_walk_kernel(AcceptParams p) {
           }
         }
       }
-      y = cluster_join(cl, sh, y, step, true);
+      y = cluster_join(cl, sh, y, step, true, scale2);
       if (y.top != 0ull) pick = key_index(y.top);
     }
     break;

@@ -413,6 +413,45 @@ def test_accept_is_the_same_both_ways(draft):
     assert int(whole.len.max()) >= 4
 
 
+@pytest.mark.parametrize("B,n,V", [(13, 6, 3001), (13, 22, 140001), (13, 64, 90001)])
+@pytest.mark.parametrize("draft", [None, "f32"])
+def test_accept_at_small_temperatures(B, n, V, draft):
+    """Down to the smallest fp32 number: z / T passes 2^24 (where its rounding passes 1) and fp32's largest number."""
+    assert at_once(B, n, V, draft) == (n == 6 or (n == 22 and draft is not None))
+    rng = np.random.default_rng(52)
+    temps = [1e-2, 1e-4, 1e-6, 1e-7, 1e-8, 1e-9, 1e-12, 1e-20, 1e-30, 1e-36, 1e-38, 1e-41, 1.4e-45]
+    for shift in (0.0, 30.0, -200.0):
+        trees = [S.chain_tree(n) if b % 2 else S.random_tree(n, rng) for b in range(B)]
+        tokens = rng.integers(0, V, (B, n))
+        z = torch.from_numpy((shift + 2 * rng.standard_normal((B, n, V))).astype(np.float32))
+        for b in range(B):
+            for i in range(1, n):
+                if rng.random() < 0.8:
+                    z[b, trees[b][i], tokens[b, i]] += 20.0
+        acc, _ = accept_case(rng, B, n, V, "f32", temps, draft=draft, trees=trees, tokens=None if draft else tokens,
+                             logits=z)
+        acc.check_error()
+
+
+@pytest.mark.parametrize("V", [3001, 140001])
+def test_accept_draws_among_equal_logits_at_small_temperatures(V):
+    """Equal largest logits share the probability whatever the temperature: the Gumbel numbers decide."""
+    from gated_deltanet_tree_gb300 import runtime as R
+    rng = np.random.default_rng(53)
+    temps = [1.0, 1e-3, 1e-5, 1e-6, 1e-7, 1e-8, 1e-12, 1e-30, 1e-38, 1.4e-45]
+    B = 10 * len(temps)
+    z = torch.from_numpy(rng.standard_normal((B, 1, V)).astype(np.float32)).cuda()
+    ties = np.stack([np.sort(rng.choice(V, 5, replace=False)) for _ in range(B)])
+    z.view(B, V).scatter_(1, torch.from_numpy(ties).cuda(), 47.3)
+    g = torch.from_numpy(-np.log(-np.log(rng.random((B, V)))).astype(np.float32)).cuda()
+    acc = R.TreeAcceptor(B, 1, V)
+    acc.accept(schedule([np.array([-1])] * B, 1), z, i32(np.zeros((B, 1))), torch.zeros(B, 1, device="cuda"), g,
+               torch.tensor(temps * 10, device="cuda"))
+    acc.check_error()
+    best = np.take_along_axis(g.cpu().numpy(), ties, 1).argmax(1)
+    assert acc.next.tolist() == ties[np.arange(B), best].tolist()
+
+
 # ---- large batches and many launches --------------------------------------------------------------------------------
 
 @pytest.mark.parametrize("Hq,Hkv,D,n,dtype", [(6, 1, 256, 1, "bf16"), (4, 1, 64, 2, "f32"), (24, 1, 256, 2, "bf16"),
