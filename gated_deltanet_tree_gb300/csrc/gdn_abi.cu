@@ -1,6 +1,6 @@
 // extern "C" entry points: argument checks, the factor-bank lifecycle and the
 // kernel launches.  No entry point allocates memory or synchronises the host
-// except gdn_check_error.
+// except gdn_check_error and gdn_check_error_words.
 #include <algorithm>
 #include <cmath>
 #include <cstdarg>

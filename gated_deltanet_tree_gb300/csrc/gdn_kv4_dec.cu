@@ -31,9 +31,11 @@
 // time (86 -> 95 us).
 //
 // Measured: 32 requests of 16640 to 32768 tokens, 24 query and 4 kv heads of 256, one bf16
-// token each: 912 MB in 191 us, 4.8 TB/s, 0.70 of a plain copy's rate.  Unpacking
-// sets the pace (issue slots 55% and the ALU 47% taken), so the schedule gives every
-// CTA the same number of pages.  One request of 4096 tokens: 17 us, latencies.
+// token each: 912 MB in 192 us, 4.8 TB/s, 0.70 of a plain copy's rate.  No unit is full
+// (issue slots 55%, ALU 46%): the latencies of a warp's chain of scores, shuffles and
+// output, with two pages in flight a pair of warps, set the pace, and the schedule gives
+// every CTA the same number of pages.  One request of 4096 tokens: 17 us, latencies.
+// The same 32 requests in fp32: 397 us (one CTA of D = 256 fits an SM).
 #include "gdn_kv4_attn.cuh"
 #include "gdn_umma.cuh"
 

@@ -26,10 +26,10 @@
 // adds its own ancestors in fp32 at the end.
 //
 // Measured: trees of 64 and 48 nodes over 200001 and 150001 tokens (three tiles each),
-// 24 query and 4 kv heads of 256: 480 to 511 us from run to run, 0.94 to 1.0 PFLOP/s of
+// 24 query and 4 kv heads of 256: 497 to 515 us from run to run, 0.94 to 0.97 PFLOP/s of
 // useful products, about half of cuBLAS' bf16 rate.  A 64-token step takes about 1.9
 // times its MMAs' 1024 cycles; issue slots
-// (57%) and the latencies of tensor memory share the rest.
+// (60%) and the latencies of tensor memory share the rest.
 #include "gdn_kv4_attn.cuh"
 #include "gdn_umma.cuh"
 

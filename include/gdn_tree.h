@@ -476,7 +476,10 @@ gdn_status gdn_kv4_read(const gdn_attn_dims* d, int32_t layers, int32_t n_rows, 
  * Many bf16 rows' k_new and v_new enter in fp16 too, k_new scaled per row like q; v_new
  * values below 2^-17 keep 2^-25 where one of the same channel and eight nodes is 2^-12
  * or larger, and all their bits where none is.
- * GDN_ERR_UNSUPPORTED: layers * Hkv * ceil(n_max * Hq / Hkv / 8) above 16384.
+ * GDN_ERR_UNSUPPORTED: more tiles of rows a request than a launch has counters for:
+ * layers * Hkv * ceil(n_max * Hq / Hkv / 8) above 16384, unless the call is bf16 with
+ * more than 16 (D = 128: 20, D = 64: 28) rows n_max * Hq / Hkv and at most 4096 tiles
+ * of 128 of them.
  * ------------------------------------------------------------------------- */
 size_t gdn_kv4_workspace_bytes(const gdn_attn_dims* d, int32_t B, int32_t layers, int32_t n_max, int32_t max_len);
 gdn_status gdn_kv4_attention(const gdn_attn_dims* d, int32_t layers, const gdn_batch_schedule* sched, const void* q,
