@@ -369,7 +369,7 @@ __global__ void __launch_bounds__(32 * kWarpsOf<D>, 2) kv4_attn_dec_kernel(KvAtt
           n0 = fmaxf(n0, __shfl_xor_sync(0xffffffffu, n0, off));
           n1 = fmaxf(n1, __shfl_xor_sync(0xffffffffu, n1, off));
         }
-        if (__any_sync(0xffffffffu, n0 > m0 + kSlack || n1 > m1 + kSlack)) {
+        if (__any_sync(0xffffffffu, n0 - m0 > kSlack || n1 - m1 > kSlack)) {       // (the sums would round)
           const float f0 = m0 == -INFINITY ? 0.f : exp2f(m0 - n0), f1 = m1 == -INFINITY ? 0.f : exp2f(m1 - n1);
           m0 = n0;
           m1 = n1;
@@ -386,7 +386,8 @@ __global__ void __launch_bounds__(32 * kWarpsOf<D>, 2) kv4_attn_dec_kernel(KvAtt
             }
         }
         // a row whose scores so far are all -inf keeps weight 0 (its maximum is not subtracted)
-        const float r0 = m0 == -INFINITY ? kLift : kLift - m0, r1 = m1 == -INFINITY ? kLift : kLift - m1;
+        // (rounded down: where the scores' own steps are larger than kLift, no weight passes fp16's largest number)
+        const float r0 = m0 == -INFINITY ? kLift : __fsub_rd(kLift, m0), r1 = m1 == -INFINITY ? kLift : __fsub_rd(kLift, m1);
         uint32_t pf[kTerms][2][2];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {

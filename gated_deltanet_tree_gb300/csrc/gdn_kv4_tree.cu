@@ -52,6 +52,7 @@ constexpr float kSlack = 9.f;
 // joined in fp32 in the place of its partial result: 131072 tokens a run leave 2^-10, and cost a start and an end
 // (some 10 us of 2 ms).
 constexpr int kRun = 2048;
+constexpr float kLarge = 0x1p22f;     // scores (base 2) whose steps are 1/2 or more
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kTooLarge = 6.0e4f;   // new values beyond this take the fp32 path,
 constexpr float kTooSmall = 0x1p-12f; // as do those that fp16 rounds (below 2^-17) where eight nodes' channel has none this large
@@ -403,8 +404,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tree_kernel(KvAttnParams
             }
             top = fmaxf(top, fmaxf(t0, t1));
           }
-          // rounded up: no score times c passes it, however large the scores
-          top = __fmul_ru(top, c);
+          // rounded up, so that no score times c passes it; large scores' products are rounded themselves (below)
+          top = fabsf(top) * c < kLarge ? __fmul_ru(top, c) : __fmul_rn(top, c);
           // the reference: the other thread's of the page before, raised where this page passes it by too much
           float before = -INFINITY;
           if (i > 0) {
@@ -412,7 +413,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tree_kernel(KvAttnParams
             if (!alive) break;
             before = *const_cast<volatile float*>(ref);
           }
-          const float now = top > before + kSlack ? top : before;
+          const float now = top - before > kSlack ? top : before;       // (the sum would round)
           *ref = now;
           arrive_warp(kDecided + quarter);
           follow(now);
@@ -433,8 +434,25 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tree_kernel(KvAttnParams
             }
             tmem_wait_st();
           }
-          const float base = m == -INFINITY ? kLift : kLift - m;
-          const u64 c2 = pack2(c, c), b2 = pack2(base, base);
+          // (rounded down: where the scores' own steps are larger than kLift, no weight passes fp16's largest number)
+          const float base = m == -INFINITY ? kLift : __fsub_rd(kLift, m);
+          float times = c;
+          const bool large = fabsf(m) >= kLarge && m > -INFINITY;
+          if (__any_sync(0xffffffffu, large)) {
+            // the products' own rounding has to be the reference's: a fused multiply-add would leave it in the exponent
+            if (large) times = 1.f;
+#pragma unroll 1
+            for (int x = 0; x < kTok; x += 16) {
+              float t[16];
+              tmem_ld16(ts + x, t);
+              tmem_wait_ld();
+#pragma unroll
+              for (int y = 0; y < 16; ++y) t[y] = large ? __fmul_rn(t[y], c) : t[y];
+              tmem_st16(ts + x, t);
+            }
+            tmem_wait_st();
+          }
+          const u64 c2 = pack2(times, times), b2 = pack2(base, base);
           u64 sum[2] = {0, 0};
 #pragma unroll 1
           for (int h = 0; h < kTok; h += 32) {

@@ -212,6 +212,35 @@ def test_small_new_values_keep_their_bits(Hq, Hkv, D, size):
         check(f64(out[b, 0, :len(t)]), ref[b], float(vn.abs().max()), "bf16", b)
 
 
+@pytest.mark.parametrize("Hq,D,B,dtype", [(24, 256, 152, "bf16"), (24, 128, 152, "bf16"), (32, 64, 152, "bf16"),
+                                          (8, 256, 304, "bf16"), (8, 64, 304, "bf16"), (8, 256, 304, "f32"),
+                                          (8, 64, 304, "f32")])
+@pytest.mark.parametrize("scale", [float(np.log(2.0)), 0.3, 0.0625])
+@pytest.mark.parametrize("size", [2.0 ** 22, 2.0 ** 25, 1.5 * 2.0 ** 25, 1.25 * 2.0 ** 26, 2.0 ** 27, 2.0 ** 40])
+def test_scores_whose_steps_are_larger_than_one(Hq, D, B, dtype, size, scale):
+    """Scores of 2^22 to 2^40 (base 2), one page's a few steps above the others': equal values come out as they are,
+    whatever the weights."""
+    from gated_deltanet_tree_gb300 import runtime as R
+    dims = R.make_attn_dims(Hq, 1, D, dtype=DT[dtype], scale=scale)
+    pool = torch.zeros(1, 2, 1, 72 * D, dtype=torch.uint8, device="cuda")
+    k = torch.zeros(1, 1, 128, 1, D, device="cuda")
+    k[..., 0] = 1.0
+    k[0, 0, 64:, 0, 40] = 1.0
+    first = R.KV4Cache(dims, pool, i32([[0, 1]]), i32([0]))
+    first.append(k.to(DT[dtype]), torch.ones_like(k).to(DT[dtype]), i32([128]))
+    table = torch.zeros(B, 26, dtype=torch.int32, device="cuda")
+    table[:, [12, 24]] = 1
+    c = R.KV4Cache(dims, pool, table, i32([64 * 26] * B))
+    q = torch.zeros(B, 1, 1, Hq, D, dtype=DT[dtype], device="cuda")
+    for sign in (1.0, -1.0):
+        for step in (4.0, 8.0, 16.0):
+            q[..., 0], q[..., 40] = sign * size, step
+            out = torch.zeros_like(q)
+            c.attention(q, None, None, out, max_len=64 * 26)
+            c.check_error()
+            assert (out == 1.0).all() if dtype == "bf16" else ((out - 1.0).abs() <= 1e-6).all(), (sign, step)
+
+
 # ---- long contexts --------------------------------------------------------------------------------------------------
 
 def one_and_many(Hq, D, B, T, gap, dtype, dominant, tail):
