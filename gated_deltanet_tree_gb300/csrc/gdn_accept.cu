@@ -368,24 +368,28 @@ __global__ void __launch_bounds__(kThreads) accept_walk_kernel(AcceptParams p) {
     }
     __syncthreads();
     int child = sh.child;
-    float c = 0.f;
+    // what is left after the last rejection is (p - next q)+; where that is empty, it stays what it was, (p - c q)+ of sum N
+    float c = 0.f, N = 1.f, next = 0.f;
     if (kDraft && !cold && sh.more >= 0) {
-      c = 1.f;
+      next = 1.f;
       // the rejected child's later siblings
       for (unsigned long long kids = sh.kids[node] & ~((2ull << sh.more) - 1); child < 0 && kids; kids &= kids - 1) {
         const int k = __ffsll(static_cast<long long>(kids)) - 1;
-        // N = sum (p - c q)+
         Partial y = empty_partial();
         y.m = 0.f;
         for (int i = rank * kThreads + tid; i < V; i += ranks * kThreads)
-          y.s += fmaxf(prob(to_f(z[i])) - c * to_f(q[i]), 0.f);
+          y.s += fmaxf(prob(to_f(z[i])) - next * to_f(q[i]), 0.f);
         const float mass = cluster_join(cl, sh, y, step, false, scale2).s;
+        if (mass > 0.f) {
+          c = next;
+          N = mass;
+        }
         const int t = sh.token[k];
         const float r = fmaxf(prob(sh.zc[k]) - c * sh.qc[k], 0.f);
-        if (t >= 0 && t < V && sh.uniform[k] * sh.qc[k] * mass < r)
+        if (t >= 0 && t < V && sh.uniform[k] * sh.qc[k] * N < r)
           child = k;
         else
-          c += mass;
+          next = c + N;
       }
     }
     if (child >= 0) {
@@ -399,11 +403,11 @@ __global__ void __launch_bounds__(kThreads) accept_walk_kernel(AcceptParams p) {
       break;
     }
     const float rT = over_temperature(1.f, T), rtotal = 1.f / total;
-    for (int whole = 0; whole < 2 && pick < 0; ++whole) {   // p itself where nothing is left
+    for (int whole = 0; whole < 2 && pick < 0; ++whole) {   // what there was before where nothing is left
       constexpr int kAhead = 8;
       Partial y = empty_partial();
       const float* g = p.gumbel + static_cast<size_t>(b) * V;
-      const float use = whole ? 0.f : c;
+      const float use = whole ? c : next;
       const int stride = ranks * kThreads;
       float best = -INFINITY, floor = -INFINITY;            // this thread's best score, of ascending indices; the warp's bound
 #pragma unroll 1

@@ -501,8 +501,9 @@ gdn_status gdn_kv4_attention(const gdn_attn_dims* d, int32_t layers, const gdn_b
  *    child j is accepted if u_j * q(t_j) < (p(t_j) - c_j q(t_j))+ / N_j, with
  *    c_0 = 0, N_0 = 1, c_{j+1} = c_j + N_j, N_{j+1} = sum (p - c_{j+1} q)+.
  * The next token is then drawn from what is left at the node -- p without the
- * tried tokens, or (p - c q)+ with the c after the last rejection (p itself where
- * nothing is left) -- as the lowest index of the largest log weight + gumbel.
+ * tried tokens, or (p - c q)+ with the c after the last rejection -- as the lowest
+ * index of the largest log weight + gumbel.  A rejection that would leave nothing
+ * leaves the distribution as it was (chosen drafts: p), here and for later siblings.
  * Either way the tokens are distributed as the target's own samples.  With
  * temperature 0 a child is accepted if its token is the lowest index of the
  * row's largest logit, which is also the next token.

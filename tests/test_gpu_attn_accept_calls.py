@@ -481,6 +481,32 @@ def test_accept_draws_among_equal_logits_at_small_temperatures(V):
     assert acc.next.tolist() == ties[np.arange(B), best].tolist()
 
 
+def test_accept_rejections_that_leave_nothing():
+    """Drafts whose probabilities are the target's own, exactly, with tokens that cannot have been drawn (outside the
+    vocabulary): the rejection leaves nothing, and later siblings are tried against the distribution as it was."""
+    rng = np.random.default_rng(54)
+    B, n = 16, 9
+    star = np.array([-1] + [0] * (n - 1))
+    for V, keep in ((1, 1), (2, 2), (16, 16), (16, 4), (8192, 8192)):
+        z = torch.zeros(B, n, V)
+        z[..., keep:] = -float("inf")
+        tokens = rng.integers(-1, keep + 1, (B, n))
+        tokens[tokens >= keep] = V + 5
+        tokens[:, 1] = V
+        q = torch.softmax(z, -1).cuda()
+        assert torch.equal(q[0, 0, :keep], torch.full((keep,), 1.0 / keep, device="cuda"))
+        u = torch.from_numpy(rng.random((B, n)).astype(np.float32))
+        noise = torch.from_numpy(-np.log(-np.log(rng.random((B, V)))).astype(np.float32))
+        from gated_deltanet_tree_gb300 import runtime as R
+        acc = R.TreeAcceptor(B, n, V)
+        path, length, token = acc.accept(schedule([star] * B, n), z.cuda(), i32(tokens), u.cuda(), noise.cuda(),
+                                         torch.ones(B, device="cuda"), draft_probs=q)
+        acc.check_error()
+        for b in range(B):
+            want, nxt = A.accept(star.tolist(), tokens[b].tolist(), f64(z[b]), f64(u[b]), f64(noise[b]), 1.0, f64(q[b]))
+            assert path[b, :int(length[b])].tolist() == want and int(token[b]) == nxt, (V, keep, b)
+
+
 # ---- large batches and many launches --------------------------------------------------------------------------------
 
 @pytest.mark.parametrize("Hq,Hkv,D,n,dtype", [(6, 1, 256, 1, "bf16"), (4, 1, 64, 2, "f32"), (24, 1, 256, 2, "bf16"),
