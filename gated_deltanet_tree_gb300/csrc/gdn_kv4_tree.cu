@@ -417,41 +417,43 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tree_kernel(KvAttnParams
           *ref = now;
           arrive_warp(kDecided + quarter);
           follow(now);
-          if (i > 0 && __any_sync(0xffffffffu, now != before)) {
-            // rescale the output: the product of the step before has to be in it first
-            const float f = before == -INFINITY ? 0.f : exp2f(before - now);
-            alive = wait_all(kAdded + (buf ^ 1), (k - 1) >> 1);
-            if (!alive) break;
-            tmem_fence_after();
+          const bool raised = i > 0 && now != before, large = fabsf(now) >= kLarge && now > -INFINITY;
+          float times = c;
+          if (__any_sync(0xffffffffu, raised || large)) {          // (one vote for both, which are rare)
+            if (__any_sync(0xffffffffu, raised)) {
+              // rescale the output: the product of the step before has to be in it first
+              const float f = before == -INFINITY ? 0.f : exp2f(before - now);
+              alive = wait_all(kAdded + (buf ^ 1), (k - 1) >> 1);
+              if (!alive) break;
+              tmem_fence_after();
 #pragma unroll 1
-            for (int x = 0; x < D; x += 32) {
-              float o[32];
-              tmem_ld32(lanes + Sm::kO + x, o);
-              tmem_wait_ld();
+              for (int x = 0; x < D; x += 32) {
+                float o[32];
+                tmem_ld32(lanes + Sm::kO + x, o);
+                tmem_wait_ld();
 #pragma unroll
-              for (int y = 0; y < 32; ++y) o[y] *= f;
-              tmem_st32(lanes + Sm::kO + x, o);
+                for (int y = 0; y < 32; ++y) o[y] *= f;
+                tmem_st32(lanes + Sm::kO + x, o);
+              }
+              tmem_wait_st();
             }
-            tmem_wait_st();
+            if (__any_sync(0xffffffffu, large)) {
+              // the products' own rounding has to be the reference's: a fused multiply-add would leave it in the exponent
+              if (large) times = 1.f;
+#pragma unroll 1
+              for (int x = 0; x < kTok; x += 16) {
+                float t[16];
+                tmem_ld16(ts + x, t);
+                tmem_wait_ld();
+#pragma unroll
+                for (int y = 0; y < 16; ++y) t[y] = large ? __fmul_rn(t[y], c) : t[y];
+                tmem_st16(ts + x, t);
+              }
+              tmem_wait_st();
+            }
           }
           // (rounded down: where the scores' own steps are larger than kLift, no weight passes fp16's largest number)
           const float base = m == -INFINITY ? kLift : __fsub_rd(kLift, m);
-          float times = c;
-          const bool large = fabsf(m) >= kLarge && m > -INFINITY;
-          if (__any_sync(0xffffffffu, large)) {
-            // the products' own rounding has to be the reference's: a fused multiply-add would leave it in the exponent
-            if (large) times = 1.f;
-#pragma unroll 1
-            for (int x = 0; x < kTok; x += 16) {
-              float t[16];
-              tmem_ld16(ts + x, t);
-              tmem_wait_ld();
-#pragma unroll
-              for (int y = 0; y < 16; ++y) t[y] = large ? __fmul_rn(t[y], c) : t[y];
-              tmem_st16(ts + x, t);
-            }
-            tmem_wait_st();
-          }
           const u64 c2 = pack2(times, times), b2 = pack2(base, base);
           u64 sum[2] = {0, 0};
 #pragma unroll 1
