@@ -40,6 +40,7 @@ GDN_VERIFY_TC_PER_HEAD = 8
 GDN_VERIFY_CHAINS = 16
 GDN_MAX_NODES = 64
 GDN_KV4_PAGE = 64
+GDN_MAX_TOP = 32
 
 
 class GdnError(RuntimeError):
@@ -129,8 +130,15 @@ def lib():
         L.gdn_tree_accept.argtypes = [P(gdn_batch_schedule), c_i32, c_i32, c_i32, c_p, c_p, c_p, c_i32, c_p, c_p, c_p,
                                       c_p, c_p, c_p, c_p, c_p, ctypes.c_size_t, c_p]
         L.gdn_check_error_words.argtypes = [c_p, c_p]
+        c_i64, c_size = ctypes.c_int64, ctypes.c_size_t
+        L.gdn_prefill_workspace_bytes.argtypes = [P(gdn_dims)]
+        L.gdn_prefill_workspace_bytes.restype = c_size
+        layer_args = [c_p, c_i64, c_p, c_p, c_p, c_i64, c_p, c_p, c_p, c_p, c_p, c_i32, c_p, c_p]
+        L.gdn_prefill.argtypes = [P(gdn_dims), c_i32, c_i32, c_i32, P(c_i32)] + layer_args + [c_p, c_size, c_p]
+        L.gdn_step.argtypes = [P(gdn_dims), c_i32, c_i32, c_i32, c_p] + layer_args + [c_p]
+        L.gdn_top_logprobs.argtypes = [c_i32, c_i32, c_i64, c_i32, c_p, c_p, c_i32, c_p, c_p, c_p, c_p, c_p, c_p]
         for name in ("gdn_kv4_append", "gdn_kv4_read", "gdn_kv4_attention", "gdn_tree_accept",
-                     "gdn_check_error_words"):
+                     "gdn_check_error_words", "gdn_prefill", "gdn_step", "gdn_top_logprobs"):
             getattr(L, name).restype = c_i32
         for name in ("gdn_hld_schedule", "gdn_pack_schedules", "gdn_pack_schedules_per_node", "gdn_ddtree_build",
                      "gdn_ddtree_build_batch", "gdn_banks_init", "gdn_tree_verify",
@@ -349,3 +357,36 @@ def gdn_tree_accept(sched: gdn_batch_schedule, V: int, v_stride: int, logits_dty
                                  _ptr(draft_probs), draft_dtype, _ptr(uniform), _ptr(gumbel), _ptr(temperature),
                                  _ptr(path), _ptr(length), _ptr(next_token), _ptr(err), _ptr(workspace),
                                  workspace_bytes, _stream(stream)))
+
+
+def gdn_prefill_workspace_bytes(dims: gdn_dims) -> int:
+    return int(lib().gdn_prefill_workspace_bytes(ctypes.byref(dims)))
+
+
+def _banks_ref(banks: Optional[gdn_banks]):
+    return None if banks is None else ctypes.addressof(banks)
+
+
+def gdn_prefill(dims: gdn_dims, layers: int, layer: int, lens, x_raw, x_row: int, conv_w, beta, log_g, gate_row: int,
+                state, conv_state, state_out, conv_out, out_o, out_dtype: int, banks: Optional[gdn_banks], err, workspace,
+                workspace_bytes: int, stream=None):
+    """lens: the requests' numbers of rows, a sequence or array on the host."""
+    lens = np.ascontiguousarray(lens, dtype=np.int32)
+    _check(lib().gdn_prefill(ctypes.byref(dims), layers, layer, lens.shape[0],
+                             lens.ctypes.data_as(ctypes.POINTER(c_i32)), _ptr(x_raw), x_row, _ptr(conv_w), _ptr(beta),
+                             _ptr(log_g), gate_row, _ptr(state), _ptr(conv_state), _ptr(state_out), _ptr(conv_out),
+                             _ptr(out_o), out_dtype, _banks_ref(banks), _ptr(err), _ptr(workspace), workspace_bytes,
+                             _stream(stream)))
+
+
+def gdn_step(dims: gdn_dims, layers: int, layer: int, B: int, live, x_raw, x_row: int, conv_w, beta, log_g, gate_row: int,
+             state, conv_state, state_out, conv_out, out_o, out_dtype: int, banks: Optional[gdn_banks], err, stream=None):
+    _check(lib().gdn_step(ctypes.byref(dims), layers, layer, B, _ptr(live), _ptr(x_raw), x_row, _ptr(conv_w), _ptr(beta),
+                          _ptr(log_g), gate_row, _ptr(state), _ptr(conv_state), _ptr(state_out), _ptr(conv_out),
+                          _ptr(out_o), out_dtype, _banks_ref(banks), _ptr(err), _stream(stream)))
+
+
+def gdn_top_logprobs(rows: int, V: int, v_stride: int, dtype: int, logits, tokens, top_k: int, top_logp, top_token, given,
+                     entropy, err, stream=None):
+    _check(lib().gdn_top_logprobs(rows, V, v_stride, dtype, _ptr(logits), _ptr(tokens), top_k, _ptr(top_logp),
+                                  _ptr(top_token), _ptr(given), _ptr(entropy), _ptr(err), _stream(stream)))

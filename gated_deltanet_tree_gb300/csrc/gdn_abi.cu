@@ -10,6 +10,8 @@
 #include "gdn_accept.cuh"
 #include "gdn_internal.h"
 #include "gdn_kv4.cuh"
+#include "gdn_logprobs.cuh"
+#include "gdn_seq.cuh"
 
 namespace gdn {
 namespace {
@@ -138,8 +140,8 @@ gdn_status read_error_words(int32_t* err, cudaStream_t stream) {
     return fail(GDN_ERR_CACHE, "4-bit cache of request %d: a length, page number, path entry or row count is out of "
                 "range; the offending accesses were skipped", w[1] - 1);
   if (w[0] & GDN_DEVERR_LOGITS)
-    return fail(GDN_ERR_LOGITS, "request %d: a visited logits row holds no distribution, or its temperature is "
-                "negative or not finite; the walk stopped there", w[1] - 1);
+    return fail(GDN_ERR_LOGITS, "request (or row) %d: a visited logits row holds no distribution, or its "
+                "temperature is negative or not finite; nothing was taken from it", w[1] - 1);
   return fail(GDN_ERR_CUDA, "unknown device error word 0x%x", w[0]);
 }
 
@@ -571,6 +573,161 @@ gdn_status gdn_tree_accept(const gdn_batch_schedule* sched, int32_t V, int32_t v
   p.slices = workspace;
   cudaError_t e = gdn::launch_accept(p, stream);
   if (e != cudaSuccess) return cuda_fail(e, "acceptance launch");
+  return GDN_OK;
+}
+
+// ---- sequences through one layer ----
+
+namespace {
+
+bool known_dtype(int32_t t) { return t == GDN_DTYPE_F32 || t == GDN_DTYPE_BF16; }
+
+// An output that is its input's buffer, or does not overlap it.
+gdn_status check_moved(const void* in, const void* out, size_t bytes, const char* name) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(in), b = reinterpret_cast<uintptr_t>(out);
+  if (in && a != b && a < b + bytes && b < a + bytes)
+    return fail(GDN_ERR_INVALID_ARG, "%s_out overlaps %s without being it", name, name);
+  return GDN_OK;
+}
+
+// Everything that gdn_prefill and gdn_step share; fills p for the given layer.
+gdn_status check_seq(const gdn_dims* d, int32_t layers, int32_t layer, int32_t B, const void* x_raw, int64_t x_row,
+                     const float* conv_w, const void* beta, const void* log_g, int64_t gate_row, const float* state,
+                     const float* conv_state, float* state_out, float* conv_out, void* out_o, int32_t out_dtype,
+                     const gdn_banks* banks, int32_t* err, gdn::SeqParams& p) {
+  GDN_TRY(check_dims(d));
+  if (layers < 1 || layer < 0 || layer >= layers) return fail(GDN_ERR_INVALID_ARG, "layer %d of %d", layer, layers);
+  if (B < 1) return fail(GDN_ERR_INVALID_ARG, "B = %d", B);
+  const long long C = 2ll * d->Hk * d->dk + static_cast<long long>(d->Hv) * d->dv;
+  // the kernels number a request's CTAs (up to eight a k-head) and channels with 32 bits
+  if (C > (1 << 24) || static_cast<long long>(B) * d->Hk > (1 << 27) || static_cast<long long>(B) * d->Hv > (1 << 27))
+    return fail(GDN_ERR_UNSUPPORTED, "B = %d, Hk = %d, Hv = %d: too many heads", B, d->Hk, d->Hv);
+  if (!known_dtype(out_dtype)) return fail(GDN_ERR_INVALID_ARG, "out_dtype = %d", out_dtype);
+  const int vec = d->in_dtype == GDN_DTYPE_F32 ? 4 : 8;
+  if (x_row != 0 && (x_row < C || x_row % vec || x_row > INT32_MAX))
+    return fail(GDN_ERR_INVALID_ARG, "x_row = %lld: below C = %lld, above 2^31 or not a multiple of 16 bytes",
+                static_cast<long long>(x_row), C);
+  if (gate_row != 0 && (gate_row < d->Hv || gate_row > INT32_MAX))
+    return fail(GDN_ERR_INVALID_ARG, "gate_row = %lld, Hv = %d", static_cast<long long>(gate_row), d->Hv);
+  const bool conv = d->conv_mode == 1, window = conv && d->K > 1;
+  GDN_CHECK_PTR(x_raw, "x_raw");
+  if (conv) GDN_CHECK_PTR(conv_w, "conv_w");
+  // rows of gates lie where a fused projection puts them
+  if (!beta || !log_g) return fail(GDN_ERR_INVALID_ARG, "beta or log_g is NULL");
+  const uintptr_t one = d->in_dtype == GDN_DTYPE_F32 ? 3 : 1;
+  if ((reinterpret_cast<uintptr_t>(beta) | reinterpret_cast<uintptr_t>(log_g)) & one)
+    return fail(GDN_ERR_INVALID_ARG, "beta or log_g is not aligned to its elements");
+  if (state) GDN_CHECK_PTR(state, "state");
+  GDN_CHECK_PTR(state_out, "state_out");
+  if (window) {
+    if (conv_state) GDN_CHECK_PTR(conv_state, "conv_state");
+    GDN_CHECK_PTR(conv_out, "conv_out");
+  }
+  GDN_CHECK_PTR(out_o, "out_o");
+  GDN_CHECK_PTR(err, "err");
+  const long long tile = static_cast<long long>(d->Hv) * d->dk * d->dv, rows = conv ? (d->K - 1) * C : 0;
+  if (B * static_cast<long long>(layers) > (1ll << 60) / (4 * (tile > C * 8 ? tile : C * 8)))
+    return fail(GDN_ERR_UNSUPPORTED, "B = %d, layers = %d", B, layers);
+  GDN_TRY(check_moved(state, state_out, static_cast<size_t>(B) * layers * tile * sizeof(float), "state"));
+  if (window) GDN_TRY(check_moved(conv_state, conv_out, static_cast<size_t>(B) * layers * rows * sizeof(float), "conv"));
+  if (banks) {
+    if (banks->B != B || banks->layers != layers)
+      return fail(GDN_ERR_CAPACITY, "banks sized for B=%d layers=%d, call has B=%d layers=%d", banks->B, banks->layers, B,
+                  layers);
+    if (banks->verified_bank >= 0) return fail(GDN_ERR_STATE, "a verified tree is not committed (gdn_commit_fold, then gdn_finish)");
+    if (banks->pend_bank >= 0) return fail(GDN_ERR_STATE, "a committed path is not in the state yet (gdn_finish folds it in)");
+  }
+  p.Hk = d->Hk; p.Hv = d->Hv; p.dk = d->dk; p.dv = d->dv; p.K = conv ? d->K : 1; p.C = static_cast<int>(C);
+  p.conv_mode = d->conv_mode; p.act = d->act; p.in_dtype = d->in_dtype; p.out_dtype = out_dtype;
+  p.q_scale = d->q_scale; p.l2_eps = d->l2_eps;
+  p.x_row = x_row ? x_row : C; p.gate_row = gate_row ? gate_row : d->Hv;
+  p.x = x_raw; p.beta = beta; p.log_g = log_g;
+  p.conv_w = conv ? conv_w + static_cast<long long>(layer) * C * d->K : nullptr;
+  p.state_in = state ? state + layer * tile : nullptr;
+  p.state_out = state_out + layer * tile;
+  p.conv_in = window && conv_state ? conv_state + layer * rows : nullptr;
+  p.conv_out = window ? conv_out + layer * rows : nullptr;
+  p.state_stride = layers * tile; p.conv_stride = layers * rows;
+  p.out = out_o; p.err = err;
+  return GDN_OK;
+}
+
+}  // namespace
+
+size_t gdn_prefill_workspace_bytes(const gdn_dims* d) { return check_dims(d) == GDN_OK ? gdn::seq_workspace_bytes(*d) : 0; }
+
+gdn_status gdn_prefill(const gdn_dims* d, int32_t layers, int32_t layer, int32_t B, const int32_t* lens,
+                       const void* x_raw, int64_t x_row, const float* conv_w, const void* beta, const void* log_g,
+                       int64_t gate_row, const float* state, const float* conv_state, float* state_out, float* conv_out,
+                       void* out_o, int32_t out_dtype, const gdn_banks* banks, int32_t* err, void* workspace,
+                       size_t workspace_bytes, cudaStream_t stream) {
+  gdn::clear_error();
+  gdn::SeqParams p{};
+  if (!lens) return fail(GDN_ERR_INVALID_ARG, "lens is NULL");
+  long long rows = 0;
+  for (int32_t b = 0; b < B; ++b) {
+    if (lens[b] < 0) return fail(GDN_ERR_INVALID_ARG, "lens[%d] = %d", b, lens[b]);
+    rows += lens[b];
+  }
+  if (rows > INT32_MAX) return fail(GDN_ERR_UNSUPPORTED, "%lld rows", rows);
+  GDN_TRY(check_seq(d, layers, layer, B, x_raw, x_row, conv_w, beta, log_g, gate_row, state, conv_state, state_out,
+                    conv_out, out_o, out_dtype, banks, err, p));
+  GDN_CHECK_PTR(workspace, "workspace");
+  const size_t need = gdn::seq_workspace_bytes(*d);
+  if (workspace_bytes < need)
+    return fail(GDN_ERR_CAPACITY, "workspace holds %zu bytes, the call needs %zu", workspace_bytes, need);
+  cudaError_t e = gdn::launch_prefill(p, lens, B, workspace, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "prefill launch");
+  return GDN_OK;
+}
+
+gdn_status gdn_step(const gdn_dims* d, int32_t layers, int32_t layer, int32_t B, const int32_t* live, const void* x_raw,
+                    int64_t x_row, const float* conv_w, const void* beta, const void* log_g, int64_t gate_row,
+                    const float* state, const float* conv_state, float* state_out, float* conv_out, void* out_o,
+                    int32_t out_dtype, const gdn_banks* banks, int32_t* err, cudaStream_t stream) {
+  gdn::clear_error();
+  gdn::SeqParams p{};
+  GDN_TRY(check_seq(d, layers, layer, B, x_raw, x_row, conv_w, beta, log_g, gate_row, state, conv_state, state_out,
+                    conv_out, out_o, out_dtype, banks, err, p));
+  if (live) GDN_CHECK_PTR(live, "live");
+  p.live = live;
+  cudaError_t e = gdn::launch_seq_rec(p, nullptr, B, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "step launch");
+  return GDN_OK;
+}
+
+// ---- log-probabilities ----
+
+gdn_status gdn_top_logprobs(int32_t rows, int32_t V, int64_t v_stride, int32_t dtype, const void* logits,
+                            const int32_t* tokens, int32_t top_k, float* top_logp, int32_t* top_token, float* given,
+                            float* entropy, int32_t* err, cudaStream_t stream) {
+  gdn::clear_error();
+  if (rows < 1 || V < 1) return fail(GDN_ERR_INVALID_ARG, "rows = %d, V = %d", rows, V);
+  if (V > gdn::kLogprobVocab) return fail(GDN_ERR_UNSUPPORTED, "V = %d above %d", V, gdn::kLogprobVocab);
+  if (rows > INT32_MAX / 8) return fail(GDN_ERR_UNSUPPORTED, "rows = %d", rows);
+  if (v_stride != 0 && v_stride < V)
+    return fail(GDN_ERR_INVALID_ARG, "v_stride = %lld, V = %d", static_cast<long long>(v_stride), V);
+  if (v_stride > (1ll << 60) / (4ll * rows))
+    return fail(GDN_ERR_UNSUPPORTED, "v_stride = %lld", static_cast<long long>(v_stride));
+  if (!known_dtype(dtype)) return fail(GDN_ERR_INVALID_ARG, "dtype = %d", dtype);
+  if (top_k < 1 || top_k > V) return fail(GDN_ERR_INVALID_ARG, "top_k = %d, V = %d", top_k, V);
+  if (top_k > GDN_MAX_TOP) return fail(GDN_ERR_UNSUPPORTED, "top_k = %d above %d", top_k, GDN_MAX_TOP);
+  GDN_CHECK_PTR(logits, "logits");
+  if ((tokens == nullptr) != (given == nullptr)) return fail(GDN_ERR_INVALID_ARG, "tokens and given: both or neither");
+  if (tokens) {
+    GDN_CHECK_PTR(tokens, "tokens");
+    GDN_CHECK_PTR(given, "given");
+  }
+  GDN_CHECK_PTR(top_logp, "top_logp");
+  GDN_CHECK_PTR(top_token, "top_token");
+  if (entropy) GDN_CHECK_PTR(entropy, "entropy");
+  GDN_CHECK_PTR(err, "err");
+  gdn::LogprobParams p{};
+  p.rows = rows; p.V = V; p.top = top_k; p.dtype = dtype; p.v_stride = v_stride ? v_stride : V;
+  p.logits = logits; p.tokens = tokens; p.top_logp = top_logp; p.top_token = top_token;
+  p.given = given; p.entropy = entropy; p.err = err;
+  cudaError_t e = gdn::launch_logprobs(p, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "log-probability launch");
   return GDN_OK;
 }
 

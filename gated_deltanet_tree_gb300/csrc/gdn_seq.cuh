@@ -1,0 +1,38 @@
+// Parameters of the kernels that take sequences (prompts, single tokens) through one GDN layer.
+#pragma once
+#include "gdn_internal.h"
+
+namespace gdn {
+
+struct SeqParams {
+  int Hk, Hv, dk, dv, K, C, conv_mode, act, in_dtype, out_dtype;
+  float q_scale, l2_eps;
+  long long x_row, gate_row;            // elements from one token's row to the next
+  const void* x;                        // [rows][C]
+  const float* conv_w;                  // [C][K], the layer's
+  const void* beta;                     // [rows][Hv]
+  const void* log_g;
+  const float* state_in;                // the layer's, request 0; nullptr: zero states
+  const float* conv_in;                 // nullptr: zero windows
+  float* state_out;
+  float* conv_out;
+  long long state_stride, conv_stride;  // floats from one request to the next
+  void* out;                            // [rows][Hv][dv] out_dtype
+  const int32_t* live;                  // [requests] (single tokens only): 0 leaves the request as it is; nullptr: all
+  int32_t* err;
+};
+// The requests of one launch: where their rows begin and how many there are.
+constexpr int kSeqReqs = 128;
+struct SeqReqs {
+  int n;
+  int b[kSeqReqs], start[kSeqReqs], len[kSeqReqs];
+};
+
+// Token by token; reqs nullptr: requests 0 .. n - 1 with one row each.
+cudaError_t launch_seq_rec(const SeqParams& p, const SeqReqs* reqs, int n, cudaStream_t s);
+
+// A ragged batch of prompts: lens[b] rows of each of B requests, one after another.
+size_t seq_workspace_bytes(const gdn_dims& d);
+cudaError_t launch_prefill(const SeqParams& p, const int32_t* lens, int B, void* workspace, cudaStream_t s);
+
+}  // namespace gdn

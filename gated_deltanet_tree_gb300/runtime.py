@@ -396,3 +396,161 @@ class TreeAcceptor:
 
     def check_error(self, stream=None):
         N.gdn_check_error_words(self.err, stream)
+
+
+class SequenceRunner:
+    """Prompts and single tokens through the GDN layers of a stack: the error words and the workspace of the calls.
+
+    The caller owns the states and conv windows, [B, layers, Hv, dk, dv] and [B, layers, K - 1, C], the same that a
+    TreeVerifier's calls take.  Given that verifier, a call is refused while it holds a verified or committed tree that
+    the states do not (its finish() folds that in), and errors are reported through it as well.
+
+    A call may go to any stream, or into a CUDA graph (prefill with the lengths it was captured with).  prefill calls
+    share the workspace, so they must follow one another; step calls share nothing."""
+
+    def __init__(self, dims: N.gdn_dims, B: int, layers: int = 1, device="cuda", verifier: Optional[TreeVerifier] = None):
+        if verifier is not None and (verifier.B, verifier.layers) != (B, layers):
+            raise ValueError(f"the verifier's batch and layers are {verifier.B}, {verifier.layers}")
+        self.dims, self.B, self.layers = N.gdn_dims.from_buffer_copy(dims), B, layers
+        self.device = torch.device(device)
+        self.verifier = verifier
+        self.err = verifier.err if verifier is not None else torch.zeros(4, dtype=torch.int32, device=self.device)
+        self._banks = verifier.banks if verifier is not None else None
+        self.C = channels(dims)
+        self.workspace = torch.empty(max(256, N.gdn_prefill_workspace_bytes(self.dims)), dtype=torch.uint8,
+                                     device=self.device)
+        self._index = self.err.get_device()
+        self._type = torch.bfloat16 if dims.in_dtype == N.GDN_DTYPE_BF16 else torch.float32
+        d = dims
+        self._state = (B, layers, d.Hv, d.dk, d.dv)
+        self._window = (B, layers, d.K - 1, self.C) if d.conv_mode == 1 else None
+        self._taps = (layers, self.C, d.K)
+        self._ref = ctypes.byref(self.dims)
+        _finish_fills(self.device)
+
+    def _f32(self, t: torch.Tensor, name: str, shape: tuple) -> int:
+        if t.shape != shape or t.dtype is not torch.float32 or not t.is_contiguous() or t.get_device() != self._index:
+            raise ValueError(f"{name} is a contiguous float32 tensor {shape} on {self.device}, got {tuple(t.shape)} "
+                             f"{t.dtype} on {t.device}")
+        return t.data_ptr()
+
+    def _rows(self, t: torch.Tensor, name: str, rows: int, width: int) -> int:
+        """Elements from one token's row to the next."""
+        if t.dtype is not self._type or t.get_device() != self._index or t.shape != (rows, width):
+            raise ValueError(f"{name} is {self._type} ({rows}, {width}) on {self.device}, got {tuple(t.shape)} {t.dtype} "
+                             f"on {t.device}")
+        if t.is_contiguous():
+            return width
+        if t.stride(1) != 1 and width > 1:
+            raise ValueError(f"{name} has strides {t.stride()}: a row's values are contiguous")
+        return _stride_in_range(t.stride(0), width, name) if rows > 1 else width
+
+    def _args(self, rows, x_raw, conv_w, beta, log_g, state, conv_state, out, state_out, conv_out) -> tuple:
+        d = self.dims
+        x_row = self._rows(x_raw, "x_raw", rows, self.C)
+        gate_row = self._rows(beta, "beta", rows, d.Hv)
+        if self._rows(log_g, "log_g", rows, d.Hv) != gate_row:
+            raise ValueError("beta and log_g have different row strides")
+        if out.shape != (rows, d.Hv, d.dv) or not out.is_contiguous() or out.get_device() != self._index:
+            raise ValueError(f"out is a contiguous tensor {(rows, d.Hv, d.dv)} on {self.device}, got {tuple(out.shape)} on "
+                             f"{out.device}")
+        state_out = state if state_out is None else state_out
+        if state_out is None:
+            raise ValueError("state_out is needed where state is None")
+        s_in = None if state is None else self._f32(state, "state", self._state)
+        s_out = self._f32(state_out, "state_out", self._state)
+        w = c_in = c_out = None
+        if self._window is not None:
+            w = self._f32(conv_w, "conv_w", self._taps)
+            conv_out = conv_state if conv_out is None else conv_out
+            if conv_out is None:
+                raise ValueError("conv_out is needed where conv_state is None")
+            c_in = None if conv_state is None else self._f32(conv_state, "conv_state", self._window)
+            c_out = self._f32(conv_out, "conv_out", self._window)
+        return (x_raw.data_ptr(), x_row, w, beta.data_ptr(), log_g.data_ptr(), gate_row, s_in, c_in, s_out, c_out,
+                out.data_ptr(), _dtype_code(out.dtype, "out"), N._banks_ref(self._banks), self.err.data_ptr())
+
+    def prefill(self, lens: Sequence[int], x_raw: torch.Tensor, conv_w: Optional[torch.Tensor], beta: torch.Tensor,
+                log_g: torch.Tensor, state: Optional[torch.Tensor], conv_state: Optional[torch.Tensor], out: torch.Tensor,
+                layer: int = 0, state_out: Optional[torch.Tensor] = None, conv_out: Optional[torch.Tensor] = None,
+                stream=None):
+        """lens[b] rows of request b, one request after another: x_raw [rows, C], beta and log_g [rows, Hv] -> out
+        [rows, Hv, dv], fp32 or bf16.  The states and windows are updated in place, or written to state_out and conv_out;
+        None in their place: the requests start from zeros."""
+        lens = np.ascontiguousarray(lens, dtype=np.int32)
+        if lens.shape != (self.B,):
+            raise ValueError(f"lens holds {lens.shape} lengths for {self.B} requests")
+        rows = int(lens.sum(dtype=np.int64))
+        if rows == 0 and (lens == 0).all():
+            return
+        args = self._args(rows, x_raw, conv_w, beta, log_g, state, conv_state, out, state_out, conv_out)
+        N._check(N.lib().gdn_prefill(self._ref, self.layers, layer, self.B,
+                                     lens.ctypes.data_as(ctypes.POINTER(ctypes.c_int32)), *args,
+                                     self.workspace.data_ptr(), self.workspace.numel(), N._stream_of(stream, self._index)))
+
+    def step(self, x_raw: torch.Tensor, conv_w: Optional[torch.Tensor], beta: torch.Tensor, log_g: torch.Tensor,
+             state: Optional[torch.Tensor], conv_state: Optional[torch.Tensor], out: torch.Tensor, layer: int = 0,
+             state_out: Optional[torch.Tensor] = None, conv_out: Optional[torch.Tensor] = None,
+             live: Optional[torch.Tensor] = None, stream=None):
+        """One token of every request: x_raw [B, C], beta and log_g [B, Hv] -> out [B, Hv, dv]; the rest as in prefill.
+        Requests where live [B] int32 is 0 are left as they are."""
+        args = self._args(self.B, x_raw, conv_w, beta, log_g, state, conv_state, out, state_out, conv_out)
+        if live is not None and (live.dtype is not torch.int32 or live.shape != (self.B,) or not live.is_contiguous()
+                                 or live.get_device() != self._index):
+            raise ValueError(f"live is a contiguous int32 tensor ({self.B},) on {self.device}, got {tuple(live.shape)} "
+                             f"{live.dtype} on {live.device}")
+        N._check(N.lib().gdn_step(self._ref, self.layers, layer, self.B, None if live is None else live.data_ptr(), *args,
+                                  N._stream_of(stream, self._index)))
+
+    def check_error(self, stream=None):
+        N.gdn_check_error_words(self.err, stream)
+
+
+class TokenScorer:
+    """Outputs and error words of the log-probabilities of up to `rows` rows of logits: the best top_k tokens' (what
+    gdn_ddtree_build takes), given tokens', and the entropies."""
+
+    def __init__(self, rows: int, V: int, top_k: int, device="cuda"):
+        if not 1 <= top_k <= min(V, N.GDN_MAX_TOP):
+            raise ValueError(f"top_k = {top_k}: 1 to {min(V, N.GDN_MAX_TOP)}")
+        self.rows, self.V, self.top_k = rows, V, top_k
+        self.device = torch.device(device)
+        self.top = torch.zeros(rows, top_k, device=self.device)
+        self.tokens = torch.full((rows, top_k), -1, dtype=torch.int32, device=self.device)
+        self.given = torch.zeros(rows, device=self.device)
+        self.entropy = torch.zeros(rows, device=self.device)
+        self.err = torch.zeros(4, dtype=torch.int32, device=self.device)
+        self._index = self.top.get_device()
+        self._out = (self.top.data_ptr(), self.tokens.data_ptr())
+        _finish_fills(self.device)
+
+    def score(self, logits: torch.Tensor, tokens: Optional[torch.Tensor] = None, stream=None):
+        """logits [n, V] -> (top [n, top_k], their tokens [n, top_k], the given tokens' [n] or None, entropy [n]): this
+        object's buffers, the first n rows of them."""
+        if logits.dim() != 2 or logits.shape[1] != self.V or not 1 <= logits.shape[0] <= self.rows \
+                or logits.get_device() != self._index:
+            raise ValueError(f"logits is (1 .. {self.rows}, {self.V}) on {self.device}, got {tuple(logits.shape)} on "
+                             f"{logits.device}")
+        n = logits.shape[0]
+        row = self.V
+        if not logits.is_contiguous():
+            if self.V > 1 and logits.stride(1) != 1:
+                raise ValueError(f"logits has strides {logits.stride()}: a row's values are contiguous")
+            if n > 1:
+                row = _stride_in_range(logits.stride(0), self.V, "logits")
+        tok = None
+        if tokens is not None:
+            if tokens.dtype is not torch.int32 or tokens.shape != (n,) or not tokens.is_contiguous() \
+                    or tokens.get_device() != self._index:
+                raise ValueError(f"tokens is a contiguous int32 tensor ({n},) on {self.device}, got {tuple(tokens.shape)} "
+                                 f"{tokens.dtype} on {tokens.device}")
+            tok = tokens.data_ptr()
+        N._check(N.lib().gdn_top_logprobs(n, self.V, row, _dtype_code(logits.dtype, "logits"), logits.data_ptr(), tok,
+                                          self.top_k, *self._out, None if tok is None else self.given.data_ptr(),
+                                          self.entropy.data_ptr(), self.err.data_ptr(),
+                                          N._stream_of(stream, self._index)))
+        given = None if tok is None else self.given[:n]
+        return self.top[:n], self.tokens[:n], given, self.entropy[:n]
+
+    def check_error(self, stream=None):
+        N.gdn_check_error_words(self.err, stream)

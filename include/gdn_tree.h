@@ -52,7 +52,7 @@
 extern "C" {
 #endif
 
-#define GDN_ABI_VERSION 3
+#define GDN_ABI_VERSION 4
 #define GDN_MAX_NODES 64   /* largest tree (n_max) the kernels accept */
 #define GDN_MAX_TAPS 8     /* largest conv kernel K */
 
@@ -78,7 +78,7 @@ typedef enum { GDN_DTYPE_F32 = 0, GDN_DTYPE_BF16 = 1 } gdn_dtype;
 #define GDN_DEVERR_SCHEDULE 2      /* packed schedule words out of range; the access was skipped */
 #define GDN_DEVERR_TIMEOUT 4       /* an asynchronous copy or MMA did not complete in time; the CTA stopped */
 #define GDN_DEVERR_CACHE 8         /* 4-bit cache: length, page number or row count out of range; the access was skipped */
-#define GDN_DEVERR_LOGITS 16       /* acceptance: a visited row has a NaN, a +inf or no finite logit; the walk stopped there */
+#define GDN_DEVERR_LOGITS 16       /* acceptance, log-probabilities: a (visited) row has a NaN, a +inf or no finite logit; the walk stopped there */
 
 /* Shapes and modes of one GDN layer stack. */
 typedef struct {
@@ -531,8 +531,72 @@ gdn_status gdn_tree_accept(const gdn_batch_schedule* sched, int32_t V, int32_t v
                            int32_t* len, int32_t* next, int32_t* err, void* workspace, size_t workspace_bytes,
                            cudaStream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * gdn_prefill -- a batch of prompts through one GDN layer (before a request's first tree; the
+ * chunked Gated DeltaNet form of the SpecLA article, "想深入源码").
+ * Request b has lens[b] tokens (host; 0: it takes no part, nothing of it is read or written), whose
+ * rows follow those of request b - 1.  Every token takes the step stated at the top of this file,
+ * from the state and conv window given, which may be an earlier part of the same prompt's.
+ *   layers, layer  the stack of state, conv_state and conv_w, and which of it this call is for
+ *   lens       [B] host
+ *   x_raw      [rows][C] in_dtype, rows = sum of lens, x_row elements apart (0: C; rows start
+ *              on 16 bytes)
+ *   beta, log_g [rows][Hv] in_dtype, gate_row elements apart (0: Hv).  log_g -inf (forget
+ *              everything) is fine; above 0 the state grows, which fp32 must hold
+ *   conv_w     [layers][C][K] fp32 (conv_mode 1; else may be NULL)
+ *   state      [B][layers][Hv][dk][dv] fp32: before the call; NULL: zeros
+ *   conv_state [B][layers][K-1][C] fp32: raw rows before the call, oldest first; NULL: zeros
+ *   state_out, conv_out  the same after the call.  Each may be the buffer it came from, or one
+ *              that does not overlap it (a prefix that several requests continue is kept)
+ *   out_o      [rows][Hv][dv] out_dtype
+ *   banks      NULL, or the banks of the stack's tree verifies: GDN_ERR_STATE while a verified tree
+ *              is not committed or a committed path is pending, which `state` does not hold yet
+ *              (gdn_finish folds it in)
+ *   err        error words (int32 [4], as gdn_banks.err, or those themselves)
+ *   workspace  >= gdn_prefill_workspace_bytes(d) bytes; nothing in it needs clearing; calls that may
+ *              overlap need one each
+ * The lengths are the host's, so a captured call replays with the same ones.
+ * ------------------------------------------------------------------------- */
+size_t gdn_prefill_workspace_bytes(const gdn_dims* d);
+gdn_status gdn_prefill(const gdn_dims* d, int32_t layers, int32_t layer, int32_t B, const int32_t* lens,
+                       const void* x_raw, int64_t x_row, const float* conv_w, const void* beta, const void* log_g,
+                       int64_t gate_row, const float* state, const float* conv_state, float* state_out, float* conv_out,
+                       void* out_o, int32_t out_dtype, const gdn_banks* banks, int32_t* err, void* workspace,
+                       size_t workspace_bytes, cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * gdn_step -- one token of every request through one GDN layer (plain decoding).
+ * As gdn_prefill with one row a request, and no workspace.
+ *   live       [B] device int32, or NULL: all.  Where it is 0 the request takes no part: nothing
+ *              of it is read or written (ended requests of a captured batch)
+ * ------------------------------------------------------------------------- */
+gdn_status gdn_step(const gdn_dims* d, int32_t layers, int32_t layer, int32_t B, const int32_t* live, const void* x_raw,
+                    int64_t x_row, const float* conv_w, const void* beta, const void* log_g, int64_t gate_row,
+                    const float* state, const float* conv_state, float* state_out, float* conv_out, void* out_o,
+                    int32_t out_dtype, const gdn_banks* banks, int32_t* err, cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * gdn_top_logprobs -- log-probabilities of rows of logits: the best tokens' (the draft's candidates
+ * that gdn_ddtree_build takes), a given token's, and the entropy.
+ *   logits  [rows] rows of V values, dtype, v_stride elements apart (0: V); -inf masks a token.
+ *           Rows may have any alignment
+ *   tokens  [rows] int32, or NULL: the given tokens; one outside [0, V) gives NaN
+ *   top_k   1 .. min(V, GDN_MAX_TOP)
+ *   top_logp, top_token [rows][top_k] fp32, int32 out: larger logits first, the lower index on ties;
+ *           masked tokens (-inf) come last
+ *   given   [rows] fp32 out: the given token's log-probability (NULL where tokens is)
+ *   entropy [rows] fp32 out, or NULL: -sum p log p in nats
+ * A row with a NaN, a +inf or no finite logit sets GDN_DEVERR_LOGITS in err (int32 [4], as
+ * gdn_banks.err; the request it names is the row) and gives NaN and tokens -1.
+ * GDN_ERR_UNSUPPORTED: V above 2^30, top_k above GDN_MAX_TOP.
+ * ------------------------------------------------------------------------- */
+#define GDN_MAX_TOP 32
+gdn_status gdn_top_logprobs(int32_t rows, int32_t V, int64_t v_stride, int32_t dtype, const void* logits,
+                            const int32_t* tokens, int32_t top_k, float* top_logp, int32_t* top_token, float* given,
+                            float* entropy, int32_t* err, cudaStream_t stream);
+
 /* Synchronise the stream, read and clear a caller's error words (int32 [4]) as
- * gdn_check_error does for banks->err: of a gdn_kv4_cache or of gdn_tree_accept. */
+ * gdn_check_error does for banks->err: of a gdn_kv4_cache, or of the calls that take err. */
 gdn_status gdn_check_error_words(int32_t* err, cudaStream_t stream);
 
 /* Synchronise the stream, read and clear banks->err.  Returns GDN_OK or the
