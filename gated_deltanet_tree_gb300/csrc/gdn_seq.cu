@@ -1,26 +1,77 @@
-// Which kernels take a batch of prompts.
+// Which kernels take a batch of prompts, and in which order.
+//
+// Prompts of more than kTokenByToken rows go through the chunked form, 64 tokens at a time.  As many requests as fill the
+// GPU with heads are in work together, the longest first; a segment is the next few chunks of each, as many as the
+// workspace has places for.  Its operands are prepared, then run through; the next segment finds the states where this
+// one left them.  The workspace is sized to stay in L2 between the two.
+#include <algorithm>
+#include <new>
+
 #include "gdn_seq.cuh"
 
 namespace gdn {
+namespace {
 
-size_t seq_workspace_bytes(const gdn_dims&) { return 256; }
+constexpr int kTokenByToken = 8;
+constexpr size_t kWorkspace = 104u << 20;
 
-cudaError_t launch_prefill(const SeqParams& p, const int32_t* lens, int B, void*, cudaStream_t s) {
-  SeqReqs r{};
-  int start = 0;
+int workspace_slots(const size_t slot) {
+  const size_t n = kWorkspace / slot;
+  return n < 16 ? 16 : n > 1024 ? 1024 : static_cast<int>(n);
+}
+
+}  // namespace
+
+size_t seq_workspace_bytes(const gdn_dims& d) {
+  const size_t slot = seq_slot_bytes(d.Hk, d.Hv, d.dk, d.dv);
+  return workspace_slots(slot) * slot;
+}
+
+cudaError_t launch_prefill(const SeqParams& p, const int32_t* lens, int B, void* workspace, cudaStream_t s) {
+  SeqReqs few{};
+  const int at_once = seq_requests_at_once(p.Hv), slots = workspace_slots(seq_slot_bytes(p.Hk, p.Hv, p.dk, p.dv));
+  SegReq* todo = new (std::nothrow) SegReq[B];
+  if (!todo) return cudaErrorMemoryAllocation;
+  int n = 0, start = 0;
+  cudaError_t e = cudaSuccess;
   for (int b = 0; b < B; ++b) {
-    if (lens[b] > 0) {
-      r.b[r.n] = b, r.start[r.n] = start, r.len[r.n] = lens[b];
-      ++r.n;
+    if (lens[b] > kTokenByToken) {
+      todo[n++] = SegReq{b, start, lens[b], 0, 0, 0};
+    } else if (lens[b] > 0) {
+      few.b[few.n] = b, few.start[few.n] = start, few.len[few.n] = lens[b];
+      ++few.n;
     }
     start += lens[b];
-    if (r.n == kSeqReqs || (b == B - 1 && r.n > 0)) {
-      const cudaError_t e = launch_seq_rec(p, &r, r.n, s);
-      if (e != cudaSuccess) return e;
-      r.n = 0;
+    if (few.n == kSeqReqs || (b == B - 1 && few.n > 0)) {
+      if (e == cudaSuccess) e = launch_seq_rec(p, &few, few.n, s);
+      few.n = 0;
     }
   }
-  return cudaSuccess;
+  std::sort(todo, todo + n, [](const SegReq& a, const SegReq& c) { return a.len != c.len ? a.len > c.len : a.b < c.b; });
+  Segment seg{};
+  int active[kSegReqs], n_active = 0, next = 0;
+  while (e == cudaSuccess && (n_active > 0 || next < n)) {
+    while (n_active < std::min(at_once, slots) && next < n) active[n_active++] = next++;
+    const int share = slots / n_active;
+    seg.n = seg.slots = 0;
+    for (int i = 0; i < n_active; ++i) {
+      SegReq& r = todo[active[i]];
+      r.c0 += r.nc;
+      r.nc = std::min(share, (r.len + kChunk - 1) / kChunk - r.c0);
+      r.slot0 = seg.slots;
+      seg.slots += r.nc;
+      seg.r[seg.n++] = r;
+    }
+    e = launch_seq_chunks(p, seg, workspace, s);
+    int left = 0;
+    for (int i = 0; i < n_active; ++i) {
+      const SegReq& r = todo[active[i]];
+      if ((r.c0 + r.nc) * kChunk < r.len) active[left++] = active[i];
+    }
+    n_active = left;
+  }
+  delete[] todo;
+  return e;
 }
 
 }  // namespace gdn

@@ -31,6 +31,28 @@ struct SeqReqs {
 // Token by token; reqs nullptr: requests 0 .. n - 1 with one row each.
 cudaError_t launch_seq_rec(const SeqParams& p, const SeqReqs* reqs, int n, cudaStream_t s);
 
+// ---- the chunked form: 64 tokens at a time ----
+constexpr int kChunk = 64;
+// Bytes of one chunk's operands in the workspace (see gdn_seq_chunk.cu), for one k-head and for one v-head.
+__host__ __device__ constexpr size_t seq_kq_bytes(int dk) { return 4ull * kChunk * dk * 2; }
+constexpr int kSeqMeta = 2 * kChunk + 16;                      // floats
+__host__ __device__ constexpr size_t seq_v_bytes(int dv) { return 2ull * 128 * kChunk * 2 + kChunk * dv * 4ull + kSeqMeta * 4ull; }
+__host__ __device__ constexpr size_t seq_slot_bytes(int Hk, int Hv, int dk, int dv) {
+  return Hk * seq_kq_bytes(dk) + Hv * seq_v_bytes(dv);
+}
+// A stretch of chunks of several requests, prepared and then run through.
+constexpr int kSegReqs = 64;
+struct SegReq {
+  int b, start, len;           // request, its first row, its rows
+  int c0, nc, slot0;           // first chunk, chunks, place of the first in the workspace
+};
+struct Segment {
+  int n, slots;
+  SegReq r[kSegReqs];
+};
+cudaError_t launch_seq_chunks(const SeqParams& p, const Segment& seg, void* workspace, cudaStream_t s);
+int seq_requests_at_once(int Hv);   // requests whose heads fill the GPU
+
 // A ragged batch of prompts: lens[b] rows of each of B requests, one after another.
 size_t seq_workspace_bytes(const gdn_dims& d);
 cudaError_t launch_prefill(const SeqParams& p, const int32_t* lens, int B, void* workspace, cudaStream_t s);
