@@ -34,7 +34,7 @@ cudaError_t launch_seq_rec(const SeqParams& p, const SeqReqs* reqs, int n, cudaS
 // ---- the chunked form: 64 tokens at a time ----
 constexpr int kChunk = 64;
 // Bytes of one chunk's operands in the workspace (see gdn_seq_chunk.cu), for one k-head and for one v-head.
-__host__ __device__ constexpr size_t seq_kq_bytes(int dk) { return 4ull * kChunk * dk * 2; }
+__host__ __device__ constexpr size_t seq_kq_bytes(int dk) { return 4ull * kChunk * dk * 2 + 2ull * kChunk * kChunk * 4; }
 constexpr int kSeqMeta = 2 * kChunk + 16;                      // floats
 __host__ __device__ constexpr size_t seq_v_bytes(int dv) { return 2ull * 128 * kChunk * 2 + kChunk * dv * 4ull + kSeqMeta * 4ull; }
 __host__ __device__ constexpr size_t seq_slot_bytes(int Hk, int Hv, int dk, int dv) {
@@ -51,7 +51,6 @@ struct Segment {
   SegReq r[kSegReqs];
 };
 cudaError_t launch_seq_chunks(const SeqParams& p, const Segment& seg, void* workspace, cudaStream_t s);
-int seq_requests_at_once(int Hv);   // requests whose heads fill the GPU
 
 // A ragged batch of prompts: lens[b] rows of each of B requests, one after another.
 size_t seq_workspace_bytes(const gdn_dims& d);

@@ -11,10 +11,12 @@
 //
 // Precision: operands enter the products as two fp16 terms, x = hi + lo, and hi hi + hi lo + lo hi is accumulated in fp32:
 // 22 bits of every element, half the tensor-core time of a tf32 split in three.  fp16's range is met by powers of two: k
-// and q are normalised (2^12), M, N and T scaled by their largest entry, w and u by bounds that follow from those of T
+// and q are normalised (2^12), M and N scaled by their largest entry, w and u by bounds that follow from those of T
 // and v:  |w| <= max v + max e^c sqrt(dk) max T,  |u| <= max_i sum_j |M_ij| max w.  An element keeps 2^-23 of itself or
-// 2^-40 of the bound, and the bounds lie some 2^6 above the values.  Where they lie 2^17 above the largest entry of T' or of
-// the chunk's o (values that shrink or grow by that much within 64 tokens), the chunk is taken again token by token.
+// 2^-40 of the bound, and the bounds lie some 2^6 above the values.  T' is handed on scaled by a bound as well,
+// |T'| <= e^c max T + 64 max u, some 2^11 above it, and the largest entry is looked at afterwards: no warp waits for the
+// others'.  Where a bound turns out to lie 2^17 above the largest entry of T' or of the chunk's o (values that shrink or grow
+// by that much within 64 tokens), T' is handed on again, or the chunk is taken again, token by token.
 //
 // Operands in shared memory have no swizzle: 8 rows x 16 bytes are 128 contiguous bytes.  With 16 bytes of d_k per
 // token, a core matrix of K serves as K-major operand of D1 and as M-major operand of D3.
@@ -52,7 +54,7 @@ __device__ __forceinline__ bool elect_one() {
   asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(yes));
   return yes != 0;
 }
-// D = A B in two-term operands, K elements deep: `steps` instructions of 16 each, three times.  Descriptors of the high
+// D = A B in two-term operands, K elements deep: `kSteps` instructions of 16 each, three times.  Descriptors of the high
 // terms; the low ones lie a_lo and b_lo bytes behind.  a_step, b_step: bytes from one instruction's operands to the next.
 template <int kSteps>
 __device__ __forceinline__ void product(uint32_t d, uint64_t a, uint64_t b, uint32_t a_lo, uint32_t b_lo, uint32_t a_step,
@@ -65,6 +67,17 @@ __device__ __forceinline__ void product(uint32_t d, uint64_t a, uint64_t b, uint
 #pragma unroll
   for (int i = 0; i < kSteps; ++i) umma_f16_ss(d, a + al + i * as, b + i * bs, idesc, 1);
 }
+// The same where b's low terms are its columns n .. 2 n - 1: one instruction takes both (the high terms of A are read once
+// instead of twice; an instruction of 64 columns is bound by those reads).  D is columns 0 .. n - 1 plus n .. 2 n - 1.
+template <int kSteps, int n>
+__device__ __forceinline__ void product_wide(uint32_t d, uint64_t a, uint64_t b, uint32_t a_lo, uint32_t a_step, uint32_t b_step,
+                                             bool a_mn) {
+  const uint64_t al = a_lo >> 4, as = a_step >> 4, bs = b_step >> 4;
+#pragma unroll
+  for (int i = 0; i < kSteps; ++i) umma_f16_ss(d, a + i * as, b + i * bs, idesc_f16(2 * n, a_mn, true), i > 0);
+#pragma unroll
+  for (int i = 0; i < kSteps; ++i) umma_f16_ss(d, a + al + i * as, b + i * bs, idesc_f16(n, a_mn, true), 1);
+}
 // Two values as fp16 pairs of their high and low terms.
 __device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& lo) {
   const __half2 h = __floats2half2_rn(x, y);
@@ -72,6 +85,54 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t&
   const __half2 l = __floats2half2_rn(x - f.x, y - f.y);
   hi = *reinterpret_cast<const uint32_t*>(&h);
   lo = *reinterpret_cast<const uint32_t*>(&l);
+}
+__device__ __forceinline__ u64 add2(u64 a, u64 b) {
+  u64 d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+// Sixteen columns at `ta` and sixteen at `tb`, added.
+__device__ __forceinline__ void tmem_sum_pairs(uint32_t ta, uint32_t tb, u64 (&v)[8]) {
+  u64 w[8];
+  asm volatile(
+      "{\n"
+      " .reg .b32 t<16>;\n"
+      " .reg .b32 s<16>;\n"
+      " tcgen05.ld.sync.aligned.32x32b.x16.b32 {t0, t1, t2, t3, t4, t5, t6, t7, t8, t9, t10, t11, t12, t13, t14, t15}, [%16];\n"
+      " tcgen05.ld.sync.aligned.32x32b.x16.b32 {s0, s1, s2, s3, s4, s5, s6, s7, s8, s9, s10, s11, s12, s13, s14, s15}, [%17];\n"
+      " tcgen05.wait::ld.sync.aligned;\n"
+      " mov.b64 %0, {t0, t1};\n"
+      " mov.b64 %1, {t2, t3};\n"
+      " mov.b64 %2, {t4, t5};\n"
+      " mov.b64 %3, {t6, t7};\n"
+      " mov.b64 %4, {t8, t9};\n"
+      " mov.b64 %5, {t10, t11};\n"
+      " mov.b64 %6, {t12, t13};\n"
+      " mov.b64 %7, {t14, t15};\n"
+      " mov.b64 %8, {s0, s1};\n"
+      " mov.b64 %9, {s2, s3};\n"
+      " mov.b64 %10, {s4, s5};\n"
+      " mov.b64 %11, {s6, s7};\n"
+      " mov.b64 %12, {s8, s9};\n"
+      " mov.b64 %13, {s10, s11};\n"
+      " mov.b64 %14, {s12, s13};\n"
+      " mov.b64 %15, {s14, s15};\n"
+      "}"
+      : "=l"(v[0]), "=l"(v[1]), "=l"(v[2]), "=l"(v[3]), "=l"(v[4]), "=l"(v[5]), "=l"(v[6]), "=l"(v[7]), "=l"(w[0]), "=l"(w[1]),
+        "=l"(w[2]), "=l"(w[3]), "=l"(w[4]), "=l"(w[5]), "=l"(w[6]), "=l"(w[7])
+      : "r"(ta), "r"(tb)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = add2(v[i], w[i]);
+}
+__device__ __forceinline__ void tmem_put_pairs(uint32_t ta, const u64* v) {   // complete at tmem_wait_st()
+  float f[16];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float2 x = unpack2(v[i]);
+    f[2 * i] = x.x, f[2 * i + 1] = x.y;
+  }
+  tmem_st16(ta, f);
 }
 // Four packed pairs as eight fp16 high terms and eight low ones.
 __device__ __forceinline__ void split_pair(u64 x, uint32_t& hi, uint32_t& lo) {
@@ -121,6 +182,11 @@ __device__ __forceinline__ void tmem_pairs(uint32_t ta, u64 (&v)[8]) {
       : "=l"(v[0]), "=l"(v[1]), "=l"(v[2]), "=l"(v[3]), "=l"(v[4]), "=l"(v[5]), "=l"(v[6]), "=l"(v[7])
       : "r"(ta)
       : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t ta, const float (&v)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(ta), "f"(v[0]), "f"(v[1]),
+               "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+               : "memory");
 }
 __device__ __forceinline__ float exp2_fast(float x) {   // results below 2^-126 are zero
   float y;
@@ -218,38 +284,89 @@ __device__ __forceinline__ void conv_tokens(const SeqParams& p, const InT* x, co
 // ---- what does not depend on the state ------------------------------------------------------------------------------
 
 constexpr int kPrepThreads = 256, kPrepWarps = kPrepThreads / 32;
-constexpr int kHeads = 3;                  // v-heads of a k-head in work together
 constexpr int kLd = 68;                    // floats a row of A and X
 constexpr int kRowLd = 132;                // of rows of q, k or v
+constexpr int kRowBytes = kChunk * kRowLd * 4;
+constexpr int kSq = kChunk * kChunk * 2;   // an fp16 image of a 64 x 64 matrix
 
+// What a chunk and k-head's kernel holds: Kh Qh Kl Ql | rows | barrier
 template <int DK>
-struct Prep {
+struct PrepK {
   static constexpr int kImage = kChunk * DK * 2;              // one fp16 image of K or Q
-  static constexpr int kImages = 0;                           // Kh Qh Kl Ql
-  static constexpr int kRows = 4 * kImage;                    // rows of q, k or v in 32 bits
-  static constexpr int kRowBytes = kChunk * kRowLd * 4;
-  // later, in the images' place: A and X of kHeads heads, images (high, low) of their M
-  static constexpr int kSq = kChunk * kChunk * 2;             // an fp16 image of a 64 x 64 matrix
-  static constexpr int kAx = 0, kAxBytes = kChunk * kLd * 4;
-  static constexpr int kM = kHeads * kAxBytes;
-  static constexpr int kEnd = kRows + kRowBytes > kM + kHeads * 2 * kSq ? kRows + kRowBytes : kM + kHeads * 2 * kSq;
-  static constexpr int kGate = kEnd;                          // a head: float2 [64] log2 of the cumulated gates (high, low part), beta [64], left [64]
-  static constexpr int kRed = kGate + kHeads * 4 * kChunk * 4;  // float [128]
-  static constexpr int kBar = kRed + 128 * 4;                 // Gram product, N
-  static constexpr int kTotal = kBar + 64;
+  static constexpr int kRows = 4 * kImage, kBar = kRows + kRowBytes, kTotal = kBar + 32;
 };
-// Columns of tensor memory: the Gram product, later N | C of the heads
-constexpr uint32_t kTmGram = 0, kTmC = 64, kTmPrep = 256;
+// A chunk and v-head's: rows of v, later A and X, and the images (high, low) of M in their place | gates | maxima | barrier
+struct PrepV {
+  static constexpr int kAx = 0, kM = kChunk * kLd * 4;
+  static constexpr int kEnd = kRowBytes > kM + 2 * kSq ? kRowBytes : kM + 2 * kSq;
+  static constexpr int kGate = kEnd;                          // float2 [64] log2 of the cumulated gates (high, low part), beta [64], left [64]
+  static constexpr int kRed = kGate + 4 * kChunk * 4;         // float [48]
+  static constexpr int kBar = kRed + 48 * 4, kTotal = kBar + 32;
+  static constexpr uint32_t kTmN = 0, kTmC = 64, kTmem = 128;   // columns of tensor memory: N | C
+};
 
 // 16-byte places of an fp16 image of `width` columns: row r, columns 8 c ..
 __device__ __forceinline__ int image_at(int r, int c, int width) { return (r >> 3) * width * 16 + c * 128 + (r & 7) * 16; }
 
-// X = (1 + A)^-1 for strictly lower A, columns 32 half ..: lane = column, forward substitution by blocks of 16 rows.
-// ax[j][i] (kLd floats a row) holds A_ij in i > j; X_kj goes to ax[k][j], j <= k, which A leaves free.
-__device__ __forceinline__ void solve_columns(float* ax, int half, int lane) {
+// Where a CTA's chunk is: request, rows, window, and the chunk's places in the workspace.
+template <typename InT>
+struct Place {
+  SegReq req;
+  int chunk, t0, len;
+  const InT* x;
+  const float* win;
+  char* kq;       // of k-head 0; seq_kq_bytes apart
+  char* v;        // of v-head 0; seq_v_bytes apart
+  __device__ __forceinline__ Place(const SeqParams& p, const Segment& seg, char* ws, int slot) {
+    int ri = 0;
+    while (ri + 1 < seg.n && slot >= seg.r[ri + 1].slot0) ++ri;
+    req = seg.r[ri];
+    chunk = req.c0 + slot - req.slot0, t0 = chunk * kChunk, len = req.len;
+    x = static_cast<const InT*>(p.x) + static_cast<long long>(req.start) * p.x_row;
+    win = p.conv_in ? p.conv_in + req.b * p.conv_stride : nullptr;
+    kq = ws + slot * seq_slot_bytes(p.Hk, p.Hv, p.dk, p.dv);
+    v = kq + p.Hk * seq_kq_bytes(p.dk);
+  }
+};
+
+// Conv and activation of the chunk's 64 tokens in `width` channels from ch on, into rows; norm as well where kNorm.
+// A lane takes four channels of kTok adjacent tokens, a warp eight tokens.  Returns the warp's largest entry.
+template <bool kNorm, int kTok, int KT, typename InT>
+__device__ __forceinline__ float conv_rows(const SeqParams& p, const Place<InT>& at, int width, int ch, float* rows) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, lanes = width / 4, sub = lane / lanes, cl = (lane % lanes) * 4;
+  float most = 0.f;
+#pragma unroll 1
+  for (int t = kTok * sub; t - kTok * sub < 8; t += lanes == 32 ? kTok : 8) {
+    const int first = warp * 8 + t;
+    float4 y[kTok];
+#pragma unroll
+    for (int i = 0; i < kTok; ++i) y[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (t < 8) conv_tokens<InT, KT, kTok>(p, at.x, at.win, at.t0 + first, at.len, ch + cl, y);
+#pragma unroll
+    for (int i = 0; i < kTok; ++i) {
+      if (kNorm) {
+        float ss = fmaf(y[i].x, y[i].x, fmaf(y[i].y, y[i].y, fmaf(y[i].z, y[i].z, y[i].w * y[i].w)));
+        for (int o = lanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(~0u, ss, o);
+        const float f = at.t0 + first + i < at.len ? rsqrtf(ss + p.l2_eps) * kUnit : 0.f;
+        y[i] = make_float4(y[i].x * f, y[i].y * f, y[i].z * f, y[i].w * f);
+      }
+      if (t < 8) {
+        *reinterpret_cast<float4*>(rows + (first + i) * kRowLd + cl) = y[i];
+        if (!kNorm) most = fmaxf(most, fmaxf(fmaxf(fabsf(y[i].x), fabsf(y[i].y)), fmaxf(fabsf(y[i].z), fabsf(y[i].w))));
+      }
+    }
+  }
+  __syncwarp();
+  return kNorm ? 0.f : warp_max(most);
+}
+
+// X = (1 + A)^-1 for strictly lower A.  ax[j][i] (kLd floats a row) holds A_ij in i > j; X_kj goes to ax[k][j], j <= k,
+// which A leaves free.  First the diagonal blocks of 32, a warp each: lane = column, forward substitution by blocks of 16
+// rows; then X21 = -X22 (A21 X11) by all warps, four rows a warp, through T in tmp (32 x 32, its own memory).
+__device__ __forceinline__ void solve_block(float* ax, int half, int lane) {
   const int col = half * 32 + lane;
 #pragma unroll 1
-  for (int bi = 2 * half; bi < 4; ++bi) {                      // blocks above the columns' own are zero
+  for (int bi = 2 * half; bi < 2 * half + 2; ++bi) {
     const int r0 = 16 * bi;
     u64 acc[8];
 #pragma unroll
@@ -295,148 +412,64 @@ __device__ __forceinline__ void solve_columns(float* ax, int half, int lane) {
     __syncwarp();
   }
 }
+__device__ __forceinline__ void solve(float* ax, float* tmp, int warp, int lane) {
+  if (warp < 2) solve_block(ax, warp, lane);
+  __syncthreads();
+  const int r = 4 * warp;                          // rows of the lower block; lane = column
+  u64 s0 = 0ull, s1 = 0ull;
+#pragma unroll 8
+  for (int k = 0; k < 32; ++k) {                   // T = A21 X11
+    const float x = lane <= k ? ax[k * kLd + lane] : 0.f;
+    const ulonglong2 a = *reinterpret_cast<const ulonglong2*>(ax + k * kLd + 32 + r);
+    s0 = fma2(pack2(x, x), a.x, s0);
+    s1 = fma2(pack2(x, x), a.y, s1);
+  }
+  const float2 a = unpack2(s0), b = unpack2(s1);
+  tmp[r * 32 + lane] = a.x, tmp[(r + 1) * 32 + lane] = a.y, tmp[(r + 2) * 32 + lane] = b.x, tmp[(r + 3) * 32 + lane] = b.y;
+  __syncthreads();
+  float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+  for (int k = 0; k <= r; k += 4) {                // -X22 T: rows r .. r + 3 end at their diagonals
+    const float t[4] = {tmp[k * 32 + lane], tmp[(k + 1) * 32 + lane], tmp[(k + 2) * 32 + lane], tmp[(k + 3) * 32 + lane]};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float4 v = *reinterpret_cast<const float4*>(ax + (32 + r + e) * kLd + 32 + k);
+      s[e] = fmaf(-v.x, t[0], s[e]);               // (k <= r)
+      s[e] = fmaf(k + 1 <= r + e ? -v.y : 0.f, t[1], s[e]);
+      s[e] = fmaf(k + 2 <= r + e ? -v.z : 0.f, t[2], s[e]);
+      s[e] = fmaf(k + 3 <= r + e ? -v.w : 0.f, t[3], s[e]);
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) ax[(32 + r + e) * kLd + lane] = s[e];
+  __syncthreads();
+}
 
+// k and q of a chunk and k-head: rows, two-term images, Gram matrices.
 template <typename InT, int DK, int KT>
 __global__ void __launch_bounds__(kPrepThreads, 2)
-seq_prepare_kernel(const SeqParams p, const __grid_constant__ Segment seg, char* ws) {
-  using P = Prep<DK>;
+seq_keys_kernel(const SeqParams p, const __grid_constant__ Segment seg, char* ws) {
+  using P = PrepK<DK>;
   extern __shared__ __align__(128) char sm[];
   float* rows = reinterpret_cast<float*>(sm + P::kRows);
-  float* red = reinterpret_cast<float*>(sm + P::kRed);
   uint64_t* bar = reinterpret_cast<uint64_t*>(sm + P::kBar);
-  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(bar + 3);
-  float* unit = reinterpret_cast<float*>(bar + 4);             // [2 kHeads] scales of C, inverse ones of M
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int kh = blockIdx.x, slot = blockIdx.y;
-  int ri = 0;
-  while (ri + 1 < seg.n && slot >= seg.r[ri + 1].slot0) ++ri;
-  const SegReq req = seg.r[ri];
-  const int chunk = req.c0 + slot - req.slot0, t0 = chunk * kChunk, len = req.len;
-  const int R = p.Hv / p.Hk, dv = p.dv;
-  const InT* x = static_cast<const InT*>(p.x) + static_cast<long long>(req.start) * p.x_row;
-  const float* win = p.conv_in ? p.conv_in + req.b * p.conv_stride : nullptr;
-  char* const slot_ws = ws + slot * (p.Hk * seq_kq_bytes(DK) + p.Hv * seq_v_bytes(dv));
-  char* const kq_ws = slot_ws + kh * seq_kq_bytes(DK);
-  const int h0 = blockIdx.z * kHeads, nh = min(kHeads, R - h0);      // the k-head's v-heads this CTA takes
-  auto head_ws = [&](int h) { return slot_ws + p.Hk * seq_kq_bytes(DK) + (kh * R + h0 + h) * seq_v_bytes(dv); };
-  auto head_meta = [&](int h) { return reinterpret_cast<float*>(head_ws(h) + 4 * 128 * kChunk + kChunk * dv * 4); };
-  auto gates_of = [&](int h) { return reinterpret_cast<float*>(sm + P::kGate) + h * 4 * kChunk; };
+  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(bar + 1);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, kh = blockIdx.x;
+  const Place<InT> at(p, seg, ws, blockIdx.y);
+  char* const out = at.kq + kh * seq_kq_bytes(DK);
   const bool aborted = launch_aborted(p.err);
-
-  if (warp == 0) tmem_alloc(tmem_at, kTmPrep);
-  if (tid == 0)
-    for (int i = 0; i < 2; ++i) mbar_init(bar + i);
-  if (__syncthreads_or(aborted)) {
-    if (warp == 0) {
-      tmem_relinquish();
-      tmem_dealloc(*tmem_at, kTmPrep);
-    }
-    return;
-  }
+  if (warp == 0) tmem_alloc(tmem_at, kChunk);
+  if (tid == 0) mbar_init(bar);
+  const bool stop = __syncthreads_or(aborted);
   if (warp == 0) tmem_relinquish();
   const uint32_t tmem = *tmem_at;
   bool late = false;
-  auto wait = [&](int which, int parity) {
-    if (!late && !mbar_wait_quiet(bar + which, parity)) late = true;
-  };
-
-  if (tid < kChunk + 3) {                          // the raw rows on their way into L2
-    const int t = t0 + tid - 3;
-    if (t >= 0 && t < len) {
-      const InT* r = x + static_cast<long long>(t) * p.x_row;
-      prefetch_l2(r + kh * DK, DK * sizeof(InT));
-      prefetch_l2(r + (p.Hk + kh) * DK, DK * sizeof(InT));
-      prefetch_l2(r + 2 * p.Hk * DK + (kh * R + h0) * dv, nh * dv * sizeof(InT));
-    }
-  }
-  // gates, a warp a head: cumulated in 64 bits and base 2, kept as two floats
-  if (warp < nh) {
-    float* const gate = gates_of(warp);
-    float* const meta = head_meta(warp);
-    double c[2];
-    float rise = 0.f;
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int t = t0 + 2 * lane + k;
-      float lg = 0.f, b = 0.f;
-      if (t < len) {
-        const long long at = (req.start + static_cast<long long>(t)) * p.gate_row + kh * R + h0 + warp;
-        b = load_f(static_cast<const InT*>(p.beta) + at);
-        lg = load_f(static_cast<const InT*>(p.log_g) + at);
-        lg = lg < kGateFloor ? kGateFloor : lg;
-      }
-      rise += fmaxf(lg, 0.f);
-      c[k] = static_cast<double>(lg) * 1.4426950408889634;
-      gate[2 * kChunk + 2 * lane + k] = b;
-    }
-    c[1] += c[0];
-    double sum = c[1];
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const double s = __shfl_up_sync(~0u, sum, o);
-      if (lane >= o) sum += s;
-    }
-    const double before = sum - c[1], total = __shfl_sync(~0u, sum, 31);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) rise += __shfl_xor_sync(~0u, rise, o);
-    float most = 0.f;
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const double s = before + c[k];
-      const float hi = static_cast<float>(s), lo = static_cast<float>(s - hi);
-      const float first = exp2f(hi) * fmaf(lo, 0.69314718f, 1.f), left = exp2f(static_cast<float>(total - s));
-      reinterpret_cast<float2*>(gate)[2 * lane + k] = make_float2(hi, lo);
-      gate[3 * kChunk + 2 * lane + k] = left;
-      meta[2 * lane + k] = first;
-      meta[kChunk + 2 * lane + k] = left;
-      most = fmaxf(most, first);
-    }
-    most = warp_max(most);
-    if (lane == 0) {
-      meta[2 * kChunk] = exp2f(static_cast<float>(total));
-      meta[2 * kChunk + 5] = most;
-      // no product of gates is above e^rise (1 unless a log gate is above 0)
-      unit[warp] = exp2f(floorf(11.f - rise * kLog2e));
-    }
-  }
-
-  // k, q, then the heads' v: conv and activation (k and q: norm) into rows; from there k and q as two-term images, here and
-  // in the workspace, and v four columns of all tokens together, [dv / 4][64][4].
-  // A lane takes four channels of kTok adjacent tokens, a warp eight tokens.
-  constexpr int kTok = DK == 128 ? 8 : 4;
+  if (!stop) {
 #pragma unroll 1
-  for (int kind = 0; kind < 2 + nh; ++kind) {
-    const int width = kind < 2 ? DK : dv, lanes = width / 4, sub = lane / lanes, cl = (lane % lanes) * 4;
-    const int ch = kind == 0 ? (p.Hk + kh) * DK : kind == 1 ? kh * DK : 2 * p.Hk * DK + (kh * R + h0 + kind - 2) * dv;
-    float most = 0.f;
-#pragma unroll 1
-    for (int t = kTok * sub; t - kTok * sub < 8; t += lanes == 32 ? kTok : 8) {
-      const int first = warp * 8 + t;
-      float4 y[kTok];
-      if (t < 8) conv_tokens<InT, KT, kTok>(p, x, win, t0 + first, len, ch + cl, y);
-#pragma unroll
-      for (int i = 0; i < kTok; ++i) {
-        if (kind < 2) {
-          float ss = fmaf(y[i].x, y[i].x, fmaf(y[i].y, y[i].y, fmaf(y[i].z, y[i].z, y[i].w * y[i].w)));
-#pragma unroll
-          for (int o = DK / 8; o > 0; o >>= 1) ss += __shfl_xor_sync(~0u, ss, o);
-          const float f = t0 + first + i < len ? rsqrtf(ss + p.l2_eps) * kUnit : 0.f;
-          y[i] = make_float4(y[i].x * f, y[i].y * f, y[i].z * f, y[i].w * f);
-        }
-        if (t < 8) {
-          *reinterpret_cast<float4*>(rows + (first + i) * kRowLd + cl) = y[i];
-          most = fmaxf(most, fmaxf(fmaxf(fabsf(y[i].x), fabsf(y[i].y)), fmaxf(fabsf(y[i].z), fabsf(y[i].w))));
-        }
-      }
-    }
-    __syncwarp();
-    most = warp_max(most);
-    if (lane == 0) red[warp] = most;
-    __syncthreads();
-    const int t = tid & 63;
-    if (kind < 2) {
-      char* const hi_sm = sm + P::kImages + kind * P::kImage;
-      char* const hi_ws = kq_ws + 2 * kind * P::kImage;
+    for (int kind = 0; kind < 2; ++kind) {         // k, q
+      conv_rows<true, DK == 128 ? 8 : 4, KT>(p, at, DK, ((kind == 0 ? p.Hk : 0) + kh) * DK, rows);
+      __syncthreads();
+      const int t = tid & 63;
 #pragma unroll
       for (int c = 0; c < DK / 8; c += kPrepThreads / 64) {
         const int cc = c + (tid >> 6);
@@ -445,146 +478,253 @@ seq_prepare_kernel(const SeqParams p, const __grid_constant__ Segment seg, char*
         const u64 v[4] = {v0.x, v0.y, v1.x, v1.y};
         uint4 hi, lo;
         split_pairs(v, hi, lo);
-        const int at = image_at(t, cc, DK);
-        *reinterpret_cast<uint4*>(hi_sm + at) = hi;
-        *reinterpret_cast<uint4*>(hi_sm + 2 * P::kImage + at) = lo;
-        if (h0 == 0) {
-          *reinterpret_cast<uint4*>(hi_ws + at) = hi;
-          *reinterpret_cast<uint4*>(hi_ws + P::kImage + at) = lo;
-        }
+        const int to = image_at(t, cc, DK);
+        *reinterpret_cast<uint4*>(sm + kind * P::kImage + to) = hi;
+        *reinterpret_cast<uint4*>(sm + (kind + 2) * P::kImage + to) = lo;
+        *reinterpret_cast<uint4*>(out + 2 * kind * P::kImage + to) = hi;
+        *reinterpret_cast<uint4*>(out + (2 * kind + 1) * P::kImage + to) = lo;
       }
       fence_proxy_async();
-    } else {
-      float4* const V = reinterpret_cast<float4*>(head_ws(kind - 2) + 4 * 128 * kChunk);
-#pragma unroll 4
-      for (int c = tid >> 6; c < dv / 4; c += kPrepThreads / 64)
-        V[c * kChunk + t] = *reinterpret_cast<const float4*>(rows + t * kRowLd + 4 * c);
-      if (tid == 0) {
-        most = 0.f;
-        for (int w = 0; w < kPrepWarps; ++w) most = fmaxf(most, red[w]);
-        head_meta(kind - 2)[2 * kChunk + 3] = most;
-      }
+      __syncthreads();
     }
-    __syncthreads();
-    if (kind == 1 && warp == 0) {
-      // G = K K^T (lanes 0 to 63) and H = Q K^T
+    // G = K K^T (lanes 0 to 63) and H = Q K^T
+    if (warp == 0) {
       if (elect_one()) {
-        const uint64_t a = umma_desc(smem_addr(sm + P::kImages), 128, DK * 16);
-        product<DK / 16>(tmem + kTmGram, a, a, 2 * P::kImage, 2 * P::kImage, 256, 256, idesc_f16(kChunk, false, false));
+        const uint64_t a = umma_desc(smem_addr(sm), 128, DK * 16);
+        product<DK / 16>(tmem, a, a, 2 * P::kImage, 2 * P::kImage, 256, 256, idesc_f16(kChunk, false, false));
         umma_commit(bar);
       }
       __syncwarp();
     }
-  }
-  wait(0, 0);
-  tmem_fence_after();
-  __syncthreads();                                 // A takes the Gram operands' place
-
-  // A thread has 32 entries of a row of G (warps 0, 1, 4, 5) or H (the others).
-  const int trow = (warp & 3) * 32 + lane, tcol = (warp >> 2) * 32, i = trow & 63;
-  const bool q_row = trow >= kChunk;
-  const uint32_t ta = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-  {
-    u64 g[16];
-    tmem_pairs(ta + kTmGram + tcol, *reinterpret_cast<u64(*)[8]>(g));
-    tmem_pairs(ta + kTmGram + tcol + 16, *reinterpret_cast<u64(*)[8]>(g + 8));
-#pragma unroll 1
-    for (int h = 0; h < nh; ++h) {
-      const float* const gate = gates_of(h);
-      const float4* const c = reinterpret_cast<const float4*>(gate) + tcol / 2;     // two tokens' sums
-      const float2 ci = reinterpret_cast<const float2*>(gate)[i];
-      const float f = (q_row ? unit[h] : gate[2 * kChunk + i]) * (1.f / (kUnit * kUnit));
-      float* const ax = reinterpret_cast<float*>(sm + P::kAx + h * P::kAxBytes) + tcol * kLd + i;
-      float hi[16], lo[16];
-      // e^(c_i - c_j) times the row: the sums in base 2, their low parts apart
+    late = !mbar_wait_quiet(bar, 0);
+    tmem_fence_after();
+    // four columns of all rows together, [16][64][4]: G, then H
+    const int row = (warp & 3) * 32 + lane, col = (warp >> 2) * 32;
+    float4* const gram = reinterpret_cast<float4*>(out + 4 * P::kImage) + (row >> 6) * (kChunk / 4 * kChunk) + (row & 63);
 #pragma unroll
-      for (int k = 0; k < 16; ++k) {
-        const int j = tcol + 2 * k;
-        const float4 cj = c[k];
-        const float2 e = unpack2(g[k]);
-        const float a = exp2_fast((ci.x - cj.x) + (ci.y - cj.y)) * (f * e.x);
-        const float b = exp2_fast((ci.x - cj.z) + (ci.y - cj.w)) * (f * e.y);
-        if (q_row) {
-          // C = e^(c_i - c_j) H_ij up to the diagonal: A operand in tensor memory, in two terms, two columns of C a cell
-          uint32_t x0, x1;
-          split2(j <= i ? a : 0.f, j + 1 <= i ? b : 0.f, x0, x1);
-          hi[k] = __uint_as_float(x0), lo[k] = __uint_as_float(x1);
-        } else {
-          // A = beta_i e^(c_i - c_j) G_ij below it, transposed
-          if (j < i) ax[2 * k * kLd] = a;
-          if (j + 1 < i) ax[(2 * k + 1) * kLd] = b;
-        }
-      }
-      if (q_row) {
-        tmem_st16(ta + kTmC + h * 64 + tcol / 2, hi);
-        tmem_st16(ta + kTmC + h * 64 + 32 + tcol / 2, lo);
+    for (int half = 0; half < 2; ++half) {
+      u64 v[8];
+      tmem_pairs(tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + col + 16 * half, v);
+#pragma unroll
+      for (int k = 0; k < 8; k += 2) {
+        const float2 a = unpack2(v[k]), b = unpack2(v[k + 1]);
+        constexpr float f = 1.f / (kUnit * kUnit);
+        gram[((col + 16 * half) / 4 + k / 2) * kChunk] = make_float4(a.x * f, a.y * f, b.x * f, b.y * f);
       }
     }
-    tmem_wait_st();
     tmem_fence_before();
   }
-  __syncthreads();
-  if (warp < 2 * nh) solve_columns(reinterpret_cast<float*>(sm + P::kAx + (warp >> 1) * P::kAxBytes), warp & 1, lane);
-  __syncthreads();
-  // M = X diag(beta): its largest entry, a bound of its rows' sums times the gates behind them, its image.
-  // A thread has sixteen columns of row mi.  Rows of [M; N] change places with every chunk of the request, as [K; Q] do.
-  const int mi = tid & 63, j0 = (tid >> 6) * 16;
-  const int m_row = (chunk & 1) * kChunk, n_row = kChunk - m_row;
-#pragma unroll 1
-  for (int h = 0; h < nh; ++h) {
-    const float* const ax = reinterpret_cast<const float*>(sm + P::kAx + h * P::kAxBytes) + mi * kLd + j0;
-    const float* const beta = gates_of(h) + 2 * kChunk + j0;
-    float m[16], big = 0.f, sum = 0.f;
-#pragma unroll
-    for (int k = 0; k < 16; k += 4) {
-      const float4 a = *reinterpret_cast<const float4*>(ax + k), b = *reinterpret_cast<const float4*>(beta + k);
-      m[k] = j0 + k <= mi ? a.x * b.x : 0.f;
-      m[k + 1] = j0 + k + 1 <= mi ? a.y * b.y : 0.f;
-      m[k + 2] = j0 + k + 2 <= mi ? a.z * b.z : 0.f;
-      m[k + 3] = j0 + k + 3 <= mi ? a.w * b.w : 0.f;
+  if (__syncthreads_or(late) && tid == 0) device_error(p.err, GDN_DEVERR_TIMEOUT, at.req.b);
+  if (warp == 0) tmem_dealloc(tmem, kChunk);
+}
+
+// v, the gates, M and N of a chunk and v-head.
+template <typename InT, int KT>
+__global__ void __launch_bounds__(kPrepThreads, 3)
+seq_values_kernel(const SeqParams p, const __grid_constant__ Segment seg, char* ws) {
+  using P = PrepV;
+  extern __shared__ __align__(128) char sm[];
+  float* rows = reinterpret_cast<float*>(sm);
+  float* ax = reinterpret_cast<float*>(sm + P::kAx);
+  float* gate = reinterpret_cast<float*>(sm + P::kGate);
+  float* red = reinterpret_cast<float*>(sm + P::kRed);
+  uint64_t* bar = reinterpret_cast<uint64_t*>(sm + P::kBar);
+  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(bar + 1);
+  float* unit = reinterpret_cast<float*>(bar + 2);             // scale of C
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, vh = blockIdx.x, dv = p.dv;
+  const Place<InT> at(p, seg, ws, blockIdx.y);
+  const float* const grams = reinterpret_cast<const float*>(at.kq + vh / (p.Hv / p.Hk) * seq_kq_bytes(p.dk) + 4 * kChunk * p.dk * 2);
+  char* const out = at.v + vh * seq_v_bytes(dv);
+  float4* const V = reinterpret_cast<float4*>(out + 4 * 128 * kChunk);
+  float* const meta = reinterpret_cast<float*>(V + dv / 4 * kChunk);
+  const bool aborted = launch_aborted(p.err);
+  if (warp == 0) tmem_alloc(tmem_at, P::kTmem);
+  if (tid == 0) mbar_init(bar);
+  const bool stop = __syncthreads_or(aborted);
+  if (warp == 0) tmem_relinquish();
+  const uint32_t tmem = *tmem_at;
+  bool late = false;
+  if (!stop) {
+    // The raw rows on their way into L2, and two tokens' gates for each lane of the last warp.
+    if (tid < kChunk + 3) {
+      const int t = at.t0 + tid - 3;
+      if (t >= 0 && t < at.len) prefetch_l2(at.x + static_cast<long long>(t) * p.x_row + 2 * p.Hk * p.dk + vh * dv, dv * sizeof(InT));
     }
+    float lg[2] = {0.f, 0.f}, be[2] = {0.f, 0.f};
+    if (warp == kPrepWarps - 1) {
 #pragma unroll
-    for (int k = 0; k < 16; ++k) big = fmaxf(big, fabsf(m[k])), sum += fabsf(m[k]);
-    big = warp_max(big);
-    sum = warp_max(sum * gates_of(h)[3 * kChunk + mi]);
-    if (lane == 0) red[h * 16 + warp] = big, red[h * 16 + 8 + warp] = sum;
+      for (int k = 0; k < 2; ++k) {
+        const int t = at.t0 + 2 * lane + k;
+        if (t < at.len) {
+          const long long from = (at.req.start + static_cast<long long>(t)) * p.gate_row + vh;
+          be[k] = load_f(static_cast<const InT*>(p.beta) + from);
+          lg[k] = load_f(static_cast<const InT*>(p.log_g) + from);
+          lg[k] = lg[k] < kGateFloor ? kGateFloor : lg[k];
+        }
+      }
+    }
+    // v: rows, then four columns of all tokens together, [dv / 4][64][4]
+    {
+      float most = conv_rows<false, 4, KT>(p, at, dv, 2 * p.Hk * p.dk + vh * dv, rows);
+      if (lane == 0) red[warp] = most;
+    }
     __syncthreads();
-    big = sum = 0.f;
+    if (warp == kPrepWarps - 1) {
+      // the gates meanwhile: cumulated in 64 bits and base 2, kept as two floats
+      double c[2];
+      float rise = 0.f;
 #pragma unroll
-    for (int w = 0; w < kPrepWarps; w += 2) {
-      big = fmaxf(big, fmaxf(red[h * 16 + w], red[h * 16 + w + 1]));
-      sum += fmaxf(red[h * 16 + 8 + w], red[h * 16 + 8 + w + 1]);
+      for (int k = 0; k < 2; ++k) {
+        rise += fmaxf(lg[k], 0.f);
+        c[k] = static_cast<double>(lg[k]) * 1.4426950408889634;
+        gate[2 * kChunk + 2 * lane + k] = be[k];
+      }
+      c[1] += c[0];
+      double sum = c[1];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const double s = __shfl_up_sync(~0u, sum, o);
+        if (lane >= o) sum += s;
+      }
+      const double before = sum - c[1], total = __shfl_sync(~0u, sum, 31);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) rise += __shfl_xor_sync(~0u, rise, o);
+      float most = 0.f;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const double s = before + c[k];
+        const float hi = static_cast<float>(s), lo = static_cast<float>(s - hi);
+        const float first = exp2f(hi) * fmaf(lo, 0.69314718f, 1.f), left = exp2f(static_cast<float>(total - s));
+        reinterpret_cast<float2*>(gate)[2 * lane + k] = make_float2(hi, lo);
+        gate[3 * kChunk + 2 * lane + k] = left;
+        meta[2 * lane + k] = first;
+        meta[kChunk + 2 * lane + k] = left;
+        most = fmaxf(most, first);
+      }
+      most = warp_max(most);
+      if (lane == 0) {
+        meta[2 * kChunk] = exp2f(static_cast<float>(total));
+        meta[2 * kChunk + 5] = most;
+        // no product of gates is above e^rise (1 unless a log gate is above 0)
+        *unit = exp2f(floorf(11.f - rise * kLog2e));
+      }
+    } else {
+#pragma unroll 4
+      for (int c = tid; c < dv / 4 * kChunk; c += kPrepThreads - 32)
+        V[c] = *reinterpret_cast<const float4*>(rows + (c & 63) * kRowLd + (c >> 6) * 4);
+      if (tid == 0) {
+        float most = 0.f;
+        for (int w = 0; w < kPrepWarps; ++w) most = fmaxf(most, red[w]);
+        meta[2 * kChunk + 3] = most;
+      }
     }
-    float inv;
-    const float sc = scale_for(big, inv);
-    char* const ws_h = head_ws(h);
+    __syncthreads();                               // A takes the rows' place
+    // A thread has 32 entries of a row of G (warps 0, 1, 4, 5) or H (the others).
+    const int trow = (warp & 3) * 32 + lane, tcol = (warp >> 2) * 32, i = trow & 63;
+    const bool q_row = trow >= kChunk;
+    const uint32_t ta = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    {
+      const float4* g = reinterpret_cast<const float4*>(grams) + (q_row ? kChunk / 4 * kChunk : 0) + tcol / 4 * kChunk + i;
+      const float4* const c = reinterpret_cast<const float4*>(gate) + tcol / 2;     // two tokens' sums
+      const float2 ci = reinterpret_cast<const float2*>(gate)[i];
+      const float f = q_row ? *unit : gate[2 * kChunk + i];
+      // e^(c_i - c_j) times the row: the sums in base 2, their low parts apart
+      auto decayed = [&](float4 cj, float x, float y, float& a, float& b) {
+        a = exp2_fast((ci.x - cj.x) + (ci.y - cj.y)) * (f * x);
+        b = exp2_fast((ci.x - cj.z) + (ci.y - cj.w)) * (f * y);
+      };
 #pragma unroll
-    for (int k = 0; k < 16; k += 8) {
-      u64 v[4];
+      for (int half = 0; half < 2; ++half) {
+        float4 e[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = mul2(pack2(m[k + 2 * e], m[k + 2 * e + 1]), pack2(sc, sc));
-      uint4 hi, lo;
-      split_pairs(v, hi, lo);
-      const int at = image_at(mi, (j0 + k) >> 3, kChunk);
-      char* const dst = sm + P::kM + h * 2 * P::kSq + at;
-      *reinterpret_cast<uint4*>(dst) = hi;
-      *reinterpret_cast<uint4*>(dst + P::kSq) = lo;
-      *reinterpret_cast<uint4*>(ws_h + m_row * 128 + at) = hi;
-      *reinterpret_cast<uint4*>(ws_h + 128 * 128 + m_row * 128 + at) = lo;
+        for (int k = 0; k < 4; ++k) e[k] = __ldg(g + (4 * half + k) * kChunk);
+        float hi[8], lo[8];
+        if (tcol + 16 * half > ((warp & 1) * 32 + 31)) {       // all above the diagonal
+#pragma unroll
+          for (int k = 0; k < 8; ++k) hi[k] = lo[k] = 0.f;
+        } else
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int j = tcol + 16 * half + 4 * k;
+          float a[4];
+          decayed(c[8 * half + 2 * k], e[k].x, e[k].y, a[0], a[1]);
+          decayed(c[8 * half + 2 * k + 1], e[k].z, e[k].w, a[2], a[3]);
+          if (q_row) {
+            // C = e^(c_i - c_j) H_ij up to the diagonal: A operand in tensor memory, in two terms, two columns of C a cell
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+              uint32_t x0, x1;
+              split2(j + 2 * n <= i ? a[2 * n] : 0.f, j + 2 * n + 1 <= i ? a[2 * n + 1] : 0.f, x0, x1);
+              hi[2 * k + n] = __uint_as_float(x0), lo[2 * k + n] = __uint_as_float(x1);
+            }
+          } else {
+            // A = beta_i e^(c_i - c_j) G_ij below it, transposed
+#pragma unroll
+            for (int n = 0; n < 4; ++n)
+              if (j + n < i) ax[(j + n) * kLd + i] = a[n];
+          }
+        }
+        if (q_row) {
+          tmem_st8(ta + P::kTmC + tcol / 2 + 8 * half, hi);
+          tmem_st8(ta + P::kTmC + 32 + tcol / 2 + 8 * half, lo);
+        }
+      }
+      tmem_wait_st();
+      tmem_fence_before();
     }
-    if (tid == 0) head_meta(h)[2 * kChunk + 1] = inv, head_meta(h)[2 * kChunk + 4] = sum, unit[kHeads + h] = inv;
-  }
-  fence_proxy_async();
-  __syncthreads();
-  // N = C M, by the warps that hold the rows of H
-  if (q_row) {
-    auto q_barrier = [] { asm volatile("bar.sync 1, 128;" ::: "memory"); };
-#pragma unroll 1
-    for (int h = 0; h < nh; ++h) {
-      if (warp == 2 && elect_one()) {
+    __syncthreads();
+    solve(ax, reinterpret_cast<float*>(sm + P::kM), warp, lane);
+    // M = X diag(beta): its largest entry, a bound of its rows' sums times the gates behind them, its image.
+    // A thread has sixteen columns of row mi.  Rows of [M; N] change places with every chunk of the request, as [K; Q] do.
+    const int mi = tid & 63, j0 = (tid >> 6) * 16;
+    const int m_row = (at.chunk & 1) * kChunk, n_row = kChunk - m_row;
+    float inv_m;
+    {
+      float m[16], big = 0.f, sum = 0.f;
+#pragma unroll
+      for (int k = 0; k < 16; k += 4) {
+        const float4 a = *reinterpret_cast<const float4*>(ax + mi * kLd + j0 + k), b = *reinterpret_cast<const float4*>(gate + 2 * kChunk + j0 + k);
+        m[k] = j0 + k <= mi ? a.x * b.x : 0.f;
+        m[k + 1] = j0 + k + 1 <= mi ? a.y * b.y : 0.f;
+        m[k + 2] = j0 + k + 2 <= mi ? a.z * b.z : 0.f;
+        m[k + 3] = j0 + k + 3 <= mi ? a.w * b.w : 0.f;
+      }
+#pragma unroll
+      for (int k = 0; k < 16; ++k) big = fmaxf(big, fabsf(m[k])), sum += fabsf(m[k]);
+      big = warp_max(big);
+      sum = warp_max(sum * gate[3 * kChunk + mi]);
+      if (lane == 0) red[8 + warp] = big, red[16 + warp] = sum;
+      __syncthreads();
+      big = sum = 0.f;
+#pragma unroll
+      for (int w = 0; w < kPrepWarps; w += 2) {
+        big = fmaxf(big, fmaxf(red[8 + w], red[9 + w]));
+        sum += fmaxf(red[16 + w], red[17 + w]);
+      }
+      const float sc = scale_for(big, inv_m);
+#pragma unroll
+      for (int k = 0; k < 16; k += 8) {
+        u64 v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = mul2(pack2(m[k + 2 * e], m[k + 2 * e + 1]), pack2(sc, sc));
+        uint4 hi, lo;
+        split_pairs(v, hi, lo);
+        const int to = image_at(mi, (j0 + k) >> 3, kChunk);
+        *reinterpret_cast<uint4*>(sm + P::kM + to) = hi;
+        *reinterpret_cast<uint4*>(sm + P::kM + kSq + to) = lo;
+        *reinterpret_cast<uint4*>(out + m_row * 128 + to) = hi;
+        *reinterpret_cast<uint4*>(out + 128 * 128 + m_row * 128 + to) = lo;
+      }
+      if (tid == 0) meta[2 * kChunk + 1] = inv_m, meta[2 * kChunk + 4] = sum;
+    }
+    fence_proxy_async();
+    __syncthreads();
+    // N = C M
+    if (warp == 0) {
+      if (elect_one()) {
         tmem_fence_after();
-        const uint32_t d = tmem + kTmGram, a = tmem + kTmC + h * 64;
-        const uint64_t b = umma_desc(smem_addr(sm + P::kM + h * 2 * P::kSq), 1024, 128), lo = P::kSq >> 4;
+        const uint32_t d = tmem + P::kTmN, a = tmem + P::kTmC;
+        const uint64_t b = umma_desc(smem_addr(sm + P::kM), 1024, 128), lo = kSq >> 4;
         const uint32_t id = idesc_f16(kChunk, false, true);
 #pragma unroll
         for (int k = 0; k < 4; ++k) umma_f16_ts(d, a + 8 * k, b + k * (2048 >> 4), id, k > 0);
@@ -592,14 +732,16 @@ seq_prepare_kernel(const SeqParams p, const __grid_constant__ Segment seg, char*
         for (int k = 0; k < 4; ++k) umma_f16_ts(d, a + 8 * k, b + lo + k * (2048 >> 4), id, 1);
 #pragma unroll
         for (int k = 0; k < 4; ++k) umma_f16_ts(d, a + 32 + 8 * k, b + k * (2048 >> 4), id, 1);
-        umma_commit(bar + 1);
+        umma_commit(bar);
       }
       __syncwarp();
-      wait(1, h & 1);
-      tmem_fence_after();
+    }
+    late = !mbar_wait_quiet(bar, 0);
+    tmem_fence_after();
+    if (q_row) {                                   // N is in the lanes of H's rows
       u64 v[16];
-      tmem_pairs(ta + kTmGram + tcol, *reinterpret_cast<u64(*)[8]>(v));
-      tmem_pairs(ta + kTmGram + tcol + 16, *reinterpret_cast<u64(*)[8]>(v + 8));
+      tmem_pairs(ta + P::kTmN + tcol, *reinterpret_cast<u64(*)[8]>(v));
+      tmem_pairs(ta + P::kTmN + tcol + 16, *reinterpret_cast<u64(*)[8]>(v + 8));
       tmem_fence_before();
       float big = 0.f, sum = 0.f;
 #pragma unroll
@@ -610,73 +752,83 @@ seq_prepare_kernel(const SeqParams p, const __grid_constant__ Segment seg, char*
       }
       big = warp_max(big);
       sum = warp_max(sum);
-      if (lane == 0) red[64 + h * 16 + warp] = big, red[64 + h * 16 + 8 + warp] = sum;
-      q_barrier();                                             // also: N of this head has been read
-      const float* const rb = red + 64 + h * 16;
-      big = fmaxf(fmaxf(rb[2], rb[3]), fmaxf(rb[6], rb[7]));
-      sum = fmaxf(rb[10], rb[11]) + fmaxf(rb[14], rb[15]);     // the rows' halves lie in two warps
-      const float inv = unit[kHeads + h] / unit[h];            // what N is known times
+      if (lane == 0) red[24 + warp] = big, red[32 + warp] = sum;
+      asm volatile("bar.sync 1, 128;" ::: "memory");
+      big = fmaxf(fmaxf(red[26], red[27]), fmaxf(red[30], red[31]));
+      sum = fmaxf(red[34], red[35]) + fmaxf(red[38], red[39]);   // the rows' halves lie in two warps
+      const float inv = inv_m / *unit;             // what N is known times
       float inv_n;
       const float sc = scale_for(big, inv_n);
-      char* const ws_h = head_ws(h);
 #pragma unroll
       for (int k = 0; k < 16; k += 4) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[k + e] = mul2(v[k + e], pack2(sc, sc));
         uint4 hi, lo;
         split_pairs(v + k, hi, lo);
-        const int at = image_at(i, (tcol + 2 * k) >> 3, kChunk);
-        *reinterpret_cast<uint4*>(ws_h + n_row * 128 + at) = hi;
-        *reinterpret_cast<uint4*>(ws_h + 128 * 128 + n_row * 128 + at) = lo;
+        const int to = image_at(i, (tcol + 2 * k) >> 3, kChunk);
+        *reinterpret_cast<uint4*>(out + n_row * 128 + to) = hi;
+        *reinterpret_cast<uint4*>(out + 128 * 128 + n_row * 128 + to) = lo;
       }
-      if (tid == 64) head_meta(h)[2 * kChunk + 2] = inv_n * inv, head_meta(h)[2 * kChunk + 6] = sum * inv;
+      if (tid == 64) meta[2 * kChunk + 2] = inv_n * inv, meta[2 * kChunk + 6] = sum * inv;
     }
   }
-  if (__syncthreads_or(late) && tid == 0) device_error(p.err, GDN_DEVERR_TIMEOUT, req.b);
-  if (warp == 0) tmem_dealloc(tmem, kTmPrep);
+  if (__syncthreads_or(late) && tid == 0) device_error(p.err, GDN_DEVERR_TIMEOUT, at.req.b);
+  if (warp == 0) tmem_dealloc(tmem, P::kTmem);
 }
 
 // ---- the chunks of a head, one after another ------------------------------------------------------------------------
 
 template <int DK, int NB>
 struct Chain {
-  // columns of a thread: with 16, twice as many warps share a step's latencies (32 warps and the issuing one would be
-  // more than a CTA's 1024 threads)
-  static constexpr int kCols = NB == 128 ? 32 : 16;
+  // Two groups of columns take turns at the tensor cores: one's products run while the other's threads work.
+  static constexpr int kTurns = 2, kN = NB / kTurns;           // columns of a group
+  static constexpr int kCols = 16;                             // of a thread
   static constexpr int kGroups = NB / kCols;                   // warpgroups
-  static constexpr int kSoft = 128 * kGroups, kThreads = kSoft + 32, kWarps = 4 * kGroups;
+  static constexpr int kThreads = 128 * kGroups, kWarps = 4 * kGroups;
+  static constexpr int kTurnWarps = kWarps / kTurns;
   static constexpr int kImage = kChunk * DK * 2;               // K or Q, one term
   static constexpr int kKq = 0, kKqLo = 3 * kImage;            // K of even chunks | Q | K of odd chunks
   static constexpr int kMn = 6 * kImage, kMnLo = 128 * kChunk * 2;
-  static constexpr int kS = kMn + 2 * kMnLo, kSLo = DK * NB * 2;
-  static constexpr int kW = kS + 2 * kSLo, kWLo = kChunk * NB * 2;
-  static constexpr int kBar = kW + 2 * kWLo;
-  static constexpr int kMax = kBar + 8 * 10;                   // float [2][kWarps]: largest entries of T, of o
+  // operands of a group: T [high | low], w or u [high | low]
+  static constexpr int kS = kMn + 2 * kMnLo, kSLo = DK * kN * 2, kSTurn = 2 * kSLo;
+  static constexpr int kW = kS + kTurns * kSTurn, kWLo = kChunk * kN * 2, kWTurn = 2 * kWLo;
+  static constexpr int kMeta = kW + kTurns * kWTurn;           // two chunks' gates and bounds
+  static constexpr int kMetaBytes = kSeqMeta * 4;
+  static constexpr int kBar = kMeta + 2 * kMetaBytes;
+  static constexpr int kCount = kBar + 8 * 16;                 // int [16]: arrivals
+  static constexpr int kMax = kCount + 4 * 16;                 // float [2 chunks][groups][T, o][kTurnWarps]: largest entries
   // K^T is read as 128 rows of d_k: from its last core matrices up to 1536 bytes past the image, into the next place
-  static constexpr int kTotal = kMax + 2 * kWarps * 4;
-  static constexpr uint32_t kTmem = 3 * NB <= 128 ? 128 : 3 * NB <= 256 ? 256 : 512;
+  static constexpr int kTotal = kMax + 2 * 2 * kWarps * 4;
+  // tensor memory of a group: D1 and later D3 | D2, high and low terms' products side by side
+  static constexpr uint32_t kD = 2 * kN, kTmem = kTurns * 2 * kD < 32 ? 32 : kTurns * 2 * kD;
 };
-enum ChainBar { kKqFull, kMnFull, kSReady, kD1, kWReady, kD2, kUReady, kD3, kTmemAt };
 
+// kMetaFull: one for even and one for odd chunks (the copy for a chunk may be under way while the other group has still to look
+// at the chunk before); the others from kD1 on: one a group of columns
+enum ChainBar { kKqFull, kMnFull, kTmemAt, kMetaFull = 4, kD1 = 6, kD2 = 8, kD3 = 10, kMeet = 12 };
+enum ChainCount { kSDone = 0, kWDone = 2, kUDone = 4 };                               // warps of a group
 constexpr float kRange = 0x1p-17f;   // bounds this far above the largest value still leave 2^-22 of it
 
-// A chunk by the rule itself, with fp32 sums, from the state in its operand (S / scale, 22 bits): its outputs are written
-// again and S is the state after it.  All threads of the warpgroups; rare and slow (some 0.1 ms).
+// A chunk by the rule itself, with fp32 sums, from the state S before it: its outputs are written again and S is the state
+// after it.  All threads of a group; rare and slow (some 0.1 ms).
 template <int DK, int NB>
-__device__ __noinline__ void again_by_token(const SeqParams& p, const SegReq& req, int vh, int row, bool has_row, int c0,
-                                            int col0, int t0, float inv_s, const char* kq, const float* V, char* sm,
-                                            float* S) {
+__device__ __noinline__ void again_by_token(const SeqParams& p, const SegReq& req, int vh, int row, bool has_row, int g,
+                                            int gw, int c0, int t0, const char* kq, const float* V,
+                                            char* sm, float* S, int& meetings, bool& late) {
   using L = Chain<DK, NB>;
   constexpr int CP = L::kCols;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  auto barrier = [] { asm volatile("bar.sync 1, %0;" ::"n"(L::kSoft) : "memory"); };
+  const int lane = threadIdx.x & 31;
+  uint64_t* const meet = reinterpret_cast<uint64_t*>(sm + L::kBar) + kMeet + g;
+  auto barrier = [&] {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(meet);
+    if (!late && !mbar_wait_quiet(meet, meetings & 1)) late = true;
+    ++meetings;
+  };
   auto term = [](const char* at) { return __half2float(*reinterpret_cast<const __half*>(at)); };
-  float* const part = reinterpret_cast<float*>(sm + L::kW);     // [warps][p, r: CP each], then [warps] q.k
-  float* const dots = part + L::kWarps * 2 * CP;
-  for (int j = 0; j < CP; ++j) {
-    const char* at = sm + L::kS + ((c0 + j) >> 3) * DK * 16 + row * 16 + (j & 7) * 2;
-    S[j] = has_row ? (term(at) + term(at + L::kSLo)) * inv_s : 0.f;
-  }
+  float* const part = reinterpret_cast<float*>(sm + L::kW + g * L::kWTurn);   // [warps][p, r: CP each], then [warps] q.k
+  float* const dots = part + L::kTurnWarps * 2 * CP;
+  barrier();                                                    // the group's o are written, w's place is free
   for (int t = 0; t < kChunk && t0 + t < req.len; ++t) {
     const long long gate = (req.start + static_cast<long long>(t0 + t)) * p.gate_row + vh;
     const bool bf16 = p.in_dtype == GDN_DTYPE_BF16;
@@ -699,20 +851,20 @@ __device__ __noinline__ void again_by_token(const SeqParams& p, const SegReq& re
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) qk += __shfl_xor_sync(~0u, qk, o);
     if (lane < CP) {
-      part[warp * 2 * CP + lane] = mine_p;
-      part[warp * 2 * CP + CP + lane] = mine_r;
+      part[gw * 2 * CP + lane] = mine_p;
+      part[gw * 2 * CP + CP + lane] = mine_r;
     }
-    if (lane == 0) dots[warp] = qk;
+    if (lane == 0) dots[gw] = qk;
     barrier();
     const int j = lane % CP;                                    // this lane's column
-    const float* mine = part + (warp & ~3) * 2 * CP + j;
+    const float* mine = part + (gw & ~3) * 2 * CP + j;
     qk = (dots[0] + dots[1]) + (dots[2] + dots[3]);
     const float pj = (mine[0] + mine[2 * CP]) + (mine[4 * CP] + mine[6 * CP]);
     const float rj = (mine[CP] + mine[3 * CP]) + (mine[5 * CP] + mine[7 * CP]);
-    const float u = beta * (V[((col0 + c0 + j) / 4 * kChunk + t) * 4 + (j & 3)] - pj), o = p.q_scale * fmaf(qk, u, rj);
+    const float u = beta * (V[((c0 + j) / 4 * kChunk + t) * 4 + (j & 3)] - pj), o = p.q_scale * fmaf(qk, u, rj);
     for (int i = 0; i < CP; ++i) S[i] = fmaf(k, __shfl_sync(~0u, u, i), S[i]);
-    if ((warp & 3) == 0 && lane < CP) {
-      const long long at = ((req.start + static_cast<long long>(t0 + t)) * p.Hv + vh) * p.dv + col0 + c0 + j;
+    if ((gw & 3) == 0 && lane < CP) {
+      const long long at = ((req.start + static_cast<long long>(t0 + t)) * p.Hv + vh) * p.dv + c0 + j;
       if (p.out_dtype == GDN_DTYPE_BF16) static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(o);
       else static_cast<float*>(p.out)[at] = o;
     }
@@ -737,108 +889,115 @@ seq_chain_kernel(const SeqParams p, const __grid_constant__ Segment seg, const c
   const char* const v_ws = ws + req.slot0 * slot_bytes + p.Hk * seq_kq_bytes(DK) + vh * seq_v_bytes(p.dv);
   const bool aborted = launch_aborted(p.err);
 
-  if (warp == L::kWarps) tmem_alloc(reinterpret_cast<uint32_t*>(bar + kTmemAt), L::kTmem);
+  if (warp == 0) tmem_alloc(reinterpret_cast<uint32_t*>(bar + kTmemAt), L::kTmem);
   if (tid == 0) {
     mbar_init_n(bar + kKqFull, 1);
     mbar_init_n(bar + kMnFull, 1);
-    mbar_init_n(bar + kSReady, L::kWarps);
-    mbar_init_n(bar + kD1, 1);
-    mbar_init_n(bar + kWReady, 2 * L::kGroups);
-    mbar_init_n(bar + kD2, 1);
-    mbar_init_n(bar + kUReady, 2 * L::kGroups);
-    mbar_init_n(bar + kD3, 1);
+    for (int g = 0; g < L::kTurns; ++g) {
+      mbar_init_n(bar + kMetaFull + g, 1);
+      mbar_init_n(bar + kD1 + g, 1), mbar_init_n(bar + kD2 + g, 1), mbar_init_n(bar + kD3 + g, 1);
+      mbar_init_n(bar + kMeet + g, L::kTurnWarps);
+    }
+    static_assert(L::kTurns == 2, "two of each");
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     fence_proxy_async();
   }
+  int* const count = reinterpret_cast<int*>(sm + L::kCount);
+  if (tid < 16) count[tid] = 0;
   const bool stop = __syncthreads_or(aborted);
   const uint32_t tmem = *reinterpret_cast<uint32_t*>(bar + kTmemAt);
-  if (warp == L::kWarps) tmem_relinquish();
+  if (warp == 0) tmem_relinquish();
   bool late = false;
   // A wait that gave up is not repeated: the loops run to their end, the results are reported as lost.
   auto wait = [&](int which, int parity) {
     if (!late && !mbar_wait_quiet(bar + which, parity)) late = true;
   };
-
-  if (stop) {
-    // an earlier launch gave up: nothing is done
-  } else if (warp == L::kWarps) {
-    // The whole warp walks the loop and one elected lane issues: descriptors stay in uniform registers.
-    auto load_k = [&](int i) {         // chunk i of the segment
-      const int place = (req.c0 + i) & 1 ? 2 : 0;
-      const char* src = kq_ws + i * slot_bytes;
+  // k, q and [M; N] of chunk i of the segment, by a warp: a lane a copy
+  auto load_chunk = [&](int i) {
+    if (lane == 0) {
       mbar_expect(bar + kKqFull, 4 * L::kImage);
-      bulk_g2s(sm + L::kKq + place * L::kImage, src, L::kImage, bar + kKqFull);
-      bulk_g2s(sm + L::kKq + L::kKqLo + place * L::kImage, src + L::kImage, L::kImage, bar + kKqFull);
-    };
-    auto load_q = [&](int i) {
-      const char* src = kq_ws + i * slot_bytes + 2 * L::kImage;
-      bulk_g2s(sm + L::kKq + L::kImage, src, L::kImage, bar + kKqFull);
-      bulk_g2s(sm + L::kKq + L::kKqLo + L::kImage, src + L::kImage, L::kImage, bar + kKqFull);
-    };
-    auto load_mn = [&](int i) {
       mbar_expect(bar + kMnFull, 2 * L::kMnLo);
-      bulk_g2s(sm + L::kMn, v_ws + i * slot_bytes, 2 * L::kMnLo, bar + kMnFull);
-    };
-    auto given_up = [&]() { return late = __any_sync(~0u, late); };
-    if (elect_one()) {
-      load_k(0);
-      load_q(0);
-      load_mn(0);
     }
     __syncwarp();
-    const uint64_t s_b = umma_desc(smem_addr(sm + L::kS), 128, DK * 16);
-    const uint64_t w_b = umma_desc(smem_addr(sm + L::kW), 128, kChunk * 16);
-    const uint64_t mn_a = umma_desc(smem_addr(sm + L::kMn), 128, 1024);
-    for (int i = 0; i < req.nc; ++i) {
-      const int odd = (req.c0 + i) & 1, ph = i & 1;
-      wait(kKqFull, ph);
-      wait(kSReady, ph);
-      if (given_up()) break;
-      tmem_fence_after();
-      if (elect_one()) {
-        // rows 0 to 127: [K; Q], or [Q; K] in odd chunks
-        product<DK / 16>(tmem, umma_desc(smem_addr(sm + L::kKq + odd * L::kImage), 128, DK * 16), s_b, L::kKqLo, L::kSLo, 256,
-                         256, idesc_f16(NB, false, true));
-        umma_commit(bar + kD1);
-        if (i + 1 < req.nc) load_k(i + 1);
-      }
-      __syncwarp();
-      wait(kD1, ph);
-      if (i + 1 < req.nc && elect_one()) load_q(i + 1);
-      __syncwarp();
-      wait(kMnFull, ph);
-      wait(kWReady, ph);
-      if (given_up()) break;
-      tmem_fence_after();
-      if (elect_one()) {
-        product<kChunk / 16>(tmem + NB, mn_a, w_b, L::kMnLo, L::kWLo, 256, 256, idesc_f16(NB, false, true));
-        umma_commit(bar + kD2);
-      }
-      __syncwarp();
-      wait(kD2, ph);
-      if (i + 1 < req.nc && elect_one()) load_mn(i + 1);
-      __syncwarp();
-      wait(kUReady, ph);
-      if (given_up()) break;
-      tmem_fence_after();
-      if (elect_one()) {
-        product<kChunk / 16>(tmem + 2 * NB, umma_desc(smem_addr(sm + L::kKq + odd * 2 * L::kImage), DK * 16, 128), w_b, L::kKqLo,
-                             L::kWLo, 2 * DK * 16, 256, idesc_f16(NB, true, true));
-        umma_commit(bar + kD3);
-      }
-      __syncwarp();
-    }
-    wait(kD3, (req.nc - 1) & 1);
-    if (late) {        // whatever was in flight has had twice the time that a wait gives it
-      mbar_wait(bar + kKqFull, 0), mbar_wait(bar + kKqFull, 1), mbar_wait(bar + kMnFull, 0), mbar_wait(bar + kMnFull, 1);
+    if (lane < 5) {
+      const int place = lane >= 2 ? 1 : (req.c0 + i) & 1 ? 2 : 0;              // lanes 0 to 3: Kh Kl Qh Ql
+      const char* src = kq_ws + i * slot_bytes + lane * L::kImage;
+      char* dst = sm + L::kKq + (lane & 1) * L::kKqLo + place * L::kImage;
+      if (lane == 4) src = v_ws + i * slot_bytes, dst = sm + L::kMn;
+      bulk_g2s(dst, src, lane == 4 ? 2 * L::kMnLo : L::kImage, bar + (lane == 4 ? kMnFull : kKqFull));
     }
     __syncwarp();
-  } else {
+  };
+  auto load_meta = [&](int i) {        // gates and bounds, by a thread
+    mbar_expect(bar + kMetaFull + (i & 1), L::kMetaBytes);
+    bulk_g2s(sm + L::kMeta + (i & 1) * L::kMetaBytes, v_ws + i * slot_bytes + 2 * L::kMnLo + kChunk * p.dv * 4, L::kMetaBytes,
+             bar + kMetaFull + (i & 1));
+  };
+
+  if (!stop) {
+    if (tid == 0) load_meta(0);
+    if (warp == 0) load_chunk(0);
     constexpr int CP = L::kCols, kPairs = CP / 2;
     const int row = (warp & 3) * 32 + lane, c0 = (warp >> 2) * CP;            // lane of tensor memory, columns of the slice
-    const uint32_t ta = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + c0;
+    const int g = c0 / L::kN, cg = c0 % L::kN;                                // group, columns in it
+    const uint32_t ta = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + 2 * g * L::kD + cg;
+    char* const s_op = sm + L::kS + g * L::kSTurn + (cg >> 3) * DK * 16;
+    char* const w_op = sm + L::kW + g * L::kWTurn + (cg >> 3) * kChunk * 16;
+    float* const most = maxima + g * 2 * L::kTurnWarps;                      // [2][2 groups][T, o][warps]
+    const int gw = warp - g * L::kTurnWarps;                                  // warp of the group
     const bool has_row = row < DK;
-    auto soft_barrier = [] { asm volatile("bar.sync 1, %0;" ::"n"(L::kSoft) : "memory"); };
+    const bool copies = g == L::kTurns - 1 && (gw & 1) == 0 && gw < 4;        // of these two warps that with q rows issues the copies
+    // The warp that arrives last of n issues what the others have made ready: no warp is kept for it (a seventeenth would
+    // leave each thread 96 registers), and no other has to be woken.
+    auto last_of = [&](int which, int n) {
+      int last = 0;
+      __syncwarp();
+      if (lane == 0) {
+        int old;
+        asm volatile("atom.acq_rel.cta.shared::cta.add.u32 %0, [%1], 1;" : "=r"(old) : "r"(smem_addr(count + which)) : "memory");
+        last = old == n - 1;
+        if (last) count[which] = 0;
+      }
+      return __shfl_sync(~0u, last, 0) != 0;
+    };
+    auto issue_d1 = [&](int i) {                   // rows 0 to 127: [K; Q], or [Q; K] in odd chunks
+      wait(kKqFull, i & 1);
+      tmem_fence_after();
+      if (elect_one()) {
+        product_wide<DK / 16, L::kN>(tmem + 2 * g * L::kD, umma_desc(smem_addr(sm + L::kKq + ((req.c0 + i) & 1) * L::kImage), 128, DK * 16),
+                                     umma_desc(smem_addr(sm + L::kS + g * L::kSTurn), 128, DK * 16), L::kKqLo, 256, 256, false);
+        umma_commit(bar + kD1 + g);
+      }
+      __syncwarp();
+    };
+    auto issue_d2 = [&](int i) {
+      wait(kMnFull, i & 1);
+      tmem_fence_after();
+      if (elect_one()) {
+        product_wide<kChunk / 16, L::kN>(tmem + 2 * g * L::kD + L::kD, umma_desc(smem_addr(sm + L::kMn), 128, 1024),
+                                         umma_desc(smem_addr(sm + L::kW + g * L::kWTurn), 128, kChunk * 16), L::kMnLo, 256, 256, false);
+        umma_commit(bar + kD2 + g);
+      }
+      __syncwarp();
+    };
+    auto issue_d3 = [&](int i) {
+      tmem_fence_after();
+      if (elect_one()) {
+        product_wide<kChunk / 16, L::kN>(tmem + 2 * g * L::kD, umma_desc(smem_addr(sm + L::kKq + ((req.c0 + i) & 1) * 2 * L::kImage), DK * 16, 128),
+                                         umma_desc(smem_addr(sm + L::kW + g * L::kWTurn), 128, kChunk * 16), L::kKqLo, 2 * DK * 16, 256, true);
+        umma_commit(bar + kD3 + g);
+      }
+      __syncwarp();
+    };
+// the group's warps meet; bounded like every other wait (what the warps decide on may be garbage once one has given up)
+    int meetings = 0;
+    auto group_barrier = [&] {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar + kMeet + g);
+      wait(kMeet + g, meetings++ & 1);
+    };
+    // sixteen columns of a product, its two parts added
+    auto product_at = [&](uint32_t at, u64 (&d)[8]) { tmem_sum_pairs(at, at + L::kN, d); };
     u64 S[kPairs];
     // the state before the segment: the call's, or what the segment before left
     {
@@ -854,18 +1013,22 @@ seq_chain_kernel(const SeqParams p, const __grid_constant__ Segment seg, const c
         }
       }
     }
-    float smax, omax = 0.f, inv_s;
-    // the largest entry of T, and of the chunk's o, over all threads
-    auto find_maxima = [&]() {
+    float smax = 0.f, omax = 0.f, inv_s;
+    // The largest entries of T and of the chunk's o: each warp notes its own when it hands T on, in the half of the table
+    // that the chunk's number gives, and all read them once D1 is there.
+    auto note_maxima = [&](int half) {
       float big = 0.f;
 #pragma unroll
       for (int j = 0; j < kPairs; ++j) big = abs_max(big, S[j]);
       big = warp_max(big);
       const float bigo = warp_max(omax);
-      if (lane == 0) maxima[warp] = big, maxima[L::kWarps + warp] = bigo;
-      soft_barrier();
-      smax = warp_max(lane < L::kWarps ? maxima[lane] : 0.f);
-      omax = warp_max(lane < L::kWarps ? maxima[L::kWarps + lane] : 0.f);
+      if (lane == 0) most[half * 2 * L::kWarps + gw] = big, most[half * 2 * L::kWarps + L::kTurnWarps + gw] = bigo;
+      omax = 0.f;
+    };
+    auto read_maxima = [&](int half, float& s, float& o) {
+      const float* m = most + half * 2 * L::kWarps;
+      s = warp_max(lane < L::kTurnWarps ? m[lane] : 0.f);
+      o = warp_max(lane < L::kTurnWarps ? m[L::kTurnWarps + lane] : 0.f);
     };
     // packed pairs, scaled, into a two-term operand at `at`, whose groups of eight columns lie `step` bytes apart
     auto put = [&](const u64* x, float sc, char* at, int step, int lo_at) {
@@ -881,19 +1044,48 @@ seq_chain_kernel(const SeqParams p, const __grid_constant__ Segment seg, const c
         *reinterpret_cast<uint4*>(at + j / 4 * step + lo_at) = lo;
       }
     };
-    auto put_state = [&]() {
-      const float sc = scale_for(smax, inv_s);
+    // T, whose entries are at most `bound`, into its operand for chunk i
+    auto put_state = [&](int i, float bound) {
+      const float sc = scale_for(bound, inv_s);
       if (has_row) {
 #pragma unroll
-        for (int j = 0; j < CP; j += 16) put(S + j / 2, sc, sm + L::kS + ((c0 + j) >> 3) * DK * 16 + row * 16, DK * 16, L::kSLo);
+        for (int j = 0; j < CP; j += 16) put(S + j / 2, sc, s_op + (j >> 3) * DK * 16 + row * 16, DK * 16, L::kSLo);
       }
+      note_maxima(i & 1);
       fence_proxy_async();
       tmem_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar + kSReady);
+      if (last_of(kSDone + g, L::kTurnWarps)) issue_d1(i);
+    };
+    // T once more with the scale that its largest entry allows, by all warps of the group (D1 of chunk i is done)
+    auto put_again = [&](int i) {
+      group_barrier();                             // all have read the maxima
+      note_maxima(i & 1);
+      group_barrier();
+      float unused;
+      read_maxima(i & 1, smax, unused);
+      put_state(i, smax);
+    };
+    // Chunk i once more, token by token: T before it lies in D2's place.
+    auto take_again = [&](int i) {
+      float s[CP];
+#pragma unroll
+      for (int j = 0; j < CP; j += 16) {
+        u64 d[8];
+        tmem_pairs(ta + L::kD + j, d);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float2 f = unpack2(d[k]);
+          s[j + 2 * k] = f.x, s[j + 2 * k + 1] = f.y;
+        }
+      }
+      again_by_token<DK, NB>(p, req, vh, row, has_row, g, gw, col0 + c0, (req.c0 + i) * kChunk, kq_ws + i * slot_bytes,
+                             reinterpret_cast<const float*>(v_ws + i * slot_bytes + 4 * 128 * kChunk), sm, s, meetings, late);
+#pragma unroll
+      for (int j = 0; j < kPairs; ++j) S[j] = pack2(s[2 * j], s[2 * j + 1]);
     };
     u64 a[kPairs];                                             // v of a k row; the first part of o of a q row
-    auto load_v = [&](int i) {
+    u64 ahead[kPairs];                                         // v of the next chunk
+    auto load_v = [&](int i, u64* a) {
       const float4* V = reinterpret_cast<const float4*>(v_ws + i * slot_bytes + 4 * 128 * kChunk) + (col0 + c0) / 4 * kChunk + (row & 63);
 #pragma unroll
       for (int j = 0; j < kPairs; j += 2) {
@@ -905,7 +1097,7 @@ seq_chain_kernel(const SeqParams p, const __grid_constant__ Segment seg, const c
     // bytes, so that neither rows nor units share banks; the units are the places of w that this warp itself writes.
     auto store_out = [&](int t0) {
       auto place = [&](int unit, int r) {                      // units: eight columns, high and low terms
-        return sm + L::kW + (unit & 1) * L::kWLo + ((c0 >> 3) + (unit >> 1)) * kChunk * 16 + (row & 32) * 16 + (r ^ unit) * 16;
+        return w_op + (unit & 1) * L::kWLo + (unit >> 1) * kChunk * 16 + (row & 32) * 16 + (r ^ unit) * 16;
       };
       const bool bf16 = p.out_dtype == GDN_DTYPE_BF16;
       if (bf16) {
@@ -937,70 +1129,99 @@ seq_chain_kernel(const SeqParams p, const __grid_constant__ Segment seg, const c
       }
       __syncwarp();
     };
-    if ((row >> 6) == (req.c0 & 1)) load_v(0);
-    find_maxima();
-    put_state();
+    if ((row >> 6) == (req.c0 & 1)) load_v(0, a);
+    // the first T's scale: its largest entry
+    int d1_done = 0;                               // D1's so far: one a chunk, and those taken again
+    note_maxima(1);
+    group_barrier();
+    {
+      float unused;
+      read_maxima(1, smax, unused);
+    }
+    put_state(0, smax);
+    float s_bound = smax, u_bound = 0.f, o_bound = 0.f, omax_before;   // of the chunk before
     for (int i = 0; i < req.nc; ++i) {
       const int odd = (req.c0 + i) & 1, ph = i & 1;
       const bool k_row = (row >> 6) == odd;                    // this thread's row is a token's k (else its q)
       const int t = row & 63;
-      const float* meta = reinterpret_cast<const float*>(v_ws + i * slot_bytes + 4 * 128 * kChunk + kChunk * p.dv * 4);
-      const float first = __ldg(meta + t), left = __ldg(meta + kChunk + t);
-      const float4 m0 = __ldg(reinterpret_cast<const float4*>(meta + 2 * kChunk));
-      const float4 m1 = __ldg(reinterpret_cast<const float4*>(meta + 2 * kChunk + 4));
+      const float* meta = reinterpret_cast<const float*>(sm + L::kMeta + ph * L::kMetaBytes);
+      wait(kMetaFull + ph, (i >> 1) & 1);
+      const float first = meta[t], left = meta[kChunk + t];
+      const float4 m0 = *reinterpret_cast<const float4*>(meta + 2 * kChunk);
+      const float4 m1 = *reinterpret_cast<const float4*>(meta + 2 * kChunk + 4);
       const float whole = m0.x, inv_m = m0.y, inv_n = m0.z, vmax = m0.w, mbound = m1.x, fmax_ = m1.y, nbound = m1.z;
+      if (!k_row && i + 1 < req.nc) load_v(i + 1, ahead);      // a q row is the next chunk's k row
+      wait(kD1 + g, d1_done++ & 1);
+      tmem_fence_after();
+      read_maxima(ph, smax, omax_before);
+      // Bounds far above the values have cost these their bits.  T itself is exact: its operand is made again.  u and o are
+      // not: the chunk before is taken again, token by token.
+      if (i > 0 && (s_bound * kRange > smax || o_bound * kRange > omax_before)) {
+        if (u_bound * kRange > smax || o_bound * kRange > omax_before) take_again(i - 1);
+        put_again(i);
+        wait(kD1 + g, d1_done++ & 1);
+        tmem_fence_after();
+      }
       const float w_bound = (vmax + fmax_ * (DK == 128 ? 11.32f : DK == 64 ? 8.001f : 5.657f) * smax) * 1.001f;
-      const float u_bound = mbound * w_bound * 1.001f;
+      u_bound = mbound * w_bound * 1.001f;
+      o_bound = nbound * w_bound * fabsf(p.q_scale);
+      s_bound = (whole * smax + 64.f * u_bound) * 1.001f;
       float inv_w, inv_u;
       const float sc_w = scale_for(w_bound, inv_w), sc_u = scale_for(u_bound, inv_u);
       const float f1 = first * (inv_s * (1.f / kUnit));
-      char* const w_at = sm + L::kW + (c0 >> 3) * kChunk * 16 + t * 16;
-      wait(kD1, ph);
-      tmem_fence_after();
+      char* const w_at = w_op + t * 16;
       if (k_row) {
         const u64 f = pack2(-f1, -f1);
 #pragma unroll
         for (int j = 0; j < CP; j += 16) {
           u64 d[8];
-          tmem_pairs(ta + j, d);
+          product_at(ta + j, d);
 #pragma unroll
           for (int k = 0; k < 8; ++k) d[k] = fma2(f, d[k], a[j / 2 + k]);
           put(d, sc_w, w_at + (j >> 3) * kChunk * 16, kChunk * 16, L::kWLo);
         }
         fence_proxy_async();
         tmem_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar + kWReady);
       } else {
         const u64 f = pack2(f1 * p.q_scale, f1 * p.q_scale);
 #pragma unroll
         for (int j = 0; j < CP; j += 16) {
           u64 d[8];
-          tmem_pairs(ta + j, d);
+          product_at(ta + j, d);
 #pragma unroll
           for (int k = 0; k < 8; ++k) a[j / 2 + k] = mul2(d[k], f);
         }
+        tmem_fence_before();                                   // D3 takes D1's place
       }
-      wait(kD2, ph);
+      if (last_of(kWDone + g, L::kTurnWarps)) issue_d2(i);
+      // (the other group has read the gates of the chunk before: it took part in D2 there, without which nobody is here)
+      if (!k_row && copies && i + 1 < req.nc && elect_one()) load_meta(i + 1);
+      __syncwarp();
+      wait(kD2 + g, ph);
       tmem_fence_after();
+      if (!k_row && copies && i + 1 < req.nc) {
+        // A warp of q rows fetches the next chunk: with D2 of both groups done nothing reads Q or [M; N] any more, and D3 of
+        // the chunk before, the last to read the other K, was done before T went to D1.
+        wait(kD2, ph);
+        load_chunk(i + 1);
+      }
       if (k_row) {
         const float f = left * inv_m * inv_w * sc_u;
 #pragma unroll
         for (int j = 0; j < CP; j += 16) {
           u64 d[8];
-          tmem_pairs(ta + NB + j, d);
+          product_at(ta + L::kD + j, d);
           put(d, f, w_at + (j >> 3) * kChunk * 16, kChunk * 16, L::kWLo);
         }
         fence_proxy_async();
         tmem_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar + kUReady);
+        if (last_of(kUDone + g, L::kTurnWarps / 2)) issue_d3(i);
       } else {
         const u64 f = pack2(inv_n * inv_w * p.q_scale, inv_n * inv_w * p.q_scale);
 #pragma unroll
         for (int j = 0; j < CP; j += 16) {
           u64 d[8];
-          tmem_pairs(ta + NB + j, d);
+          product_at(ta + L::kD + j, d);
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
             a[j / 2 + k] = fma2(f, d[k], a[j / 2 + k]);
@@ -1008,36 +1229,32 @@ seq_chain_kernel(const SeqParams p, const __grid_constant__ Segment seg, const c
           }
         }
       }
-      wait(kD3, ph);
+      // T before the chunk is kept in D2's place, of which this thread has read its part
+#pragma unroll
+      for (int j = 0; j < CP; j += 16) tmem_put_pairs(ta + L::kD + j, S + j / 2);
+      wait(kD3 + g, ph);
       tmem_fence_after();
       const u64 f3 = pack2(inv_u * (1.f / kUnit), inv_u * (1.f / kUnit)), whole2 = pack2(whole, whole);
 #pragma unroll
       for (int j = 0; j < CP; j += 16) {
         u64 d[8];
-        tmem_pairs(ta + 2 * NB + j, d);
+        product_at(ta + j, d);
 #pragma unroll
         for (int k = 0; k < 8; ++k) S[j / 2 + k] = has_row ? fma2(whole2, S[j / 2 + k], mul2(f3, d[k])) : 0ull;
       }
-      find_maxima();
-      // Values far below what the bounds allow have lost their bits: the chunk is taken again, token by token.
-      const float o_bound = nbound * w_bound * fabsf(p.q_scale);
-      const bool again = u_bound * kRange > smax || o_bound * kRange > omax;
-      if (again) {
-        float s[CP];
-        again_by_token<DK, NB>(p, req, vh, row, has_row, c0, col0, (req.c0 + i) * kChunk, inv_s, kq_ws + i * slot_bytes,
-                               reinterpret_cast<const float*>(v_ws + i * slot_bytes + 4 * 128 * kChunk), sm, s);
-#pragma unroll
-        for (int j = 0; j < kPairs; ++j) S[j] = pack2(s[2 * j], s[2 * j + 1]);
-        find_maxima();
-      }
-      omax = 0.f;
-      if (i + 1 < req.nc) put_state();
+      tmem_wait_st();
+      if (i + 1 < req.nc) put_state(i + 1, s_bound);
       if (!k_row) {
         // o, in rows again: through the warp's own part of w's operand, which D3 was the last to read
-        if (!again) store_out((req.c0 + i) * kChunk + (row & 32));
-        if (i + 1 < req.nc) load_v(i + 1);                     // a q row is the next chunk's k row
+        store_out((req.c0 + i) * kChunk + (row & 32));
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j) a[j] = ahead[j];
       }
     }
+    note_maxima(req.nc & 1);
+    group_barrier();
+    read_maxima(req.nc & 1, smax, omax_before);
+    if (u_bound * kRange > smax || o_bound * kRange > omax_before) take_again(req.nc - 1);
     if (has_row) {
       float* dst = p.state_out + req.b * p.state_stride + (static_cast<long long>(vh) * DK + row) * p.dv + col0 + c0;
 #pragma unroll
@@ -1064,8 +1281,13 @@ seq_chain_kernel(const SeqParams p, const __grid_constant__ Segment seg, const c
       }
     }
   }
-  if (__syncthreads_or(late) && tid == 0) device_error(p.err, GDN_DEVERR_TIMEOUT, req.b);
-  if (warp == L::kWarps) tmem_dealloc(tmem, L::kTmem);
+  if (__syncthreads_or(late) && tid == 0) {
+    // whatever was in flight has had twice the time that a wait gives it
+    mbar_wait(bar + kKqFull, 0), mbar_wait(bar + kKqFull, 1), mbar_wait(bar + kMnFull, 0), mbar_wait(bar + kMnFull, 1);
+    device_error(p.err, GDN_DEVERR_TIMEOUT, req.b);
+  }
+  __syncthreads();
+  if (warp == 0) tmem_dealloc(tmem, L::kTmem);
 }
 
 template <typename F>
@@ -1074,10 +1296,13 @@ cudaError_t with_smem(F kernel, int bytes) {
 }
 template <typename InT, int DK, int KT>
 cudaError_t launch_prepare(const SeqParams& p, const Segment& seg, char* ws, cudaStream_t s) {
-  auto k = seq_prepare_kernel<InT, DK, KT>;
-  cudaError_t e = with_smem(k, Prep<DK>::kTotal);
+  auto keys = seq_keys_kernel<InT, DK, KT>;
+  auto values = seq_values_kernel<InT, KT>;
+  cudaError_t e = with_smem(keys, PrepK<DK>::kTotal);
+  if (e == cudaSuccess) e = with_smem(values, PrepV::kTotal);
   if (e != cudaSuccess) return e;
-  k<<<dim3(p.Hk, seg.slots, (p.Hv / p.Hk + kHeads - 1) / kHeads), kPrepThreads, Prep<DK>::kTotal, s>>>(p, seg, ws);
+  keys<<<dim3(p.Hk, seg.slots), kPrepThreads, PrepK<DK>::kTotal, s>>>(p, seg, ws);
+  values<<<dim3(p.Hv, seg.slots), kPrepThreads, PrepV::kTotal, s>>>(p, seg, ws);
   return cudaGetLastError();
 }
 template <int DK, int NB>
@@ -1096,15 +1321,13 @@ cudaError_t launch_d(const SeqParams& p, const Segment& seg, char* ws, cudaStrea
                       ? (wide ? launch_prepare<bf16, DK, 8>(p, seg, ws, s) : launch_prepare<bf16, DK, 4>(p, seg, ws, s))
                       : (wide ? launch_prepare<float, DK, 8>(p, seg, ws, s) : launch_prepare<float, DK, 4>(p, seg, ws, s));
   if (e != cudaSuccess) return e;
-  // whole heads a CTA, or half ones where the other half of the GPU would be idle
-  if (p.dv == 128 && seg.n * p.Hv > 76) return launch_chain<DK, 128>(p, seg, ws, s);
-  if (p.dv >= 64 && seg.n * p.Hv * (p.dv / 64) > 38) return launch_chain<DK, 64>(p, seg, ws, s);
+  // 64 columns a CTA, or 32 where the other half of the GPU would be idle.  (With all 128 of a head a chunk takes more than
+  // twice the time: 9.3 against 3.8 us.)
+  if (p.dv >= 64 && seg.n * p.Hv * (p.dv / 64) > 76) return launch_chain<DK, 64>(p, seg, ws, s);
   return launch_chain<DK, 32>(p, seg, ws, s);
 }
 
 }  // namespace
-
-int seq_requests_at_once(int Hv) { return Hv >= 152 ? 1 : 152 / Hv < kSegReqs ? 152 / Hv : kSegReqs; }
 
 cudaError_t launch_seq_chunks(const SeqParams& p, const Segment& seg, void* workspace, cudaStream_t s) {
   char* ws = static_cast<char*>(workspace);
