@@ -22,7 +22,7 @@ LIB_PATH = os.path.join(LIB_DIR, "libgdn_tree.so")
 
 SOURCES = ["hld_schedule.cpp", "ddtree.cpp", "gdn_abi.cu", "gdn_conv.cu", "gdn_verify.cu", "gdn_verify_ut.cu", "gdn_verify_tc.cu", "gdn_verify_tcp.cu", "gdn_commit.cu", "gdn_noalloc.cu",
            "gdn_kv4.cu", "gdn_kv4_attn.cu", "gdn_kv4_dec.cu", "gdn_kv4_tree.cu",
-           "gdn_accept.cu", "gdn_seq.cu", "gdn_seq_chunk.cu", "gdn_seq_rec.cu", "gdn_logprobs.cu"]
+           "gdn_accept.cu", "gdn_seq.cu", "gdn_seq_chunk.cu", "gdn_seq_rec.cu", "gdn_seq_step.cu", "gdn_logprobs.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

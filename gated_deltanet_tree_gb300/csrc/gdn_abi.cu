@@ -691,7 +691,8 @@ gdn_status gdn_step(const gdn_dims* d, int32_t layers, int32_t layer, int32_t B,
                     conv_out, out_o, out_dtype, banks, err, p));
   if (live) GDN_CHECK_PTR(live, "live");
   p.live = live;
-  cudaError_t e = gdn::launch_seq_rec(p, nullptr, B, stream);
+  cudaError_t e = cudaSuccess;
+  if (!gdn::launch_seq_step(p, B, stream, e)) e = gdn::launch_seq_rec(p, nullptr, B, stream);
   if (e != cudaSuccess) return cuda_fail(e, "step launch");
   return GDN_OK;
 }

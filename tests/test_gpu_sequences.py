@@ -307,6 +307,37 @@ def test_step(heads, dtype, out, B):
     assert not s2[:, 0].any() and not w2[:, 0].any()
 
 
+@pytest.mark.parametrize("heads", ["qwen", "d64", "d64x128", "d128x64", "one_head"])
+@pytest.mark.parametrize("dtype,out", [("bf16", "bf16"), ("f32", "f32")])
+@pytest.mark.parametrize("K,conv", [(4, 1), (1, 1), (3, 1), (4, 0)])
+def test_step_of_many(heads, dtype, out, K, conv):
+    """Batches large enough for the stream of tiles: in place, to other buffers, and with requests that take no part (runs of
+    them at the front, in the middle and at the end)."""
+    B = {"qwen": 170, "d64": 190, "d64x128": 320, "d128x64": 155, "one_head": 460}[heads]
+    shape = (1, 1, 128, 128) if heads == "one_head" else heads
+    c = Case(22, shape, [1] * B, dtype, out, K=K, conv=conv, layers=1, layer=0)
+    ref = c.reference()
+    state, window = c.state.clone(), c.conv.clone()
+    r = c.runner()
+    r.step(*c.inputs(), state, window, c.out)
+    r.check_error()
+    check(c, ref, c.out, state[:, 0], window[:, 0])
+    live = torch.ones(B, dtype=torch.int32, device="cuda")
+    live[:7], live[60:75], live[B - 9:], live[::11] = 0, 0, 0, 0
+    on = live.bool()
+    s2, w2, o2 = torch.full_like(state, 5.0), torch.full_like(window, 5.0), torch.full_like(c.out, 5.0)
+    r.step(*c.inputs(), c.state, c.conv, o2, state_out=s2, conv_out=w2, live=live)
+    r.check_error()
+    assert torch.equal(s2[on], state[on]) and torch.equal(o2[on], c.out[on])
+    assert (s2[~on] == 5.0).all() and (o2[~on] == 5.0).all() and (w2[~on] == 5.0).all()
+    if conv:
+        assert torch.equal(w2[on], window[on])
+    live.zero_()
+    r.step(*c.inputs(), s2, w2, o2, live=live)
+    r.check_error()
+    assert torch.equal(s2[on], state[on]) and torch.equal(o2[on], c.out[on])
+
+
 @pytest.mark.parametrize("K,conv,act", [(1, 1, 1), (2, 1, 0), (6, 1, 1), (8, 1, 1), (4, 0, 1)])
 def test_step_taps_and_modes(K, conv, act):
     c = Case(21, "qwen", [1, 1, 1], "bf16", K=K, conv=conv, act=act)
