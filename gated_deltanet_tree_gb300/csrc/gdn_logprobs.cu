@@ -4,10 +4,11 @@
 // t = sum e^(z - m) (z - m); then log p_i = z_i - m - log s and the entropy is log s - t / s.
 //
 // The best `top` tokens (larger logit first, lower index on ties) come from the same pass.  A tile
-// of 8192 entries lies in the CTA's registers; the top-th largest of 32 group maxima bounds the
-// top-th largest entry from below, so a handful of entries pass it and are put on a list in shared
-// memory; its exact best are picked by counting, and the worst of them is the bound from then on.
-// A tile with more candidates than the list holds (long ties, sorted rows) picks its best one by one.
+// of 4096 entries lies in the CTA's registers; the top-th largest of 32 group maxima of the first
+// one bounds its top-th largest entry from below, so a handful of entries pass and are put on a list
+// in shared memory.  Its exact best are picked by counting, and the worst of them is the bound of
+// later tiles; it is renewed after ever more of them, and the warps need no barrier in between.  Where more entries pass than the list holds
+// (long ties, rising rows) the best are found tile by tile, one after another, in a second pass.
 //
 // A cluster of up to eight CTAs shares a row where rows are few, joined through distributed
 // shared memory.  The bound is the row's bytes, read once.
@@ -23,7 +24,7 @@ namespace {
 
 typedef unsigned long long u64;
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kVals = 32;                    // entries of a tile in a thread's registers
+constexpr int kVals = 16;                    // entries of a tile in a thread's registers
 constexpr int kCap = 1024;                   // candidates
 constexpr int kMaxCluster = 8;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -70,13 +71,18 @@ __device__ __forceinline__ float exp2_fast(float x) {   // results below 2^-126 
   return y;
 }
 
+__device__ __forceinline__ float max_nan(float a, float b) {   // a NaN stays
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
 struct Sums {
   float m, s, t;
 };
 __device__ __forceinline__ float finite_ref(float m) { return m == -INFINITY ? 0.f : m; }
 __device__ __forceinline__ Sums join(const Sums& a, const Sums& b) {
   Sums r;
-  r.m = fmaxf(a.m, b.m);
+  r.m = max_nan(a.m, b.m);
   const float ref = finite_ref(r.m);
   // a side that saw nothing has s = t = 0 and m = -inf: its difference only must not be infinite
   const float da = fmaxf(a.m - ref, -1e4f), db = fmaxf(b.m - ref, -1e4f);
@@ -96,7 +102,7 @@ struct Shared {
 };
 
 // The best min(n, top) of the first n candidates, in order, at the front of the list; n is uniform.  Returns how many.
-__device__ int pick(Shared& sh, int n, int top) {
+__device__ __forceinline__ int pick(Shared& sh, int n, int top) {
   const int tid = threadIdx.x;
   for (int i = tid; i < n; i += kThreads) {
     const u64 k = sh.cand[i];
@@ -112,8 +118,92 @@ __device__ int pick(Shared& sh, int n, int top) {
   return n;
 }
 
+// A tile of a row in a thread's registers: entry i is index_of(at, i) of the row; entries outside [0, V) and the CTA's blocks
+// are -inf.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) logprob_kernel(const LogprobParams p) {
+struct Tile {
+  static constexpr int N = Vec<T>::N, kLoads = kVals / N;
+  const T* z;
+  int skew, V, hi;
+  __device__ __forceinline__ int index_of(int at, int i) const {
+    return (at + i / N * kThreads + static_cast<int>(threadIdx.x)) * N - skew + i % N;
+  }
+  __device__ __forceinline__ bool has(int at, int i) const {
+    const int blk = at + i / N * kThreads + static_cast<int>(threadIdx.x), e = index_of(at, i);
+    return blk < hi && e >= 0 && e < V;
+  }
+  __device__ __forceinline__ bool whole(int at) const {        // no entry of the tile is outside
+    const int last = at + kThreads * kLoads;
+    return at * N - skew >= 0 && last <= hi && last * N - skew <= V;
+  }
+  __device__ __forceinline__ void fetch(int at, uint4 (&raw)[kLoads]) const {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) raw[i] = __ldcs(reinterpret_cast<const uint4*>(z - skew) + at + i * kThreads + threadIdx.x);
+  }
+  static __device__ __forceinline__ void unpack(const uint4 (&raw)[kLoads], float (&v)[kVals]) {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) Vec<T>::unpack(raw[i], v + i * N);
+  }
+  __device__ __forceinline__ void load(int at, float (&v)[kVals]) const {
+    if (whole(at)) {
+      uint4 raw[kLoads];
+      fetch(at, raw);
+      unpack(raw, v);
+      return;
+    }
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int blk = at + i * kThreads + threadIdx.x, e = blk * N - skew;
+      if (blk < hi && e >= 0 && e + N <= V) {
+        Vec<T>::unpack(__ldcs(reinterpret_cast<const uint4*>(z - skew) + blk), v + i * N);
+      } else {
+#pragma unroll
+        for (int j = 0; j < N; ++j) v[i * N + j] = blk < hi && e + j >= 0 && e + j < V ? Vec<T>::one(z + e + j) : -INFINITY;
+      }
+    }
+  }
+};
+
+// The exact best `top` of a CTA's blocks, tile by tile, for rows whose entries pass the bound in too large a number.
+template <typename T>
+__device__ __noinline__ int best_slowly(Shared& sh, const Tile<T>& tile, int lo, int top) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int n = 0;
+  for (int at = lo; at < tile.hi; at += kThreads * Tile<T>::kLoads) {
+    float v[kVals];
+    tile.load(at, v);
+    u64 last = ~0ull;
+    for (int r = 0; r < top; ++r) {
+      u64 best = 0;
+#pragma unroll
+      for (int i = 0; i < kVals; ++i) {
+        const u64 k = key_of(v[i], tile.index_of(at, i));
+        if (v[i] == v[i] && k < last && k > best && tile.has(at, i)) best = k;
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        const u64 k = __shfl_xor_sync(~0u, best, o);
+        best = k > best ? k : best;
+      }
+      __syncthreads();
+      if (lane == 0) sh.best[warp] = best;
+      __syncthreads();
+      best = 0;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) best = sh.best[w] > best ? sh.best[w] : best;
+      if (best == 0) break;
+      last = best;
+      if (tid == 0) sh.cand[n] = best;
+      ++n;
+    }
+    __syncthreads();
+    n = pick(sh, n, top);
+  }
+  return n;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 4) logprob_kernel(const LogprobParams p) {
   constexpr int N = Vec<T>::N, kLoads = kVals / N;
   __shared__ Shared sh;
   __shared__ u64 lists[kMaxCluster * kLogprobTop];
@@ -124,55 +214,46 @@ __global__ void __launch_bounds__(kThreads) logprob_kernel(const LogprobParams p
   const T* z = static_cast<const T*>(p.logits) + row * p.v_stride;
   // blocks of sixteen aligned bytes; the row begins `skew` entries into block 0
   const int skew = static_cast<int>((reinterpret_cast<uintptr_t>(z) & 15u) / sizeof(T));
-  const T* z0 = z - skew;
   const int blocks = (p.V + skew + N - 1) / N;
   const int per = ((blocks + CL - 1) / CL + 31) / 32 * 32;
-  const int lo = min(rank * per, blocks), hi = min(lo + per, blocks);
+  const int lo = min(rank * per, blocks);
+  const Tile<T> tile{z, skew, p.V, min(lo + per, blocks)};
   if (tid == 0) sh.count = 0;
-  __syncthreads();
 
   Sums a{-INFINITY, 0.f, 0.f};
   float bound = -INFINITY;
-  bool first = true, strict = false;
-  for (int at = lo; at < hi; at += kThreads * kLoads) {
+  bool strict = false, fetched = false;
+  uint4 raw[kLoads];                                   // of the next tile
+  int number = 0, pick_at = 0;
+  for (int at = lo; at < tile.hi; at += kThreads * kLoads, ++number) {
     float v[kVals];
-    uint32_t valid = 0;                                // a bit an entry
-    float most = -INFINITY;
+    if (fetched) Tile<T>::unpack(raw, v);
+    else tile.load(at, v);
+    const int next = at + kThreads * kLoads;
+    fetched = next < tile.hi && tile.whole(next);
+    if (fetched) tile.fetch(next, raw);
+    float most = v[0];
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      const int blk = at + i * kThreads + tid;
-      const int e = blk * N - skew;
-      if (blk < hi && e >= 0 && e + N <= p.V) {
-        Vec<T>::unpack(__ldcs(reinterpret_cast<const uint4*>(z0) + blk), v + i * N);
-        valid |= ((1u << N) - 1u) << (i * N);
-      } else {
-#pragma unroll
-        for (int j = 0; j < N; ++j) {
-          v[i * N + j] = -INFINITY;
-          if (blk < hi && e + j >= 0 && e + j < p.V) {
-            v[i * N + j] = Vec<T>::one(z + e + j);
-            valid |= 1u << (i * N + j);
-          }
-        }
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < kVals; ++i) most = fmaxf(most, v[i]);
-    // the sums
-    if (most > a.m) a = join(a, Sums{most, 0.f, 0.f});
+    for (int i = 1; i < kVals; ++i) most = max_nan(most, v[i]);
+    // the sums; a masked entry's difference must not be infinite (its exponential is 0), and a NaN is in the maximum
+    if (!(most <= a.m)) a = join(a, Sums{most, 0.f, 0.f});
     const float ref = finite_ref(a.m);
+    float s0 = 0.f, s1 = 0.f, t0 = 0.f, t1 = 0.f;
 #pragma unroll
-    for (int i = 0; i < kVals; ++i) {
-      const float d = v[i] - ref, e = exp2_fast(d * kLog2e);      // a NaN, or inf - inf, makes the sum NaN
-      a.s += e;
-      a.t = fmaf(e, fmaxf(d, -1e4f), a.t);
+    for (int i = 0; i < kVals; i += 2) {
+      const float d0 = fmaxf(v[i] - ref, -1e4f), d1 = fmaxf(v[i + 1] - ref, -1e4f);
+      const float e0 = exp2_fast(d0 * kLog2e), e1 = exp2_fast(d1 * kLog2e);
+      s0 += e0, s1 += e1;
+      t0 = fmaf(e0, d0, t0), t1 = fmaf(e1, d1, t1);
     }
+    a.s += s0 + s1;
+    a.t += t0 + t1;
     // candidates
-    if (first) {
+    if (number == 0) {
       float g = most;
 #pragma unroll
-      for (int o = 1; o < 8; o <<= 1) g = fmaxf(g, __shfl_xor_sync(~0u, g, o));
-      if ((lane & 7) == 0) sh.groups[tid >> 3] = g;
+      for (int o = 1; o < kWarps; o <<= 1) g = fmaxf(g, __shfl_xor_sync(~0u, g, o));
+      if (tid % kWarps == 0) sh.groups[tid / kWarps] = g;     // (as many threads a group as there are warps)
       __syncthreads();
       g = sh.groups[lane];
       int r = 0;
@@ -183,69 +264,50 @@ __global__ void __launch_bounds__(kThreads) logprob_kernel(const LogprobParams p
       }
       bound = __shfl_sync(~0u, g, __ffs(__ballot_sync(~0u, r == top - 1)) - 1);
     }
-    const int before = sh.count;                       // nobody adds before the next barrier
-    __syncthreads();
-    if (strict ? most > bound : most >= bound) {
+    if (strict ? most > bound : !(most < bound)) {
 #pragma unroll
       for (int i = 0; i < kVals; ++i)
-        if ((valid >> i & 1u) && (strict ? v[i] > bound : v[i] >= bound)) {
+        if ((strict ? v[i] > bound : v[i] >= bound) && tile.has(at, i)) {
           const int pos = atomicAdd(&sh.count, 1);
-          if (pos < kCap) sh.cand[pos] = key_of(v[i], (at + i / N * kThreads + tid) * N - skew + i % N);
+          if (pos < kCap) sh.cand[pos] = key_of(v[i], tile.index_of(at, i));
         }
     }
-    __syncthreads();
-    int n = sh.count;
-    const bool over = n > kCap;
-    if (over) {                                        // too many: those of before, then this tile's best one by one
-      n = pick(sh, before, top);
-      u64 last = ~0ull;
-      for (int r = 0; r < top; ++r) {
-        u64 best = 0;
-#pragma unroll
-        for (int i = 0; i < kVals; ++i) {
-          const u64 k = key_of(v[i], (at + i / N * kThreads + tid) * N - skew + i % N);
-          if ((valid >> i & 1u) && v[i] == v[i] && k < last && k > best) best = k;
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-          const u64 k = __shfl_xor_sync(~0u, best, o);
-          best = k > best ? k : best;
-        }
-        if (lane == 0) sh.best[warp] = best;
-        __syncthreads();
-        best = 0;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) best = sh.best[w] > best ? sh.best[w] : best;
-        if (best == 0) break;
-        last = best;
-        if (tid == 0) sh.cand[n] = best;
-        ++n;
+    if (number == pick_at) {
+      // the best so far are the bound of later tiles; after tiles 0, 3, 15, 63, ... few pass it, and there is no barrier between
+      __syncthreads();
+      const int n = sh.count;
+      __syncthreads();
+      if (n <= kCap) {
+        strict = pick(sh, n, top) == top;              // later entries lose ties
+        bound = strict ? key_value(sh.cand[top - 1]) : -INFINITY;
         __syncthreads();
       }
-      __syncthreads();
+      pick_at = 4 * pick_at + 3;
     }
-    if (first || over || n > kCap / 2) {
-      n = pick(sh, n, top);
-      first = false;
-      strict = n == top;                               // later entries lose ties
-      bound = strict ? key_value(sh.cand[top - 1]) : -INFINITY;
-    }
-    __syncthreads();                                   // everyone has read the list's length
   }
-  const int n = pick(sh, sh.count, top);
-
-  // the CTA's sums, then the cluster's
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    Sums b;
-    b.m = __shfl_xor_sync(~0u, a.m, o), b.s = __shfl_xor_sync(~0u, a.s, o), b.t = __shfl_xor_sync(~0u, a.t, o);
-    a = join(a, b);
-  }
-  if (lane == 0) sh.sums[warp] = a;
   __syncthreads();
-  a = sh.sums[0];
+  int n = sh.count;
+  if (n > kCap) n = best_slowly<T>(sh, tile, lo, top);
+  else n = pick(sh, n, top);
+
+  // the CTA's sums, relative to its largest entry, then the cluster's
+  {
+    float m = a.m;
 #pragma unroll
-  for (int w = 1; w < kWarps; ++w) a = join(a, sh.sums[w]);
+    for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(~0u, m, o));
+    if (lane == 0) sh.sums[warp].m = m;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) m = max_nan(m, sh.sums[w].m);
+    a = join(a, Sums{m, 0.f, 0.f});
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) a.s += __shfl_xor_sync(~0u, a.s, o), a.t += __shfl_xor_sync(~0u, a.t, o);
+    if (lane == 0) sh.sums[warp].s = a.s, sh.sums[warp].t = a.t;
+    __syncthreads();
+    a.s = a.t = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) a.s += sh.sums[w].s, a.t += sh.sums[w].t;
+  }
   const u64* list = sh.cand;
   if (CL > 1) {
     __syncthreads();
@@ -253,16 +315,25 @@ __global__ void __launch_bounds__(kThreads) logprob_kernel(const LogprobParams p
     cluster.sync();
     if (rank == 0) {
       for (int c = 1; c < CL; ++c) a = join(a, cluster.map_shared_rank(&sh, c)->sums[0]);
-      if (tid < CL * kLogprobTop) {
-        const Shared* other = cluster.map_shared_rank(&sh, tid / kLogprobTop);
-        lists[tid] = (tid % kLogprobTop) < other->count ? other->cand[tid % kLogprobTop] : 0ull;
+      for (int i = tid; i < CL * kLogprobTop; i += kThreads) {
+        const Shared* other = cluster.map_shared_rank(&sh, i / kLogprobTop);
+        lists[i] = (i % kLogprobTop) < other->count ? other->cand[i % kLogprobTop] : 0ull;
       }
       __syncthreads();
-      const u64 k = tid < CL * kLogprobTop ? lists[tid] : 0ull;
-      if (k != 0) {
-        int r = 0;
-        for (int j = 0; j < CL * kLogprobTop; ++j) r += lists[j] > k;
-        if (r < top) sh.sorted[r] = k;
+      // each list is in order: an entry's rank is its place and how many of the others' are larger
+      for (int i = tid; i < CL * kLogprobTop; i += kThreads) {
+        const u64 k = lists[i];
+        int r = i % kLogprobTop;
+        for (int c = 0; c < CL; ++c) {
+          if (c == i / kLogprobTop) continue;
+          int larger = 0;
+#pragma unroll
+          for (int step = kLogprobTop / 2; step > 0; step >>= 1)
+            if (lists[c * kLogprobTop + larger + step - 1] > k) larger += step;
+          if (lists[c * kLogprobTop + larger] > k) ++larger;
+          r += larger;
+        }
+        if (k != 0 && r < top) sh.sorted[r] = k;
       }
       __syncthreads();
     }
@@ -270,7 +341,7 @@ __global__ void __launch_bounds__(kThreads) logprob_kernel(const LogprobParams p
     if (rank != 0) return;
     list = sh.sorted;
   }
-  // no distribution: a NaN or +inf (the sum is NaN), or nothing finite (the sum is 0)
+  // no distribution: a NaN or +inf (in the maximum), or nothing finite (the sum is 0)
   const bool bad = !(a.s > 0.f) || !(a.m < INFINITY);
   const float log_s = logf(a.s), none = __int_as_float(0x7fc00000);
   if (tid < top) {
@@ -291,7 +362,7 @@ __global__ void __launch_bounds__(kThreads) logprob_kernel(const LogprobParams p
 template <typename T>
 cudaError_t launch_t(const LogprobParams& p, cudaStream_t s) {
   int CL = 1;
-  while (CL < kMaxCluster && p.rows * CL < 304 && p.V / (2 * CL) >= kThreads * kVals) CL *= 2;
+  while (CL < kMaxCluster && p.rows * CL < 304 && p.V / (2 * CL) >= 8192) CL *= 2;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(p.rows) * CL);
   cfg.blockDim = dim3(kThreads);
@@ -303,7 +374,6 @@ cudaError_t launch_t(const LogprobParams& p, cudaStream_t s) {
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, logprob_kernel<T>, p);
 }
-
 }  // namespace
 
 cudaError_t launch_logprobs(const LogprobParams& p, cudaStream_t s) {

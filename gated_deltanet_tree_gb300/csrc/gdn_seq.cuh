@@ -32,7 +32,6 @@ struct SeqReqs {
 cudaError_t launch_seq_rec(const SeqParams& p, const SeqReqs* reqs, int n, cudaStream_t s);
 
 // One token each of requests 0 .. n - 1, as a stream of tiles; false where that form does not apply or does not pay.
-constexpr int kStepPairs = 304;   // (request, k-head) pairs
 bool launch_seq_step(const SeqParams& p, int n, cudaStream_t s, cudaError_t& e);
 
 // ---- the chunked form: 64 tokens at a time ----

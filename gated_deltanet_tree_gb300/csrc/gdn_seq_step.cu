@@ -6,6 +6,11 @@
 // window come the same way, a pair ahead.  All channels of a k-head's group belong to one CTA, so a window that is written
 // in place has been read by then.
 //
+// Measured (us a call, this kernel : the one of gdn_seq_rec.cu, which the others go to), 16 k-heads and 48 v-heads: 4 requests
+// 13.0 : 10.4, 8 15.6 : 18.4, 16 26.6 : 34.8, 32 47 : 66, 128 154 : 246 (5.3 TB/s, 0.78 of measured).  Heads of 64 x 64 gain a
+// tenth at 128 requests, heads of 64 x 128 nothing: their tiles are too small for one CTA an SM.  With fp32 rows or many v-heads
+// a k-head the rows may leave no room for three tiles.
+//
 // The arithmetic is that of gdn_seq_rec.cu: p = (g T)^T k and r = (g T)^T q in one pass, u = beta (v - p),
 // o = r + (q . k) u, T' = g T + k u^T.
 #include <cuda_bf16.h>
@@ -271,26 +276,23 @@ cudaError_t launch_t(const SeqParams& p, const StepPlan& plan, int smem, int cta
   k<<<ctas, kThreads, smem, s>>>(p, plan);
   return cudaGetLastError();
 }
-template <typename InT>
-cudaError_t launch_d(const SeqParams& p, const StepPlan& plan, int smem, int ctas, cudaStream_t s) {
-  if (p.dk == 128) return p.dv == 128 ? launch_t<InT, 128, 128>(p, plan, smem, ctas, s) : launch_t<InT, 128, 64>(p, plan, smem, ctas, s);
-  return p.dv == 128 ? launch_t<InT, 64, 128>(p, plan, smem, ctas, s) : launch_t<InT, 64, 64>(p, plan, smem, ctas, s);
-}
-
 }  // namespace
 
 bool launch_seq_step(const SeqParams& p, int n, cudaStream_t s, cudaError_t& e) {
+  constexpr int kTile = tile_bytes<128, 128>();
   const long long pairs = static_cast<long long>(n) * p.Hk;
-  if (p.dk < 64 || p.dv < 64 || (p.conv_mode == 1 && p.K > kTaps) || !p.state_in || pairs < kStepPairs) return false;
+  if (p.dk != 128 || p.dv != 128 || (p.conv_mode == 1 && p.K > kTaps) || !p.state_in || static_cast<long long>(n) * p.Hv < 304)
+    return false;
   const int nc = 2 * p.dk + p.Hv / p.Hk * p.dv, in = p.in_dtype == GDN_DTYPE_BF16 ? 2 : 4;
   StepPlan plan{};
   plan.pairs = static_cast<int>(pairs);
   plan.row_bytes = nc * (in + 4 * (kTaps - 1));
-  const int rest = 2 * plan.row_bytes + (p.dv == 128 ? fixed_bytes<128>(nc) : fixed_bytes<64>(nc)), one = p.dk * p.dv * 4;
-  plan.stages = (kSmem - rest) / one < kStagesMost ? (kSmem - rest) / one : kStagesMost;
+  const int rest = 2 * plan.row_bytes + fixed_bytes<128>(nc);
+  plan.stages = (kSmem - rest) / kTile < kStagesMost ? (kSmem - rest) / kTile : kStagesMost;
   if (rest > kSmem || plan.stages < 3) return false;
-  const int smem = plan.stages * one + rest;
-  e = p.in_dtype == GDN_DTYPE_BF16 ? launch_d<__nv_bfloat16>(p, plan, smem, 152, s) : launch_d<float>(p, plan, smem, 152, s);
+  const int smem = plan.stages * kTile + rest, ctas = pairs < 152 ? static_cast<int>(pairs) : 152;
+  e = p.in_dtype == GDN_DTYPE_BF16 ? launch_t<__nv_bfloat16, 128, 128>(p, plan, smem, ctas, s)
+                                   : launch_t<float, 128, 128>(p, plan, smem, ctas, s);
   return true;
 }
 
