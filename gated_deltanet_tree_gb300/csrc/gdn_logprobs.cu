@@ -10,8 +10,15 @@
 // later tiles; it is renewed after ever more of them, and the warps need no barrier in between.  Where more entries pass than the list holds
 // (long ties, rising rows) the best are found tile by tile, one after another, in a second pass.
 //
-// A cluster of up to eight CTAs shares a row where rows are few, joined through distributed
-// shared memory.  The bound is the row's bytes, read once.
+// A cluster of up to eight CTAs shares a row where rows are few; each puts its sums and its list into
+// the first one's shared memory.
+//
+// The bytes, read once, are the floor; instruction issue is nearer (some nine instructions an entry, a
+// MUFU exponential among them) and, where a row has few tiles, the latencies of its start and end.
+// Measured (us): 10 rows of 131072 bf16 7.8, 320 of them 33 (floor 12), 1500 rows of 65537 fp32 with
+// 20 best 92 (floor 58).  Two CTAs a row where there are 320 took 37; a warp's entries that pass, taken
+// in unrolled code, cost the ten rows 1.4 us more, because code that runs once is fetched slowly.
+// Four CTAs an SM for bf16 (64 registers), three for fp32: 92 against 106 us with spills.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
@@ -29,6 +36,38 @@ constexpr int kCap = 1024;                   // candidates
 constexpr int kMaxCluster = 8;
 constexpr float kLog2e = 1.4426950408889634f;
 
+__device__ __forceinline__ float max_nan(float a, float b) {   // a NaN stays
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+// packed pairs of fp32
+__device__ __forceinline__ u64 pack2(float lo, float hi) {
+  u64 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(u64 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ u64 add2(u64 a, u64 b) {
+  u64 d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ u64 mul2(u64 a, u64 b) {
+  u64 d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ u64 fma2(u64 a, u64 b, u64 c) {
+  u64 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+
 template <typename T>
 struct Vec;
 template <>
@@ -38,6 +77,10 @@ struct Vec<float> {
     x[0] = __uint_as_float(v.x), x[1] = __uint_as_float(v.y), x[2] = __uint_as_float(v.z), x[3] = __uint_as_float(v.w);
   }
   static __device__ __forceinline__ float one(const float* p) { return *p; }
+  // the largest of the sixteen bytes' entries, a NaN if one is
+  static __device__ __forceinline__ float most(uint4 v) {
+    return max_nan(max_nan(__uint_as_float(v.x), __uint_as_float(v.y)), max_nan(__uint_as_float(v.z), __uint_as_float(v.w)));
+  }
 };
 template <>
 struct Vec<__nv_bfloat16> {
@@ -51,18 +94,26 @@ struct Vec<__nv_bfloat16> {
     }
   }
   static __device__ __forceinline__ float one(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+  static __device__ __forceinline__ float most(uint4 v) {        // (two entries an instruction)
+    auto pair = [](uint32_t w) { return *reinterpret_cast<__nv_bfloat162*>(&w); };
+    const __nv_bfloat162 m = __hmax2_nan(__hmax2_nan(pair(v.x), pair(v.y)), __hmax2_nan(pair(v.z), pair(v.w)));
+    return max_nan(__low2float(m), __high2float(m));
+  }
 };
 
-// Order-preserving key of (value, lowest index wins); never 0 for a value that is not NaN.
-__device__ __forceinline__ u64 key_of(float v, int idx) {
+// A value's bits in an order that integers have; not 0 for a value that is not NaN.
+__device__ __forceinline__ uint32_t ordered(float v) {
   const uint32_t u = __float_as_uint(v + 0.f);     // -0 counts as +0
-  const uint32_t o = (u & 0x80000000u) ? ~u : (u | 0x80000000u);
-  return (static_cast<u64>(o) << 32) | (0xFFFFFFFFu - static_cast<uint32_t>(idx));
+  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
-__device__ __forceinline__ float key_value(u64 k) {
-  const uint32_t o = static_cast<uint32_t>(k >> 32);
+__device__ __forceinline__ float unordered(uint32_t o) {
   return __uint_as_float((o & 0x80000000u) ? (o & 0x7FFFFFFFu) : ~o);
 }
+// Order-preserving key of (value, lowest index wins).
+__device__ __forceinline__ u64 key_of(float v, int idx) {
+  return (static_cast<u64>(ordered(v)) << 32) | (0xFFFFFFFFu - static_cast<uint32_t>(idx));
+}
+__device__ __forceinline__ float key_value(u64 k) { return unordered(static_cast<uint32_t>(k >> 32)); }
 __device__ __forceinline__ int key_index(u64 k) { return static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(k)); }
 
 __device__ __forceinline__ float exp2_fast(float x) {   // results below 2^-126 are zero
@@ -71,11 +122,6 @@ __device__ __forceinline__ float exp2_fast(float x) {   // results below 2^-126 
   return y;
 }
 
-__device__ __forceinline__ float max_nan(float a, float b) {   // a NaN stays
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
 struct Sums {
   float m, s, t;
 };
@@ -107,6 +153,7 @@ __device__ __forceinline__ int pick(Shared& sh, int n, int top) {
   for (int i = tid; i < n; i += kThreads) {
     const u64 k = sh.cand[i];
     int r = 0;
+#pragma unroll 4
     for (int j = 0; j < n; ++j) r += sh.cand[j] > k;
     if (r < top) sh.sorted[r] = k;
   }
@@ -203,10 +250,11 @@ __device__ __noinline__ int best_slowly(Shared& sh, const Tile<T>& tile, int lo,
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 4) logprob_kernel(const LogprobParams p) {
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : 4) logprob_kernel(const LogprobParams p) {
   constexpr int N = Vec<T>::N, kLoads = kVals / N;
   __shared__ Shared sh;
   __shared__ u64 lists[kMaxCluster * kLogprobTop];
+  __shared__ Sums parts[kMaxCluster];
   cg::cluster_group cluster = cg::this_cluster();
   const int CL = cluster.num_blocks(), rank = cluster.block_rank();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -226,28 +274,37 @@ __global__ void __launch_bounds__(kThreads, 4) logprob_kernel(const LogprobParam
   uint4 raw[kLoads];                                   // of the next tile
   int number = 0, pick_at = 0;
   for (int at = lo; at < tile.hi; at += kThreads * kLoads, ++number) {
-    float v[kVals];
-    if (fetched) Tile<T>::unpack(raw, v);
-    else tile.load(at, v);
+    float v[kVals], most;
+    if (fetched) {
+      most = Vec<T>::most(raw[0]);
+#pragma unroll
+      for (int i = 1; i < kLoads; ++i) most = max_nan(most, Vec<T>::most(raw[i]));
+      Tile<T>::unpack(raw, v);
+    } else {
+      tile.load(at, v);
+      most = v[0];
+#pragma unroll
+      for (int i = 1; i < kVals; ++i) most = max_nan(most, v[i]);
+    }
     const int next = at + kThreads * kLoads;
     fetched = next < tile.hi && tile.whole(next);
     if (fetched) tile.fetch(next, raw);
-    float most = v[0];
-#pragma unroll
-    for (int i = 1; i < kVals; ++i) most = max_nan(most, v[i]);
     // the sums; a masked entry's difference must not be infinite (its exponential is 0), and a NaN is in the maximum
     if (!(most <= a.m)) a = join(a, Sums{most, 0.f, 0.f});
     const float ref = finite_ref(a.m);
-    float s0 = 0.f, s1 = 0.f, t0 = 0.f, t1 = 0.f;
+    u64 s2 = 0ull, t2 = 0ull;
 #pragma unroll
     for (int i = 0; i < kVals; i += 2) {
-      const float d0 = fmaxf(v[i] - ref, -1e4f), d1 = fmaxf(v[i + 1] - ref, -1e4f);
-      const float e0 = exp2_fast(d0 * kLog2e), e1 = exp2_fast(d1 * kLog2e);
-      s0 += e0, s1 += e1;
-      t0 = fmaf(e0, d0, t0), t1 = fmaf(e1, d1, t1);
+      const float2 f = unpack2(add2(pack2(v[i], v[i + 1]), pack2(-ref, -ref)));
+      const u64 d = pack2(fmaxf(f.x, -1e4f), fmaxf(f.y, -1e4f));
+      const float2 x = unpack2(mul2(d, pack2(kLog2e, kLog2e)));
+      const u64 e = pack2(exp2_fast(x.x), exp2_fast(x.y));
+      s2 = add2(s2, e);
+      t2 = fma2(e, d, t2);
     }
-    a.s += s0 + s1;
-    a.t += t0 + t1;
+    const float2 s = unpack2(s2), ts = unpack2(t2);
+    a.s += s.x + s.y;
+    a.t += ts.x + ts.y;
     // candidates
     if (number == 0) {
       float g = most;
@@ -255,22 +312,31 @@ __global__ void __launch_bounds__(kThreads, 4) logprob_kernel(const LogprobParam
       for (int o = 1; o < kWarps; o <<= 1) g = fmaxf(g, __shfl_xor_sync(~0u, g, o));
       if (tid % kWarps == 0) sh.groups[tid / kWarps] = g;     // (as many threads a group as there are warps)
       __syncthreads();
-      g = sh.groups[lane];
-      int r = 0;
-#pragma unroll
-      for (int j = 0; j < 32; ++j) {
-        const float o = __shfl_sync(~0u, g, j);
-        r += o > g || (o == g && j < lane);
+      // the top-th largest of the 32: one after another is taken out
+      uint32_t left = ordered(sh.groups[lane]), m = 0;
+      for (int r = 0; r < top; ++r) {
+        m = __reduce_max_sync(~0u, left);
+        if (lane == __ffs(__ballot_sync(~0u, left == m)) - 1) left = 0;
       }
-      bound = __shfl_sync(~0u, g, __ffs(__ballot_sync(~0u, r == top - 1)) - 1);
+      bound = unordered(m);
     }
-    if (strict ? most > bound : !(most < bound)) {
+    if (strict ? most > bound : most >= bound) {
+      // which entries pass; then one after another, in little code (what runs seldom is fetched slowly)
+      uint32_t in = 0;
 #pragma unroll
-      for (int i = 0; i < kVals; ++i)
-        if ((strict ? v[i] > bound : v[i] >= bound) && tile.has(at, i)) {
+      for (int i = 0; i < kVals; ++i) in |= (strict ? v[i] > bound : v[i] >= bound) ? 1u << i : 0u;
+#pragma unroll 1
+      while (in) {
+        const int i = __ffs(in) - 1;
+        in &= in - 1;
+        float x = v[0];
+#pragma unroll
+        for (int k = 1; k < kVals; ++k) x = k == i ? v[k] : x;
+        if (tile.has(at, i)) {
           const int pos = atomicAdd(&sh.count, 1);
-          if (pos < kCap) sh.cand[pos] = key_of(v[i], tile.index_of(at, i));
+          if (pos < kCap) sh.cand[pos] = key_of(x, tile.index_of(at, i));
         }
+      }
     }
     if (number == pick_at) {
       // the best so far are the bound of later tiles; after tiles 0, 3, 15, 63, ... few pass it, and there is no barrier between
@@ -310,35 +376,25 @@ __global__ void __launch_bounds__(kThreads, 4) logprob_kernel(const LogprobParam
   }
   const u64* list = sh.cand;
   if (CL > 1) {
-    __syncthreads();
-    if (tid == 0) sh.sums[0] = a, sh.count = n;
+    // every CTA puts its list and sums into the first one's memory
+    if (tid < top) cluster.map_shared_rank(lists, 0)[rank * top + tid] = tid < n ? sh.cand[tid] : 0ull;
+    if (tid == 0) cluster.map_shared_rank(parts, 0)[rank] = a;
     cluster.sync();
-    if (rank == 0) {
-      for (int c = 1; c < CL; ++c) a = join(a, cluster.map_shared_rank(&sh, c)->sums[0]);
-      for (int i = tid; i < CL * kLogprobTop; i += kThreads) {
-        const Shared* other = cluster.map_shared_rank(&sh, i / kLogprobTop);
-        lists[i] = (i % kLogprobTop) < other->count ? other->cand[i % kLogprobTop] : 0ull;
-      }
-      __syncthreads();
-      // each list is in order: an entry's rank is its place and how many of the others' are larger
-      for (int i = tid; i < CL * kLogprobTop; i += kThreads) {
-        const u64 k = lists[i];
-        int r = i % kLogprobTop;
-        for (int c = 0; c < CL; ++c) {
-          if (c == i / kLogprobTop) continue;
-          int larger = 0;
+    if (rank != 0) return;
+    a = parts[0];
 #pragma unroll
-          for (int step = kLogprobTop / 2; step > 0; step >>= 1)
-            if (lists[c * kLogprobTop + larger + step - 1] > k) larger += step;
-          if (lists[c * kLogprobTop + larger] > k) ++larger;
-          r += larger;
-        }
+    for (int c = 1; c < kMaxCluster; ++c)
+      if (c < CL) a = join(a, parts[c]);
+    {
+      for (int i = tid; i < CL * top; i += kThreads) {
+        const u64 k = lists[i];
+        int r = 0;
+#pragma unroll 4
+        for (int j = 0; j < CL * top; ++j) r += lists[j] > k;
         if (k != 0 && r < top) sh.sorted[r] = k;
       }
       __syncthreads();
     }
-    cluster.sync();                                    // the others' lists have been read
-    if (rank != 0) return;
     list = sh.sorted;
   }
   // no distribution: a NaN or +inf (in the maximum), or nothing finite (the sum is 0)
@@ -362,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprob_kernel(const LogprobParam
 template <typename T>
 cudaError_t launch_t(const LogprobParams& p, cudaStream_t s) {
   int CL = 1;
-  while (CL < kMaxCluster && p.rows * CL < 304 && p.V / (2 * CL) >= 8192) CL *= 2;
+  while (CL < kMaxCluster && p.rows * CL < 304 && p.V / (2 * CL) >= 16384) CL *= 2;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(p.rows) * CL);
   cfg.blockDim = dim3(kThreads);
