@@ -1,6 +1,7 @@
 // Which kernels take a batch of prompts, and in which order.
 //
-// Prompts of more than kTokenByToken rows go through the chunked form, 64 tokens at a time.  Up to kSegReqs requests are in
+// Prompts of more than kTokenByToken rows go through the chunked form, 64 tokens at a time.  (The two take the same time, of
+// one request and of 32, at 13 and 27 rows with 48 heads of 128 x 128, at 24 and 24 with small heads.)  Up to kSegReqs requests are in
 // work together, the longest first; a segment is the next chunks of each, as many as the workspace has places for.  Its
 // operands are prepared, then run through; the next segment finds the states where this one left them.
 // The workspace is large rather than kept in L2: every segment pays three launches, rounds of CTAs that do not fill the GPU
@@ -14,7 +15,7 @@
 namespace gdn {
 namespace {
 
-constexpr int kTokenByToken = 8;
+constexpr int kTokenByToken = 16;
 constexpr size_t kWorkspace = 1000u << 20;
 
 int workspace_slots(const gdn_dims& d) {

@@ -157,6 +157,7 @@ __device__ __forceinline__ float abs_max(float m, u64 x) {
 
 // A bounded wait that leaves the issue slots to the working warps.
 __device__ __forceinline__ bool mbar_wait_quiet(uint64_t* bar, uint32_t parity) {
+  if (mbar_ready(bar, parity)) return true;
   const long long t0 = clock64();
   while (!mbar_ready(bar, parity))
     if (clock64() - t0 > kWaitCycles) return false;
@@ -280,6 +281,12 @@ __device__ __forceinline__ void conv_tokens(const SeqParams& p, const InT* x, co
       if (t0 + t >= len) y[t] = make_float4(0.f, 0.f, 0.f, 0.f);
   }
 }
+
+// Programmatic dependent launches: a kernel may start while the last CTAs of the one before finish, and waits for it (and all
+// it waited for) where it reads that one's results.
+__device__ __forceinline__ void start_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+// (Those are read by loads that the wait orders: not __ldg, which may be moved before it.)
+__device__ __forceinline__ void wait_for_primary() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // ---- what does not depend on the state ------------------------------------------------------------------------------
 
@@ -462,6 +469,7 @@ seq_keys_kernel(const SeqParams p, const __grid_constant__ Segment seg, char* ws
   if (tid == 0) mbar_init(bar);
   const bool stop = __syncthreads_or(aborted);
   if (warp == 0) tmem_relinquish();
+  start_dependents();
   const uint32_t tmem = *tmem_at;
   bool late = false;
   if (!stop) {
@@ -520,7 +528,7 @@ seq_keys_kernel(const SeqParams p, const __grid_constant__ Segment seg, char* ws
 
 // v, the gates, M and N of a chunk and v-head.
 template <typename InT, int KT>
-__global__ void __launch_bounds__(kPrepThreads, 3)
+__global__ void __launch_bounds__(kPrepThreads, 4)
 seq_values_kernel(const SeqParams p, const __grid_constant__ Segment seg, char* ws) {
   using P = PrepV;
   extern __shared__ __align__(128) char sm[];
@@ -542,6 +550,7 @@ seq_values_kernel(const SeqParams p, const __grid_constant__ Segment seg, char* 
   if (tid == 0) mbar_init(bar);
   const bool stop = __syncthreads_or(aborted);
   if (warp == 0) tmem_relinquish();
+  start_dependents();
   const uint32_t tmem = *tmem_at;
   bool late = false;
   if (!stop) {
@@ -619,6 +628,7 @@ seq_values_kernel(const SeqParams p, const __grid_constant__ Segment seg, char* 
       }
     }
     __syncthreads();                               // A takes the rows' place
+    wait_for_primary();                            // the Gram matrices
     // A thread has 32 entries of a row of G (warps 0, 1, 4, 5) or H (the others).
     const int trow = (warp & 3) * 32 + lane, tcol = (warp >> 2) * 32, i = trow & 63;
     const bool q_row = trow >= kChunk;
@@ -637,7 +647,7 @@ seq_values_kernel(const SeqParams p, const __grid_constant__ Segment seg, char* 
       for (int half = 0; half < 2; ++half) {
         float4 e[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) e[k] = __ldg(g + (4 * half + k) * kChunk);
+        for (int k = 0; k < 4; ++k) e[k] = __ldcg(g + (4 * half + k) * kChunk);
         float hi[8], lo[8];
         if (tcol + 16 * half > ((warp & 1) * 32 + 31)) {       // all above the diagonal
 #pragma unroll
@@ -772,6 +782,7 @@ seq_values_kernel(const SeqParams p, const __grid_constant__ Segment seg, char* 
       if (tid == 64) meta[2 * kChunk + 2] = inv_n * inv, meta[2 * kChunk + 6] = sum * inv;
     }
   }
+  if (stop) wait_for_primary();
   if (__syncthreads_or(late) && tid == 0) device_error(p.err, GDN_DEVERR_TIMEOUT, at.req.b);
   if (warp == 0) tmem_dealloc(tmem, P::kTmem);
 }
@@ -935,8 +946,12 @@ seq_chain_kernel(const SeqParams p, const __grid_constant__ Segment seg, const c
   };
 
   if (!stop) {
-    if (tid == 0) load_meta(0);
-    if (warp == 0) load_chunk(0);
+    if (warp == 0) {
+      wait_for_primary();
+      if (lane == 0) load_meta(0);
+      __syncwarp();
+      load_chunk(0);
+    }
     constexpr int CP = L::kCols, kPairs = CP / 2;
     const int row = (warp & 3) * 32 + lane, c0 = (warp >> 2) * CP;            // lane of tensor memory, columns of the slice
     const int g = c0 / L::kN, cg = c0 % L::kN;                                // group, columns in it
@@ -1089,7 +1104,7 @@ seq_chain_kernel(const SeqParams p, const __grid_constant__ Segment seg, const c
       const float4* V = reinterpret_cast<const float4*>(v_ws + i * slot_bytes + 4 * 128 * kChunk) + (col0 + c0) / 4 * kChunk + (row & 63);
 #pragma unroll
       for (int j = 0; j < kPairs; j += 2) {
-        const float4 f = __ldg(V + j / 2 * kChunk);
+        const float4 f = __ldcg(V + j / 2 * kChunk);
         a[j] = pack2(f.x, f.y), a[j + 1] = pack2(f.z, f.w);
       }
     };
@@ -1129,6 +1144,7 @@ seq_chain_kernel(const SeqParams p, const __grid_constant__ Segment seg, const c
       }
       __syncwarp();
     };
+    wait_for_primary();
     if ((row >> 6) == (req.c0 & 1)) load_v(0, a);
     // the first T's scale: its largest entry
     int d1_done = 0;                               // D1's so far: one a chunk, and those taken again
@@ -1163,11 +1179,8 @@ seq_chain_kernel(const SeqParams p, const __grid_constant__ Segment seg, const c
         tmem_fence_after();
       }
       const float w_bound = (vmax + fmax_ * (DK == 128 ? 11.32f : DK == 64 ? 8.001f : 5.657f) * smax) * 1.001f;
-      u_bound = mbound * w_bound * 1.001f;
-      o_bound = nbound * w_bound * fabsf(p.q_scale);
-      s_bound = (whole * smax + 64.f * u_bound) * 1.001f;
       float inv_w, inv_u;
-      const float sc_w = scale_for(w_bound, inv_w), sc_u = scale_for(u_bound, inv_u);
+      const float sc_w = scale_for(w_bound, inv_w);
       const float f1 = first * (inv_s * (1.f / kUnit));
       char* const w_at = w_op + t * 16;
       if (k_row) {
@@ -1194,6 +1207,10 @@ seq_chain_kernel(const SeqParams p, const __grid_constant__ Segment seg, const c
         tmem_fence_before();                                   // D3 takes D1's place
       }
       if (last_of(kWDone + g, L::kTurnWarps)) issue_d2(i);
+      u_bound = mbound * w_bound * 1.001f;
+      o_bound = nbound * w_bound * fabsf(p.q_scale);
+      s_bound = (whole * smax + 64.f * u_bound) * 1.001f;
+      const float sc_u = scale_for(u_bound, inv_u);
       // (the other group has read the gates of the chunk before: it took part in D2 there, without which nobody is here)
       if (!k_row && copies && i + 1 < req.nc && elect_one()) load_meta(i + 1);
       __syncwarp();
@@ -1294,6 +1311,21 @@ template <typename F>
 cudaError_t with_smem(F kernel, int bytes) {
   return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
+// A launch that may start before the one before it has ended.
+template <typename F, typename... A>
+cudaError_t launch_after(F kernel, dim3 grid, int threads, int smem, cudaStream_t s, const A&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
 template <typename InT, int DK, int KT>
 cudaError_t launch_prepare(const SeqParams& p, const Segment& seg, char* ws, cudaStream_t s) {
   auto keys = seq_keys_kernel<InT, DK, KT>;
@@ -1302,16 +1334,15 @@ cudaError_t launch_prepare(const SeqParams& p, const Segment& seg, char* ws, cud
   if (e == cudaSuccess) e = with_smem(values, PrepV::kTotal);
   if (e != cudaSuccess) return e;
   keys<<<dim3(p.Hk, seg.slots), kPrepThreads, PrepK<DK>::kTotal, s>>>(p, seg, ws);
-  values<<<dim3(p.Hv, seg.slots), kPrepThreads, PrepV::kTotal, s>>>(p, seg, ws);
-  return cudaGetLastError();
+  e = cudaGetLastError();
+  return e != cudaSuccess ? e : launch_after(values, dim3(p.Hv, seg.slots), kPrepThreads, PrepV::kTotal, s, p, seg, ws);
 }
 template <int DK, int NB>
 cudaError_t launch_chain(const SeqParams& p, const Segment& seg, const char* ws, cudaStream_t s) {
   auto k = seq_chain_kernel<DK, NB>;
   cudaError_t e = with_smem(k, Chain<DK, NB>::kTotal);
   if (e != cudaSuccess) return e;
-  k<<<dim3(p.Hv * (p.dv / NB), seg.n), Chain<DK, NB>::kThreads, Chain<DK, NB>::kTotal, s>>>(p, seg, ws);
-  return cudaGetLastError();
+  return launch_after(k, dim3(p.Hv * (p.dv / NB), seg.n), Chain<DK, NB>::kThreads, Chain<DK, NB>::kTotal, s, p, seg, ws);
 }
 template <int DK>
 cudaError_t launch_d(const SeqParams& p, const Segment& seg, char* ws, cudaStream_t s) {

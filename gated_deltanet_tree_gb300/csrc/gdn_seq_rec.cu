@@ -90,25 +90,32 @@ __global__ void __launch_bounds__(kThreads) seq_rec_kernel(const SeqParams p, co
       for (int c = tid; c < NC; c += kThreads) {
         const int ch = c < DK ? kh * DK + c : c < 2 * DK ? kq + kh * DK + c - DK : 2 * kq + h * p.dv + col0 + c - 2 * DK;
         float xr[TB + KT - 1], w[KT];
+        // the rows, all in flight at once: those outside the request are read at its nearest row, and not used
 #pragma unroll
-        for (int i = 0; i < TB + KT - 1; ++i) {
-          const int t = t0 + i - (KT - 1);             // token of this row; before the first: the window
-          xr[i] = 0.f;
-          if (i >= KT - K && i < nt + KT - 1) {
-            if (t >= 0) xr[i] = load_f(x + t * p.x_row + ch);
-            else if (win) xr[i] = win[static_cast<long long>(K - 1 + t) * p.C + ch];
-          }
-        }
+        for (int i = 0; i < TB + KT - 1; ++i)
+          xr[i] = load_f(x + static_cast<long long>(min(max(t0 + i - (KT - 1), 0), len - 1)) * p.x_row + ch);
 #pragma unroll
         for (int j = 0; j < KT; ++j) {
-          w[j] = 0.f;
-          if (j >= KT - K) w[j] = p.conv_mode == 1 ? __ldg(p.conv_w + static_cast<long long>(ch) * K + j - (KT - K)) : 1.f;
+          w[j] = j == KT - 1 && p.conv_mode != 1 ? 1.f : 0.f;
+          if (p.conv_mode == 1) {
+            const float f = __ldg(p.conv_w + static_cast<long long>(ch) * K + max(j - (KT - K), 0));
+            w[j] = j >= KT - K ? f : 0.f;
+          }
+        }
+        if (t0 == 0) {                                 // rows before the first: the window's, zeros where there is none
+          float old[KT - 1];
+#pragma unroll
+          for (int i = 0; i < KT - 1; ++i)
+            old[i] = win ? win[static_cast<long long>(max(i - (KT - K), 0)) * p.C + ch] : 0.f;
+#pragma unroll
+          for (int i = 0; i < KT - 1; ++i) xr[i] = i >= KT - K ? old[i] : 0.f;
         }
 #pragma unroll
         for (int t = 0; t < TB; ++t) {
           float y = w[KT - 1] * xr[t + KT - 1];
 #pragma unroll
-          for (int i = 1; i < KT; ++i) y = fmaf(w[KT - 1 - i], xr[t + KT - 1 - i], y);
+          for (int i = 1; i < KT; ++i)
+            if (i < K) y = fmaf(w[KT - 1 - i], xr[t + KT - 1 - i], y);
           if (p.act == 1) y = silu(y);
           if (t < nt) ys[t][c] = y;
         }
