@@ -408,7 +408,8 @@ class SequenceRunner:
     A call may go to any stream, or into a CUDA graph (prefill with the lengths it was captured with).  prefill calls
     share the workspace, so they must follow one another; step calls share nothing."""
 
-    def __init__(self, dims: N.gdn_dims, B: int, layers: int = 1, device="cuda", verifier: Optional[TreeVerifier] = None):
+    def __init__(self, dims: N.gdn_dims, B: int, layers: int = 1, device="cuda", verifier: Optional[TreeVerifier] = None,
+                 prompts: bool = True):
         if verifier is not None and (verifier.B, verifier.layers) != (B, layers):
             raise ValueError(f"the verifier's batch and layers are {verifier.B}, {verifier.layers}")
         self.dims, self.B, self.layers = N.gdn_dims.from_buffer_copy(dims), B, layers
@@ -417,7 +418,8 @@ class SequenceRunner:
         self.err = verifier.err if verifier is not None else torch.zeros(4, dtype=torch.int32, device=self.device)
         self._banks = verifier.banks if verifier is not None else None
         self.C = channels(dims)
-        self.workspace = torch.empty(max(256, N.gdn_prefill_workspace_bytes(self.dims)), dtype=torch.uint8,
+        # made once, for any call (a gigabyte or less, whatever the batch); prompts False: single tokens only, and none
+        self.workspace = torch.empty(N.gdn_prefill_workspace_bytes(self.dims) if prompts else 0, dtype=torch.uint8,
                                      device=self.device)
         self._index = self.err.get_device()
         self._type = torch.bfloat16 if dims.in_dtype == N.GDN_DTYPE_BF16 else torch.float32
@@ -477,6 +479,8 @@ class SequenceRunner:
         """lens[b] rows of request b, one request after another: x_raw [rows, C], beta and log_g [rows, Hv] -> out
         [rows, Hv, dv], fp32 or bf16.  The states and windows are updated in place, or written to state_out and conv_out;
         None in their place: the requests start from zeros."""
+        if self.workspace.numel() == 0:
+            raise ValueError("this runner was made for single tokens (prompts=False)")
         lens = np.ascontiguousarray(lens, dtype=np.int32)
         if lens.shape != (self.B,):
             raise ValueError(f"lens holds {lens.shape} lengths for {self.B} requests")
