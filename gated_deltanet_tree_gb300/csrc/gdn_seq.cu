@@ -3,11 +3,14 @@
 // Prompts of more than kTokenByToken rows go through the chunked form, 64 tokens at a time.  (The two take the same time, of
 // one request and of 32, at 13 and 27 rows with 48 heads of 128 x 128, at 24 and 24 with small heads.)  Up to kSegReqs requests are in
 // work together, the longest first; a segment is the next chunks of each, as many as the workspace has places for.  Its
-// operands are prepared, then run through; the next segment finds the states where this one left them.
+// operands are prepared, then run through; the next segment finds the states where this one left them.  Where few requests
+// leave SMs idle, the next segment is prepared beside it: the workspace's halves take turns, and the chains go to a stream
+// of the library's own, which has the higher priority and which the caller's stream waits for at the end.
 // The workspace is large rather than kept in L2: every segment pays three launches, rounds of CTAs that do not fill the GPU
 // and the states' way through memory.  8191 tokens of 48 heads took 858 us with 104 MB, 801 with 300 and 735 with 1000; 32
 // prompts of up to 500 tokens 1447, 1323 and 1237.
 #include <algorithm>
+#include <initializer_list>
 #include <new>
 
 #include "gdn_seq.cuh"
@@ -22,6 +25,77 @@ int workspace_slots(const gdn_dims& d) {
   const size_t n = kWorkspace / seq_slot_bytes(d.Hk, d.Hv, d.dk, d.dv);
   return n < kSegReqs ? kSegReqs : n > 1024 ? 1024 : static_cast<int>(n);
 }
+
+// The segments of a batch of prompts, one after another.
+struct Planner {
+  SegReq* todo;                // the longest first
+  int n;
+  int active[kSegReqs];
+  int n_active = 0, begun = 0;
+  Planner(SegReq* t, int count) : todo(t), n(count) {}
+  // The next chunks of up to kSegReqs requests, at most `slots` in all; false when there are none.
+  bool next(Segment& seg, int slots) {
+    int left = 0;
+    for (int i = 0; i < n_active; ++i)
+      if ((todo[active[i]].c0 + todo[active[i]].nc) * kChunk < todo[active[i]].len) active[left++] = active[i];
+    n_active = left;
+    while (n_active < std::min(kSegReqs, slots) && begun < n) active[n_active++] = begun++;
+    if (n_active == 0) return false;
+    // the longest one's chunks in even parts (the others' follow from its)
+    int most = 0;
+    for (int i = 0; i < n_active; ++i) {
+      const SegReq& r = todo[active[i]];
+      most = std::max(most, (r.len + kChunk - 1) / kChunk - (r.c0 + r.nc));
+    }
+    const int parts = (most + slots / n_active - 1) / (slots / n_active), share = (most + parts - 1) / parts;
+    seg.n = seg.slots = 0;
+    for (int i = 0; i < n_active; ++i) {
+      SegReq& r = todo[active[i]];
+      r.c0 += r.nc;
+      r.nc = std::min(share, (r.len + kChunk - 1) / kChunk - r.c0);
+      r.slot0 = seg.slots;
+      seg.slots += r.nc;
+      seg.r[seg.n++] = r;
+    }
+    return true;
+  }
+};
+
+// A stream and events for the chains that run beside the next segment's preparation, one set a thread and device, made when
+// first needed and kept.  nullptr where there are none: a capturing stream (a stream of ours in somebody's graph would be
+// theirs until the capture ends), or no room for one.
+struct Side {
+  int state = 0;               // 0: not made, 1: there, 2: cannot be made
+  cudaStream_t stream;
+  cudaEvent_t ready[2], go[2], done[2];
+};
+constexpr int kDevices = 64;
+Side* side_stream(cudaStream_t s) {
+  thread_local Side sides[kDevices];
+  cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+  int device = 0;
+  if (cudaStreamIsCapturing(s, &capture) != cudaSuccess || capture != cudaStreamCaptureStatusNone ||
+      cudaGetDevice(&device) != cudaSuccess || device >= kDevices) {
+    cudaGetLastError();
+    return nullptr;
+  }
+  Side& side = sides[device];
+  if (side.state == 0) {
+    int least = 0, greatest = 0;
+    cudaError_t e = cudaDeviceGetStreamPriorityRange(&least, &greatest);
+    if (e == cudaSuccess) e = cudaStreamCreateWithPriority(&side.stream, cudaStreamNonBlocking, greatest);
+    for (int i = 0; i < 2; ++i)
+      for (cudaEvent_t* v : {&side.ready[i], &side.go[i], &side.done[i]})
+        if (e == cudaSuccess) e = cudaEventCreateWithFlags(v, cudaEventDisableTiming);
+    side.state = e == cudaSuccess ? 1 : 2;
+    if (e != cudaSuccess) cudaGetLastError();
+  }
+  return side.state == 1 ? &side : nullptr;
+}
+// Chains of at most kFewCtas CTAs, of at least kAheadLeast chunks, in segments of kAheadChunks chunks a request: 8191 tokens of
+// one request 741 -> 675 us (16 chunks 757, 32 689, 64 677), 20001 and 15001 tokens 3018 -> 2620 us; three requests (288 CTAs)
+// gain nothing.
+constexpr int kFewCtas = 240, kAheadLeast = 48, kAheadChunks = 48;
 
 }  // namespace
 
@@ -52,33 +126,41 @@ cudaError_t launch_prefill(const SeqParams& p, const int32_t* lens, int B, void*
     }
   }
   std::sort(todo, todo + n, [](const SegReq& a, const SegReq& c) { return a.len != c.len ? a.len > c.len : a.b < c.b; });
+  Planner plan{todo, n};
+  const int chunks = n ? (todo[0].len + kChunk - 1) / kChunk : 0;
+  // Few requests leave SMs to the next segment's preparation; several segments are needed for that.
+  Side* side = nullptr;
+  if (n > 0 && n * p.Hv * (p.dv / 64 ? p.dv / 64 : 1) <= kFewCtas && chunks >= kAheadLeast) side = side_stream(s);
+  char* const ws = static_cast<char*>(workspace);
   Segment seg{};
-  int active[kSegReqs], n_active = 0, next = 0;
-  while (e == cudaSuccess && (n_active > 0 || next < n)) {
-    while (n_active < kSegReqs && next < n) active[n_active++] = next++;
-    // the longest one's chunks in even parts (the others' follow from its)
-    int most = 0;
-    for (int i = 0; i < n_active; ++i) {
-      const SegReq& r = todo[active[i]];
-      most = std::max(most, (r.len + kChunk - 1) / kChunk - (r.c0 + r.nc));
+  if (!side) {
+    while (e == cudaSuccess && plan.next(seg, slots)) {
+      e = launch_seq_prepare(p, seg, ws, s);
+      if (e == cudaSuccess) e = launch_seq_chain(p, seg, ws, true, s);
     }
-    const int parts = (most + slots / n_active - 1) / (slots / n_active), share = (most + parts - 1) / parts;
-    seg.n = seg.slots = 0;
-    for (int i = 0; i < n_active; ++i) {
-      SegReq& r = todo[active[i]];
-      r.c0 += r.nc;
-      r.nc = std::min(share, (r.len + kChunk - 1) / kChunk - r.c0);
-      r.slot0 = seg.slots;
-      seg.slots += r.nc;
-      seg.r[seg.n++] = r;
+  } else {
+    const size_t half = slots / 2 * seq_slot_bytes(p.Hk, p.Hv, p.dk, p.dv);
+    const int most = std::min(slots / 2, std::max(n * kAheadChunks, 1));
+    auto step = [&](cudaError_t r) {
+      if (e == cudaSuccess) e = r;
+    };
+    int i = 0;
+    for (; e == cudaSuccess && plan.next(seg, most); ++i) {
+      if (i >= 2) step(cudaStreamWaitEvent(s, side->done[i & 1], 0));            // who used this half before
+      if (i >= 1) step(cudaStreamWaitEvent(s, side->go[(i - 1) & 1], 0));        // the chain before takes its SMs first
+      step(launch_seq_prepare(p, seg, ws + (i & 1) * half, s));
+      step(cudaEventRecord(side->ready[i & 1], s));
+      step(cudaStreamWaitEvent(side->stream, side->ready[i & 1], 0));
+      step(cudaEventRecord(side->go[i & 1], side->stream));
+      step(launch_seq_chain(p, seg, ws + (i & 1) * half, false, side->stream));
+      step(cudaEventRecord(side->done[i & 1], side->stream));
     }
-    e = launch_seq_chunks(p, seg, workspace, s);
-    int left = 0;
-    for (int i = 0; i < n_active; ++i) {
-      const SegReq& r = todo[active[i]];
-      if ((r.c0 + r.nc) * kChunk < r.len) active[left++] = active[i];
+    // whatever has been launched there comes before what follows on the caller's stream
+    if (i > 0) {
+      const cudaError_t r = cudaEventRecord(side->done[0], side->stream);
+      step(r);
+      if (r == cudaSuccess) step(cudaStreamWaitEvent(s, side->done[0], 0));
     }
-    n_active = left;
   }
   delete[] todo;
   return e;

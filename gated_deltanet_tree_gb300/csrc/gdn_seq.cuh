@@ -53,7 +53,9 @@ struct Segment {
   int n, slots;
   SegReq r[kSegReqs];
 };
-cudaError_t launch_seq_chunks(const SeqParams& p, const Segment& seg, void* workspace, cudaStream_t s);
+cudaError_t launch_seq_prepare(const SeqParams& p, const Segment& seg, void* workspace, cudaStream_t s);
+// right_after: the launch before it on the stream is that segment's preparation, whose end it may overlap
+cudaError_t launch_seq_chain(const SeqParams& p, const Segment& seg, const void* workspace, bool right_after, cudaStream_t s);
 
 // A ragged batch of prompts: lens[b] rows of each of B requests, one after another.
 size_t seq_workspace_bytes(const gdn_dims& d);

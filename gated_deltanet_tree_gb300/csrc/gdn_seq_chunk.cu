@@ -960,7 +960,7 @@ seq_chain_kernel(const SeqParams p, const __grid_constant__ Segment seg, const c
     char* const w_op = sm + L::kW + g * L::kWTurn + (cg >> 3) * kChunk * 16;
     float* const most = maxima + g * 2 * L::kTurnWarps;                      // [2][2 groups][T, o][warps]
     const int gw = warp - g * L::kTurnWarps;                                  // warp of the group
-    const bool has_row = row < DK;
+    const bool has_row = DK == 128 || row < DK;
     const bool copies = g == L::kTurns - 1 && (gw & 1) == 0 && gw < 4;        // of these two warps that with q rows issues the copies
     // The warp that arrives last of n issues what the others have made ready: no warp is kept for it (a seventeenth would
     // leave each thread 96 registers), and no other has to be woken.
@@ -1338,33 +1338,43 @@ cudaError_t launch_prepare(const SeqParams& p, const Segment& seg, char* ws, cud
   return e != cudaSuccess ? e : launch_after(values, dim3(p.Hv, seg.slots), kPrepThreads, PrepV::kTotal, s, p, seg, ws);
 }
 template <int DK, int NB>
-cudaError_t launch_chain(const SeqParams& p, const Segment& seg, const char* ws, cudaStream_t s) {
+cudaError_t launch_chain(const SeqParams& p, const Segment& seg, const char* ws, bool right_after, cudaStream_t s) {
   auto k = seq_chain_kernel<DK, NB>;
   cudaError_t e = with_smem(k, Chain<DK, NB>::kTotal);
   if (e != cudaSuccess) return e;
-  return launch_after(k, dim3(p.Hv * (p.dv / NB), seg.n), Chain<DK, NB>::kThreads, Chain<DK, NB>::kTotal, s, p, seg, ws);
+  const dim3 grid(p.Hv * (p.dv / NB), seg.n);
+  if (right_after) return launch_after(k, grid, Chain<DK, NB>::kThreads, Chain<DK, NB>::kTotal, s, p, seg, ws);
+  k<<<grid, Chain<DK, NB>::kThreads, Chain<DK, NB>::kTotal, s>>>(p, seg, ws);
+  return cudaGetLastError();
 }
 template <int DK>
-cudaError_t launch_d(const SeqParams& p, const Segment& seg, char* ws, cudaStream_t s) {
+cudaError_t launch_prepare_d(const SeqParams& p, const Segment& seg, char* ws, cudaStream_t s) {
   using bf16 = __nv_bfloat16;
-  const bool wide = p.K > 4;
-  cudaError_t e = p.in_dtype == GDN_DTYPE_BF16
-                      ? (wide ? launch_prepare<bf16, DK, 8>(p, seg, ws, s) : launch_prepare<bf16, DK, 4>(p, seg, ws, s))
-                      : (wide ? launch_prepare<float, DK, 8>(p, seg, ws, s) : launch_prepare<float, DK, 4>(p, seg, ws, s));
-  if (e != cudaSuccess) return e;
+  if (p.in_dtype == GDN_DTYPE_BF16)
+    return p.K > 4 ? launch_prepare<bf16, DK, 8>(p, seg, ws, s) : launch_prepare<bf16, DK, 4>(p, seg, ws, s);
+  return p.K > 4 ? launch_prepare<float, DK, 8>(p, seg, ws, s) : launch_prepare<float, DK, 4>(p, seg, ws, s);
+}
+template <int DK>
+cudaError_t launch_chain_d(const SeqParams& p, const Segment& seg, const char* ws, bool right_after, cudaStream_t s) {
   // 64 columns a CTA, or 32 where the other half of the GPU would be idle.  (With all 128 of a head a chunk takes more than
   // twice the time: 9.3 against 3.8 us.)
-  if (p.dv >= 64 && seg.n * p.Hv * (p.dv / 64) > 76) return launch_chain<DK, 64>(p, seg, ws, s);
-  return launch_chain<DK, 32>(p, seg, ws, s);
+  if (p.dv >= 64 && seg.n * p.Hv * (p.dv / 64) > 76) return launch_chain<DK, 64>(p, seg, ws, right_after, s);
+  return launch_chain<DK, 32>(p, seg, ws, right_after, s);
 }
 
 }  // namespace
 
-cudaError_t launch_seq_chunks(const SeqParams& p, const Segment& seg, void* workspace, cudaStream_t s) {
+cudaError_t launch_seq_prepare(const SeqParams& p, const Segment& seg, void* workspace, cudaStream_t s) {
   char* ws = static_cast<char*>(workspace);
-  if (p.dk == 128) return launch_d<128>(p, seg, ws, s);
-  if (p.dk == 64) return launch_d<64>(p, seg, ws, s);
-  return launch_d<32>(p, seg, ws, s);
+  if (p.dk == 128) return launch_prepare_d<128>(p, seg, ws, s);
+  if (p.dk == 64) return launch_prepare_d<64>(p, seg, ws, s);
+  return launch_prepare_d<32>(p, seg, ws, s);
+}
+cudaError_t launch_seq_chain(const SeqParams& p, const Segment& seg, const void* workspace, bool right_after, cudaStream_t s) {
+  const char* ws = static_cast<const char*>(workspace);
+  if (p.dk == 128) return launch_chain_d<128>(p, seg, ws, right_after, s);
+  if (p.dk == 64) return launch_chain_d<64>(p, seg, ws, right_after, s);
+  return launch_chain_d<32>(p, seg, ws, right_after, s);
 }
 
 }  // namespace gdn

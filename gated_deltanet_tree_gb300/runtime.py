@@ -481,15 +481,15 @@ class SequenceRunner:
         None in their place: the requests start from zeros."""
         if self.workspace.numel() == 0:
             raise ValueError("this runner was made for single tokens (prompts=False)")
-        lens = np.ascontiguousarray(lens, dtype=np.int32)
-        if lens.shape != (self.B,):
-            raise ValueError(f"lens holds {lens.shape} lengths for {self.B} requests")
-        rows = int(lens.sum(dtype=np.int64))
-        if rows == 0 and (lens == 0).all():
+        if not isinstance(lens, (list, tuple)):
+            lens = np.asarray(lens).tolist()
+        if len(lens) != self.B:
+            raise ValueError(f"lens holds {len(lens)} lengths for {self.B} requests")
+        rows = sum(lens)
+        if rows == 0 and not any(lens):
             return
         args = self._args(rows, x_raw, conv_w, beta, log_g, state, conv_state, out, state_out, conv_out)
-        N._check(N.lib().gdn_prefill(self._ref, self.layers, layer, self.B,
-                                     lens.ctypes.data_as(ctypes.POINTER(ctypes.c_int32)), *args,
+        N._check(N.lib().gdn_prefill(self._ref, self.layers, layer, self.B, (ctypes.c_int32 * self.B)(*lens), *args,
                                      self.workspace.data_ptr(), self.workspace.numel(), N._stream_of(stream, self._index)))
 
     def step(self, x_raw: torch.Tensor, conv_w: Optional[torch.Tensor], beta: torch.Tensor, log_g: torch.Tensor,
@@ -526,16 +526,16 @@ class TokenScorer:
         self.err = torch.zeros(4, dtype=torch.int32, device=self.device)
         self._index = self.top.get_device()
         self._out = (self.top.data_ptr(), self.tokens.data_ptr())
+        self._given, self._rest = self.given.data_ptr(), (self.entropy.data_ptr(), self.err.data_ptr())
         _finish_fills(self.device)
 
     def score(self, logits: torch.Tensor, tokens: Optional[torch.Tensor] = None, stream=None):
         """logits [n, V] -> (top [n, top_k], their tokens [n, top_k], the given tokens' [n] or None, entropy [n]): this
         object's buffers, the first n rows of them."""
-        if logits.dim() != 2 or logits.shape[1] != self.V or not 1 <= logits.shape[0] <= self.rows \
-                or logits.get_device() != self._index:
-            raise ValueError(f"logits is (1 .. {self.rows}, {self.V}) on {self.device}, got {tuple(logits.shape)} on "
-                             f"{logits.device}")
-        n = logits.shape[0]
+        shape = logits.shape
+        if len(shape) != 2 or shape[1] != self.V or not 1 <= shape[0] <= self.rows or logits.get_device() != self._index:
+            raise ValueError(f"logits is (1 .. {self.rows}, {self.V}) on {self.device}, got {tuple(shape)} on {logits.device}")
+        n = shape[0]
         row = self.V
         if not logits.is_contiguous():
             if self.V > 1 and logits.stride(1) != 1:
@@ -550,11 +550,11 @@ class TokenScorer:
                                  f"{tokens.dtype} on {tokens.device}")
             tok = tokens.data_ptr()
         N._check(N.lib().gdn_top_logprobs(n, self.V, row, _dtype_code(logits.dtype, "logits"), logits.data_ptr(), tok,
-                                          self.top_k, *self._out, None if tok is None else self.given.data_ptr(),
-                                          self.entropy.data_ptr(), self.err.data_ptr(),
+                                          self.top_k, *self._out, None if tok is None else self._given, *self._rest,
                                           N._stream_of(stream, self._index)))
-        given = None if tok is None else self.given[:n]
-        return self.top[:n], self.tokens[:n], given, self.entropy[:n]
+        if n == self.rows:                                     # (a view takes as long as a check or two)
+            return self.top, self.tokens, None if tok is None else self.given, self.entropy
+        return self.top[:n], self.tokens[:n], None if tok is None else self.given[:n], self.entropy[:n]
 
     def check_error(self, stream=None):
         N.gdn_check_error_words(self.err, stream)

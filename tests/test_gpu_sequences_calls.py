@@ -144,6 +144,59 @@ def test_two_runners_at_once():
             check(cases[i], cases[i].reference(), cases[i].out, states[i][0][:, 0], states[i][1][:, 0], (order, i))
 
 
+def test_long_prompts_on_two_busy_streams_and_captured():
+    """Prompts long enough to be prepared beside their chains (on a stream of the library's own): two at once on busy streams
+    whose next work overwrites the inputs, again, and captured into a graph, where all of it stays on the one stream.  The
+    four results agree within the tolerance of two calls that round differently, 2e-5 and 1e-5, and with the oracle's last
+    tokens, continued from the state before them."""
+    n, tail = 3400, 60
+    cases = [Case(30 + i, (1, 2, 128, 128), [n, 3300], "bf16", slow=True, layers=1, layer=0) for i in range(2)]
+    runs, streams = [c.runner() for c in cases], [torch.cuda.Stream() for _ in cases]
+    kept = [[t.clone() for t in (c.x, c.beta, c.log_g, c.state, c.conv)] for c in cases]
+    results = []
+    torch.cuda.synchronize()
+    for again in range(2):
+        torch.cuda.synchronize()
+        for c, r, st, k in zip(cases, runs, streams, kept):
+            with torch.cuda.stream(st):
+                torch.cuda._sleep(4_000_000)
+                for a, b in zip((c.x, c.beta, c.log_g, c.state, c.conv), k):
+                    a.copy_(b)
+                r.prefill(c.lens, *c.inputs(), c.state, c.conv, c.out)
+                results.append((c.out.clone(), c.state.clone(), c.conv.clone()))
+                for t in (c.x, c.beta, c.log_g, c.state, c.conv, c.out):
+                    t.fill_(float("nan"))
+    torch.cuda.synchronize()
+    for r in runs:
+        r.check_error()
+    assert all(torch.equal(a, b) for i in range(2) for a, b in zip(results[i], results[2 + i]))
+    c, r = cases[0], runs[0]
+    graph = torch.cuda.CUDAGraph()
+    for a, b in zip((c.x, c.beta, c.log_g, c.state, c.conv), kept[0]):
+        a.copy_(b)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        r.prefill(c.lens, *c.inputs(), c.state, c.conv, c.out)
+    graph.replay()
+    torch.cuda.synchronize()
+    r.check_error()
+    out, state, conv = results[0]
+    assert (c.out - out).abs().max() <= 2e-5 * out.abs().max() and torch.equal(c.conv, conv)
+    assert (c.state - state).norm() <= 1e-5 * state.norm()
+    # the last tokens against the oracle
+    for b, at in enumerate((n, n + 3300)):
+        s, w = kept[0][3][b:b + 1].clone(), kept[0][4][b:b + 1].clone()
+        one = Case(0, (1, 2, 128, 128), [1], "bf16", layers=1, layer=0).runner()
+        first, size = (0, n) if b == 0 else (n, 3300)
+        rows = slice(first, first + size - tail)
+        k = kept[0]
+        one.prefill([size - tail], k[0][rows], c.w, k[1][rows], k[2][rows], s, w, torch.empty_like(c.out[rows]))
+        rows = slice(at - tail, at)
+        o, T, _ = Q.run_sequence(f64(s[0, 0]), f64(w[0, 0]), f64(k[0][rows]), f64(k[1][rows]), f64(k[2][rows]), f64(c.w[0]), c.d)
+        assert np.abs(f64(out[rows]) - o).max() <= 4e-5 * np.abs(o).max()
+        assert np.linalg.norm(f64(state[b, 0]) - T) <= 2e-5 * np.linalg.norm(T)
+
+
 @pytest.mark.parametrize("B", [2, 160])
 def test_captured_calls_replay(B):
     """A graph of a prompt, a token and the tokens' scores follows its buffers; larger calls in between do not change it."""

@@ -123,7 +123,7 @@ class Recorder:
             return getattr(self.real, name)
 
         def call(*args):
-            self.calls.append((name, [list(a[:2]) if isinstance(a, ctypes._Pointer) else a for a in args]))
+            self.calls.append((name, [list(a[:2]) if isinstance(a, (ctypes._Pointer, ctypes.Array)) else a for a in args]))
             return 0
         return call
 
