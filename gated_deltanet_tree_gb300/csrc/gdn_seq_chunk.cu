@@ -227,9 +227,15 @@ __device__ __forceinline__ void conv_tokens(const SeqParams& p, const InT* x, co
   const int K = p.K;
   // The rows, all in flight at once: those outside the request are read at its nearest row, and replaced after.
   float4 f[kTok + KT - 1];
+  if (t0 >= KT - 1 && t0 + kTok <= len) {
+    const InT* at = x + static_cast<long long>(t0 - (KT - 1)) * p.x_row + ch;
 #pragma unroll
-  for (int i = 0; i < kTok + KT - 1; ++i)
-    f[i] = raw4(x + static_cast<long long>(min(max(t0 + i - (KT - 1), 0), len - 1)) * p.x_row + ch);
+    for (int i = 0; i < kTok + KT - 1; ++i, at += p.x_row) f[i] = raw4(at);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kTok + KT - 1; ++i)
+      f[i] = raw4(x + static_cast<long long>(min(max(t0 + i - (KT - 1), 0), len - 1)) * p.x_row + ch);
+  }
 #pragma unroll
   for (int j = 0; j < KT; ++j) w[j][0] = w[j][1] = 0ull;
   if (p.conv_mode != 1) {
@@ -369,7 +375,7 @@ __device__ __forceinline__ float conv_rows(const SeqParams& p, const Place<InT>&
 
 // X = (1 + A)^-1 for strictly lower A.  ax[j][i] (kLd floats a row) holds A_ij in i > j; X_kj goes to ax[k][j], j <= k,
 // which A leaves free.  First the diagonal blocks of 32, a warp each: lane = column, forward substitution by blocks of 16
-// rows; then X21 = -X22 (A21 X11) by all warps, four rows a warp, through T in tmp (32 x 32, its own memory).
+// rows; then X21 = -X22 (A21 X11) by all warps, a tile of 16 x 8 each, through T = A21 X11 in tmp (its own memory).
 __device__ __forceinline__ void solve_block(float* ax, int half, int lane) {
   const int col = half * 32 + lane;
 #pragma unroll 1
@@ -419,36 +425,55 @@ __device__ __forceinline__ void solve_block(float* ax, int half, int lane) {
     __syncwarp();
   }
 }
+// c (16 x 8) += a (16 x 8) b (8 x 8) with both in two tf32 terms: a tile of 1024 multiply-adds is too small for tcgen05, whose
+// operands would have to be laid out and results fetched from tensor memory.
+__device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+  asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+__device__ __forceinline__ void mma_exact(float (&c)[4], const float (&a)[4], const float (&b)[2]) {
+  uint32_t ah[4], al[4], bh[2], bl[2];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) ah[i] = __float_as_uint(tf32_hi(a[i])), al[i] = __float_as_uint(tf32_lo(a[i]));
+#pragma unroll
+  for (int i = 0; i < 2; ++i) bh[i] = __float_as_uint(tf32_hi(b[i])), bl[i] = __float_as_uint(tf32_lo(b[i]));
+  mma_tf32(c, al, bl);             // (the terms are cut off, not rounded: their product has a sign and counts)
+  mma_tf32(c, al, bh);
+  mma_tf32(c, ah, bl);
+  mma_tf32(c, ah, bh);
+}
 __device__ __forceinline__ void solve(float* ax, float* tmp, int warp, int lane) {
   if (warp < 2) solve_block(ax, warp, lane);
   __syncthreads();
-  const int r = 4 * warp;                          // rows of the lower block; lane = column
-  u64 s0 = 0ull, s1 = 0ull;
-#pragma unroll 8
-  for (int k = 0; k < 32; ++k) {                   // T = A21 X11
-    const float x = lane <= k ? ax[k * kLd + lane] : 0.f;
-    const ulonglong2 a = *reinterpret_cast<const ulonglong2*>(ax + k * kLd + 32 + r);
-    s0 = fma2(pack2(x, x), a.x, s0);
-    s1 = fma2(pack2(x, x), a.y, s1);
+  // a warp takes rows m0 .. and columns n0 .. of the lower left block
+  const int m0 = 16 * (warp & 1), n0 = 8 * (warp >> 1), g = lane >> 2, q = lane & 3;
+  float c[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int k = 0; k < 32; k += 8) {                // T = A21 X11
+    if (k + 7 < n0) continue;                      // above X11's diagonal
+    const float* a = ax + (k + q) * kLd;
+    const float av[4] = {a[32 + m0 + g], a[32 + m0 + g + 8], a[4 * kLd + 32 + m0 + g], a[4 * kLd + 32 + m0 + g + 8]};
+    const float bv[2] = {n0 + g <= k + q ? a[n0 + g] : 0.f, n0 + g <= k + q + 4 ? a[4 * kLd + n0 + g] : 0.f};
+    mma_exact(c, av, bv);
   }
-  const float2 a = unpack2(s0), b = unpack2(s1);
-  tmp[r * 32 + lane] = a.x, tmp[(r + 1) * 32 + lane] = a.y, tmp[(r + 2) * 32 + lane] = b.x, tmp[(r + 3) * 32 + lane] = b.y;
+  constexpr int kT = 40;                           // floats a row of T: the reads below touch all banks once
+  *reinterpret_cast<float2*>(tmp + (m0 + g) * kT + n0 + 2 * q) = make_float2(c[0], c[1]);
+  *reinterpret_cast<float2*>(tmp + (m0 + g + 8) * kT + n0 + 2 * q) = make_float2(c[2], c[3]);
   __syncthreads();
-  float s[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 1
-  for (int k = 0; k <= r; k += 4) {                // -X22 T: rows r .. r + 3 end at their diagonals
-    const float t[4] = {tmp[k * 32 + lane], tmp[(k + 1) * 32 + lane], tmp[(k + 2) * 32 + lane], tmp[(k + 3) * 32 + lane]};
+  c[0] = c[1] = c[2] = c[3] = 0.f;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float4 v = *reinterpret_cast<const float4*>(ax + (32 + r + e) * kLd + 32 + k);
-      s[e] = fmaf(-v.x, t[0], s[e]);               // (k <= r)
-      s[e] = fmaf(k + 1 <= r + e ? -v.y : 0.f, t[1], s[e]);
-      s[e] = fmaf(k + 2 <= r + e ? -v.z : 0.f, t[2], s[e]);
-      s[e] = fmaf(k + 3 <= r + e ? -v.w : 0.f, t[3], s[e]);
-    }
+  for (int k = 0; k < 32; k += 8) {                // X22 T
+    if (k > m0 + 15) continue;                     // above X22's diagonal
+    const float* a = ax + (32 + m0 + g) * kLd + 32 + k + q;
+    const int d = m0 + g - k - q;                  // how far the first entry is below the diagonal
+    const float av[4] = {d >= 0 ? a[0] : 0.f, d + 8 >= 0 ? a[8 * kLd] : 0.f, d - 4 >= 0 ? a[4] : 0.f, d + 4 >= 0 ? a[8 * kLd + 4] : 0.f};
+    const float bv[2] = {tmp[(k + q) * kT + n0 + g], tmp[(k + q + 4) * kT + n0 + g]};
+    mma_exact(c, av, bv);
   }
-#pragma unroll
-  for (int e = 0; e < 4; ++e) ax[(32 + r + e) * kLd + lane] = s[e];
+  float* const x = ax + (32 + m0 + g) * kLd + n0 + 2 * q;
+  *reinterpret_cast<float2*>(x) = make_float2(-c[0], -c[1]);
+  *reinterpret_cast<float2*>(x + 8 * kLd) = make_float2(-c[2], -c[3]);
   __syncthreads();
 }
 
