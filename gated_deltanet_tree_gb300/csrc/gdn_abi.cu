@@ -669,7 +669,7 @@ gdn_status gdn_prefill(const gdn_dims* d, int32_t layers, int32_t layer, int32_t
     if (lens[b] < 0) return fail(GDN_ERR_INVALID_ARG, "lens[%d] = %d", b, lens[b]);
     rows += lens[b];
   }
-  if (rows > INT32_MAX) return fail(GDN_ERR_UNSUPPORTED, "%lld rows", rows);
+  if (rows > INT32_MAX - gdn::kChunk) return fail(GDN_ERR_UNSUPPORTED, "%lld rows", rows);   // a last chunk ends within 32 bits
   GDN_TRY(check_seq(d, layers, layer, B, x_raw, x_row, conv_w, beta, log_g, gate_row, state, conv_state, state_out,
                     conv_out, out_o, out_dtype, banks, err, p));
   GDN_CHECK_PTR(workspace, "workspace");

@@ -81,12 +81,16 @@ Side* side_stream(cudaStream_t s) {
   }
   Side& side = sides[device];
   if (side.state == 0) {
+    // another thread's capture is no concern of these calls, which put nothing on a stream
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    cudaThreadExchangeStreamCaptureMode(&mode);
     int least = 0, greatest = 0;
     cudaError_t e = cudaDeviceGetStreamPriorityRange(&least, &greatest);
     if (e == cudaSuccess) e = cudaStreamCreateWithPriority(&side.stream, cudaStreamNonBlocking, greatest);
     for (int i = 0; i < 2; ++i)
       for (cudaEvent_t* v : {&side.ready[i], &side.go[i], &side.done[i]})
         if (e == cudaSuccess) e = cudaEventCreateWithFlags(v, cudaEventDisableTiming);
+    cudaThreadExchangeStreamCaptureMode(&mode);
     side.state = e == cudaSuccess ? 1 : 2;
     if (e != cudaSuccess) cudaGetLastError();
   }

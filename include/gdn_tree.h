@@ -27,8 +27,8 @@
  *    tree (GDN_DEVERR_INVALID_PATH), packed schedule words out of range
  *    (GDN_DEVERR_SCHEDULE), an asynchronous copy or MMA that a bounded wait gave
  *    up on (GDN_DEVERR_TIMEOUT).  gdn_check_error() reads and clears them.
- *    GDN_DEVERR_TIMEOUT is sticky: while it is set, every conv-window, verify and
- *    finish kernel of every later call (not only the rest of the launch that set
+ *    GDN_DEVERR_TIMEOUT is sticky: while it is set, every conv-window, verify,
+ *    finish, prefill and step kernel of every later call (not only the rest of the launch that set
  *    it) exits at once without doing work, so outputs stay unwritten and pending
  *    factors stay unfolded.  The host-side bank lifecycle still advances
  *    (pend_bank, verified_bank), and gdn_commit_fold still records paths.  A
@@ -539,8 +539,8 @@ gdn_status gdn_tree_accept(const gdn_batch_schedule* sched, int32_t V, int32_t v
  * from the state and conv window given, which may be an earlier part of the same prompt's.
  *   layers, layer  the stack of state, conv_state and conv_w, and which of it this call is for
  *   lens       [B] host
- *   x_raw      [rows][C] in_dtype, rows = sum of lens, x_row elements apart (0: C; rows start
- *              on 16 bytes)
+ *   x_raw      [rows][C] in_dtype, rows = sum of lens (2^31 - 64 or more: GDN_ERR_UNSUPPORTED),
+ *              x_row elements apart (0: C; rows start on 16 bytes)
  *   beta, log_g [rows][Hv] in_dtype, gate_row elements apart (0: Hv).  log_g -inf (forget
  *              everything) is fine; above 0 the state grows, which fp32 must hold
  *   conv_w     [layers][C][K] fp32 (conv_mode 1; else may be NULL)
@@ -555,7 +555,14 @@ gdn_status gdn_tree_accept(const gdn_batch_schedule* sched, int32_t V, int32_t v
  *   err        error words (int32 [4], as gdn_banks.err, or those themselves)
  *   workspace  >= gdn_prefill_workspace_bytes(d) bytes; nothing in it needs clearing; calls that may
  *              overlap need one each
- * The lengths are the host's, so a captured call replays with the same ones.
+ *   out_o, state_out and conv_out overlap no other argument but as said.
+ * The lengths are the host's, so a captured call replays with the same ones.  All sums and states are
+ * fp32; the products of prompts above 16 rows take their operands as two fp16 terms (22 bits of each
+ * element, scaled by powers of two), so that a prompt taken in parts, or beside other requests, gives
+ * the same values up to rounding, and the same call the same bits.  A request with a NaN or an infinity
+ * does not touch the others.  Long prompts of few requests use a stream of the library's own besides the
+ * given one (not while that is being captured), which waits for it: to the caller all of the work is on
+ * `stream`.
  * ------------------------------------------------------------------------- */
 size_t gdn_prefill_workspace_bytes(const gdn_dims* d);
 gdn_status gdn_prefill(const gdn_dims* d, int32_t layers, int32_t layer, int32_t B, const int32_t* lens,

@@ -1,6 +1,8 @@
 """Prompt, single-token and log-probability calls as programs make them on a GPU: streams, CUDA graphs, calls between tree
 verifies, values that change their size within a chunk, and sizes beyond 32-bit offsets.  Tolerances as in
 test_gpu_sequences.py unless a test derives its own."""
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -195,6 +197,37 @@ def test_long_prompts_on_two_busy_streams_and_captured():
         o, T, _ = Q.run_sequence(f64(s[0, 0]), f64(w[0, 0]), f64(k[0][rows]), f64(k[1][rows]), f64(k[2][rows]), f64(c.w[0]), c.d)
         assert np.abs(f64(out[rows]) - o).max() <= 4e-5 * np.abs(o).max()
         assert np.linalg.norm(f64(state[b, 0]) - T) <= 2e-5 * np.linalg.norm(T)
+
+
+def test_first_long_prompt_of_a_thread_while_another_captures():
+    """A thread's first long prompt makes the library's stream for that thread: it must end no capture of another one, and give
+    the bits of the same call made outside."""
+    c = Case(34, (1, 2, 128, 128), [3200], "bf16", slow=True, layers=1, layer=0)
+    r, work = c.runner(), torch.cuda.Stream()
+    want, out = c.out.clone(), torch.empty_like(c.out)
+    state, window = torch.empty_like(c.state), torch.empty_like(c.conv)
+    r.prefill(c.lens, *c.inputs(), c.state, c.conv, want, state_out=state, conv_out=window)
+    x, y = torch.ones(1000, device="cuda"), torch.zeros(1000, device="cuda")
+    torch.cuda.synchronize()
+    failed = []
+
+    def call():
+        try:
+            r.prefill(c.lens, *c.inputs(), c.state, c.conv, out, state_out=state, conv_out=window, stream=work)
+        except Exception as e:
+            failed.append(e)
+
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y.add_(x)
+        thread = threading.Thread(target=call)
+        thread.start()
+        thread.join()
+        y.add_(x)
+    graph.replay()
+    torch.cuda.synchronize()
+    r.check_error()
+    assert not failed and torch.equal(out, want) and torch.equal(y, 2 * x)
 
 
 @pytest.mark.parametrize("B", [2, 160])
