@@ -19,6 +19,7 @@ namespace gdn {
 namespace {
 
 constexpr int kTokenByToken = 16;
+constexpr int kManyCtas = 608;
 constexpr size_t kWorkspace = 1000u << 20;
 
 int workspace_slots(const gdn_dims& d) {
@@ -29,30 +30,40 @@ int workspace_slots(const gdn_dims& d) {
 // The segments of a batch of prompts, one after another.
 struct Planner {
   SegReq* todo;                // the longest first
-  int n;
+  int n, ctas;                 // ctas: of one request's chains
   int active[kSegReqs];
   int n_active = 0, begun = 0;
-  Planner(SegReq* t, int count) : todo(t), n(count) {}
-  // The next chunks of up to kSegReqs requests, at most `slots` in all; false when there are none.
+  Planner(SegReq* t, int count, int c) : todo(t), n(count), ctas(c) {}
+  static int left(const SegReq& r) { return (r.len + kChunk - 1) / kChunk - (r.c0 + r.nc); }
+  // The next chunks of some requests, at most `slots` in all; false when there are none.
   bool next(Segment& seg, int slots) {
-    int left = 0;
+    int kept = 0, sum = 0, most = 0;
     for (int i = 0; i < n_active; ++i)
-      if ((todo[active[i]].c0 + todo[active[i]].nc) * kChunk < todo[active[i]].len) active[left++] = active[i];
-    n_active = left;
-    while (n_active < std::min(kSegReqs, slots) && begun < n) active[n_active++] = begun++;
-    if (n_active == 0) return false;
-    // the longest one's chunks in even parts (the others' follow from its)
-    int most = 0;
-    for (int i = 0; i < n_active; ++i) {
-      const SegReq& r = todo[active[i]];
-      most = std::max(most, (r.len + kChunk - 1) / kChunk - (r.c0 + r.nc));
+      if (const int c = left(todo[active[i]])) active[kept++] = active[i], sum += c, most = std::max(most, c);
+    n_active = kept;
+    while (n_active < std::min(kSegReqs, slots) && begun < n) {
+      const int c = left(todo[begun]);
+      if (n_active * ctas >= kManyCtas && sum + c > slots) break;
+      active[n_active++] = begun++, sum += c, most = std::max(most, c);
     }
-    const int parts = (most + slots / n_active - 1) / (slots / n_active), share = (most + parts - 1) / parts;
+    if (n_active == 0) return false;
+    // at most `share` chunks of each: as many as there are places for, the longest one's in even parts
+    int share = most, low = slots / n_active;
+    for (int high = most; low < high;) {
+      const int mid = low + (high - low + 1) / 2;
+      int total = 0;
+      for (int i = 0; i < n_active; ++i) total += std::min(mid, left(todo[active[i]]));
+      if (total <= slots) low = mid; else high = mid - 1;
+      share = low;
+    }
+    const int parts = (most + share - 1) / share;
+    share = (most + parts - 1) / parts;
     seg.n = seg.slots = 0;
     for (int i = 0; i < n_active; ++i) {
       SegReq& r = todo[active[i]];
+      const int c = std::min(share, left(r));
       r.c0 += r.nc;
-      r.nc = std::min(share, (r.len + kChunk - 1) / kChunk - r.c0);
+      r.nc = c;
       r.slot0 = seg.slots;
       seg.slots += r.nc;
       seg.r[seg.n++] = r;
@@ -130,11 +141,12 @@ cudaError_t launch_prefill(const SeqParams& p, const int32_t* lens, int B, void*
     }
   }
   std::sort(todo, todo + n, [](const SegReq& a, const SegReq& c) { return a.len != c.len ? a.len > c.len : a.b < c.b; });
-  Planner plan{todo, n};
+  const int ctas = p.Hv * (p.dv / 64 ? p.dv / 64 : 1);
+  Planner plan{todo, n, ctas};
   const int chunks = n ? (todo[0].len + kChunk - 1) / kChunk : 0;
   // Few requests leave SMs to the next segment's preparation; several segments are needed for that.
   Side* side = nullptr;
-  if (n > 0 && n * p.Hv * (p.dv / 64 ? p.dv / 64 : 1) <= kFewCtas && chunks >= kAheadLeast) side = side_stream(s);
+  if (n > 0 && n * ctas <= kFewCtas && chunks >= kAheadLeast) side = side_stream(s);
   char* const ws = static_cast<char*>(workspace);
   Segment seg{};
   if (!side) {

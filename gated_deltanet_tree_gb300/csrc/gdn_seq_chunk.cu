@@ -1180,6 +1180,19 @@ seq_chain_kernel(const SeqParams p, const __grid_constant__ Segment seg, const c
       read_maxima(1, smax, unused);
     }
     put_state(0, smax);
+    // While D1 runs: the window after the prompt, its last K - 1 rows (the launches before have read the old ones).
+    if ((req.c0 + req.nc) * kChunk >= req.len) {
+      float* wout = p.conv_out + req.b * p.conv_stride;
+      const int kq = p.Hk * DK, extra = vh % R == 0 && col0 == 0 ? 2 * DK : 0;
+      for (int c = tid; c < NB + extra; c += L::kThreads) {
+        const int ch = c < NB ? 2 * kq + vh * p.dv + col0 + c : c - NB < DK ? kh * DK + c - NB : kq + kh * DK + c - NB - DK;
+        for (int j = 0; j < p.K - 1; ++j) {
+          const long long at = (req.start + static_cast<long long>(req.len - (p.K - 1) + j)) * p.x_row + ch;
+          wout[static_cast<long long>(j) * p.C + ch] = p.in_dtype == GDN_DTYPE_BF16 ? load_f(static_cast<const __nv_bfloat16*>(p.x) + at)
+                                                                                    : load_f(static_cast<const float*>(p.x) + at);
+        }
+      }
+    }
     float s_bound = smax, u_bound = 0.f, o_bound = 0.f, omax_before;   // of the chunk before
     for (int i = 0; i < req.nc; ++i) {
       const int odd = (req.c0 + i) & 1, ph = i & 1;
@@ -1303,23 +1316,6 @@ seq_chain_kernel(const SeqParams p, const __grid_constant__ Segment seg, const c
       for (int j = 0; j < kPairs; j += 2) {
         const float2 x = unpack2(S[j]), y = unpack2(S[j + 1]);
         *reinterpret_cast<float4*>(dst + 2 * j) = make_float4(x.x, x.y, y.x, y.y);
-      }
-    }
-  }
-  // The window after the prompt: its last K - 1 rows (the launch before has read the old ones).
-  if (!stop && p.K > 1 && (req.c0 + req.nc) * kChunk >= req.len) {
-    const float* win = p.conv_in ? p.conv_in + req.b * p.conv_stride : nullptr;
-    float* wout = p.conv_out + req.b * p.conv_stride;
-    const int kq = p.Hk * DK, extra = vh % R == 0 && col0 == 0 ? 2 * DK : 0;
-    for (int c = tid; c < NB + extra; c += L::kThreads) {
-      const int ch = c < NB ? 2 * kq + vh * p.dv + col0 + c : c - NB < DK ? kh * DK + c - NB : kq + kh * DK + c - NB - DK;
-      for (int j = 0; j < p.K - 1; ++j) {
-        const int t = req.len - (p.K - 1) + j;
-        const long long at = (req.start + static_cast<long long>(t)) * p.x_row + ch;
-        wout[static_cast<long long>(j) * p.C + ch] =
-            t < 0 ? (win ? win[static_cast<long long>(p.K - 1 + t) * p.C + ch] : 0.f)
-                  : p.in_dtype == GDN_DTYPE_BF16 ? load_f(static_cast<const __nv_bfloat16*>(p.x) + at)
-                                                 : load_f(static_cast<const float*>(p.x) + at);
       }
     }
   }
