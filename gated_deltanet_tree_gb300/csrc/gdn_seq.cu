@@ -3,12 +3,16 @@
 // Prompts of more than kTokenByToken rows go through the chunked form, 64 tokens at a time.  (The two take the same time, of
 // one request and of 32, at 13 and 27 rows with 48 heads of 128 x 128, at 24 and 24 with small heads.)  Up to kSegReqs requests are in
 // work together, the longest first; a segment is the next chunks of each, as many as the workspace has places for.  Its
-// operands are prepared, then run through; the next segment finds the states where this one left them.  Where few requests
-// leave SMs idle, the next segment is prepared beside it: the workspace's halves take turns, and the chains go to a stream
+// operands are prepared, then run through; the next segment finds the states where this one left them.  A chain's CTA takes
+// some 5 us besides its chunks (3 us each), so no more requests are begun than fill the GPU: once they have kManyCtas CTAs, four
+// an SM, another has to fit in whole.  Where few requests leave SMs idle, the next segment is prepared beside it: the workspace's halves take turns, and the chains go to a stream
 // of the library's own, which has the higher priority and which the caller's stream waits for at the end.
 // The workspace is large rather than kept in L2: every segment pays three launches, rounds of CTAs that do not fill the GPU
-// and the states' way through memory.  8191 tokens of 48 heads took 858 us with 104 MB, 801 with 300 and 735 with 1000; 32
-// prompts of up to 500 tokens 1447, 1323 and 1237.
+// and the states' way through memory.  8191 tokens of 48 heads took 858 us with 104 MB, 801 with 300 and 735 with 1000 (before
+// the halves took turns).
+//
+// Measured, 16 k-heads and 48 v-heads of 128 x 128, bf16 (us): 70 tokens 32, 1024 104, 8191 657, 20001 and 15001 together 2550,
+// 32 prompts of 250 to 500 tokens 1028, 128 of 50 to 100 1505.
 #include <algorithm>
 #include <initializer_list>
 #include <new>
@@ -19,6 +23,8 @@ namespace gdn {
 namespace {
 
 constexpr int kTokenByToken = 16;
+// 32 prompts of 1000 to 2000 rows: 3681 us, with 32 at a time 3900; 64 of 125 to 250 1300 and 1543; with 304 CTAs six of 1500 to
+// 3000 took 1133 us instead of 1065.
 constexpr int kManyCtas = 608;
 constexpr size_t kWorkspace = 1000u << 20;
 

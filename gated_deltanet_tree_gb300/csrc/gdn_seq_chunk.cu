@@ -4,8 +4,9 @@
 //   A = (beta_i e^(c_i - c_j) k_i.k_j)_{j < i},   M = (1 + A)^-1 diag(beta),   N = (e^(c_i - c_j) q_i.k_j)_{j <= i} M,
 //   w_i = v_i - e^(c_i) T^T k_i,   u = M w,   o_i = e^(c_i) T^T q_i + (N w)_i,
 //   T' = e^(c_63) T + sum_i k_i (e^(c_63 - c_i) u_i)^T.
-// Everything in the first line is independent of T: seq_prepare_kernel computes it for many chunks at once, with the conv,
-// the activation and the norms.  seq_chain_kernel then walks each head's chunks:
+// Everything in the first line is independent of T: seq_keys_kernel (k, q and their products, once a k-head) and
+// seq_values_kernel (gates, v, M and N of a v-head) compute it for many chunks at once, with the conv, the activation and the
+// norms.  seq_chain_kernel then walks each head's chunks:
 //   D1 = [K; Q] T   ->   w   ->   D2 = [M; N] w   ->   u, o   ->   D3 = K^T u   ->   T'
 // with T in fp32 in registers, a row of d_k and 32 columns a thread.  Columns of d_v do not depend on each other.
 //
@@ -477,7 +478,12 @@ __device__ __forceinline__ void solve(float* ax, float* tmp, int warp, int lane)
   __syncthreads();
 }
 
-// k and q of a chunk and k-head: rows, two-term images, Gram matrices.
+// k and q of a chunk and k-head: rows, two-term images, Gram matrices (K K^T and Q K^T in one 128 x 64 product).
+//
+// Bound: the latencies of a CTA's five steps (rows from memory, conv, images, product, results) with two CTAs an SM, whose
+// shared memory the images and the rows in 32 bits fill; 128 chunks of 16 heads of 128 take 86 us, 2.4 TB/s, 41% of the issue
+// slots.  (Rows in the places of images that are not written yet leave room for three CTAs, at 80 registers: 3% off 32 prompts,
+// but 4% more for a prompt of 70 tokens and 6% for heads of 64.)
 template <typename InT, int DK, int KT>
 __global__ void __launch_bounds__(kPrepThreads, 2)
 seq_keys_kernel(const SeqParams p, const __grid_constant__ Segment seg, char* ws) {
@@ -552,6 +558,11 @@ seq_keys_kernel(const SeqParams p, const __grid_constant__ Segment seg, char* ws
 }
 
 // v, the gates, M and N of a chunk and v-head.
+//
+// (1 + A)^-1 by substitution in blocks: two 32 x 32 triangles, a warp each, and the block below them as a product of three on
+// mma.sync: tiles of 16 x 8 straight from and into A's rows in shared memory, where tcgen05 would want images, tensor memory
+// and two barriers for two products of 32 x 32 x 32.  N = C M is on tcgen05.  Bound: instruction issue (57% of the slots; the
+// rest goes with the barriers between the steps); 128 chunks of 48 heads take 201 us.
 template <typename InT, int KT>
 __global__ void __launch_bounds__(kPrepThreads, 4)
 seq_values_kernel(const SeqParams p, const __grid_constant__ Segment seg, char* ws) {
@@ -814,6 +825,10 @@ seq_values_kernel(const SeqParams p, const __grid_constant__ Segment seg, char* 
 
 // ---- the chunks of a head, one after another ------------------------------------------------------------------------
 
+// Bound: the way from one chunk to the next.  Its three products, T's and w's conversion to operands and the six hand-overs
+// between tensor cores and threads take 3.1 us for 64 columns (tensor pipe 45% busy by the two groups together: a product with
+// few columns runs at the rate at which A, 128 rows, is read from shared memory; issue 35%).  All 128 columns of a head in a CTA
+// would halve the reading of K, Q, M and N, but take 9.3 us a chunk and leave half the SMs without work where requests are few.
 template <int DK, int NB>
 struct Chain {
   // Two groups of columns take turns at the tensor cores: one's products run while the other's threads work.
@@ -1377,8 +1392,7 @@ cudaError_t launch_prepare_d(const SeqParams& p, const Segment& seg, char* ws, c
 }
 template <int DK>
 cudaError_t launch_chain_d(const SeqParams& p, const Segment& seg, const char* ws, bool right_after, cudaStream_t s) {
-  // 64 columns a CTA, or 32 where the other half of the GPU would be idle.  (With all 128 of a head a chunk takes more than
-  // twice the time: 9.3 against 3.8 us.)
+  // 64 columns a CTA, or 32 where the other half of the GPU would be idle.
   if (p.dv >= 64 && seg.n * p.Hv * (p.dv / 64) > 76) return launch_chain<DK, 64>(p, seg, ws, right_after, s);
   return launch_chain<DK, 32>(p, seg, ws, right_after, s);
 }
