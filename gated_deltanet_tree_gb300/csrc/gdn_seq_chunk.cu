@@ -17,7 +17,8 @@
 // 2^-40 of the bound, and the bounds lie some 2^6 above the values.  T' is handed on scaled by a bound as well,
 // |T'| <= e^c max T + 64 max u, some 2^11 above it, and the largest entry is looked at afterwards: no warp waits for the
 // others'.  Where a bound turns out to lie 2^17 above the largest entry of T' or of the chunk's o (values that shrink or grow
-// by that much within 64 tokens), T' is handed on again, or the chunk is taken again, token by token.
+// by that much within 64 tokens), T' is handed on again, or the chunk is taken again, token by token.  Entries of T and v that
+// are not finite count for no bound: they stay in their own column of d_v, as in the rule.
 //
 // Operands in shared memory have no swizzle: 8 rows x 16 bytes are 128 contiguous bytes.  With 16 bytes of d_k per
 // token, a core matrix of K serves as K-major operand of D1 and as M-major operand of D3.
@@ -155,6 +156,8 @@ __device__ __forceinline__ float abs_max(float m, u64 x) {
   const float2 f = unpack2(x);
   return fmaxf(m, fmaxf(fabsf(f.x), fabsf(f.y)));
 }
+constexpr float kInf = __builtin_huge_valf();
+__device__ __forceinline__ float finite_max(float m, float x) { return fabsf(x) < kInf ? fmaxf(m, fabsf(x)) : m; }
 
 // A bounded wait that leaves the issue slots to the working warps.
 __device__ __forceinline__ bool mbar_wait_quiet(uint64_t* bar, uint32_t parity) {
@@ -202,7 +205,7 @@ __device__ __forceinline__ float scale_for(float bound, float& inverse) {
   inverse = __uint_as_float(static_cast<uint32_t>(254 - f) << 23);
   return __uint_as_float(static_cast<uint32_t>(f) << 23);
 }
-__device__ __forceinline__ float warp_max(float x) {     // x >= 0 (or NaN, which counts as larger than all)
+__device__ __forceinline__ float warp_max(float x) {     // x >= 0 (a NaN counts as larger than all)
   return __uint_as_float(__reduce_max_sync(~0u, __float_as_uint(x)));
 }
 __device__ __forceinline__ void mbar_init_n(uint64_t* bar, uint32_t count) {
@@ -369,6 +372,11 @@ __device__ __forceinline__ float conv_rows(const SeqParams& p, const Place<InT>&
         if (!kNorm) most = fmaxf(most, fmaxf(fmaxf(fabsf(y[i].x), fabsf(y[i].y)), fmaxf(fabsf(y[i].z), fabsf(y[i].w))));
       }
     }
+  }
+  if (!kNorm && most == kInf) {
+    most = 0.f;
+    for (int t = kTok * sub; t < 8; t += lanes == 32 ? kTok : 8)
+      for (int i = 0; i < 4 * kTok; ++i) most = finite_max(most, rows[(warp * 8 + t + i / 4) * kRowLd + cl + i % 4]);
   }
   __syncwarp();
   return kNorm ? 0.f : warp_max(most);
@@ -1075,6 +1083,14 @@ seq_chain_kernel(const SeqParams p, const __grid_constant__ Segment seg, const c
       float big = 0.f;
 #pragma unroll
       for (int j = 0; j < kPairs; ++j) big = abs_max(big, S[j]);
+      if (big == kInf) {
+        big = 0.f;
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j) {
+          const float2 f = unpack2(S[j]);
+          big = finite_max(finite_max(big, f.x), f.y);
+        }
+      }
       big = warp_max(big);
       const float bigo = warp_max(omax);
       if (lane == 0) most[half * 2 * L::kWarps + gw] = big, most[half * 2 * L::kWarps + L::kTurnWarps + gw] = bigo;

@@ -556,13 +556,16 @@ gdn_status gdn_tree_accept(const gdn_batch_schedule* sched, int32_t V, int32_t v
  *   workspace  >= gdn_prefill_workspace_bytes(d) bytes; nothing in it needs clearing; calls that may
  *              overlap need one each
  *   out_o, state_out and conv_out overlap no other argument but as said.
- * The lengths are the host's, so a captured call replays with the same ones.  All sums and states are
- * fp32; the products of prompts above 16 rows take their operands as two fp16 terms (22 bits of each
- * element, scaled by powers of two), so that a prompt taken in parts, or beside other requests, gives
- * the same values up to rounding, and the same call the same bits.  A request with a NaN or an infinity
- * does not touch the others.  Long prompts of few requests use a stream of the library's own besides the
- * given one (not while that is being captured), which waits for it: to the caller all of the work is on
- * `stream`.
+ * The lengths are the host's, so a captured call replays with the same ones. All sums and states
+ * are fp32; the products of prompts above 16 rows take their operands as two fp16 terms (22 bits of
+ * each element, scaled by powers of two), so that a prompt taken in parts, or beside other
+ * requests, gives the same values up to rounding, and the same call the same bits. An element keeps
+ * 2^-23 of itself or 2^-40 of the largest one of its head's state or values, whichever is more. A
+ * request with a NaN or an infinity does not touch the others, nor a column of v or of a state the
+ * other columns; tokens before it may lose their outputs where they share its 64 (the chunks count
+ * from the call's first row). Long prompts of few requests use a stream of the library's own
+ * besides the given one (not while that is being captured), which waits for it: to the caller all
+ * of the work is on `stream`.
  * ------------------------------------------------------------------------- */
 size_t gdn_prefill_workspace_bytes(const gdn_dims* d);
 gdn_status gdn_prefill(const gdn_dims* d, int32_t layers, int32_t layer, int32_t B, const int32_t* lens,

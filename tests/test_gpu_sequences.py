@@ -268,6 +268,34 @@ def test_prefill_many_requests():
     check(c, c.reference(), c.out, state[:, 0], conv[:, 0])
 
 
+@pytest.mark.parametrize("value", [float("inf"), -float("inf"), float("nan")])
+@pytest.mark.parametrize("heads", ["qwen", "d32"])
+def test_prefill_values_that_are_not_finite_stay_in_their_column(value, heads):
+    """Columns of v do not touch each other: an infinity or a NaN in one, of a row or of a state, leaves the others' outputs and
+    states within the tolerances, and its own from there on without a finite value."""
+    c = Case(12, heads, [150, 40], "f32")
+    d = c.d
+    head, col, at = d.Hv - 1, 5, 70
+    c.x[at, 2 * d.Hk * d.dk + head * d.dv + col] = value
+    c.state[0, 1, 0, 3, 7] = value
+    with np.errstate(invalid="ignore", over="ignore"):
+        o, T, W = c.reference()
+    state, conv = c.state.clone(), c.conv.clone()
+    r = c.runner()
+    r.prefill(c.lens, *c.inputs(), state, conv, c.out, layer=1)
+    r.check_error()
+    got, S1 = f64(c.out), f64(state[:, 1])
+    for a, s in ((o, T), (got, S1)):
+        assert not np.isfinite(a[at:150, head, col]).any() and not np.isfinite(a[:150, 0, 7]).any()
+        assert not np.isfinite(s[0, head, :, col]).any() and not np.isfinite(s[0, 0, :, 7]).any()
+        a[64:150, head, col] = a[:150, 0, 7] = s[0, head, :, col] = s[0, 0, :, 7] = 0   # (a chunk's outputs are one product)
+    assert np.array_equal(f64(conv[:, 1]), W, equal_nan=True)
+    for b, rows in enumerate((slice(0, 150), slice(150, 190))):
+        for h in range(d.Hv):
+            assert np.abs(got[rows, h] - o[rows, h]).max() <= 2e-5 * np.abs(o[rows, h]).max(), (b, h)
+            assert np.linalg.norm(S1[b, h] - T[b, h]) <= 1e-5 * np.linalg.norm(T[b, h]), (b, h)
+
+
 def test_prefill_does_not_mix_requests():
     """A request with NaN everywhere leaves the others' results as they were, bit for bit."""
     c = Case(11, "qwen", [90, 100, 64, 5], "bf16")
