@@ -259,6 +259,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : 4) logprob_kern
   const int CL = cluster.num_blocks(), rank = cluster.block_rank();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int row = blockIdx.x / CL, top = p.top;
+  // here, so that the others know that this CTA runs: they write into the first one's memory
+  if (CL > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;");
   const T* z = static_cast<const T*>(p.logits) + row * p.v_stride;
   // blocks of sixteen aligned bytes; the row begins `skew` entries into block 0
   const int skew = static_cast<int>((reinterpret_cast<uintptr_t>(z) & 15u) / sizeof(T));
@@ -377,6 +379,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : 4) logprob_kern
   const u64* list = sh.cand;
   if (CL > 1) {
     // every CTA puts its list and sums into the first one's memory
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
     if (tid < top) cluster.map_shared_rank(lists, 0)[rank * top + tid] = tid < n ? sh.cand[tid] : 0ull;
     if (tid == 0) cluster.map_shared_rank(parts, 0)[rank] = a;
     cluster.sync();
