@@ -33,7 +33,7 @@ namespace {
 
 constexpr float kUnit = 4096.f;            // scale of k and q
 constexpr float kGateFloor = -1.0e4f;      // e to this is 0; keeps differences of sums finite
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kMostGrowth = 127.f;       // log2 of products of gates that fp32 holds; the scale of larger ones stays finite
 
 // ---- operands ----
 __host__ __device__ constexpr uint32_t idesc_f16(int n, bool a_mn, bool b_mn) {   // M = 128, fp32 accumulator
@@ -625,10 +625,8 @@ seq_values_kernel(const SeqParams p, const __grid_constant__ Segment seg, char* 
     if (warp == kPrepWarps - 1) {
       // the gates meanwhile: cumulated in 64 bits and base 2, kept as two floats
       double c[2];
-      float rise = 0.f;
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        rise += fmaxf(lg[k], 0.f);
         c[k] = static_cast<double>(lg[k]) * 1.4426950408889634;
         gate[2 * kChunk + 2 * lane + k] = be[k];
       }
@@ -640,8 +638,17 @@ seq_values_kernel(const SeqParams p, const __grid_constant__ Segment seg, char* 
         if (lane >= o) sum += s;
       }
       const double before = sum - c[1], total = __shfl_sync(~0u, sum, 31);
+      // the largest product of gates in a row: how far a sum lies above the least one before it
+      const float s0 = static_cast<float>(before + c[0]), s1 = static_cast<float>(sum);
+      float least = fminf(s0, s1);
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) rise += __shfl_xor_sync(~0u, rise, o);
+      for (int o = 1; o < 32; o <<= 1) {
+        const float s = __shfl_up_sync(~0u, least, o);
+        if (lane >= o) least = fminf(least, s);
+      }
+      least = __shfl_up_sync(~0u, least, 1);
+      least = lane == 0 ? 0.f : fminf(least, 0.f);
+      const float growth = warp_max(fmaxf(fmaxf(s0 - least, s1 - fminf(least, s0)), 0.f));
       float most = 0.f;
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
@@ -658,8 +665,8 @@ seq_values_kernel(const SeqParams p, const __grid_constant__ Segment seg, char* 
       if (lane == 0) {
         meta[2 * kChunk] = exp2f(static_cast<float>(total));
         meta[2 * kChunk + 5] = most;
-        // no product of gates is above e^rise (1 unless a log gate is above 0)
-        *unit = exp2f(floorf(11.f - rise * kLog2e));
+        // no product of gates is above 2^growth (1 unless a log gate is above 0)
+        *unit = exp2f(floorf(11.f - fminf(growth, kMostGrowth)));
       }
     } else {
 #pragma unroll 4
