@@ -17,7 +17,8 @@
 // 2^-40 of the bound, and the bounds lie some 2^6 above the values.  T' is handed on scaled by a bound as well,
 // |T'| <= e^c max T + 64 max u, some 2^11 above it, and the largest entry is looked at afterwards: no warp waits for the
 // others'.  Where a bound turns out to lie 2^17 above the largest entry of T' or of the chunk's o (values that shrink or grow
-// by that much within 64 tokens), T' is handed on again, or the chunk is taken again, token by token.  Entries of T and v that
+// by that much within 64 tokens), T' is handed on again, or the chunk is taken again, token by token; so are chunks in which
+// products of gates, or M, grow (kMostGrowth).  Entries of T and v that
 // are not finite count for no bound: they stay in their own column of d_v, as in the rule.
 //
 // Operands in shared memory have no swizzle: 8 rows x 16 bytes are 128 contiguous bytes.  With 16 bytes of d_k per
@@ -33,7 +34,11 @@ namespace {
 
 constexpr float kUnit = 4096.f;            // scale of k and q
 constexpr float kGateFloor = -1.0e4f;      // e to this is 0; keeps differences of sums finite
-constexpr float kMostGrowth = 127.f;       // log2 of products of gates that fp32 holds; the scale of larger ones stays finite
+// What grows within a chunk and shrinks again keeps its rounding errors, in the triangular system's fp32 and in operands that
+// are scaled by their largest entry, where the rule forgets them.  Chunks in which a product of gates or an entry of M is above
+// this are taken token by token.  Gates up to 1 and beta in [0, 2] stay at 4 and below (u_i depends on w_j through
+// beta_i k_i^T (1 - beta k k^T) .. k_j beta_j, whose factors have norms up to 1).  It costs four bits of fp32's 24.
+constexpr float kMostGrowth = 4.f;         // log2
 
 // ---- operands ----
 __host__ __device__ constexpr uint32_t idesc_f16(int n, bool a_mn, bool b_mn) {   // M = 128, fp32 accumulator
@@ -582,7 +587,7 @@ seq_values_kernel(const SeqParams p, const __grid_constant__ Segment seg, char* 
   float* red = reinterpret_cast<float*>(sm + P::kRed);
   uint64_t* bar = reinterpret_cast<uint64_t*>(sm + P::kBar);
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(bar + 1);
-  float* unit = reinterpret_cast<float*>(bar + 2);             // scale of C
+  float* unit = reinterpret_cast<float*>(bar + 2);             // scale of C, log2 of the largest product of gates
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, vh = blockIdx.x, dv = p.dv;
   const Place<InT> at(p, seg, ws, blockIdx.y);
   const float* const grams = reinterpret_cast<const float*>(at.kq + vh / (p.Hv / p.Hk) * seq_kq_bytes(p.dk) + 4 * kChunk * p.dk * 2);
@@ -666,7 +671,8 @@ seq_values_kernel(const SeqParams p, const __grid_constant__ Segment seg, char* 
         meta[2 * kChunk] = exp2f(static_cast<float>(total));
         meta[2 * kChunk + 5] = most;
         // no product of gates is above 2^growth (1 unless a log gate is above 0)
-        *unit = exp2f(floorf(11.f - fminf(growth, kMostGrowth)));
+        unit[0] = exp2f(floorf(11.f - fminf(growth, kMostGrowth)));
+        unit[1] = growth;
       }
     } else {
 #pragma unroll 4
@@ -776,7 +782,10 @@ seq_values_kernel(const SeqParams p, const __grid_constant__ Segment seg, char* 
         *reinterpret_cast<uint4*>(out + m_row * 128 + to) = hi;
         *reinterpret_cast<uint4*>(out + 128 * 128 + m_row * 128 + to) = lo;
       }
-      if (tid == 0) meta[2 * kChunk + 1] = inv_m, meta[2 * kChunk + 4] = sum;
+      if (tid == 0) {
+        meta[2 * kChunk + 1] = inv_m, meta[2 * kChunk + 4] = sum;
+        meta[2 * kChunk + 7] = unit[1] > kMostGrowth || big > exp2f(kMostGrowth) ? 1.f : 0.f;
+      }
     }
     fence_proxy_async();
     __syncthreads();
@@ -1286,6 +1295,7 @@ seq_chain_kernel(const SeqParams p, const __grid_constant__ Segment seg, const c
       u_bound = mbound * w_bound * 1.001f;
       o_bound = nbound * w_bound * fabsf(p.q_scale);
       s_bound = (whole * smax + 64.f * u_bound) * 1.001f;
+      if (m1.w != 0.f) u_bound = s_bound = kInf;               // to be taken again, whatever the chunk came to
       const float sc_u = scale_for(u_bound, inv_u);
       // (the other group has read the gates of the chunk before: it took part in D2 there, without which nobody is here)
       if (!k_row && copies && i + 1 < req.nc && elect_one()) load_meta(i + 1);

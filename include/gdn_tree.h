@@ -542,7 +542,9 @@ gdn_status gdn_tree_accept(const gdn_batch_schedule* sched, int32_t V, int32_t v
  *   x_raw      [rows][C] in_dtype, rows = sum of lens (2^31 - 64 or more: GDN_ERR_UNSUPPORTED),
  *              x_row elements apart (0: C; rows start on 16 bytes)
  *   beta, log_g [rows][Hv] in_dtype, gate_row elements apart (0: Hv).  log_g -inf (forget
- *              everything) is fine; above 0 the state grows, which fp32 must hold
+ *              everything) is fine; above 0 the state grows, which fp32 must hold.  64 tokens in which
+ *              gates above 1, or beta outside [0, 2], grow anything 16 times are taken one by one,
+ *              some 30 times as slowly
  *   conv_w     [layers][C][K] fp32 (conv_mode 1; else may be NULL)
  *   state      [B][layers][Hv][dk][dv] fp32: before the call; NULL: zeros
  *   conv_state [B][layers][K-1][C] fp32: raw rows before the call, oldest first; NULL: zeros
