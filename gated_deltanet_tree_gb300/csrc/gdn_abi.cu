@@ -713,7 +713,10 @@ gdn_status gdn_top_logprobs(int32_t rows, int32_t V, int64_t v_stride, int32_t d
   if (!known_dtype(dtype)) return fail(GDN_ERR_INVALID_ARG, "dtype = %d", dtype);
   if (top_k < 1 || top_k > V) return fail(GDN_ERR_INVALID_ARG, "top_k = %d, V = %d", top_k, V);
   if (top_k > GDN_MAX_TOP) return fail(GDN_ERR_UNSUPPORTED, "top_k = %d above %d", top_k, GDN_MAX_TOP);
-  GDN_CHECK_PTR(logits, "logits");
+  // rows lie at any element: the kernel begins a row within sixteen aligned bytes
+  if (!logits) return fail(GDN_ERR_INVALID_ARG, "logits is NULL");
+  if (reinterpret_cast<uintptr_t>(logits) & (dtype == GDN_DTYPE_F32 ? 3 : 1))
+    return fail(GDN_ERR_INVALID_ARG, "logits is not aligned to its elements");
   if ((tokens == nullptr) != (given == nullptr)) return fail(GDN_ERR_INVALID_ARG, "tokens and given: both or neither");
   if (tokens) {
     GDN_CHECK_PTR(tokens, "tokens");

@@ -591,7 +591,7 @@ gdn_status gdn_step(const gdn_dims* d, int32_t layers, int32_t layer, int32_t B,
  * gdn_top_logprobs -- log-probabilities of rows of logits: the best tokens' (the draft's candidates
  * that gdn_ddtree_build takes), a given token's, and the entropy.
  *   logits  [rows] rows of V values, dtype, v_stride elements apart (0: V); -inf masks a token.
- *           Rows may have any alignment
+ *           Rows, the first among them, may begin at any element
  *   tokens  [rows] int32, or NULL: the given tokens; one outside [0, V) gives NaN
  *   top_k   1 .. min(V, GDN_MAX_TOP)
  *   top_logp, top_token [rows][top_k] fp32, int32 out: larger logits first, the lower index on ties;
