@@ -522,6 +522,7 @@ class TokenScorer:
         self.top = torch.zeros(rows, top_k, device=self.device)
         self.tokens = torch.full((rows, top_k), -1, dtype=torch.int32, device=self.device)
         self.given = torch.zeros(rows, device=self.device)
+        self._shifted = torch.zeros(rows, dtype=torch.int32, device=self.device)   # tokens that do not begin on 16 bytes
         self.entropy = torch.zeros(rows, device=self.device)
         self.err = torch.zeros(4, dtype=torch.int32, device=self.device)
         self._index = self.top.get_device()
@@ -529,9 +530,22 @@ class TokenScorer:
         self._given, self._rest = self.given.data_ptr(), (self.entropy.data_ptr(), self.err.data_ptr())
         _finish_fills(self.device)
 
+    def _shift(self, tokens: torch.Tensor, stream) -> int:
+        """A copy on 16 bytes of a slice of token numbers, made on the call's stream."""
+        to = self._shifted[:tokens.shape[0]]
+        if stream is None or self._index < 0:
+            to.copy_(tokens)
+        else:
+            if isinstance(stream, int):
+                stream = torch.cuda.ExternalStream(stream, device=self._index)
+            with torch.cuda.stream(stream):
+                to.copy_(tokens)
+        return to.data_ptr()
+
     def score(self, logits: torch.Tensor, tokens: Optional[torch.Tensor] = None, stream=None):
         """logits [n, V] -> (top [n, top_k], their tokens [n, top_k], the given tokens' [n] or None, entropy [n]): this
-        object's buffers, the first n rows of them."""
+        object's buffers, the first n rows of them.  Both arguments may be slices, as in score(logits[:-1], tokens[1:]):
+        logits begin anywhere, tokens that do not begin on 16 bytes are copied first."""
         shape = logits.shape
         if len(shape) != 2 or shape[1] != self.V or not 1 <= shape[0] <= self.rows or logits.get_device() != self._index:
             raise ValueError(f"logits is (1 .. {self.rows}, {self.V}) on {self.device}, got {tuple(shape)} on {logits.device}")
@@ -549,6 +563,8 @@ class TokenScorer:
                 raise ValueError(f"tokens is a contiguous int32 tensor ({n},) on {self.device}, got {tuple(tokens.shape)} "
                                  f"{tokens.dtype} on {tokens.device}")
             tok = tokens.data_ptr()
+            if tok & 15:
+                tok = self._shift(tokens, stream)
         N._check(N.lib().gdn_top_logprobs(n, self.V, row, _dtype_code(logits.dtype, "logits"), logits.data_ptr(), tok,
                                           self.top_k, *self._out, None if tok is None else self._given, *self._rest,
                                           N._stream_of(stream, self._index)))

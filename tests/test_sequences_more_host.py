@@ -12,3 +12,17 @@ def test_logits_begin_at_any_element(N, dtype, at, fine):
         N.gdn_top_logprobs(4, 1000, 1000, dtype, P + at, None, 4, P, P, None, P, None, 0)
     assert e.value.status == N.GDN_ERR_INVALID_ARG
     assert ("err" if fine else "logits") in str(e.value)
+
+
+def test_tokens_begin_at_any_element(N, R):
+    """The library takes token numbers on 16 bytes: slices that begin elsewhere are copied, others passed on as they are."""
+    s = R.TokenScorer(6, 100, 4, device="cpu")
+    z, tokens = torch.zeros(7, 100), torch.arange(8, dtype=torch.int32)
+    base = tokens.data_ptr()
+    assert base % 16 == 0
+    for n, first in ((6, 0), (6, 1), (3, 2), (4, 4), (1, 7)):
+        s.score(z[:n], tokens[first:first + n], stream=7)
+        at = R.recorder.calls[-1][1][5]
+        assert at % 16 == 0 and (at == base + 4 * first) == (first % 4 == 0)
+        if first % 4:
+            assert torch.equal(s._shifted[:n], tokens[first:first + n]) and at == s._shifted.data_ptr()
