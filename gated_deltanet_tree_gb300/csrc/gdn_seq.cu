@@ -5,8 +5,9 @@
 // work together, the longest first; a segment is the next chunks of each, as many as the workspace has places for.  Its
 // operands are prepared, then run through; the next segment finds the states where this one left them.  A chain's CTA takes
 // some 5 us besides its chunks (3 us each), so no more requests are begun than fill the GPU: once they have kManyCtas CTAs, four
-// an SM, another has to fit in whole.  Where few requests leave SMs idle, the next segment is prepared beside it: the workspace's halves take turns, and the chains go to a stream
-// of the library's own, which has the higher priority and which the caller's stream waits for at the end.
+// an SM, another has to fit in whole.  Where few requests leave SMs idle, the next segment is prepared beside it: the workspace's
+// halves take turns, and the chains go to a stream of the library's own, which has the higher priority and which the caller's
+// stream waits for at the end.
 // The workspace is large rather than kept in L2: every segment pays three launches, rounds of CTAs that do not fill the GPU
 // and the states' way through memory.  8191 tokens of 48 heads took 858 us with 104 MB, 801 with 300 and 735 with 1000 (before
 // the halves took turns).
@@ -15,6 +16,7 @@
 // 32 prompts of 250 to 500 tokens 1028, 128 of 50 to 100 1505.
 #include <algorithm>
 #include <initializer_list>
+#include <mutex>
 #include <new>
 
 #include "gdn_seq.cuh"
@@ -78,40 +80,66 @@ struct Planner {
   }
 };
 
-// A stream and events for the chains that run beside the next segment's preparation, one set a thread and device, made when
-// first needed and kept.  nullptr where there are none: a capturing stream (a stream of ours in somebody's graph would be
-// theirs until the capture ends), or no room for one.
+// A stream and events for the chains that run beside the next segment's preparation.  They are made when first needed, kept
+// for the process, and lent to one call at a time: a set still at work is lent on to the same stream only, whose order it keeps,
+// so that no stream waits for another one's work.
 struct Side {
   int state = 0;               // 0: not made, 1: there, 2: cannot be made
+  bool lent = false;
+  unsigned long long user = 0; // the number of the stream it was lent to last
   cudaStream_t stream;
   cudaEvent_t ready[2], go[2], done[2];
 };
-constexpr int kDevices = 64;
-Side* side_stream(cudaStream_t s) {
-  thread_local Side sides[kDevices];
+constexpr int kDevices = 64, kSides = 8;
+std::mutex side_lock;
+Side sides[kDevices][kSides];
+
+bool make_side(Side& side) {
+  int least = 0, greatest = 0;
+  cudaError_t e = cudaDeviceGetStreamPriorityRange(&least, &greatest);
+  if (e == cudaSuccess) e = cudaStreamCreateWithPriority(&side.stream, cudaStreamNonBlocking, greatest);
+  for (int i = 0; i < 2; ++i)
+    for (cudaEvent_t* v : {&side.ready[i], &side.go[i], &side.done[i]})
+      if (e == cudaSuccess) e = cudaEventCreateWithFlags(v, cudaEventDisableTiming);
+  if (e != cudaSuccess) cudaGetLastError();
+  side.state = e == cudaSuccess ? 1 : 2;
+  return side.state == 1;
+}
+bool capturing(cudaStream_t s) {
   cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(s, &capture) == cudaSuccess) return capture != cudaStreamCaptureStatusNone;
+  cudaGetLastError();
+  return true;
+}
+// nullptr: none is free, and the caller's stream does all of the work.
+Side* borrow_side(cudaStream_t s) {
   int device = 0;
-  if (cudaStreamIsCapturing(s, &capture) != cudaSuccess || capture != cudaStreamCaptureStatusNone ||
-      cudaGetDevice(&device) != cudaSuccess || device >= kDevices) {
+  unsigned long long user = 0;
+  if (cudaGetDevice(&device) != cudaSuccess || device >= kDevices) {
     cudaGetLastError();
     return nullptr;
   }
-  Side& side = sides[device];
-  if (side.state == 0) {
-    // another thread's capture is no concern of these calls, which put nothing on a stream
-    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
-    cudaThreadExchangeStreamCaptureMode(&mode);
-    int least = 0, greatest = 0;
-    cudaError_t e = cudaDeviceGetStreamPriorityRange(&least, &greatest);
-    if (e == cudaSuccess) e = cudaStreamCreateWithPriority(&side.stream, cudaStreamNonBlocking, greatest);
-    for (int i = 0; i < 2; ++i)
-      for (cudaEvent_t* v : {&side.ready[i], &side.go[i], &side.done[i]})
-        if (e == cudaSuccess) e = cudaEventCreateWithFlags(v, cudaEventDisableTiming);
-    cudaThreadExchangeStreamCaptureMode(&mode);
-    side.state = e == cudaSuccess ? 1 : 2;
-    if (e != cudaSuccess) cudaGetLastError();
+  // another thread's capture is no concern of these calls, which put nothing on a stream
+  cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+  cudaThreadExchangeStreamCaptureMode(&mode);
+  Side* found = nullptr;
+  if (cudaStreamGetId(s, &user) == cudaSuccess) {
+    std::lock_guard<std::mutex> hold(side_lock);
+    for (Side& side : sides[device])
+      if (!found && side.state == 1 && !side.lent && side.user == user) found = &side;
+    for (Side& side : sides[device])
+      if (!found && side.state == 1 && !side.lent && cudaEventQuery(side.done[0]) == cudaSuccess) found = &side;
+    for (Side& side : sides[device])
+      if (!found && side.state == 0 && make_side(side)) found = &side;
+    if (found) found->lent = true, found->user = user;
   }
-  return side.state == 1 ? &side : nullptr;
+  cudaGetLastError();          // (among others: a set's work is not done yet)
+  cudaThreadExchangeStreamCaptureMode(&mode);
+  return found;
+}
+void return_side(Side* side) {
+  std::lock_guard<std::mutex> hold(side_lock);
+  side->lent = false;
 }
 // Chains of at most kFewCtas CTAs, of at least kAheadLeast chunks, in segments of kAheadChunks chunks a request: 8191 tokens of
 // one request 741 -> 675 us (16 chunks 757, 32 689, 64 677), 20001 and 15001 tokens 3018 -> 2620 us; three requests (288 CTAs)
@@ -150,23 +178,24 @@ cudaError_t launch_prefill(const SeqParams& p, const int32_t* lens, int B, void*
   const int ctas = p.Hv * (p.dv / 64 ? p.dv / 64 : 1);
   Planner plan{todo, n, ctas};
   const int chunks = n ? (todo[0].len + kChunk - 1) / kChunk : 0;
-  // Few requests leave SMs to the next segment's preparation; several segments are needed for that.
-  Side* side = nullptr;
-  if (n > 0 && n * ctas <= kFewCtas && chunks >= kAheadLeast) side = side_stream(s);
+  // Few requests leave SMs to the next segment's preparation; several segments are needed for that.  The segments are the same
+  // whether there is a stream for it or not, and with them the results.
+  const bool ahead = n > 0 && n * ctas <= kFewCtas && chunks >= kAheadLeast && !capturing(s);
+  Side* const side = ahead ? borrow_side(s) : nullptr;
   char* const ws = static_cast<char*>(workspace);
+  const size_t half = ahead ? slots / 2 * seq_slot_bytes(p.Hk, p.Hv, p.dk, p.dv) : 0;
+  const int most = ahead ? std::min(slots / 2, std::max(n * kAheadChunks, 1)) : slots;
   Segment seg{};
+  int i = 0;
   if (!side) {
-    while (e == cudaSuccess && plan.next(seg, slots)) {
-      e = launch_seq_prepare(p, seg, ws, s);
-      if (e == cudaSuccess) e = launch_seq_chain(p, seg, ws, true, s);
+    for (; e == cudaSuccess && plan.next(seg, most); ++i) {
+      e = launch_seq_prepare(p, seg, ws + (i & 1) * half, s);
+      if (e == cudaSuccess) e = launch_seq_chain(p, seg, ws + (i & 1) * half, true, s);
     }
   } else {
-    const size_t half = slots / 2 * seq_slot_bytes(p.Hk, p.Hv, p.dk, p.dv);
-    const int most = std::min(slots / 2, std::max(n * kAheadChunks, 1));
     auto step = [&](cudaError_t r) {
       if (e == cudaSuccess) e = r;
     };
-    int i = 0;
     for (; e == cudaSuccess && plan.next(seg, most); ++i) {
       if (i >= 2) step(cudaStreamWaitEvent(s, side->done[i & 1], 0));            // who used this half before
       if (i >= 1) step(cudaStreamWaitEvent(s, side->go[(i - 1) & 1], 0));        // the chain before takes its SMs first
@@ -183,6 +212,7 @@ cudaError_t launch_prefill(const SeqParams& p, const int32_t* lens, int B, void*
       step(r);
       if (r == cudaSuccess) step(cudaStreamWaitEvent(s, side->done[0], 0));
     }
+    return_side(side);
   }
   delete[] todo;
   return e;

@@ -566,8 +566,10 @@ gdn_status gdn_tree_accept(const gdn_batch_schedule* sched, int32_t V, int32_t v
  * request with a NaN or an infinity does not touch the others, nor a column of v or of a state the
  * other columns; tokens before it may lose their outputs where they share its 64 (the chunks count
  * from the call's first row). Long prompts of few requests use a stream of the library's own
- * besides the given one (not while that is being captured), which waits for it: to the caller all
- * of the work is on `stream`.
+ * besides the given one (not while that is being captured, which rounds otherwise), which waits
+ * for it: to the caller all of the work is on `stream`. The library keeps up to eight for the
+ * process and device; one with work in flight serves no other stream, and a call that finds none
+ * free does without, with the same results.
  * ------------------------------------------------------------------------- */
 size_t gdn_prefill_workspace_bytes(const gdn_dims* d);
 gdn_status gdn_prefill(const gdn_dims* d, int32_t layers, int32_t layer, int32_t B, const int32_t* lens,

@@ -1,5 +1,9 @@
 """Prompt, single-token and log-probability calls on a GPU, beside test_gpu_sequences.py and test_gpu_sequences_calls.py, whose
 tolerances these tests use."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -60,3 +64,113 @@ def test_scores_of_a_prompt_s_next_tokens():
     torch.cuda.synchronize()
     s.check_error()
     check_scores(z[:-1], 3, (s.top[:n - 1], s.tokens[:n - 1], s.given[:n - 1], s.entropy[:n - 1]), late[1:])
+
+
+# ---- the library's own streams: programs of their own, which hold few streams -------------------------------------------
+
+PROMPTS = """
+import threading
+import torch
+from gated_deltanet_tree_gb300 import runtime as R
+n, made = 3200, []
+torch.manual_seed(5)
+x = torch.randn(n, 512, device="cuda").bfloat16()
+beta, log_g = torch.rand(n, 2, device="cuda").bfloat16(), -torch.rand(n, 2, device="cuda").bfloat16()
+w = 0.5 * torch.randn(1, 512, 4, device="cuda")
+
+
+class Prompt:
+    def __init__(self):
+        self.run, self.stream = R.SequenceRunner(R.make_dims(1, 2, 128, 128, 4), 1), torch.cuda.Stream()
+        self.state, self.conv = torch.empty(1, 1, 2, 128, 128, device="cuda"), torch.empty(1, 1, 3, 512, device="cuda")
+        self.out, self.end = torch.empty(n, 2, 128, device="cuda"), torch.cuda.Event()
+        torch.cuda.synchronize()
+
+    def call(self, wait=0):
+        with torch.cuda.stream(self.stream):
+            if wait:
+                torch.cuda._sleep(wait)                        # ends by itself
+            self.run.prefill([n], x, w, beta, log_g, None, None, self.out, state_out=self.state, conv_out=self.conv)
+            self.end.record()
+
+    def results(self):
+        return [t.clone() for t in (self.out, self.state, self.conv)]
+
+
+def same(a, b):
+    return all(torch.equal(s, t) for s, t in zip(a, b))
+
+"""
+
+
+def program(text):
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    done = subprocess.run([sys.executable, "-c", PROMPTS + text], cwd=root, capture_output=True, text=True, timeout=300)
+    assert done.returncode == 0, done.stderr[-2000:]
+
+
+def test_long_prompts_of_one_thread_do_not_wait_for_each_other():
+    """A prompt behind work of 0.2 s or more on one stream; another one's on a second stream is done before it."""
+    program("""
+a, b = Prompt(), Prompt()
+a.call()
+torch.cuda.synchronize()
+want = a.results()
+for first, second in ((a, b), (b, a), (a, b)):
+    for t in (*first.results(), *second.results()):
+        t.zero_()
+    first.call(wait=400_000_000)
+    second.call()
+    second.end.synchronize()
+    assert not first.end.query()
+    assert same(second.results(), want)
+    torch.cuda.synchronize()
+    assert same(first.results(), want)
+""")
+
+
+def test_more_long_prompts_at_work_than_the_library_has_streams():
+    """Twelve streams' prompts at once, and again from a thread each: those that find none of the library's streams free give
+    the same bits."""
+    program("""
+prompts = [Prompt() for _ in range(12)]
+prompts[0].call()
+torch.cuda.synchronize()
+want = prompts[0].results()
+for threads in (False, True, False):
+    for p in prompts:
+        for t in (p.out, p.state, p.conv):
+            t.fill_(7.0)
+    torch.cuda.synchronize()
+    if threads:
+        calls = [threading.Thread(target=p.call, args=(20_000_000,)) for p in prompts]
+        for c in calls:
+            c.start()
+        for c in calls:
+            c.join()
+    else:
+        for p in prompts:
+            p.call(20_000_000)
+    torch.cuda.synchronize()
+    for p in prompts:
+        p.run.check_error()
+        assert same(p.results(), want)
+""")
+
+
+def test_threads_that_end_leave_nothing_behind():
+    """A long prompt each from threads that end: the library's streams are the process's (a stream and its events take half a
+    megabyte of device memory)."""
+    program("""
+p = Prompt()
+p.call()
+torch.cuda.synchronize()
+before = torch.cuda.mem_get_info()[0]
+for _ in range(100):
+    t = threading.Thread(target=p.call)
+    t.start()
+    t.join()
+torch.cuda.synchronize()
+p.run.check_error()
+assert before - torch.cuda.mem_get_info()[0] < 16 << 20
+""")
