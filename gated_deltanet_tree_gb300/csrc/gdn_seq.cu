@@ -30,9 +30,10 @@ constexpr int kTokenByToken = 16;
 constexpr int kManyCtas = 608;
 constexpr size_t kWorkspace = 1000u << 20;
 
+// As many chunks as kWorkspace holds; two at least (a half each of the workspace), which fit it up to some 2000 heads.
 int workspace_slots(const gdn_dims& d) {
   const size_t n = kWorkspace / seq_slot_bytes(d.Hk, d.Hv, d.dk, d.dv);
-  return n < kSegReqs ? kSegReqs : n > 1024 ? 1024 : static_cast<int>(n);
+  return n < 2 ? 2 : n > 1024 ? 1024 : static_cast<int>(n);
 }
 
 // The segments of a batch of prompts, one after another.

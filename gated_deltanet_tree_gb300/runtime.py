@@ -418,7 +418,7 @@ class SequenceRunner:
         self.err = verifier.err if verifier is not None else torch.zeros(4, dtype=torch.int32, device=self.device)
         self._banks = verifier.banks if verifier is not None else None
         self.C = channels(dims)
-        # made once, for any call (a gigabyte or less, whatever the batch); prompts False: single tokens only, and none
+        # made once, for any call (1000 MiB or less up to some 2000 heads, whatever the batch); prompts False: single tokens only, and none
         self.workspace = torch.empty(N.gdn_prefill_workspace_bytes(self.dims) if prompts else 0, dtype=torch.uint8,
                                      device=self.device)
         self._index = self.err.get_device()

@@ -8,6 +8,8 @@ import numpy as np
 import pytest
 import torch
 
+from oracle import gdn_oracle as O
+from oracle import seq_oracle as Q
 from test_gpu_sequences import DT, Case, built, check, check_scores, f64, rows_of  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -64,6 +66,54 @@ def test_scores_of_a_prompt_s_next_tokens():
     torch.cuda.synchronize()
     s.check_error()
     check_scores(z[:-1], 3, (s.top[:n - 1], s.tokens[:n - 1], s.given[:n - 1], s.entropy[:n - 1]), late[1:])
+
+
+@pytest.mark.parametrize("Hk,Hv,lens", [(128, 128, [20 + 3 * i for i in range(60)]), (512, 512, [130, 0, 65, 17, 3, 64, 100, 20, 40, 30, 200, 18, 19, 90]),
+                                        (1024, 1024, [150, 40, 70])])
+def test_prompts_of_many_heads(Hk, Hv, lens):
+    """So many heads that the workspace holds fewer chunks than there are requests, or chunks (49, 12 and 6): each request's results are those
+    of a call of its own, bit for bit where that takes the same chunks at a time (up to 64 rows), within two calls' rounding
+    (2e-5 of a head's largest output, 1e-5 of a state) else."""
+    from gated_deltanet_tree_gb300 import runtime as R
+    dims, gen, B, rows = R.make_dims(Hk, Hv, 128, 128, 4), torch.Generator(device="cuda").manual_seed(2), len(lens), sum(lens)
+    C = R.channels(dims)
+
+    def normal(*shape):
+        return torch.empty(*shape, device="cuda").normal_(generator=gen)
+
+    x, w = normal(rows, C).bfloat16(), 0.5 * normal(1, C, 4)
+    beta, log_g = torch.sigmoid(normal(rows, Hv)).bfloat16(), -normal(rows, Hv).abs().bfloat16()
+    state, conv = normal(B, 1, Hv, 128, 128), normal(B, 1, 3, C)
+    s2, w2, out = torch.full_like(state, 5.0), torch.full_like(conv, 5.0), torch.empty(rows, Hv, 128, device="cuda")
+    R.SequenceRunner(dims, B).prefill(lens, x, w, beta, log_g, state, conv, out, state_out=s2, conv_out=w2)
+    own, at = R.SequenceRunner(dims, 1), 0
+    for b, n in enumerate(lens):
+        r = slice(at, at + n)
+        at += n
+        if n == 0:
+            assert (s2[b] == 5.0).all() and (w2[b] == 5.0).all()
+            continue
+        s, v, o = torch.empty_like(s2[:1]), torch.empty_like(w2[:1]), torch.empty_like(out[r])
+        own.prefill([n], x[r], w, beta[r], log_g[r], state[b:b + 1], conv[b:b + 1], o, state_out=s, conv_out=v)
+        own.check_error()
+        assert torch.equal(v[0], w2[b])
+        if n <= 64:
+            assert torch.equal(o, out[r]) and torch.equal(s[0], s2[b]), b
+        else:
+            assert ((o - out[r]).abs().amax((0, 2)) <= 2e-5 * o.abs().amax((0, 2))).all(), b
+            assert ((s[0] - s2[b]).norm(dim=(2, 3)) <= 1e-5 * s[0].norm(dim=(2, 3))).all(), b
+    # a head of each request against the oracle
+    d = O.Dims(1, 1, 128, 128, 4, 1, 1, dims.q_scale, dims.l2_eps)
+    h, at = Hv - 1, 0
+    cols = torch.cat([torch.arange(128) + 128 * i for i in (h, Hk + h, 2 * Hk + h)]).cuda()
+    for b, n in enumerate(lens[:8]):
+        r = slice(at, at + n)
+        at += n
+        if n:
+            o, T, _ = Q.run_sequence(f64(state[b, 0, h:h + 1]), f64(conv[b, 0][:, cols]), f64(x[r][:, cols]), f64(beta[r, h:h + 1]),
+                                     f64(log_g[r, h:h + 1]), f64(w[0, cols]), d)
+            assert np.abs(f64(out[r, h:h + 1]) - o).max() <= 2e-5 * np.abs(o).max(), b
+            assert np.linalg.norm(f64(s2[b, 0, h]) - T[0]) <= 1e-5 * np.linalg.norm(T[0]), b
 
 
 # ---- the library's own streams: programs of their own, which hold few streams -------------------------------------------

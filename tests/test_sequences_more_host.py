@@ -26,3 +26,12 @@ def test_tokens_begin_at_any_element(N, R):
         assert at % 16 == 0 and (at == base + 4 * first) == (first % 4 == 0)
         if first % 4:
             assert torch.equal(s._shifted[:n], tokens[first:first + n]) and at == s._shifted.data_ptr()
+
+
+@pytest.mark.parametrize("Hk,Hv,dk,dv", [(1, 1, 32, 32), (16, 48, 128, 128), (128, 128, 128, 128), (64, 512, 128, 128), (1000, 1000, 128, 128),
+                                         (2048, 2048, 32, 32), (1, 4096, 64, 128)])
+def test_prompts_workspace_has_a_bound(N, Hk, Hv, dk, dv):
+    """1000 MiB, however many heads fit two chunks into them; the two chunks where none do."""
+    assert 0 < N.gdn_prefill_workspace_bytes(dims(N, Hk=Hk, Hv=Hv, dk=dk, dv=dv)) <= 1000 << 20
+    many = N.gdn_prefill_workspace_bytes(dims(N, Hk=16384, Hv=16384, dk=128, dv=128))
+    assert many == 2 * 16384 * (4 * 64 * 128 * 2 + 2 * 64 * 64 * 4 + 2 * 128 * 64 * 2 + 64 * 128 * 4 + 144 * 4)
