@@ -69,11 +69,12 @@ def test_scores_of_a_prompt_s_next_tokens():
 
 
 @pytest.mark.parametrize("Hk,Hv,lens", [(128, 128, [20 + 3 * i for i in range(60)]), (512, 512, [130, 0, 65, 17, 3, 64, 100, 20, 40, 30, 200, 18, 19, 90]),
-                                        (1024, 1024, [150, 40, 70])])
+                                        (1024, 1024, [150, 40, 70]), (16, 48, [590 - 37 * (i % 11) - i for i in range(40)])])
 def test_prompts_of_many_heads(Hk, Hv, lens):
-    """So many heads that the workspace holds fewer chunks than there are requests, or chunks (49, 12 and 6): each request's results are those
-    of a call of its own, bit for bit where that takes the same chunks at a time (up to 64 rows), within two calls' rounding
-    (2e-5 of a head's largest output, 1e-5 of a state) else."""
+    """So many heads that the workspace holds fewer chunks than there are requests, or chunks: 49, 12 and 6; 220 of 16 and 48 heads,
+    where forty requests have 270 (no more are begun than fill the GPU and fit in whole, the others in later segments).  Each
+    request's results are those of a call of its own: bit for bit where that takes the same chunks at a time (up to 64 rows),
+    else within two calls' rounding (2e-5 of a head's largest output, 1e-5 of a state)."""
     from gated_deltanet_tree_gb300 import runtime as R
     dims, gen, B, rows = R.make_dims(Hk, Hv, 128, 128, 4), torch.Generator(device="cuda").manual_seed(2), len(lens), sum(lens)
     C = R.channels(dims)
@@ -105,7 +106,8 @@ def test_prompts_of_many_heads(Hk, Hv, lens):
     # a head of each request against the oracle
     d = O.Dims(1, 1, 128, 128, 4, 1, 1, dims.q_scale, dims.l2_eps)
     h, at = Hv - 1, 0
-    cols = torch.cat([torch.arange(128) + 128 * i for i in (h, Hk + h, 2 * Hk + h)]).cuda()
+    kh = h // (Hv // Hk)
+    cols = torch.cat([torch.arange(128) + 128 * i for i in (kh, Hk + kh, 2 * Hk + h)]).cuda()
     for b, n in enumerate(lens[:8]):
         r = slice(at, at + n)
         at += n
