@@ -164,6 +164,9 @@ __device__ __forceinline__ float abs_max(float m, u64 x) {
 constexpr float kInf = __builtin_huge_valf();
 __device__ __forceinline__ float finite_max(float m, float x) { return fabsf(x) < kInf ? fmaxf(m, fabsf(x)) : m; }
 
+// The same, where zeros count as something: 0 stays where nothing is finite.
+__device__ __forceinline__ float finite_some(float m, float x) { return fabsf(x) < kInf ? fmaxf(m, fmaxf(fabsf(x), 0x1p-149f)) : m; }
+
 // A bounded wait that leaves the issue slots to the working warps.
 __device__ __forceinline__ bool mbar_wait_quiet(uint64_t* bar, uint32_t parity) {
   if (mbar_ready(bar, parity)) return true;
@@ -1093,18 +1096,18 @@ seq_chain_kernel(const SeqParams p, const __grid_constant__ Segment seg, const c
       }
     }
     float smax = 0.f, omax = 0.f, inv_s;
-    // The largest entries of T and of the chunk's o: each warp notes its own when it hands T on, in the half of the table
+    // The largest entries of T and of the chunk's o (0: none is finite): each warp notes its own when it hands T on, in the half of the table
     // that the chunk's number gives, and all read them once D1 is there.
     auto note_maxima = [&](int half) {
       float big = 0.f;
 #pragma unroll
       for (int j = 0; j < kPairs; ++j) big = abs_max(big, S[j]);
-      if (big == kInf) {
+      if (has_row && (big == kInf || big == 0.f)) {
         big = 0.f;
 #pragma unroll
         for (int j = 0; j < kPairs; ++j) {
           const float2 f = unpack2(S[j]);
-          big = finite_max(finite_max(big, f.x), f.y);
+          big = finite_some(finite_some(big, f.x), f.y);
         }
       }
       big = warp_max(big);
@@ -1117,6 +1120,9 @@ seq_chain_kernel(const SeqParams p, const __grid_constant__ Segment seg, const c
       s = warp_max(lane < L::kTurnWarps ? m[lane] : 0.f);
       o = warp_max(lane < L::kTurnWarps ? m[L::kTurnWarps + lane] : 0.f);
     };
+    // A bound lies far above the values that it was for.  Where none of these is finite there is nothing to take again; a chunk
+    // that has to be, whatever it came to, has infinite bounds.
+    auto too_far = [](float bound, float most) { return bound * kRange > most && (most > 0.f || bound == kInf); };
     // packed pairs, scaled, into a two-term operand at `at`, whose groups of eight columns lie `step` bytes apart
     auto put = [&](const u64* x, float sc, char* at, int step, int lo_at) {
       const u64 sc2 = pack2(sc, sc);
@@ -1257,8 +1263,8 @@ seq_chain_kernel(const SeqParams p, const __grid_constant__ Segment seg, const c
       read_maxima(ph, smax, omax_before);
       // Bounds far above the values have cost these their bits.  T itself is exact: its operand is made again.  u and o are
       // not: the chunk before is taken again, token by token.
-      if (i > 0 && (s_bound * kRange > smax || o_bound * kRange > omax_before)) {
-        if (u_bound * kRange > smax || o_bound * kRange > omax_before) take_again(i - 1);
+      if (i > 0 && (too_far(s_bound, smax) || too_far(o_bound, omax_before))) {
+        if (too_far(u_bound, smax) || too_far(o_bound, omax_before)) take_again(i - 1);
         put_again(i);
         wait(kD1 + g, d1_done++ & 1);
         tmem_fence_after();
@@ -1331,6 +1337,12 @@ seq_chain_kernel(const SeqParams p, const __grid_constant__ Segment seg, const c
             omax = abs_max(omax, a[j / 2 + k]);
           }
         }
+        if (omax == 0.f)
+#pragma unroll
+          for (int j = 0; j < kPairs; ++j) {
+            const float2 f = unpack2(a[j]);
+            omax = finite_some(finite_some(omax, f.x), f.y);
+          }
       }
       // T before the chunk is kept in D2's place, of which this thread has read its part
 #pragma unroll
@@ -1357,7 +1369,7 @@ seq_chain_kernel(const SeqParams p, const __grid_constant__ Segment seg, const c
     note_maxima(req.nc & 1);
     group_barrier();
     read_maxima(req.nc & 1, smax, omax_before);
-    if (u_bound * kRange > smax || o_bound * kRange > omax_before) take_again(req.nc - 1);
+    if (too_far(u_bound, smax) || too_far(o_bound, omax_before)) take_again(req.nc - 1);
     if (has_row) {
       float* dst = p.state_out + req.b * p.state_stride + (static_cast<long long>(vh) * DK + row) * p.dv + col0 + c0;
 #pragma unroll

@@ -118,6 +118,41 @@ def test_prompts_of_many_heads(Hk, Hv, lens):
             assert np.linalg.norm(f64(s2[b, 0, h]) - T[0]) <= 1e-5 * np.linalg.norm(T[0]), b
 
 
+@pytest.mark.parametrize("what", ["state", "row", "gate", "columns"])
+def test_a_request_that_is_not_finite_takes_no_longer(what):
+    """A NaN state, or one from a NaN row or gate on, or with finite values in some columns only: no chunk is worth taking again
+    (token by token, thirty times as slow), and other requests' results keep their bits."""
+    c = Case(50, (1, 2, 128, 128), [2500, 2400], "bf16", slow=True, layers=1, layer=0)
+    r, times, results = c.runner(), [], []
+    for bad in (False, True):
+        if bad and what == "state":
+            c.state[0] = float("nan")
+        elif bad and what == "columns":
+            c.state[0, 0, :, :, :100] = float("nan")
+        elif bad:
+            (c.x if what == "row" else c.log_g)[70] = float("nan")
+        best = float("inf")
+        for _ in range(5):
+            state, conv = torch.empty_like(c.state), torch.empty_like(c.conv)
+            begin, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            begin.record()
+            r.prefill(c.lens, *c.inputs(), c.state, c.conv, c.out, state_out=state, conv_out=conv)
+            end.record()
+            torch.cuda.synchronize()
+            best = min(best, begin.elapsed_time(end))
+        r.check_error()
+        times.append(best)
+        results.append((c.out.clone(), state))
+    (out, state), (out2, state2) = results
+    assert torch.equal(out[2500:], out2[2500:]) and torch.equal(state[1], state2[1])
+    cols = slice(0, 100) if what == "columns" else slice(None)
+    assert torch.isnan(out2[128:2500, :, cols]).all() and torch.isnan(state2[0, :, :, :, cols]).all()
+    if what == "columns":
+        for a, b in ((out[:2500, :, 100:], out2[:2500, :, 100:]), (state[0, ..., 100:], state2[0, ..., 100:])):
+            assert (a - b).abs().max() <= 2e-5 * a.abs().max()     # (the largest entry, and with it the scale, may be another one)
+    assert times[1] <= 2 * times[0], times
+
+
 # ---- the library's own streams: programs of their own, which hold few streams -------------------------------------------
 
 PROMPTS = """
