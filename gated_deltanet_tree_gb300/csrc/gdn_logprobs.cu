@@ -7,14 +7,19 @@
 // of 4096 entries lies in the CTA's registers; the top-th largest of 32 group maxima of the first
 // one bounds its top-th largest entry from below, so a handful of entries pass and are put on a list
 // in shared memory.  Its exact best are picked by counting, and the worst of them is the bound of
-// later tiles; it is renewed after ever more of them, and the warps need no barrier in between.  Where more entries pass than the list holds
-// (long ties, rising rows) the best are found tile by tile, one after another, in a second pass.
+// later tiles; it is renewed after ever more of them, and the warps need no barrier in between.  Where
+// more entries pass than the list holds the best are found tile by tile, one after another, in a second
+// pass: long ties, rising rows, and rows whose first 4096 entries hold fewer than `top` groups with one
+// that is not masked (the bound is -inf then, which masked entries pass).  That is some 4 times as slow
+// at ten rows and 14 times at 320 (us, 131072 entries of bf16, 8 best): 300 entries not masked 48 and 476,
+// equal entries 45 and 461, the first 4096 masked 62 and 652, against 11 and 33.
 //
 // A cluster of up to eight CTAs shares a row where rows are few; each puts its sums and its list into
 // the first one's shared memory.
 //
-// The bytes, read once, are the floor; instruction issue is nearer (some nine instructions an entry, a
-// MUFU exponential among them) and, where a row has few tiles, the latencies of its start and end.
+// The bytes, read once, are the floor.  Instruction issue is nearer, half its slots taken (by the counters
+// 12 to 22 instructions an entry, tiles' and rows' starts and ends among them, for clocks of 1440 to
+// 2070 MHz), and, where a row has few tiles, the latencies of its start and end.
 // Measured (us): 10 rows of 131072 bf16 7.8, 320 of them 33 (floor 12), 1500 rows of 65537 fp32 with
 // 20 best 92 (floor 58).  Two CTAs a row where there are 320 took 37; a warp's entries that pass, taken
 // in unrolled code, cost the ten rows 1.4 us more, because code that runs once is fetched slowly.

@@ -12,8 +12,8 @@
 // and the states' way through memory.  8191 tokens of 48 heads took 858 us with 104 MB, 801 with 300 and 735 with 1000 (before
 // the halves took turns).
 //
-// Measured, 16 k-heads and 48 v-heads of 128 x 128, bf16 (us): 70 tokens 32, 1024 104, 8191 657, 20001 and 15001 together 2550,
-// 32 prompts of 250 to 500 tokens 1028, 128 of 50 to 100 1505.
+// Measured, 16 k-heads and 48 v-heads of 128 x 128, bf16 (us): 70 tokens 31, 1024 104, 8191 651, 20001 and 15001 together 2535,
+// 32 prompts of 250 to 500 tokens 1022, 128 of 50 to 100 1505.
 #include <algorithm>
 #include <initializer_list>
 #include <mutex>

@@ -578,7 +578,8 @@ seq_keys_kernel(const SeqParams p, const __grid_constant__ Segment seg, char* ws
 // (1 + A)^-1 by substitution in blocks: two 32 x 32 triangles, a warp each, and the block below them as a product of three on
 // mma.sync: tiles of 16 x 8 straight from and into A's rows in shared memory, where tcgen05 would want images, tensor memory
 // and two barriers for two products of 32 x 32 x 32.  N = C M is on tcgen05.  Bound: instruction issue (57% of the slots; the
-// rest goes with the barriers between the steps); 128 chunks of 48 heads take 201 us.
+// rest goes with the barriers between the steps); 128 chunks of 48 heads take 201 us.  The 64 registers that let four CTAs share
+// an SM spill some 110 bytes a thread, with more than four taps 540 to 680.
 template <typename InT, int KT>
 __global__ void __launch_bounds__(kPrepThreads, 4)
 seq_values_kernel(const SeqParams p, const __grid_constant__ Segment seg, char* ws) {

@@ -9,7 +9,7 @@
 // Measured (us a call, this kernel : the one of gdn_seq_rec.cu, which the others go to), 16 k-heads and 48 v-heads: 4 requests
 // 13.0 : 10.4, 8 15.6 : 18.4, 16 26.6 : 34.8, 32 47 : 66, 128 154 : 246 (5.3 TB/s, 0.78 of measured).  Heads of 64 x 64 gain a
 // tenth at 128 requests, heads of 64 x 128 nothing: their tiles are too small for one CTA an SM.  With fp32 rows or many v-heads
-// a k-head the rows may leave no room for three tiles.
+// a k-head the rows may leave no room for three tiles.  (At its 168 registers the kernel spills 24 bytes a thread.)
 //
 // The arithmetic is that of gdn_seq_rec.cu: p = (g T)^T k and r = (g T)^T q in one pass, u = beta (v - p),
 // o = r + (q . k) u, T' = g T + k u^T.

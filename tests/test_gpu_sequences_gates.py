@@ -122,3 +122,13 @@ def test_growing_chunks_of_one_head():
     o, T, _ = c.reference()
     assert np.abs(f64(out[:, 2]) - o[:, 2]).max() <= 2e-5 * np.abs(o[:, 2]).max()
     assert np.linalg.norm(f64(s2[0, 1, 2]) - T[0, 2]) <= 1e-5 * np.linalg.norm(T[0, 2])
+
+
+@pytest.mark.parametrize("at", [1590, 1600, 3190])
+def test_growing_chunks_at_the_ends_of_a_long_prompt_s_parts(at):
+    """3200 tokens are 50 chunks, taken in two halves: the chunk that is taken again is the last of the first (before token 1600),
+    the first of the second, or the last of all."""
+    c = Case(48, (1, 2, 128, 128), [3200], "f32", slow=True)
+    g = f64(c.log_g)
+    g[at:at + 10] += 1.5
+    run_and_check(c, g)
