@@ -537,7 +537,8 @@ class TokenScorer:
             to.copy_(tokens)
         else:
             if isinstance(stream, int):
-                stream = torch.cuda.ExternalStream(stream, device=self._index)
+                # (a pointer of 0 would make torch take one of its own)
+                stream = torch.cuda.ExternalStream(stream, device=self._index) if stream else torch.cuda.default_stream(self._index)
             with torch.cuda.stream(stream):
                 to.copy_(tokens)
         return to.data_ptr()

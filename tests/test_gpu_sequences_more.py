@@ -261,3 +261,22 @@ torch.cuda.synchronize()
 p.run.check_error()
 assert before - torch.cuda.mem_get_info()[0] < 16 << 20
 """)
+
+
+def test_scores_on_the_default_stream_given_as_0():
+    """Slices of tokens are copied on the stream that the call is given, also where that is the default stream's 0 and another
+    one is current."""
+    from gated_deltanet_tree_gb300.runtime import TokenScorer
+    rng = np.random.default_rng(4)
+    V, n = 501, 20
+    z = rows_of(rng, n, V, "normal", "f32")
+    tokens = torch.from_numpy(rng.integers(0, V, n).astype(np.int32)).cuda()
+    s, late, other = TokenScorer(n, V, 3), torch.zeros_like(tokens), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(20_000_000)                              # ends by itself, about 10 ms
+    late.copy_(tokens)
+    with torch.cuda.stream(other):
+        s.score(z[:-1], late[1:], stream=0)
+    torch.cuda.synchronize()
+    s.check_error()
+    check_scores(z[:-1], 3, (s.top[:n - 1], s.tokens[:n - 1], s.given[:n - 1], s.entropy[:n - 1]), tokens[1:])
