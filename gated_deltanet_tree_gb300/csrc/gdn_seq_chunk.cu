@@ -18,8 +18,8 @@
 // |T'| <= e^c max T + 64 max u, some 2^11 above it, and the largest entry is looked at afterwards: no warp waits for the
 // others'.  Where a bound turns out to lie 2^17 above the largest entry of T' or of the chunk's o (values that shrink or grow
 // by that much within 64 tokens), T' is handed on again, or the chunk is taken again, token by token; so are chunks in which
-// products of gates, or M, grow (kMostGrowth).  Entries of T and v that
-// are not finite count for no bound: they stay in their own column of d_v, as in the rule.
+// products of gates, or M, grow (kMostGrowth).  Entries of T and v that are not finite count for no bound: they stay in their
+// own column of d_v, as in the rule.
 //
 // Operands in shared memory have no swizzle: 8 rows x 16 bytes are 128 contiguous bytes.  With 16 bytes of d_k per
 // token, a core matrix of K serves as K-major operand of D1 and as M-major operand of D3.
@@ -1097,8 +1097,8 @@ seq_chain_kernel(const SeqParams p, const __grid_constant__ Segment seg, const c
       }
     }
     float smax = 0.f, omax = 0.f, inv_s;
-    // The largest entries of T and of the chunk's o (0: none is finite): each warp notes its own when it hands T on, in the half of the table
-    // that the chunk's number gives, and all read them once D1 is there.
+    // The largest entries of T and of the chunk's o (0: none is finite): each warp notes its own when it hands T on, in the half
+    // of the table that the chunk's number gives, and all read them once D1 is there.
     auto note_maxima = [&](int half) {
       float big = 0.f;
 #pragma unroll
